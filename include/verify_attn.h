@@ -80,6 +80,11 @@ typedef enum va_mode {
 #define VA_DEV_BAD_ROWS 0x8u     /* cu_rows not ascending, n > max_rows_per_seq, total mismatch,
                                     or a tree sequence with more than VA_MAX_TREE_ROWS rows */
 #define VA_DEV_TIMEOUT 0x10u     /* a bounded pipeline wait gave up */
+#define VA_DEV_BAD_SAMPLING 0x20u /* a temperature that is neither 0 nor in [1e-6, inf) */
+#define VA_DEV_BAD_TOKEN 0x40u   /* a drafted token outside [0, vocab) */
+#define VA_DEV_BAD_LOGITS 0x80u  /* NaN, +inf or nothing but -inf in the row the next token is drawn from */
+#define VA_DEV_NO_PAGES 0x100u   /* fewer free pages than a fork needs */
+#define VA_DEV_BAD_COPY 0x200u   /* a page pair outside the pool, or more pairs than the list holds */
 
 /* Problem flags. */
 #define VA_FLAG_CUDA_CORES 0x1u /* run the CUDA-core (SIMT) partial kernel for any dtype */
@@ -350,6 +355,160 @@ va_status va_timing_read(int32_t max_calls, float *partial_ms, float *merge_ms,
 
 va_status verify_attn_noalloc(const va_problem *p, const va_kv *kv, int32_t mode, float *o,
                               float *lse, uint32_t *status, void *stream);
+
+/*
+ * Acceptance of drafted tokens from given random numbers, and the token
+ * that follows them: the step between a verify call (whose rows the target's
+ * logits come from) and verify_attn_promote.
+ *
+ * Of va_problem, num_seqs, cu_rows, parent, seq_kind, total_rows and
+ * max_rows_per_seq are read (kinds and row limits as for verify calls).  Row
+ * 0 of a sequence is the token that is already known (a tree has one root:
+ * parent[0] = -1, parent[j] in [0, j)); row j > 0 proposes tokens[row] for
+ * the place after its parent.  Let p be softmax(logits[a] / temperature) at
+ * the node a reached so far, starting from row 0.  The children of a are
+ * tried in row order; one with token x is taken iff
+ *     accept_u[row] * g(x) < r(x),
+ * with r = p for the first child.  A child that is not taken leaves
+ * r <- max(r - g, 0), renormalised.  g is draft_probs[a], the distribution
+ * that the children of a were drawn from, or the indicator of x where
+ * draft_probs is NULL (proposals that were not drawn; r then only loses x).
+ * At the node where no child is taken, the next token is the lowest i with
+ * r_0 + .. + r_i > sample_u[s] (r_0 + r_1 + ..).  Should r be zero
+ * everywhere, p takes its place.  Temperature 0: a child is taken iff its
+ * token is the lowest index of the row's maximum, and so is the next token;
+ * no random number is used.
+ *   accepted_len[s]: rows on the path taken, row 0 among them (>= 1);
+ *   accepted_nodes[cu_rows[s] + i]: local index of its i-th row for i <
+ *     accepted_len[s], -1 for the sequence's other rows;
+ *   promote_len[s] (may be NULL): accepted_len[s] for a tree, 0 for a chain,
+ *     as verify_attn_promote takes it;
+ *   next_token[s].
+ * Outputs of rows that no sequence covers stay as they were.  A sequence of
+ * no rows gets accepted_len 0 and next_token -1.
+ * Masked vocabulary entries are -inf.  A row whose logits hold NaN, +inf or
+ * nothing but -inf has no distribution: none of its children is taken, and
+ * if the path ends there next_token is -1 (VA_DEV_BAD_LOGITS).  A sequence
+ * with a bad row range, parent, drafted token or temperature gets
+ * accepted_len 0, accepted_nodes and next_token -1 and the status bit
+ * (VA_DEV_BAD_ROWS: its accepted_nodes stay as they were).  accept_u and
+ * sample_u are in [0, 1), draft_probs in [0, 1].
+ * The result does not depend on what else shares the launch, nor on the
+ * order of any sum of the last row (its weights are summed as integers).
+ */
+typedef struct va_draft {
+  int32_t vocab;              /* 1 .. 2^20 */
+  va_dtype logits_dtype;      /* VA_F32 or VA_BF16 */
+  const void *logits;         /* device [total_rows][logits_stride], element-aligned */
+  int64_t logits_stride;      /* elements from row to row, >= vocab */
+  const float *draft_probs;   /* device [total_rows][draft_stride] by parent row, or NULL */
+  int64_t draft_stride;
+  const int32_t *tokens;      /* device [total_rows]; row 0 of a sequence is not read */
+  const float *accept_u;      /* device [total_rows] */
+  const float *sample_u;      /* device [num_seqs] */
+  const float *temperature;   /* device [num_seqs]: 0 or >= 1e-6; NULL: 1 */
+} va_draft;
+
+/* Bytes of device workspace (256-byte aligned; may be 0, ws may then be
+ * NULL).  Contents carry nothing from call to call. */
+size_t verify_attn_accept_workspace_size(const va_problem *p, const va_draft *d);
+
+va_status verify_attn_accept(const va_problem *p, const va_draft *d, int32_t mode, void *ws,
+                             size_t ws_bytes, int32_t *accepted_len, int32_t *accepted_nodes,
+                             int32_t *promote_len, int32_t *next_token, uint32_t *status,
+                             void *stream);
+
+/*
+ * Pages of a paged cache.  block_table is the table that verify calls read
+ * (va_kv.block_table), here written; an entry of -1 holds no page.
+ * ref_count[b] is the number of table entries that hold page b; a page is
+ * free while it is 0.  Sequences may share pages; a shared page is one that
+ * no sequence writes again (a full one).  An empty pool is a table of -1 and
+ * counts of 0.
+ * The calls run on the device in stream order, with lengths and commands in
+ * device memory.  A planning call (fork, free, compact) checks everything
+ * before it changes anything: a status word that is non-zero on entry, or a
+ * finding of its own, leaves table and counts as they were (and num_copies
+ * 0).  status may be NULL.  Two calls on one pool must not overlap in time.
+ */
+typedef struct va_page_pool {
+  int32_t num_seqs;
+  int32_t max_blocks_per_seq;
+  int32_t num_blocks;
+  int32_t *block_table; /* device [num_seqs][max_blocks_per_seq] */
+  int32_t *ref_count;   /* device [num_blocks] */
+} va_page_pool;
+
+/* Bytes of device workspace (256-byte aligned) of a fork of num_forks
+ * commands, or (num_forks = 0) of a compaction. */
+size_t verify_attn_pages_workspace_size(const va_page_pool *pool, int32_t num_forks);
+
+/*
+ * Fork and grow sequences.  Command i (device arrays of num_forks):
+ *   src[i] != dst[i]: the row of dst becomes a fork of the first len[i] tokens
+ *     of src.  Full pages are shared; a partial last page is replaced by a
+ *     fresh one and the pair (old, fresh) is written to copies; fresh pages
+ *     follow up to entry pages[i], -1 beyond.  Entries of -1 below the length
+ *     (pages behind a window) stay -1.  What dst's row held before is
+ *     overwritten, not given back.
+ *   src[i] == dst[i]: the sequence grows.  Entries from ceil(len[i] / 16) to
+ *     pages[i] that hold no page get fresh ones; everything else stays.
+ * Fresh pages are the free pages of lowest index, in command order and then
+ * entry order.  copies: device [num_forks][2], in command order; num_copies:
+ * device, the number written.  The caller then copies the pairs in every
+ * pool (verify_attn_pages_copy).
+ * Errors (nothing changes): a sequence out of range, named as dst twice, or a
+ * src (!= dst) that is another command's dst (VA_DEV_BAD_ROWS); len or pages
+ * out of range, or len > 16 pages (VA_DEV_CTX_OVERFLOW); a table entry that
+ * is neither -1 nor a page in use, no page where the partial page should be,
+ * a negative count (VA_DEV_BAD_BLOCK); too few free pages (VA_DEV_NO_PAGES).
+ */
+va_status verify_attn_pages_fork(const va_page_pool *pool, int32_t num_forks, const int32_t *src,
+                                 const int32_t *dst, const int32_t *len, const int32_t *pages,
+                                 int32_t *copies, int32_t *num_copies, void *ws, size_t ws_bytes,
+                                 uint32_t *status, void *stream);
+
+/*
+ * Give back the table entries first[i] .. last[i] - 1 of sequence seq[i]: each
+ * held page loses a reference and the entry becomes -1 (entries of -1 are
+ * passed over; ranges may overlap).  With a window W and `sinks` first
+ * tokens, a sequence of ctx tokens needs no entry from ceil(sinks / 16) to
+ * floor((ctx - W + 1) / 16).  Errors (nothing changes): a sequence
+ * (VA_DEV_BAD_ROWS) or range (VA_DEV_CTX_OVERFLOW) out of range, an entry that
+ * is neither -1 nor a page in use (VA_DEV_BAD_BLOCK).  A page with fewer
+ * references than entries is left at 0 and sets VA_DEV_BAD_BLOCK.
+ */
+va_status verify_attn_pages_free(const va_page_pool *pool, int32_t num_ranges, const int32_t *seq,
+                                 const int32_t *first, const int32_t *last, uint32_t *status,
+                                 void *stream);
+
+/*
+ * Pull the N pages in use together at the front of the pool: the k-th page in
+ * use at or above N moves to the k-th free page below N (ascending).  Table,
+ * counts and the pairs (from, to) in copies (device [num_blocks / 2][2]) are
+ * written; *num_copies (device) is their number, *live_blocks (device, may be
+ * NULL) is N.  No pair's target is another's source, so the pairs may be
+ * copied in any order.  Errors (nothing changes): a table entry that is
+ * neither -1 nor a page in use, a negative count (VA_DEV_BAD_BLOCK).
+ */
+va_status verify_attn_pages_compact(const va_page_pool *pool, int32_t *copies, int32_t *num_copies,
+                                    int32_t *live_blocks, void *ws, size_t ws_bytes,
+                                    uint32_t *status, void *stream);
+
+/*
+ * Copy pages in num_pools pools (host array of device pointers, 16-byte
+ * aligned: the K and V arrays of every layer), each [num_blocks][page_bytes]:
+ * for the first *num_copies (device) pairs of copies (device [max_copies][2]),
+ * page copies[i][0] to page copies[i][1].  page_bytes is a multiple of 16
+ * (num_kv_heads * 16 * row bytes for a cache).  No target may be another
+ * pair's source or target.  Nothing is copied when *status holds a finding of
+ * an earlier call; a pair outside the pool is passed over and sets
+ * VA_DEV_BAD_COPY, as does *num_copies > max_copies.
+ */
+va_status verify_attn_pages_copy(void *const *pools, int32_t num_pools, int64_t page_bytes,
+                                 int32_t num_blocks, const int32_t *copies,
+                                 const int32_t *num_copies, int32_t max_copies, uint32_t *status,
+                                 void *stream);
 
 #ifdef __cplusplus
 }

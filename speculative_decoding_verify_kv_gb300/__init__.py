@@ -27,6 +27,11 @@ DEV_BAD_BLOCK = 0x2
 DEV_CTX_OVERFLOW = 0x4
 DEV_BAD_ROWS = 0x8
 DEV_TIMEOUT = 0x10
+DEV_BAD_SAMPLING = 0x20
+DEV_BAD_TOKEN = 0x40
+DEV_BAD_LOGITS = 0x80
+DEV_NO_PAGES = 0x100
+DEV_BAD_COPY = 0x200
 
 # Rows per sequence (chain / tree); see VA_MAX_ROWS_PER_SEQ in the header.
 MAX_ROWS_PER_SEQ = 1024
@@ -41,7 +46,10 @@ MODE_CODES = {"chain": MODE_CHAIN, "tree": MODE_TREE, "mixed": MODE_MIXED}
 EXPORTED = ["va_version", "va_status_string", "va_last_cuda_error", "va_workspace_size", "va_validate",
             "verify_attn_chain", "verify_attn_tree", "verify_attn_mixed",
             "va_debug_row_map", "va_debug_gather_index", "va_plan", "va_timing_enable",
-            "va_timing_read", "verify_attn_noalloc", "verify_attn_promote", "va_debug_split_ranges"]
+            "va_timing_read", "verify_attn_noalloc", "verify_attn_promote", "va_debug_split_ranges",
+            "verify_attn_accept", "verify_attn_accept_workspace_size",
+            "verify_attn_pages_workspace_size", "verify_attn_pages_fork", "verify_attn_pages_free",
+            "verify_attn_pages_compact", "verify_attn_pages_copy"]
 
 
 class VaKV(ctypes.Structure):
@@ -61,6 +69,20 @@ class VaProblem(ctypes.Structure):
                 ("total_rows", ctypes.c_int32), ("max_rows_per_seq", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("num_splits", ctypes.c_int32),
                 ("flags", ctypes.c_uint32)]
+
+
+class VaDraft(ctypes.Structure):
+    _fields_ = [("vocab", ctypes.c_int32), ("logits_dtype", ctypes.c_int),
+                ("logits", ctypes.c_void_p), ("logits_stride", ctypes.c_int64),
+                ("draft_probs", ctypes.c_void_p), ("draft_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_void_p), ("accept_u", ctypes.c_void_p),
+                ("sample_u", ctypes.c_void_p), ("temperature", ctypes.c_void_p)]
+
+
+class VaPagePool(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("block_table", ctypes.c_void_p),
+                ("ref_count", ctypes.c_void_p)]
 
 
 class VaPlanInfo(ctypes.Structure):
@@ -113,6 +135,21 @@ def _load():
     lib.verify_attn_promote.restype = ctypes.c_int
     lib.verify_attn_promote.argtypes = [P(VaProblem), P(VaKV), ctypes.c_int32, ctypes.c_void_p,
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+    ptr, i32, i64, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    for name, res, args in (
+            ("verify_attn_accept_workspace_size", size, [P(VaProblem), P(VaDraft)]),
+            ("verify_attn_accept", ctypes.c_int,
+             [P(VaProblem), P(VaDraft), i32, ptr, size, ptr, ptr, ptr, ptr, ptr, ptr]),
+            ("verify_attn_pages_workspace_size", size, [P(VaPagePool), i32]),
+            ("verify_attn_pages_fork", ctypes.c_int,
+             [P(VaPagePool), i32, ptr, ptr, ptr, ptr, ptr, ptr, ptr, size, ptr, ptr]),
+            ("verify_attn_pages_free", ctypes.c_int, [P(VaPagePool), i32, ptr, ptr, ptr, ptr, ptr]),
+            ("verify_attn_pages_compact", ctypes.c_int,
+             [P(VaPagePool), ptr, ptr, ptr, ptr, size, ptr, ptr]),
+            ("verify_attn_pages_copy", ctypes.c_int,
+             [P(ptr), i32, i64, i32, ptr, ptr, i32, ptr, ptr])):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = res, args
     return lib
 
 
@@ -370,3 +407,8 @@ def timing_read(max_calls: int = 4096):
     if st:
         raise VaError(st, "va_timing_read")
     return list(a[:n.value]), list(b[:n.value])
+
+
+from ._calls import (AcceptCall, CompactCall, Draft, ForkCall, FreeCall, PageCopyCall,  # noqa: E402,F401
+                     PagePool, verify_attn_accept, verify_attn_pages_compact,
+                     verify_attn_pages_copy, verify_attn_pages_fork, verify_attn_pages_free)

@@ -1,0 +1,263 @@
+"""Bound calls of the operators around a verify step: acceptance of drafted
+tokens and the pages of a paged cache.
+
+A serving loop makes the same call step after step over buffers that it
+keeps.  Each ``...Call`` object checks its tensors, allocates what the
+caller left out (outputs, workspace) and fills the C structs once; calling
+it launches on the current stream (or the one given) and returns the output
+tensors, which the next call of the same object overwrites.  The functions
+of the C names bind and call in one go.  Two calls that may overlap in time
+need two objects (the workspace is the object's).
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import BF16, F32, Problem, VaDraft, VaError, VaPagePool, VaProblem, _ptr, lib
+
+_FLOAT = {F32: torch.float32, BF16: torch.bfloat16}
+
+
+def _tensor(name, t, dtype, numel, device=None, optional=False):
+    """Check one argument: a contiguous tensor of the type, with at least
+    numel elements, on the given device."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.numel() < numel:
+        raise ValueError(f"{name}: {t.numel()} elements, {numel} needed")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the other arguments on {device}")
+    return t
+
+
+class _Call:
+    """Arguments of one entry point, bound.  Subclasses fill ``_fn``,
+    ``_args`` (all but the stream), ``_out`` and ``device``."""
+    _where = ""
+
+    def __call__(self, stream=None):
+        dev = self.device
+        if dev.type != "cuda":
+            raise ValueError(f"{self._where}: tensors on {dev}, not on a GPU")
+        if torch.cuda.current_device() != dev.index:
+            raise ValueError(f"{self._where}: tensors on {dev}, current device cuda:{torch.cuda.current_device()}")
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        st = self._fn(*self._args, stream.cuda_stream)
+        if st:
+            raise VaError(st, self._where)
+        return self._out
+
+    def _buffer(self, name, t, shape, dtype):
+        n = 1
+        for d in shape:
+            n *= d
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        return _tensor(name, t, dtype, n, self.device)
+
+    def _workspace(self, ws, need):
+        if ws is None:
+            return torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        return _tensor("ws", ws, torch.uint8, need, self.device)
+
+
+@dataclass
+class Draft:
+    """Logits, proposals and random numbers of an acceptance step (va_draft)."""
+    logits: object                  # [total_rows][logits_stride]
+    vocab: int
+    tokens: object                  # int32 [total_rows]
+    accept_u: object                # float32 [total_rows]
+    sample_u: object                # float32 [num_seqs]
+    logits_dtype: int = BF16
+    logits_stride: int = 0          # 0: vocab
+    draft_probs: object = None      # float32 [total_rows][draft_stride]
+    draft_stride: int = 0           # 0: vocab
+    temperature: object = None      # float32 [num_seqs]
+
+    def c(self) -> VaDraft:
+        return VaDraft(self.vocab, self.logits_dtype, _ptr(self.logits), self.logits_stride or self.vocab,
+                       _ptr(self.draft_probs), self.draft_stride or self.vocab, _ptr(self.tokens),
+                       _ptr(self.accept_u), _ptr(self.sample_u), _ptr(self.temperature))
+
+
+def _check_rows(p: Problem, mode: int, dev):
+    _tensor("cu_rows", p.cu_rows, torch.int32, p.num_seqs + 1, dev)
+    _tensor("parent", p.parent, torch.int32, p.total_rows if mode else 0, dev, optional=mode == 0)
+    _tensor("seq_kind", p.seq_kind, torch.uint8, p.num_seqs if mode == 2 else 0, dev, optional=mode != 2)
+
+
+class AcceptCall(_Call):
+    """verify_attn_accept.  Returns a dict of accepted_len, accepted_nodes,
+    next_token (and promote_len where given)."""
+    _where = "verify_attn_accept"
+
+    def __init__(self, p: Problem, draft: Draft, mode: int, *, accepted_len=None, accepted_nodes=None,
+                 promote_len=None, next_token=None, ws=None, status=None):
+        self.device = dev = draft.logits.device
+        rows, seqs = p.total_rows, p.num_seqs
+        _check_rows(p, mode, dev)
+        if draft.logits_dtype not in _FLOAT:
+            raise VaError(2, self._where)
+        span = lambda stride: (rows - 1) * (stride or draft.vocab) + draft.vocab if rows else 0  # noqa: E731
+        _tensor("logits", draft.logits, _FLOAT[draft.logits_dtype], span(draft.logits_stride), dev)
+        _tensor("draft_probs", draft.draft_probs, torch.float32, span(draft.draft_stride), dev, optional=True)
+        _tensor("tokens", draft.tokens, torch.int32, rows, dev)
+        _tensor("accept_u", draft.accept_u, torch.float32, rows, dev)
+        _tensor("sample_u", draft.sample_u, torch.float32, seqs, dev)
+        _tensor("temperature", draft.temperature, torch.float32, seqs, dev, optional=True)
+        _tensor("status", status, torch.int32, 1, dev, optional=True)
+        _tensor("promote_len", promote_len, torch.int32, seqs, dev, optional=True)
+        out = {"accepted_len": self._buffer("accepted_len", accepted_len, (seqs,), torch.int32),
+               "accepted_nodes": self._buffer("accepted_nodes", accepted_nodes, (rows,), torch.int32),
+               "next_token": self._buffer("next_token", next_token, (seqs,), torch.int32)}
+        if promote_len is not None:
+            out["promote_len"] = promote_len
+        pc, dc = p.c(), draft.c()
+        need = int(lib.verify_attn_accept_workspace_size(ctypes.byref(pc), ctypes.byref(dc)))
+        ws = self._workspace(ws, need)
+        self._fn, self._out = lib.verify_attn_accept, out
+        self._args = (ctypes.byref(pc), ctypes.byref(dc), mode, _ptr(ws), ws.numel(), _ptr(out["accepted_len"]),
+                      _ptr(out["accepted_nodes"]), _ptr(promote_len), _ptr(out["next_token"]), _ptr(status))
+        self._keep = (p, draft, ws, status, pc, dc)
+
+
+def verify_attn_accept(p: Problem, draft: Draft, mode: int, *, stream=None, **kw):
+    """Which drafted rows the target accepts, and the next token of each
+    sequence (see verify_attn_accept in the header)."""
+    return AcceptCall(p, draft, mode, **kw)(stream)
+
+
+@dataclass
+class PagePool:
+    """Block table (int32 [num_seqs][max_blocks]) and reference counts
+    (int32 [num_blocks]) of a paged cache, on the device."""
+    block_table: object
+    ref_count: object
+
+    def c(self) -> VaPagePool:
+        t = self.block_table
+        return VaPagePool(t.shape[0], t.shape[1], self.ref_count.numel(), _ptr(t), _ptr(self.ref_count))
+
+
+class _PageCall(_Call):
+    def _bind(self, pool: PagePool, status):
+        if not isinstance(pool.block_table, torch.Tensor) or pool.block_table.dim() != 2:
+            raise ValueError("block_table: expected a tensor of two dimensions")
+        self.device = pool.block_table.device
+        _tensor("block_table", pool.block_table, torch.int32, 1)
+        _tensor("ref_count", pool.ref_count, torch.int32, 1, self.device)
+        _tensor("status", status, torch.int32, 1, self.device, optional=True)
+        return pool.c()
+
+    def _commands(self, **kw):
+        n = None
+        for name, t in kw.items():
+            _tensor(name, t, torch.int32, 0, self.device)
+            if n is not None and t.numel() != n:
+                raise ValueError(f"{name}: {t.numel()} commands, the others have {n}")
+            n = t.numel()
+        return n
+
+
+class ForkCall(_PageCall):
+    """verify_attn_pages_fork.  Returns (copies, num_copies)."""
+    _where = "verify_attn_pages_fork"
+
+    def __init__(self, pool: PagePool, src, dst, length, pages, *, copies=None, num_copies=None, ws=None,
+                 status=None):
+        c = self._bind(pool, status)
+        n = self._commands(src=src, dst=dst, length=length, pages=pages)
+        copies = self._buffer("copies", copies, (n, 2), torch.int32)
+        num_copies = self._buffer("num_copies", num_copies, (1,), torch.int32)
+        ws = self._workspace(ws, int(lib.verify_attn_pages_workspace_size(ctypes.byref(c), n)))
+        self._fn, self._out = lib.verify_attn_pages_fork, (copies, num_copies)
+        self._args = (ctypes.byref(c), n, _ptr(src), _ptr(dst), _ptr(length), _ptr(pages), _ptr(copies),
+                      _ptr(num_copies), _ptr(ws), ws.numel(), _ptr(status))
+        self._keep = (pool, src, dst, length, pages, ws, status, c)
+
+
+class FreeCall(_PageCall):
+    """verify_attn_pages_free.  Returns nothing."""
+    _where = "verify_attn_pages_free"
+
+    def __init__(self, pool: PagePool, seq, first, last, *, status=None):
+        c = self._bind(pool, status)
+        n = self._commands(seq=seq, first=first, last=last)
+        self._fn, self._out = lib.verify_attn_pages_free, None
+        self._args = (ctypes.byref(c), n, _ptr(seq), _ptr(first), _ptr(last), _ptr(status))
+        self._keep = (pool, seq, first, last, status, c)
+
+
+class CompactCall(_PageCall):
+    """verify_attn_pages_compact.  Returns (copies, num_copies, live_blocks)."""
+    _where = "verify_attn_pages_compact"
+
+    def __init__(self, pool: PagePool, *, copies=None, num_copies=None, live_blocks=None, ws=None, status=None):
+        c = self._bind(pool, status)
+        copies = self._buffer("copies", copies, (pool.ref_count.numel() // 2, 2), torch.int32)
+        num_copies = self._buffer("num_copies", num_copies, (1,), torch.int32)
+        live_blocks = self._buffer("live_blocks", live_blocks, (1,), torch.int32)
+        ws = self._workspace(ws, int(lib.verify_attn_pages_workspace_size(ctypes.byref(c), 0)))
+        self._fn, self._out = lib.verify_attn_pages_compact, (copies, num_copies, live_blocks)
+        self._args = (ctypes.byref(c), _ptr(copies), _ptr(num_copies), _ptr(live_blocks), _ptr(ws), ws.numel(),
+                      _ptr(status))
+        self._keep = (pool, ws, status, c)
+
+
+class PageCopyCall(_Call):
+    """verify_attn_pages_copy over a list of pools, tensors whose first
+    dimension is the pages (the K and V arrays of every layer)."""
+    _where = "verify_attn_pages_copy"
+
+    def __init__(self, pools, copies, num_copies, *, status=None):
+        if not pools:
+            raise ValueError("pools: none given")
+        self.device = dev = copies.device
+        blocks = pools[0].shape[0]
+        bytes_of = lambda t: t.numel() * t.element_size()  # noqa: E731
+        for i, t in enumerate(pools):
+            _tensor(f"pools[{i}]", t, pools[0].dtype, 1, dev)
+            if t.shape[0] != blocks or bytes_of(t) != bytes_of(pools[0]):
+                raise ValueError(f"pools[{i}]: another size than pools[0]")
+        _tensor("copies", copies, torch.int32, 0)
+        _tensor("num_copies", num_copies, torch.int32, 1, dev)
+        _tensor("status", status, torch.int32, 1, dev, optional=True)
+        ptrs = (ctypes.c_void_p * len(pools))(*[_ptr(t) for t in pools])
+        self._fn, self._out = lib.verify_attn_pages_copy, None
+        self._args = (ptrs, len(pools), bytes_of(pools[0]) // blocks, blocks, _ptr(copies), _ptr(num_copies),
+                      copies.numel() // 2, _ptr(status))
+        self._keep = (pools, copies, num_copies, status)
+
+
+def verify_attn_pages_fork(pool: PagePool, src, dst, length, pages, *, stream=None, **kw):
+    """Fork and grow sequences of a paged cache; returns (copies, num_copies)
+    for verify_attn_pages_copy."""
+    return ForkCall(pool, src, dst, length, pages, **kw)(stream)
+
+
+def verify_attn_pages_free(pool: PagePool, seq, first, last, *, status=None, stream=None):
+    """Give back table entries first[i] .. last[i] - 1 of sequence seq[i]."""
+    return FreeCall(pool, seq, first, last, status=status)(stream)
+
+
+def verify_attn_pages_compact(pool: PagePool, *, stream=None, **kw):
+    """Pull the pages in use together at the front of the pool; returns
+    (copies, num_copies, live_blocks)."""
+    return CompactCall(pool, **kw)(stream)
+
+
+def verify_attn_pages_copy(pools, copies, num_copies, *, status=None, stream: Optional[object] = None):
+    """Copy the page pairs in every pool."""
+    return PageCopyCall(pools, copies, num_copies, status=status)(stream)

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "va_common.cuh"
+#include "va_host.h"
 
 namespace va {
 cudaError_t launch_simt_partial(const Params& p, dim3 grid, cudaStream_t st);
@@ -27,7 +28,7 @@ int tq8_threads();
 int tq8_smem_bytes(int D);
 
 static thread_local cudaError_t g_last_cuda = cudaSuccess;
-static va_status note_cuda(cudaError_t e) {
+va_status note_cuda(cudaError_t e) {
   g_last_cuda = e;
   return VA_ERR_CUDA;
 }
@@ -61,7 +62,7 @@ static bool aligned16(const void* ptr) { return ((uintptr_t)ptr & 15u) == 0; }
 // streams always do.  Checked outside stream capture only: querying a
 // capturing stream's device is not a capturable operation and would
 // invalidate the capture.
-static va_status check_stream_device(cudaStream_t s) {
+va_status check_stream_device(cudaStream_t s) {
   if (s == nullptr || s == cudaStreamLegacy || s == cudaStreamPerThread) return VA_OK;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(s, &cap);
