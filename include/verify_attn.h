@@ -357,6 +357,53 @@ va_status verify_attn_noalloc(const va_problem *p, const va_kv *kv, int32_t mode
                               float *lse, uint32_t *status, void *stream);
 
 /*
+ * Windowed verify attention: every row sees a sliding window and the first
+ * few tokens of its sequence (attention sinks).
+ *
+ * A row at position P (a chain row j: ctx + j; a tree row: ctx + its depth,
+ * 0 for a root) sees, of the tokens that verify_attn_chain / tree / mixed
+ * would show it, those at positions > P - window and those at positions <
+ * sinks.  A context token t stands at t, a drafted row at its own P.  With
+ * window > ctx + rows the result is that of the unwindowed call.
+ *   - K/V of tokens that no row of the sequence sees are not read, and their
+ *     pages need not exist: block-table entries of pages that hold no
+ *     visible token may be anything (pages behind the window can be given
+ *     back, verify_attn_pages_free).  A page that holds visible tokens and
+ *     others may hold anything in the others.
+ *   - K/V that some rows see and others do not must be finite (a masked
+ *     score weighs 0, and 0 times infinity is NaN).
+ *   - num_splits is here the largest number of chunks that a sequence's
+ *     visible tokens are cut into (whole 64-token tiles, at least 128
+ *     tokens); no choice depends on the other sequences of the launch.  About
+ *     SMs / (num_seqs * num_kv_heads) chunks fill the GPU once
+ *     (va_window_splits).
+ *   - o: [total_rows][num_heads][head_dim] of o_dtype (VA_F32, or VA_BF16:
+ *     rounded once, at the end); lse fp32.  ws of at least
+ *     va_window_workspace_size() bytes, 256-byte aligned; its contents carry
+ *     nothing from call to call.  Two calls that may overlap in time need
+ *     two workspaces.
+ * Everything else (types, layouts, tree scratch KV, errors, streams, graph
+ * capture) as for verify_attn_chain / tree / mixed.
+ */
+typedef struct va_window {
+  int32_t window;  /* >= 1: positions a row sees up to and including its own */
+  int32_t sinks;   /* >= 0: first positions that stay visible */
+  int32_t o_dtype; /* VA_F32 or VA_BF16 */
+} va_window;
+
+/* Bytes of device workspace; 0 for an invalid problem. */
+size_t va_window_workspace_size(const va_problem *p, const va_kv *kv, const va_window *w);
+
+/* A chunk count (num_splits) that fills the current device once with this
+ * problem's sequences, at least 256 visible tokens to a chunk; 0 for an
+ * invalid problem. */
+int32_t va_window_splits(const va_problem *p, const va_kv *kv, const va_window *w);
+
+va_status verify_attn_window(const va_problem *p, const va_kv *kv, int32_t mode, const va_window *w,
+                             void *ws, size_t ws_bytes, void *o, float *lse, uint32_t *status,
+                             void *stream);
+
+/*
  * Acceptance of drafted tokens from given random numbers, and the token
  * that follows them: the step between a verify call (whose rows the target's
  * logits come from) and verify_attn_promote.

@@ -191,3 +191,70 @@ def pages_compact(table, ref):
         r[b], r[a] = r[a], 0
     t = np.vectorize(lambda e: to.get(int(e), int(e)))(t).astype(np.int32)
     return t, r, list(to.items()), live, set()
+
+
+# ---------------------------------------------------------------------------
+# Windowed verify attention.
+
+def window_places(ctx: int, n: int, kind: int, parent_local):
+    """Position of each draft row: ctx + j in a chain, ctx + depth in a tree."""
+    depth = []
+    for j in range(n):
+        up = j - 1 if kind == 0 else int(parent_local[j])
+        depth.append(0 if up < 0 else depth[up] + 1)
+    return [ctx + d for d in depth]
+
+
+def window_tokens(ctx: int, n: int, kind: int, parent_local, j: int, window: int, sinks: int) -> list:
+    """Cache tokens (drafts as ctx + a) that row j sees."""
+    place = window_places(ctx, n, kind, parent_local)
+    path, a = [], j
+    while a >= 0:
+        path.append(a)
+        a = a - 1 if kind == 0 else int(parent_local[a])
+    seen = lambda pos: pos > place[j] - window or pos < sinks  # noqa: E731
+    return [t for t in range(ctx) if seen(t)] + [ctx + a for a in sorted(path) if seen(place[a])]
+
+
+def window_case(case, window: int, sinks: int):
+    """O [rows, H, D] and LSE [rows, H] of a case object (see verify_case)."""
+    from . import verify_oracle as vo
+    H, KVH, D = case.num_heads, case.num_kv_heads, case.head_dim
+    G, total = H // KVH, int(case.cu_rows[-1])
+    scale = case.scale or 1.0 / np.sqrt(D)
+    Q = vo.decode_q(np.asarray(case.q).reshape(total, H, -1), case.q_dtype)
+    O, LSE = np.full((total, H, D), np.nan), np.full((total, H), np.nan)
+    flat = {"k": case.k.reshape(-1, case.k.shape[-1]), "v": case.v.reshape(-1, case.v.shape[-1])}
+    for s in range(len(case.ctx_len)):
+        lo, hi, ctx = int(case.cu_rows[s]), int(case.cu_rows[s + 1]), int(case.ctx_len[s])
+        kind = vo.seq_kind_of(s, case.seq_kind, case.mode)
+        scratch = case.draft_k is not None and kind == 1
+        for j in range(hi - lo):
+            t = np.asarray(window_tokens(ctx, hi - lo, kind, case.parent[lo:hi], j, window, sinks), np.int64)
+            for kvh in range(KVH):
+                rows = {}
+                for name, draft in (("k", case.draft_k), ("v", case.draft_v)):
+                    cached = t[t < ctx] if scratch else t
+                    got = flat[name][vo.gather_index(s, kvh, cached, page_size=case.page_size,
+                                                     capacity=case.capacity, num_kv_heads=KVH,
+                                                     block_table=case.block_table)]
+                    if scratch:
+                        got = np.concatenate([got, draft[lo + (t[t >= ctx] - ctx), kvh]])
+                    rows[name] = vo.decode_rows(got, case.kv_dtype)
+                for h in range(kvh * G, (kvh + 1) * G):
+                    O[lo + j, h], LSE[lo + j, h], _ = vo.attend(Q[lo + j, h], rows["k"], rows["v"], scale)
+    return O, LSE
+
+
+def seen_tokens(case, window: int, sinks: int):
+    """Per sequence, the set of cache tokens that some row sees."""
+    from . import verify_oracle as vo
+    out = []
+    for s in range(len(case.ctx_len)):
+        lo, hi, ctx = int(case.cu_rows[s]), int(case.cu_rows[s + 1]), int(case.ctx_len[s])
+        kind = vo.seq_kind_of(s, case.seq_kind, case.mode)
+        seen = set()
+        for j in range(hi - lo):
+            seen |= set(window_tokens(ctx, hi - lo, kind, case.parent[lo:hi], j, window, sinks))
+        out.append(seen)
+    return out

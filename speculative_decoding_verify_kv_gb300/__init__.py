@@ -47,6 +47,7 @@ EXPORTED = ["va_version", "va_status_string", "va_last_cuda_error", "va_workspac
             "verify_attn_chain", "verify_attn_tree", "verify_attn_mixed",
             "va_debug_row_map", "va_debug_gather_index", "va_plan", "va_timing_enable",
             "va_timing_read", "verify_attn_noalloc", "verify_attn_promote", "va_debug_split_ranges",
+            "verify_attn_window", "va_window_workspace_size", "va_window_splits",
             "verify_attn_accept", "verify_attn_accept_workspace_size",
             "verify_attn_pages_workspace_size", "verify_attn_pages_fork", "verify_attn_pages_free",
             "verify_attn_pages_compact", "verify_attn_pages_copy"]
@@ -69,6 +70,10 @@ class VaProblem(ctypes.Structure):
                 ("total_rows", ctypes.c_int32), ("max_rows_per_seq", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("num_splits", ctypes.c_int32),
                 ("flags", ctypes.c_uint32)]
+
+
+class VaWindow(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("o_dtype", ctypes.c_int32)]
 
 
 class VaDraft(ctypes.Structure):
@@ -137,6 +142,10 @@ def _load():
                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
     ptr, i32, i64, size = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     for name, res, args in (
+            ("va_window_workspace_size", size, [P(VaProblem), P(VaKV), P(VaWindow)]),
+            ("va_window_splits", i32, [P(VaProblem), P(VaKV), P(VaWindow)]),
+            ("verify_attn_window", ctypes.c_int,
+             [P(VaProblem), P(VaKV), i32, P(VaWindow), ptr, size, ptr, ptr, ptr, ptr]),
             ("verify_attn_accept_workspace_size", size, [P(VaProblem), P(VaDraft)]),
             ("verify_attn_accept", ctypes.c_int,
              [P(VaProblem), P(VaDraft), i32, ptr, size, ptr, ptr, ptr, ptr, ptr, ptr]),
@@ -410,5 +419,6 @@ def timing_read(max_calls: int = 4096):
 
 
 from ._calls import (AcceptCall, CompactCall, Draft, ForkCall, FreeCall, PageCopyCall,  # noqa: E402,F401
-                     PagePool, verify_attn_accept, verify_attn_pages_compact,
-                     verify_attn_pages_copy, verify_attn_pages_fork, verify_attn_pages_free)
+                     PagePool, Window, WindowCall, verify_attn_accept, verify_attn_pages_compact,
+                     verify_attn_pages_copy, verify_attn_pages_fork, verify_attn_pages_free,
+                     verify_attn_window, window_splits)

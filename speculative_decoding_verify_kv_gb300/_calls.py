@@ -1,5 +1,5 @@
-"""Bound calls of the operators around a verify step: acceptance of drafted
-tokens and the pages of a paged cache.
+"""Bound calls of the operators around a verify step: windowed verify
+attention, acceptance of drafted tokens and the pages of a paged cache.
 
 A serving loop makes the same call step after step over buffers that it
 keeps.  Each ``...Call`` object checks its tensors, allocates what the
@@ -17,7 +17,7 @@ from typing import Optional
 
 import torch
 
-from . import BF16, F32, Problem, VaDraft, VaError, VaPagePool, VaProblem, _ptr, lib
+from . import BF16, F32, KV, Q8_0, Problem, VaDraft, VaError, VaPagePool, VaWindow, _ptr, lib
 
 _FLOAT = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -70,6 +70,80 @@ class _Call:
         if ws is None:
             return torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
         return _tensor("ws", ws, torch.uint8, need, self.device)
+
+
+@dataclass
+class Window:
+    """Sliding window and first visible tokens of a windowed call (va_window)."""
+    window: int
+    sinks: int = 0
+    o_dtype: int = F32
+
+    def c(self) -> VaWindow:
+        return VaWindow(self.window, self.sinks, self.o_dtype)
+
+
+_ELEMENT = {F32: 4, BF16: 2}
+
+
+def _row_bytes(kv: KV) -> int:
+    return kv.head_dim // 32 * 34 if kv.dtype == Q8_0 else kv.head_dim * _ELEMENT.get(kv.dtype, 4)
+
+
+def _check_bytes(name, t, need, dev):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the other arguments on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    if t.numel() * t.element_size() < need:
+        raise ValueError(f"{name}: {t.numel() * t.element_size()} bytes, {need} needed")
+
+
+class WindowCall(_Call):
+    """verify_attn_window.  Returns (o, lse)."""
+    _where = "verify_attn_window"
+
+    def __init__(self, p: Problem, kv: KV, mode: int, window: Window, *, ws=None, o=None, lse=None, status=None):
+        self.device = dev = p.q.device
+        rows, heads, dim = p.total_rows, p.num_heads, kv.head_dim
+        _check_rows(p, mode, dev)
+        _tensor("ctx_len", p.ctx_len, torch.int32, p.num_seqs, dev)
+        _check_bytes("q", p.q, rows * heads * dim * _ELEMENT.get(p.q_dtype, 4), dev)
+        if kv.page_size:
+            _tensor("block_table", kv.block_table, torch.int32, p.num_seqs * kv.max_blocks_per_seq, dev)
+            cells = kv.num_blocks * kv.page_size
+        else:
+            cells = p.num_seqs * kv.capacity
+        for name, t in (("k", kv.k), ("v", kv.v)):
+            _check_bytes(name, t, cells * kv.num_kv_heads * _row_bytes(kv), dev)
+        for name, t in (("draft_k", kv.draft_k), ("draft_v", kv.draft_v)):
+            if t is not None:
+                _check_bytes(name, t, rows * kv.num_kv_heads * _row_bytes(kv), dev)
+        _tensor("status", status, torch.int32, 1, dev, optional=True)
+        if window.o_dtype not in _FLOAT:
+            raise VaError(2, self._where)
+        o = self._buffer("o", o, (rows, heads, dim), _FLOAT[window.o_dtype])
+        lse = self._buffer("lse", lse, (rows, heads), torch.float32)
+        pc, kc, wc = p.c(), kv.c(), window.c()
+        ws = self._workspace(ws, int(lib.va_window_workspace_size(ctypes.byref(pc), ctypes.byref(kc),
+                                                                  ctypes.byref(wc))))
+        self._fn, self._out = lib.verify_attn_window, (o, lse)
+        self._args = (ctypes.byref(pc), ctypes.byref(kc), mode, ctypes.byref(wc), _ptr(ws), ws.numel(), _ptr(o),
+                      _ptr(lse), _ptr(status))
+        self._keep = (p, kv, ws, status, pc, kc, wc)
+
+
+def verify_attn_window(p: Problem, kv: KV, mode: int, window: Window, *, stream=None, **kw):
+    """Verify attention through a sliding window with a few first tokens that
+    stay visible; returns (o, lse)."""
+    return WindowCall(p, kv, mode, window, **kw)(stream)
+
+
+def window_splits(p: Problem, kv: KV, window: Window) -> int:
+    """A num_splits that fills the current GPU once (va_window_splits)."""
+    return int(lib.va_window_splits(ctypes.byref(p.c()), ctypes.byref(kv.c()), ctypes.byref(window.c())))
 
 
 @dataclass

@@ -22,6 +22,7 @@ int simt_smem_bytes(int D);
 cudaError_t launch_umma_partial(const Params& p, dim3 grid, cudaStream_t st);
 int umma_smem_bytes(int D, int kv_dtype);
 int umma_threads(int D, int kv_dtype);
+cudaError_t launch_umma_window(const Params& p, dim3 grid, cudaStream_t st);
 cudaError_t launch_tq8_partial(const Params& p, dim3 grid, cudaStream_t st);
 int tq8_rows_per_block();
 int tq8_threads();
@@ -469,6 +470,82 @@ va_status verify_attn_promote(const va_problem* p, const va_kv* kv, int32_t mode
   Plan pl = make_plan(p, kv);
   Params q = make_params(p, kv, mode, pl, nullptr, nullptr, nullptr, status);
   cudaError_t e = launch_promote(q, accepted_len, accepted_nodes, (cudaStream_t)stream);
+  return e == cudaSuccess ? VA_OK : note_cuda(e);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Windowed verify attention.
+
+namespace va {
+
+static va_status check_window(const va_problem* p, const va_kv* kv, int mode, const va_window* w) {
+  va_status st = check(p, kv, mode);
+  if (st != VA_OK) return st;
+  if (!w || w->window < 1 || w->sinks < 0) return VA_ERR_INVALID_ARG;
+  if (w->o_dtype < VA_F32 || w->o_dtype > VA_Q8_0) return VA_ERR_INVALID_ARG;
+  return w->o_dtype == VA_Q8_0 ? VA_ERR_UNSUPPORTED : VA_OK;
+}
+
+// num_splits is the chunk count of a one-row-block sequence; a sequence of
+// b row blocks takes max(1, num_splits / b) chunks.
+static Plan window_plan(const va_problem* p, const va_kv* kv) {
+  Plan pl = make_plan(p, kv);
+  if (pl.kernel == VA_KERNEL_TENSOR_Q8) {  // the row-major kernel reads contiguous caches by pages here
+    pl.kernel = VA_KERNEL_TENSOR;
+    pl.rows_per_block = kUmmaRowsPerBlock;
+    const int rows = p->max_rows_per_seq * (p->num_heads / kv->num_kv_heads);
+    pl.row_blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
+  }
+  pl.P = pl.slots = p->num_splits;
+  pl.grid.x = (unsigned)(pl.slots > pl.row_blocks ? pl.slots : pl.row_blocks);
+  return pl;
+}
+
+}  // namespace va
+
+extern "C" {
+
+size_t va_window_workspace_size(const va_problem* p, const va_kv* kv, const va_window* w) {
+  if (check_window(p, kv, VA_MODE_CHAIN, w) != VA_OK && check_window(p, kv, VA_MODE_MIXED, w) != VA_OK)
+    return 0;
+  return ws_bytes_for(p, kv, window_plan(p, kv));
+}
+
+int32_t va_window_splits(const va_problem* p, const va_kv* kv, const va_window* w) {
+  if (check_window(p, kv, VA_MODE_CHAIN, w) != VA_OK && check_window(p, kv, VA_MODE_MIXED, w) != VA_OK)
+    return 0;
+  const long long jobs = (long long)p->num_seqs * kv->num_kv_heads;
+  const long long tokens = (long long)w->window + w->sinks + p->max_rows_per_seq;
+  long long n = sm_count() / jobs;
+  if (n > (tokens + 255) / 256) n = (tokens + 255) / 256;
+  if (n > kMaxSubSplits) n = kMaxSubSplits;
+  return (int32_t)(n < 1 ? 1 : n);
+}
+
+va_status verify_attn_window(const va_problem* p, const va_kv* kv, int32_t mode, const va_window* w, void* ws,
+                             size_t ws_bytes, void* o, float* lse, uint32_t* status, void* stream) {
+  va_status st = check_window(p, kv, mode, w);
+  if (st != VA_OK) return st;
+  if (p->total_rows == 0) return VA_OK;
+  if (!o || !lse) return VA_ERR_INVALID_ARG;
+  if (!aligned16(o)) return VA_ERR_ALIGNMENT;
+  Plan pl = window_plan(p, kv);
+  if (!ws || ws_bytes < ws_bytes_for(p, kv, pl)) return VA_ERR_WORKSPACE_TOO_SMALL;
+  if (((uintptr_t)ws & 255u) != 0) return VA_ERR_ALIGNMENT;
+  cudaStream_t cs = (cudaStream_t)stream;
+  st = check_stream_device(cs);
+  if (st != VA_OK) return st;
+  Params q = make_params(p, kv, mode, pl, ws, (float*)o, lse, status);
+  q.min_splits = 1;
+  q.window = w->window;
+  q.sinks = w->sinks;
+  q.o_bf16 = w->o_dtype == VA_BF16;
+  cudaError_t e = pl.kernel == VA_KERNEL_TENSOR ? launch_umma_window(q, pl.grid, cs)
+                                                : launch_simt_partial(q, pl.grid, cs);
+  if (e != cudaSuccess) return note_cuda(e);
+  e = launch_merge(q, cs);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }
 

@@ -47,6 +47,8 @@ struct Params {
   float* o;               // [total_rows][H][D]
   float* lse;             // [total_rows][H]
   unsigned* status;
+  int window, sinks;      // windowed calls: positions a row sees, first positions that stay (window 0: none)
+  int o_bf16;             // o holds bf16
   int rows_per_block;     // query rows (j, g pairs) one partial CTA owns
   int row_blocks;         // ceil(max_rows * G / rows_per_block)
 };
@@ -192,6 +194,62 @@ __device__ __forceinline__ unsigned visible_bits(int kind, unsigned anc, int j, 
     }
     m |= dm;
   }
+  return m;
+}
+
+// Windowed calls.  A row at position pos sees positions [win_low(pos), pos]
+// and [0, sinks).  The rows of a sequence stand at ctx or later, so its
+// visible tokens are [0, sinks) and [b, ctx + n), b = win_low(ctx).  Laid end
+// to end in whole pages they are the span that the chunks cut: span token u
+// is token u below head = sinks rounded up to a page, and u + skip from there
+// on, skip a whole number of pages.  Span tokens [dead_lo, dead_hi) belong to
+// the pages where the gap starts and ends but are seen by no row; every page
+// of the span holds a token that some row sees.
+struct WinSpan {
+  int len, head, skip, dead_lo, dead_hi;
+};
+
+__device__ __forceinline__ int win_low(const Params& p, int pos) {
+  return pos >= p.window ? pos - p.window + 1 : 0;
+}
+
+__device__ __forceinline__ WinSpan win_span(const Params& p, int ctx, int n) {
+  const int b = win_low(p, ctx);
+  const int first = b / kPage * kPage;
+  // Sinks past b are in the window of some row as well.
+  const int sinks = min(p.sinks, b);
+  const int head = (sinks + kPage - 1) / kPage * kPage;
+  WinSpan w;
+  w.skip = first > head ? first - head : 0;
+  w.head = w.skip ? head : 0;
+  w.len = ctx + n - w.skip;
+  w.dead_lo = sinks;
+  w.dead_hi = b - w.skip;
+  return w;
+}
+
+// Ancestor mask anc of tree row j (depth d, standing at ctx + d) without the
+// ancestors outside its window that are no sinks either.  Ancestors come
+// parent first, one position apart.
+__device__ __forceinline__ unsigned window_mask(const Params& p, const int* parent_seq, int j, int ctx,
+                                                unsigned anc) {
+  const int depth = __popc(anc) - 1;
+  unsigned m = 0u;
+  int a = j;
+  for (int d = depth; d >= 0; --d) {
+    if (depth - d < p.window || ctx + d < p.sinks) m |= 1u << a;
+    a = d > 0 ? parent_seq[a] : a;
+  }
+  return m;
+}
+
+// Which of the 32 span tokens t0 .. t0 + 31 a row's window and the sinks
+// allow, as bits (wlo: the span token where its window starts).  A tree's
+// drafts (from vctx on) are decided by their ancestor mask alone.
+__device__ __forceinline__ unsigned window_bits(int kind, int sinks, int wlo, int vctx, int t0) {
+  unsigned m = bit_range(wlo - t0, 32);
+  if (t0 < sinks) m |= bit_range(0, sinks - t0);
+  if (kind == 1) m |= bit_range(vctx - t0, 32);
   return m;
 }
 

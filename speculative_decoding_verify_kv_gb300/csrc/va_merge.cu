@@ -29,7 +29,9 @@ constexpr int kMergeThreads = 256;
 // 16 rows x 24 heads) run in one wave on 152 SMs.  Each group keeps its own
 // maximum M_g; the groups are then combined in ascending group order with
 // the overall maximum M:  l = sum_g 2^(M_g - M) l_g, acc likewise.
-template <int D>
+// WIN: a windowed call (its chunks cut the span of visible tokens; O may be
+// bf16, rounded once here).
+template <int D, bool WIN>
 __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const Params p) {
   constexpr int TC = D / 4;
   constexpr int NG = kMergeThreads / TC;
@@ -68,7 +70,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const Params p)
   int live = p.slots;
   if (!nan && p.S == 1 && sctx >= 0) {
     int lo0, hi0;
-    split_range(sctx + sn, 1, 0, &lo0, &hi0);
+    split_range(WIN ? win_span(p, sctx, sn).len : sctx + sn, 1, 0, &lo0, &hi0);
     live = max(1, live_subs(lo0, hi0, seq_subs(p, sn), p.min_sub));
   }
   for (int s0 = grp; s0 < live && !nan; s0 += BATCH * NG) {
@@ -142,7 +144,15 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const Params p)
     const float inv = 1.f / lt;
     float4 out = bad ? make_float4(NAN, NAN, NAN, NAN)
                      : make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv);
-    *reinterpret_cast<float4*>(p.o + item * D + 4 * tcol) = out;
+    if (WIN && p.o_bf16) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(out.x, out.y), b = __floats2bfloat162_rn(out.z, out.w);
+      uint2 w;
+      memcpy(&w.x, &a, 4);
+      memcpy(&w.y, &b, 4);
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + item * D + 4 * tcol) = w;
+    } else {
+      *reinterpret_cast<float4*>(p.o + item * D + 4 * tcol) = out;
+    }
     if (tcol == 0) p.lse[item] = bad ? NAN : (M + log2f(lt)) * kLn2;
   }
 }
@@ -160,7 +170,8 @@ static cudaError_t launch_merge_t(const Params& p, cudaStream_t st, long long it
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
+  return p.window > 0 ? cudaLaunchKernelEx(&cfg, merge_kernel<D, true>, p)
+                      : cudaLaunchKernelEx(&cfg, merge_kernel<D, false>, p);
 }
 
 cudaError_t launch_merge(const Params& p, cudaStream_t st) {

@@ -30,7 +30,9 @@ constexpr int simt_smem_floats() {
   return kSimtRows * D + kSimtTile * (D + 1) + kSimtTile * D + kSimtRows * kSimtTile;
 }
 
-template <int D, int KVT>
+// WIN: a windowed call; token indexes then count the span of visible tokens
+// (WinSpan).
+template <int D, int KVT, bool WIN>
 __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params p) {
   constexpr int NK = D / 32;  // accumulator columns per lane
   extern __shared__ float sm[];
@@ -40,6 +42,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
   float* Ps = Vs + kSimtTile * D;              // [16][32]
   __shared__ float alpha_s[kSimtRows];
   __shared__ unsigned mask_s[kSimtRows];
+  __shared__ int wlo_s[kSimtRows];
   __shared__ int bad_s;
 
   // The merge kernel may launch now; it waits for this grid to finish.
@@ -64,7 +67,9 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
   const int rbase = rb * kSimtRows;
   if (rbase >= R) return;
   const int nrows = min(kSimtRows, R - rbase);
-  const int L = ctx + n;
+  const WinSpan ws = WIN ? win_span(p, ctx, n) : WinSpan{ctx + n, 0, 0, 0, 0};
+  const int L = ws.len;
+  const int vctx = WIN ? ctx - ws.skip : ctx;  // where the drafts start in the span
   const int kind = seq_kind_of(p, s);
   const bool scratch = uses_scratch(p, kind);  // drafts from the tree scratch KV
 
@@ -74,6 +79,10 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
     int j = (rbase + tid) / p.G;
     bool bad = false;
     mask_s[tid] = row_mask(kind, p.parent + row0, j, &bad);
+    if (WIN && !bad) {
+      wlo_s[tid] = win_low(p, ctx + (kind == 1 ? __popc(mask_s[tid]) - 1 : j)) - ws.skip;
+      if (kind == 1) mask_s[tid] = window_mask(p, p.parent + row0, j, ctx, mask_s[tid]);
+    }
     if (bad) atomicOr(&bad_s, 1);
   }
   __syncthreads();
@@ -109,12 +118,14 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
         int t = i / D, d = i % D;
         int tok = t0 + t;
         float kx = 0.f, vx = 0.f;
-        if (tok < shi && tok >= ctx && scratch) {
-          const long long row = scratch_row(p, row0, kvh, tok - ctx);
+        if (WIN && tok >= ws.dead_lo && tok < ws.dead_hi) {
+          // seen by no row: not read
+        } else if (tok < shi && tok >= vctx && scratch) {
+          const long long row = scratch_row(p, row0, kvh, tok - vctx);
           kx = load_kv<KVT>(p.dk, row, p.row_bytes, d);
           vx = load_kv<KVT>(p.dv, row, p.row_bytes, d);
         } else if (tok < shi) {
-          long long row = kv_row(p, s, kvh, tok);
+          long long row = kv_row(p, s, kvh, WIN && tok >= ws.head ? tok + ws.skip : tok);
           if (row < 0) {
             atomicOr(&bad_s, 2);
           } else {
@@ -140,7 +151,9 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
 #pragma unroll 8
         for (int d = 0; d < D; ++d) dot = fmaf(Qs[rl * D + d], Ks[lane * (D + 1) + d], dot);
         bool vis = tok < shi &&
-                   (tok < ctx || draft_visible(kind, mask_s[rl], (rbase + rl) / p.G, tok - ctx));
+                   (tok < vctx || draft_visible(kind, mask_s[rl], (rbase + rl) / p.G, tok - vctx));
+        if (WIN)
+          vis = vis && (tok < p.sinks || tok >= wlo_s[rl] || (kind == 1 && tok >= vctx));
         float s2 = vis ? dot * p.scale_log2 : -INFINITY;
         float mt = s2;
 #pragma unroll
@@ -194,12 +207,12 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
   }
 }
 
-template <int D, int KVT>
+template <int D, int KVT, bool WIN>
 static cudaError_t launch_simt_t(const Params& p, dim3 grid, cudaStream_t st) {
   constexpr int smem = simt_smem_floats<D>() * 4;
   static bool attr_set = false;
   if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(simt_partial_kernel<D, KVT>,
+    cudaError_t e = cudaFuncSetAttribute(simt_partial_kernel<D, KVT, WIN>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     attr_set = true;
@@ -215,7 +228,7 @@ static cudaError_t launch_simt_t(const Params& p, dim3 grid, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, simt_partial_kernel<D, KVT>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, simt_partial_kernel<D, KVT, WIN>, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -229,8 +242,10 @@ int simt_smem_bytes(int D) {
 }
 
 cudaError_t launch_simt_partial(const Params& p, dim3 grid, cudaStream_t st) {
-#define VA_SIMT_CASE(DD, KT) \
-  if (p.D == DD && p.kv_dtype == KT) return launch_simt_t<DD, KT>(p, grid, st);
+#define VA_SIMT_CASE(DD, KT)                                                  \
+  if (p.D == DD && p.kv_dtype == KT)                                          \
+    return p.window > 0 ? launch_simt_t<DD, KT, true>(p, grid, st)            \
+                        : launch_simt_t<DD, KT, false>(p, grid, st);
   VA_SIMT_CASE(64, VA_F32) VA_SIMT_CASE(64, VA_BF16) VA_SIMT_CASE(64, VA_Q8_0)
   VA_SIMT_CASE(128, VA_F32) VA_SIMT_CASE(128, VA_BF16) VA_SIMT_CASE(128, VA_Q8_0)
   VA_SIMT_CASE(256, VA_F32) VA_SIMT_CASE(256, VA_BF16) VA_SIMT_CASE(256, VA_Q8_0)

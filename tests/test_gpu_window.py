@@ -1,0 +1,204 @@
+"""Windowed verify attention on the GPU against the fp64 oracle (bounds in
+window_util).  Tokens that no row sees hold NaN, and the block-table entries
+of pages without a visible token hold no page."""
+import dataclasses
+
+import numpy as np
+import pytest
+
+import oracle
+import oracle.step_oracle as so
+import synthetic as sy
+from window_util import check, poison_unseen
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import speculative_decoding_verify_kv_gb300 as va  # noqa: E402
+
+
+def run(case, window, sinks, out=va.F32, splits=1, flags=0, status=0, device="cuda"):
+    p, kv, mode = va.upload(case, device, num_splits=splits, flags=flags)
+    st = torch.zeros(1, dtype=torch.int32, device=device)
+    o, lse = va.verify_attn_window(p, kv, mode, va.Window(window, sinks, out), status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == status, f"{int(st.item()):#x}"
+    return o.float().cpu().numpy(), lse.cpu().numpy()
+
+
+def make(kv, heads, kvh, dim, ctx, rows, kinds=None, mode="chain", paged=False, seed=0):
+    return sy.make_case("window", num_heads=heads, num_kv_heads=kvh, head_dim=dim, kv_dtype=kv,
+                        q_dtype="f32" if kv == "f32" else "bf16", ctx=ctx, rows=rows, kinds=kinds, mode=mode,
+                        paged=paged, seed=seed, extra_blocks=3 if paged else 0)
+
+
+SHAPES = [("bf16", 8, 2, 128), ("bf16", 6, 1, 256), ("bf16", 4, 4, 64), ("q8_0", 6, 1, 256), ("q8_0", 8, 2, 128),
+          ("q8_0", 2, 2, 64), ("f32", 4, 1, 64), ("f32", 2, 1, 128), ("f32", 3, 3, 256)]
+
+
+@pytest.mark.parametrize("kv,heads,kvh,dim", SHAPES)
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("window,sinks,splits", [(1, 0, 1), (1, 3, 2), (17, 4, 1), (64, 0, 3), (100, 33, 2),
+                                                 (250, 16, 4), (512, 200, 1)])
+def test_chains(kv, heads, kvh, dim, paged, window, sinks, splits):
+    case = make(kv, heads, kvh, dim, [0, 5, 63, 200, 777], [1, 3, 16, 1, 5], paged=paged, seed=window + dim)
+    case = poison_unseen(case, window, sinks)
+    ref = so.window_case(case, window, sinks)
+    for out in (va.F32, va.BF16):
+        check(case, *run(case, window, sinks, out, splits), ref, out == va.BF16, f"out {out}")
+
+
+@pytest.mark.parametrize("kv,heads,kvh,dim", SHAPES)
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("scratch", [False, True])
+@pytest.mark.parametrize("window,sinks,splits", [(1, 0, 1), (2, 1, 1), (5, 200, 2), (90, 18, 3), (333, 0, 2)])
+def test_trees_and_direct_rows(kv, heads, kvh, dim, paged, scratch, window, sinks, splits):
+    """Trees deeper than the window, sinks that reach into the drafts."""
+    case = make(kv, heads, kvh, dim, [0, 190, 401, 3, 130], [32, 8, 1, 9, 7], kinds=[1, 1, 0, 1, 0], mode="mixed",
+                paged=paged, seed=window * 7 + dim)
+    if scratch:
+        case = sy.with_tree_scratch(case)
+        keep = dataclasses.replace(case)
+        case = poison_unseen(case, window, sinks)
+        case = dataclasses.replace(case, draft_k=keep.draft_k, draft_v=keep.draft_v)
+    else:
+        case = poison_unseen(case, window, sinks)
+    ref = so.window_case(case, window, sinks)
+    check(case, *run(case, window, sinks, va.F32, splits), ref, False)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "q8_0"])
+def test_deep_trees(kv):
+    """Chains as trees: a window shorter than the tree."""
+    n = 32
+    case = make(kv, 4, 2, 128, [100, 7], [n, n], mode="tree", paged=True, seed=3)
+    par = np.concatenate([np.arange(-1, n - 1)] * 2).astype(np.int32)
+    case = dataclasses.replace(case, parent=par)
+    for window, sinks in [(3, 0), (20, 9), (40, 103)]:
+        c = poison_unseen(case, window, sinks)
+        check(c, *run(c, window, sinks, splits=2), so.window_case(c, window, sinks), False)
+        chain = dataclasses.replace(c, mode="chain", seq_kind=np.zeros(2, np.uint8))
+        a, b = run(c, window, sinks, splits=2), run(chain, window, sinks, splits=2)
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("kv,heads,kvh,dim", SHAPES)
+def test_many_rows(kv, heads, kvh, dim):
+    """A prompt segment of several row blocks beside a direct row."""
+    case = make(kv, heads, kvh, dim, [150, 260], [150, 1], paged=True, seed=dim)
+    for window, sinks, splits in [(40, 5, 1), (170, 0, 5)]:
+        c = poison_unseen(case, window, sinks)
+        check(c, *run(c, window, sinks, splits=splits), so.window_case(c, window, sinks), False)
+
+
+@pytest.mark.parametrize("kv,heads,kvh,dim", SHAPES)
+@pytest.mark.parametrize("flags", [0, va.FLAG_CUDA_CORES])
+def test_a_wide_window_is_the_unwindowed_call(kv, heads, kvh, dim, flags):
+    case = make(kv, heads, kvh, dim, [300, 17, 0], [8, 1, 4], kinds=[1, 0, 1], mode="mixed", paged=True, seed=4)
+    O, L = oracle.verify_case(case)
+    for window in (2 ** 31 - 1, 310):
+        check(case, *run(case, window, 0, splits=2, flags=flags), (O, L), False)
+
+
+@pytest.mark.parametrize("kv,heads,kvh,dim", SHAPES)
+def test_cuda_core_kernel(kv, heads, kvh, dim):
+    case = make(kv, heads, kvh, dim, [200, 90], [16, 6], kinds=[0, 1], mode="mixed", paged=True, seed=8)
+    c = poison_unseen(case, 50, 20, entry=2 ** 30)
+    check(c, *run(c, 50, 20, splits=2, flags=va.FLAG_CUDA_CORES), so.window_case(c, 50, 20), False)
+
+
+def test_a_sequence_does_not_depend_on_the_launch():
+    case = make("q8_0", 6, 1, 256, [700, 90, 333, 40], [16, 1, 8, 1], kinds=[0, 0, 1, 0], mode="mixed", paged=True,
+                seed=12)
+    whole = run(case, 300, 4, splits=3)
+    for s in range(4):
+        one = sy.subset_sequences(case, [s])
+        got = run(one, 300, 4, splits=3)
+        a, b = int(case.cu_rows[s]), int(case.cu_rows[s + 1])
+        assert np.array_equal(got[0], whole[0][a:b]) and np.array_equal(got[1], whole[1][a:b])
+
+
+@pytest.mark.parametrize("kv,heads,kvh,dim", [SHAPES[0], SHAPES[3], SHAPES[6]])
+def test_device_errors_poison_only_their_sequence(kv, heads, kvh, dim):
+    case = make(kv, heads, kvh, dim, [200, 90, 64], [4, 4, 4], kinds=[0, 1, 0], mode="mixed", paged=True, seed=2)
+    ref = so.window_case(case, 40, 3)
+    for what in ("block", "parent", "ctx", "rows"):
+        c = dataclasses.replace(case, block_table=case.block_table.copy(), parent=case.parent.copy(),
+                                ctx_len=case.ctx_len.copy(), cu_rows=case.cu_rows.copy())
+        p, kvs, mode = va.upload(c, "cuda", num_splits=2)
+        if what == "block":      # a page inside the window; pages out of sight hold none
+            kvs.block_table[1, 4] = 10 ** 6
+            kvs.block_table[0, 3] = -5
+        elif what == "parent":
+            p.parent[5] = 3
+        elif what == "ctx":
+            p.ctx_len[1] = 10 ** 6
+        else:
+            p.cu_rows[1:3] = torch.tensor([8, 6], dtype=torch.int32)
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        o, lse = va.verify_attn_window(p, kvs, mode, va.Window(40, 3), status=st)
+        bit = {"block": va.DEV_BAD_BLOCK, "parent": va.DEV_BAD_PARENT, "ctx": va.DEV_CTX_OVERFLOW,
+               "rows": va.DEV_BAD_ROWS}[what]
+        assert int(st.item()) == bit, (what, hex(int(st.item())))
+        o, lse = o.cpu().numpy(), lse.cpu().numpy()
+        if what == "rows":
+            continue
+        assert np.isnan(lse[4:8]).any(), what
+        keep = np.r_[0:4, 8:12]
+        sub = dataclasses.replace(case)
+        check(sub, o[keep], lse[keep], (ref[0][keep], ref[1][keep]), False, what)
+
+
+def test_graphs_streams_and_rows_behind_the_last_sequence():
+    case = make("bf16", 8, 2, 128, [500, 90], [4, 1], paged=True, seed=6)
+    p, kv, mode = va.upload(case, "cuda", num_splits=2)
+    ref = so.window_case(case, 128, 4)
+    calls = [va.WindowCall(p, kv, mode, va.Window(128, 4, va.BF16)) for _ in range(2)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for c in calls:
+            c()
+    torch.cuda.synchronize()
+    graphs = []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = c()
+        graphs.append((g, out))
+    for _, (o, lse) in graphs:
+        o.zero_(), lse.zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, (o, lse) in graphs:
+        check(case, o.float().cpu().numpy(), lse.cpu().numpy(), ref, True)
+
+
+def test_offsets_past_32_bits():
+    """A contiguous bf16 cache of two times 4.8 GB: windows past 2^31 elements and 2^32 bytes."""
+    cap, ctx = 9 * 2 ** 20, 9 * 2 ** 20 - 30
+    k = torch.zeros(2, 1, cap, 256, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for t in (slice(0, 4), slice(ctx - 40, ctx + 2)):
+        for x in (k, v):
+            x[:, :, t] = torch.randn(x[:, :, t].shape, generator=g, device="cuda", dtype=torch.bfloat16)
+    q = torch.randn(4, 4, 256, generator=g, device="cuda", dtype=torch.bfloat16)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    p = va.Problem(2, 4, va.BF16, q, i32(0, 2, 4), i32(ctx, ctx), i32(-1, 0, -1, 0),
+                   torch.zeros(2, dtype=torch.uint8, device="cuda"), 4, 2, num_splits=1)
+    o, lse = va.verify_attn_window(p, va.KV(va.BF16, 1, 256, k, v, capacity=cap), 0, va.Window(30, 4))
+    for s in range(2):
+        for j in range(2):
+            pos = ctx + j
+            t = torch.tensor(list(range(4)) + list(range(pos - 29, pos + 1)), device="cuda")
+            z = q[2 * s + j].double() @ k[s, 0, t].double().T / 256 ** 0.5
+            want = torch.softmax(z, -1) @ v[s, 0, t].double()
+            assert (o[2 * s + j].double() - want).abs().max() < 2e-4
+            assert (lse[2 * s + j].double() - torch.logsumexp(z, -1)).abs().max() < 1e-4

@@ -124,3 +124,61 @@ def test_bound_calls_check_their_tensors():
                  ("temperature", z(1, dt=f)), ("logits_dtype", va.Q8_0)]:
         with pytest.raises((TypeError, ValueError, va.VaError)):
             va.AcceptCall(p, va.Draft(**{**good, k: v}), 0)
+
+
+def _window(w=(128, 4, va.F32), fn="verify_attn_window", p=None, kv=None, mode=0, ws=FAKE, b=1 << 40, o=FAKE, lse=FAKE):
+    d = dict(num_seqs=2, num_heads=8, q_dtype=va.BF16, q=FAKE, cu_rows=FAKE, ctx_len=FAKE, parent=FAKE, seq_kind=FAKE,
+             total_rows=8, max_rows_per_seq=4, scale=0.0, num_splits=2, flags=0)
+    d.update(p or {})
+    c = dict(dtype=va.BF16, num_kv_heads=2, head_dim=128, k=FAKE, v=FAKE, page_size=16, capacity=0, block_table=FAKE,
+             max_blocks_per_seq=9, num_blocks=99, draft_k=None, draft_v=None)
+    c.update(kv or {})
+    pc, kc, wc = va.VaProblem(*d.values()), va.VaKV(*c.values()), va.VaWindow(*w)
+    a = (ctypes.byref(pc), ctypes.byref(kc))
+    if fn != "verify_attn_window":
+        return getattr(va.lib, fn)(*a, ctypes.byref(wc))
+    return va.lib.verify_attn_window(*a, mode, ctypes.byref(wc), ws, b, o, lse, None, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(w=(0, 4, 0)), 1), (dict(w=(-1, 4, 0)), 1), (dict(w=(8, -1, 0)), 1), (dict(w=(8, 0, 9)), 1),
+    (dict(w=(8, 0, va.Q8_0)), 2), (dict(mode=7), 1), (dict(p=dict(num_seqs=0)), 1), (dict(kv=dict(head_dim=96)), 2),
+    (dict(p=dict(q_dtype=va.F32)), 2), (dict(p=dict(num_splits=257)), 2), (dict(o=None), 1), (dict(lse=None), 1),
+    (dict(o=FAKE + 8), 3), (dict(ws=None), 4), (dict(b=1000), 4), (dict(ws=FAKE + 16), 3), (dict(kv=dict(k=FAKE + 4)), 3),
+])
+def test_window_refusals(kw, code):
+    assert _window(**kw) == code
+    if "w" in kw:
+        assert _window(w=kw["w"], fn="va_window_workspace_size") == 0
+        assert _window(w=kw["w"], fn="va_window_splits") == 0
+
+
+def test_window_workspace_and_splits():
+    # slots * rows * heads * (D + 2) floats, each part a multiple of 256 bytes.
+    assert _window(fn="va_window_workspace_size") == 2 * 8 * 8 * 130 * 4
+    assert _window(fn="va_window_splits") == 1                       # 136 tokens
+    assert _window(w=(4096, 0, 0), fn="va_window_splits") == 16
+    assert _window(w=(4096, 0, 0), p=dict(num_seqs=300), fn="va_window_splits") == 1
+
+
+def test_window_calls_check_their_tensors():
+    z = lambda *s, dt=torch.int32: torch.zeros(s, dtype=dt)  # noqa: E731
+    p = lambda **kw: va.Problem(**{**dict(  # noqa: E731
+        num_seqs=2, num_heads=4, q_dtype=va.BF16, q=z(3, 4, 64, dt=torch.bfloat16), cu_rows=z(3), ctx_len=z(2),
+        parent=z(3), seq_kind=z(2, dt=torch.uint8), total_rows=3, max_rows_per_seq=2), **kw})
+    kv = lambda **kw: va.KV(**{**dict(  # noqa: E731
+        dtype=va.BF16, num_kv_heads=2, head_dim=64, k=z(5, 2, 16, 64, dt=torch.bfloat16),
+        v=z(5, 2, 16, 64, dt=torch.bfloat16), page_size=16, block_table=z(2, 4), max_blocks_per_seq=4, num_blocks=5),
+        **kw})
+    w = va.Window(8, 1, va.BF16)
+    call = va.WindowCall(p(), kv(), 0, w)
+    assert call._out[0].dtype == torch.bfloat16
+    with pytest.raises(ValueError, match="not on a GPU"):
+        call()
+    for bad in (dict(p=p(q=z(3, 4, 63, dt=torch.bfloat16))), dict(p=p(ctx_len=z(1))), dict(p=p(cu_rows=z(2))),
+                dict(kv=kv(k=z(5, 2, 16, 63, dt=torch.bfloat16))), dict(kv=kv(block_table=z(7))),
+                dict(kv=kv(draft_k=z(3, 2, 60, dt=torch.bfloat16), draft_v=z(3, 2, 64, dt=torch.bfloat16))),
+                dict(w=va.Window(8, 1, va.Q8_0)), dict(o=z(3, 4, 64, dt=torch.float32)), dict(status=z(1, dt=torch.int64))):
+        kw = {k: v for k, v in bad.items() if k not in ("p", "kv", "w")}
+        with pytest.raises((TypeError, ValueError, va.VaError)):
+            va.WindowCall(bad.get("p", p()), bad.get("kv", kv()), 0, bad.get("w", w), **kw)
