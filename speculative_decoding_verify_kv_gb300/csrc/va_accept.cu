@@ -17,10 +17,11 @@
 // sampling, applied to one sibling after another).
 //
 // Two kernels.  accept_stats_kernel reads the logits of every row that has
-// a child, once, in pieces of 8,192 values (one CTA each, the whole piece
-// in registers): the piece's maximum, its sum of exponentials relative to
-// it, and the place of the maximum.  It is bound by the logits' bytes.
-// accept_walk_kernel gives each sequence a cluster of eight CTAs: every
+// a child, once, in pieces of 4,096 values (one warp each, the next 2 KB in
+// flight while the last are summed): the piece's maximum, its sum of
+// exponentials relative to it, and the place of the maximum.  It is bound
+// by the logits' bytes.
+// accept_walk_kernel gives each sequence a cluster of 8 or 16 CTAs: every
 // CTA walks the path redundantly (the tests need one logit and one drafted
 // probability per row, fetched for all rows at once), and the cluster then
 // works through the one row that the next token is drawn from.
@@ -30,12 +31,15 @@
 // every later border by e, so that over a vocabulary the share of v that
 // draws another token is e times the number of tokens that matter.  The
 // weights of the last row are therefore 64-bit fixed-point numbers
-// (2^43 exp(z - max), relative error about 2^-32) summed as integers: no
-// order of summation changes the result, and borders move by about 1e-10.
+// (2^41 exp(z - max) for a vocabulary of 2^17, relative error about 2^-32)
+// summed as integers: no order of summation changes the result, and borders
+// move by about 1e-10.
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
 #include <string.h>
+
+#include <atomic>
 
 #include "va_common.cuh"
 #include "va_host.h"
@@ -43,19 +47,22 @@
 namespace va {
 namespace cg = cooperative_groups;
 
-constexpr int kPiece = 8192;         // values per statistics CTA
+constexpr int kPiece = 4096;         // values per statistics warp
 constexpr int kStatThreads = 256;
-constexpr int kPerThread = kPiece / kStatThreads;
+constexpr int kStatWarps = kStatThreads / 32;
 constexpr int kWalkThreads = 512;
 constexpr int kWalkWarps = kWalkThreads / 32;
-constexpr int kCluster = 8;          // CTAs per sequence (the portable limit)
-constexpr int kSegs = kCluster * kWalkWarps;
-constexpr int kMaxVocab = 1 << 20;   // 2^20 weights of 2^43 fit 63 bits
+constexpr int kMaxCluster = 16;      // CTAs per sequence: 8, or 16 (see walk_cluster)
+constexpr int kUnit = 256;           // values a warp takes at a time, 8 per lane
+constexpr int kMaxVocab = 1 << 20;
+constexpr int kMaxCacheBytes = 72 * 1024;  // of a CTA's weights in shared memory: two CTAs share an SM
 constexpr float kMinTemperature = 1e-6f;  // below it, only 0
 
 struct AcceptParams {
   int num_seqs, total_rows, max_rows, mode;
   int vocab, pieces;
+  int weight_bits;        // weights are 2^weight_bits exp(..)
+  int cached;             // the walk keeps its row's weights in shared memory
   const int* cu_rows;
   const int* parent;
   const unsigned char* seq_kind;
@@ -110,23 +117,59 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Statistics of one piece of one row.  grid = (pieces, max_rows, num_seqs).
-// The cut into pieces depends on the vocabulary and the row's alignment
-// alone, so a row's statistics do not depend on what shares the launch.
+// Four 16-byte vectors of a row per lane: values [i, i + VEC) and so on, 32
+// lanes apart; values outside the row are -inf.
+template <typename T>
+struct RowStep {
+  static constexpr int VEC = 16 / (int)sizeof(T);
+  static constexpr int N = 4 * VEC;
+  uint4 w[4];
+  __device__ __forceinline__ void load(const T* row, int vocab, int i) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int a = i + k * 32 * VEC;
+      if (a >= 0 && a + VEC <= vocab) {
+        w[k] = __ldcs(reinterpret_cast<const uint4*>(row + a));
+      } else {
+        uint32_t c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (sizeof(T) == 4) {
+            c[e] = a + e >= 0 && a + e < vocab ? reinterpret_cast<const uint32_t*>(row)[a + e] : 0xFF800000u;
+          } else {
+            const unsigned short* r = reinterpret_cast<const unsigned short*>(row);
+            const int b = a + 2 * e;
+            c[e] = (b >= 0 && b < vocab ? r[b] : 0xFF80u) |
+                   (b + 1 >= 0 && b + 1 < vocab ? (uint32_t)r[b + 1] << 16 : 0xFF800000u);
+          }
+        }
+        w[k] = make_uint4(c[0], c[1], c[2], c[3]);
+      }
+    }
+  }
+  // Value e of vector k.
+  __device__ __forceinline__ float at(int k, int e) const {
+    const uint32_t c[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+    if (sizeof(T) == 4) return __uint_as_float(c[e]);
+    return __uint_as_float(e & 1 ? c[e / 2] & 0xFFFF0000u : c[e / 2] << 16);
+  }
+};
+
+// Statistics of one piece of one row per warp.  grid = (pieces / 8,
+// max_rows, num_seqs).  The cut into pieces depends on the vocabulary and
+// the row's alignment alone, so a row's statistics do not depend on what
+// shares the launch.  A lane keeps its own running maximum and sum.
 template <typename T>
 __global__ void __launch_bounds__(kStatThreads) accept_stats_kernel(const AcceptParams p) {
-  constexpr int VEC = 16 / (int)sizeof(T);
-  constexpr int NV = kPerThread / VEC;
-  __shared__ float red[kStatThreads / 32];
-  __shared__ float red2[kStatThreads / 32];
-  __shared__ int redi[kStatThreads / 32];
+  using S = RowStep<T>;
+  constexpr int STEP = 32 * S::N;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int s = blockIdx.z, j = blockIdx.y, piece = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int s = blockIdx.z, j = blockIdx.y;
+  const int lane = threadIdx.x & 31, piece = blockIdx.x * kStatWarps + (threadIdx.x >> 5);
   const int kind = accept_kind(p, s);
   int row0, n;
-  if (!accept_rows(p, s, kind, &row0, &n) || j >= n) return;
+  if (!accept_rows(p, s, kind, &row0, &n) || j >= n || piece >= p.pieces) return;
   bool child = j + 1 < n;
   if (kind == 1)  // n <= 32: one row per lane
     child = __any_sync(0xffffffffu, lane > j && lane < n && p.parent[row0 + lane] == j);
@@ -136,144 +179,138 @@ __global__ void __launch_bounds__(kStatThreads) accept_stats_kernel(const Accept
   // Values are counted from the 16-byte boundary at or before the row.
   const int pad = (int)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
   const float temp = accept_temperature(p, s);
-  float x[kPerThread];
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = piece * kPiece + (k * kStatThreads + tid) * VEC - pad;
-    if (i >= 0 && i + VEC <= p.vocab) {
-      const uint4 w = __ldcs(reinterpret_cast<const uint4*>(row + i));
-      const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (sizeof(T) == 4) x[k * VEC + e] = __uint_as_float(c[e]);
-        else x[k * VEC + e] = __uint_as_float(e & 1 ? c[e / 2] & 0xFFFF0000u : c[e / 2] << 16);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        x[k * VEC + e] = i + e >= 0 && i + e < p.vocab ? to_float<T>(row[i + e]) : -INFINITY;
-    }
-  }
-  float m = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < kPerThread; ++e) m = fmaxf(m, x[e]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  m = red[0];
-#pragma unroll
-  for (int w = 1; w < kStatThreads / 32; ++w) m = fmaxf(m, red[w]);
-
-  float sum = 0.f;
+  const int first = piece * kPiece + lane * S::VEC - pad;
+  const int steps = min(kPiece / STEP, (p.vocab + pad - piece * kPiece + STEP - 1) / STEP);
+  S cur, next;
+  if (steps > 0) cur.load(row, p.vocab, first);
+  float m = -INFINITY, sum = 0.f;
   int at = INT_MAX;
-  if (temp > 0.f) {
-    // exp((x - m) / T); a piece without a finite value (m = -inf) sums to 0.
-    const float c = 1.4426950408889634f / temp;
-    if (m != -INFINITY) {
+  const float c = temp > 0.f ? 1.4426950408889634f / temp : 0.f;
+  for (int t = 0; t < steps; ++t) {
+    if (t + 1 < steps) next.load(row, p.vocab, first + (t + 1) * STEP);
+    float tm = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e) sum += exp2_fast((x[e] - m) * c);
-    } else {
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e)
-        if (x[e] != x[e]) sum = NAN;
-    }
-  } else {
-#pragma unroll
-    for (int k = NV - 1; k >= 0; --k)
-#pragma unroll
-      for (int e = VEC - 1; e >= 0; --e) {
-        if (x[k * VEC + e] == m) at = piece * kPiece + (k * kStatThreads + tid) * VEC + e - pad;
-        if (!(x[k * VEC + e] < INFINITY)) sum = NAN;  // NaN or +inf: no distribution
+      for (int e = 0; e < S::VEC; ++e) tm = fmaxf(tm, cur.at(k, e));
+    if (temp > 0.f) {
+      if (tm > m) {
+        sum *= exp2_fast((m - tm) * c);  // exp2(-inf) = 0 at the first
+        m = tm;
       }
-    if (m == -INFINITY) at = INT_MAX;
+      // exp((x - m) / T); while nothing is finite only a NaN shows.
+      const float off = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < S::VEC; ++e) sum += exp2_fast((cur.at(k, e) + off) * c);
+    } else {
+      if (tm > m) {
+        m = tm;
+#pragma unroll
+        for (int k = 3; k >= 0; --k)
+#pragma unroll
+          for (int e = S::VEC - 1; e >= 0; --e)
+            if (cur.at(k, e) == m) at = first + t * STEP + k * 32 * S::VEC + e;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < S::VEC; ++e)
+          if (!(cur.at(k, e) < INFINITY)) sum = NAN;  // NaN or +inf: no distribution
+    }
+    cur = next;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    at = min(at, __shfl_xor_sync(0xffffffffu, at, o));
-  }
-  if (lane == 0) {
-    red2[warp] = sum;
-    redi[warp] = at;
-  }
-  __syncthreads();
-  if (tid == 0) {
-#pragma unroll
-    for (int w = 1; w < kStatThreads / 32; ++w) {
-      sum += red2[w];
-      at = min(at, redi[w]);
+    const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, sum, o);
+    const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+    const float nm = fmaxf(m, om);
+    if (temp > 0.f && nm != -INFINITY) {
+      sum = sum * exp2_fast((m - nm) * c) + os * exp2_fast((om - nm) * c);
+    } else {
+      sum += os;
     }
-    p.stats[(long long)(row0 + j) * p.pieces + piece] = make_float4(m, sum, __int_as_float(at), 0.f);
+    at = om > m ? oa : om == m ? min(at, oa) : at;
+    m = nm;
   }
+  if (lane == 0)
+    p.stats[(long long)(row0 + j) * p.pieces + piece] = make_float4(m, sum, __int_as_float(at), 0.f);
 }
 
 // ---------------------------------------------------------------------------
-// Fixed-point weights: 2^(j / 64) * 2^43, rounded, for the reduction
-// exp(y) = 2^(k / 64) exp(r), k = rint(64 y / ln 2), |r| <= ln 2 / 128 (the
+// Fixed-point weights: 2^(j / 32) * 2^43, rounded, for the reduction
+// exp(y) = 2^(k / 32) exp(r), k = rint(32 y / ln 2), |r| <= ln 2 / 64 (the
 // argument reduction in two parts of Cody and Waite; exp(r) - 1 by its
 // Taylor series).
-__device__ const unsigned long long kPow2[64] = {
-    0x80000000000ull, 0x8164d1f3bc0ull, 0x82cd8698ac3ull, 0x843a28c3aceull,
-    0x85aac367cc5ull, 0x871f61969e9ull, 0x88980e8092eull, 0x8a14d575497ull,
-    0x8b95c1e3ea9ull, 0x8d1adf5b7e6ull, 0x8ea4398b45dull, 0x9031dc43146ull,
-    0x91c3d373ab1ull, 0x935a2b2f13eull, 0x94f4efa8fefull, 0x96942d37202ull,
-    0x9837f0518dcull, 0x99e0459320bull, 0x9b8d39b9d55ull, 0x9d3ed9a72d0ull,
-    0x9ef5326091aull, 0xa0b0510fb97ull, 0xa27043030c5ull, 0xa43515ae09eull,
-    0xa5fed6a9b15ull, 0xa7cd93b4e96ull, 0xa9a15ab4ea8ull, 0xab7a39b5a94ull,
-    0xad583eea42aull, 0xaf3b78ad691ull, 0xb123f581d2bull, 0xb311c412a91ull,
-    0xb504f333f9eull, 0xb6fd91e328dull, 0xb8fbaf47630ull, 0xbaff5ab2134ull,
-    0xbd08a39f581ull, 0xbf1799b67a7ull, 0xc12c4cca667ull, 0xc346ccda249ull,
-    0xc5672a11550ull, 0xc78d74c8abcull, 0xc9b9bd866e3ull, 0xcbec14fef27ull,
-    0xce248c151f8ull, 0xd06333daef3ull, 0xd2a81d91f13ull, 0xd4f35aabcffull,
-    0xd744fccad6aull, 0xd99d15c278bull, 0xdbfbb797dafull, 0xde60f4825e1ull,
-    0xe0ccdeec2a9ull, 0xe33f8972be9ull, 0xe5b906e77c8ull, 0xe8396a503c5ull,
-    0xeac0c6e7dd2ull, 0xed4f301ed99ull, 0xefe4b99bdceull, 0xf281773c5a0ull,
-    0xf5257d15248ull, 0xf7d0df730adull, 0xfa83b2db723ull, 0xfd3e0c0cf48ull};
+constexpr int kPow2 = 32;
+__device__ const unsigned long long kPow2Fix[kPow2] = {
+    0x80000000000ull, 0x82cd8698ac3ull, 0x85aac367cc5ull, 0x88980e8092eull,
+    0x8b95c1e3ea9ull, 0x8ea4398b45dull, 0x91c3d373ab1ull, 0x94f4efa8fefull,
+    0x9837f0518dcull, 0x9b8d39b9d55ull, 0x9ef5326091aull, 0xa27043030c5ull,
+    0xa5fed6a9b15ull, 0xa9a15ab4ea8ull, 0xad583eea42aull, 0xb123f581d2bull,
+    0xb504f333f9eull, 0xb8fbaf47630ull, 0xbd08a39f581ull, 0xc12c4cca667ull,
+    0xc5672a11550ull, 0xc9b9bd866e3ull, 0xce248c151f8ull, 0xd2a81d91f13ull,
+    0xd744fccad6aull, 0xdbfbb797dafull, 0xe0ccdeec2a9ull, 0xe5b906e77c8ull,
+    0xeac0c6e7dd2ull, 0xefe4b99bdceull, 0xf5257d15248ull, 0xfa83b2db723ull};
+
+// The table in shared memory, one copy per lane: an entry's three words lie
+// in the lane's own bank, so that 32 different entries are read at once.
+struct Pow2Table {
+  uint32_t lo[kPow2][32], hi[kPow2][32];
+  float f[kPow2][32];  // 2^(j / 32)
+};
 
 struct Weights {
   float top;              // the row's maximum
   float inv_hi, inv_lo;   // 1 / T
+  int drop;               // 43 - weight_bits
 };
 
-// 2^43 exp((x - top) / T), rounded.  x <= top, both finite or x = -inf.
-__device__ __forceinline__ unsigned long long fixed_weight(const Weights& w, const unsigned long long* pow2,
-                                                           float x) {
+// 2^weight_bits exp((x - top) / T), rounded.  x <= top, both finite or x =
+// -inf.
+__device__ __forceinline__ unsigned long long fixed_weight(const Weights& w, const Pow2Table& pow2, int lane, float x) {
   // x - top exactly, as d + dl.
   const float d = x - w.top;
   const float bb = d - x;
   const float dl = (x - (d - bb)) + (-w.top - bb);
   const float y = d * w.inv_hi;
-  if (!(y > -32.f)) return 0ull;  // below 2^-46 of the maximum; x = -inf
   const float yl = fmaf(d, w.inv_hi, -y) + fmaf(d, w.inv_lo, dl * w.inv_hi);
-  const float kf = rintf(y * 92.332482616893656f);  // 64 / ln 2
-  float r = fmaf(-kf, 0x1.62e430p-7f, y);
-  r += yl - kf * -0x1.05c610p-35f;
-  const int k = (int)kf;  // <= 0
-  const unsigned long long t = pow2[k & 63];
+  // k = rint(32 y / ln 2) through the last bits of a sum with 1.5 * 2^23.
+  const float yc = fmaxf(y, -33.f);  // (-inf and what rounds to 0 in the end)
+  const float kt = fmaf(yc, 46.16624069213867f, 12582912.f);
+  const float kf = kt - 12582912.f;
+  const int k = __float_as_int(kt) - 0x4B400000;  // <= 0
+  float r = fmaf(-kf, 0x1.62e43p-6f, yc);
+  r += yl - kf * -0x1.05c61p-34f;
+  const int j = k & (kPow2 - 1);
+  const unsigned long long fix = ((unsigned long long)pow2.hi[j][lane] << 32) | pow2.lo[j][lane];
   const float em1 = fmaf(r * r, fmaf(r, fmaf(r, 1.f / 24.f, 1.f / 6.f), 0.5f), r);
-  const float tf = (float)(unsigned)(t >> 20) * 0x1p-23f;  // 2^(j / 64) to 24 bits
-  const long long v = (long long)t + ((long long)__float2int_rn(tf * em1 * 0x1p37f) << 6);
-  const int sh = -(k >> 6);
-  return sh == 0 ? (unsigned long long)v : ((unsigned long long)v + (1ull << (sh - 1))) >> sh;
+  const unsigned long long v = fix + ((long long)__float2int_rn(pow2.f[j][lane] * em1 * 0x1p36f) << 7);
+  const int sh = w.drop - (k >> 5);
+  const unsigned long long half = sh ? 1ull << (sh - 1) : 0ull;
+  return y > -32.f ? (v + half) >> sh : 0ull;  // below 2^-46 of the maximum: 0
 }
 
-// floor(c q) up to one unit, for q in [0, 1] (NaN and negative count as 0).
-__device__ __forceinline__ unsigned long long mul_prob(unsigned long long c, float q) {
-  if (!(q > 0.f)) return 0ull;
-  const unsigned long long f = __float2ull_rz(fminf(q, 1.f) * 0x1p63f);
+// A probability in units of 2^-63 (NaN and negative count as 0), and c
+// times it, rounded down to an even number.
+__device__ __forceinline__ unsigned long long fixed_prob(float q) {
+  return q > 0.f ? __float2ull_rz(fminf(q, 1.f) * 0x1p63f) : 0ull;
+}
+__device__ __forceinline__ unsigned long long mul_prob(unsigned long long c, unsigned long long f) {
   return __umul64hi(c, f) << 1;
 }
 
 constexpr int kMaxRej = kMaxTreeRows;  // rejected siblings of one node
 
 struct WalkShared {
-  unsigned long long pow2[64];
-  unsigned long long seg[2][kSegs];  // a pass's sum over each warp's part of the row
-  unsigned long long scale[kMaxRej + 1];  // sum of the weights before the k-th rejection
-  float segmax[2][kCluster];
-  unsigned segbad[2][kCluster];
-  int segat[2][kCluster];
+  Pow2Table pow2;
+  unsigned long long warps[2][kWalkWarps];  // sums over each warp's part of the row
+  unsigned long long ctas[2][kMaxCluster];  // and over each CTA's
+  unsigned long long scale[kMaxRej + 1];  // c_k: sum of the weights left by k rejections
+  unsigned long long cut[kMaxRej + 2];    // c_0 + .. + c_(k-1)
+  float ctamax[2][kMaxCluster];
+  int ctaat[2][kMaxCluster];
   float p[kMaxRows], q[kMaxRows], u[kMaxRows], top[kMaxRows];
   int token[kMaxRows], at[kMaxRows];
   short par[kMaxRows];
@@ -285,35 +322,14 @@ struct WalkShared {
   float rej_mass;
 };
 
-// One row's weights after nrej rejections: without drafted probabilities,
-// the weight unless the token is one of the rejected; with them, the
-// recursion s <- max(s - c g, 0) on unnormalised weights of sum c.
-__device__ __forceinline__ unsigned long long weight_left(const WalkShared& sh, const Weights& w, const float* grow,
-                                                          int nrej, int i, float x) {
-  unsigned long long v = fixed_weight(w, sh.pow2, x);
-  if (grow == nullptr) {
-    for (int k = 0; k < nrej; ++k)
-      if (sh.rej_token[k] == i) v = 0ull;
-    return v;
-  }
-  if (nrej > 0 && v > 0ull) {
-    const float g = grow[i];
-    for (int k = 0; k < nrej; ++k) {
-      const unsigned long long c = mul_prob(sh.scale[k], g);
-      v = v > c ? v - c : 0ull;
-    }
-  }
-  return v;
-}
-
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
 __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v, int lane) {
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
@@ -321,11 +337,60 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v, in
   return v;
 }
 
+// The largest m of the warp and its lowest place; a place of -1 anywhere wins.
+__device__ __forceinline__ void best_of_lanes(float& m, int& at) {
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, m, o);
+    const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+    at = at < 0 || oa < 0 ? -1 : om > m ? oa : om == m ? min(at, oa) : at;
+    m = fmaxf(m, om);
+  }
+}
+
+// The walk runs for a few microseconds and most of its code once, so the
+// instructions that it has to fetch count like the work: loops stay rolled,
+// and what several places need is one function out of line.  (65 KB of
+// unrolled code took 27 us for one sequence's draw, 20 KB of it 8.)
+
+// Weights of a unit of 256 values: lane's values i, i + 32, .. into its
+// places of dst, 32 apart.  i counts from the row's start.
+template <typename T>
+__device__ __noinline__ void fill_unit(const WalkShared& sh, const Weights w, const T* row, int vocab, int i,
+                                       unsigned long long* dst) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = i + 32 * e < vocab ? to_float<T>(row[i + 32 * e]) : -INFINITY;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) *reinterpret_cast<float*>(dst + 32 * e) = x[e];
+#pragma unroll 2
+  for (int e = 0; e < 8; ++e) dst[32 * e] = fixed_weight(w, sh.pow2, threadIdx.x & 31, *reinterpret_cast<const float*>(dst + 32 * e));
+}
+
+// The sum of a lane's weights of a unit, less cut times the drafted
+// probabilities.  A rejection takes s to max(s - c g, 0), c the sum of all s
+// before it; a weight that reached 0 stays there, so after several of them it
+// is max(v - cut g, 0) with cut = c_0 + c_1 + ...
+__device__ __noinline__ unsigned long long sum_unit(const unsigned long long* src, const float* guess, int vocab,
+                                                    int i, unsigned long long cut) {
+  unsigned long long sum = 0ull;
+  float g[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) g[e] = cut && i + 32 * e < vocab ? guess[i + 32 * e] : 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const unsigned long long v = src[32 * e], c = mul_prob(cut, fixed_prob(g[e]));
+    sum += v > c ? v - c : 0ull;
+  }
+  return sum;
+}
+
 // Walk of one sequence by a cluster.  Every CTA takes the same decisions
 // from the same numbers, so the cluster's barriers always match.
-template <typename T>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWalkThreads)
-    accept_walk_kernel(const AcceptParams p) {
+template <typename T, int kCluster>
+__global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const AcceptParams p) {
+  constexpr int kSegs = kCluster * kWalkWarps;
+  extern __shared__ __align__(16) unsigned long long weights[];
   __shared__ WalkShared sh;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -338,7 +403,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWalkThreads)
   const bool greedy = temp == 0.f;
   int row0, n;
   const bool fits = accept_rows(p, s, kind, &row0, &n);
-  if (tid < 64) sh.pow2[tid] = kPow2[tid];
+#pragma unroll 1
+  for (int i = tid; i < kPow2 * 32; i += kWalkThreads) {
+    const unsigned long long t = kPow2Fix[i / 32];
+    sh.pow2.lo[i / 32][lane] = (uint32_t)t;
+    sh.pow2.hi[i / 32][lane] = (uint32_t)(t >> 32);
+    sh.pow2.f[i / 32][lane] = (float)t * 0x1p-43f;
+  }
   if (tid == 0) {
     sh.err = fits ? 0u : VA_DEV_BAD_ROWS;
     if (temp != 0.f && !(temp >= kMinTemperature && temp < INFINITY)) sh.err |= VA_DEV_BAD_SAMPLING;
@@ -347,6 +418,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWalkThreads)
     sh.nrej = 0;
     sh.cursor = 1;
     sh.rej_mass = 0.f;
+    sh.cut[0] = 0ull;
   }
   if (!fits || n == 0) {
     // Rows unknown, or none: nothing to choose.  The same for every CTA.
@@ -358,50 +430,66 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWalkThreads)
     }
     return;
   }
+#pragma unroll 1
   for (int j = tid; j < n; j += kWalkThreads) sh.at[j] = -2;  // no statistics
   __syncthreads();
 
-  // Every row's test, at once: its parent, p(x) and g(x).
+  // Every row's test, at once: its parent, p(x) and g(x).  A warp per row
+  // joins the statistics of its parent's pieces.
   const T* logits = reinterpret_cast<const T*>(p.logits);
-  for (int j = tid; j < n; j += kWalkThreads) {
+  const float inv = greedy ? 0.f : 1.4426950408889634f / temp;
+#pragma unroll 1
+  for (int j = warp; j < n; j += kWalkWarps) {
     const int a = kind == 1 ? p.parent[row0 + j] : j - 1;
     if (kind == 1 && (j == 0 ? a != -1 : a < 0 || a >= j)) {
-      atomicOr(&sh.err, VA_DEV_BAD_PARENT);
+      if (lane == 0) atomicOr(&sh.err, VA_DEV_BAD_PARENT);
       continue;
     }
     if (j == 0) continue;
     const int x = p.tokens[row0 + j];
     if (x < 0 || x >= p.vocab) {
-      atomicOr(&sh.err, VA_DEV_BAD_TOKEN);
+      if (lane == 0) atomicOr(&sh.err, VA_DEV_BAD_TOKEN);
       continue;
     }
     const float z = to_float<T>(logits[(long long)(row0 + a) * p.logits_stride + x]);
     const float g = p.probs ? p.probs[(long long)(row0 + a) * p.probs_stride + x] : 1.f;
+    const float u = p.accept_u[row0 + j];
     const float4* st = p.stats + (long long)(row0 + a) * p.pieces;
-    float m = -INFINITY;
-    int at = -1;
-    for (int c = 0; c < p.pieces; ++c) {
+    // At temperature 0 inv is 0 and the sums are 0 or NaN: the scaling by
+    // exp2(0) (or by NaN, of a sum that is NaN anyway) changes nothing.
+    // Pieces of -inf alone add nothing; a NaN in any piece stays.
+    float m = -INFINITY, sum = 0.f;
+    int at = INT_MAX;
+#pragma unroll 1
+    for (int c = lane; c < p.pieces; c += 32) {
       const float4 t = st[c];
       if (t.x > m) {
+        sum = m == -INFINITY ? sum : sum * exp2_fast((m - t.x) * inv);
         m = t.x;
         at = __float_as_int(t.z);
       }
+      sum += t.x == -INFINITY ? t.y : t.y * exp2_fast((t.x - m) * inv);
     }
-    float sum = 0.f;
-    const float inv = greedy ? 0.f : 1.4426950408889634f / temp;
-    for (int c = 0; c < p.pieces; ++c) {
-      const float4 t = st[c];
-      // Pieces of -inf alone add nothing; a NaN in any piece stays.
-      if (t.x != -INFINITY || t.y != t.y) sum += t.y * (greedy ? 1.f : exp2f((t.x - m) * inv));
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) {
+      const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, sum, o);
+      const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+      const float nm = fmaxf(m, om);
+      sum = (m == -INFINITY ? sum : sum * exp2_fast((m - nm) * inv)) +
+            (om == -INFINITY ? os : os * exp2_fast((om - nm) * inv));
+      at = om > m ? oa : om == m ? min(at, oa) : at;
+      m = nm;
     }
-    const bool usable = sum == sum && m < INFINITY && m > -INFINITY;
-    sh.par[j] = (short)a;
-    sh.token[j] = x;
-    sh.u[j] = p.accept_u[row0 + j];
-    sh.q[j] = g;
-    sh.p[j] = !usable ? -1.f : greedy ? (x == at ? 1.f : 0.f) : exp2f((z - m) * inv) / sum;
-    sh.top[a] = usable ? m : NAN;  // siblings write the same values
-    sh.at[a] = at;
+    if (lane == 0) {
+      const bool usable = sum == sum && m < INFINITY && m > -INFINITY;
+      sh.par[j] = (short)a;
+      sh.token[j] = x;
+      sh.u[j] = u;
+      sh.q[j] = g;
+      sh.p[j] = !usable ? -1.f : greedy ? (x == at ? 1.f : 0.f) : exp2_fast((z - m) * inv) / sum;
+      sh.top[a] = m;  // siblings write the same values
+      sh.at[a] = usable ? at : -1;
+    }
   }
   __syncthreads();
   if (sh.err) {
@@ -412,272 +500,257 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kWalkThreads)
         if (p.promote_len) p.promote_len[s] = 0;
         p.next_token[s] = -1;
       }
+#pragma unroll 1
       for (int j = tid; j < n; j += kWalkThreads) p.accepted_nodes[row0 + j] = -1;
     }
     return;  // every CTA saw the same error and leaves here
   }
 
-  // This warp's part of a row.
-  const int seglen = ((p.vocab + kSegs - 1) / kSegs + 31) / 32 * 32;
-  const int seg = rank * kWalkWarps + warp;
-  const int lo = min(seg * seglen, p.vocab), hi = min(lo + seglen, p.vocab);
+  // This warp's part of a row: per units of 256 values.  Their weights are
+  // kept in shared memory where the parts fit (p.cached), else a unit's are
+  // made in the warp's 2 KB each time.
+  const int per = (p.vocab + kUnit * kSegs - 1) / (kUnit * kSegs);
+  const int lo = (rank * kWalkWarps + warp) * per * kUnit;
+  const int units = lo < p.vocab ? min(per, (p.vocab - lo + kUnit - 1) / kUnit) : 0;
+  unsigned long long* const mine = weights + warp * (p.cached ? per : 1) * kUnit;
   Weights w;
   w.top = 0.f;
-  {
-    const double inv = greedy ? 1.0 : 1.0 / (double)temp;
-    w.inv_hi = (float)inv;
-    w.inv_lo = (float)(inv - (double)w.inv_hi);
-  }
-  int pass = 0;       // exchanges so far: the buffers alternate
-  int have = -1;      // scale[0 .. have] hold sums at this node
-  bool topped = false, bad = false;
-  int best = -1;
-  const T* row = logits;
-  const float* grow = nullptr;
+  w.drop = 43 - p.weight_bits;
+  w.inv_hi = greedy ? 1.f : 1.f / temp;  // with its rounding error
+  w.inv_lo = greedy ? 0.f : fmaf(-w.inv_hi, temp, 1.f) / temp;
+  int at_node = -1;     // the node that the row variables describe
+  int pass = 0;         // exchanges so far: the buffers alternate
+  int have = -1;        // scale[0 .. have] hold sums at this node
+  int best = -1;        // place of the row's maximum, -1: no distribution
+  bool filled = false;  // the table of weights is this row's
+  const T* row = nullptr;
+  const float* guess = nullptr;
 
-  // Sum of every segment's values in each CTA's table.
-  auto exchange = [&](unsigned long long v) {
-    v = warp_sum(v);
-    const int b = pass & 1;
-    if (lane < kCluster) *cluster.map_shared_rank(&sh.seg[b][seg], lane) = v;
-    cluster.sync();
-    ++pass;
-    return b;
-  };
-  auto total_of = [&](int b) {
-    unsigned long long t = 0ull;
-    for (int g = lane; g < kSegs; g += 32) t += sh.seg[b][g];
-    return warp_sum(t);
-  };
-  // The row's maximum (and its place), where the statistics kernel left
-  // the row out.
-  auto find_top = [&](int node) {
-    topped = true;
-    if (sh.at[node] != -2) {
-      w.top = sh.top[node];
-      best = sh.at[node];
-      bad = w.top != w.top;
-      return;
-    }
-    float m = -INFINITY;
-    int at = INT_MAX;
-    bool odd = false;
-#pragma unroll 8
-    for (int i = lo + lane; i < hi; i += 32) {
-      const float x = to_float<T>(row[i]);
-      odd |= !(x < INFINITY);
-      if (x > m) {
-        m = x;
-        at = i;
+  // The weights of unit k after the rejections, in the table: the sum of this
+  // lane's.  Proposals without probabilities: a rejected token weighs 0.
+  auto unit_left = [&](int k, int nrej) {
+    unsigned long long* at = mine + (p.cached ? k * kUnit : 0) + lane;
+    const int i = lo + k * kUnit + lane;
+    if (!filled) {
+      fill_unit<T>(sh, w, row, p.vocab, i, at);
+      if (!p.probs) {
+        __syncwarp();
+        const int x = lane < nrej ? sh.rej_token[lane] - (i - lane) : -1;
+        if (x >= 0 && x < kUnit) at[x - lane] = 0ull;
+        __syncwarp();
       }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float om = __shfl_xor_sync(0xffffffffu, m, o);
-      const int oa = __shfl_xor_sync(0xffffffffu, at, o);
-      if (om > m || (om == m && oa < at)) {
-        m = om;
-        at = oa;
-      }
-    }
-    odd = __any_sync(0xffffffffu, odd);
-    if (lane == 0) {
-      sh.wmax[warp] = m;
-      sh.wat[warp] = odd ? -1 : at;
-    }
-    __syncthreads();
-    const int b = pass & 1;
-    if (tid < kCluster) {
-      float bm = -INFINITY;
-      int ba = INT_MAX;
-      unsigned bo = 0u;
-      for (int k = 0; k < kWalkWarps; ++k) {
-        if (sh.wat[k] == -1) bo = 1u;
-        else if (sh.wmax[k] > bm) {
-          bm = sh.wmax[k];
-          ba = sh.wat[k];
-        }
-      }
-      *cluster.map_shared_rank(&sh.segmax[b][rank], tid) = bm;
-      *cluster.map_shared_rank(&sh.segat[b][rank], tid) = ba;
-      *cluster.map_shared_rank(&sh.segbad[b][rank], tid) = bo;
-    }
-    cluster.sync();
-    ++pass;
-    w.top = -INFINITY;
-    for (int k = 0; k < kCluster; ++k) {
-      if (sh.segbad[b][k]) bad = true;
-      if (sh.segmax[b][k] > w.top) {
-        w.top = sh.segmax[b][k];
-        best = sh.segat[b][k];
-      }
-    }
-    if (w.top == -INFINITY) bad = true;
-  };
-  // The sum of the weights left after k rejections (k = 0: of all).
-  auto sum_left = [&](int k) {
-    unsigned long long v = 0ull;
-#pragma unroll 4
-    for (int i = lo + lane; i < hi; i += 32) v += weight_left(sh, w, grow, k, i, to_float<T>(row[i]));
-    return exchange(v);
+    return sum_unit(at, guess, p.vocab, i, p.probs ? sh.cut[nrej] : 0ull);
   };
 
   enum { DONE = 0, NEED_SUMS = 1 };
+  int left = 0;  // the rejections behind the last sums
+  unsigned long long total = 0ull;
+#pragma unroll 1
   for (;;) {
-    if (tid == 0) {
-      // Try the rows in order: a row counts when its parent is the node
-      // reached so far (its siblings come later, its children after it).
+    if (warp == 0) {
+      // Try the children of the node reached so far in row order: a taken
+      // child becomes the node, and its children come after it.
+      __syncwarp();
       int node = sh.node, count = sh.count, nrej = sh.nrej, j = sh.cursor;
       float mass = sh.rej_mass;
       int cmd = DONE;
-      for (; j < n; ++j) {
-        if (sh.par[j] != node) continue;
-        const float u = sh.u[j];
-        bool yes;
-        int x = 0;
-        if (greedy) {
-          yes = sh.p[j] > 0.f;
-        } else if (sh.p[j] < 0.f) {
-          yes = false;  // the row has no distribution
-        } else if (!p.probs) {
-          x = sh.token[j];
-          bool again = false;
-          for (int k = 0; k < nrej; ++k) again |= sh.rej_token[k] == x;
-          yes = !again && u * (1.f - mass) < sh.p[j];
-          if (!yes && !again) {
-            sh.rej_token[nrej++] = x;
-            mass += sh.p[j];
-          }
-        } else if (nrej == 0) {
-          yes = u * sh.q[j] < sh.p[j];
-          if (!yes) ++nrej;
+      const int up = kind == 1 && lane > 0 && lane < n ? sh.par[lane] : -1;
+#pragma unroll 1
+      for (;;) {
+        if (kind == 1) {
+          const unsigned kids = __ballot_sync(0xffffffffu, up == node && lane >= j);
+          j = kids ? __ffs(kids) - 1 : n;
         } else {
-          // Against the weights left by the rejected siblings.
-          if (have < nrej) {
-            cmd = NEED_SUMS;
-            break;
-          }
-          x = sh.token[j];
-          const float* gr = p.probs + (long long)(row0 + node) * p.probs_stride;
-          const unsigned long long left = weight_left(
-              sh, w, gr, nrej, x, to_float<T>(logits[(long long)(row0 + node) * p.logits_stride + x]));
-          yes = (double)u * (double)sh.q[j] * (double)sh.scale[nrej] < (double)left;
-          if (!yes) ++nrej;
+          j = j <= node + 1 ? node + 1 : n;
+        }
+        if (j >= n) break;
+        const float u = sh.u[j], pj = sh.p[j], qj = sh.q[j];
+        const int x = sh.token[j];
+        bool yes = false, lost = false;  // taken; rejected, with an effect
+        if (greedy || pj < 0.f) {
+          yes = pj > 0.f;  // below 0: the row has no distribution
+        } else if (!p.probs) {
+          const bool again = __any_sync(0xffffffffu, lane < nrej && sh.rej_token[lane] == x);
+          yes = !again && u * (1.f - mass) < pj;
+          lost = !yes && !again;
+        } else if (nrej == 0) {
+          yes = u * qj < pj;
+          lost = !yes;
+        } else if (have < nrej) {
+          cmd = NEED_SUMS;  // the weights left by the rejected siblings
+          break;
+        } else {
+          const float z = to_float<T>(logits[(long long)(row0 + node) * p.logits_stride + x]);
+          const unsigned long long v = fixed_weight(w, sh.pow2, lane, z), c = mul_prob(sh.cut[nrej], fixed_prob(qj));
+          yes = (double)u * (double)qj * (double)sh.scale[nrej] < (double)(v > c ? v - c : 0ull);
+          lost = !yes;
         }
         if (yes) {
-          if (rank == 0) p.accepted_nodes[row0 + count] = j;
+          if (rank == 0 && lane == 0) p.accepted_nodes[row0 + count] = j;
           node = j;
           ++count;
           nrej = 0;
           mass = 0.f;
           have = -1;
+        } else if (lost) {
+          if (!p.probs && lane == 0) sh.rej_token[nrej] = x;
+          __syncwarp();
+          ++nrej;
+          mass += pj;
         }
+        ++j;
       }
-      sh.node = node;
-      sh.count = count;
-      sh.nrej = nrej;
-      sh.cursor = j;
-      sh.rej_mass = mass;
-      sh.cmd = cmd;
+      __syncwarp();
+      if (lane == 0) {
+        sh.node = node;
+        sh.count = count;
+        sh.nrej = nrej;
+        sh.cursor = j;
+        sh.rej_mass = mass;
+        sh.cmd = cmd;
+      }
     }
     __syncthreads();
     const int node = sh.node, cmd = sh.cmd, nrej = sh.nrej;
-    const T* nrow = logits + (long long)(row0 + node) * p.logits_stride;
-    if (nrow != row || !topped) {
-      row = nrow;
-      grow = p.probs ? p.probs + (long long)(row0 + node) * p.probs_stride : nullptr;
+    if (node != at_node) {
+      at_node = node;
+      row = logits + (long long)(row0 + node) * p.logits_stride;
+      guess = p.probs ? p.probs + (long long)(row0 + node) * p.probs_stride : nullptr;
       have = -1;
-      topped = false;
-      bad = false;
-      best = -1;
+      filled = false;
+      w.top = sh.top[node];
+      best = sh.at[node];
+      if (best == -2) {
+        // The statistics kernel left the row out (a leaf): its maximum.
+        float m = -INFINITY;
+        int at = INT_MAX;
+        bool odd = false;
+        const int end = min(lo + units * kUnit, p.vocab);
+#pragma unroll 8
+        for (int i = lo + lane; i < end; i += 32) {
+          const float x = to_float<T>(row[i]);
+          odd |= !(x < INFINITY);
+          if (x > m) {
+            m = x;
+            at = i;
+          }
+        }
+        if (odd) at = -1;
+        best_of_lanes(m, at);
+        const int b = pass++ & 1;
+        if (lane == 0) {
+          sh.wmax[warp] = m;
+          sh.wat[warp] = at;
+        }
+        __syncthreads();
+        if (warp == 0) {
+          m = lane < kWalkWarps ? sh.wmax[lane] : -INFINITY;
+          at = lane < kWalkWarps ? sh.wat[lane] : INT_MAX;
+          best_of_lanes(m, at);
+          if (lane < kCluster) {
+            *cluster.map_shared_rank(&sh.ctamax[b][rank], lane) = m;
+            *cluster.map_shared_rank(&sh.ctaat[b][rank], lane) = at;
+          }
+        }
+        cluster.sync();
+        m = lane < kCluster ? sh.ctamax[b][lane] : -INFINITY;
+        at = lane < kCluster ? sh.ctaat[b][lane] : INT_MAX;
+        best_of_lanes(m, at);
+        w.top = m;
+        best = at == INT_MAX ? -1 : at;  // nothing but -inf
+      }
+    }
+    if (cmd == DONE && (greedy || best < 0)) break;
+    // Sums of what the rejections left, one exchange each (proposals without
+    // probabilities: of what all of them left, at once).
+    left = nrej;
+#pragma unroll 1
+    for (int k = p.probs ? min(have + 1, nrej) : nrej;;) {
+      unsigned long long v = 0ull;
+#pragma unroll 1
+      for (int t = 0; t < units; ++t) v += unit_left(t, k);
+      filled = p.cached;
+      // Each warp's sum into this CTA's table, each CTA's into every CTA's.
+      v = warp_sum(v);
+      const int b = pass++ & 1;
+      if (lane == 0) sh.warps[b][warp] = v;
+      __syncthreads();
+      if (warp == 0) {
+        const unsigned long long c = warp_sum(lane < kWalkWarps ? sh.warps[b][lane] : 0ull);
+        if (lane < kCluster) *cluster.map_shared_rank(&sh.ctas[b][rank], lane) = c;
+      }
+      cluster.sync();
+      total = warp_sum(lane < kCluster ? sh.ctas[b][lane] : 0ull);
+      if (p.probs) {
+        if (tid == 0) {
+          sh.scale[k] = total;
+          sh.cut[k + 1] = sh.cut[k] + total;
+        }
+        __syncthreads();
+        have = k;
+      }
+      if (total == 0ull && k > 0) {
+        // Nothing is left: the next sibling, or the draw, meets p itself.
+        left = k = 0;
+        filled = filled && p.probs;
+        if (cmd == DONE) continue;
+        have = 0;
+        if (tid == 0) sh.nrej = 0;
+        break;
+      }
+      if (k++ == left) break;
     }
     if (cmd == DONE) break;
-    if (!topped) find_top(node);
-    // Sums before each rejection so far, one exchange each.
-    while (have < nrej) {
-      const int b = sum_left(have + 1);
-      const unsigned long long t = total_of(b);
-      if (tid == 0) sh.scale[have + 1] = t;
-      __syncthreads();
-      ++have;
-      if (t == 0ull && have > 0) break;
-    }
-    if (sh.scale[have] == 0ull) {  // nothing is left: the next sibling meets p itself
-      have = 0;
-      if (tid == 0) sh.nrej = 0;
-    }
   }
 
   // Outputs of the walk.
-  const int node = sh.node, count = sh.count;
-  int nrej = sh.nrej;
+  const int count = sh.count;
   if (rank == 0) {
     if (tid == 0) {
       p.accepted_len[s] = count;
       if (p.promote_len) p.promote_len[s] = kind == 1 ? count : 0;
       p.accepted_nodes[row0] = 0;
+      if (best < 0) flag(p.status, VA_DEV_BAD_LOGITS);
+      if (best < 0 || greedy) p.next_token[s] = best;
     }
+#pragma unroll 1
     for (int j = count + tid; j < n; j += kWalkThreads) p.accepted_nodes[row0 + j] = -1;
   }
-  // The next token, from what is left at the last node.
-  if (!topped) find_top(node);
-  if (bad || greedy) {
-    if (rank == 0 && tid == 0) {
-      if (bad) flag(p.status, VA_DEV_BAD_LOGITS);
-      p.next_token[s] = bad ? -1 : best;
-    }
-  } else {
-    int b = 0;
-    unsigned long long total = 0ull;
-    if (grow == nullptr) {
-      b = sum_left(nrej);
-      total = total_of(b);
-    } else {
-      for (int k = have < 0 ? 0 : have; k <= nrej; ++k) {
-        b = sum_left(k);
-        total = total_of(b);
-        if (tid == 0) sh.scale[k] = total;
-        __syncthreads();
-        if (total == 0ull) break;
-      }
-    }
-    if (total == 0ull) {  // nothing is left: from p itself
-      nrej = 0;
-      b = sum_left(0);
-      total = total_of(b);
-    }
-    // The lowest i whose running sum passes t = floor(v total).
+  // The next token, from what is left at the last node: the lowest i whose
+  // running sum passes t = floor(v total).
+  if (best >= 0 && !greedy) {
     const float v = p.sample_u[s];
     unsigned long long t = v > 0.f ? __umul64hi(total, v < 1.f ? (unsigned long long)__float2ull_rz(v * 0x1p63f) << 1
                                                                : ~0ull)
                                    : 0ull;
     if (t >= total) t = total - 1;
-    unsigned long long head = 0ull;
-    for (int g = lane; g < seg; g += 32) head += sh.seg[b][g];
-    head = warp_sum(head);
-    const unsigned long long mine = sh.seg[b][seg];
-    if (t >= head && t < head + mine) {
-      // One warp owns the border: a lane sums a contiguous block, the block
-      // that holds the border is then spread over the lanes again.
-      const int blk = seglen / 32;
-      const int b0 = lo + lane * blk, b1 = min(b0 + blk, hi);
-      unsigned long long sum = 0ull;
-#pragma unroll 4
-      for (int i = b0; i < b1; ++i) sum += weight_left(sh, w, grow, nrej, i, to_float<T>(row[i]));
-      const unsigned long long inc = warp_scan(sum, lane) + head;
-      const int owner = __ffs(__ballot_sync(0xffffffffu, t < inc)) - 1;
-      unsigned long long base = __shfl_sync(0xffffffffu, inc - sum, owner);
-      const int c0 = lo + owner * blk, c1 = min(c0 + blk, hi);
-      for (int i0 = c0; i0 < c1; i0 += 32) {
-        const int i = i0 + lane;
-        const unsigned long long wt = i < c1 ? weight_left(sh, w, grow, nrej, i, to_float<T>(row[i])) : 0ull;
-        const unsigned long long c = warp_scan(wt, lane) + base;
-        const unsigned hit = __ballot_sync(0xffffffffu, t < c);
-        if (hit) {
-          if (lane == __ffs(hit) - 1) p.next_token[s] = i;
-          break;
+    const int b = (pass & 1) ^ 1;  // the last sums
+    unsigned long long base = warp_sum(lane < rank ? sh.ctas[b][lane] : 0ull);
+    base += warp_sum(lane < warp ? sh.warps[b][lane] : 0ull);
+    if (t >= base && t - base < sh.warps[b][warp]) {
+      // One warp owns the border: the unit that holds it, then the 32 values.
+#pragma unroll 1
+      for (int k = 0; k < units; ++k) {
+        const unsigned long long sum = warp_sum(unit_left(k, left));
+        if (t - base >= sum) {
+          base += sum;
+          continue;
         }
-        base = __shfl_sync(0xffffffffu, c, 31);
+        const unsigned long long* at = mine + (p.cached ? k * kUnit : 0) + lane;
+        const unsigned long long cut = p.probs ? sh.cut[left] : 0ull;
+#pragma unroll 1
+        for (int i = lo + k * kUnit + lane, e = 0; e < kUnit / 32; ++e, i += 32, at += 32) {
+          const unsigned long long c = cut && i < p.vocab ? mul_prob(cut, fixed_prob(guess[i])) : 0ull;
+          const unsigned long long inc = warp_scan(*at > c ? *at - c : 0ull, lane) + base;
+          const unsigned hit = __ballot_sync(0xffffffffu, t < inc);
+          if (hit) {
+            if (lane == __ffs(hit) - 1) p.next_token[s] = i;
+            break;
+          }
+          base = __shfl_sync(0xffffffffu, inc, 31);
+        }
+        break;
       }
     }
   }
@@ -712,31 +785,94 @@ static size_t accept_ws_bytes(const va_problem* p, const va_draft* d) {
   return (b + 255) / 256 * 256;
 }
 
-template <typename K>
-static cudaError_t launch_after(K kernel, dim3 grid, int threads, cudaStream_t st, const AcceptParams& q) {
+// Launch configuration of a kernel that starts early and waits for the work
+// before it on the stream (programmatic dependent).
+struct Launch {
   cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, q);
+  cudaLaunchAttribute attr[2];
+  Launch(unsigned gx, unsigned gy, unsigned gz, int threads, int cluster, size_t smem, cudaStream_t st) {
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(gx, gy, gz);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+  }
+};
+
+// What a kernel's clusters of 16 need and may have is found out once per
+// device: 0 unknown, 1 usable, 2 not (a GPC with too few SMs).
+constexpr int kMaxDevices = 64;
+
+template <typename T, int kCluster>
+static cudaError_t prepare_walk(int dev, bool* usable) {
+  static std::atomic<int> known[kMaxDevices];
+  int k = known[dev].load(std::memory_order_acquire);
+  if (k == 0) {
+    auto* kernel = accept_walk_kernel<T, kCluster>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCacheBytes);
+    if (e != cudaSuccess) return e;
+    k = 1;
+    if (kCluster > 8) {
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      Launch l(kCluster, 1, 1, kWalkThreads, kCluster, kMaxCacheBytes, nullptr);
+      int n = 0;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      if (n < 1) k = 2;
+    }
+    known[dev].store(k, std::memory_order_release);
+  }
+  *usable = k == 1;
+  return cudaSuccess;
+}
+
+template <typename T, int kCluster>
+static cudaError_t launch_walk(AcceptParams q, cudaStream_t st) {
+  // The weights of a CTA's part of the row where they fit, else one unit per
+  // warp.
+  const int per = (q.vocab + kUnit * kCluster * kWalkWarps - 1) / (kUnit * kCluster * kWalkWarps);
+  const size_t unit = (size_t)kWalkWarps * kUnit * sizeof(unsigned long long);
+  q.cached = per * unit <= (size_t)kMaxCacheBytes;
+  Launch l((unsigned)(q.num_seqs * kCluster), 1, 1, kWalkThreads, kCluster, q.cached ? per * unit : unit, st);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, accept_walk_kernel<T, kCluster>, q);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T>
 static cudaError_t launch_accept(const AcceptParams& q, cudaStream_t st) {
-  // A sequence of one row has no proposal: nothing to prepare.
-  if (q.max_rows > 1) {
-    const dim3 grid((unsigned)q.pieces, (unsigned)q.max_rows, (unsigned)q.num_seqs);
-    cudaError_t e = launch_after(accept_stats_kernel<T>, grid, kStatThreads, st, q);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  // Clusters of 16 for few sequences: the GPU holds about one per GPC at a
+  // time, so more sequences than that run better on clusters of 8.
+  bool wide = q.num_seqs <= 8, usable = true;
+  if (wide) {
+    e = prepare_walk<T, 16>(dev, &wide);
     if (e != cudaSuccess) return e;
   }
-  return launch_after(accept_walk_kernel<T>, dim3((unsigned)(q.num_seqs * kCluster)), kWalkThreads, st, q);
+  if (!wide) {
+    e = prepare_walk<T, 8>(dev, &usable);
+    if (e != cudaSuccess) return e;
+  }
+  // A sequence of one row has no proposal: nothing to prepare.
+  if (q.max_rows > 1) {
+    Launch l((unsigned)((q.pieces + kStatWarps - 1) / kStatWarps), (unsigned)q.max_rows, (unsigned)q.num_seqs,
+             kStatThreads, 1, 0, st);
+    e = cudaLaunchKernelEx(&l.cfg, accept_stats_kernel<T>, q);
+    if (e != cudaSuccess) return e;
+  }
+  return wide ? launch_walk<T, 16>(q, st) : launch_walk<T, 8>(q, st);
 }
 
 }  // namespace va
@@ -770,6 +906,10 @@ va_status verify_attn_accept(const va_problem* p, const va_draft* d, int32_t mod
   q.mode = mode;
   q.vocab = d->vocab;
   q.pieces = accept_pieces(d->vocab);
+  // The weights of a row sum to at most 2^58, the cuts of 31 rejections to 2^63.
+  int bits = 58;
+  while (bits > 38 && (1LL << (58 - bits)) < d->vocab) --bits;
+  q.weight_bits = bits < 43 ? bits : 43;
   q.cu_rows = p->cu_rows;
   q.parent = p->parent;
   q.seq_kind = p->seq_kind;

@@ -41,11 +41,11 @@ def test_accept_refusals(kw, code):
 
 
 def test_accept_workspace():
-    # One 16-byte record per row and piece of 8,192 values (a row may start 7 values past a boundary).
+    # One 16-byte record per row and piece of 4,096 values (a row may start 7 values past a boundary).
     size = lambda **kw: _accept(ws_bytes=0, **kw)[1]  # noqa: E731
     assert size(vocab=100, total_rows=8) == 256
-    assert size(vocab=8185, logits_stride=8185, total_rows=64) == 1024
-    assert size(vocab=8186, logits_stride=8186, total_rows=64) == 2048
+    assert size(vocab=4089, logits_stride=4089, total_rows=64) == 1024
+    assert size(vocab=4090, logits_stride=4090, total_rows=64) == 2048
     assert size(max_rows_per_seq=1) == 0 and size(vocab=0) == 0
 
 
