@@ -239,66 +239,81 @@ __global__ void __launch_bounds__(kStatThreads) accept_stats_kernel(const Accept
 }
 
 // ---------------------------------------------------------------------------
-// Fixed-point weights: 2^(j / 32) * 2^43, rounded, for the reduction
+// Fixed-point weights: 2^(j / 32) * 2^30, rounded, for the reduction
 // exp(y) = 2^(k / 32) exp(r), k = rint(32 y / ln 2), |r| <= ln 2 / 64 (the
 // argument reduction in two parts of Cody and Waite; exp(r) - 1 by its
 // Taylor series).
 constexpr int kPow2 = 32;
-__device__ const unsigned long long kPow2Fix[kPow2] = {
-    0x80000000000ull, 0x82cd8698ac3ull, 0x85aac367cc5ull, 0x88980e8092eull,
-    0x8b95c1e3ea9ull, 0x8ea4398b45dull, 0x91c3d373ab1ull, 0x94f4efa8fefull,
-    0x9837f0518dcull, 0x9b8d39b9d55ull, 0x9ef5326091aull, 0xa27043030c5ull,
-    0xa5fed6a9b15ull, 0xa9a15ab4ea8ull, 0xad583eea42aull, 0xb123f581d2bull,
-    0xb504f333f9eull, 0xb8fbaf47630ull, 0xbd08a39f581ull, 0xc12c4cca667ull,
-    0xc5672a11550ull, 0xc9b9bd866e3ull, 0xce248c151f8ull, 0xd2a81d91f13ull,
-    0xd744fccad6aull, 0xdbfbb797dafull, 0xe0ccdeec2a9ull, 0xe5b906e77c8ull,
-    0xeac0c6e7dd2ull, 0xefe4b99bdceull, 0xf5257d15248ull, 0xfa83b2db723ull};
+__device__ const uint32_t kPow2Fix[kPow2] = {
+    0x40000000u, 0x4166c34cu, 0x42d561b4u, 0x444c0740u, 0x45cae0f2u, 0x47521cc6u, 0x48e1e9bau, 0x4a7a77d4u,
+    0x4c1bf829u, 0x4dc69cddu, 0x4f7a9930u, 0x51382182u, 0x52ff6b55u, 0x54d0ad5au, 0x56ac1f75u, 0x5891fac1u,
+    0x5a82799au, 0x5c7dd7a4u, 0x5e8451d0u, 0x60962665u, 0x62b39509u, 0x64dcdec3u, 0x6712460bu, 0x69540ec9u,
+    0x6ba27e65u, 0x6dfddbccu, 0x70666f76u, 0x72dc8374u, 0x75606374u, 0x77f25cceu, 0x7a92be8bu, 0x7d41d96eu};
 
-// The table in shared memory, one copy per lane: an entry's three words lie
-// in the lane's own bank, so that 32 different entries are read at once.
+// The table in shared memory, one copy per lane: an entry's two words lie in
+// the lane's own bank, so that 32 different entries are read at once.
 struct Pow2Table {
-  uint32_t lo[kPow2][32], hi[kPow2][32];
-  float f[kPow2][32];  // 2^(j / 32)
+  uint32_t fix[kPow2][32];
+  float f[kPow2][32];  // the same value
 };
 
 struct Weights {
   float top;              // the row's maximum
   float inv_hi, inv_lo;   // 1 / T
-  int drop;               // 43 - weight_bits
+  int drop;               // 43 - weight_bits >= 0
 };
 
 // 2^weight_bits exp((x - top) / T), rounded.  x <= top, both finite or x =
-// -inf.
+// -inf.  About 35 instructions.
+template <typename T>
 __device__ __forceinline__ unsigned long long fixed_weight(const Weights& w, const Pow2Table& pow2, int lane, float x) {
-  // x - top exactly, as d + dl.
+  // (x - top) / T as y + yl.  The difference of two bf16 values is exact but
+  // for a value 2^16 times smaller than the maximum; of two fp32 values its
+  // rounding error is added back.
   const float d = x - w.top;
-  const float bb = d - x;
-  const float dl = (x - (d - bb)) + (-w.top - bb);
   const float y = d * w.inv_hi;
-  const float yl = fmaf(d, w.inv_hi, -y) + fmaf(d, w.inv_lo, dl * w.inv_hi);
+  float yl = fmaf(d, w.inv_lo, fmaf(d, w.inv_hi, -y));
+  if (sizeof(T) == 4) {
+    const float bb = d - x;
+    yl = fmaf((x - (d - bb)) + (-w.top - bb), w.inv_hi, yl);
+  }
   // k = rint(32 y / ln 2) through the last bits of a sum with 1.5 * 2^23.
   const float yc = fmaxf(y, -33.f);  // (-inf and what rounds to 0 in the end)
-  const float kt = fmaf(yc, 46.16624069213867f, 12582912.f);
+  const float kt = fmaf(yc, 46.16624f, 12582912.f);
   const float kf = kt - 12582912.f;
   const int k = __float_as_int(kt) - 0x4B400000;  // <= 0
-  float r = fmaf(-kf, 0x1.62e43p-6f, yc);
-  r += yl - kf * -0x1.05c61p-34f;
+  const float r = fmaf(-kf, 0x1.62e43p-6f, yc) + fmaf(kf, 0x1.05c61p-34f, yl);
   const int j = k & (kPow2 - 1);
-  const unsigned long long fix = ((unsigned long long)pow2.hi[j][lane] << 32) | pow2.lo[j][lane];
   const float em1 = fmaf(r * r, fmaf(r, fmaf(r, 1.f / 24.f, 1.f / 6.f), 0.5f), r);
-  const unsigned long long v = fix + ((long long)__float2int_rn(pow2.f[j][lane] * em1 * 0x1p36f) << 7);
+  const uint32_t v = pow2.fix[j][lane] + __float2int_rn(pow2.f[j][lane] * em1);  // 2^30 .. 2^31
+  // v 2^13 / 2^sh, rounded: sh >= 0.
   const int sh = w.drop - (k >> 5);
-  const unsigned long long half = sh ? 1ull << (sh - 1) : 0ull;
-  return y > -32.f ? (v + half) >> sh : 0ull;  // below 2^-46 of the maximum: 0
+  const unsigned long long u = ((unsigned long long)v << 14) >> sh;
+  return y > -32.f ? (u + 1) >> 1 : 0ull;  // below 2^-46 of the maximum: 0
 }
 
-// A probability in units of 2^-63 (NaN and negative count as 0), and c
-// times it, rounded down to an even number.
-__device__ __forceinline__ unsigned long long fixed_prob(float q) {
-  return q > 0.f ? __float2ull_rz(fminf(q, 1.f) * 0x1p63f) : 0ull;
+// c g for a probability g (NaN and negative count as 0, above 1 as 1), to 31
+// significant bits of c: c = c31 * 2^cs, g = m * 2^(e - 150).
+struct Cut {
+  uint32_t c31;
+  int shift;  // 150 - cs
+};
+
+__device__ __forceinline__ Cut make_cut(unsigned long long c) {
+  Cut k;
+  const int cs = max(33 - __clzll((long long)c), 0);
+  k.c31 = (uint32_t)(c >> cs);
+  k.shift = 150 - cs;
+  return k;
 }
-__device__ __forceinline__ unsigned long long mul_prob(unsigned long long c, unsigned long long f) {
-  return __umul64hi(c, f) << 1;
+
+__device__ __forceinline__ unsigned long long cut_times(const Cut& k, float g) {
+  const uint32_t b = __float_as_uint(fminf(fmaxf(g, 0.f), 1.f));
+  const unsigned long long m = (unsigned long long)k.c31 * ((b & 0x7FFFFFu) | 0x800000u);  // < 2^55
+  const int sh = k.shift - (int)(b >> 23);
+  // Below 0: at most 9 more bits (c up to 2^63).  A subnormal g counts double
+  // at most and is shifted out.
+  return sh >= 0 ? (sh < 64 ? m >> sh : 0ull) : m << -sh;
 }
 
 constexpr int kMaxRej = kMaxTreeRows;  // rejected siblings of one node
@@ -354,32 +369,36 @@ __device__ __forceinline__ void best_of_lanes(float& m, int& at) {
 // unrolled code took 27 us for one sequence's draw, 20 KB of it 8.)
 
 // Weights of a unit of 256 values: lane's values i, i + 32, .. into its
-// places of dst, 32 apart.  i counts from the row's start.
+// places of dst, 32 apart; their sum.  i counts from the row's start.
 template <typename T>
-__device__ __noinline__ void fill_unit(const WalkShared& sh, const Weights w, const T* row, int vocab, int i,
-                                       unsigned long long* dst) {
+__device__ __noinline__ unsigned long long fill_unit(const WalkShared& sh, const Weights w, const T* row, int vocab,
+                                                     int i, unsigned long long* dst) {
   float x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = i + 32 * e < vocab ? to_float<T>(row[i + 32 * e]) : -INFINITY;
+  unsigned long long sum = 0ull;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) *reinterpret_cast<float*>(dst + 32 * e) = x[e];
-#pragma unroll 2
-  for (int e = 0; e < 8; ++e) dst[32 * e] = fixed_weight(w, sh.pow2, threadIdx.x & 31, *reinterpret_cast<const float*>(dst + 32 * e));
+  for (int e = 0; e < 8; ++e) {
+    const unsigned long long v = fixed_weight<T>(w, sh.pow2, threadIdx.x & 31, x[e]);
+    dst[32 * e] = v;
+    sum += v;
+  }
+  return sum;
 }
 
-// The sum of a lane's weights of a unit, less cut times the drafted
+// The sum of a lane's weights of a unit, less the cut times the drafted
 // probabilities.  A rejection takes s to max(s - c g, 0), c the sum of all s
 // before it; a weight that reached 0 stays there, so after several of them it
-// is max(v - cut g, 0) with cut = c_0 + c_1 + ...
+// is max(v - (c_0 + c_1 + ..) g, 0).
 __device__ __noinline__ unsigned long long sum_unit(const unsigned long long* src, const float* guess, int vocab,
-                                                    int i, unsigned long long cut) {
+                                                    int i, const Cut cut) {
   unsigned long long sum = 0ull;
   float g[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) g[e] = cut && i + 32 * e < vocab ? guess[i + 32 * e] : 0.f;
+  for (int e = 0; e < 8; ++e) g[e] = cut.c31 && i + 32 * e < vocab ? guess[i + 32 * e] : 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const unsigned long long v = src[32 * e], c = mul_prob(cut, fixed_prob(g[e]));
+    const unsigned long long v = src[32 * e], c = cut_times(cut, g[e]);
     sum += v > c ? v - c : 0ull;
   }
   return sum;
@@ -405,10 +424,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
   const bool fits = accept_rows(p, s, kind, &row0, &n);
 #pragma unroll 1
   for (int i = tid; i < kPow2 * 32; i += kWalkThreads) {
-    const unsigned long long t = kPow2Fix[i / 32];
-    sh.pow2.lo[i / 32][lane] = (uint32_t)t;
-    sh.pow2.hi[i / 32][lane] = (uint32_t)(t >> 32);
-    sh.pow2.f[i / 32][lane] = (float)t * 0x1p-43f;
+    sh.pow2.fix[i / 32][lane] = kPow2Fix[i / 32];
+    sh.pow2.f[i / 32][lane] = (float)kPow2Fix[i / 32];
   }
   if (tid == 0) {
     sh.err = fits ? 0u : VA_DEV_BAD_ROWS;
@@ -446,23 +463,25 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
       continue;
     }
     if (j == 0) continue;
+    // Loads that wait on nothing first.
+    const float4* st = p.stats + (long long)(row0 + a) * p.pieces;
+    const float4 none = make_float4(-INFINITY, 0.f, __int_as_float(INT_MAX), 0.f);
     const int x = p.tokens[row0 + j];
+    const float u = p.accept_u[row0 + j];
+    float4 t = lane < p.pieces ? st[lane] : none;
     if (x < 0 || x >= p.vocab) {
       if (lane == 0) atomicOr(&sh.err, VA_DEV_BAD_TOKEN);
       continue;
     }
     const float z = to_float<T>(logits[(long long)(row0 + a) * p.logits_stride + x]);
     const float g = p.probs ? p.probs[(long long)(row0 + a) * p.probs_stride + x] : 1.f;
-    const float u = p.accept_u[row0 + j];
-    const float4* st = p.stats + (long long)(row0 + a) * p.pieces;
     // At temperature 0 inv is 0 and the sums are 0 or NaN: the scaling by
     // exp2(0) (or by NaN, of a sum that is NaN anyway) changes nothing.
     // Pieces of -inf alone add nothing; a NaN in any piece stays.
     float m = -INFINITY, sum = 0.f;
     int at = INT_MAX;
 #pragma unroll 1
-    for (int c = lane; c < p.pieces; c += 32) {
-      const float4 t = st[c];
+    for (int c = lane; c < p.pieces; c += 32, t = c < p.pieces ? st[c] : none) {
       if (t.x > m) {
         sum = m == -INFINITY ? sum : sum * exp2_fast((m - t.x) * inv);
         m = t.x;
@@ -526,21 +545,27 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
   const T* row = nullptr;
   const float* guess = nullptr;
 
-  // The weights of unit k after the rejections, in the table: the sum of this
-  // lane's.  Proposals without probabilities: a rejected token weighs 0.
+  // The sum of this lane's weights of unit k after the rejections; the
+  // weights are in the table then.  Proposals without probabilities: a
+  // rejected token weighs 0 there.
+  Cut cut = {0u, 0};
   auto unit_left = [&](int k, int nrej) {
     unsigned long long* at = mine + (p.cached ? k * kUnit : 0) + lane;
     const int i = lo + k * kUnit + lane;
     if (!filled) {
-      fill_unit<T>(sh, w, row, p.vocab, i, at);
-      if (!p.probs) {
+      unsigned long long sum = fill_unit<T>(sh, w, row, p.vocab, i, at);
+      if (!p.probs && nrej > 0) {
         __syncwarp();
         const int x = lane < nrej ? sh.rej_token[lane] - (i - lane) : -1;
-        if (x >= 0 && x < kUnit) at[x - lane] = 0ull;
+        if (x >= 0 && x < kUnit) {
+          sum -= at[x - lane];
+          at[x - lane] = 0ull;
+        }
         __syncwarp();
       }
+      if (cut.c31 == 0u) return sum;
     }
-    return sum_unit(at, guess, p.vocab, i, p.probs ? sh.cut[nrej] : 0ull);
+    return sum_unit(at, guess, p.vocab, i, cut);
   };
 
   enum { DONE = 0, NEED_SUMS = 1 };
@@ -582,7 +607,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
           break;
         } else {
           const float z = to_float<T>(logits[(long long)(row0 + node) * p.logits_stride + x]);
-          const unsigned long long v = fixed_weight(w, sh.pow2, lane, z), c = mul_prob(sh.cut[nrej], fixed_prob(qj));
+          const unsigned long long v = fixed_weight<T>(w, sh.pow2, lane, z);
+          const unsigned long long c = cut_times(make_cut(sh.cut[nrej]), qj);
           yes = (double)u * (double)qj * (double)sh.scale[nrej] < (double)(v > c ? v - c : 0ull);
           lost = !yes;
         }
@@ -668,6 +694,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
 #pragma unroll 1
     for (int k = p.probs ? min(have + 1, nrej) : nrej;;) {
       unsigned long long v = 0ull;
+      cut = make_cut(p.probs ? sh.cut[k] : 0ull);
 #pragma unroll 1
       for (int t = 0; t < units; ++t) v += unit_left(t, k);
       filled = p.cached;
@@ -738,10 +765,9 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
           continue;
         }
         const unsigned long long* at = mine + (p.cached ? k * kUnit : 0) + lane;
-        const unsigned long long cut = p.probs ? sh.cut[left] : 0ull;
 #pragma unroll 1
         for (int i = lo + k * kUnit + lane, e = 0; e < kUnit / 32; ++e, i += 32, at += 32) {
-          const unsigned long long c = cut && i < p.vocab ? mul_prob(cut, fixed_prob(guess[i])) : 0ull;
+          const unsigned long long c = cut.c31 && i < p.vocab ? cut_times(cut, guess[i]) : 0ull;
           const unsigned long long inc = warp_scan(*at > c ? *at - c : 0ull, lane) + base;
           const unsigned hit = __ballot_sync(0xffffffffu, t < inc);
           if (hit) {
@@ -836,14 +862,23 @@ static cudaError_t prepare_walk(int dev, bool* usable) {
   return cudaSuccess;
 }
 
+// Bytes of a CTA's part of a row's weights, and whether they are kept.
+static size_t walk_cache_bytes(int vocab, int cluster) {
+  const int per = (vocab + kUnit * cluster * kWalkWarps - 1) / (kUnit * cluster * kWalkWarps);
+  return (size_t)per * kWalkWarps * kUnit * sizeof(unsigned long long);
+}
+static bool walk_caches(int vocab, int cluster) {
+  return walk_cache_bytes(vocab, cluster) <= (size_t)kMaxCacheBytes;
+}
+
 template <typename T, int kCluster>
 static cudaError_t launch_walk(AcceptParams q, cudaStream_t st) {
   // The weights of a CTA's part of the row where they fit, else one unit per
   // warp.
-  const int per = (q.vocab + kUnit * kCluster * kWalkWarps - 1) / (kUnit * kCluster * kWalkWarps);
-  const size_t unit = (size_t)kWalkWarps * kUnit * sizeof(unsigned long long);
-  q.cached = per * unit <= (size_t)kMaxCacheBytes;
-  Launch l((unsigned)(q.num_seqs * kCluster), 1, 1, kWalkThreads, kCluster, q.cached ? per * unit : unit, st);
+  const size_t bytes = walk_cache_bytes(q.vocab, kCluster);
+  q.cached = walk_caches(q.vocab, kCluster);
+  Launch l((unsigned)(q.num_seqs * kCluster), 1, 1, kWalkThreads, kCluster,
+           q.cached ? bytes : (size_t)kWalkWarps * kUnit * sizeof(unsigned long long), st);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, accept_walk_kernel<T, kCluster>, q);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -854,9 +889,8 @@ static cudaError_t launch_accept(const AcceptParams& q, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  // Clusters of 16 for few sequences: the GPU holds about one per GPC at a
-  // time, so more sequences than that run better on clusters of 8.
-  bool wide = q.num_seqs <= 8, usable = true;
+  // Clusters of 16 while they all run at once (14 on 152 SMs), else of 8.
+  bool wide = q.num_seqs <= 14, usable = true;
   if (wide) {
     e = prepare_walk<T, 16>(dev, &wide);
     if (e != cudaSuccess) return e;
