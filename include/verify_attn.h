@@ -374,9 +374,12 @@ va_status verify_attn_noalloc(const va_problem *p, const va_kv *kv, int32_t mode
  *     score weighs 0, and 0 times infinity is NaN).
  *   - num_splits is here the largest number of chunks that a sequence's
  *     visible tokens are cut into (whole 64-token tiles, at least 128
- *     tokens); no choice depends on the other sequences of the launch.  About
- *     SMs / (num_seqs * num_kv_heads) chunks fill the GPU once
- *     (va_window_splits).
+ *     tokens).  About SMs / (num_seqs * num_kv_heads) chunks fill the GPU once
+ *     (va_window_splits).  No choice depends on the other sequences of the
+ *     launch: kernel and chunks follow from the types, from num_splits and
+ *     max_rows_per_seq as given, and from the sequence itself.
+ *   - Rows that no sequence covers stay as they were.  Where row offsets
+ *     overlap (VA_DEV_BAD_ROWS), a row claimed twice holds either result.
  *   - o: [total_rows][num_heads][head_dim] of o_dtype (VA_F32, or VA_BF16:
  *     rounded once, at the end); lse fp32.  ws of at least
  *     va_window_workspace_size() bytes, 256-byte aligned; its contents carry

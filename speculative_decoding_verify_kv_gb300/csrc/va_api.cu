@@ -23,6 +23,7 @@ cudaError_t launch_umma_partial(const Params& p, dim3 grid, cudaStream_t st);
 int umma_smem_bytes(int D, int kv_dtype);
 int umma_threads(int D, int kv_dtype);
 cudaError_t launch_umma_window(const Params& p, dim3 grid, cudaStream_t st);
+cudaError_t launch_window_rows(const Params& p, cudaStream_t st);
 cudaError_t launch_tq8_partial(const Params& p, dim3 grid, cudaStream_t st);
 int tq8_rows_per_block();
 int tq8_threads();
@@ -130,6 +131,7 @@ static va_status check(const va_problem* p, const va_kv* kv, int mode) {
 struct Plan {
   int kernel;  // VA_KERNEL_*
   int P, slots, rows_per_block, row_blocks, threads, smem;
+  bool few_rows = false;  // windowed calls
   dim3 grid;
 };
 
@@ -498,6 +500,10 @@ static Plan window_plan(const va_problem* p, const va_kv* kv) {
     const int rows = p->max_rows_per_seq * (p->num_heads / kv->num_kv_heads);
     pl.row_blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
   }
+  // At most 16 query rows per KV head (by the caller's bound, never by the
+  // rows of one launch): the kernel for few rows.
+  pl.few_rows = pl.kernel == VA_KERNEL_TENSOR && !kv->draft_k &&
+                p->max_rows_per_seq * (p->num_heads / kv->num_kv_heads) <= 16;
   pl.P = pl.slots = p->num_splits;
   pl.grid.x = (unsigned)(pl.slots > pl.row_blocks ? pl.slots : pl.row_blocks);
   return pl;
@@ -542,9 +548,11 @@ va_status verify_attn_window(const va_problem* p, const va_kv* kv, int32_t mode,
   q.window = w->window;
   q.sinks = w->sinks;
   q.o_bf16 = w->o_dtype == VA_BF16;
-  cudaError_t e = pl.kernel == VA_KERNEL_TENSOR ? launch_umma_window(q, pl.grid, cs)
-                                                : launch_simt_partial(q, pl.grid, cs);
+  cudaError_t e = pl.few_rows                       ? launch_window_rows(q, cs)
+                  : pl.kernel == VA_KERNEL_TENSOR ? launch_umma_window(q, pl.grid, cs)
+                                                  : launch_simt_partial(q, pl.grid, cs);
   if (e != cudaSuccess) return note_cuda(e);
+  if (pl.few_rows && pl.slots == 1) return VA_OK;  // it writes the outputs itself
   e = launch_merge(q, cs);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }

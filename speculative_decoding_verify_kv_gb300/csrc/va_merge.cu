@@ -60,6 +60,8 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const Params p)
     if (p.cu_rows[mid] <= grow) s_lo = mid;
     else s_hi = mid - 1;
   }
+  // A windowed call leaves a row that no sequence covers as it was.
+  if (WIN && !(p.cu_rows[s_lo] <= grow && grow < p.cu_rows[s_lo + 1])) return;
   int sr0, sn, sctx;
   int nan = !(p.cu_rows[s_lo] <= grow && grow < p.cu_rows[s_lo + 1]) ||
             (check_sequence(p, s_lo, &sr0, &sn, &sctx) & VA_DEV_BAD_ROWS) != 0u;

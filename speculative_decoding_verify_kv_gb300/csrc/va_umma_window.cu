@@ -3,6 +3,11 @@
 
 namespace va {
 
+// Maps over a bf16 cache whose boxes are one page of 64 columns.
+bool make_page_maps(const Params& p, CUtensorMap* k, CUtensorMap* v) {
+  return make_map(k, p, p.k, true) && make_map(v, p, p.v, true);
+}
+
 cudaError_t launch_umma_window(const Params& p, dim3 grid, cudaStream_t st) {
 #define VA_U_WIN(DD)                                                                             \
   if (p.D == DD)                                                                                 \

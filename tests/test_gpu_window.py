@@ -110,22 +110,60 @@ def test_cuda_core_kernel(kv, heads, kvh, dim):
 def test_a_sequence_does_not_depend_on_the_launch():
     case = make("q8_0", 6, 1, 256, [700, 90, 333, 40], [16, 1, 8, 1], kinds=[0, 0, 1, 0], mode="mixed", paged=True,
                 seed=12)
-    whole = run(case, 300, 4, splits=3)
-    for s in range(4):
-        one = sy.subset_sequences(case, [s])
-        got = run(one, 300, 4, splits=3)
-        a, b = int(case.cu_rows[s]), int(case.cu_rows[s + 1])
-        assert np.array_equal(got[0], whole[0][a:b]) and np.array_equal(got[1], whole[1][a:b])
+    for splits in (1, 3):
+        whole = run(case, 300, 4, splits=splits)
+        for s in range(4):
+            p, kv, mode = va.upload(sy.subset_sequences(case, [s]), "cuda", num_splits=splits)
+            p.max_rows_per_seq = 16  # the bound of the whole launch
+            got = [x.cpu().numpy() for x in va.verify_attn_window(p, kv, mode, va.Window(300, 4))]
+            a, b = int(case.cu_rows[s]), int(case.cu_rows[s + 1])
+            assert np.array_equal(got[0], whole[0][a:b]) and np.array_equal(got[1], whole[1][a:b])
 
 
-@pytest.mark.parametrize("kv,heads,kvh,dim", [SHAPES[0], SHAPES[3], SHAPES[6]])
-def test_device_errors_poison_only_their_sequence(kv, heads, kvh, dim):
+FEW = [(kv, h, k, d) for kv in ("bf16", "q8_0") for h, k, d in ((8, 1, 64), (8, 2, 128), (3, 3, 128), (5, 1, 256))]
+
+
+@pytest.mark.parametrize("kv,heads,kvh,dim", FEW)
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("window,sinks,splits", [(1, 0, 1), (17, 4, 1), (40, 33, 2), (700, 0, 1), (700, 20, 3),
+                                                 (1300, 5, 1), (1300, 5, 7)])
+def test_few_rows(kv, heads, kvh, dim, paged, window, sinks, splits):
+    """At most 16 query rows per KV head: rings that go round, chunks of no
+    and of one page, trees of two and three rows, both outputs."""
+    n = 16 * kvh // heads
+    case = make(kv, heads, kvh, dim, [0, 15, 16, 130, 1500], [n, 1, min(n, 3), n, 1], kinds=[1, 0, 1, 0, 0],
+                mode="mixed", paged=paged, seed=window + dim)
+    case = poison_unseen(case, window, sinks)
+    ref = so.window_case(case, window, sinks)
+    for out in (va.F32, va.BF16):
+        check(case, *run(case, window, sinks, out, splits), ref, out == va.BF16, f"out {out}")
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("rows", [1, 16])
+def test_rows_that_no_sequence_covers_stay(splits, rows):
+    case = make("bf16", 4, 2, 64, [300, 20], [rows, 1], seed=3)
+    p, kv, mode = va.upload(case, "cuda", num_splits=splits)
+    ref = so.window_case(case, 64, 2)
+    total = p.total_rows
+    p.total_rows += 2
+    p.q = torch.cat([p.q, p.q[:2]])
+    o = torch.full((total + 2, 4, 64), 7.0, device="cuda")
+    lse = torch.full((total + 2, 4), 7.0, device="cuda")
+    va.verify_attn_window(p, kv, mode, va.Window(64, 2), o=o, lse=lse)
+    assert (o[total:] == 7).all() and (lse[total:] == 7).all()
+    check(case, o[:total].cpu().numpy(), lse[:total].cpu().numpy(), ref, False)
+
+
+@pytest.mark.parametrize("kv,heads,kvh,dim", [SHAPES[0], SHAPES[3], SHAPES[6], ("bf16", 8, 2, 64), ("q8_0", 2, 1, 256)])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_device_errors_poison_only_their_sequence(kv, heads, kvh, dim, splits):
     case = make(kv, heads, kvh, dim, [200, 90, 64], [4, 4, 4], kinds=[0, 1, 0], mode="mixed", paged=True, seed=2)
     ref = so.window_case(case, 40, 3)
     for what in ("block", "parent", "ctx", "rows"):
         c = dataclasses.replace(case, block_table=case.block_table.copy(), parent=case.parent.copy(),
                                 ctx_len=case.ctx_len.copy(), cu_rows=case.cu_rows.copy())
-        p, kvs, mode = va.upload(c, "cuda", num_splits=2)
+        p, kvs, mode = va.upload(c, "cuda", num_splits=splits)
         if what == "block":      # a page inside the window; pages out of sight hold none
             kvs.block_table[1, 4] = 10 ** 6
             kvs.block_table[0, 3] = -5
