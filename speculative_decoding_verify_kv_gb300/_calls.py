@@ -40,6 +40,12 @@ def _tensor(name, t, dtype, numel, device=None, optional=False):
     return t
 
 
+# The current stream's handle without a Stream object around it (2.9 us of
+# the 7 that a bound call took on the host).
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _Call:
     """Arguments of one entry point, bound.  Subclasses fill ``_fn``,
     ``_args`` (all but the stream), ``_out`` and ``device``."""
@@ -49,11 +55,10 @@ class _Call:
         dev = self.device
         if dev.type != "cuda":
             raise ValueError(f"{self._where}: tensors on {dev}, not on a GPU")
-        if torch.cuda.current_device() != dev.index:
-            raise ValueError(f"{self._where}: tensors on {dev}, current device cuda:{torch.cuda.current_device()}")
-        if stream is None:
-            stream = torch.cuda.current_stream()
-        st = self._fn(*self._args, stream.cuda_stream)
+        index = torch.cuda.current_device()
+        if index != dev.index:
+            raise ValueError(f"{self._where}: tensors on {dev}, current device cuda:{index}")
+        st = self._fn(*self._args, _current_stream(index) if stream is None else stream.cuda_stream)
         if st:
             raise VaError(st, self._where)
         return self._out

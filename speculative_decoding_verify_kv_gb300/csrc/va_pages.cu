@@ -8,11 +8,11 @@
 // ranks come from prefix sums, the atomics only add.
 //
 // The planning kernels (fork, free, compact) touch a few hundred kilobytes
-// of integers and are bound by latency.  Each is one launch of one cluster
-// of eight CTAs: the counts are split over its 256 warps, whose partial
-// sums meet through distributed shared memory, and the cluster's barriers
-// order the steps (check everything, then change anything) without a
-// second launch.  The copy kernel is bound by the bytes it moves.
+// of integers and are bound by latency: each is one launch of one CTA, or
+// for large pools of one cluster of eight, so that barriers order the steps
+// (check everything, then change anything) without a second launch.  The
+// counts are split over the warps, whose partial sums meet in (distributed)
+// shared memory.  The copy kernel is bound by the bytes it moves.
 #include <cooperative_groups.h>
 #include <string.h>
 
@@ -23,8 +23,13 @@ namespace va {
 namespace cg = cooperative_groups;
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCtas = 8;
-constexpr int kPlanWarps = kPlanCtas * kPlanThreads / 32;
+constexpr int kCtaWarps = kPlanThreads / 32;
+constexpr int kPart = 128;  // table entries that a warp goes through at once
+constexpr int kWideCtas = 8;
+// Largest plan of one CTA.  Three forks over 2,048 pages (2,300 integers):
+// 8.5 us against 10.5 with a cluster; a compaction of 27,000: 16.3 against
+// 13.0; 60 forks of rows of 514 entries over 32,768 pages: 41 against 18.
+constexpr long long kOneCtaInts = 8192;
 
 struct PageParams {
   int num_seqs, max_blocks, num_blocks;
@@ -43,29 +48,43 @@ struct PageParams {
 };
 
 struct PlanShared {
-  unsigned seg[kPlanWarps];  // each warp's count
+  unsigned seg[kWideCtas * kCtaWarps];  // each warp's count
   unsigned err;
-  unsigned scan[32];
+  unsigned total_need, total_tail;
   int below;
 };
 
+// The CTAs of a planning kernel: one, or a cluster of NC.
+template <int NC>
+struct Team {
+  cg::cluster_group cluster;
+  __device__ __forceinline__ Team() : cluster(cg::this_cluster()) {}
+  __device__ __forceinline__ int rank() const { return NC > 1 ? (int)cluster.block_rank() : 0; }
+  __device__ __forceinline__ void sync() {
+    if (NC > 1) cluster.sync();
+    else __syncthreads();
+  }
+  template <typename V>
+  __device__ __forceinline__ V* at(V* p, int r) {
+    return NC > 1 ? cluster.map_shared_rank(p, r) : p;
+  }
+};
+
 // One warp's share of n items, in whole groups of 32.
+template <int NC>
 __device__ __forceinline__ void warp_share(int n, int warp, int* lo, int* hi) {
-  const int per = ((n + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+  constexpr int W = NC * kCtaWarps;
+  const int per = ((n + W - 1) / W + 31) / 32 * 32;
   *lo = (int)min((long long)warp * per, (long long)n);
   *hi = min(*lo + per, n);
 }
 
-__device__ __forceinline__ unsigned warp_add(unsigned v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+__device__ __forceinline__ unsigned warp_add(unsigned v) { return __reduce_add_sync(0xffffffffu, v); }
 
 // Each warp's count v (the same in every lane) into every CTA's table.
-__device__ __forceinline__ void share_count(cg::cluster_group& cluster, PlanShared& sh, int gwarp, int lane,
-                                            unsigned v) {
-  if (lane < kPlanCtas) *cluster.map_shared_rank(&sh.seg[gwarp], lane) = v;
+template <int NC>
+__device__ __forceinline__ void share_count(Team<NC>& team, PlanShared& sh, int gwarp, int lane, unsigned v) {
+  if (lane < NC) *team.at(&sh.seg[gwarp], lane) = v;
 }
 
 __device__ __forceinline__ unsigned sum_before(const PlanShared& sh, int gwarp, int lane) {
@@ -74,12 +93,14 @@ __device__ __forceinline__ unsigned sum_before(const PlanShared& sh, int gwarp, 
   return warp_add(t);
 }
 
-// An error anywhere reaches the first CTA; read_error after a cluster barrier.
-__device__ __forceinline__ void note_error(cg::cluster_group& cluster, PlanShared& sh, unsigned bits) {
-  atomicOr(cluster.map_shared_rank(&sh.err, 0), bits);
+// An error anywhere reaches the first CTA; read_error after a barrier.
+template <int NC>
+__device__ __forceinline__ void note_error(Team<NC>& team, PlanShared& sh, unsigned bits) {
+  atomicOr(team.at(&sh.err, 0), bits);
 }
-__device__ __forceinline__ unsigned read_error(cg::cluster_group& cluster, PlanShared& sh) {
-  return *cluster.map_shared_rank(&sh.err, 0);
+template <int NC>
+__device__ __forceinline__ unsigned read_error(Team<NC>& team, PlanShared& sh) {
+  return *team.at(&sh.err, 0);
 }
 
 // What the caller's status word holds on entry: after an earlier step of
@@ -101,13 +122,13 @@ __device__ __forceinline__ bool takes_fresh(bool grow, int full, int keep, int p
 
 // Fork and grow.  Workspace: mark[num_seqs], need[count], tail[count],
 // free pages found [num_blocks].
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    pages_fork_kernel(const PageParams p) {
+template <int NC>
+__global__ void __launch_bounds__(kPlanThreads) pages_fork_kernel(const PageParams p) {
   __shared__ PlanShared sh;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
+  Team<NC> team;
+  const int rank = team.rank();
   const int tid = threadIdx.x, lane = tid & 31, gwarp = rank * (kPlanThreads / 32) + tid / 32;
   const int gtid = rank * kPlanThreads + tid;
   int* mark = p.ws;
@@ -115,15 +136,17 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
   int* tail = need + p.count;
   int* found = tail + p.count;
   if (tid == 0) sh.err = rank == 0 ? status_before(p) : 0u;
-  for (int s = gtid; s < p.num_seqs; s += kPlanCtas * kPlanThreads) mark[s] = 0;
-  cluster.sync();
+  for (int s = gtid; s < p.num_seqs; s += NC * kPlanThreads) mark[s] = 0;
+  for (int i = gtid; i < p.count; i += NC * kPlanThreads) need[i] = 0;
+  team.sync();
 
-  // Check every command and count what it needs, one warp each; count the
-  // free pages, one part of the pool per warp.
-  for (int i = gwarp; i < p.count; i += kPlanWarps) {
+  // Check every command and count what it needs, a warp per 128 entries;
+  // count the free pages, one part of the pool per warp.
+  const int parts = (p.max_blocks + kPart - 1) / kPart;
+  for (long long job = gwarp; job < (long long)p.count * parts; job += NC * kCtaWarps) {
+    const int i = (int)(job / parts), part = (int)(job % parts);
     const int src = p.a[i], dst = p.b[i], len = p.c[i], pages = p.d[i];
     unsigned err = 0u;
-    int fresh = 0, tails = 0;
     if (src < 0 || src >= p.num_seqs || dst < 0 || dst >= p.num_seqs) {
       err = VA_DEV_BAD_ROWS;
     } else if (len < 0 || pages < 0 || pages > p.max_blocks || len > pages * kPage) {
@@ -133,85 +156,83 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       const int full = len / kPage, keep = (len + kPage - 1) / kPage;
       const int* row = p.table + (long long)src * p.max_blocks;
       const int end = grow ? pages : keep;
-      for (int c = lane; c < end; c += 32) {
-        const int e = row[c];
-        if (e != -1 && !page_in_use(p, e)) err = VA_DEV_BAD_BLOCK;
-        if (!grow && c == full && e < 0) err = VA_DEV_BAD_BLOCK;  // the page to copy
-        if (grow && takes_fresh(true, full, keep, pages, c, e)) ++fresh;
+      int e[4], r[4], fresh = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = part * kPart + 32 * k + lane;
+        e[k] = c < end ? row[c] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = e[k] >= 0 && e[k] < p.num_blocks ? p.ref[e[k]] : 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = part * kPart + 32 * k + lane;
+        if (c >= end) continue;
+        if (e[k] != -1 && r[k] <= 0) err = VA_DEV_BAD_BLOCK;
+        if (!grow && c == full && e[k] < 0) err = VA_DEV_BAD_BLOCK;  // the page to copy
+        if (grow && takes_fresh(true, full, keep, pages, c, e[k])) ++fresh;
       }
       fresh = (int)warp_add((unsigned)fresh);
-      if (!grow) {
-        fresh = pages - full;
-        tails = keep - full;
+      if (lane == 0) {
+        if (grow && fresh) atomicAdd(&need[i], fresh);
+        if (part == 0) {
+          if (!grow) need[i] = pages - full;
+          tail[i] = grow ? 0 : keep - full;
+          if (atomicAdd(&mark[dst], 1) != 0) err = VA_DEV_BAD_ROWS;  // named twice
+        }
       }
-      if (lane == 0 && atomicAdd(&mark[dst], 1) != 0) err = VA_DEV_BAD_ROWS;  // named twice
     }
-    if (lane == 0) {
-      need[i] = fresh;
-      tail[i] = tails;
-    }
-    if (err) note_error(cluster, sh, err);
+    if (err) note_error(team, sh, err);
   }
   int lo, hi;
-  warp_share(p.num_blocks, gwarp, &lo, &hi);
+  warp_share<NC>(p.num_blocks, gwarp, &lo, &hi);
   unsigned freec = 0;
 #pragma unroll 4
   for (int i = lo + lane; i < hi; i += 32) {
     const int r = p.ref[i];
-    if (r < 0) note_error(cluster, sh, VA_DEV_BAD_BLOCK);
+    if (r < 0) note_error(team, sh, VA_DEV_BAD_BLOCK);
     freec += r == 0;
   }
   freec = warp_add(freec);
-  share_count(cluster, sh, gwarp, lane, freec);
-  cluster.sync();
+  share_count(team, sh, gwarp, lane, freec);
+  team.sync();
   // A source that this call rewrites has no defined contents.
-  for (int i = gtid; i < p.count; i += kPlanCtas * kPlanThreads) {
+  for (int i = gtid; i < p.count; i += NC * kPlanThreads) {
     const int src = p.a[i], dst = p.b[i];
-    if (src >= 0 && src < p.num_seqs && src != dst && mark[src] != 0) note_error(cluster, sh, VA_DEV_BAD_ROWS);
+    if (src >= 0 && src < p.num_seqs && src != dst && mark[src] != 0) note_error(team, sh, VA_DEV_BAD_ROWS);
   }
-  // The first CTA turns the needs into running totals.
-  if (rank == 0) {
-    __shared__ unsigned base_need, base_tail;
-    if (tid == 0) base_need = base_tail = 0u;
-    __syncthreads();
-    for (int i0 = 0; i0 < p.count; i0 += kPlanThreads) {
-      const int i = i0 + tid;
-      unsigned a = i < p.count ? (unsigned)need[i] : 0u, b = i < p.count ? (unsigned)tail[i] : 0u;
-      unsigned long long v = ((unsigned long long)b << 32) | a;
-      unsigned long long inc = v;
+  // One warp turns the needs into running totals.
+  if (gwarp == 0) {
+    unsigned base_need = 0u, base_tail = 0u;
+    for (int i0 = 0; i0 < p.count; i0 += 32) {
+      const int i = i0 + lane;
+      const unsigned a = i < p.count ? (unsigned)need[i] : 0u, b = i < p.count ? (unsigned)tail[i] : 0u;
+      unsigned ia = a, ib = b;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
+        const unsigned ua = __shfl_up_sync(0xffffffffu, ia, o), ub = __shfl_up_sync(0xffffffffu, ib, o);
+        if (lane >= o) {
+          ia += ua;
+          ib += ub;
+        }
       }
-      __shared__ unsigned long long part[32];
-      if (lane == 31) part[tid / 32] = inc;
-      __syncthreads();
-      unsigned long long off = 0ull;
-      for (int w = 0; w < tid / 32; ++w) off += part[w];
-      const unsigned long long ex = off + inc - v;
-      const unsigned bn = base_need, bt = base_tail;
       if (i < p.count) {
-        need[i] = (int)(bn + (unsigned)ex);
-        tail[i] = (int)(bt + (unsigned)(ex >> 32));
+        need[i] = (int)(base_need + ia - a);
+        tail[i] = (int)(base_tail + ib - b);
       }
-      __syncthreads();
-      if (tid == kPlanThreads - 1) {
-        base_need = bn + (unsigned)(off + inc);
-        base_tail = bt + (unsigned)((off + inc) >> 32);
-      }
-      __syncthreads();
+      base_need += __shfl_sync(0xffffffffu, ia, 31);
+      base_tail += __shfl_sync(0xffffffffu, ib, 31);
     }
-    if (tid == 0) {
-      sh.below = (int)base_need;
-      sh.scan[0] = base_tail;
+    if (lane == 0) {
+      sh.total_need = base_need;
+      sh.total_tail = base_tail;
     }
   }
-  cluster.sync();
-  const unsigned wanted = (unsigned)*cluster.map_shared_rank(&sh.below, 0);
-  const unsigned tails_all = *cluster.map_shared_rank(&sh.scan[0], 0);
-  unsigned err = read_error(cluster, sh);
-  const unsigned total = sum_before(sh, kPlanWarps, lane);
+  team.sync();
+  const unsigned wanted = *team.at(&sh.total_need, 0);
+  const unsigned tails_all = *team.at(&sh.total_tail, 0);
+  unsigned err = read_error(team, sh);
+  const unsigned total = sum_before(sh, (NC * kCtaWarps), lane);
   if (!err && total < wanted) err = VA_DEV_NO_PAGES;
   const unsigned ahead = sum_before(sh, gwarp, lane);
   if (err) {
@@ -219,7 +240,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
       flag(p.status, err);
       *p.num_copies = 0;
     }
-    cluster.sync();  // the first CTA's memory is read until here
+    team.sync();  // the first CTA's memory is read until here
     return;
   }
   // The wanted free pages, ascending, and their first reference.
@@ -232,52 +253,66 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (is_free && r < wanted) found[r] = i;
     at += __popc(m);
   }
-  cluster.sync();
-  // Apply, one warp per command.
-  for (int i = gwarp; i < p.count; i += kPlanWarps) {
+  team.sync();
+  // Apply: a warp per 128 entries of a fork, one for a sequence that grows.
+  for (long long job = gwarp; job < (long long)p.count * parts; job += NC * kCtaWarps) {
+    const int i = (int)(job / parts), part = (int)(job % parts);
     const int src = p.a[i], dst = p.b[i], len = p.c[i], pages = p.d[i];
-    const bool grow = src == dst;
     const int full = len / kPage, keep = (len + kPage - 1) / kPage;
     const int* from = p.table + (long long)src * p.max_blocks;
     int* to = p.table + (long long)dst * p.max_blocks;
-    int next = need[i];
-    const int end = grow ? pages : p.max_blocks;
-    for (int c0 = grow ? keep : 0; c0 < end; c0 += 32) {
-      const int c = c0 + lane;
-      const bool in = c < end;
-      const int old = in && (grow || c < keep) ? from[c] : -1;
-      const bool fresh = in && takes_fresh(grow, full, keep, pages, c, old);
-      const unsigned m = __ballot_sync(0xffffffffu, fresh);
-      int e = grow || c < full ? old : -1;
-      if (fresh) {
-        e = found[next + __popc(m & ((1u << lane) - 1u))];
-        p.ref[e] = 1;
-        if (!grow && c == full && keep > full) {  // the partial page is copied
-          p.copies[2 * tail[i]] = old;
-          p.copies[2 * tail[i] + 1] = e;
+    if (src != dst) {
+      const int* mine = found + need[i] - full;  // of entry c in [full, pages)
+#pragma unroll 4
+      for (int k = 0; k < kPart; k += 32) {
+        const int c = part * kPart + k + lane;
+        if (c >= p.max_blocks) continue;
+        const int old = c < keep ? from[c] : -1;
+        int e = c < full ? old : -1;
+        if (c >= full && c < pages) {
+          e = mine[c];
+          p.ref[e] = 1;
+          if (c < keep) {  // the partial page is copied
+            p.copies[2 * tail[i]] = old;
+            p.copies[2 * tail[i] + 1] = e;
+          }
+        } else if (e >= 0) {
+          atomicAdd(&p.ref[e], 1);
         }
-      } else if (in && !grow && e >= 0) {
-        atomicAdd(&p.ref[e], 1);
+        to[c] = e;
       }
-      next += __popc(m);
-      if (in && (!grow || fresh)) to[c] = e;
+    } else if (part == 0) {
+      int next = need[i];
+      for (int c0 = keep; c0 < pages; c0 += 32) {
+        const int c = c0 + lane;
+        const bool fresh = c < pages && from[c] < 0;
+        const unsigned m = __ballot_sync(0xffffffffu, fresh);
+        if (fresh) {
+          const int e = found[next + __popc(m & ((1u << lane) - 1u))];
+          p.ref[e] = 1;
+          to[c] = e;
+        }
+        next += __popc(m);
+      }
     }
   }
   if (rank == 0 && tid == 0) *p.num_copies = (int)tails_all;
 }
 
 // Give back the table entries [first, last) of the listed sequences.
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    pages_free_kernel(const PageParams p) {
+template <int NC>
+__global__ void __launch_bounds__(kPlanThreads) pages_free_kernel(const PageParams p) {
   __shared__ PlanShared sh;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
+  Team<NC> team;
+  const int rank = team.rank();
   const int tid = threadIdx.x, lane = tid & 31, gwarp = rank * (kPlanThreads / 32) + tid / 32;
   if (tid == 0) sh.err = rank == 0 ? status_before(p) : 0u;
-  cluster.sync();
-  for (int i = gwarp; i < p.count; i += kPlanWarps) {
+  team.sync();
+  const int parts = (p.max_blocks + kPart - 1) / kPart;
+  for (long long job = gwarp; job < (long long)p.count * parts; job += NC * kCtaWarps) {
+    const int i = (int)(job / parts), c0 = (int)(job % parts) * kPart;
     const int s = p.a[i], first = p.b[i], last = p.c[i];
     unsigned err = 0u;
     if (s < 0 || s >= p.num_seqs) {
@@ -285,23 +320,30 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     } else if (first < 0 || last < first || last > p.max_blocks) {
       err = VA_DEV_CTX_OVERFLOW;
     } else {
-      for (int c = first + lane; c < last; c += 32) {
+#pragma unroll
+      for (int k = 0; k < kPart; k += 32) {
+        const int c = c0 + k + lane;
+        if (c < first || c >= last) continue;
         const int e = p.table[(long long)s * p.max_blocks + c];
         if (e != -1 && !page_in_use(p, e)) err = VA_DEV_BAD_BLOCK;
       }
     }
-    if (err) note_error(cluster, sh, err);
+    if (err) note_error(team, sh, err);
   }
-  cluster.sync();
-  const unsigned err = read_error(cluster, sh);
-  cluster.sync();  // the first CTA's memory is read until here
+  team.sync();
+  const unsigned err = read_error(team, sh);
+  team.sync();  // the first CTA's memory is read until here
   if (err) {
     if (rank == 0 && tid == 0) flag(p.status, err);
     return;
   }
-  for (int i = gwarp; i < p.count; i += kPlanWarps) {
+  for (long long job = gwarp; job < (long long)p.count * parts; job += NC * kCtaWarps) {
+    const int i = (int)(job / parts), c0 = (int)(job % parts) * kPart;
     const int s = p.a[i], first = p.b[i], last = p.c[i];
-    for (int c = first + lane; c < last; c += 32) {
+#pragma unroll
+    for (int k = 0; k < kPart; k += 32) {
+      const int c = c0 + k + lane;
+      if (c < first || c >= last) continue;
       // Ranges may overlap: the exchange gives each entry to one of them.
       const int e = atomicExch(&p.table[(long long)s * p.max_blocks + c], -1);
       if (e < 0) continue;
@@ -316,37 +358,37 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
 // Pull the live pages together: with N pages in use, the k-th page in use
 // at or above N moves to the k-th hole below N.  Workspace: new place of
 // each page [num_blocks].
-__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
-    pages_compact_kernel(const PageParams p) {
+template <int NC>
+__global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(const PageParams p) {
   __shared__ PlanShared sh;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank();
+  Team<NC> team;
+  const int rank = team.rank();
   const int tid = threadIdx.x, lane = tid & 31, gwarp = rank * (kPlanThreads / 32) + tid / 32;
   const int gtid = rank * kPlanThreads + tid;
   if (tid == 0) sh.err = rank == 0 ? status_before(p) : 0u;
-  cluster.sync();
+  team.sync();
   int lo, hi;
-  warp_share(p.num_blocks, gwarp, &lo, &hi);
+  warp_share<NC>(p.num_blocks, gwarp, &lo, &hi);
   unsigned livec = 0;
 #pragma unroll 4
   for (int i = lo + lane; i < hi; i += 32) {
     const int r = p.ref[i];
-    if (r < 0) note_error(cluster, sh, VA_DEV_BAD_BLOCK);
+    if (r < 0) note_error(team, sh, VA_DEV_BAD_BLOCK);
     livec += r > 0;
   }
   livec = warp_add(livec);
   const long long entries = (long long)p.num_seqs * p.max_blocks;
 #pragma unroll 4
-  for (long long i = gtid; i < entries; i += kPlanCtas * kPlanThreads) {
+  for (long long i = gtid; i < entries; i += NC * kPlanThreads) {
     const int e = p.table[i];
-    if (e != -1 && !page_in_use(p, e)) note_error(cluster, sh, VA_DEV_BAD_BLOCK);
+    if (e != -1 && !page_in_use(p, e)) note_error(team, sh, VA_DEV_BAD_BLOCK);
   }
-  share_count(cluster, sh, gwarp, lane, livec);
-  cluster.sync();
-  const unsigned err = read_error(cluster, sh);
-  const int live = (int)sum_before(sh, kPlanWarps, lane);
+  share_count(team, sh, gwarp, lane, livec);
+  team.sync();
+  const unsigned err = read_error(team, sh);
+  const int live = (int)sum_before(sh, (NC * kCtaWarps), lane);
   const unsigned ahead = sum_before(sh, gwarp, lane);
   // The warp whose part holds page N counts the pages in use below N.
   if (!err && (live < p.num_blocks ? lo <= live && live < hi : gwarp == 0)) {
@@ -357,9 +399,9 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     } else {
       c = (unsigned)live;
     }
-    if (lane < kPlanCtas) *cluster.map_shared_rank(&sh.below, lane) = (int)c;
+    if (lane < NC) *team.at(&sh.below, lane) = (int)c;
   }
-  cluster.sync();
+  team.sync();
   if (err) {
     if (rank == 0 && tid == 0) {
       flag(p.status, err);
@@ -379,7 +421,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (i < hi && i < live && !used) p.copies[2 * (i - rank_live) + 1] = i;
     at += __popc(m);
   }
-  cluster.sync();
+  team.sync();
   at = ahead;
   for (int i0 = lo; i0 < hi; i0 += 32) {
     const int i = i0 + lane;
@@ -398,9 +440,9 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     }
     at += __popc(m);
   }
-  cluster.sync();
+  team.sync();
 #pragma unroll 4
-  for (long long i = gtid; i < entries; i += kPlanCtas * kPlanThreads) {
+  for (long long i = gtid; i < entries; i += NC * kPlanThreads) {
     const int e = p.table[i];
     if (e >= live) p.table[i] = p.ws[e];
   }
@@ -468,19 +510,30 @@ static PageParams page_params(const va_page_pool* g, uint32_t* status) {
 }
 
 template <typename P>
-static cudaError_t launch_pages(void (*kernel)(const P), dim3 grid, int threads, cudaStream_t st, const P& q) {
+static cudaError_t launch_pages(void (*kernel)(const P), dim3 grid, int threads, int cluster, cudaStream_t st,
+                                const P& q) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, q);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// One CTA or a cluster of eight, by the integers a plan goes through.
+template <typename K>
+static cudaError_t launch_plan(K one, K wide, long long ints, cudaStream_t st, const PageParams& q) {
+  if (ints <= kOneCtaInts) return launch_pages(one, dim3(1), kPlanThreads, 1, st, q);
+  return launch_pages(wide, dim3(kWideCtas), kPlanThreads, kWideCtas, st, q);
 }
 
 static size_t pages_ws_bytes(const va_page_pool* g, int32_t num_forks) {
@@ -526,7 +579,8 @@ va_status verify_attn_pages_fork(const va_page_pool* pool, int32_t num_forks, co
   q.copies = copies;
   q.num_copies = num_copies;
   q.ws = (int*)ws;
-  cudaError_t e = launch_pages(pages_fork_kernel, dim3(kPlanCtas), kPlanThreads, cs, q);
+  cudaError_t e = launch_plan(pages_fork_kernel<1>, pages_fork_kernel<kWideCtas>,
+                              pool->num_blocks + (long long)num_forks * pool->max_blocks_per_seq, cs, q);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }
 
@@ -544,7 +598,8 @@ va_status verify_attn_pages_free(const va_page_pool* pool, int32_t num_ranges, c
   q.a = seq;
   q.b = first;
   q.c = last;
-  cudaError_t e = launch_pages(pages_free_kernel, dim3(kPlanCtas), kPlanThreads, cs, q);
+  cudaError_t e = launch_plan(pages_free_kernel<1>, pages_free_kernel<kWideCtas>,
+                              (long long)num_ranges * pool->max_blocks_per_seq, cs, q);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }
 
@@ -562,7 +617,8 @@ va_status verify_attn_pages_compact(const va_page_pool* pool, int32_t* copies, i
   q.num_copies = num_copies;
   q.live = live_blocks;
   q.ws = (int*)ws;
-  cudaError_t e = launch_pages(pages_compact_kernel, dim3(kPlanCtas), kPlanThreads, cs, q);
+  cudaError_t e = launch_plan(pages_compact_kernel<1>, pages_compact_kernel<kWideCtas>,
+                              pool->num_blocks + (long long)pool->num_seqs * pool->max_blocks_per_seq, cs, q);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }
 
@@ -594,7 +650,7 @@ va_status verify_attn_pages_copy(void* const* pools, int32_t num_pools, int64_t 
     q.status = (unsigned*)status;
     int per = (152 * 8 + m - 1) / m;
     if (per > max_copies) per = max_copies;
-    cudaError_t e = launch_pages(pages_copy_kernel, dim3((unsigned)per, (unsigned)m), kCopyThreads, cs, q);
+    cudaError_t e = launch_pages(pages_copy_kernel, dim3((unsigned)per, (unsigned)m), kCopyThreads, 1, cs, q);
     if (e != cudaSuccess) return note_cuda(e);
   }
   return VA_OK;

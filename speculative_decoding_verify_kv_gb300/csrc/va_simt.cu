@@ -25,20 +25,24 @@ constexpr int kSimtRows = 16;    // query rows per CTA
 constexpr int kSimtTile = 32;    // tokens per tile
 constexpr int kSimtThreads = 128;
 
-template <int D>
-constexpr int simt_smem_floats() {
-  return kSimtRows * D + kSimtTile * (D + 1) + kSimtTile * D + kSimtRows * kSimtTile;
-}
+// Floats from one K row of the tile to the next: the scores are read one
+// value per lane and token, or (WIN) four.
+template <int D, bool WIN>
+struct SimtCfg {
+  static constexpr int LDK = WIN ? D + 4 : D + 1;
+  static constexpr int SMEM = (kSimtRows * D + kSimtTile * LDK + kSimtTile * D + kSimtRows * kSimtTile) * 4;
+};
 
 // WIN: a windowed call; token indexes then count the span of visible tokens
 // (WinSpan).
 template <int D, int KVT, bool WIN>
 __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params p) {
   constexpr int NK = D / 32;  // accumulator columns per lane
+  constexpr int LDK = SimtCfg<D, WIN>::LDK;
   extern __shared__ float sm[];
   float* Qs = sm;                              // [16][D]
-  float* Ks = Qs + kSimtRows * D;              // [32][D+1]
-  float* Vs = Ks + kSimtTile * (D + 1);        // [32][D]
+  float* Ks = Qs + kSimtRows * D;              // [32][LDK]
+  float* Vs = Ks + kSimtTile * LDK;            // [32][D]
   float* Ps = Vs + kSimtTile * D;              // [16][32]
   __shared__ float alpha_s[kSimtRows];
   __shared__ unsigned mask_s[kSimtRows];
@@ -110,22 +114,54 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
     for (int k = 0; k < NK; ++k) acc[i][k] = 0.f;
   }
 
+  // A chain's row block sees no token past its last row, nor (but for the
+  // sinks) one before its first row's window.
+  const bool cut = WIN && kind == 0;
+  const int see_lo = cut ? win_low(p, ctx + rbase / p.G) - ws.skip : 0;
+  const int see_hi = cut ? vctx + (rbase + nrows - 1) / p.G + 1 : shi;
   if (!err) {
     for (int t0 = slo; t0 < shi; t0 += kSimtTile) {
+      if (cut && (t0 >= see_hi || (t0 + kSimtTile <= see_lo && t0 >= p.sinks))) continue;
       __syncthreads();
+      if constexpr (WIN) {
+        // Four elements per thread and step.
+        for (int i = tid; i < kSimtTile * (D / 4); i += kSimtThreads) {
+          const int t = i / (D / 4), d = 4 * (i % (D / 4));
+          const int tok = t0 + t;
+          float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
+          if (tok < shi && !(tok >= ws.dead_lo && tok < ws.dead_hi)) {  // seen by some row
+            const bool draft = tok >= vctx && scratch;
+            const long long row = draft ? scratch_row(p, row0, kvh, tok - vctx)
+                                        : kv_row(p, s, kvh, tok >= ws.head ? tok + ws.skip : tok);
+            const void* kb = draft ? p.dk : p.k;
+            const void* vb = draft ? p.dv : p.v;
+            if (row < 0) {
+              atomicOr(&bad_s, 2);
+            } else if (KVT == VA_F32) {
+              kx = reinterpret_cast<const float4*>(kb)[(row * D + d) / 4];
+              vx = reinterpret_cast<const float4*>(vb)[(row * D + d) / 4];
+            } else {
+              kx = make_float4(load_kv<KVT>(kb, row, p.row_bytes, d), load_kv<KVT>(kb, row, p.row_bytes, d + 1),
+                               load_kv<KVT>(kb, row, p.row_bytes, d + 2), load_kv<KVT>(kb, row, p.row_bytes, d + 3));
+              vx = make_float4(load_kv<KVT>(vb, row, p.row_bytes, d), load_kv<KVT>(vb, row, p.row_bytes, d + 1),
+                               load_kv<KVT>(vb, row, p.row_bytes, d + 2), load_kv<KVT>(vb, row, p.row_bytes, d + 3));
+            }
+          }
+          *reinterpret_cast<float4*>(Ks + t * LDK + d) = kx;
+          *reinterpret_cast<float4*>(Vs + t * D + d) = vx;
+        }
+      } else {
       // Decode the K/V tile; tokens past the range become zeros.
       for (int i = tid; i < kSimtTile * D; i += kSimtThreads) {
         int t = i / D, d = i % D;
         int tok = t0 + t;
         float kx = 0.f, vx = 0.f;
-        if (WIN && tok >= ws.dead_lo && tok < ws.dead_hi) {
-          // seen by no row: not read
-        } else if (tok < shi && tok >= vctx && scratch) {
-          const long long row = scratch_row(p, row0, kvh, tok - vctx);
+        if (tok < shi && tok >= ctx && scratch) {
+          const long long row = scratch_row(p, row0, kvh, tok - ctx);
           kx = load_kv<KVT>(p.dk, row, p.row_bytes, d);
           vx = load_kv<KVT>(p.dv, row, p.row_bytes, d);
         } else if (tok < shi) {
-          long long row = kv_row(p, s, kvh, WIN && tok >= ws.head ? tok + ws.skip : tok);
+          long long row = kv_row(p, s, kvh, tok);
           if (row < 0) {
             atomicOr(&bad_s, 2);
           } else {
@@ -133,8 +169,9 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
             vx = load_kv<KVT>(p.v, row, p.row_bytes, d);
           }
         }
-        Ks[t * (D + 1) + d] = kx;
+        Ks[t * LDK + d] = kx;
         Vs[t * D + d] = vx;
+      }
       }
       __syncthreads();
       if (bad_s & 2) {
@@ -143,13 +180,29 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
       }
       // Scores: lane = token, rows warp + 4i.
       const int tok = t0 + lane;
+      float dots[4] = {0.f, 0.f, 0.f, 0.f};
+      if (WIN) {
+        // The four rows of the warp from one read of K (rows past the block's
+        // last hold whatever the shared memory held and are dropped below).
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+          const float4 k4 = *reinterpret_cast<const float4*>(Ks + lane * LDK + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 q = *reinterpret_cast<const float4*>(Qs + (warp + 4 * i) * D + d);
+            dots[i] = fmaf(q.w, k4.w, fmaf(q.z, k4.z, fmaf(q.y, k4.y, fmaf(q.x, k4.x, dots[i]))));
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int rl = warp + 4 * i;
         if (rl >= nrows) continue;
-        float dot = 0.f;
+        float dot = dots[i];
+        if (!WIN) {
 #pragma unroll 8
-        for (int d = 0; d < D; ++d) dot = fmaf(Qs[rl * D + d], Ks[lane * (D + 1) + d], dot);
+          for (int d = 0; d < D; ++d) dot = fmaf(Qs[rl * D + d], Ks[lane * LDK + d], dot);
+        }
         bool vis = tok < shi &&
                    (tok < vctx || draft_visible(kind, mask_s[rl], (rbase + rl) / p.G, tok - vctx));
         if (WIN)
@@ -171,6 +224,28 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
       }
       __syncthreads();
       // acc[row][d] = alpha * acc + sum_t P[row][t] V[t][d]; lane owns d = lane + 32k.
+      if constexpr (WIN) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = warp + 4 * i < nrows ? alpha_s[warp + 4 * i] : 0.f;
+#pragma unroll
+          for (int k = 0; k < NK; ++k) acc[i][k] *= a;
+        }
+#pragma unroll 2
+        for (int t = 0; t < kSimtTile; t += 4) {
+          float4 pv[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (warp + 4 * i) * kSimtTile + t);
+#pragma unroll
+          for (int k = 0; k < NK; ++k) {
+            const float* v = Vs + t * D + lane + 32 * k;
+            const float v0 = v[0], v1 = v[D], v2 = v[2 * D], v3 = v[3 * D];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[i][k] = fmaf(pv[i].w, v3, fmaf(pv[i].z, v2, fmaf(pv[i].y, v1, fmaf(pv[i].x, v0, acc[i][k]))));
+          }
+        }
+      } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int rl = warp + 4 * i;
@@ -183,6 +258,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
 #pragma unroll
           for (int k = 0; k < NK; ++k) acc[i][k] = fmaf(pv, Vs[t * D + lane + 32 * k], acc[i][k]);
         }
+      }
       }
     }
   }
@@ -209,7 +285,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
 
 template <int D, int KVT, bool WIN>
 static cudaError_t launch_simt_t(const Params& p, dim3 grid, cudaStream_t st) {
-  constexpr int smem = simt_smem_floats<D>() * 4;
+  constexpr int smem = SimtCfg<D, WIN>::SMEM;
   static bool attr_set = false;
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(simt_partial_kernel<D, KVT, WIN>,
@@ -235,9 +311,9 @@ static cudaError_t launch_simt_t(const Params& p, dim3 grid, cudaStream_t st) {
 
 int simt_smem_bytes(int D) {
   switch (D) {
-    case 64: return simt_smem_floats<64>() * 4;
-    case 128: return simt_smem_floats<128>() * 4;
-    default: return simt_smem_floats<256>() * 4;
+    case 64: return SimtCfg<64, false>::SMEM;
+    case 128: return SimtCfg<128, false>::SMEM;
+    default: return SimtCfg<256, false>::SMEM;
   }
 }
 

@@ -444,6 +444,14 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
   int lo, hi, slo, shi;
   split_range(L, p.S, split, &lo, &hi);
   sub_range(lo, hi, nsub, p.min_sub, sub, &slo, &shi);
+  if (WIN && seq_kind_of(p, s) == 0) {
+    // A chain's row block sees no token past its last row, nor (but for the
+    // sinks) one before its first row's window.
+    shi = min(shi, vctx + (min(R, (rb + 1) * kM) - 1) / G + 1);
+    const int a = win_low(p, ctx + rb * kM / G) - ws.skip;
+    if (slo >= p.sinks && a > slo) slo += (a - slo) / kNT * kNT;
+    shi = max(shi, slo);
+  }
   const int ntiles = (shi - slo + kNT - 1) / kNT;
   if (ntiles == 0 && !err) {
     // An empty chunk (short span): its rows' slots become (-inf, 0) at once,
