@@ -35,6 +35,7 @@ va_status note_cuda(cudaError_t e) {
   return VA_ERR_CUDA;
 }
 cudaError_t launch_merge(const Params& p, cudaStream_t st);
+cudaError_t launch_window_merge(const Params& p, cudaStream_t st);
 cudaError_t launch_debug_row_map(const Params& p, int* row_seq, unsigned* anc, cudaStream_t st);
 cudaError_t launch_debug_split(const Params& p, int* ranges, cudaStream_t st);
 cudaError_t launch_promote(const Params& p, const int* acc_len, const int* nodes,
@@ -553,7 +554,7 @@ va_status verify_attn_window(const va_problem* p, const va_kv* kv, int32_t mode,
                                                   : launch_simt_partial(q, pl.grid, cs);
   if (e != cudaSuccess) return note_cuda(e);
   if (pl.few_rows && pl.slots == 1) return VA_OK;  // it writes the outputs itself
-  e = launch_merge(q, cs);
+  e = launch_window_merge(q, cs);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }
 

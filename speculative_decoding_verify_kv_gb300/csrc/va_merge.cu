@@ -29,9 +29,7 @@ constexpr int kMergeThreads = 256;
 // 16 rows x 24 heads) run in one wave on 152 SMs.  Each group keeps its own
 // maximum M_g; the groups are then combined in ascending group order with
 // the overall maximum M:  l = sum_g 2^(M_g - M) l_g, acc likewise.
-// WIN: a windowed call (its chunks cut the span of visible tokens; O may be
-// bf16, rounded once here).
-template <int D, bool WIN>
+template <int D>
 __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const Params p) {
   constexpr int TC = D / 4;
   constexpr int NG = kMergeThreads / TC;
@@ -60,8 +58,6 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const Params p)
     if (p.cu_rows[mid] <= grow) s_lo = mid;
     else s_hi = mid - 1;
   }
-  // A windowed call leaves a row that no sequence covers as it was.
-  if (WIN && !(p.cu_rows[s_lo] <= grow && grow < p.cu_rows[s_lo + 1])) return;
   int sr0, sn, sctx;
   int nan = !(p.cu_rows[s_lo] <= grow && grow < p.cu_rows[s_lo + 1]) ||
             (check_sequence(p, s_lo, &sr0, &sn, &sctx) & VA_DEV_BAD_ROWS) != 0u;
@@ -72,7 +68,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const Params p)
   int live = p.slots;
   if (!nan && p.S == 1 && sctx >= 0) {
     int lo0, hi0;
-    split_range(WIN ? win_span(p, sctx, sn).len : sctx + sn, 1, 0, &lo0, &hi0);
+    split_range(sctx + sn, 1, 0, &lo0, &hi0);
     live = max(1, live_subs(lo0, hi0, seq_subs(p, sn), p.min_sub));
   }
   for (int s0 = grp; s0 < live && !nan; s0 += BATCH * NG) {
@@ -146,15 +142,7 @@ __global__ void __launch_bounds__(kMergeThreads, 3) merge_kernel(const Params p)
     const float inv = 1.f / lt;
     float4 out = bad ? make_float4(NAN, NAN, NAN, NAN)
                      : make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv);
-    if (WIN && p.o_bf16) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(out.x, out.y), b = __floats2bfloat162_rn(out.z, out.w);
-      uint2 w;
-      memcpy(&w.x, &a, 4);
-      memcpy(&w.y, &b, 4);
-      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + item * D + 4 * tcol) = w;
-    } else {
-      *reinterpret_cast<float4*>(p.o + item * D + 4 * tcol) = out;
-    }
+    *reinterpret_cast<float4*>(p.o + item * D + 4 * tcol) = out;
     if (tcol == 0) p.lse[item] = bad ? NAN : (M + log2f(lt)) * kLn2;
   }
 }
@@ -172,8 +160,143 @@ static cudaError_t launch_merge_t(const Params& p, cudaStream_t st, long long it
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.window > 0 ? cudaLaunchKernelEx(&cfg, merge_kernel<D, true>, p)
-                      : cudaLaunchKernelEx(&cfg, merge_kernel<D, false>, p);
+  return cudaLaunchKernelEx(&cfg, merge_kernel<D>, p);
+}
+
+// Merge of a windowed call: few chunks (one to about sixteen) of many rows,
+// so one warp per (row, head), eight to a CTA, and no barrier; the chunks'
+// loads of a lane's columns are in flight together, four at a time.  Same
+// sums in the same order as above with one slot group.  O may be bf16,
+// rounded once here.  (A CTA per (row, head) took 18.7 us for 96 rows x 24
+// heads of D = 256 in 6 chunks, 5 waves of CTAs that each wait for the row's
+// sequence.)
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Params p) {
+  constexpr int NC = D / 128 > 0 ? D / 128 : 1;  // float4 columns per lane (D = 64: half the lanes)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * (kMergeThreads / 32) + threadIdx.x / 32;
+  if (item >= (long long)p.total_rows * p.H) return;
+  const int grow = (int)(item / p.H), h = (int)(item % p.H);
+  // The row's sequence: the last s with cu_rows[s] <= row (32 at a time).
+  int s = -1;
+  for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+    const unsigned m = __ballot_sync(0xffffffffu, s0 + lane < p.num_seqs && p.cu_rows[s0 + lane] <= grow);
+    if (m) s = s0 + 31 - __clz(m);
+  }
+  // A row that no sequence covers stays as it was.
+  if (s < 0 || grow >= p.cu_rows[s + 1]) return;
+  int sr0, sn, sctx;
+  bool nan = (check_sequence(p, s, &sr0, &sn, &sctx) & VA_DEV_BAD_ROWS) != 0u;
+  int live = p.slots;
+  if (!nan && sctx >= 0) {
+    int lo0, hi0;
+    split_range(win_span(p, sctx, sn).len, 1, 0, &lo0, &hi0);
+    live = max(1, live_subs(lo0, hi0, seq_subs(p, sn), p.min_sub));
+  }
+  float M = -INFINITY, l = 0.f;
+  float4 acc[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool mine = D >= 128 || lane < 16;
+  for (int s0 = 0; s0 < live && !nan; s0 += 4) {
+    float mm[4], ll[4];
+    float4 aa[4][NC];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      mm[k] = -INFINITY;
+      ll[k] = 0.f;
+      const bool in = s0 + k < live;
+      const long long si = slot_index(p, in ? s0 + k : s0, grow, h);
+      if (in) {
+        mm[k] = p.ws_ml[2 * si];
+        ll[k] = p.ws_ml[2 * si + 1];
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        aa[k][c] = in && mine ? *reinterpret_cast<const float4*>(p.ws_acc + si * D + 4 * (lane + 32 * c))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float bm = M;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (isnan(mm[k]) || isnan(ll[k])) nan = true;
+      if (ll[k] > 0.f) bm = fmaxf(bm, mm[k]);
+    }
+    if (bm > M) {
+      const float f = exp2f(M - bm);  // 0 while nothing was live
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        acc[c].x *= f;
+        acc[c].y *= f;
+        acc[c].z *= f;
+        acc[c].w *= f;
+      }
+      M = bm;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!(ll[k] > 0.f)) continue;  // an empty chunk: its acc is never read as data
+      const float w = exp2f(mm[k] - M);
+      l = fmaf(w, ll[k], l);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        acc[c].x = fmaf(w, aa[k][c].x, acc[c].x);
+        acc[c].y = fmaf(w, aa[k][c].y, acc[c].y);
+        acc[c].z = fmaf(w, aa[k][c].z, acc[c].z);
+        acc[c].w = fmaf(w, aa[k][c].w, acc[c].w);
+      }
+    }
+  }
+  const float inv = nan ? NAN : 1.f / l;
+  if (mine) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const float4 out = make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv);
+      const long long at = item * D + 4 * (lane + 32 * c);
+      if (p.o_bf16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(out.x, out.y), b = __floats2bfloat162_rn(out.z, out.w);
+        uint2 w;
+        memcpy(&w.x, &a, 4);
+        memcpy(&w.y, &b, 4);
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + at) = w;
+      } else {
+        *reinterpret_cast<float4*>(p.o + at) = out;
+      }
+    }
+  }
+  if (lane == 0) p.lse[item] = nan ? NAN : (M + log2f(l)) * kLn2;
+}
+
+template <int D>
+static cudaError_t launch_window_merge_t(const Params& p, cudaStream_t st, long long items) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = dim3((unsigned)((items + kMergeThreads / 32 - 1) / (kMergeThreads / 32)));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, window_merge_kernel<D>, p);
+}
+
+cudaError_t launch_window_merge(const Params& p, cudaStream_t st) {
+  const long long items = (long long)p.total_rows * p.H;
+  if (items == 0) return cudaSuccess;
+  cudaError_t e;
+  switch (p.D) {
+    case 64: e = launch_window_merge_t<64>(p, st, items); break;
+    case 128: e = launch_window_merge_t<128>(p, st, items); break;
+    case 256: e = launch_window_merge_t<256>(p, st, items); break;
+    default: return cudaErrorInvalidValue;
+  }
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
 }
 
 cudaError_t launch_merge(const Params& p, cudaStream_t st) {
