@@ -375,7 +375,9 @@ va_status verify_attn_noalloc(const va_problem *p, const va_kv *kv, int32_t mode
  *   - num_splits is here the largest number of chunks that a sequence's
  *     visible tokens are cut into (whole 64-token tiles, at least 128
  *     tokens).  About SMs / (num_seqs * num_kv_heads) chunks fill the GPU once
- *     (va_window_splits).  No choice depends on the other sequences of the
+ *     (va_window_splits).  With o_dtype VA_F32 more may be made, so that
+ *     none holds more than 2,048 tokens: over more, the tensor cores' running
+ *     sums drift visibly.  No choice depends on the other sequences of the
  *     launch: kernel and chunks follow from the types, from num_splits and
  *     max_rows_per_seq as given, and from the sequence itself.
  *   - Rows that no sequence covers stay as they were.  Where row offsets

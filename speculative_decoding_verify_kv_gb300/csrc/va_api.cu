@@ -24,6 +24,8 @@ int umma_smem_bytes(int D, int kv_dtype);
 int umma_threads(int D, int kv_dtype);
 cudaError_t launch_umma_window(const Params& p, dim3 grid, cudaStream_t st);
 cudaError_t launch_window_rows(const Params& p, cudaStream_t st);
+cudaError_t launch_window_tiles(const Params& p, cudaStream_t st);
+int window_tiles_rows(int D);
 cudaError_t launch_tq8_partial(const Params& p, dim3 grid, cudaStream_t st);
 int tq8_rows_per_block();
 int tq8_threads();
@@ -48,6 +50,8 @@ constexpr int kSimtThreadsPerBlock = 128;
 constexpr int kUmmaRowsPerBlock = 128;
 constexpr int kMinSubTokens = 128;
 constexpr int kMaxSubSplits = 16;
+constexpr int kMaxExactTokens = 2048;  // of a chunk, see window_plan
+constexpr int kJoinedChunks = 8;       // that the kernels for few rows join themselves
 
 static int sm_count() {
   int dev = 0;
@@ -132,7 +136,7 @@ static va_status check(const va_problem* p, const va_kv* kv, int mode) {
 struct Plan {
   int kernel;  // VA_KERNEL_*
   int P, slots, rows_per_block, row_blocks, threads, smem;
-  bool few_rows = false;  // windowed calls
+  int min_splits = 1, small = 0;  // windowed calls: 1 the kernel for few rows, 2 the one for row tiles
   dim3 grid;
 };
 
@@ -493,20 +497,35 @@ static va_status check_window(const va_problem* p, const va_kv* kv, int mode, co
 
 // num_splits is the chunk count of a one-row-block sequence; a sequence of
 // b row blocks takes max(1, num_splits / b) chunks.
-static Plan window_plan(const va_problem* p, const va_kv* kv) {
+static Plan window_plan(const va_problem* p, const va_kv* kv, const va_window* w) {
   Plan pl = make_plan(p, kv);
   if (pl.kernel == VA_KERNEL_TENSOR_Q8) {  // the row-major kernel reads contiguous caches by pages here
     pl.kernel = VA_KERNEL_TENSOR;
     pl.rows_per_block = kUmmaRowsPerBlock;
-    const int rows = p->max_rows_per_seq * (p->num_heads / kv->num_kv_heads);
-    pl.row_blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
+    pl.row_blocks = (p->max_rows_per_seq * (p->num_heads / kv->num_kv_heads) + pl.rows_per_block - 1) / pl.rows_per_block;
   }
-  // At most 16 query rows per KV head (by the caller's bound, never by the
-  // rows of one launch): the kernel for few rows.
-  pl.few_rows = pl.kernel == VA_KERNEL_TENSOR && !kv->draft_k &&
-                p->max_rows_per_seq * (p->num_heads / kv->num_kv_heads) <= 16;
+  // By the query rows per KV head that the caller's bound allows (never by the
+  // rows of one launch): the kernel for at most 16, the row tiles of a bf16
+  // cache, else the 128-row kernel.
+  const int rows = p->max_rows_per_seq * (p->num_heads / kv->num_kv_heads);
+  if (pl.kernel == VA_KERNEL_TENSOR && !kv->draft_k)
+    pl.small = rows <= 16 ? 1 : kv->dtype == VA_BF16 && rows <= window_tiles_rows(kv->head_dim) ? 2 : 0;
   pl.P = pl.slots = p->num_splits;
-  pl.grid.x = (unsigned)(pl.slots > pl.row_blocks ? pl.slots : pl.row_blocks);
+  pl.min_splits = 1;
+  if (pl.kernel == VA_KERNEL_TENSOR && !pl.small && w->o_dtype == VA_F32) {
+    // The tensor cores round their fp32 sums towards zero at every step: O
+    // drifts by some 1e-5 of itself over 4,096 tokens.  Where O is returned in
+    // fp32 a chunk holds at most 2,048.
+    const long long cap = kv->page_size ? (long long)kv->max_blocks_per_seq * kPage : (long long)kv->capacity;
+    long long most = (long long)w->window + w->sinks + p->max_rows_per_seq + 4 * kPage;
+    if (most > cap + p->max_rows_per_seq) most = cap + p->max_rows_per_seq;
+    long long need = (most + kMaxExactTokens - 1) / kMaxExactTokens;
+    if (need > 256) need = 256;
+    pl.min_splits = (int)need;
+    if (pl.slots < pl.min_splits) pl.P = pl.slots = pl.min_splits;
+  }
+  const int per = pl.min_splits * pl.row_blocks;
+  pl.grid.x = (unsigned)(pl.slots > per ? pl.slots : per);
   return pl;
 }
 
@@ -517,7 +536,7 @@ extern "C" {
 size_t va_window_workspace_size(const va_problem* p, const va_kv* kv, const va_window* w) {
   if (check_window(p, kv, VA_MODE_CHAIN, w) != VA_OK && check_window(p, kv, VA_MODE_MIXED, w) != VA_OK)
     return 0;
-  return ws_bytes_for(p, kv, window_plan(p, kv));
+  return ws_bytes_for(p, kv, window_plan(p, kv, w));
 }
 
 int32_t va_window_splits(const va_problem* p, const va_kv* kv, const va_window* w) {
@@ -538,22 +557,23 @@ va_status verify_attn_window(const va_problem* p, const va_kv* kv, int32_t mode,
   if (p->total_rows == 0) return VA_OK;
   if (!o || !lse) return VA_ERR_INVALID_ARG;
   if (!aligned16(o)) return VA_ERR_ALIGNMENT;
-  Plan pl = window_plan(p, kv);
+  Plan pl = window_plan(p, kv, w);
   if (!ws || ws_bytes < ws_bytes_for(p, kv, pl)) return VA_ERR_WORKSPACE_TOO_SMALL;
   if (((uintptr_t)ws & 255u) != 0) return VA_ERR_ALIGNMENT;
   cudaStream_t cs = (cudaStream_t)stream;
   st = check_stream_device(cs);
   if (st != VA_OK) return st;
   Params q = make_params(p, kv, mode, pl, ws, (float*)o, lse, status);
-  q.min_splits = 1;
+  q.min_splits = pl.min_splits;
   q.window = w->window;
   q.sinks = w->sinks;
   q.o_bf16 = w->o_dtype == VA_BF16;
-  cudaError_t e = pl.few_rows                       ? launch_window_rows(q, cs)
+  cudaError_t e = pl.small == 1                     ? launch_window_rows(q, cs)
+                  : pl.small == 2                 ? launch_window_tiles(q, cs)
                   : pl.kernel == VA_KERNEL_TENSOR ? launch_umma_window(q, pl.grid, cs)
                                                   : launch_simt_partial(q, pl.grid, cs);
   if (e != cudaSuccess) return note_cuda(e);
-  if (pl.few_rows && pl.slots == 1) return VA_OK;  // it writes the outputs itself
+  if (pl.small && pl.slots <= kJoinedChunks) return VA_OK;  // these write the outputs themselves
   e = launch_window_merge(q, cs);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }

@@ -1,0 +1,613 @@
+// Warp-MMA attention of 16 query rows over 16-token pages: what the windowed
+// kernels for few rows (one row tile per CTA) and for row tiles share.
+//
+// Per page, in base 2 (c = scale log2 e):
+//   S = Q K^T          16 rows x 16 tokens, fp32
+//   m' = max(m, max S c), a = 2^(m - m'), P = 2^(S c - m')
+//   l <- a l + sum P,  O <- a O + P V
+// P V starts from zero for every page and is added in fp32 registers, where
+// the rescaling by a costs nothing more (one fused multiply-add): tensor
+// cores round their running sum towards zero, which over the pages of a
+// long window is a drift of 2^-24 each (1e-5 after 4,096 tokens, measured).
+//
+// bf16: P enters as bf16 hi + lo (16 bits).  Q8_0: the codes enter the MMAs as
+// exact fp16 integers, K's scales multiply the fp32 sums of each 32-element
+// block, V's elements become fp16(d q) (one rounding) and P is fp16.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <string.h>
+
+#include "va_common.cuh"
+#include "va_sm100.cuh"
+
+namespace va {
+using namespace sm100;
+namespace cg = cooperative_groups;
+
+constexpr int kTileRows = 16;  // query rows of one warp
+constexpr uint64_t kPageWaitNs = 2000000000ull;
+
+// A page of one tensor in shared memory: bf16 [D / 64][16 tokens][128 bytes]
+// with 128-byte swizzle, Q8_0 16 raw rows.
+template <int D, int KVT>
+struct PageCfg {
+  static constexpr bool kQ8 = KVT == VA_Q8_0;
+  static constexpr int RB = kQ8 ? D / 32 * 34 : D * 2;  // bytes of a cache row
+  static constexpr int TILE = kPage * RB;
+  static constexpr int TILE_S = (TILE + 1023) / 1024 * 1024;  // K, then V from a 1,024-byte boundary
+  static constexpr int STAGE = 2 * TILE_S;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+
+__device__ __forceinline__ uint32_t h2_sub(uint32_t a, uint32_t b) {
+  __half2 x, y;
+  memcpy(&x, &a, 4);
+  memcpy(&y, &b, 4);
+  x = __hsub2(x, y);
+  memcpy(&a, &x, 4);
+  return a;
+}
+
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+  __half2 x, y;
+  memcpy(&x, &a, 4);
+  memcpy(&y, &b, 4);
+  x = __hmul2(x, y);
+  memcpy(&a, &x, 4);
+  return a;
+}
+
+constexpr uint32_t kBias = 0x64806480u;  // fp16 1152 twice: 0x6400 | (q + 128) is 1152 + q
+
+// The word of four codes at byte address p (even), biased to q + 128.
+__device__ __forceinline__ uint32_t code_word(const unsigned char* p) {
+  const uint32_t lo = *reinterpret_cast<const unsigned short*>(p);
+  const uint32_t hi = *reinterpret_cast<const unsigned short*>(p + 2);
+  return (lo | (hi << 16)) ^ 0x80808080u;
+}
+
+// A warp's 16 rows: Q fragments, what masks them, and their softmax state.  In
+// MMA fragments a lane holds rows g = lane / 4 and g + 8 and column pair
+// lane % 4.
+template <int D, int KVT>
+struct RowTile {
+  static constexpr bool Q8 = KVT == VA_Q8_0;
+  static constexpr int KS = D / 16;  // k steps of S
+  static constexpr int NT = D / 8;   // column tiles of O
+  uint32_t qa[KS][4];
+  unsigned anc[2];
+  int jrow[2], wlo[2];
+  bool rvalid[2];
+  float c2[2];
+  float o[NT][4];
+  float m[2], l[2];
+
+  // Rows r0 .. r0 + R - 1 (at most 16) of the KV head's; false for a bad
+  // parent.
+  __device__ __forceinline__ bool init(const Params& p, const WinSpan& ws, int row0, int ctx, int kind, int kvh,
+                                       int r0, int R, bool check) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3, G = p.G;
+    bool fine = true;
+    // Q8_0: fp16 after a power of two that brings the row's largest |q| below
+    // 1 (exact), the columns of a 32-element block permuted as the codes are.
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = g + 8 * h;
+      rvalid[h] = r < R;
+      anc[h] = 0u;
+      wlo[h] = 0;
+      c2[h] = p.scale_log2;
+      jrow[h] = rvalid[h] ? (r0 + r) / G : 0;
+      const unsigned short* qp = reinterpret_cast<const unsigned short*>(p.q) +
+                                 ((long long)(row0 + jrow[h]) * p.H + kvh * G + (rvalid[h] ? (r0 + r) % G : 0)) * D;
+      if (Q8) {
+        // Per 32-element block b this lane owns elements 32 b + 8 q4 .. + 7.
+        uint4 w[D / 32];
+        float amax = 0.f;
+  #pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+          w[b] = rvalid[h] ? *reinterpret_cast<const uint4*>(qp + 32 * b + 8 * q4) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t u[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+  #pragma unroll
+          for (int k = 0; k < 4; ++k)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xFFFF0000u))));
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        int e = 0;
+        if (amax > 0.f) frexpf(amax, &e);
+        const float qs = ldexpf(1.f, -e);
+        c2[h] = ldexpf(p.scale_log2, e);
+  #pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+          const uint32_t u[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+  #pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t v = pack_f16(__uint_as_float(u[k] << 16) * qs, __uint_as_float(u[k] & 0xFFFF0000u) * qs);
+            qa[2 * b + k / 2][h + 2 * (k & 1)] = v;  // steps of 4 elements per lane: (0,1 | 2,3), (4,5 | 6,7)
+          }
+        }
+      } else {
+  #pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t* qw = reinterpret_cast<const uint32_t*>(qp + 16 * k + 2 * q4);
+          qa[k][h] = rvalid[h] ? qw[0] : 0u;
+          qa[k][h + 2] = rvalid[h] ? qw[4] : 0u;
+        }
+      }
+      if (rvalid[h] && check) {
+        bool bad = false;
+        anc[h] = row_mask(kind, p.parent + row0, jrow[h], &bad);
+        if (bad) {
+          fine = false;
+        } else {
+          wlo[h] = win_low(p, ctx + (kind == 1 ? __popc(anc[h]) - 1 : jrow[h])) - ws.skip;
+          if (kind == 1) anc[h] = window_mask(p, p.parent + row0, jrow[h], ctx, anc[h]);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+    return fine;
+  }
+
+  // One page: its K and V in shared memory, u0 its first span token, shi the
+  // end of the chunk, edge the span token from which no row's window starts
+  // any more.
+  __device__ __forceinline__ void page(const Params& p, int kind, int vctx, int shi, int edge, int u0,
+                                       const unsigned char* ks, const unsigned char* vs) {
+    using C = PageCfg<D, KVT>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+    // S = Q K^T: two tiles of 8 tokens.
+    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    if (Q8) {
+      // A lane's 8 codes of a block (elements 8 q4 .. + 7 of token g of the
+      // tile) make two k steps; the block's sum takes the token's scale.
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) {
+        float cb[2][4];
+        uint32_t x[2], y[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const unsigned char* kr = ks + (8 * t + g) * C::RB + 34 * b + 2 + 8 * q4;
+          x[t] = code_word(kr);
+          y[t] = code_word(kr + 4);
+          cb[t][0] = cb[t][1] = cb[t][2] = cb[t][3] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          mma_f16(cb[t], qa[2 * b], h2_sub(__byte_perm(x[t], 0x64646464u, 0x4140), kBias),
+                  h2_sub(__byte_perm(x[t], 0x64646464u, 0x4342), kBias));
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          mma_f16(cb[t], qa[2 * b + 1], h2_sub(__byte_perm(y[t], 0x64646464u, 0x4140), kBias),
+                  h2_sub(__byte_perm(y[t], 0x64646464u, 0x4342), kBias));
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const unsigned char* d0 = ks + (8 * t + 2 * q4) * C::RB + 34 * b;  // this lane's score columns
+          const float s0 = __half2float(*reinterpret_cast<const __half*>(d0));
+          const float s1 = __half2float(*reinterpret_cast<const __half*>(d0 + C::RB));
+          sc[t][0] = fmaf(s0, cb[t][0], sc[t][0]);
+          sc[t][1] = fmaf(s1, cb[t][1], sc[t][1]);
+          sc[t][2] = fmaf(s0, cb[t][2], sc[t][2]);
+          sc[t][3] = fmaf(s1, cb[t][3], sc[t][3]);
+        }
+      }
+    } else {
+      // Lane's row of the 8 x 8 matrices: tokens 0-7 (k low, k high), 8-15.
+      const int tr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+      const uint32_t kb = smem_u32(ks) + tr * 128;
+      // Four k steps' matrices at a time, four running sums (a warp has few
+      // neighbours to hide an MMA's latency behind).
+      float s2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int k0 = 0; k0 < KS; k0 += 4) {
+        uint32_t b[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          ldmatrix4<false>(b[k], kb + (k0 / 4) * kPage * 128 + (((k * 2 + kc) ^ (tr & 7)) << 4));
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+          mma_bf16(sc[0], qa[k0 + k], b[k][0], b[k][1]);
+          mma_bf16(sc[1], qa[k0 + k], b[k][2], b[k][3]);
+          mma_bf16(s2[0], qa[k0 + k + 1], b[k + 1][0], b[k + 1][1]);
+          mma_bf16(s2[1], qa[k0 + k + 1], b[k + 1][2], b[k + 1][3]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sc[0][e] += s2[0][e];
+        sc[1][e] += s2[1][e];
+      }
+    }
+
+    // Masks, running maximum, P.
+    const bool plain = u0 + kPage <= min(vctx, shi) && (u0 >= edge || u0 + kPage <= p.sinks);
+    float a[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      unsigned vis = 0xFFFFu;
+      if (!plain)
+        vis = rvalid[h] ? visible_bits(kind, anc[h], jrow[h], vctx, shi, u0) & window_bits(kind, p.sinks, wlo[h], vctx, u0)
+                        : 0u;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& x = sc[t][2 * h + e];
+          x = (vis >> (8 * t + 2 * q4 + e)) & 1u ? x * c2[h] : -INFINITY;
+          mx = fmaxf(mx, x);
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float mn = fmaxf(m[h], mx);
+      const float off = mn == -INFINITY ? 0.f : mn;  // while nothing is visible every P is 2^-inf
+      a[h] = ex2f(m[h] - off);
+      m[h] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& x = sc[t][2 * h + e];
+          x = ex2f(x - off);
+          sum += x;
+        }
+      l[h] = fmaf(l[h], a[h], sum);
+    }
+    // P as the MMA's A operand: the score fragments are its rows.
+    uint32_t ph[4], pl[4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float x = sc[t][2 * h], y = sc[t][2 * h + 1];
+        if (Q8) {
+          ph[2 * t + h] = pack_f16(x, y);
+        } else {
+          const uint32_t w = pack_bf16(x, y);
+          ph[2 * t + h] = w;
+          pl[2 * t + h] = pack_bf16(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xFFFF0000u));
+        }
+      }
+    if (Q8) {
+      // V: a lane's word of codes (elements 4 g .. + 3 of a block) of each of
+      // its four tokens; column tile i of the block takes byte i.
+      const unsigned char* v0 = vs + 2 * q4 * C::RB;
+#pragma unroll
+      for (int b = 0; b < D / 32; ++b) {
+        uint32_t w[4], d2[2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = code_word(v0 + ((k & 1) + 8 * (k >> 1)) * C::RB + 34 * b + 2 + 4 * g);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const unsigned char* d = v0 + 8 * k * C::RB + 34 * b;
+          d2[k] = *reinterpret_cast<const unsigned short*>(d) |
+                  ((uint32_t)*reinterpret_cast<const unsigned short*>(d + C::RB) << 16);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // Bytes c of two tokens into the low halves of two fp16 values.
+          const uint32_t sel = 0x4000u | (uint32_t)c | ((uint32_t)(c + 4) << 4);
+          uint32_t f[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t pr = __byte_perm(w[2 * k], w[2 * k + 1], sel);  // bytes: q0, q1
+            f[k] = h2_mul(h2_sub(__byte_perm(pr, 0x64646464u, 0x4140), kBias), d2[k]);
+          }
+          float cc[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16(cc, ph, f[0], f[1]);
+          float(&ot)[4] = o[4 * b + c];
+          ot[0] = fmaf(ot[0], a[0], cc[0]);
+          ot[1] = fmaf(ot[1], a[0], cc[1]);
+          ot[2] = fmaf(ot[2], a[1], cc[2]);
+          ot[3] = fmaf(ot[3], a[1], cc[3]);
+        }
+      }
+    } else {
+      // Lane's row of the transposed matrices: tokens 0-7, 8-15 of columns
+      // 0-7, then of columns 8-15.
+      const int tr = lane & 15, dc = lane >> 4;
+      const uint32_t vb = smem_u32(vs) + tr * 128;
+      // Several column tiles at a time, for the same reason (fewer at D = 256,
+      // whose accumulator leaves fewer registers).
+      constexpr int GR = D == 256 ? 2 : 4;
+#pragma unroll
+      for (int t0 = 0; t0 < NT / 2; t0 += GR) {
+        uint32_t b[GR][4];
+        float cc[2 * GR][4];
+#pragma unroll
+        for (int t = 0; t < GR; ++t)
+          ldmatrix4<true>(b[t], vb + ((t0 + t) / 4) * kPage * 128 + (((((t0 + t) % 4) * 2 + dc) ^ (tr & 7)) << 4));
+#pragma unroll
+        for (int c = 0; c < 2 * GR; ++c) {
+          cc[c][0] = cc[c][1] = cc[c][2] = cc[c][3] = 0.f;
+          mma_bf16(cc[c], pl, b[c / 2][2 * (c & 1)], b[c / 2][2 * (c & 1) + 1]);
+        }
+#pragma unroll
+        for (int c = 0; c < 2 * GR; ++c) mma_bf16(cc[c], ph, b[c / 2][2 * (c & 1)], b[c / 2][2 * (c & 1) + 1]);
+#pragma unroll
+        for (int c = 0; c < 2 * GR; ++c) {
+          float(&ot)[4] = o[2 * t0 + c];
+          ot[0] = fmaf(ot[0], a[0], cc[c][0]);
+          ot[1] = fmaf(ot[1], a[0], cc[c][1]);
+          ot[2] = fmaf(ot[2], a[1], cc[c][2]);
+          ot[3] = fmaf(ot[3], a[1], cc[c][3]);
+        }
+      }
+    }
+  }
+
+  // The state into shared memory: O rows of LD floats, m and l.
+  __device__ __forceinline__ void store(float* os, int ld, float* ms, float* ls) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if (q4 == 0) {
+        ms[g + 8 * h] = m[h];
+        ls[g + 8 * h] = l[h];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      // Q8_0: column tile 4 b + c holds elements 32 b + 4 j + c, j the column.
+      const int col = Q8 ? (t / 4) * 32 + t % 4 + 8 * q4 : 8 * t + 2 * q4;
+      constexpr int next = Q8 ? 4 : 1;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        os[(g + 8 * h) * ld + col] = o[t][2 * h];
+        os[(g + 8 * h) * ld + col + next] = o[t][2 * h + 1];
+      }
+    }
+  }
+};
+
+// Clears what no row sees of a page's V (its tokens may hold anything): the
+// tokens from tail on and span tokens [dead_lo, dead_hi).  Q8_0: their
+// scales.  One warp; its writes reach the copy engine's next fill in order.
+template <int D, int KVT>
+__device__ __forceinline__ void clear_unseen(unsigned char* vs, int u0, int tail, int dead_lo, int dead_hi) {
+  using C = PageCfg<D, KVT>;
+  const int lane = threadIdx.x & 31, t = lane & 15, u = u0 + t;
+  if (t >= tail || (u >= dead_lo && u < dead_hi)) {
+    if (C::kQ8) {
+      if (lane < 16)
+        for (int b = 0; b < D / 32; ++b) *reinterpret_cast<unsigned short*>(vs + t * C::RB + 34 * b) = 0;
+    } else {
+      for (int b = lane >> 4; b < D / 8; b += 2)
+        *reinterpret_cast<uint4*>(vs + (b / 8) * kPage * 128 + t * 128 + (b % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// A page of the cache into shared memory; one thread.  at: the block, or
+// (contiguous cache) the page of the sequence.
+template <int D, int KVT>
+__device__ __forceinline__ void load_page(const Params& p, const CUtensorMap* tmK, const CUtensorMap* tmV, int s,
+                                          int kvh, int at, uint32_t dst, uint32_t bar, uint64_t pol) {
+  using C = PageCfg<D, KVT>;
+  mbar_arrive_expect_tx(bar, 2 * C::TILE);
+  if (C::kQ8) {
+    const long long row = p.page_size == 0 ? ((long long)s * p.KVH + kvh) * p.capacity + (long long)at * kPage
+                                           : ((long long)at * p.KVH + kvh) * kPage;
+    bulk_g2s(dst, (const unsigned char*)p.k + row * C::RB, C::TILE, bar, pol);
+    bulk_g2s(dst + C::TILE_S, (const unsigned char*)p.v + row * C::RB, C::TILE, bar, pol);
+  } else {
+#pragma unroll
+    for (int db = 0; db < D / 64; ++db) {
+      const uint32_t off = db * kPage * 128;
+      if (p.page_size == 0) {
+        tma_load_3d(dst + off, tmK, db * 64, at * kPage, s * p.KVH + kvh, bar, pol);
+        tma_load_3d(dst + C::TILE_S + off, tmV, db * 64, at * kPage, s * p.KVH + kvh, bar, pol);
+      } else {
+        tma_load_4d(dst + off, tmK, db * 64, 0, kvh, at, bar, pol);
+        tma_load_4d(dst + C::TILE_S + off, tmV, db * 64, 0, kvh, at, bar, pol);
+      }
+    }
+  }
+}
+
+// Place of page vp of the span: its block (-1 for a bad table entry), or in a
+// contiguous cache the page of the sequence.
+__device__ __forceinline__ int page_place(const Params& p, const WinSpan& ws, int s, int vp) {
+  const int rp = vp * kPage >= ws.head ? vp + ws.skip / kPage : vp;
+  if (p.page_size == 0) return rp;
+  const int blk = p.block_table[(long long)s * p.max_blocks + rp];
+  return blk < 0 || blk >= p.num_blocks ? -1 : blk;
+}
+
+// Rows of a sequence whose row range is inconsistent come out NaN (called
+// where no merge kernel follows).
+template <int D>
+__device__ __forceinline__ void nan_rows(const Params& p, int s, int kvh) {
+  const int a = max(p.cu_rows[s], 0), b = min(p.cu_rows[s + 1], p.total_rows);
+  for (long long i = (long long)a * p.H * D + threadIdx.x; i < (long long)b * p.H * D; i += blockDim.x)
+    if (i / D % p.H / p.G == kvh) {
+      if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[i] = __float2bfloat16(NAN);
+      else p.o[i] = NAN;
+      if (i % D == 0) p.lse[i / D] = NAN;
+    }
+}
+
+// Where a row's result goes: with one chunk the outputs, and else the chunk's
+// partial for the merge kernel.
+template <int D>
+__device__ __forceinline__ void put_pair(const Params& p, bool partial, int slot, int grow, int head, int c, float x,
+                                         float y) {
+  const long long item = (long long)grow * p.H + head;
+  if (partial)
+    *reinterpret_cast<float2*>(p.ws_acc + slot_index(p, slot, grow, head) * D + c) = make_float2(x, y);
+  else if (p.o_bf16)
+    reinterpret_cast<uint32_t*>(p.o)[(item * D + c) / 2] = pack_bf16(x, y);
+  else
+    *reinterpret_cast<float2*>(p.o + item * D + c) = make_float2(x, y);
+}
+
+// Join the states of each row's NG page groups, in order, and write the rows
+// out.  State (group x, row tile y) lies at index x RT + y.  Every warp of the
+// CTA.  With several chunks in one cluster (at most kJoinChunks) the chunks'
+// states are joined here too, in chunk order, each CTA for its share of the
+// rows, through distributed shared memory; with more, each chunk's partial
+// goes to the workspace.
+constexpr int kJoinChunks = 8;
+
+template <int D, int NG, int RT>
+__device__ __forceinline__ void join_rows(const Params& p, int slot, int row0, int kvh, int R, bool fail, float* os,
+                                          int ld, float (*ms)[kTileRows], float (*ls)[kTileRows]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const bool one = p.slots == 1, partial = p.slots > kJoinChunks;
+  for (int r = warp; r < R; r += warps) {
+    const int tile = r / kTileRows, rt = r % kTileRows;
+    float mr = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NG; ++w) mr = fmaxf(mr, ms[w * RT + tile][rt]);
+    const float off = mr == -INFINITY ? 0.f : mr;
+    float f[NG], lr = 0.f;
+#pragma unroll
+    for (int w = 0; w < NG; ++w) {
+      f[w] = ex2f(ms[w * RT + tile][rt] - off);
+      lr = fmaf(f[w], ls[w * RT + tile][rt], lr);
+    }
+    if (fail) mr = lr = NAN;
+    const int grow = row0 + r / p.G, head = kvh * p.G + r % p.G;
+    const float inv = one ? 1.f / lr : fail ? NAN : 1.f;
+    for (int c = 2 * lane; c < D; c += 64) {
+      float x = 0.f, y = 0.f;
+      float* at = os + (tile * kTileRows + rt) * ld + c;
+#pragma unroll
+      for (int w = 0; w < NG; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(at + w * RT * kTileRows * ld);
+        x = fmaf(f[w], v.x, x);
+        y = fmaf(f[w], v.y, y);
+      }
+      if (one || partial) put_pair<D>(p, partial, slot, grow, head, c, x * inv, y * inv);
+      else *reinterpret_cast<float2*>(at) = make_float2(x, y);  // the first group's place
+    }
+    __syncwarp();
+    if (lane == 0) {
+      if (one) {
+        p.lse[(long long)grow * p.H + head] = (mr + log2f(lr)) * kLn2;
+      } else if (partial) {
+        const long long si = slot_index(p, slot, grow, head);
+        p.ws_ml[2 * si] = mr;
+        p.ws_ml[2 * si + 1] = lr;
+      } else {
+        ms[tile][rt] = mr;
+        ls[tile][rt] = lr;
+      }
+    }
+  }
+  if (one || partial) return;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int r = warp * p.slots + slot; r < R; r += warps * p.slots) {
+    const int tile = r / kTileRows, rt = r % kTileRows;
+    // Lane k holds chunk k's m and l; a chunk without a visible token has l
+    // = 0 and weighs nothing, a failed one is NaN.
+    const bool in = lane < p.slots;
+    const float mk = in ? *cluster.map_shared_rank(&ms[tile][rt], lane) : -INFINITY;
+    const float lk = in ? *cluster.map_shared_rank(&ls[tile][rt], lane) : 0.f;
+    float mr = mk;
+#pragma unroll
+    for (int o = kJoinChunks / 2; o > 0; o >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+    mr = __shfl_sync(0xffffffffu, mr, 0);
+    const bool bad = __any_sync(0xffffffffu, lk != lk);
+    const float fk = lk > 0.f ? ex2f(mk - mr) : 0.f;
+    float lr = 0.f;
+    for (int k = 0; k < p.slots; ++k) lr += __shfl_sync(0xffffffffu, fk * lk, k);
+    const float inv = bad ? NAN : 1.f / lr;
+    const int grow = row0 + r / p.G, head = kvh * p.G + r % p.G;
+    for (int c = 2 * lane; c < D; c += 64) {
+      float x = 0.f, y = 0.f;
+      float* at = os + (tile * kTileRows + rt) * ld + c;
+#pragma unroll 4
+      for (int k = 0; k < p.slots; ++k) {
+        const float w = __shfl_sync(0xffffffffu, fk, k);
+        const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(at, k));
+        x = fmaf(w, v.x, x);
+        y = fmaf(w, v.y, y);
+      }
+      put_pair<D>(p, false, slot, grow, head, c, x * inv, y * inv);
+    }
+    if (lane == 0) p.lse[(long long)grow * p.H + head] = bad ? NAN : (mr + log2f(lr)) * kLn2;
+  }
+  cluster.sync();  // no CTA leaves while its rows are read
+}
+
+// Launch configuration of these kernels: a programmatic dependent, a sequence
+// and KV head's chunks one cluster where they are joined in the kernel.
+struct WindowLaunch {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  WindowLaunch(const Params& p, int threads, size_t smem, cudaStream_t st) {
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)p.slots, (unsigned)p.KVH, (unsigned)p.num_seqs);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.slots;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.slots > 1 && p.slots <= kJoinChunks ? 2 : 1;
+  }
+};
+
+bool make_page_maps(const Params& p, CUtensorMap* k, CUtensorMap* v);
+
+}  // namespace va
