@@ -23,10 +23,10 @@ template <int D, int KVT, int NW>
 struct FewCfg : PageCfg<D, KVT> {
   using C = PageCfg<D, KVT>;
   // Ring depth: as many stages as leave the CTA its share of an SM (2 warps:
-  // a quarter, or half where a quarter holds no two stages), at most 4.
+  // a quarter, or half where a quarter holds no two stages), at most 6.
   static constexpr int BUDGET = (NW > 2 ? 216 : 54 * 1024 / (NW * C::STAGE) >= 2 ? 54 : 108) * 1024;
   static constexpr int FIT = BUDGET / (NW * C::STAGE);
-  static constexpr int NST = FIT > 4 ? 4 : FIT;
+  static constexpr int NST = FIT > 6 ? 6 : FIT;
   static constexpr int EPI = NW * kTileRows * (D + 4) * 4;  // the warps' O rows at the end
   static constexpr int RING = NW * NST * C::STAGE;
   static constexpr int SMEM = (RING > EPI ? RING : EPI) + 1024;
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, co
                                                               const __grid_constant__ CUtensorMap tmV) {
   using C = FewCfg<D, KVT, NW>;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[NW][4];
+  __shared__ __align__(8) uint64_t bars[NW][C::NST];
   __shared__ float m_s[NW][kTileRows], l_s[NW][kTileRows];
   __shared__ int err_s, abort_s;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -85,8 +85,10 @@ __global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, co
   int place = lookup(lane);
   const uint64_t pol = policy_evict_first();
   auto load = [&](int i, int at) {  // page i of this warp into its stage; one lane
-    load_page<D, KVT>(p, &tmK, &tmV, s, kvh, at, smem_u32(ring + (i % C::NST) * C::STAGE),
-                      smem_u32(&bars[warp][i % C::NST]), pol);
+    const uint32_t bar = smem_u32(&bars[warp][i % C::NST]), dst = smem_u32(ring + (i % C::NST) * C::STAGE);
+    mbar_arrive_expect_tx(bar, 2 * C::TILE);
+    load_half<D, KVT>(p, &tmK, false, s, kvh, at, dst, bar, pol);
+    load_half<D, KVT>(p, &tmV, true, s, kvh, at, dst + C::TILE_S, bar, pol);
   };
   // A bad entry loads nothing and stops the warp's loop at that page.
   int good = mine;
@@ -117,7 +119,10 @@ __global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, co
     const int tail = min(shi - u0, kPage);         // tokens of the chunk in it
     if (tail < kPage || (u0 < ws.dead_hi && u0 + kPage > ws.dead_lo))
       clear_unseen<D, KVT>(vs, u0, tail, ws.dead_lo, ws.dead_hi);
-    rows.page(p, kind, vctx, shi, edge, u0, ks, vs);
+    typename RowTile<D, KVT>::Page pg;
+    rows.scores(pg, ks);
+    rows.softmax(pg, p, kind, vctx, shi, edge, u0);
+    rows.values(pg, p, vs);
     // The stage is free: the page NST further on.
     __syncwarp();
     const int nx = i + C::NST;
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, co
 template <int D, int KVT, int NW>
 static cudaError_t launch_few_t(const Params& p, cudaStream_t st) {
   using C = FewCfg<D, KVT, NW>;
-  static_assert(C::NST >= 2 && C::NST <= 4, "ring depth");
+  static_assert(C::NST >= 2 && C::NST <= 6, "ring depth");
   static std::atomic<unsigned long long> ready{0ull};  // devices whose attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -10,7 +10,7 @@
 // cores round their running sum towards zero, which over the pages of a
 // long window is a drift of 2^-24 each (1e-5 after 4,096 tokens, measured).
 //
-// bf16: P enters as bf16 hi + lo (16 bits).  Q8_0: the codes enter the MMAs as
+// bf16: P enters as bf16 hi + lo (16 bits), and a third part where O is fp32.  Q8_0: the codes enter the MMAs as
 // exact fp16 integers, K's scales multiply the fp32 sums of each 32-element
 // block, V's elements become fp16(d q) (one rounding) and P is fp16.
 #pragma once
@@ -35,7 +35,8 @@ struct PageCfg {
   static constexpr bool kQ8 = KVT == VA_Q8_0;
   static constexpr int RB = kQ8 ? D / 32 * 34 : D * 2;  // bytes of a cache row
   static constexpr int TILE = kPage * RB;
-  static constexpr int TILE_S = (TILE + 1023) / 1024 * 1024;  // K, then V from a 1,024-byte boundary
+  static constexpr int ALIGN = kQ8 ? 128 : 1024;  // (the swizzle's period)
+  static constexpr int TILE_S = (TILE + ALIGN - 1) / ALIGN * ALIGN;  // K, then V
   static constexpr int STAGE = 2 * TILE_S;
 };
 
@@ -105,11 +106,21 @@ __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
 
 constexpr uint32_t kBias = 0x64806480u;  // fp16 1152 twice: 0x6400 | (q + 128) is 1152 + q
 
-// The word of four codes at byte address p (even), biased to q + 128.
-__device__ __forceinline__ uint32_t code_word(const unsigned char* p) {
-  const uint32_t lo = *reinterpret_cast<const unsigned short*>(p);
-  const uint32_t hi = *reinterpret_cast<const unsigned short*>(p + 2);
-  return (lo | (hi << 16)) ^ 0x80808080u;
+// Codes 4 w .. 4 w + 3 (N words from w on) of block b of a row, biased to q +
+// 128.  Blocks are 34 bytes, so the codes of odd blocks start on a word and
+// those of even blocks two bytes into one.
+template <int N>
+__device__ __forceinline__ void code_words(uint32_t (&x)[N], const unsigned char* row, int b, int w) {
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(row + 34 * b + (b & 1 ? 2 : 0)) + w;
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = p[k];
+  if (!(b & 1)) {
+    const uint32_t last = p[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = __funnelshift_r(x[k], k + 1 < N ? x[k + 1] : last, 16);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] ^= 0x80808080u;
 }
 
 // A warp's 16 rows: Q fragments, what masks them, and their softmax state.  In
@@ -199,37 +210,43 @@ struct RowTile {
     return fine;
   }
 
-  // One page: its K and V in shared memory, u0 its first span token, shi the
-  // end of the chunk, edge the span token from which no row's window starts
-  // any more.
-  __device__ __forceinline__ void page(const Params& p, int kind, int vctx, int shi, int edge, int u0,
-                                       const unsigned char* ks, const unsigned char* vs) {
+  // What a page leaves between its two products: the scores, then P as the
+  // second MMA's A operand (in parts), and the factor of the earlier sums.
+  struct Page {
+    float sc[2][4];
+    float a[2];
+    uint32_t ph[4], pl[4], pr[4];
+  };
+
+  // Scores of one page: its K in shared memory.  (K's stage is free after
+  // this.)
+  __device__ __forceinline__ void scores(Page& pg, const unsigned char* ks) {
     using C = PageCfg<D, KVT>;
     const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
     // S = Q K^T: two tiles of 8 tokens.
-    float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    float(&sc)[2][4] = pg.sc;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
     if (Q8) {
       // A lane's 8 codes of a block (elements 8 q4 .. + 7 of token g of the
       // tile) make two k steps; the block's sum takes the token's scale.
 #pragma unroll
       for (int b = 0; b < D / 32; ++b) {
         float cb[2][4];
-        uint32_t x[2], y[2];
+        uint32_t x[2][2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const unsigned char* kr = ks + (8 * t + g) * C::RB + 34 * b + 2 + 8 * q4;
-          x[t] = code_word(kr);
-          y[t] = code_word(kr + 4);
+          code_words<2>(x[t], ks + (8 * t + g) * C::RB, b, 2 * q4);
           cb[t][0] = cb[t][1] = cb[t][2] = cb[t][3] = 0.f;
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          mma_f16(cb[t], qa[2 * b], h2_sub(__byte_perm(x[t], 0x64646464u, 0x4140), kBias),
-                  h2_sub(__byte_perm(x[t], 0x64646464u, 0x4342), kBias));
+          mma_f16(cb[t], qa[2 * b], h2_sub(__byte_perm(x[t][0], 0x64646464u, 0x4140), kBias),
+                  h2_sub(__byte_perm(x[t][0], 0x64646464u, 0x4342), kBias));
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          mma_f16(cb[t], qa[2 * b + 1], h2_sub(__byte_perm(y[t], 0x64646464u, 0x4140), kBias),
-                  h2_sub(__byte_perm(y[t], 0x64646464u, 0x4342), kBias));
+          mma_f16(cb[t], qa[2 * b + 1], h2_sub(__byte_perm(x[t][1], 0x64646464u, 0x4140), kBias),
+                  h2_sub(__byte_perm(x[t][1], 0x64646464u, 0x4342), kBias));
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const unsigned char* d0 = ks + (8 * t + 2 * q4) * C::RB + 34 * b;  // this lane's score columns
@@ -269,9 +286,16 @@ struct RowTile {
       }
     }
 
+  }
+
+  // The softmax step of a page: u0 its first span token, shi the end of the
+  // chunk, edge the span token from which no row's window starts any more.
+  __device__ __forceinline__ void softmax(Page& pg, const Params& p, int kind, int vctx, int shi, int edge, int u0) {
+    const int lane = threadIdx.x & 31, q4 = lane & 3;
+    float(&sc)[2][4] = pg.sc;
+    float(&a)[2] = pg.a;
     // Masks, running maximum, P.
     const bool plain = u0 + kPage <= min(vctx, shi) && (u0 >= edge || u0 + kPage <= p.sinks);
-    float a[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       unsigned vis = 0xFFFFu;
@@ -305,7 +329,7 @@ struct RowTile {
       l[h] = fmaf(l[h], a[h], sum);
     }
     // P as the MMA's A operand: the score fragments are its rows.
-    uint32_t ph[4], pl[4];
+    uint32_t(&ph)[4] = pg.ph, (&pl)[4] = pg.pl, (&pr)[4] = pg.pr;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -315,10 +339,22 @@ struct RowTile {
           ph[2 * t + h] = pack_f16(x, y);
         } else {
           const uint32_t w = pack_bf16(x, y);
+          const float xl = x - __uint_as_float(w << 16), yl = y - __uint_as_float(w & 0xFFFF0000u);
+          const uint32_t wl = pack_bf16(xl, yl);
           ph[2 * t + h] = w;
-          pl[2 * t + h] = pack_bf16(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xFFFF0000u));
+          pl[2 * t + h] = wl;
+          // What is left (to 24 bits in all) counts where O leaves in fp32.
+          pr[2 * t + h] = pack_bf16(xl - __uint_as_float(wl << 16), yl - __uint_as_float(wl & 0xFFFF0000u));
         }
       }
+  }
+
+  // O <- a O + P V of a page: its V in shared memory.
+  __device__ __forceinline__ void values(const Page& pg, const Params& p, const unsigned char* vs) {
+    using C = PageCfg<D, KVT>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
+    const float(&a)[2] = pg.a;
+    const uint32_t(&ph)[4] = pg.ph, (&pl)[4] = pg.pl, (&pr)[4] = pg.pr;
     if (Q8) {
       // V: a lane's word of codes (elements 4 g .. + 3 of a block) of each of
       // its four tokens; column tile i of the block takes byte i.
@@ -327,13 +363,18 @@ struct RowTile {
       for (int b = 0; b < D / 32; ++b) {
         uint32_t w[4], d2[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = code_word(v0 + ((k & 1) + 8 * (k >> 1)) * C::RB + 34 * b + 2 + 4 * g);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t x[1];
+          code_words<1>(x, v0 + ((k & 1) + 8 * (k >> 1)) * C::RB, b, g);
+          w[k] = x[0];
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const unsigned char* d = v0 + 8 * k * C::RB + 34 * b;
           d2[k] = *reinterpret_cast<const unsigned short*>(d) |
                   ((uint32_t)*reinterpret_cast<const unsigned short*>(d + C::RB) << 16);
         }
+        float cc[4][4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           // Bytes c of two tokens into the low halves of two fp16 values.
@@ -344,13 +385,16 @@ struct RowTile {
             const uint32_t pr = __byte_perm(w[2 * k], w[2 * k + 1], sel);  // bytes: q0, q1
             f[k] = h2_mul(h2_sub(__byte_perm(pr, 0x64646464u, 0x4140), kBias), d2[k]);
           }
-          float cc[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(cc, ph, f[0], f[1]);
+          cc[c][0] = cc[c][1] = cc[c][2] = cc[c][3] = 0.f;
+          mma_f16(cc[c], ph, f[0], f[1]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
           float(&ot)[4] = o[4 * b + c];
-          ot[0] = fmaf(ot[0], a[0], cc[0]);
-          ot[1] = fmaf(ot[1], a[0], cc[1]);
-          ot[2] = fmaf(ot[2], a[1], cc[2]);
-          ot[3] = fmaf(ot[3], a[1], cc[3]);
+          ot[0] = fmaf(ot[0], a[0], cc[c][0]);
+          ot[1] = fmaf(ot[1], a[0], cc[c][1]);
+          ot[2] = fmaf(ot[2], a[1], cc[c][2]);
+          ot[3] = fmaf(ot[3], a[1], cc[c][3]);
         }
       }
     } else {
@@ -371,8 +415,10 @@ struct RowTile {
 #pragma unroll
         for (int c = 0; c < 2 * GR; ++c) {
           cc[c][0] = cc[c][1] = cc[c][2] = cc[c][3] = 0.f;
-          mma_bf16(cc[c], pl, b[c / 2][2 * (c & 1)], b[c / 2][2 * (c & 1) + 1]);
+          if (!p.o_bf16) mma_bf16(cc[c], pr, b[c / 2][2 * (c & 1)], b[c / 2][2 * (c & 1) + 1]);
         }
+#pragma unroll
+        for (int c = 0; c < 2 * GR; ++c) mma_bf16(cc[c], pl, b[c / 2][2 * (c & 1)], b[c / 2][2 * (c & 1) + 1]);
 #pragma unroll
         for (int c = 0; c < 2 * GR; ++c) mma_bf16(cc[c], ph, b[c / 2][2 * (c & 1)], b[c / 2][2 * (c & 1) + 1]);
 #pragma unroll
@@ -433,30 +479,19 @@ __device__ __forceinline__ void clear_unseen(unsigned char* vs, int u0, int tail
   __syncwarp();
 }
 
-// A page of the cache into shared memory; one thread.  at: the block, or
+// A page of K (v false) or V into shared memory; one thread.  at: the block, or
 // (contiguous cache) the page of the sequence.
 template <int D, int KVT>
-__device__ __forceinline__ void load_page(const Params& p, const CUtensorMap* tmK, const CUtensorMap* tmV, int s,
-                                          int kvh, int at, uint32_t dst, uint32_t bar, uint64_t pol) {
+__device__ __forceinline__ void load_half(const Params& p, const CUtensorMap* map, bool v, int s, int kvh, int at,
+                                          uint32_t dst, uint32_t bar, uint64_t pol) {
   using C = PageCfg<D, KVT>;
-  mbar_arrive_expect_tx(bar, 2 * C::TILE);
   if (C::kQ8) {
     const long long row = p.page_size == 0 ? ((long long)s * p.KVH + kvh) * p.capacity + (long long)at * kPage
                                            : ((long long)at * p.KVH + kvh) * kPage;
-    bulk_g2s(dst, (const unsigned char*)p.k + row * C::RB, C::TILE, bar, pol);
-    bulk_g2s(dst + C::TILE_S, (const unsigned char*)p.v + row * C::RB, C::TILE, bar, pol);
+    bulk_g2s(dst, (const unsigned char*)(v ? p.v : p.k) + row * C::RB, C::TILE, bar, pol);
   } else {
-#pragma unroll
-    for (int db = 0; db < D / 64; ++db) {
-      const uint32_t off = db * kPage * 128;
-      if (p.page_size == 0) {
-        tma_load_3d(dst + off, tmK, db * 64, at * kPage, s * p.KVH + kvh, bar, pol);
-        tma_load_3d(dst + C::TILE_S + off, tmV, db * 64, at * kPage, s * p.KVH + kvh, bar, pol);
-      } else {
-        tma_load_4d(dst + off, tmK, db * 64, 0, kvh, at, bar, pol);
-        tma_load_4d(dst + C::TILE_S + off, tmV, db * 64, 0, kvh, at, bar, pol);
-      }
-    }
+    if (p.page_size == 0) tma_load_4d(dst, map, 0, at * kPage, 0, s * p.KVH + kvh, bar, pol);
+    else tma_load_5d(dst, map, 0, 0, 0, kvh, at, bar, pol);
   }
 }
 

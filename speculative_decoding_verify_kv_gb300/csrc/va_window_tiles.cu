@@ -113,8 +113,12 @@ __global__ void __launch_bounds__((TileCfg<D, RT, PG>::THREADS), 1)
         // overwritten with NaN at the end.
         if (at < 0)
           mbar_arrive(smem_u32(&full[st]));
-        else
-          load_page<D, VA_BF16>(p, &tmK, &tmV, s, kvh, at, smem_u32(ring + st * C::STAGE), smem_u32(&full[st]), pol);
+        else {
+          const uint32_t dst = smem_u32(ring + st * C::STAGE), bar = smem_u32(&full[st]);
+          mbar_arrive_expect_tx(bar, 2 * C::TILE);
+          load_half<D, VA_BF16>(p, &tmK, false, s, kvh, at, dst, bar, pol);
+          load_half<D, VA_BF16>(p, &tmV, true, s, kvh, at, dst + C::TILE_S, bar, pol);
+        }
       }
       issued = i + 1;
     }
@@ -149,7 +153,10 @@ __global__ void __launch_bounds__((TileCfg<D, RT, PG>::THREADS), 1)
         // the same zeros.
         if (tail < kPage || (u0 < ws.dead_hi && u0 + kPage > ws.dead_lo))
           clear_unseen<D, VA_BF16>(vs, u0, tail, ws.dead_lo, ws.dead_hi);
-        rows.page(p, kind, vctx, shi, edge, u0, ks, vs);
+        typename RowTile<D, VA_BF16>::Page pg;
+        rows.scores(pg, ks);
+        rows.softmax(pg, p, kind, vctx, shi, edge, u0);
+        rows.values(pg, p, vs);
         __syncwarp();
       }
       if (lane == 0) mbar_arrive(smem_u32(&empty[st]));
