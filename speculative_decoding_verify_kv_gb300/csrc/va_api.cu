@@ -22,9 +22,9 @@ int simt_smem_bytes(int D);
 cudaError_t launch_umma_partial(const Params& p, dim3 grid, cudaStream_t st);
 int umma_smem_bytes(int D, int kv_dtype);
 int umma_threads(int D, int kv_dtype);
-cudaError_t launch_umma_window(const Params& p, dim3 grid, cudaStream_t st);
-cudaError_t launch_window_rows(const Params& p, cudaStream_t st);
-cudaError_t launch_window_tiles(const Params& p, cudaStream_t st);
+cudaError_t launch_umma_window(Params& p, dim3 grid, cudaStream_t st);
+cudaError_t launch_window_rows(Params& p, cudaStream_t st);
+cudaError_t launch_window_tiles(Params& p, cudaStream_t st);
 int window_tiles_rows(int D);
 cudaError_t launch_tq8_partial(const Params& p, dim3 grid, cudaStream_t st);
 int tq8_rows_per_block();
@@ -51,7 +51,6 @@ constexpr int kUmmaRowsPerBlock = 128;
 constexpr int kMinSubTokens = 128;
 constexpr int kMaxSubSplits = 16;
 constexpr int kMaxExactTokens = 2048;  // of a chunk, see window_plan
-constexpr int kJoinedChunks = 8;       // that the kernels for few rows join themselves
 
 static int sm_count() {
   int dev = 0;
@@ -573,7 +572,7 @@ va_status verify_attn_window(const va_problem* p, const va_kv* kv, int32_t mode,
                   : pl.kernel == VA_KERNEL_TENSOR ? launch_umma_window(q, pl.grid, cs)
                                                   : launch_simt_partial(q, pl.grid, cs);
   if (e != cudaSuccess) return note_cuda(e);
-  if (pl.small && pl.slots <= kJoinedChunks) return VA_OK;  // these write the outputs themselves
+  if (q.joined) return VA_OK;  // the kernel joined the chunks: the outputs are written
   e = launch_window_merge(q, cs);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }

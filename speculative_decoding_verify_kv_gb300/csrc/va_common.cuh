@@ -49,6 +49,7 @@ struct Params {
   unsigned* status;
   int window, sinks;      // windowed calls: positions a row sees, first positions that stay (window 0: none)
   int o_bf16;             // o holds bf16
+  int joined;             // a sequence's chunks are one cluster and joined in the partial kernel
   int rows_per_block;     // query rows (j, g pairs) one partial CTA owns
   int row_blocks;         // ceil(max_rows * G / rows_per_block)
 };

@@ -15,6 +15,7 @@
 #include <string.h>
 
 #include "va_common.cuh"
+#include "va_window_join.cuh"
 
 namespace va {
 
@@ -165,9 +166,8 @@ static cudaError_t launch_merge_t(const Params& p, cudaStream_t st, long long it
 
 // Merge of a windowed call: few chunks (one to about sixteen) of many rows,
 // so one warp per (row, head), eight to a CTA, and no barrier; the chunks'
-// loads of a lane's columns are in flight together, four at a time.  Same
-// sums in the same order as above with one slot group.  O may be bf16,
-// rounded once here.  (A CTA per (row, head) took 18.7 us for 96 rows x 24
+// loads of a lane's columns are in flight together, four at a time.  O may be
+// bf16, rounded once here.  (A CTA per (row, head) took 18.7 us for 96 rows x 24
 // heads of D = 256 in 6 chunks, 5 waves of CTAs that each wait for the row's
 // sequence.)
 template <int D>
@@ -195,7 +195,19 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Param
     split_range(win_span(p, sctx, sn).len, 1, 0, &lo0, &hi0);
     live = max(1, live_subs(lo0, hi0, seq_subs(p, sn), p.min_sub));
   }
-  float M = -INFINITY, l = 0.f;
+  // M over the live chunks, then l and O with the weights 2^(m - M), in chunk
+  // order: the sums of join_chunks.
+  float M = -INFINITY;
+  for (int k = lane; k < live && !nan; k += 32) {
+    const long long si = slot_index(p, k, grow, h);
+    const float mk = p.ws_ml[2 * si], lk = p.ws_ml[2 * si + 1];
+    if (isnan(mk) || isnan(lk)) nan = true;
+    if (lk > 0.f) M = fmaxf(M, mk);
+  }
+  nan = __any_sync(0xffffffffu, nan);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float l = 0.f;
   float4 acc[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -218,28 +230,11 @@ __global__ void __launch_bounds__(kMergeThreads) window_merge_kernel(const Param
         aa[k][c] = in && mine ? *reinterpret_cast<const float4*>(p.ws_acc + si * D + 4 * (lane + 32 * c))
                               : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    float bm = M;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (isnan(mm[k]) || isnan(ll[k])) nan = true;
-      if (ll[k] > 0.f) bm = fmaxf(bm, mm[k]);
-    }
-    if (bm > M) {
-      const float f = exp2f(M - bm);  // 0 while nothing was live
-      l *= f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        acc[c].x *= f;
-        acc[c].y *= f;
-        acc[c].z *= f;
-        acc[c].w *= f;
-      }
-      M = bm;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (!(ll[k] > 0.f)) continue;  // an empty chunk: its acc is never read as data
-      const float w = exp2f(mm[k] - M);
+      // An empty chunk, or one too small to weigh: its acc is not read as data.
+      const float w = ll[k] > 0.f ? ex2f(mm[k] - M) : 0.f;
+      if (!(w > 0.f)) continue;
       l = fmaf(w, ll[k], l);
 #pragma unroll
       for (int c = 0; c < NC; ++c) {

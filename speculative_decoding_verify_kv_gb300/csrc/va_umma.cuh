@@ -63,8 +63,11 @@
 #include <limits.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "va_common.cuh"
 #include "va_sm100.cuh"
+#include "va_window_join.cuh"
 
 namespace va {
 using namespace sm100;
@@ -411,6 +414,7 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
   __shared__ float red_max[2][2][kM];
   __shared__ float red_q[2][kM];
   __shared__ float red_l[kM];
+  __shared__ float join_m[WIN ? kM : 1], join_l[WIN ? kM : 1];
 
   // The merge kernel may launch now; it waits for this grid to finish.
   asm volatile("griddepcontrol.launch_dependents;");
@@ -425,6 +429,7 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
   unsigned err = check_sequence(p, s, &row0, &n, &ctx);
   if (err & VA_DEV_BAD_ROWS) {
     if (tid == 0) flag(p.status, err);
+    if (WIN && p.joined && blockIdx.x == 0) nan_rows<D>(p, s, kvh);
     return;
   }
   // Row block and chunk (one level of chunks: split 0, slot = chunk).
@@ -453,7 +458,24 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
     shi = max(shi, slo);
   }
   const int ntiles = (shi - slo + kNT - 1) / kNT;
+  // Joined chunks (WIN): every CTA of the cluster ends in join_chunks.
+  const bool joined = WIN && p.joined;
+  constexpr int kORow = D * 4 + 16;
+  unsigned char* sm = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  auto join_without = [&](float m, float l) {  // no rows of O: an empty or failed chunk
+    if (tid < kM) {
+      join_m[WIN ? tid : 0] = m;
+      join_l[WIN ? tid : 0] = l;
+    }
+    __syncthreads();
+    join_chunks<D>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l);
+  };
   if (ntiles == 0 && !err) {
+    if (joined) {
+      join_without(-INFINITY, 0.f);
+      return;
+    }
     // An empty chunk (short span): its rows' slots become (-inf, 0) at once,
     // without the prologue.  The sequence's other CTAs check its parents.
     if (tid < kM) {
@@ -482,8 +504,6 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
   // scratch KV to the CUDA-core kernel.)
   const bool scratch = PAGED && uses_scratch(p, kind);
 
-  unsigned char* sm = reinterpret_cast<unsigned char*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   // Shared-memory regions.
@@ -672,6 +692,10 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
       mbar_wait(bar(Q8 ? B_QFULL + 3 : B_VFULL), 0, never, kWaitNs);
     }
     if (err && tid == 0) flag(p.status, err);
+    if (joined) {
+      join_without(err ? NAN : -INFINITY, err ? NAN : 0.f);
+      return;
+    }
     if (rvalid) {
       p.ws_ml[2 * si] = err ? NAN : -INFINITY;
       p.ws_ml[2 * si + 1] = err ? NAN : 0.f;
@@ -1102,13 +1126,17 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
     named_barrier_sync(5 + quad, 64);  // the row's two halves
     const bool bad = __any_sync(0xffffffffu, *abort_p != 0);
     if (rvalid && half == 0) {
-      p.ws_ml[2 * si] = bad ? NAN : m_use;
-      p.ws_ml[2 * si + 1] = bad ? NAN : l_run + red_l[r];
+      if (joined) {
+        join_m[WIN ? r : 0] = bad ? NAN : m_use;
+        join_l[WIN ? r : 0] = bad ? NAN : l_run + red_l[r];
+      } else {
+        p.ws_ml[2 * si] = bad ? NAN : m_use;
+        p.ws_ml[2 * si + 1] = bad ? NAN : l_run + red_l[r];
+      }
     }
     // O rows go through shared memory (the tile buffers are idle now; rows
     // padded by 16 bytes so a warp's stores hit distinct bank groups) and
     // leave row by row with coalesced warp-wide stores.
-    constexpr int kORow = D * 4 + 16;
     if (!bad && warp_live) {
 #pragma unroll 1
       for (int c0 = half * (D / 2); c0 < (half + 1) * (D / 2); c0 += 32) {
@@ -1124,7 +1152,7 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
       }
     }
     named_barrier_sync(1, 256);
-    if (!bad) {
+    if (!bad && !joined) {
       // Warp w copies rows w - 2, w + 6, ... (eight warps share the rows),
       // each row with whole-warp 16-byte stores (coalesced 512-byte runs).
       const int nrows_blk = min(kM, R - rb * kM);
@@ -1287,6 +1315,7 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tm, C::TMEM_COLS);
+  if (joined) join_chunks<D>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l);
 }
 
 // ---------------------------------------------------------------------------
@@ -1341,7 +1370,7 @@ static bool make_map(CUtensorMap* map, const Params& p, const void* base, bool b
 }
 
 template <int D, int KVT, bool PAGED, bool WIN>
-static cudaError_t launch_umma_t(const Params& p, dim3 grid, cudaStream_t st) {
+static cudaError_t launch_umma_t(std::conditional_t<WIN, Params&, const Params&> p, dim3 grid, cudaStream_t st) {
   using C = UCfg<D, KVT>;
   static bool attr_done = false;
   if (!attr_done) {
@@ -1355,6 +1384,12 @@ static cudaError_t launch_umma_t(const Params& p, dim3 grid, cudaStream_t st) {
   memset(&mv, 0, sizeof(mv));
   if (!C::kQ8) {
     if (!make_map(&mk, p, p.k, WIN) || !make_map(&mv, p, p.v, WIN)) return cudaErrorInvalidValue;
+  }
+  if constexpr (WIN) p.joined = chunks_join<umma_partial_kernel<D, KVT, PAGED, WIN>>(p, C::THREADS, C::SMEM, st);
+  if (WIN && p.joined) {
+    WindowLaunch l(p, C::THREADS, C::SMEM, st);
+    cudaError_t e = cudaLaunchKernelEx(&l.cfg, umma_partial_kernel<D, KVT, PAGED, WIN>, p, mk, mv);
+    return e != cudaSuccess ? e : cudaGetLastError();
   }
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));

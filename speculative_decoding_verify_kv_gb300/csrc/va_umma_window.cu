@@ -35,7 +35,7 @@ bool make_page_maps(const Params& p, CUtensorMap* k, CUtensorMap* v) {
   return make_page_map(k, p, p.k) && make_page_map(v, p, p.v);
 }
 
-cudaError_t launch_umma_window(const Params& p, dim3 grid, cudaStream_t st) {
+cudaError_t launch_umma_window(Params& p, dim3 grid, cudaStream_t st) {
 #define VA_U_WIN(DD)                                                                             \
   if (p.D == DD)                                                                                 \
     return p.kv_dtype == VA_BF16 ? launch_umma_t<DD, VA_BF16, true, true>(p, grid, st)           \

@@ -1,0 +1,159 @@
+// Where the rows of a windowed call go: joining the chunks of a sequence and KV
+// head in one cluster, and writing rows out.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <string.h>
+
+#include <atomic>
+
+#include "va_common.cuh"
+
+namespace va {
+namespace cg = cooperative_groups;
+
+// Chunks that may be joined in their kernel, as one cluster (the portable
+// size); otherwise they go through the workspace and the merge kernel.  Both
+// take the same sums in the same order, so that either gives the same bits.
+constexpr int kJoinChunks = 8;
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  uint32_t u;
+  memcpy(&u, &h, 4);
+  return u;
+}
+
+// Rows of a sequence whose row range is inconsistent come out NaN (called
+// where no merge kernel follows).
+template <int D>
+__device__ __forceinline__ void nan_rows(const Params& p, int s, int kvh) {
+  const int a = max(p.cu_rows[s], 0), b = min(p.cu_rows[s + 1], p.total_rows);
+  for (long long i = (long long)a * p.H * D + threadIdx.x; i < (long long)b * p.H * D; i += blockDim.x)
+    if (i / D % p.H / p.G == kvh) {
+      if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[i] = __float2bfloat16(NAN);
+      else p.o[i] = NAN;
+      if (i % D == 0) p.lse[i / D] = NAN;
+    }
+}
+
+// Where a row's result goes: with one chunk the outputs, and else the chunk's
+// partial for the merge kernel.
+template <int D>
+__device__ __forceinline__ void put_pair(const Params& p, bool partial, int slot, int grow, int head, int c, float x,
+                                         float y) {
+  const long long item = (long long)grow * p.H + head;
+  if (partial)
+    *reinterpret_cast<float2*>(p.ws_acc + slot_index(p, slot, grow, head) * D + c) = make_float2(x, y);
+  else if (p.o_bf16)
+    reinterpret_cast<uint32_t*>(p.o)[(item * D + c) / 2] = pack_bf16(x, y);
+  else
+    *reinterpret_cast<float2*>(p.o + item * D + c) = make_float2(x, y);
+}
+
+// Join the chunks of a cluster, in chunk order, each CTA for its share of the
+// rows, through distributed shared memory: row r of this CTA's chunk has its
+// unnormalised O at os + r ld and its m and l (in base 2) at ms[r] and ls[r].  A
+// chunk without a visible token has l = 0 and weighs nothing (its O is not
+// read as data), a failed one is NaN.  Every thread of every CTA of the
+// cluster.
+template <int D>
+__device__ __forceinline__ void join_chunks(const Params& p, int slot, int row0, int kvh, int R, float* os, int ld,
+                                            float* ms, float* ls) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int r = warp * p.slots + slot; r < R; r += warps * p.slots) {
+    // Lane k holds chunk k's m and l.
+    const bool in = lane < p.slots;
+    const float mk = in ? *cluster.map_shared_rank(ms + r, lane) : -INFINITY;
+    const float lk = in ? *cluster.map_shared_rank(ls + r, lane) : 0.f;
+    float mr = lk > 0.f ? mk : -INFINITY;
+#pragma unroll
+    for (int o = kJoinChunks / 2; o > 0; o >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+    mr = __shfl_sync(0xffffffffu, mr, 0);
+    const bool bad = __any_sync(0xffffffffu, lk != lk);
+    const float fk = lk > 0.f ? ex2f(mk - mr) : 0.f;
+    float lr = 0.f;
+    for (int k = 0; k < p.slots; ++k)
+      lr = fmaf(__shfl_sync(0xffffffffu, fk, k), __shfl_sync(0xffffffffu, lk, k), lr);
+    const float inv = bad ? NAN : 1.f / lr;
+    const int grow = row0 + r / p.G, head = kvh * p.G + r % p.G;
+    for (int c = 2 * lane; c < D; c += 64) {
+      float x = 0.f, y = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < p.slots; ++k) {
+        const float w = __shfl_sync(0xffffffffu, fk, k);
+        if (!(w > 0.f)) continue;
+        const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(os + (long long)r * ld + c, k));
+        x = fmaf(w, v.x, x);
+        y = fmaf(w, v.y, y);
+      }
+      put_pair<D>(p, false, slot, grow, head, c, x * inv, y * inv);
+    }
+    if (lane == 0) p.lse[(long long)grow * p.H + head] = bad ? NAN : (mr + log2f(lr)) * kLn2;
+  }
+  cluster.sync();  // no CTA leaves while its rows are read
+}
+
+// Launch configuration of these kernels: a programmatic dependent, a sequence
+// and KV head's chunks one cluster where they are joined in the kernel.
+struct WindowLaunch {
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  WindowLaunch(const Params& p, int threads, size_t smem, cudaStream_t st) {
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3((unsigned)p.slots, (unsigned)p.KVH, (unsigned)p.num_seqs);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.slots;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.slots > 1 && p.joined ? 2 : 1;
+  }
+};
+
+// Whether a launch's chunks are joined in the kernel: where a cluster holds
+// them all and the clusters need no more rounds on the GPU than the CTAs by
+// themselves would (a GPC takes whole clusters only: 24 clusters of 6 CTAs
+// that fill an SM each took 74 us in two rounds, 41 us apart).
+template <auto KERNEL>
+static bool chunks_join(Params p, int threads, size_t smem, cudaStream_t st) {
+  // (join_chunks takes the rows of one row block.)
+  if (p.slots > kJoinChunks || p.row_blocks > 1) return false;
+  if (p.slots == 1) return true;
+  constexpr int kDevs = 64;
+  static std::atomic<int> clusters[kDevs][kJoinChunks + 1], ctas[kDevs];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return false;
+  int n = clusters[dev][p.slots].load(std::memory_order_relaxed);
+  int c = ctas[dev].load(std::memory_order_relaxed);
+  if (n == 0 || c == 0) {
+    p.joined = 1;
+    WindowLaunch l(p, threads, smem, st);
+    int per = 0, sms = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &l.cfg) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, KERNEL, threads, smem) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1 || per < 1) {
+      cudaGetLastError();
+      return false;
+    }
+    c = per * sms;
+    clusters[dev][p.slots].store(n, std::memory_order_relaxed);
+    ctas[dev].store(c, std::memory_order_relaxed);
+  }
+  const long long jobs = (long long)p.num_seqs * p.KVH;
+  return (jobs + n - 1) / n <= (jobs * p.slots + c - 1) / c;
+}
+
+}  // namespace va

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, co
   unsigned err = check_sequence(p, s, &row0, &n, &ctx);
   if (err & VA_DEV_BAD_ROWS) {
     if (tid == 0) flag(p.status, err);
-    if (p.slots <= kJoinChunks && slot == 0) nan_rows<D>(p, s, kvh);
+    if (p.joined && slot == 0) nan_rows<D>(p, s, kvh);
     return;
   }
   const int R = n * p.G;
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, co
 }
 
 template <int D, int KVT, int NW>
-static cudaError_t launch_few_t(const Params& p, cudaStream_t st) {
+static cudaError_t launch_few_t(Params& p, cudaStream_t st) {
   using C = FewCfg<D, KVT, NW>;
   static_assert(C::NST >= 2 && C::NST <= 6, "ring depth");
   static std::atomic<unsigned long long> ready{0ull};  // devices whose attribute is set
@@ -168,6 +168,7 @@ static cudaError_t launch_few_t(const Params& p, cudaStream_t st) {
   memset(&mk, 0, sizeof(mk));
   memset(&mv, 0, sizeof(mv));
   if (!C::kQ8 && !make_page_maps(p, &mk, &mv)) return cudaErrorInvalidValue;
+  p.joined = chunks_join<window_rows_kernel<D, KVT, NW>>(p, NW * 32, C::SMEM, st);
   WindowLaunch l(p, NW * 32, C::SMEM, st);
   e = cudaLaunchKernelEx(&l.cfg, window_rows_kernel<D, KVT, NW>, p, mk, mv);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -175,7 +176,7 @@ static cudaError_t launch_few_t(const Params& p, cudaStream_t st) {
 
 // One chunk per sequence means that the sequences fill the GPU: small CTAs,
 // four to an SM.  Several chunks: few sequences, the more warps to each.
-cudaError_t launch_window_rows(const Params& p, cudaStream_t st) {
+cudaError_t launch_window_rows(Params& p, cudaStream_t st) {
 #define VA_FEW(DD)                                                                                          \
   if (p.D == DD) {                                                                                          \
     if (p.kv_dtype == VA_BF16)                                                                              \

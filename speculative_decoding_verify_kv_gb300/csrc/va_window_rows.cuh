@@ -15,15 +15,14 @@
 // block, V's elements become fp16(d q) (one rounding) and P is fp16.
 #pragma once
 
-#include <cooperative_groups.h>
 #include <string.h>
 
 #include "va_common.cuh"
 #include "va_sm100.cuh"
+#include "va_window_join.cuh"
 
 namespace va {
 using namespace sm100;
-namespace cg = cooperative_groups;
 
 constexpr int kTileRows = 16;  // query rows of one warp
 constexpr uint64_t kPageWaitNs = 2000000000ull;
@@ -64,19 +63,6 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr));
-}
-
-__device__ __forceinline__ float ex2f(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  uint32_t u;
-  memcpy(&u, &h, 4);
-  return u;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
@@ -504,46 +490,15 @@ __device__ __forceinline__ int page_place(const Params& p, const WinSpan& ws, in
   return blk < 0 || blk >= p.num_blocks ? -1 : blk;
 }
 
-// Rows of a sequence whose row range is inconsistent come out NaN (called
-// where no merge kernel follows).
-template <int D>
-__device__ __forceinline__ void nan_rows(const Params& p, int s, int kvh) {
-  const int a = max(p.cu_rows[s], 0), b = min(p.cu_rows[s + 1], p.total_rows);
-  for (long long i = (long long)a * p.H * D + threadIdx.x; i < (long long)b * p.H * D; i += blockDim.x)
-    if (i / D % p.H / p.G == kvh) {
-      if (p.o_bf16) reinterpret_cast<__nv_bfloat16*>(p.o)[i] = __float2bfloat16(NAN);
-      else p.o[i] = NAN;
-      if (i % D == 0) p.lse[i / D] = NAN;
-    }
-}
-
-// Where a row's result goes: with one chunk the outputs, and else the chunk's
-// partial for the merge kernel.
-template <int D>
-__device__ __forceinline__ void put_pair(const Params& p, bool partial, int slot, int grow, int head, int c, float x,
-                                         float y) {
-  const long long item = (long long)grow * p.H + head;
-  if (partial)
-    *reinterpret_cast<float2*>(p.ws_acc + slot_index(p, slot, grow, head) * D + c) = make_float2(x, y);
-  else if (p.o_bf16)
-    reinterpret_cast<uint32_t*>(p.o)[(item * D + c) / 2] = pack_bf16(x, y);
-  else
-    *reinterpret_cast<float2*>(p.o + item * D + c) = make_float2(x, y);
-}
-
 // Join the states of each row's NG page groups, in order, and write the rows
 // out.  State (group x, row tile y) lies at index x RT + y.  Every warp of the
-// CTA.  With several chunks in one cluster (at most kJoinChunks) the chunks'
-// states are joined here too, in chunk order, each CTA for its share of the
-// rows, through distributed shared memory; with more, each chunk's partial
-// goes to the workspace.
-constexpr int kJoinChunks = 8;
-
+// CTA.  At most kJoinChunks chunks are joined in their cluster, with more each
+// chunk's partial goes to the workspace.
 template <int D, int NG, int RT>
 __device__ __forceinline__ void join_rows(const Params& p, int slot, int row0, int kvh, int R, bool fail, float* os,
                                           int ld, float (*ms)[kTileRows], float (*ls)[kTileRows]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const bool one = p.slots == 1, partial = p.slots > kJoinChunks;
+  const bool one = p.slots == 1, partial = !p.joined;
   for (int r = warp; r < R; r += warps) {
     const int tile = r / kTileRows, rt = r % kTileRows;
     float mr = -INFINITY;
@@ -586,62 +541,8 @@ __device__ __forceinline__ void join_rows(const Params& p, int slot, int row0, i
     }
   }
   if (one || partial) return;
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
-  for (int r = warp * p.slots + slot; r < R; r += warps * p.slots) {
-    const int tile = r / kTileRows, rt = r % kTileRows;
-    // Lane k holds chunk k's m and l; a chunk without a visible token has l
-    // = 0 and weighs nothing, a failed one is NaN.
-    const bool in = lane < p.slots;
-    const float mk = in ? *cluster.map_shared_rank(&ms[tile][rt], lane) : -INFINITY;
-    const float lk = in ? *cluster.map_shared_rank(&ls[tile][rt], lane) : 0.f;
-    float mr = mk;
-#pragma unroll
-    for (int o = kJoinChunks / 2; o > 0; o >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
-    mr = __shfl_sync(0xffffffffu, mr, 0);
-    const bool bad = __any_sync(0xffffffffu, lk != lk);
-    const float fk = lk > 0.f ? ex2f(mk - mr) : 0.f;
-    float lr = 0.f;
-    for (int k = 0; k < p.slots; ++k) lr += __shfl_sync(0xffffffffu, fk * lk, k);
-    const float inv = bad ? NAN : 1.f / lr;
-    const int grow = row0 + r / p.G, head = kvh * p.G + r % p.G;
-    for (int c = 2 * lane; c < D; c += 64) {
-      float x = 0.f, y = 0.f;
-      float* at = os + (tile * kTileRows + rt) * ld + c;
-#pragma unroll 4
-      for (int k = 0; k < p.slots; ++k) {
-        const float w = __shfl_sync(0xffffffffu, fk, k);
-        const float2 v = *reinterpret_cast<const float2*>(cluster.map_shared_rank(at, k));
-        x = fmaf(w, v.x, x);
-        y = fmaf(w, v.y, y);
-      }
-      put_pair<D>(p, false, slot, grow, head, c, x * inv, y * inv);
-    }
-    if (lane == 0) p.lse[(long long)grow * p.H + head] = bad ? NAN : (mr + log2f(lr)) * kLn2;
-  }
-  cluster.sync();  // no CTA leaves while its rows are read
+  join_chunks<D>(p, slot, row0, kvh, R, os, ld, &ms[0][0], &ls[0][0]);
 }
-
-// Launch configuration of these kernels: a programmatic dependent, a sequence
-// and KV head's chunks one cluster where they are joined in the kernel.
-struct WindowLaunch {
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[2];
-  WindowLaunch(const Params& p, int threads, size_t smem, cudaStream_t st) {
-    memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = dim3((unsigned)p.slots, (unsigned)p.KVH, (unsigned)p.num_seqs);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.slots;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.slots > 1 && p.slots <= kJoinChunks ? 2 : 1;
-  }
-};
 
 bool make_page_maps(const Params& p, CUtensorMap* k, CUtensorMap* v);
 

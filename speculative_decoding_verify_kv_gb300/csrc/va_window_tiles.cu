@@ -55,7 +55,7 @@ __global__ void __launch_bounds__((TileCfg<D, RT, PG>::THREADS), 1)
   unsigned err = check_sequence(p, s, &row0, &n, &ctx);
   if (err & VA_DEV_BAD_ROWS) {
     if (tid == 0) flag(p.status, err);
-    if (p.slots <= kJoinChunks && slot == 0) nan_rows<D>(p, s, kvh);
+    if (p.joined && slot == 0) nan_rows<D>(p, s, kvh);
     return;
   }
   const int R = n * p.G;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__((TileCfg<D, RT, PG>::THREADS), 1)
 }
 
 template <int D, int RT, int PG>
-static cudaError_t launch_tiles_t(const Params& p, cudaStream_t st) {
+static cudaError_t launch_tiles_t(Params& p, cudaStream_t st) {
   using C = TileCfg<D, RT, PG>;
   static_assert(C::NST >= PG && C::SMEM <= 227 * 1024, "ring");
   static std::atomic<unsigned long long> ready{0ull};  // devices whose attribute is set
@@ -186,6 +186,7 @@ static cudaError_t launch_tiles_t(const Params& p, cudaStream_t st) {
   }
   CUtensorMap mk, mv;
   if (!make_page_maps(p, &mk, &mv)) return cudaErrorInvalidValue;
+  p.joined = chunks_join<window_tiles_kernel<D, RT, PG>>(p, C::THREADS, C::SMEM, st);
   WindowLaunch l(p, C::THREADS, C::SMEM, st);
   e = cudaLaunchKernelEx(&l.cfg, window_tiles_kernel<D, RT, PG>, p, mk, mv);
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -194,7 +195,7 @@ static cudaError_t launch_tiles_t(const Params& p, cudaStream_t st) {
 // Most rows per KV head that the row tiles take (see above).
 int window_tiles_rows(int D) { return D == 64 ? 48 : D == 128 ? 32 : 0; }
 
-cudaError_t launch_window_tiles(const Params& p, cudaStream_t st) {
+cudaError_t launch_window_tiles(Params& p, cudaStream_t st) {
   const int tiles = (p.max_rows * p.G + kTileRows - 1) / kTileRows;
   if (p.D == 64) return tiles <= 2 ? launch_tiles_t<64, 2, 6>(p, st) : launch_tiles_t<64, 3, 4>(p, st);
   if (p.D == 128) return launch_tiles_t<128, 2, 4>(p, st);

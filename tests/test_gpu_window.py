@@ -123,6 +123,21 @@ def test_a_sequence_does_not_depend_on_the_launch():
 FEW = [(kv, h, k, d) for kv in ("bf16", "q8_0") for h, k, d in ((8, 1, 64), (8, 2, 128), (3, 3, 128), (5, 1, 256))]
 
 
+@pytest.mark.parametrize("kv,heads,kvh,dim,rows", [("bf16", 8, 2, 64, 1), ("bf16", 8, 2, 128, 7), ("q8_0", 6, 1, 256, 2),
+                                                   ("q8_0", 6, 1, 256, 16), ("bf16", 6, 1, 256, 16)])
+@pytest.mark.parametrize("splits", [2, 5, 8])
+def test_many_sequences_and_one_give_the_same_bits(kv, heads, kvh, dim, rows, splits):
+    """Few clusters are joined in their kernel, many go through the merge
+    kernel: a sequence's bits are the same."""
+    one = make(kv, heads, kvh, dim, [2300], [rows], paged=True, seed=splits)
+    many = dataclasses.replace(one, ctx_len=np.repeat(one.ctx_len, 120), block_table=np.repeat(one.block_table, 120, 0),
+                               cu_rows=np.arange(121, dtype=np.int32) * rows, parent=np.tile(one.parent, 120),
+                               seq_kind=np.repeat(one.seq_kind, 120), q=np.tile(one.q, (120, 1, 1)))
+    a, b = run(one, 2000, 4, splits=splits), run(many, 2000, 4, splits=splits)
+    for x, y in zip(a, b):
+        assert np.array_equal(np.tile(x, (120,) + (1,) * (x.ndim - 1)), y)
+
+
 @pytest.mark.parametrize("kv,heads,kvh,dim", FEW)
 @pytest.mark.parametrize("paged", [False, True])
 @pytest.mark.parametrize("window,sinks,splits", [(1, 0, 1), (17, 4, 1), (40, 33, 2), (700, 0, 1), (700, 20, 3),
