@@ -543,7 +543,9 @@ int32_t va_window_splits(const va_problem* p, const va_kv* kv, const va_window* 
     return 0;
   const long long jobs = (long long)p->num_seqs * kv->num_kv_heads;
   const long long tokens = (long long)w->window + w->sinks + p->max_rows_per_seq;
-  long long n = sm_count() / jobs;
+  // (two CTAs to an SM where a sequence has few rows)
+  const int per = window_plan(p, kv, w).small == 1 ? 2 : 1;
+  long long n = per * sm_count() / jobs;
   if (n > (tokens + 255) / 256) n = (tokens + 255) / 256;
   if (n > kMaxSubSplits) n = kMaxSubSplits;
   return (int32_t)(n < 1 ? 1 : n);

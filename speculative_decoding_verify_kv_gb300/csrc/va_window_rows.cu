@@ -11,7 +11,7 @@
 // until the end, when the warps' states are joined.  The products are warp
 // MMAs of 16 x 8 x 16 with Q and the accumulator in registers (tcgen05 would
 // need 128 rows and a round trip through tensor memory per tile).  64
-// sequences of 4,100 visible tokens, H32/KV8/D128 bf16: 166 us, 6.5 TB/s (the
+// sequences of 4,100 visible tokens, H32/KV8/D128 bf16: 157 us, 6.8 TB/s (the
 // 128-row kernel: 345).
 #include <atomic>
 
@@ -22,9 +22,11 @@ namespace va {
 template <int D, int KVT, int NW>
 struct FewCfg : PageCfg<D, KVT> {
   using C = PageCfg<D, KVT>;
-  // Ring depth: as many stages as leave the CTA its share of an SM (2 warps:
-  // a quarter, or half where a quarter holds no two stages), at most 6.
-  static constexpr int BUDGET = (NW > 2 ? 216 : 54 * 1024 / (NW * C::STAGE) >= 2 ? 54 : 108) * 1024;
+  // CTAs to an SM, and as many ring stages as their share of its shared
+  // memory holds, at most 6 (with two stages, one in use, too few bytes are in
+  // flight: 257 us against 162 at D = 128).
+  static constexpr int PER_SM = NW == 4 || D == 64 ? 2 : 1;
+  static constexpr int BUDGET = 216 / PER_SM * 1024;
   static constexpr int FIT = BUDGET / (NW * C::STAGE);
   static constexpr int NST = FIT > 6 ? 6 : FIT;
   static constexpr int EPI = NW * kTileRows * (D + 4) * 4;  // the warps' O rows at the end
@@ -32,8 +34,8 @@ struct FewCfg : PageCfg<D, KVT> {
   static constexpr int SMEM = (RING > EPI ? RING : EPI) + 1024;
 };
 
-template <int D, int KVT, int NW>
-__global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
+template <int D, int KVT, int NW, bool EX>
+__global__ void __launch_bounds__(NW * 32, (FewCfg<D, KVT, NW>::PER_SM == 1 ? 0 : 2)) window_rows_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
                                                               const __grid_constant__ CUtensorMap tmV) {
   using C = FewCfg<D, KVT, NW>;
   extern __shared__ unsigned char smem_raw[];
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, co
     if (i < good && at < 0) good = i;
     if (i < good && lane == 0) load(i, at);
   }
-  RowTile<D, KVT> rows;
+  RowTile<D, KVT, EX> rows;
   if (!rows.init(p, ws, row0, ctx, kind, kvh, 0, R, !err)) atomicOr(&err_s, (int)VA_DEV_BAD_PARENT);
   const int edge = win_low(p, ctx + n - 1) - ws.skip;
   volatile int* abort_p = &abort_s;
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, co
     const int tail = min(shi - u0, kPage);         // tokens of the chunk in it
     if (tail < kPage || (u0 < ws.dead_hi && u0 + kPage > ws.dead_lo))
       clear_unseen<D, KVT>(vs, u0, tail, ws.dead_lo, ws.dead_hi);
-    typename RowTile<D, KVT>::Page pg;
+    typename RowTile<D, KVT, EX>::Page pg;
     rows.scores(pg, ks);
     rows.softmax(pg, p, kind, vctx, shi, edge, u0);
     rows.values(pg, p, vs);
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(NW * 32) window_rows_kernel(const Params p, co
   join_rows<D, NW, 1>(p, slot, row0, kvh, R, err || abort_s, os, LD, m_s, l_s);
 }
 
-template <int D, int KVT, int NW>
+template <int D, int KVT, int NW, bool EX>
 static cudaError_t launch_few_t(Params& p, cudaStream_t st) {
   using C = FewCfg<D, KVT, NW>;
   static_assert(C::NST >= 2 && C::NST <= 6, "ring depth");
@@ -160,7 +162,7 @@ static cudaError_t launch_few_t(Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(window_rows_kernel<D, KVT, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(window_rows_kernel<D, KVT, NW, EX>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
@@ -168,22 +170,31 @@ static cudaError_t launch_few_t(Params& p, cudaStream_t st) {
   memset(&mk, 0, sizeof(mk));
   memset(&mv, 0, sizeof(mv));
   if (!C::kQ8 && !make_page_maps(p, &mk, &mv)) return cudaErrorInvalidValue;
-  p.joined = chunks_join<window_rows_kernel<D, KVT, NW>>(p, NW * 32, C::SMEM, st);
+  p.joined = chunks_join<window_rows_kernel<D, KVT, NW, EX>>(p, NW * 32, C::SMEM, st);
   WindowLaunch l(p, NW * 32, C::SMEM, st);
-  e = cudaLaunchKernelEx(&l.cfg, window_rows_kernel<D, KVT, NW>, p, mk, mv);
+  e = cudaLaunchKernelEx(&l.cfg, window_rows_kernel<D, KVT, NW, EX>, p, mk, mv);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// One chunk per sequence means that the sequences fill the GPU: small CTAs,
-// four to an SM.  Several chunks: few sequences, the more warps to each.
+// Warps of a CTA.  D = 64: eight, two CTAs to an SM.  D = 128: with one chunk to
+// a sequence (many sequences) four, two CTAs to an SM, so that one's start and
+// end hide behind the other; with several (few sequences) eight, the whole SM.
+// 64 direct rows of 4,100 tokens in one chunk (H32/KV8, bf16): 157 us with four
+// warps, 172 with eight; 16 of them 66 and 46 (two chunks: 50).  D = 256: what
+// the registers leave.
+template <int D, int KVT, bool EX>
+static cudaError_t launch_few(Params& p, cudaStream_t st) {
+  if constexpr (D == 128)
+    if (p.slots == 1) return launch_few_t<D, KVT, 4, EX>(p, st);
+  return launch_few_t<D, KVT, D == 256 && KVT == VA_BF16 ? 6 : 8, EX>(p, st);
+}
+
 cudaError_t launch_window_rows(Params& p, cudaStream_t st) {
-#define VA_FEW(DD)                                                                                          \
-  if (p.D == DD) {                                                                                          \
-    if (p.kv_dtype == VA_BF16)                                                                              \
-      return p.slots == 1 ? launch_few_t<DD, VA_BF16, 2>(p, st)                                             \
-                          : launch_few_t<DD, VA_BF16, DD == 256 ? 6 : 8>(p, st);                            \
-    if (p.kv_dtype == VA_Q8_0)                                                                              \
-      return p.slots == 1 ? launch_few_t<DD, VA_Q8_0, 2>(p, st) : launch_few_t<DD, VA_Q8_0, 8>(p, st);      \
+#define VA_FEW(DD)                                                                              \
+  if (p.D == DD) {                                                                              \
+    if (p.kv_dtype == VA_BF16)                                                                  \
+      return p.o_bf16 ? launch_few<DD, VA_BF16, false>(p, st) : launch_few<DD, VA_BF16, true>(p, st); \
+    if (p.kv_dtype == VA_Q8_0) return launch_few<DD, VA_Q8_0, false>(p, st);                    \
   }
   VA_FEW(64) VA_FEW(128) VA_FEW(256)
 #undef VA_FEW

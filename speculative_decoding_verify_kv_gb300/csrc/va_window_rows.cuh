@@ -111,8 +111,8 @@ __device__ __forceinline__ void code_words(uint32_t (&x)[N], const unsigned char
 
 // A warp's 16 rows: Q fragments, what masks them, and their softmax state.  In
 // MMA fragments a lane holds rows g = lane / 4 and g + 8 and column pair
-// lane % 4.
-template <int D, int KVT>
+// lane % 4.  EX: O leaves in fp32 (bf16 caches).
+template <int D, int KVT, bool EX>
 struct RowTile {
   static constexpr bool Q8 = KVT == VA_Q8_0;
   static constexpr int KS = D / 16;  // k steps of S
@@ -284,19 +284,27 @@ struct RowTile {
     const bool plain = u0 + kPage <= min(vctx, shi) && (u0 >= edge || u0 + kPage <= p.sinks);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      unsigned vis = 0xFFFFu;
-      if (!plain)
-        vis = rvalid[h] ? visible_bits(kind, anc[h], jrow[h], vctx, shi, u0) & window_bits(kind, p.sinks, wlo[h], vctx, u0)
-                        : 0u;
-      float mx = -INFINITY;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& x = sc[t][2 * h + e];
-          x = (vis >> (8 * t + 2 * q4 + e)) & 1u ? x * c2[h] : -INFINITY;
-          mx = fmaxf(mx, x);
-        }
+        for (int e = 0; e < 2; ++e) sc[t][2 * h + e] *= c2[h];
+    }
+    if (!plain) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const unsigned vis =
+            rvalid[h] ? visible_bits(kind, anc[h], jrow[h], vctx, shi, u0) & window_bits(kind, p.sinks, wlo[h], vctx, u0)
+                      : 0u;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!((vis >> (8 * t + 2 * q4 + e)) & 1u)) sc[t][2 * h + e] = -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float mx = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const float mn = fmaxf(m[h], mx);
@@ -330,7 +338,7 @@ struct RowTile {
           ph[2 * t + h] = w;
           pl[2 * t + h] = wl;
           // What is left (to 24 bits in all) counts where O leaves in fp32.
-          pr[2 * t + h] = pack_bf16(xl - __uint_as_float(wl << 16), yl - __uint_as_float(wl & 0xFFFF0000u));
+          if (EX) pr[2 * t + h] = pack_bf16(xl - __uint_as_float(wl << 16), yl - __uint_as_float(wl & 0xFFFF0000u));
         }
       }
   }
@@ -401,7 +409,7 @@ struct RowTile {
 #pragma unroll
         for (int c = 0; c < 2 * GR; ++c) {
           cc[c][0] = cc[c][1] = cc[c][2] = cc[c][3] = 0.f;
-          if (!p.o_bf16) mma_bf16(cc[c], pr, b[c / 2][2 * (c & 1)], b[c / 2][2 * (c & 1) + 1]);
+          if (EX) mma_bf16(cc[c], pr, b[c / 2][2 * (c & 1)], b[c / 2][2 * (c & 1) + 1]);
         }
 #pragma unroll
         for (int c = 0; c < 2 * GR; ++c) mma_bf16(cc[c], pl, b[c / 2][2 * (c & 1)], b[c / 2][2 * (c & 1) + 1]);

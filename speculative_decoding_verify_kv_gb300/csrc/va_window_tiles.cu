@@ -37,7 +37,7 @@ struct TileCfg : PageCfg<D, VA_BF16> {
   static constexpr int SMEM = (RING > EPI ? RING : EPI) + 1024;
 };
 
-template <int D, int RT, int PG>
+template <int D, int RT, int PG, bool EX>
 __global__ void __launch_bounds__((TileCfg<D, RT, PG>::THREADS), 1)
     window_tiles_kernel(const Params p, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV) {
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__((TileCfg<D, RT, PG>::THREADS), 1)
     // -------------------------------------------------------------- rows
     const int tile = warp % RT, grp = warp / RT;
     const int mine = min(max(R - tile * kTileRows, 0), kTileRows);
-    RowTile<D, VA_BF16> rows;
+    RowTile<D, VA_BF16, EX> rows;
     if (!rows.init(p, ws, row0, ctx, kind, kvh, tile * kTileRows, mine, !err))
       atomicOr(&err_s, (int)VA_DEV_BAD_PARENT);
     const int edge = win_low(p, ctx + n - 1) - ws.skip;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__((TileCfg<D, RT, PG>::THREADS), 1)
         // the same zeros.
         if (tail < kPage || (u0 < ws.dead_hi && u0 + kPage > ws.dead_lo))
           clear_unseen<D, VA_BF16>(vs, u0, tail, ws.dead_lo, ws.dead_hi);
-        typename RowTile<D, VA_BF16>::Page pg;
+        typename RowTile<D, VA_BF16, EX>::Page pg;
         rows.scores(pg, ks);
         rows.softmax(pg, p, kind, vctx, shi, edge, u0);
         rows.values(pg, p, vs);
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__((TileCfg<D, RT, PG>::THREADS), 1)
   join_rows<D, PG, RT>(p, slot, row0, kvh, R, err || abort_s, os, LD, m_s, l_s);
 }
 
-template <int D, int RT, int PG>
+template <int D, int RT, int PG, bool EX>
 static cudaError_t launch_tiles_t(Params& p, cudaStream_t st) {
   using C = TileCfg<D, RT, PG>;
   static_assert(C::NST >= PG && C::SMEM <= 227 * 1024, "ring");
@@ -180,26 +180,31 @@ static cudaError_t launch_tiles_t(Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(window_tiles_kernel<D, RT, PG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(window_tiles_kernel<D, RT, PG, EX>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_release);
   }
   CUtensorMap mk, mv;
   if (!make_page_maps(p, &mk, &mv)) return cudaErrorInvalidValue;
-  p.joined = chunks_join<window_tiles_kernel<D, RT, PG>>(p, C::THREADS, C::SMEM, st);
+  p.joined = chunks_join<window_tiles_kernel<D, RT, PG, EX>>(p, C::THREADS, C::SMEM, st);
   WindowLaunch l(p, C::THREADS, C::SMEM, st);
-  e = cudaLaunchKernelEx(&l.cfg, window_tiles_kernel<D, RT, PG>, p, mk, mv);
+  e = cudaLaunchKernelEx(&l.cfg, window_tiles_kernel<D, RT, PG, EX>, p, mk, mv);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // Most rows per KV head that the row tiles take (see above).
 int window_tiles_rows(int D) { return D == 64 ? 48 : D == 128 ? 32 : 0; }
 
-cudaError_t launch_window_tiles(Params& p, cudaStream_t st) {
+template <bool EX>
+static cudaError_t launch_tiles(Params& p, cudaStream_t st) {
   const int tiles = (p.max_rows * p.G + kTileRows - 1) / kTileRows;
-  if (p.D == 64) return tiles <= 2 ? launch_tiles_t<64, 2, 6>(p, st) : launch_tiles_t<64, 3, 4>(p, st);
-  if (p.D == 128) return launch_tiles_t<128, 2, 4>(p, st);
+  if (p.D == 64) return tiles <= 2 ? launch_tiles_t<64, 2, 6, EX>(p, st) : launch_tiles_t<64, 3, 4, EX>(p, st);
+  if (p.D == 128) return launch_tiles_t<128, 2, 4, EX>(p, st);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_window_tiles(Params& p, cudaStream_t st) {
+  return p.o_bf16 ? launch_tiles<false>(p, st) : launch_tiles<true>(p, st);
 }
 
 }  // namespace va
