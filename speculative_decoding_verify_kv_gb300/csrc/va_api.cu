@@ -490,6 +490,7 @@ static va_status check_window(const va_problem* p, const va_kv* kv, int mode, co
   va_status st = check(p, kv, mode);
   if (st != VA_OK) return st;
   if (!w || w->window < 1 || w->sinks < 0) return VA_ERR_INVALID_ARG;
+  if (p->num_seqs > 65535 || kv->num_kv_heads > 65535) return VA_ERR_UNSUPPORTED;  // grid dimensions
   if (w->o_dtype < VA_F32 || w->o_dtype > VA_Q8_0) return VA_ERR_INVALID_ARG;
   return w->o_dtype == VA_Q8_0 ? VA_ERR_UNSUPPORTED : VA_OK;
 }

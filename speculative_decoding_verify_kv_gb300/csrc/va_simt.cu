@@ -18,6 +18,7 @@
 #include <string.h>
 
 #include "va_common.cuh"
+#include "va_host.h"
 
 namespace va {
 
@@ -286,13 +287,9 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
 template <int D, int KVT, bool WIN>
 static cudaError_t launch_simt_t(const Params& p, dim3 grid, cudaStream_t st) {
   constexpr int smem = SimtCfg<D, WIN>::SMEM;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(simt_partial_kernel<D, KVT, WIN>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static std::atomic<unsigned long long> ready{0ull};
+  cudaError_t allowed = allow_smem(simt_partial_kernel<D, KVT, WIN>, smem, ready);
+  if (allowed != cudaSuccess) return allowed;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;

@@ -66,6 +66,7 @@
 #include <type_traits>
 
 #include "va_common.cuh"
+#include "va_host.h"
 #include "va_sm100.cuh"
 #include "va_window_join.cuh"
 
@@ -1372,13 +1373,9 @@ static bool make_map(CUtensorMap* map, const Params& p, const void* base, bool b
 template <int D, int KVT, bool PAGED, bool WIN>
 static cudaError_t launch_umma_t(std::conditional_t<WIN, Params&, const Params&> p, dim3 grid, cudaStream_t st) {
   using C = UCfg<D, KVT>;
-  static bool attr_done = false;
-  if (!attr_done) {
-    cudaError_t e = cudaFuncSetAttribute(umma_partial_kernel<D, KVT, PAGED, WIN>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_done = true;
-  }
+  static std::atomic<unsigned long long> ready{0ull};
+  cudaError_t allowed = allow_smem(umma_partial_kernel<D, KVT, PAGED, WIN>, C::SMEM, ready);
+  if (allowed != cudaSuccess) return allowed;
   CUtensorMap mk, mv;
   memset(&mk, 0, sizeof(mk));
   memset(&mv, 0, sizeof(mv));

@@ -13,8 +13,7 @@
 // need 128 rows and a round trip through tensor memory per tile).  64
 // sequences of 4,100 visible tokens, H32/KV8/D128 bf16: 157 us, 6.8 TB/s (the
 // 128-row kernel: 345).
-#include <atomic>
-
+#include "va_host.h"
 #include "va_window_rows.cuh"
 
 namespace va {
@@ -156,16 +155,9 @@ template <int D, int KVT, int NW, bool EX>
 static cudaError_t launch_few_t(Params& p, cudaStream_t st) {
   using C = FewCfg<D, KVT, NW>;
   static_assert(C::NST >= 2 && C::NST <= 6, "ring depth");
-  static std::atomic<unsigned long long> ready{0ull};  // devices whose attribute is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<unsigned long long> ready{0ull};
+  cudaError_t e = allow_smem(window_rows_kernel<D, KVT, NW, EX>, C::SMEM, ready);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(window_rows_kernel<D, KVT, NW, EX>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit, std::memory_order_release);
-  }
   CUtensorMap mk, mv;
   memset(&mk, 0, sizeof(mk));
   memset(&mv, 0, sizeof(mv));

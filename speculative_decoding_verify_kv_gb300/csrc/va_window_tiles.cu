@@ -18,8 +18,7 @@
 // 42, 64 rows 44 against 42; D = 128 (8 KV heads) 32 rows 86 us against 97, 48
 // rows 136 against 101; D = 256 (4 KV heads) 24 rows 79 us against 71.
 // Four warps issue the loads: one thread took 150 ns a tensor copy.
-#include <atomic>
-
+#include "va_host.h"
 #include "va_window_rows.cuh"
 
 namespace va {
@@ -174,16 +173,9 @@ template <int D, int RT, int PG, bool EX>
 static cudaError_t launch_tiles_t(Params& p, cudaStream_t st) {
   using C = TileCfg<D, RT, PG>;
   static_assert(C::NST >= PG && C::SMEM <= 227 * 1024, "ring");
-  static std::atomic<unsigned long long> ready{0ull};  // devices whose attribute is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  static std::atomic<unsigned long long> ready{0ull};
+  cudaError_t e = allow_smem(window_tiles_kernel<D, RT, PG, EX>, C::SMEM, ready);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(window_tiles_kernel<D, RT, PG, EX>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit, std::memory_order_release);
-  }
   CUtensorMap mk, mv;
   if (!make_page_maps(p, &mk, &mv)) return cudaErrorInvalidValue;
   p.joined = chunks_join<window_tiles_kernel<D, RT, PG, EX>>(p, C::THREADS, C::SMEM, st);

@@ -255,3 +255,77 @@ def test_offsets_past_32_bits():
             want = torch.softmax(z, -1) @ v[s, 0, t].double()
             assert (o[2 * s + j].double() - want).abs().max() < 2e-4
             assert (lse[2 * s + j].double() - torch.logsumexp(z, -1)).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("kv,heads,kvh,dim,rows", [("bf16", 4, 1, 64, 2), ("bf16", 4, 1, 64, 9), ("bf16", 4, 1, 128, 4),
+                                                   ("bf16", 4, 1, 128, 8), ("q8_0", 4, 1, 256, 3), ("q8_0", 4, 1, 256, 16),
+                                                   ("bf16", 4, 1, 256, 9), ("f32", 4, 1, 64, 5)])
+@pytest.mark.parametrize("splits", [9, 20, 256])
+def test_more_chunks_than_a_cluster_joins(kv, heads, kvh, dim, rows, splits):
+    """Partials through the workspace; most chunks hold two tiles, many none."""
+    case = make(kv, heads, kvh, dim, [2900, 100, 1500], [rows, 1, rows], paged=True, seed=splits + rows)
+    c = poison_unseen(case, 2600, 30)
+    check(c, *run(c, 2600, 30, splits=splits), so.window_case(c, 2600, 30), False)
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+def test_long_windows_in_one_chunk_stay_exact_in_fp32(rows):
+    """O in fp32 over 9,000 bf16 tokens, one chunk asked for: the tensor cores'
+    running sums would be off by some 2e-5 of O; within 8e-6 of the norm (P
+    carries 16 bits or more: 2^-18 of each term, and 2,048 tokens of drift)."""
+    case = make("bf16", 4, 1, 256, [9000], [rows], paged=True, seed=rows)
+    O, L = so.window_case(case, 9000, 0)
+    o, lse = run(case, 9000, 0, splits=1)
+    assert np.linalg.norm(o - O) <= 8e-6 * np.linalg.norm(O)
+    assert np.abs(lse - L).max() < 1e-4
+
+
+def test_fp32_cache_with_bf16_queries():
+    case = dataclasses.replace(make("f32", 4, 1, 64, [200, 30], [7, 1], paged=True, seed=5), q_dtype="bf16")
+    case = dataclasses.replace(case, q=sy.f32_to_bf16_bits(case.q))
+    check(case, *run(case, 50, 3, splits=2), so.window_case(case, 50, 3), False)
+
+
+FIRST = """
+import sys, torch
+sys.path.insert(0, {root!r}); sys.path.insert(0, {root!r} + "/tests")
+import numpy as np
+import speculative_decoding_verify_kv_gb300 as va, synthetic as sy
+case = sy.make_case("first", num_heads=4, num_kv_heads=1, head_dim=64, kv_dtype={kv!r}, q_dtype="bf16", ctx=[300, 9],
+                    rows=[{rows}, 1], paged=True, seed=1)
+p, kv, mode = va.upload(case, "cuda", num_splits=2)
+call = va.WindowCall(p, kv, mode, va.Window(64, 2))
+z = torch.randn(p.total_rows, 500, device="cuda")
+f = lambda n: torch.rand(n, device="cuda")
+d = va.Draft(z, 500, torch.zeros(p.total_rows, dtype=torch.int32, device="cuda"), f(p.total_rows), f(2), logits_dtype=va.F32)
+accept = va.AcceptCall(p, d, 0)
+i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+table, ref = torch.full((2, 4), -1, dtype=torch.int32, device="cuda"), torch.zeros(9, dtype=torch.int32, device="cuda")
+pool = va.PagePool(table, ref)
+plan, pack = va.ForkCall(pool, i32(0), i32(0), i32(0), i32(3)), va.CompactCall(pool)
+copy = va.PageCopyCall([torch.zeros(9, 64, device="cuda")], *plan._out)
+free = va.FreeCall(pool, i32(0), i32(1), i32(2))
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    for c in (call, accept, plan, copy, free, pack):
+        c()
+g.replay()
+torch.cuda.synchronize()
+o = call._out[0].clone()
+assert table.tolist() == [[0, -1, 1, -1], [-1] * 4], table
+call()
+assert torch.equal(o, call._out[0])
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("kv,rows", [("bf16", 1), ("bf16", 6), ("q8_0", 6)])
+def test_the_first_calls_of_a_process_may_be_captured(kv, rows):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, kv=kv, rows=rows)], capture_output=True, text=True,
+                       timeout=120)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr

@@ -143,7 +143,7 @@ def _window(w=(128, 4, va.F32), fn="verify_attn_window", p=None, kv=None, mode=0
 @pytest.mark.parametrize("kw,code", [
     (dict(w=(0, 4, 0)), 1), (dict(w=(-1, 4, 0)), 1), (dict(w=(8, -1, 0)), 1), (dict(w=(8, 0, 9)), 1),
     (dict(w=(8, 0, va.Q8_0)), 2), (dict(mode=7), 1), (dict(p=dict(num_seqs=0)), 1), (dict(kv=dict(head_dim=96)), 2),
-    (dict(p=dict(q_dtype=va.F32)), 2), (dict(p=dict(num_splits=257)), 2), (dict(o=None), 1), (dict(lse=None), 1),
+    (dict(p=dict(q_dtype=va.F32)), 2), (dict(p=dict(num_splits=257)), 2), (dict(p=dict(num_seqs=65536)), 2), (dict(o=None), 1), (dict(lse=None), 1),
     (dict(o=FAKE + 8), 3), (dict(ws=None), 4), (dict(b=1000), 4), (dict(ws=FAKE + 16), 3), (dict(kv=dict(k=FAKE + 4)), 3),
 ])
 def test_window_refusals(kw, code):
