@@ -374,8 +374,9 @@ va_status verify_attn_noalloc(const va_problem *p, const va_kv *kv, int32_t mode
  *     score weighs 0, and 0 times infinity is NaN).
  *   - num_splits is here the largest number of chunks that a sequence's
  *     visible tokens are cut into (whole 64-token tiles, at least 128
- *     tokens).  About SMs / (num_seqs * num_kv_heads) chunks fill the GPU once
- *     (va_window_splits).  With o_dtype VA_F32 more may be made, so that
+ *     tokens).  About c SMs / (num_seqs * num_kv_heads) chunks fill the GPU
+ *     once (va_window_splits): c CTAs run on an SM, 2 where a KV head has at
+ *     most 16 query rows and else 1.  With o_dtype VA_F32 more may be made, so that
  *     none holds more than 2,048 tokens: over more, the tensor cores' running
  *     sums drift visibly.  No choice depends on the other sequences of the
  *     launch: kernel and chunks follow from the types, from num_splits and
@@ -554,8 +555,9 @@ va_status verify_attn_pages_compact(const va_page_pool *pool, int32_t *copies, i
  * page copies[i][0] to page copies[i][1].  page_bytes is a multiple of 16
  * (num_kv_heads * 16 * row bytes for a cache).  No target may be another
  * pair's source or target.  Nothing is copied when *status holds a finding of
- * an earlier call; a pair outside the pool is passed over and sets
- * VA_DEV_BAD_COPY, as does *num_copies > max_copies.
+ * an earlier call other than VA_DEV_BAD_COPY; a pair outside the pool is
+ * passed over and sets VA_DEV_BAD_COPY, as does *num_copies > max_copies
+ * (the first max_copies pairs are copied).
  */
 va_status verify_attn_pages_copy(void *const *pools, int32_t num_pools, int64_t page_bytes,
                                  int32_t num_blocks, const int32_t *copies,

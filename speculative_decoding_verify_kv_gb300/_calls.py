@@ -48,8 +48,10 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 class _Call:
     """Arguments of one entry point, bound.  Subclasses fill ``_fn``,
-    ``_args`` (all but the stream), ``_out`` and ``device``."""
+    ``_args`` (all but the stream), ``_out``, ``_keep`` (every tensor whose
+    address is bound) and ``device``."""
     _where = ""
+    _own = ()  # buffers that the call allocated itself
 
     def __call__(self, stream=None):
         dev = self.device
@@ -58,23 +60,39 @@ class _Call:
         index = torch.cuda.current_device()
         if index != dev.index:
             raise ValueError(f"{self._where}: tensors on {dev}, current device cuda:{index}")
-        st = self._fn(*self._args, _current_stream(index) if stream is None else stream.cuda_stream)
+        if stream is None:
+            st = self._fn(*self._args, _current_stream(index))
+        else:
+            st = self._fn(*self._args, stream.cuda_stream)
+            for t in self._own:  # freed with the call, perhaps before the stream gets to it
+                t.record_stream(stream)
         if st:
             raise VaError(st, self._where)
         return self._out
+
+    def _new(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        self._own += (t,)
+        return t
 
     def _buffer(self, name, t, shape, dtype):
         n = 1
         for d in shape:
             n *= d
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return self._new(shape, dtype)
         return _tensor(name, t, dtype, n, self.device)
 
     def _workspace(self, ws, need):
         if ws is None:
-            return torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            return self._new(max(need, 256), torch.uint8)
         return _tensor("ws", ws, torch.uint8, need, self.device)
+
+
+def _tensors(*holders):
+    """The values of argument objects as they are now: the objects may be given
+    other tensors later, the addresses are bound."""
+    return tuple(t for h in holders for t in vars(h).values())
 
 
 @dataclass
@@ -137,7 +155,7 @@ class WindowCall(_Call):
         self._fn, self._out = lib.verify_attn_window, (o, lse)
         self._args = (ctypes.byref(pc), ctypes.byref(kc), mode, ctypes.byref(wc), _ptr(ws), ws.numel(), _ptr(o),
                       _ptr(lse), _ptr(status))
-        self._keep = (p, kv, ws, status, pc, kc, wc)
+        self._keep = (_tensors(p, kv), ws, status, pc, kc, wc)
 
 
 def verify_attn_window(p: Problem, kv: KV, mode: int, window: Window, *, stream=None, **kw):
@@ -209,7 +227,7 @@ class AcceptCall(_Call):
         self._fn, self._out = lib.verify_attn_accept, out
         self._args = (ctypes.byref(pc), ctypes.byref(dc), mode, _ptr(ws), ws.numel(), _ptr(out["accepted_len"]),
                       _ptr(out["accepted_nodes"]), _ptr(promote_len), _ptr(out["next_token"]), _ptr(status))
-        self._keep = (p, draft, ws, status, pc, dc)
+        self._keep = (_tensors(p, draft), ws, status, pc, dc)
 
 
 def verify_attn_accept(p: Problem, draft: Draft, mode: int, *, stream=None, **kw):
@@ -264,7 +282,7 @@ class ForkCall(_PageCall):
         self._fn, self._out = lib.verify_attn_pages_fork, (copies, num_copies)
         self._args = (ctypes.byref(c), n, _ptr(src), _ptr(dst), _ptr(length), _ptr(pages), _ptr(copies),
                       _ptr(num_copies), _ptr(ws), ws.numel(), _ptr(status))
-        self._keep = (pool, src, dst, length, pages, ws, status, c)
+        self._keep = (_tensors(pool), src, dst, length, pages, ws, status, c)
 
 
 class FreeCall(_PageCall):
@@ -276,7 +294,7 @@ class FreeCall(_PageCall):
         n = self._commands(seq=seq, first=first, last=last)
         self._fn, self._out = lib.verify_attn_pages_free, None
         self._args = (ctypes.byref(c), n, _ptr(seq), _ptr(first), _ptr(last), _ptr(status))
-        self._keep = (pool, seq, first, last, status, c)
+        self._keep = (_tensors(pool), seq, first, last, status, c)
 
 
 class CompactCall(_PageCall):
@@ -292,7 +310,7 @@ class CompactCall(_PageCall):
         self._fn, self._out = lib.verify_attn_pages_compact, (copies, num_copies, live_blocks)
         self._args = (ctypes.byref(c), _ptr(copies), _ptr(num_copies), _ptr(live_blocks), _ptr(ws), ws.numel(),
                       _ptr(status))
-        self._keep = (pool, ws, status, c)
+        self._keep = (_tensors(pool), ws, status, c)
 
 
 class PageCopyCall(_Call):
@@ -317,7 +335,7 @@ class PageCopyCall(_Call):
         self._fn, self._out = lib.verify_attn_pages_copy, None
         self._args = (ptrs, len(pools), bytes_of(pools[0]) // blocks, blocks, _ptr(copies), _ptr(num_copies),
                       copies.numel() // 2, _ptr(status))
-        self._keep = (pools, copies, num_copies, status)
+        self._keep = (tuple(pools), copies, num_copies, status)
 
 
 def verify_attn_pages_fork(pool: PagePool, src, dst, length, pages, *, stream=None, **kw):

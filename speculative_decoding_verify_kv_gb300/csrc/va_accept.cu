@@ -365,8 +365,7 @@ __device__ __forceinline__ void best_of_lanes(float& m, int& at) {
 
 // The walk runs for a few microseconds and most of its code once, so the
 // instructions that it has to fetch count like the work: loops stay rolled,
-// and what several places need is one function out of line.  (65 KB of
-// unrolled code took 27 us for one sequence's draw, 20 KB of it 8.)
+// and what several places need is one function out of line.
 
 // Weights of a unit of 256 values: lane's values i, i + 32, .. into its
 // places of dst, 32 apart; their sum.  i counts from the row's start.

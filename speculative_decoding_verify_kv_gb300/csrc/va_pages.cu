@@ -491,8 +491,9 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const CopyPara
 static va_status check_pool(const va_page_pool* g) {
   if (!g || !g->block_table || !g->ref_count) return VA_ERR_INVALID_ARG;
   if (g->num_seqs < 1 || g->max_blocks_per_seq < 1 || g->num_blocks < 1) return VA_ERR_INVALID_ARG;
-  // Totals of fresh pages and token counts stay within 32 bits.
+  // Totals of fresh pages, token counts and loop counters stay within 32 bits.
   if (g->max_blocks_per_seq > (1 << 26)) return VA_ERR_UNSUPPORTED;
+  if (g->num_blocks > (1 << 30) || g->num_seqs > (1 << 30)) return VA_ERR_UNSUPPORTED;
   if ((uintptr_t)g->block_table % 4 || (uintptr_t)g->ref_count % 4) return VA_ERR_ALIGNMENT;
   return VA_OK;
 }
@@ -565,6 +566,7 @@ va_status verify_attn_pages_fork(const va_page_pool* pool, int32_t num_forks, co
   va_status st = check_pool(pool);
   if (st != VA_OK) return st;
   if (num_forks < 0 || !num_copies) return VA_ERR_INVALID_ARG;
+  if (num_forks > (1 << 30)) return VA_ERR_UNSUPPORTED;
   if (num_forks > 0 && (!src || !dst || !len || !pages || !copies)) return VA_ERR_INVALID_ARG;
   if ((long long)num_forks * pool->max_blocks_per_seq > 0x7fffffffLL) return VA_ERR_UNSUPPORTED;
   cudaStream_t cs = (cudaStream_t)stream;

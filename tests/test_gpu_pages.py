@@ -281,3 +281,26 @@ def test_a_captured_fork_and_copy_replays():
         (a, b), = want[2]
         assert torch.equal(pool[a], pool[b]) and int(st.item()) == 0
     assert n > 1
+
+
+def test_buffers_of_a_call_on_another_stream_outlive_it():
+    """A call that is dropped while its stream has yet to run it: its
+    workspace and outputs are not handed out again before."""
+    pool = va.PagePool(torch.full((2, 64), -1, dtype=torch.int32, device="cuda"),
+                       torch.zeros(1 << 16, dtype=torch.int32, device="cuda"))
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    side = torch.cuda.Stream()
+    call = va.ForkCall(pool, i32(0), i32(0), i32(0), i32(40))
+    held = {t.data_ptr() for t in call._own}
+    assert len(held) == 3
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)
+    call(side)
+    sizes = [t.numel() * t.element_size() for t in call._own]
+    del call
+    again = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
+    assert not side.query()  # still asleep
+    assert not held & {t.data_ptr() for t in again}
+    torch.cuda.synchronize()
+    assert pool.block_table[0].tolist() == list(range(40)) + [-1] * 24

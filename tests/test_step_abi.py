@@ -57,7 +57,7 @@ def _pool(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(num_seqs=0), 1), (dict(max_blocks_per_seq=0), 1), (dict(num_blocks=0), 1), (dict(block_table=None), 1),
-    (dict(ref_count=None), 1), (dict(max_blocks_per_seq=(1 << 26) + 1), 2), (dict(block_table=FAKE + 2), 3),
+    (dict(ref_count=None), 1), (dict(num_blocks=(1 << 30) + 1), 2), (dict(num_seqs=(1 << 30) + 1), 2), (dict(max_blocks_per_seq=(1 << 26) + 1), 2), (dict(block_table=FAKE + 2), 3),
     (dict(ref_count=FAKE + 1), 3),
 ])
 def test_pool_refusals(kw, code):
@@ -182,3 +182,25 @@ def test_window_calls_check_their_tensors():
         kw = {k: v for k, v in bad.items() if k not in ("p", "kv", "w")}
         with pytest.raises((TypeError, ValueError, va.VaError)):
             va.WindowCall(bad.get("p", p()), bad.get("kv", kv()), 0, bad.get("w", w), **kw)
+
+
+def test_bound_calls_hold_the_tensors_they_were_given():
+    """The argument objects may get other tensors later: the addresses are bound."""
+    import gc
+    import weakref
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32)  # noqa: E731
+    pool = va.PagePool(i32(-1, -1).view(1, 2), i32(0, 0))
+    pools = [torch.zeros(2, 16)]
+    call, free, copy = va.CompactCall(pool), va.FreeCall(pool, i32(0), i32(0), i32(1)), va.PageCopyCall(pools, i32(0, 1), i32(1))
+    p = va.Problem(num_seqs=1, num_heads=1, total_rows=1, max_rows_per_seq=1, q=None, q_dtype=va.F32, cu_rows=i32(0, 1),
+                   ctx_len=None, parent=None, seq_kind=None)
+    draft = va.Draft(torch.zeros(1, 8), 8, i32(0), torch.zeros(1), torch.zeros(1), logits_dtype=va.F32)
+    accept = va.AcceptCall(p, draft, 0)
+    held = [weakref.ref(t) for t in (pool.block_table, pool.ref_count, pools[0], draft.logits, draft.tokens, p.cu_rows)]
+    pool.block_table = pool.ref_count = draft.logits = draft.tokens = p.cu_rows = None
+    pools.clear()
+    gc.collect()
+    assert all(r() is not None for r in held)
+    del call, free, copy, accept
+    gc.collect()
+    assert all(r() is None for r in held)
