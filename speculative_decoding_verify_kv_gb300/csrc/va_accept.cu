@@ -31,7 +31,7 @@
 // every later border by e, so that over a vocabulary the share of v that
 // draws another token is e times the number of tokens that matter.  The
 // weights of the last row are therefore 64-bit fixed-point numbers
-// (2^41 exp(z - max) for a vocabulary of 2^17, relative error about 2^-32)
+// (2^39 exp(z - max) up to a vocabulary of 2^19, relative error about 2^-32)
 // summed as integers: no order of summation changes the result, and borders
 // move by about 1e-10.
 #include <cooperative_groups.h>
@@ -55,7 +55,13 @@ constexpr int kWalkWarps = kWalkThreads / 32;
 constexpr int kMaxCluster = 16;      // CTAs per sequence: 8, or 16 (see walk_cluster)
 constexpr int kUnit = 256;           // values a warp takes at a time, 8 per lane
 constexpr int kMaxVocab = 1 << 20;
-constexpr int kMaxCacheBytes = 72 * 1024;  // of a CTA's weights in shared memory: two CTAs share an SM
+// A CTA's dynamic shared memory: two CTAs share an SM.  It holds the weights of
+// a row's part so that a pass after a rejection does not make them again; in
+// five bytes a cluster of 8 holds 163,000 (32 chains over 131,072 values: 56
+// us, and 68 when eight-byte weights did not fit and were made again).
+constexpr int kMaxWalkBytes = 103 * 1024;
+constexpr int kWeightBytes = 5;      // of a weight kept in shared memory
+constexpr int kRowBytes = 28;        // of a row's test
 constexpr float kMinTemperature = 1e-6f;  // below it, only 0
 
 struct AcceptParams {
@@ -63,6 +69,7 @@ struct AcceptParams {
   int vocab, pieces;
   int weight_bits;        // weights are 2^weight_bits exp(..)
   int cached;             // the walk keeps its row's weights in shared memory
+  int kept;               // units that a CTA has room for
   const int* cu_rows;
   const int* parent;
   const unsigned char* seq_kind;
@@ -110,6 +117,25 @@ __device__ __forceinline__ float accept_temperature(const AcceptParams& p, int s
   return p.temperature ? p.temperature[s] : 1.f;
 }
 
+// a b + c and a + b of two values at once.
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
+  unsigned long long x, y, z, d;
+  memcpy(&x, &a, 8);
+  memcpy(&y, &b, 8);
+  memcpy(&z, &c, 8);
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+  memcpy(&a, &d, 8);
+  return a;
+}
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
+  unsigned long long x, y, d;
+  memcpy(&x, &a, 8);
+  memcpy(&y, &b, 8);
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+  memcpy(&a, &d, 8);
+  return a;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -146,6 +172,33 @@ struct RowStep {
         w[k] = make_uint4(c[0], c[1], c[2], c[3]);
       }
     }
+  }
+  // Values 2 e and 2 e + 1 of vector k, one register each.
+  __device__ __forceinline__ float2 pair(int k, int e) const {
+    const uint32_t c[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+    if (sizeof(T) == 4) return make_float2(__uint_as_float(c[(2 * e) & 3]), __uint_as_float(c[(2 * e + 1) & 3]));
+    return make_float2(__uint_as_float(c[e] << 16), __uint_as_float(c[e] & 0xFFFF0000u));
+  }
+  // The largest value (a NaN counts as none).
+  __device__ __forceinline__ float largest() const {
+    if (sizeof(T) == 4) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) m = fmaxf(m, fmaxf(pair(k, e).x, pair(k, e).y));
+      return m;
+    }
+    __nv_bfloat162 m = bf16_pair(w[0].x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m = __hmax2(m, __hmax2(__hmax2(bf16_pair(w[k].x), bf16_pair(w[k].y)), __hmax2(bf16_pair(w[k].z), bf16_pair(w[k].w))));
+    return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
+  }
+  static __device__ __forceinline__ __nv_bfloat162 bf16_pair(uint32_t u) {
+    __nv_bfloat162 b;
+    memcpy(&b, &u, 4);
+    return b;
   }
   // Value e of vector k.
   __device__ __forceinline__ float at(int k, int e) const {
@@ -326,15 +379,36 @@ struct WalkShared {
   unsigned long long cut[kMaxRej + 2];    // c_0 + .. + c_(k-1)
   float ctamax[2][kMaxCluster];
   int ctaat[2][kMaxCluster];
-  float p[kMaxRows], q[kMaxRows], u[kMaxRows], top[kMaxRows];
-  int token[kMaxRows], at[kMaxRows];
-  short par[kMaxRows];
   float wmax[kWalkWarps];
   int wat[kWalkWarps];
   int rej_token[kMaxRej];
   unsigned err;
   int node, count, nrej, cmd, cursor;
   float rej_mass;
+};
+
+// The weights of a unit, below 2^40, in shared memory: their low words, and the
+// fifth bytes of a lane's values (32 apart) in two words.
+struct Unit {
+  uint32_t lo[kUnit];
+  uint32_t hi[2][32];
+  __device__ __forceinline__ unsigned long long get(int i) const {
+    return ((unsigned long long)(hi[i >> 7][i & 31] >> (8 * (i >> 5 & 3)) & 0xFFu) << 32) | lo[i];
+  }
+  __device__ __forceinline__ void clear(int i) {
+    lo[i] = 0u;
+    reinterpret_cast<unsigned char*>(&hi[i >> 7][i & 31])[i >> 5 & 3] = 0;
+  }
+};
+static_assert(sizeof(Unit) == kUnit * kWeightBytes, "room of a unit");
+
+// The rows' tests: p(x), g(x), u, the row's own maximum, x, the place of the
+// maximum (-1: no distribution, -2: not known), the parent.
+struct WalkRows {
+  float *p, *q, *u, *top;
+  int *token, *at, *par;
+  __device__ __forceinline__ WalkRows(void* base, int n)
+      : p((float*)base), q(p + n), u(q + n), top(u + n), token((int*)(top + n)), at(token + n), par(at + n) {}
 };
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
@@ -367,21 +441,26 @@ __device__ __forceinline__ void best_of_lanes(float& m, int& at) {
 // instructions that it has to fetch count like the work: loops stay rolled,
 // and what several places need is one function out of line.
 
-// Weights of a unit of 256 values: lane's values i, i + 32, .. into its
-// places of dst, 32 apart; their sum.  i counts from the row's start.
+// Weights of a unit of 256 values: this lane's values i, i + 32, .. into dst;
+// their sum.  i counts from the row's start.
 template <typename T>
 __device__ __noinline__ unsigned long long fill_unit(const WalkShared& sh, const Weights w, const T* row, int vocab,
-                                                     int i, unsigned long long* dst) {
+                                                     int i, Unit* dst) {
+  const int lane = threadIdx.x & 31;
   float x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = i + 32 * e < vocab ? to_float<T>(row[i + 32 * e]) : -INFINITY;
   unsigned long long sum = 0ull;
+  uint32_t hi[2] = {0u, 0u};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const unsigned long long v = fixed_weight<T>(w, sh.pow2, threadIdx.x & 31, x[e]);
-    dst[32 * e] = v;
+    const unsigned long long v = fixed_weight<T>(w, sh.pow2, lane, x[e]);
+    dst->lo[lane + 32 * e] = (uint32_t)v;
+    hi[e / 4] |= (uint32_t)(v >> 32) << (8 * (e % 4));
     sum += v;
   }
+  dst->hi[0][lane] = hi[0];
+  dst->hi[1][lane] = hi[1];
   return sum;
 }
 
@@ -389,15 +468,18 @@ __device__ __noinline__ unsigned long long fill_unit(const WalkShared& sh, const
 // probabilities.  A rejection takes s to max(s - c g, 0), c the sum of all s
 // before it; a weight that reached 0 stays there, so after several of them it
 // is max(v - (c_0 + c_1 + ..) g, 0).
-__device__ __noinline__ unsigned long long sum_unit(const unsigned long long* src, const float* guess, int vocab,
-                                                    int i, const Cut cut) {
+__device__ __noinline__ unsigned long long sum_unit(const Unit* src, const float* guess, int vocab, int i,
+                                                    const Cut cut) {
+  const int lane = threadIdx.x & 31;
   unsigned long long sum = 0ull;
   float g[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) g[e] = cut.c31 && i + 32 * e < vocab ? guess[i + 32 * e] : 0.f;
+  const uint32_t hi[2] = {src->hi[0][lane], src->hi[1][lane]};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const unsigned long long v = src[32 * e], c = cut_times(cut, g[e]);
+    const unsigned long long c = cut_times(cut, g[e]);
+    const unsigned long long v = ((unsigned long long)(hi[e / 4] >> (8 * (e % 4)) & 0xFFu) << 32) | src->lo[lane + 32 * e];
     sum += v > c ? v - c : 0ull;
   }
   return sum;
@@ -408,7 +490,7 @@ __device__ __noinline__ unsigned long long sum_unit(const unsigned long long* sr
 template <typename T, int kCluster>
 __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const AcceptParams p) {
   constexpr int kSegs = kCluster * kWalkWarps;
-  extern __shared__ __align__(16) unsigned long long weights[];
+  extern __shared__ __align__(16) uint32_t dynamic[];
   __shared__ WalkShared sh;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -426,6 +508,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
     sh.pow2.fix[i / 32][lane] = kPow2Fix[i / 32];
     sh.pow2.f[i / 32][lane] = (float)kPow2Fix[i / 32];
   }
+  Unit* const weights = reinterpret_cast<Unit*>(dynamic);
+  const WalkRows rows(weights + p.kept, p.max_rows);
   if (tid == 0) {
     sh.err = fits ? 0u : VA_DEV_BAD_ROWS;
     if (temp != 0.f && !(temp >= kMinTemperature && temp < INFINITY)) sh.err |= VA_DEV_BAD_SAMPLING;
@@ -447,7 +531,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
     return;
   }
 #pragma unroll 1
-  for (int j = tid; j < n; j += kWalkThreads) sh.at[j] = -2;  // no statistics
+  for (int j = tid; j < n; j += kWalkThreads) rows.at[j] = -2;  // no statistics
   __syncthreads();
 
   // Every row's test, at once: its parent, p(x) and g(x).  A warp per row
@@ -500,13 +584,13 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
     }
     if (lane == 0) {
       const bool usable = sum == sum && m < INFINITY && m > -INFINITY;
-      sh.par[j] = (short)a;
-      sh.token[j] = x;
-      sh.u[j] = u;
-      sh.q[j] = g;
-      sh.p[j] = !usable ? -1.f : greedy ? (x == at ? 1.f : 0.f) : exp2_fast((z - m) * inv) / sum;
-      sh.top[a] = m;  // siblings write the same values
-      sh.at[a] = usable ? at : -1;
+      rows.par[j] = a;
+      rows.token[j] = x;
+      rows.u[j] = u;
+      rows.q[j] = g;
+      rows.p[j] = !usable ? -1.f : greedy ? (x == at ? 1.f : 0.f) : exp2_fast((z - m) * inv) / sum;
+      rows.top[a] = m;  // siblings write the same values
+      rows.at[a] = usable ? at : -1;
     }
   }
   __syncthreads();
@@ -526,11 +610,11 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
 
   // This warp's part of a row: per units of 256 values.  Their weights are
   // kept in shared memory where the parts fit (p.cached), else a unit's are
-  // made in the warp's 2 KB each time.
+  // made in the warp's own place each time.
   const int per = (p.vocab + kUnit * kSegs - 1) / (kUnit * kSegs);
   const int lo = (rank * kWalkWarps + warp) * per * kUnit;
   const int units = lo < p.vocab ? min(per, (p.vocab - lo + kUnit - 1) / kUnit) : 0;
-  unsigned long long* const mine = weights + warp * (p.cached ? per : 1) * kUnit;
+  Unit* const mine = weights + warp * (p.cached ? per : 1);
   Weights w;
   w.top = 0.f;
   w.drop = 43 - p.weight_bits;
@@ -549,7 +633,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
   // rejected token weighs 0 there.
   Cut cut = {0u, 0};
   auto unit_left = [&](int k, int nrej) {
-    unsigned long long* at = mine + (p.cached ? k * kUnit : 0) + lane;
+    Unit* at = mine + (p.cached ? k : 0);
     const int i = lo + k * kUnit + lane;
     if (!filled) {
       unsigned long long sum = fill_unit<T>(sh, w, row, p.vocab, i, at);
@@ -557,8 +641,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
         __syncwarp();
         const int x = lane < nrej ? sh.rej_token[lane] - (i - lane) : -1;
         if (x >= 0 && x < kUnit) {
-          sum -= at[x - lane];
-          at[x - lane] = 0ull;
+          sum -= at->get(x);
+          at->clear(x);
         }
         __syncwarp();
       }
@@ -579,7 +663,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
       int node = sh.node, count = sh.count, nrej = sh.nrej, j = sh.cursor;
       float mass = sh.rej_mass;
       int cmd = DONE;
-      const int up = kind == 1 && lane > 0 && lane < n ? sh.par[lane] : -1;
+      const int up = kind == 1 && lane > 0 && lane < n ? rows.par[lane] : -1;
 #pragma unroll 1
       for (;;) {
         if (kind == 1) {
@@ -589,8 +673,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
           j = j <= node + 1 ? node + 1 : n;
         }
         if (j >= n) break;
-        const float u = sh.u[j], pj = sh.p[j], qj = sh.q[j];
-        const int x = sh.token[j];
+        const float u = rows.u[j], pj = rows.p[j], qj = rows.q[j];
+        const int x = rows.token[j];
         bool yes = false, lost = false;  // taken; rejected, with an effect
         if (greedy || pj < 0.f) {
           yes = pj > 0.f;  // below 0: the row has no distribution
@@ -644,8 +728,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
       guess = p.probs ? p.probs + (long long)(row0 + node) * p.probs_stride : nullptr;
       have = -1;
       filled = false;
-      w.top = sh.top[node];
-      best = sh.at[node];
+      w.top = rows.top[node];
+      best = rows.at[node];
       if (best == -2) {
         // The statistics kernel left the row out (a leaf): its maximum.
         float m = -INFINITY;
@@ -763,11 +847,12 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
           base += sum;
           continue;
         }
-        const unsigned long long* at = mine + (p.cached ? k * kUnit : 0) + lane;
+        const Unit* at = mine + (p.cached ? k : 0);
 #pragma unroll 1
-        for (int i = lo + k * kUnit + lane, e = 0; e < kUnit / 32; ++e, i += 32, at += 32) {
+        for (int i = lo + k * kUnit + lane, e = 0; e < kUnit / 32; ++e, i += 32) {
           const unsigned long long c = cut.c31 && i < p.vocab ? cut_times(cut, guess[i]) : 0ull;
-          const unsigned long long inc = warp_scan(*at > c ? *at - c : 0ull, lane) + base;
+          const unsigned long long x = at->get(lane + 32 * e);
+          const unsigned long long inc = warp_scan(x > c ? x - c : 0ull, lane) + base;
           const unsigned hit = __ballot_sync(0xffffffffu, t < inc);
           if (hit) {
             if (lane == __ffs(hit) - 1) p.next_token[s] = i;
@@ -841,13 +926,13 @@ static cudaError_t prepare_walk(int dev, bool* usable) {
   int k = known[dev].load(std::memory_order_acquire);
   if (k == 0) {
     auto* kernel = accept_walk_kernel<T, kCluster>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCacheBytes);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxWalkBytes);
     if (e != cudaSuccess) return e;
     k = 1;
     if (kCluster > 8) {
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
-      Launch l(kCluster, 1, 1, kWalkThreads, kCluster, kMaxCacheBytes, nullptr);
+      Launch l(kCluster, 1, 1, kWalkThreads, kCluster, kMaxWalkBytes, nullptr);
       int n = 0;
       if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess) {
         cudaGetLastError();
@@ -861,23 +946,16 @@ static cudaError_t prepare_walk(int dev, bool* usable) {
   return cudaSuccess;
 }
 
-// Bytes of a CTA's part of a row's weights, and whether they are kept.
-static size_t walk_cache_bytes(int vocab, int cluster) {
-  const int per = (vocab + kUnit * cluster * kWalkWarps - 1) / (kUnit * cluster * kWalkWarps);
-  return (size_t)per * kWalkWarps * kUnit * sizeof(unsigned long long);
-}
-static bool walk_caches(int vocab, int cluster) {
-  return walk_cache_bytes(vocab, cluster) <= (size_t)kMaxCacheBytes;
-}
-
 template <typename T, int kCluster>
 static cudaError_t launch_walk(AcceptParams q, cudaStream_t st) {
-  // The weights of a CTA's part of the row where they fit, else one unit per
-  // warp.
-  const size_t bytes = walk_cache_bytes(q.vocab, kCluster);
-  q.cached = walk_caches(q.vocab, kCluster);
+  // The weights of a CTA's part of the row where they fit beside the rows'
+  // tests, else one unit per warp.
+  const int per = (q.vocab + kUnit * kCluster * kWalkWarps - 1) / (kUnit * kCluster * kWalkWarps);
+  const int tests = kRowBytes * q.max_rows;
+  q.cached = per * kWalkWarps * (int)sizeof(Unit) + tests <= kMaxWalkBytes;
+  q.kept = (q.cached ? per : 1) * kWalkWarps;
   Launch l((unsigned)(q.num_seqs * kCluster), 1, 1, kWalkThreads, kCluster,
-           q.cached ? bytes : (size_t)kWalkWarps * kUnit * sizeof(unsigned long long), st);
+           (size_t)(q.kept * (int)sizeof(Unit) + tests), st);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, accept_walk_kernel<T, kCluster>, q);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -939,10 +1017,11 @@ va_status verify_attn_accept(const va_problem* p, const va_draft* d, int32_t mod
   q.mode = mode;
   q.vocab = d->vocab;
   q.pieces = accept_pieces(d->vocab);
-  // The weights of a row sum to at most 2^58, the cuts of 31 rejections to 2^63.
+  // The weights of a row sum to at most 2^58, the cuts of 31 rejections to 2^63; a
+  // weight is at most 2^39 (kWeightBytes).
   int bits = 58;
   while (bits > 38 && (1LL << (58 - bits)) < d->vocab) --bits;
-  q.weight_bits = bits < 43 ? bits : 43;
+  q.weight_bits = bits < 39 ? bits : 39;
   q.cu_rows = p->cu_rows;
   q.parent = p->parent;
   q.seq_kind = p->seq_kind;

@@ -112,6 +112,15 @@ def test_trees_with_odd_strides(vocab, pad, offset, dtype, drawn):
                pad=pad, offset=offset))
 
 
+@pytest.mark.parametrize("vocab", [81921, 150001, 163841])
+@pytest.mark.parametrize("drawn", [False, True])
+def test_batches_whose_weights_fit_a_cluster_and_do_not(vocab, drawn):
+    """16 sequences: clusters of 8 CTAs, whose shared memory holds the weights
+    of a row of up to some 160,000 values."""
+    rows = [1, 3, 2, 4] * 4
+    check(Case("mixed", rows, [0, 1, 0, 1] * 4, vocab, "bf16", drawn, 1.0, vocab))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_mixed_kinds_and_temperatures(dtype):
     check(Case("mixed", [8, 1, 5, 32, 40], [1, 0, 0, 1, 0], 6007, dtype, True, [0.0, 0.0, 0.8, 1.0, 0.0], 5))
