@@ -493,21 +493,21 @@ __global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const Acce
   extern __shared__ __align__(16) uint32_t dynamic[];
   __shared__ WalkShared sh;
   asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int s = blockIdx.x / kCluster;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kind = accept_kind(p, s);
-  const float temp = accept_temperature(p, s);
-  const bool greedy = temp == 0.f;
-  int row0, n;
-  const bool fits = accept_rows(p, s, kind, &row0, &n);
 #pragma unroll 1
   for (int i = tid; i < kPow2 * 32; i += kWalkThreads) {
     sh.pow2.fix[i / 32][lane] = kPow2Fix[i / 32];
     sh.pow2.f[i / 32][lane] = (float)kPow2Fix[i / 32];
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int kind = accept_kind(p, s);
+  const float temp = accept_temperature(p, s);
+  const bool greedy = temp == 0.f;
+  int row0, n;
+  const bool fits = accept_rows(p, s, kind, &row0, &n);
   Unit* const weights = reinterpret_cast<Unit*>(dynamic);
   const WalkRows rows(weights + p.kept, p.max_rows);
   if (tid == 0) {
