@@ -115,43 +115,125 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
     for (int k = 0; k < NK; ++k) acc[i][k] = 0.f;
   }
 
-  // A chain's row block sees no token past its last row, nor (but for the
-  // sinks) one before its first row's window.
-  const bool cut = WIN && kind == 0;
-  const int see_lo = cut ? win_low(p, ctx + rbase / p.G) - ws.skip : 0;
-  const int see_hi = cut ? vctx + (rbase + nrows - 1) / p.G + 1 : shi;
-  if (!err) {
-    for (int t0 = slo; t0 < shi; t0 += kSimtTile) {
-      if (cut && (t0 >= see_hi || (t0 + kSimtTile <= see_lo && t0 >= p.sinks))) continue;
-      __syncthreads();
-      if constexpr (WIN) {
-        // Four elements per thread and step.
-        for (int i = tid; i < kSimtTile * (D / 4); i += kSimtThreads) {
-          const int t = i / (D / 4), d = 4 * (i % (D / 4));
-          const int tok = t0 + t;
-          float4 kx = make_float4(0.f, 0.f, 0.f, 0.f), vx = kx;
-          if (tok < shi && !(tok >= ws.dead_lo && tok < ws.dead_hi)) {  // seen by some row
-            const bool draft = tok >= vctx && scratch;
-            const long long row = draft ? scratch_row(p, row0, kvh, tok - vctx)
-                                        : kv_row(p, s, kvh, tok >= ws.head ? tok + ws.skip : tok);
-            const void* kb = draft ? p.dk : p.k;
-            const void* vb = draft ? p.dv : p.v;
-            if (row < 0) {
-              atomicOr(&bad_s, 2);
-            } else if (KVT == VA_F32) {
-              kx = reinterpret_cast<const float4*>(kb)[(row * D + d) / 4];
-              vx = reinterpret_cast<const float4*>(vb)[(row * D + d) / 4];
-            } else {
-              kx = make_float4(load_kv<KVT>(kb, row, p.row_bytes, d), load_kv<KVT>(kb, row, p.row_bytes, d + 1),
-                               load_kv<KVT>(kb, row, p.row_bytes, d + 2), load_kv<KVT>(kb, row, p.row_bytes, d + 3));
-              vx = make_float4(load_kv<KVT>(vb, row, p.row_bytes, d), load_kv<KVT>(vb, row, p.row_bytes, d + 1),
-                               load_kv<KVT>(vb, row, p.row_bytes, d + 2), load_kv<KVT>(vb, row, p.row_bytes, d + 3));
-            }
-          }
-          *reinterpret_cast<float4*>(Ks + t * LDK + d) = kx;
-          *reinterpret_cast<float4*>(Vs + t * D + d) = vx;
+  if constexpr (WIN) {
+    // The next tile's loads are under way while a tile is worked through: four
+    // elements of K and V per thread and step.
+    constexpr int NR = kSimtTile * (D / 4) / kSimtThreads;
+    float4 kx[NR], vx[NR];
+    bool lost = false;  // a bad block-table entry
+    auto load = [&](int t0) {
+#pragma unroll
+      for (int x = 0; x < NR; ++x) {
+        const int i = tid + x * kSimtThreads, tok = t0 + i / (D / 4), d = 4 * (i % (D / 4));
+        kx[x] = vx[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (tok >= shi || (tok >= ws.dead_lo && tok < ws.dead_hi)) continue;  // seen by no row
+        const bool draft = tok >= vctx && scratch;
+        const long long row = draft ? scratch_row(p, row0, kvh, tok - vctx)
+                                    : kv_row(p, s, kvh, tok >= ws.head ? tok + ws.skip : tok);
+        const void* kb = draft ? p.dk : p.k;
+        const void* vb = draft ? p.dv : p.v;
+        if (row < 0) {
+          lost = true;
+        } else if (KVT == VA_F32) {
+          kx[x] = reinterpret_cast<const float4*>(kb)[(row * D + d) / 4];
+          vx[x] = reinterpret_cast<const float4*>(vb)[(row * D + d) / 4];
+        } else {
+          kx[x] = make_float4(load_kv<KVT>(kb, row, p.row_bytes, d), load_kv<KVT>(kb, row, p.row_bytes, d + 1),
+                              load_kv<KVT>(kb, row, p.row_bytes, d + 2), load_kv<KVT>(kb, row, p.row_bytes, d + 3));
+          vx[x] = make_float4(load_kv<KVT>(vb, row, p.row_bytes, d), load_kv<KVT>(vb, row, p.row_bytes, d + 1),
+                              load_kv<KVT>(vb, row, p.row_bytes, d + 2), load_kv<KVT>(vb, row, p.row_bytes, d + 3));
         }
-      } else {
+      }
+    };
+    // A chain's row block sees no token past its last row, nor (but for the
+    // sinks) one before its first row's window.
+    const int end = kind == 0 ? min(shi, vctx + (rbase + nrows - 1) / p.G + 1) : shi;
+    const int see_lo = kind == 0 ? win_low(p, ctx + rbase / p.G) - ws.skip : 0;
+    auto seen = [&](int t0) {  // the first tile from t0 on that the block sees
+      if (t0 >= p.sinks && t0 + kSimtTile <= see_lo) t0 += (see_lo - t0) / kSimtTile * kSimtTile;
+      return t0;
+    };
+    int t0 = seen(slo);
+    if (!err && t0 < end) load(t0);
+    while (!err && t0 < end) {
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < NR; ++x) {
+        const int i = tid + x * kSimtThreads, t = i / (D / 4), d = 4 * (i % (D / 4));
+        *reinterpret_cast<float4*>(Ks + t * LDK + d) = kx[x];
+        *reinterpret_cast<float4*>(Vs + t * D + d) = vx[x];
+      }
+      if (__syncthreads_or(lost)) {
+        err |= VA_DEV_BAD_BLOCK;
+        break;
+      }
+      const int next = seen(t0 + kSimtTile);
+      if (next < end) load(next);
+      // Scores: lane = token, rows warp + 4 i, the four from one read of K
+      // (rows past the block's last hold whatever the shared memory held and
+      // are masked).
+      const int tok = t0 + lane;
+      float sc[4] = {0.f, 0.f, 0.f, 0.f}, m_new[4];
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(Ks + lane * LDK + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 q = *reinterpret_cast<const float4*>(Qs + (warp + 4 * i) * D + d);
+          sc[i] = fmaf(q.w, k4.w, fmaf(q.z, k4.z, fmaf(q.y, k4.y, fmaf(q.x, k4.x, sc[i]))));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rl = warp + 4 * i;
+        const bool vis = rl < nrows && tok < shi &&
+                         (tok < vctx || draft_visible(kind, mask_s[rl], (rbase + rl) / p.G, tok - vctx)) &&
+                         (tok < p.sinks || tok >= wlo_s[rl] || (kind == 1 && tok >= vctx));
+        sc[i] = vis ? sc[i] * p.scale_log2 : -INFINITY;
+        m_new[i] = sc[i];
+      }
+      // The rows' reductions side by side: each step waits for a shuffle.
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m_new[i] = fmaxf(m_new[i], __shfl_xor_sync(0xffffffffu, m_new[i], o));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m_new[i] = fmaxf(m_run[i], m_new[i]);
+        const float off = m_new[i] == -INFINITY ? 0.f : m_new[i];  // nothing seen yet: every P is 0
+        const float alpha = exp2f(m_run[i] - off);
+        const float pr = exp2f(sc[i] - off);
+        l_run[i] = fmaf(l_run[i], alpha, pr);  // this lane's tokens
+        m_run[i] = m_new[i];
+        Ps[(warp + 4 * i) * kSimtTile + lane] = pr;
+#pragma unroll
+        for (int k = 0; k < NK; ++k) acc[i][k] *= alpha;
+      }
+      __syncwarp();
+      // acc[row][d] += sum_t P[row][t] V[t][d]; lane owns d = lane + 32 k.
+#pragma unroll 2
+      for (int t = 0; t < kSimtTile; t += 4) {
+        float4 pv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (warp + 4 * i) * kSimtTile + t);
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+          const float* v = Vs + t * D + lane + 32 * k;
+          const float v0 = v[0], v1 = v[D], v2 = v[2 * D], v3 = v[3 * D];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[i][k] = fmaf(pv[i].w, v3, fmaf(pv[i].z, v2, fmaf(pv[i].y, v1, fmaf(pv[i].x, v0, acc[i][k]))));
+        }
+      }
+      t0 = next;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], o);
+  } else if (!err) {
+    for (int t0 = slo; t0 < shi; t0 += kSimtTile) {
+      __syncthreads();
       // Decode the K/V tile; tokens past the range become zeros.
       for (int i = tid; i < kSimtTile * D; i += kSimtThreads) {
         int t = i / D, d = i % D;
@@ -170,9 +252,8 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
             vx = load_kv<KVT>(p.v, row, p.row_bytes, d);
           }
         }
-        Ks[t * LDK + d] = kx;
+        Ks[t * (D + 1) + d] = kx;
         Vs[t * D + d] = vx;
-      }
       }
       __syncthreads();
       if (bad_s & 2) {
@@ -181,33 +262,15 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
       }
       // Scores: lane = token, rows warp + 4i.
       const int tok = t0 + lane;
-      float dots[4] = {0.f, 0.f, 0.f, 0.f};
-      if (WIN) {
-        // The four rows of the warp from one read of K (rows past the block's
-        // last hold whatever the shared memory held and are dropped below).
-#pragma unroll 4
-        for (int d = 0; d < D; d += 4) {
-          const float4 k4 = *reinterpret_cast<const float4*>(Ks + lane * LDK + d);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 q = *reinterpret_cast<const float4*>(Qs + (warp + 4 * i) * D + d);
-            dots[i] = fmaf(q.w, k4.w, fmaf(q.z, k4.z, fmaf(q.y, k4.y, fmaf(q.x, k4.x, dots[i]))));
-          }
-        }
-      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int rl = warp + 4 * i;
         if (rl >= nrows) continue;
-        float dot = dots[i];
-        if (!WIN) {
+        float dot = 0.f;
 #pragma unroll 8
-          for (int d = 0; d < D; ++d) dot = fmaf(Qs[rl * D + d], Ks[lane * LDK + d], dot);
-        }
+        for (int d = 0; d < D; ++d) dot = fmaf(Qs[rl * D + d], Ks[lane * (D + 1) + d], dot);
         bool vis = tok < shi &&
-                   (tok < vctx || draft_visible(kind, mask_s[rl], (rbase + rl) / p.G, tok - vctx));
-        if (WIN)
-          vis = vis && (tok < p.sinks || tok >= wlo_s[rl] || (kind == 1 && tok >= vctx));
+                   (tok < ctx || draft_visible(kind, mask_s[rl], (rbase + rl) / p.G, tok - ctx));
         float s2 = vis ? dot * p.scale_log2 : -INFINITY;
         float mt = s2;
 #pragma unroll
@@ -225,28 +288,6 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
       }
       __syncthreads();
       // acc[row][d] = alpha * acc + sum_t P[row][t] V[t][d]; lane owns d = lane + 32k.
-      if constexpr (WIN) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = warp + 4 * i < nrows ? alpha_s[warp + 4 * i] : 0.f;
-#pragma unroll
-          for (int k = 0; k < NK; ++k) acc[i][k] *= a;
-        }
-#pragma unroll 2
-        for (int t = 0; t < kSimtTile; t += 4) {
-          float4 pv[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (warp + 4 * i) * kSimtTile + t);
-#pragma unroll
-          for (int k = 0; k < NK; ++k) {
-            const float* v = Vs + t * D + lane + 32 * k;
-            const float v0 = v[0], v1 = v[D], v2 = v[2 * D], v3 = v[3 * D];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[i][k] = fmaf(pv[i].w, v3, fmaf(pv[i].z, v2, fmaf(pv[i].y, v1, fmaf(pv[i].x, v0, acc[i][k]))));
-          }
-        }
-      } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int rl = warp + 4 * i;
@@ -259,7 +300,6 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
 #pragma unroll
           for (int k = 0; k < NK; ++k) acc[i][k] = fmaf(pv, Vs[t * D + lane + 32 * k], acc[i][k]);
         }
-      }
       }
     }
   }
