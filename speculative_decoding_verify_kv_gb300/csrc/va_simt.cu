@@ -25,6 +25,7 @@ namespace va {
 constexpr int kSimtRows = 16;    // query rows per CTA
 constexpr int kSimtTile = 32;    // tokens per tile
 constexpr int kSimtThreads = 128;
+constexpr int kSimtWinThreads = 256;  // windowed calls: few tiles to a CTA, so more warps at each
 
 // Floats from one K row of the tile to the next: the scores are read one
 // value per lane and token, or (WIN) four.
@@ -37,7 +38,9 @@ struct SimtCfg {
 // WIN: a windowed call; token indexes then count the span of visible tokens
 // (WinSpan).
 template <int D, int KVT, bool WIN>
-__global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params p) {
+__global__ void __launch_bounds__(WIN ? kSimtWinThreads : kSimtThreads) simt_partial_kernel(const Params p) {
+  constexpr int TH = WIN ? kSimtWinThreads : kSimtThreads;
+  constexpr int WARPS = TH / 32, RW = kSimtRows / WARPS;  // rows of a warp: warp + WARPS i
   constexpr int NK = D / 32;  // accumulator columns per lane
   constexpr int LDK = SimtCfg<D, WIN>::LDK;
   extern __shared__ float sm[];
@@ -98,17 +101,17 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
   sub_range(lo, hi, nsub, p.min_sub, sub, &slo, &shi);
 
   // Q rows of this block -> shared (fp32).
-  for (int i = tid; i < nrows * D; i += kSimtThreads) {
+  for (int i = tid; i < nrows * D; i += TH) {
     int rl = i / D, d = i % D;
     int r = rbase + rl, j = r / p.G, g = r % p.G;
     long long qi = ((long long)(row0 + j) * p.H + (kvh * p.G + g)) * D + d;
     Qs[rl * D + d] = load_q(p, qi);
   }
 
-  float m_run[4], l_run[4];
-  float acc[4][NK];
+  float m_run[RW], l_run[RW];
+  float acc[RW][NK];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < RW; ++i) {
     m_run[i] = -INFINITY;
     l_run[i] = 0.f;
 #pragma unroll
@@ -118,13 +121,13 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
   if constexpr (WIN) {
     // The next tile's loads are under way while a tile is worked through: four
     // elements of K and V per thread and step.
-    constexpr int NR = kSimtTile * (D / 4) / kSimtThreads;
+    constexpr int NR = kSimtTile * (D / 4) / TH;
     float4 kx[NR], vx[NR];
     bool lost = false;  // a bad block-table entry
     auto load = [&](int t0) {
 #pragma unroll
       for (int x = 0; x < NR; ++x) {
-        const int i = tid + x * kSimtThreads, tok = t0 + i / (D / 4), d = 4 * (i % (D / 4));
+        const int i = tid + x * TH, tok = t0 + i / (D / 4), d = 4 * (i % (D / 4));
         kx[x] = vx[x] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (tok >= shi || (tok >= ws.dead_lo && tok < ws.dead_hi)) continue;  // seen by no row
         const bool draft = tok >= vctx && scratch;
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
       __syncthreads();
 #pragma unroll
       for (int x = 0; x < NR; ++x) {
-        const int i = tid + x * kSimtThreads, t = i / (D / 4), d = 4 * (i % (D / 4));
+        const int i = tid + x * TH, t = i / (D / 4), d = 4 * (i % (D / 4));
         *reinterpret_cast<float4*>(Ks + t * LDK + d) = kx[x];
         *reinterpret_cast<float4*>(Vs + t * D + d) = vx[x];
       }
@@ -167,25 +170,28 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
         err |= VA_DEV_BAD_BLOCK;
         break;
       }
-      const int next = seen(t0 + kSimtTile);
+      const int tok = t0 + lane, next = seen(t0 + kSimtTile);
       if (next < end) load(next);
-      // Scores: lane = token, rows warp + 4 i, the four from one read of K
+      t0 = next;
+      if (warp >= nrows) continue;
+      // Scores: lane = token, the warp's rows from one read of K
       // (rows past the block's last hold whatever the shared memory held and
       // are masked).
-      const int tok = t0 + lane;
-      float sc[4] = {0.f, 0.f, 0.f, 0.f}, m_new[4];
+      float sc[RW], m_new[RW];
+#pragma unroll
+      for (int i = 0; i < RW; ++i) sc[i] = 0.f;
 #pragma unroll 4
       for (int d = 0; d < D; d += 4) {
         const float4 k4 = *reinterpret_cast<const float4*>(Ks + lane * LDK + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4 q = *reinterpret_cast<const float4*>(Qs + (warp + 4 * i) * D + d);
+        for (int i = 0; i < RW; ++i) {
+          const float4 q = *reinterpret_cast<const float4*>(Qs + (warp + WARPS * i) * D + d);
           sc[i] = fmaf(q.w, k4.w, fmaf(q.z, k4.z, fmaf(q.y, k4.y, fmaf(q.x, k4.x, sc[i]))));
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rl = warp + 4 * i;
+      for (int i = 0; i < RW; ++i) {
+        const int rl = warp + WARPS * i;
         const bool vis = rl < nrows && tok < shi &&
                          (tok < vctx || draft_visible(kind, mask_s[rl], (rbase + rl) / p.G, tok - vctx)) &&
                          (tok < p.sinks || tok >= wlo_s[rl] || (kind == 1 && tok >= vctx));
@@ -196,16 +202,16 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m_new[i] = fmaxf(m_new[i], __shfl_xor_sync(0xffffffffu, m_new[i], o));
+        for (int i = 0; i < RW; ++i) m_new[i] = fmaxf(m_new[i], __shfl_xor_sync(0xffffffffu, m_new[i], o));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < RW; ++i) {
         m_new[i] = fmaxf(m_run[i], m_new[i]);
         const float off = m_new[i] == -INFINITY ? 0.f : m_new[i];  // nothing seen yet: every P is 0
         const float alpha = exp2f(m_run[i] - off);
         const float pr = exp2f(sc[i] - off);
         l_run[i] = fmaf(l_run[i], alpha, pr);  // this lane's tokens
         m_run[i] = m_new[i];
-        Ps[(warp + 4 * i) * kSimtTile + lane] = pr;
+        Ps[(warp + WARPS * i) * kSimtTile + lane] = pr;
 #pragma unroll
         for (int k = 0; k < NK; ++k) acc[i][k] *= alpha;
       }
@@ -213,24 +219,23 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
       // acc[row][d] += sum_t P[row][t] V[t][d]; lane owns d = lane + 32 k.
 #pragma unroll 2
       for (int t = 0; t < kSimtTile; t += 4) {
-        float4 pv[4];
+        float4 pv[RW];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (warp + 4 * i) * kSimtTile + t);
+        for (int i = 0; i < RW; ++i) pv[i] = *reinterpret_cast<const float4*>(Ps + (warp + WARPS * i) * kSimtTile + t);
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
           const float* v = Vs + t * D + lane + 32 * k;
           const float v0 = v[0], v1 = v[D], v2 = v[2 * D], v3 = v[3 * D];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < RW; ++i)
             acc[i][k] = fmaf(pv[i].w, v3, fmaf(pv[i].z, v2, fmaf(pv[i].y, v1, fmaf(pv[i].x, v0, acc[i][k]))));
         }
       }
-      t0 = next;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], o);
+      for (int i = 0; i < RW; ++i) l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], o);
   } else if (!err) {
     for (int t0 = slo; t0 < shi; t0 += kSimtTile) {
       __syncthreads();
@@ -308,8 +313,8 @@ __global__ void __launch_bounds__(kSimtThreads) simt_partial_kernel(const Params
   }
   // Write this CTA's slot for its rows (an empty range writes l = 0).
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int rl = warp + 4 * i;
+  for (int i = 0; i < RW; ++i) {
+    const int rl = warp + WARPS * i;
     if (rl >= nrows) continue;
     const int r = rbase + rl, j = r / p.G, g = r % p.G;
     const int grow = row0 + j, h = kvh * p.G + g;
@@ -333,7 +338,7 @@ static cudaError_t launch_simt_t(const Params& p, dim3 grid, cudaStream_t st) {
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kSimtThreads);
+  cfg.blockDim = dim3(WIN ? kSimtWinThreads : kSimtThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
