@@ -376,9 +376,11 @@ va_status verify_attn_noalloc(const va_problem *p, const va_kv *kv, int32_t mode
  *     visible tokens are cut into (whole 64-token tiles, at least 128
  *     tokens).  About c SMs / (num_seqs * num_kv_heads) chunks fill the GPU
  *     once (va_window_splits): c CTAs run on an SM, 2 where a KV head has at
- *     most 16 query rows and else 1.  With o_dtype VA_F32 more may be made, so that
- *     none holds more than 2,048 tokens: over more, the tensor cores' running
- *     sums drift visibly.  No choice depends on the other sequences of the
+ *     most 16 query rows and else 1.  A KV head with more query rows than a
+ *     block of its kernel (128, 16 for fp32 caches) gets fewer, in all about as
+ *     many CTAs.  With o_dtype VA_F32 more may be made, so that none holds more
+ *     than 2,048 tokens: over more, the tensor cores' running sums drift
+ *     visibly.  No choice depends on the other sequences of the
  *     launch: kernel and chunks follow from the types, from num_splits and
  *     max_rows_per_seq as given, and from the sequence itself.
  *   - Rows that no sequence covers stay as they were.  Where row offsets
