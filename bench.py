@@ -78,15 +78,15 @@ def parse():
 
 
 # DRAM bytes (read + write) of one partial launch of the headline call
-# (row-major tensor-core kernel, Q8_0 with hi + lo K, ctx 32768: 71,658,496
-# read + 1,564,160 written), from the ncu capture summarised in
+# (row-major tensor-core kernel, Q8_0 with hi + lo K, ctx 32768: 71,610,624
+# read + 1,733,632 written), from the ncu capture summarised in
 # profiles/umma_partial_q8_ctx32768.md.  Reported only while the kernel
 # sources (comments and white space aside) are the ones it was taken on.
 PROFILED_TRAFFIC = {
     "kernel": 1,
-    "bytes": 73_136_640,
-    "sources": {"va_umma.cu": "721253357a9ab7ec", "va_common.cuh": "c2688452ae35bd94",
-                "va_sm100.cuh": "ff735fa02c94f492"},
+    "bytes": 73_344_256,
+    "sources": {"va_umma.cuh": "576e2f7b2e10831c", "va_common.cuh": "e7b91b33ff01a9e4",
+                "va_sm100.cuh": "a5c927233004f795"},
 }
 
 

@@ -14,9 +14,10 @@
 // it is a warp's chain of steps per page (some 1.5 us, issue slots 40 % used);
 // with more rows, or at D = 256, fewer pages are under way and the tcgen05
 // kernel wins.  Measured against it, 32 sequences of 2,052 visible tokens, one
-// chunk each: D = 64 (4 KV heads) 24 rows 25 us against 41, 48 rows 36 against
-// 42, 64 rows 44 against 42; D = 128 (8 KV heads) 32 rows 86 us against 97, 48
-// rows 136 against 101; D = 256 (4 KV heads) 24 rows 79 us against 71.
+// chunk each: D = 64 (4 KV heads) 24 rows 22.5 us against 41, 48 rows 32 against
+// 42; D = 128 (8 KV heads) 32 rows 80 us against 97.  Past the limits, when they
+// were set: D = 64 64 rows 44 against 42; D = 128 48 rows 136 against 101; D = 256
+// (4 KV heads) 24 rows 79 against 71.
 // Four warps issue the loads: one thread took 150 ns a tensor copy.
 #include "va_host.h"
 #include "va_window_rows.cuh"
