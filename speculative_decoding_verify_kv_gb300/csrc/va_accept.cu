@@ -50,16 +50,16 @@ namespace cg = cooperative_groups;
 constexpr int kPiece = 4096;         // values per statistics warp
 constexpr int kStatThreads = 256;
 constexpr int kStatWarps = kStatThreads / 32;
-constexpr int kWalkThreads = 512;
-constexpr int kWalkWarps = kWalkThreads / 32;
-constexpr int kMaxCluster = 16;      // CTAs per sequence: 8, or 16 (see walk_cluster)
+constexpr int kMaxWalkWarps = 32;    // of a CTA: 16, or 32 (see launch_accept)
+constexpr int kMaxCluster = 16;      // CTAs per sequence: 8, or 16
 constexpr int kUnit = 256;           // values a warp takes at a time, 8 per lane
 constexpr int kMaxVocab = 1 << 20;
-// A CTA's dynamic shared memory: two CTAs share an SM.  It holds the weights of
-// a row's part so that a pass after a rejection does not make them again; in
-// five bytes a cluster of 8 holds 163,000 (32 chains over 131,072 values: 56
-// us, and 68 when eight-byte weights did not fit and were made again).
-constexpr int kMaxWalkBytes = 103 * 1024;
+// Dynamic shared memory of the walk on an SM: of one CTA of 1,024 threads or of
+// two of 512.  It holds the weights of a row's part so that a pass after a
+// rejection does not make them again; in five bytes a cluster of 8 with 512
+// threads holds 163,000 (32 chains over 131,072 values: 56 us, and 68 when
+// eight-byte weights did not fit and were made again).
+constexpr int kWalkBytes = 206 * 1024;
 constexpr int kWeightBytes = 5;      // of a weight kept in shared memory
 constexpr int kRowBytes = 28;        // of a row's test
 constexpr float kMinTemperature = 1e-6f;  // below it, only 0
@@ -373,14 +373,14 @@ constexpr int kMaxRej = kMaxTreeRows;  // rejected siblings of one node
 
 struct WalkShared {
   Pow2Table pow2;
-  unsigned long long warps[2][kWalkWarps];  // sums over each warp's part of the row
+  unsigned long long warps[2][kMaxWalkWarps];  // sums over each warp's part of the row
   unsigned long long ctas[2][kMaxCluster];  // and over each CTA's
   unsigned long long scale[kMaxRej + 1];  // c_k: sum of the weights left by k rejections
   unsigned long long cut[kMaxRej + 2];    // c_0 + .. + c_(k-1)
   float ctamax[2][kMaxCluster];
   int ctaat[2][kMaxCluster];
-  float wmax[kWalkWarps];
-  int wat[kWalkWarps];
+  float wmax[kMaxWalkWarps];
+  int wat[kMaxWalkWarps];
   int rej_token[kMaxRej];
   unsigned err;
   int node, count, nrej, cmd, cursor;
@@ -487,8 +487,9 @@ __device__ __noinline__ unsigned long long sum_unit(const Unit* src, const float
 
 // Walk of one sequence by a cluster.  Every CTA takes the same decisions
 // from the same numbers, so the cluster's barriers always match.
-template <typename T, int kCluster>
-__global__ void __launch_bounds__(kWalkThreads, 2) accept_walk_kernel(const AcceptParams p) {
+template <typename T, int kCluster, int kWalkThreads>
+__global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk_kernel(const AcceptParams p) {
+  constexpr int kWalkWarps = kWalkThreads / 32;
   constexpr int kSegs = kCluster * kWalkWarps;
   extern __shared__ __align__(16) uint32_t dynamic[];
   __shared__ WalkShared sh;
@@ -916,49 +917,49 @@ struct Launch {
   }
 };
 
-// What a kernel's clusters of 16 need and may have is found out once per
-// device: 0 unknown, 1 usable, 2 not (a GPC with too few SMs).
+// A walk of clusters of kCluster CTAs of kThreads threads.
 constexpr int kMaxDevices = 64;
 
-template <typename T, int kCluster>
-static cudaError_t prepare_walk(int dev, bool* usable) {
-  static std::atomic<int> known[kMaxDevices];
-  int k = known[dev].load(std::memory_order_acquire);
-  if (k == 0) {
-    auto* kernel = accept_walk_kernel<T, kCluster>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxWalkBytes);
-    if (e != cudaSuccess) return e;
-    k = 1;
-    if (kCluster > 8) {
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+template <typename T, int kCluster, int kThreads>
+struct Walk {
+  static constexpr int kMaxBytes = kWalkBytes / (1024 / kThreads);
+
+  // Sets the kernel's limits, once per device; how many clusters run at once
+  // (0: none, a GPC has too few SMs).
+  static cudaError_t prepare(int dev, int* at_once) {
+    static std::atomic<int> known[kMaxDevices];  // one more than that
+    int n = known[dev].load(std::memory_order_acquire) - 1;
+    if (n < 0) {
+      auto* kernel = accept_walk_kernel<T, kCluster, kThreads>;
+      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxBytes);
+      if (e == cudaSuccess && kCluster > 8)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
-      Launch l(kCluster, 1, 1, kWalkThreads, kCluster, kMaxWalkBytes, nullptr);
-      int n = 0;
+      Launch l(kCluster, 1, 1, kThreads, kCluster, kMaxBytes, nullptr);
       if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess) {
         cudaGetLastError();
         n = 0;
       }
-      if (n < 1) k = 2;
+      known[dev].store(n + 1, std::memory_order_release);
     }
-    known[dev].store(k, std::memory_order_release);
+    *at_once = n;
+    return cudaSuccess;
   }
-  *usable = k == 1;
-  return cudaSuccess;
-}
 
-template <typename T, int kCluster>
-static cudaError_t launch_walk(AcceptParams q, cudaStream_t st) {
-  // The weights of a CTA's part of the row where they fit beside the rows'
-  // tests, else one unit per warp.
-  const int per = (q.vocab + kUnit * kCluster * kWalkWarps - 1) / (kUnit * kCluster * kWalkWarps);
-  const int tests = kRowBytes * q.max_rows;
-  q.cached = per * kWalkWarps * (int)sizeof(Unit) + tests <= kMaxWalkBytes;
-  q.kept = (q.cached ? per : 1) * kWalkWarps;
-  Launch l((unsigned)(q.num_seqs * kCluster), 1, 1, kWalkThreads, kCluster,
-           (size_t)(q.kept * (int)sizeof(Unit) + tests), st);
-  cudaError_t e = cudaLaunchKernelEx(&l.cfg, accept_walk_kernel<T, kCluster>, q);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
+  static cudaError_t launch(AcceptParams q, cudaStream_t st) {
+    // The weights of a CTA's part of the row where they fit beside the rows'
+    // tests, else one unit per warp.
+    constexpr int W = kThreads / 32;
+    const int per = (q.vocab + kUnit * kCluster * W - 1) / (kUnit * kCluster * W);
+    const int tests = kRowBytes * q.max_rows;
+    q.cached = per * W * (int)sizeof(Unit) + tests <= kMaxBytes;
+    q.kept = (q.cached ? per : 1) * W;
+    Launch l((unsigned)(q.num_seqs * kCluster), 1, 1, kThreads, kCluster,
+             (size_t)(q.kept * (int)sizeof(Unit) + tests), st);
+    cudaError_t e = cudaLaunchKernelEx(&l.cfg, accept_walk_kernel<T, kCluster, kThreads>, q);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+};
 
 template <typename T>
 static cudaError_t launch_accept(const AcceptParams& q, cudaStream_t st) {
@@ -966,16 +967,17 @@ static cudaError_t launch_accept(const AcceptParams& q, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  // Clusters of 16 while they all run at once (14 on 152 SMs), else of 8.
-  bool wide = q.num_seqs <= 14, usable = true;
-  if (wide) {
-    e = prepare_walk<T, 16>(dev, &wide);
-    if (e != cudaSuccess) return e;
-  }
-  if (!wide) {
-    e = prepare_walk<T, 8>(dev, &usable);
-    if (e != cudaSuccess) return e;
-  }
+  // As many threads to a sequence as let all sequences run at once: clusters of
+  // 16 CTAs of 1,024 threads (7 of them; 4 sequences of trees and chains over
+  // 100,000 values and more 17 to 34 us against 19 to 39 with 512; up to 65,536
+  // values, one unit per warp, the smaller CTAs start sooner: 7.5 us against
+  // 8.0), of 512 (14), or of 8.
+  int n = 0;
+  int kind = 0;
+  if (q.vocab > 16 * 16 * kUnit && (e = Walk<T, 16, 1024>::prepare(dev, &n)) == cudaSuccess && q.num_seqs <= n) kind = 2;
+  if (e == cudaSuccess && kind == 0 && (e = Walk<T, 16, 512>::prepare(dev, &n)) == cudaSuccess && q.num_seqs <= n) kind = 1;
+  if (e == cudaSuccess && kind == 0) e = Walk<T, 8, 512>::prepare(dev, &n);
+  if (e != cudaSuccess) return e;
   // A sequence of one row has no proposal: nothing to prepare.
   if (q.max_rows > 1) {
     Launch l((unsigned)((q.pieces + kStatWarps - 1) / kStatWarps), (unsigned)q.max_rows, (unsigned)q.num_seqs,
@@ -983,7 +985,8 @@ static cudaError_t launch_accept(const AcceptParams& q, cudaStream_t st) {
     e = cudaLaunchKernelEx(&l.cfg, accept_stats_kernel<T>, q);
     if (e != cudaSuccess) return e;
   }
-  return wide ? launch_walk<T, 16>(q, st) : launch_walk<T, 8>(q, st);
+  if (kind == 2) return Walk<T, 16, 1024>::launch(q, st);
+  return kind == 1 ? Walk<T, 16, 512>::launch(q, st) : Walk<T, 8, 512>::launch(q, st);
 }
 
 }  // namespace va

@@ -112,6 +112,19 @@ def test_trees_with_odd_strides(vocab, pad, offset, dtype, drawn):
                pad=pad, offset=offset))
 
 
+@pytest.mark.parametrize("seqs", [7, 8, 14, 15])
+def test_batches_that_all_run_at_once_and_do_not(seqs):
+    """The threads of a sequence follow from their number; a sequence's result
+    does not."""
+    c = Case("mixed", [3, 9] * 8, [0, 1] * 8, 70001, "f32", True, 0.9, 70)
+    full = check(c)
+    c.cu, c.kinds, c.v, c.temperature = c.cu[:seqs + 1], c.kinds[:seqs], c.v[:seqs], c.temperature[:seqs]
+    n = int(c.cu[-1])
+    c.parent, c.tokens, c.u, c.logits, c.probs = c.parent[:n], c.tokens[:n], c.u[:n], c.logits[:n], c.probs[:n]
+    for g, w, k in zip(check(c), full, (seqs, n, seqs, seqs)):
+        assert np.array_equal(g[:k], w[:k])
+
+
 @pytest.mark.parametrize("vocab", [81921, 150001, 163841])
 @pytest.mark.parametrize("drawn", [False, True])
 def test_batches_whose_weights_fit_a_cluster_and_do_not(vocab, drawn):
