@@ -411,10 +411,12 @@ struct WalkRows {
       : p((float*)base), q(p + n), u(q + n), top(u + n), token((int*)(top + n)), at(token + n), par(at + n) {}
 };
 
+// In three parts of 22 bits, whose sums fit 32.
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
-#pragma unroll 1
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  const unsigned a = __reduce_add_sync(0xffffffffu, (unsigned)v & 0x3FFFFFu);
+  const unsigned b = __reduce_add_sync(0xffffffffu, (unsigned)(v >> 22) & 0x3FFFFFu);
+  const unsigned c = __reduce_add_sync(0xffffffffu, (unsigned)(v >> 44));
+  return a + ((unsigned long long)b << 22) + ((unsigned long long)c << 44);
 }
 
 __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v, int lane) {
@@ -507,6 +509,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
   const int kind = accept_kind(p, s);
   const float temp = accept_temperature(p, s);
   const bool greedy = temp == 0.f;
+  const float draw_v = p.sample_u[s];  // (used at the end)
   int row0, n;
   const bool fits = accept_rows(p, s, kind, &row0, &n);
   Unit* const weights = reinterpret_cast<Unit*>(dynamic);
@@ -831,7 +834,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
   // The next token, from what is left at the last node: the lowest i whose
   // running sum passes t = floor(v total).
   if (best >= 0 && !greedy) {
-    const float v = p.sample_u[s];
+    const float v = draw_v;
     unsigned long long t = v > 0.f ? __umul64hi(total, v < 1.f ? (unsigned long long)__float2ull_rz(v * 0x1p63f) << 1
                                                                : ~0ull)
                                    : 0ull;
@@ -843,23 +846,26 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
       // One warp owns the border: the unit that holds it, then the 32 values.
 #pragma unroll 1
       for (int k = 0; k < units; ++k) {
-        const unsigned long long sum = warp_sum(unit_left(k, left));
-        if (t - base >= sum) {
-          base += sum;
-          continue;
+        // (The last unit holds it if the ones before it do not.)
+        if (!filled || k + 1 < units) {
+          const unsigned long long sum = warp_sum(unit_left(k, left));
+          if (t - base >= sum) {
+            base += sum;
+            continue;
+          }
         }
         const Unit* at = mine + (p.cached ? k : 0);
 #pragma unroll 1
         for (int i = lo + k * kUnit + lane, e = 0; e < kUnit / 32; ++e, i += 32) {
           const unsigned long long c = cut.c31 && i < p.vocab ? cut_times(cut, guess[i]) : 0ull;
-          const unsigned long long x = at->get(lane + 32 * e);
-          const unsigned long long inc = warp_scan(x > c ? x - c : 0ull, lane) + base;
-          const unsigned hit = __ballot_sync(0xffffffffu, t < inc);
-          if (hit) {
+          const unsigned long long w = at->get(lane + 32 * e), x = w > c ? w - c : 0ull;
+          const unsigned long long sum = warp_sum(x);
+          if (t - base < sum) {
+            const unsigned hit = __ballot_sync(0xffffffffu, t < warp_scan(x, lane) + base);
             if (lane == __ffs(hit) - 1) p.next_token[s] = i;
             break;
           }
-          base = __shfl_sync(0xffffffffu, inc, 31);
+          base += sum;
         }
         break;
       }
