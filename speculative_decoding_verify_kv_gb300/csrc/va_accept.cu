@@ -57,8 +57,8 @@ constexpr int kMaxVocab = 1 << 20;
 // Dynamic shared memory of the walk on an SM: of one CTA of 1,024 threads or of
 // two of 512.  It holds the weights of a row's part so that a pass after a
 // rejection does not make them again; in five bytes a cluster of 8 with 512
-// threads holds 163,000 (32 chains over 131,072 values: 56 us, and 68 when
-// eight-byte weights did not fit and were made again).
+// threads holds 163,000 (32 chains over 131,072 values: 56 us when it was built, and 68
+// when eight-byte weights did not fit and were made again).
 constexpr int kWalkBytes = 206 * 1024;
 constexpr int kWeightBytes = 5;      // of a weight kept in shared memory
 constexpr int kRowBytes = 28;        // of a row's test
