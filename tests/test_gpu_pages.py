@@ -293,9 +293,10 @@ def test_buffers_of_a_call_on_another_stream_outlive_it():
     call = va.ForkCall(pool, i32(0), i32(0), i32(0), i32(40))
     held = {t.data_ptr() for t in call._own}
     assert len(held) == 3
+    torch.full((1,), 255, dtype=torch.uint8, device="cuda")  # (the fill below is loaded by now)
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        torch.cuda._sleep(400_000_000)
+        torch.cuda._sleep(2_000_000_000)  # a second
     call(side)
     sizes = [t.numel() * t.element_size() for t in call._own]
     del call
