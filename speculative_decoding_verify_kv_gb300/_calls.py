@@ -7,7 +7,9 @@ caller left out (outputs, workspace) and fills the C structs once; calling
 it launches on the current stream (or the one given) and returns the output
 tensors, which the next call of the same object overwrites.  The functions
 of the C names bind and call in one go.  Two calls that may overlap in time
-need two objects (the workspace is the object's).
+need two objects (the workspace is the object's).  A stream given to a call
+is recorded with its tensors (they may be dropped before it gets there); one
+made current follows the rules of any PyTorch operation.
 """
 from __future__ import annotations
 
@@ -64,11 +66,24 @@ class _Call:
             st = self._fn(*self._args, _current_stream(index))
         else:
             st = self._fn(*self._args, stream.cuda_stream)
-            for t in self._own:  # freed with the call, perhaps before the stream gets to it
+            for t in self._tensors():  # may be freed with the call, before the stream gets to it
                 t.record_stream(stream)
         if st:
             raise VaError(st, self._where)
         return self._out
+
+    def _tensors(self):
+        """Every tensor that a launch reads or writes."""
+        found, todo = [], [self._keep, self._own, self._out]
+        while todo:
+            x = todo.pop()
+            if isinstance(x, torch.Tensor):
+                found.append(x)
+            elif isinstance(x, (tuple, list)):
+                todo.extend(x)
+            elif isinstance(x, dict):
+                todo.extend(x.values())
+        return found
 
     def _new(self, shape, dtype):
         t = torch.empty(shape, dtype=dtype, device=self.device)
@@ -89,7 +104,7 @@ class _Call:
         return _tensor("ws", ws, torch.uint8, need, self.device)
 
 
-def _tensors(*holders):
+def _held(*holders):
     """The values of argument objects as they are now: the objects may be given
     other tensors later, the addresses are bound."""
     return tuple(t for h in holders for t in vars(h).values())
@@ -155,7 +170,7 @@ class WindowCall(_Call):
         self._fn, self._out = lib.verify_attn_window, (o, lse)
         self._args = (ctypes.byref(pc), ctypes.byref(kc), mode, ctypes.byref(wc), _ptr(ws), ws.numel(), _ptr(o),
                       _ptr(lse), _ptr(status))
-        self._keep = (_tensors(p, kv), ws, status, pc, kc, wc)
+        self._keep = (_held(p, kv), ws, status, pc, kc, wc)
 
 
 def verify_attn_window(p: Problem, kv: KV, mode: int, window: Window, *, stream=None, **kw):
@@ -227,7 +242,7 @@ class AcceptCall(_Call):
         self._fn, self._out = lib.verify_attn_accept, out
         self._args = (ctypes.byref(pc), ctypes.byref(dc), mode, _ptr(ws), ws.numel(), _ptr(out["accepted_len"]),
                       _ptr(out["accepted_nodes"]), _ptr(promote_len), _ptr(out["next_token"]), _ptr(status))
-        self._keep = (_tensors(p, draft), ws, status, pc, dc)
+        self._keep = (_held(p, draft), ws, status, pc, dc)
 
 
 def verify_attn_accept(p: Problem, draft: Draft, mode: int, *, stream=None, **kw):
@@ -282,7 +297,7 @@ class ForkCall(_PageCall):
         self._fn, self._out = lib.verify_attn_pages_fork, (copies, num_copies)
         self._args = (ctypes.byref(c), n, _ptr(src), _ptr(dst), _ptr(length), _ptr(pages), _ptr(copies),
                       _ptr(num_copies), _ptr(ws), ws.numel(), _ptr(status))
-        self._keep = (_tensors(pool), src, dst, length, pages, ws, status, c)
+        self._keep = (_held(pool), src, dst, length, pages, ws, status, c)
 
 
 class FreeCall(_PageCall):
@@ -294,7 +309,7 @@ class FreeCall(_PageCall):
         n = self._commands(seq=seq, first=first, last=last)
         self._fn, self._out = lib.verify_attn_pages_free, None
         self._args = (ctypes.byref(c), n, _ptr(seq), _ptr(first), _ptr(last), _ptr(status))
-        self._keep = (_tensors(pool), seq, first, last, status, c)
+        self._keep = (_held(pool), seq, first, last, status, c)
 
 
 class CompactCall(_PageCall):
@@ -310,7 +325,7 @@ class CompactCall(_PageCall):
         self._fn, self._out = lib.verify_attn_pages_compact, (copies, num_copies, live_blocks)
         self._args = (ctypes.byref(c), _ptr(copies), _ptr(num_copies), _ptr(live_blocks), _ptr(ws), ws.numel(),
                       _ptr(status))
-        self._keep = (_tensors(pool), ws, status, c)
+        self._keep = (_held(pool), ws, status, c)
 
 
 class PageCopyCall(_Call):

@@ -285,20 +285,20 @@ def test_a_captured_fork_and_copy_replays():
 
 def test_buffers_of_a_call_on_another_stream_outlive_it():
     """A call that is dropped while its stream has yet to run it: its
-    workspace and outputs are not handed out again before."""
+    workspace, outputs and arguments are not handed out again before."""
     pool = va.PagePool(torch.full((2, 64), -1, dtype=torch.int32, device="cuda"),
                        torch.zeros(1 << 16, dtype=torch.int32, device="cuda"))
     i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
     side = torch.cuda.Stream()
     call = va.ForkCall(pool, i32(0), i32(0), i32(0), i32(40))
-    held = {t.data_ptr() for t in call._own}
-    assert len(held) == 3
+    held = {t.data_ptr() for t in call._own + call._keep[1:5]}  # workspace, outputs, and the commands made for it
+    assert len(held) == 7
     torch.full((1,), 255, dtype=torch.uint8, device="cuda")  # (the fill below is loaded by now)
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
         torch.cuda._sleep(2_000_000_000)  # a second
     call(side)
-    sizes = [t.numel() * t.element_size() for t in call._own]
+    sizes = [t.numel() * t.element_size() for t in call._own + call._keep[1:5]]
     del call
     again = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(4)]
     assert not side.query()  # still asleep
