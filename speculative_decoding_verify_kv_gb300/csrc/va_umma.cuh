@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
       join_l[WIN ? tid : 0] = l;
     }
     __syncthreads();
-    join_chunks<D>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l);
+    join_chunks<D>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l, 1);
   };
   if (ntiles == 0 && !err) {
     if (joined) {
@@ -1316,7 +1316,7 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tm, C::TMEM_COLS);
-  if (joined) join_chunks<D>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l);
+  if (joined) join_chunks<D>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l, 1);
 }
 
 // ---------------------------------------------------------------------------

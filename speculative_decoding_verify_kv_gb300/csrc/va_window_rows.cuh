@@ -507,7 +507,10 @@ __device__ __forceinline__ void join_rows(const Params& p, int slot, int row0, i
                                           int ld, float (*ms)[kTileRows], float (*ls)[kTileRows]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const bool one = p.slots == 1, partial = !p.joined;
-  for (int r = warp; r < R; r += warps) {
+  // A warp takes a row, or with fewer rows than warps 64 columns of one.
+  const int parts = R < warps ? D / 64 : 1;
+  for (int item = warp; item < R * parts; item += warps) {
+    const int r = item / parts, part = item - r * parts;
     const int tile = r / kTileRows, rt = r % kTileRows;
     float mr = -INFINITY;
 #pragma unroll
@@ -522,34 +525,33 @@ __device__ __forceinline__ void join_rows(const Params& p, int slot, int row0, i
     if (fail) mr = lr = NAN;
     const int grow = row0 + r / p.G, head = kvh * p.G + r % p.G;
     const float inv = one ? 1.f / lr : fail ? NAN : 1.f;
-    for (int c = 2 * lane; c < D; c += 64) {
+    float* at = os + (tile * kTileRows + rt) * ld;
+    for (int c = 64 * part + 2 * lane; c < D; c += 64 * parts) {
       float x = 0.f, y = 0.f;
-      float* at = os + (tile * kTileRows + rt) * ld + c;
 #pragma unroll
       for (int w = 0; w < NG; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(at + w * RT * kTileRows * ld);
+        const float2 v = *reinterpret_cast<const float2*>(at + c + w * RT * kTileRows * ld);
         x = fmaf(f[w], v.x, x);
         y = fmaf(f[w], v.y, y);
       }
       if (one || partial) put_pair<D>(p, partial, slot, grow, head, c, x * inv, y * inv);
-      else *reinterpret_cast<float2*>(at) = make_float2(x, y);  // the first group's place
+      else *reinterpret_cast<float2*>(at + c) = make_float2(x, y);  // the first group's place
     }
-    __syncwarp();
-    if (lane == 0) {
+    if (lane == 0 && part == 0) {
       if (one) {
         p.lse[(long long)grow * p.H + head] = (mr + log2f(lr)) * kLn2;
       } else if (partial) {
         const long long si = slot_index(p, slot, grow, head);
         p.ws_ml[2 * si] = mr;
         p.ws_ml[2 * si + 1] = lr;
-      } else {
-        ms[tile][rt] = mr;
-        ls[tile][rt] = lr;
+      } else {  // behind the row's columns (ms and ls are still read)
+        at[D] = mr;
+        at[D + 1] = lr;
       }
     }
   }
   if (one || partial) return;
-  join_chunks<D>(p, slot, row0, kvh, R, os, ld, &ms[0][0], &ls[0][0]);
+  join_chunks<D>(p, slot, row0, kvh, R, os, ld, os + D, os + D + 1, ld);
 }
 
 bool make_page_maps(const Params& p, CUtensorMap* k, CUtensorMap* v);
