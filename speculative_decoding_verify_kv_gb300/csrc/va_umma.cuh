@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
       join_l[WIN ? tid : 0] = l;
     }
     __syncthreads();
-    join_chunks<D>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l, 1);
+    join_chunks<D, kJoinMany>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l, 1);
   };
   if (ntiles == 0 && !err) {
     if (joined) {
@@ -1316,7 +1316,7 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tm, C::TMEM_COLS);
-  if (joined) join_chunks<D>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l, 1);
+  if (joined) join_chunks<D, kJoinMany>(p, slot, row0, kvh, R, reinterpret_cast<float*>(sm), kORow / 4, join_m, join_l, 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -1382,7 +1382,7 @@ static cudaError_t launch_umma_t(std::conditional_t<WIN, Params&, const Params&>
   if (!C::kQ8) {
     if (!make_map(&mk, p, p.k, WIN) || !make_map(&mv, p, p.v, WIN)) return cudaErrorInvalidValue;
   }
-  if constexpr (WIN) p.joined = chunks_join<umma_partial_kernel<D, KVT, PAGED, WIN>>(p, C::THREADS, C::SMEM, st);
+  if constexpr (WIN) p.joined = chunks_join<umma_partial_kernel<D, KVT, PAGED, WIN>, kJoinMany>(p, C::THREADS, C::SMEM, st);
   if (WIN && p.joined) {
     WindowLaunch l(p, C::THREADS, C::SMEM, st);
     cudaError_t e = cudaLaunchKernelEx(&l.cfg, umma_partial_kernel<D, KVT, PAGED, WIN>, p, mk, mv);

@@ -12,10 +12,14 @@
 namespace va {
 namespace cg = cooperative_groups;
 
-// Chunks that may be joined in their kernel, as one cluster (the portable
-// size); otherwise they go through the workspace and the merge kernel.  Both
-// take the same sums in the same order, so that either gives the same bits.
-constexpr int kJoinChunks = 8;
+// Chunks that may be joined in their kernel, as one cluster; otherwise they go
+// through the workspace and the merge kernel.  Both take the same sums in the
+// same order, so that either gives the same bits.  With at most 16 rows per KV
+// head up to 16 (one token, 16 chunks at D = 64: 8.2 us against 12.5 through the
+// merge kernel), with more rows 8, the portable size (96 rows of D = 256 in 16
+// chunks: 29.6 us joined, 26.5 merged).
+constexpr int kJoinFew = 16;
+constexpr int kJoinMany = 8;
 
 __device__ __forceinline__ float ex2f(float x) {
   float y;
@@ -64,7 +68,7 @@ __device__ __forceinline__ void put_pair(const Params& p, bool partial, int slot
 // thread of every CTA of the cluster; a warp takes 64 columns of a row at a time,
 // with the loads from all chunks in flight together (a round trip to another
 // CTA's memory takes 0.6 us: one row's join 3.1 us with four of them in a row).
-template <int D>
+template <int D, int MAXC>
 __device__ __forceinline__ void join_chunks(const Params& p, int slot, int row0, int kvh, int R, float* os, int ld,
                                             float* ms, float* ls, int mld) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -78,22 +82,23 @@ __device__ __forceinline__ void join_chunks(const Params& p, int slot, int row0,
     const bool in = lane < p.slots;
     const float mk = in ? *cluster.map_shared_rank(ms + r * mld, lane) : -INFINITY;
     const float lk = in ? *cluster.map_shared_rank(ls + r * mld, lane) : 0.f;
-    float2 v[kJoinChunks];
+    float2 v[MAXC];
     auto load = [&](int c) {
 #pragma unroll
-      for (int k = 0; k < kJoinChunks; ++k)
+      for (int k = 0; k < MAXC; ++k)
         if (k < p.slots) v[k] = *reinterpret_cast<const float2*>(cluster.map_shared_rank(os + r * ld + c, k));
     };
     load(64 * part + 2 * lane);
     float mr = lk > 0.f ? mk : -INFINITY;
 #pragma unroll
-    for (int o = kJoinChunks / 2; o > 0; o >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+    for (int o = MAXC / 2; o > 0; o >>= 1) mr = fmaxf(mr, __shfl_xor_sync(0xffffffffu, mr, o));
     mr = __shfl_sync(0xffffffffu, mr, 0);
     const bool bad = __any_sync(0xffffffffu, lk != lk);
     const float fk = lk > 0.f ? ex2f(mk - mr) : 0.f;
-    float lr = 0.f, w[kJoinChunks];
+    float lr = 0.f, w[MAXC];
 #pragma unroll
-    for (int k = 0; k < kJoinChunks; ++k) {
+    for (int k = 0; k < MAXC; ++k) {
+      if (k % 8 == 0 && k >= p.slots) break;
       w[k] = __shfl_sync(0xffffffffu, fk, k);
       lr = fmaf(w[k], __shfl_sync(0xffffffffu, lk, k), lr);
     }
@@ -102,7 +107,8 @@ __device__ __forceinline__ void join_chunks(const Params& p, int slot, int row0,
     for (int c = 64 * part + 2 * lane;;) {
       float x = 0.f, y = 0.f;
 #pragma unroll
-      for (int k = 0; k < kJoinChunks; ++k) {
+      for (int k = 0; k < MAXC; ++k) {
+        if (k % 8 == 0 && k >= p.slots) break;
         if (k >= p.slots || !(w[k] > 0.f)) continue;
         x = fmaf(w[k], v[k].x, x);
         y = fmaf(w[k], v[k].y, y);
@@ -142,31 +148,34 @@ struct WindowLaunch {
 // them all and the clusters need no more rounds on the GPU than the CTAs by
 // themselves would (a GPC takes whole clusters only: 24 clusters of 6 CTAs
 // that fill an SM each took 74 us in two rounds, 41 us apart).
-template <auto KERNEL>
+template <auto KERNEL, int MAXC>
 static bool chunks_join(Params p, int threads, size_t smem, cudaStream_t st) {
   // (join_chunks takes the rows of one row block.)
-  if (p.slots > kJoinChunks || p.row_blocks > 1) return false;
+  if (p.slots > MAXC || p.row_blocks > 1) return false;
   if (p.slots == 1) return true;
   constexpr int kDevs = 64;
-  static std::atomic<int> clusters[kDevs][kJoinChunks + 1], ctas[kDevs];
+  static std::atomic<int> clusters[kDevs][MAXC + 1], ctas[kDevs];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevs) return false;
-  int n = clusters[dev][p.slots].load(std::memory_order_relaxed);
-  int c = ctas[dev].load(std::memory_order_relaxed);
-  if (n == 0 || c == 0) {
+  // (Stored one higher: 0 is not known yet, 1 none.)
+  int n = clusters[dev][p.slots].load(std::memory_order_relaxed) - 1;
+  int c = ctas[dev].load(std::memory_order_relaxed) - 1;
+  if (n < 0 || c < 0) {
     p.joined = 1;
     WindowLaunch l(p, threads, smem, st);
     int per = 0, sms = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, KERNEL, &l.cfg) != cudaSuccess ||
+    if ((p.slots > 8 && cudaFuncSetAttribute(KERNEL, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+        cudaOccupancyMaxActiveClusters(&n, KERNEL, &l.cfg) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, KERNEL, threads, smem) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1 || per < 1) {
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
       cudaGetLastError();
-      return false;
+      n = 0;
     }
     c = per * sms;
-    clusters[dev][p.slots].store(n, std::memory_order_relaxed);
-    ctas[dev].store(c, std::memory_order_relaxed);
+    clusters[dev][p.slots].store(n + 1, std::memory_order_relaxed);
+    ctas[dev].store(c + 1, std::memory_order_relaxed);
   }
+  if (n < 1 || c < 1) return false;
   const long long jobs = (long long)p.num_seqs * p.KVH;
   return (jobs + n - 1) / n <= (jobs * p.slots + c - 1) / c;
 }

@@ -162,7 +162,7 @@ static cudaError_t launch_few_t(Params& p, cudaStream_t st) {
   memset(&mk, 0, sizeof(mk));
   memset(&mv, 0, sizeof(mv));
   if (!C::kQ8 && !make_page_maps(p, &mk, &mv)) return cudaErrorInvalidValue;
-  p.joined = chunks_join<window_rows_kernel<D, KVT, NW, EX>>(p, NW * 32, C::SMEM, st);
+  p.joined = chunks_join<window_rows_kernel<D, KVT, NW, EX>, kJoinFew>(p, NW * 32, C::SMEM, st);
   WindowLaunch l(p, NW * 32, C::SMEM, st);
   e = cudaLaunchKernelEx(&l.cfg, window_rows_kernel<D, KVT, NW, EX>, p, mk, mv);
   return e != cudaSuccess ? e : cudaGetLastError();

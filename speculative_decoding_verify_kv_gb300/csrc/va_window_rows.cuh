@@ -500,8 +500,8 @@ __device__ __forceinline__ int page_place(const Params& p, const WinSpan& ws, in
 
 // Join the states of each row's NG page groups, in order, and write the rows
 // out.  State (group x, row tile y) lies at index x RT + y.  Every warp of the
-// CTA.  At most kJoinChunks chunks are joined in their cluster, with more each
-// chunk's partial goes to the workspace.
+// CTA.  Chunks that make a cluster are joined there, others' partials go to the
+// workspace.
 template <int D, int NG, int RT>
 __device__ __forceinline__ void join_rows(const Params& p, int slot, int row0, int kvh, int R, bool fail, float* os,
                                           int ld, float (*ms)[kTileRows], float (*ls)[kTileRows]) {
@@ -551,7 +551,7 @@ __device__ __forceinline__ void join_rows(const Params& p, int slot, int row0, i
     }
   }
   if (one || partial) return;
-  join_chunks<D>(p, slot, row0, kvh, R, os, ld, os + D, os + D + 1, ld);
+  join_chunks<D, (RT == 1 ? kJoinFew : kJoinMany)>(p, slot, row0, kvh, R, os, ld, os + D, os + D + 1, ld);
 }
 
 bool make_page_maps(const Params& p, CUtensorMap* k, CUtensorMap* v);

@@ -179,7 +179,7 @@ static cudaError_t launch_tiles_t(Params& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
   if (!make_page_maps(p, &mk, &mv)) return cudaErrorInvalidValue;
-  p.joined = chunks_join<window_tiles_kernel<D, RT, PG, EX>>(p, C::THREADS, C::SMEM, st);
+  p.joined = chunks_join<window_tiles_kernel<D, RT, PG, EX>, kJoinMany>(p, C::THREADS, C::SMEM, st);
   WindowLaunch l(p, C::THREADS, C::SMEM, st);
   e = cudaLaunchKernelEx(&l.cfg, window_tiles_kernel<D, RT, PG, EX>, p, mk, mv);
   return e != cudaSuccess ? e : cudaGetLastError();

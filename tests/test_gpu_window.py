@@ -125,7 +125,7 @@ FEW = [(kv, h, k, d) for kv in ("bf16", "q8_0") for h, k, d in ((8, 1, 64), (8, 
 
 @pytest.mark.parametrize("kv,heads,kvh,dim,rows", [("bf16", 8, 2, 64, 1), ("bf16", 8, 2, 128, 7), ("q8_0", 6, 1, 256, 2),
                                                    ("q8_0", 6, 1, 256, 16), ("bf16", 6, 1, 256, 16)])
-@pytest.mark.parametrize("splits", [2, 5, 8])
+@pytest.mark.parametrize("splits", [2, 5, 8, 12, 16])
 def test_many_sequences_and_one_give_the_same_bits(kv, heads, kvh, dim, rows, splits):
     """Few clusters are joined in their kernel, many go through the merge
     kernel: a sequence's bits are the same."""
@@ -260,8 +260,8 @@ def test_offsets_past_32_bits():
 @pytest.mark.parametrize("kv,heads,kvh,dim,rows", [("bf16", 4, 1, 64, 2), ("bf16", 4, 1, 64, 9), ("bf16", 4, 1, 128, 4),
                                                    ("bf16", 4, 1, 128, 8), ("q8_0", 4, 1, 256, 3), ("q8_0", 4, 1, 256, 16),
                                                    ("bf16", 4, 1, 256, 9), ("f32", 4, 1, 64, 5)])
-@pytest.mark.parametrize("splits", [9, 20, 256])
-def test_more_chunks_than_a_cluster_joins(kv, heads, kvh, dim, rows, splits):
+@pytest.mark.parametrize("splits", [9, 16, 20, 256])
+def test_many_chunks_joined_and_merged(kv, heads, kvh, dim, rows, splits):
     """Partials through the workspace; most chunks hold two tiles, many none."""
     case = make(kv, heads, kvh, dim, [2900, 100, 1500], [rows, 1, rows], paged=True, seed=splits + rows)
     c = poison_unseen(case, 2600, 30)
