@@ -372,6 +372,13 @@ __device__ __forceinline__ unsigned long long cut_times(const Cut& k, float g) {
   return sh >= 0 ? (sh < 64 ? m >> sh : 0ull) : m << -sh;
 }
 
+// The two halves of a cluster barrier.  Another CTA's shared memory may be
+// touched only once that CTA has started, which being scheduled together does
+// not promise: every thread says so at its start, and waits for the others'
+// behind what it would wait for anyway.
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_met() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 constexpr int kMaxRej = kMaxTreeRows;  // rejected siblings of one node
 
 struct WalkShared {
@@ -506,6 +513,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
   extern __shared__ __align__(16) uint32_t dynamic[];
   __shared__ WalkShared sh;
   asm volatile("griddepcontrol.launch_dependents;");
+  cluster_started();
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank();
   const int s = blockIdx.x / kCluster;
@@ -516,6 +524,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
     sh.pow2.f[i / 32][lane] = (float)kPow2Fix[i / 32];
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  cluster_met();  // (ahead of every return)
   const int kind = accept_kind(p, s);
   const float temp = accept_temperature(p, s);
   const bool greedy = temp == 0.f;
