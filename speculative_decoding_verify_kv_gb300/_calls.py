@@ -8,7 +8,11 @@ it launches on the current stream (or the one given) and returns the output
 tensors, which the next call of the same object overwrites.  The functions
 of the C names bind and call in one go.  Two calls that may overlap in time
 need two objects (the workspace is the object's).  A stream given to a call
-is recorded with its tensors (they may be dropped before it gets there); one
+is recorded with its tensors (they may be dropped before it gets there).  It
+also waits for the earlier work of the stream that the object's own buffers
+were allocated on, whose memory they may be; a function of a C name
+allocates them on the stream that it is given.  A stream that captures waits
+for captured work only: what the replay runs behind is the caller's.  One
 made current follows the rules of any PyTorch operation.
 """
 from __future__ import annotations
@@ -48,12 +52,52 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _stream_of(handle, device):
+    """A stream object of a raw handle (0: the default stream)."""
+    return torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+
+
+def _capturing(stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _in_one_go(cls, stream, *args, **kw):
+    """Bind a call and make it.  What it allocates belongs to the stream that
+    it runs on (memory of another one may still be in use by that one's work),
+    and the outputs are read on the stream that is current here."""
+    if stream is None:
+        return cls(*args, **kw)()
+    with torch.cuda.stream(stream):
+        call = cls(*args, **kw)
+    out = call(stream)
+    for t in _flat(out):
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return out
+
+
+def _flat(*todo):
+    """The tensors of nested tuples, lists and dicts."""
+    found, todo = [], list(todo)
+    while todo:
+        x = todo.pop()
+        if isinstance(x, torch.Tensor):
+            found.append(x)
+        elif isinstance(x, (tuple, list)):
+            todo.extend(x)
+        elif isinstance(x, dict):
+            todo.extend(x.values())
+    return found
+
+
 class _Call:
     """Arguments of one entry point, bound.  Subclasses fill ``_fn``,
     ``_args`` (all but the stream), ``_out``, ``_keep`` (every tensor whose
     address is bound) and ``device``."""
     _where = ""
     _own = ()  # buffers that the call allocated itself
+    _home = None  # handle of the stream that they were allocated on
+    _ordered = frozenset()  # handles of the streams that have waited for it
 
     def __call__(self, stream=None):
         dev = self.device
@@ -65,29 +109,31 @@ class _Call:
         if stream is None:
             st = self._fn(*self._args, _current_stream(index))
         else:
+            self._order(stream)
             st = self._fn(*self._args, stream.cuda_stream)
-            for t in self._tensors():  # may be freed with the call, before the stream gets to it
+            for t in _flat(self._keep, self._own, self._out):  # may be freed with the call, before the stream gets to it
                 t.record_stream(stream)
         if st:
             raise VaError(st, self._where)
         return self._out
 
-    def _tensors(self):
-        """Every tensor that a launch reads or writes."""
-        found, todo = [], [self._keep, self._own, self._out]
-        while todo:
-            x = todo.pop()
-            if isinstance(x, torch.Tensor):
-                found.append(x)
-            elif isinstance(x, (tuple, list)):
-                todo.extend(x)
-            elif isinstance(x, dict):
-                todo.extend(x.values())
-        return found
+    def _order(self, stream):
+        """Once per stream: what ran on the memory of the call's own buffers
+        before they were allocated comes before what this stream does there."""
+        if self._home is None or stream.cuda_stream == self._home or stream.cuda_stream in self._ordered:
+            return
+        home = _stream_of(self._home, self.device)
+        if _capturing(stream) != _capturing(home):
+            return
+        stream.wait_stream(home)
+        if not _capturing(stream):
+            self._ordered |= {stream.cuda_stream}
 
     def _new(self, shape, dtype):
         t = torch.empty(shape, dtype=dtype, device=self.device)
         self._own += (t,)
+        if self._home is None and t.is_cuda:
+            self._home = _current_stream(t.device.index)
         return t
 
     def _buffer(self, name, t, shape, dtype):
@@ -176,7 +222,7 @@ class WindowCall(_Call):
 def verify_attn_window(p: Problem, kv: KV, mode: int, window: Window, *, stream=None, **kw):
     """Verify attention through a sliding window with a few first tokens that
     stay visible; returns (o, lse)."""
-    return WindowCall(p, kv, mode, window, **kw)(stream)
+    return _in_one_go(WindowCall, stream, p, kv, mode, window, **kw)
 
 
 def window_splits(p: Problem, kv: KV, window: Window) -> int:
@@ -248,7 +294,7 @@ class AcceptCall(_Call):
 def verify_attn_accept(p: Problem, draft: Draft, mode: int, *, stream=None, **kw):
     """Which drafted rows the target accepts, and the next token of each
     sequence (see verify_attn_accept in the header)."""
-    return AcceptCall(p, draft, mode, **kw)(stream)
+    return _in_one_go(AcceptCall, stream, p, draft, mode, **kw)
 
 
 @dataclass
@@ -356,20 +402,20 @@ class PageCopyCall(_Call):
 def verify_attn_pages_fork(pool: PagePool, src, dst, length, pages, *, stream=None, **kw):
     """Fork and grow sequences of a paged cache; returns (copies, num_copies)
     for verify_attn_pages_copy."""
-    return ForkCall(pool, src, dst, length, pages, **kw)(stream)
+    return _in_one_go(ForkCall, stream, pool, src, dst, length, pages, **kw)
 
 
 def verify_attn_pages_free(pool: PagePool, seq, first, last, *, status=None, stream=None):
     """Give back table entries first[i] .. last[i] - 1 of sequence seq[i]."""
-    return FreeCall(pool, seq, first, last, status=status)(stream)
+    return _in_one_go(FreeCall, stream, pool, seq, first, last, status=status)
 
 
 def verify_attn_pages_compact(pool: PagePool, *, stream=None, **kw):
     """Pull the pages in use together at the front of the pool; returns
     (copies, num_copies, live_blocks)."""
-    return CompactCall(pool, **kw)(stream)
+    return _in_one_go(CompactCall, stream, pool, **kw)
 
 
 def verify_attn_pages_copy(pools, copies, num_copies, *, status=None, stream: Optional[object] = None):
     """Copy the page pairs in every pool."""
-    return PageCopyCall(pools, copies, num_copies, status=status)(stream)
+    return _in_one_go(PageCopyCall, stream, pools, copies, num_copies, status=status)
