@@ -187,6 +187,23 @@ def _stream_handle(stream) -> Optional[int]:
     return int(stream.cuda_stream) or None
 
 
+def _on(stream):
+    """Makes a given stream current for what a call allocates: memory of
+    another one may still be in use by that one's work."""
+    import contextlib
+
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _seen_here(stream, *tensors):
+    """Outputs that were allocated on a given stream are read on the caller's."""
+    if stream is not None:
+        import torch
+        for t in tensors:
+            t.record_stream(torch.cuda.current_stream(t.device))
+
+
 @dataclass
 class KV:
     """Device KV cache (contiguous or paged).  ``k``/``v`` are uint8, uint16
@@ -264,12 +281,18 @@ def _call(fname: str, p: Problem, kv: KV, ws=None, o=None, lse=None, status=None
     import torch
     dev = p.q.device
     D = kv.head_dim
-    if o is None:
-        o = torch.empty((p.total_rows, p.num_heads, D), dtype=torch.float32, device=dev)
-    if lse is None:
-        lse = torch.empty((p.total_rows, p.num_heads), dtype=torch.float32, device=dev)
-    if ws is None:
-        ws = alloc_workspace(p, kv, dev)
+    if o is None or lse is None or ws is None:
+        made = []
+        with _on(stream):
+            if o is None:
+                o = torch.empty((p.total_rows, p.num_heads, D), dtype=torch.float32, device=dev)
+                made.append(o)
+            if lse is None:
+                lse = torch.empty((p.total_rows, p.num_heads), dtype=torch.float32, device=dev)
+                made.append(lse)
+            if ws is None:
+                ws = alloc_workspace(p, kv, dev)
+        _seen_here(stream, *made)
     pc, kc = p.c(), kv.c()
     st = getattr(lib, fname)(ctypes.byref(pc), ctypes.byref(kc), _ptr(ws),
                              ws.numel() * ws.element_size(), _ptr(o), _ptr(lse), _ptr(status),
@@ -332,8 +355,10 @@ def verify_attn_promote(p: Problem, kv: KV, mode: int, accepted_len, accepted_no
 def debug_row_map(p: Problem, mode: int, status=None, stream=None):
     import torch
     dev = p.cu_rows.device
-    row_seq = torch.full((max(p.total_rows, 1),), -1, dtype=torch.int32, device=dev)
-    anc = torch.zeros((max(p.total_rows, 1),), dtype=torch.int32, device=dev)
+    with _on(stream):
+        row_seq = torch.full((max(p.total_rows, 1),), -1, dtype=torch.int32, device=dev)
+        anc = torch.zeros((max(p.total_rows, 1),), dtype=torch.int32, device=dev)
+    _seen_here(stream, row_seq, anc)
     st = lib.va_debug_row_map(ctypes.byref(p.c()), mode, _ptr(row_seq), _ptr(anc),
                               _ptr(status), _stream_handle(stream))
     if st:
@@ -344,7 +369,9 @@ def debug_row_map(p: Problem, mode: int, status=None, stream=None):
 def debug_gather_index(p: Problem, kv: KV, kv_head: int, max_len: int, status=None,
                        stream=None):
     import torch
-    out = torch.empty((p.num_seqs, max_len), dtype=torch.int64, device=p.cu_rows.device)
+    with _on(stream):
+        out = torch.empty((p.num_seqs, max_len), dtype=torch.int64, device=p.cu_rows.device)
+    _seen_here(stream, out)
     st = lib.va_debug_gather_index(ctypes.byref(p.c()), ctypes.byref(kv.c()), kv_head,
                                    max_len, _ptr(out), _ptr(status), _stream_handle(stream))
     if st:
@@ -357,7 +384,9 @@ def debug_split_ranges(p: Problem, kv: KV, mode: int = MODE_CHAIN, status=None, 
     tensor [num_seqs][slots][2] of (lo, hi) positions."""
     import torch
     slots = plan(p, kv, mode)["slots"]
-    out = torch.full((max(p.num_seqs, 1), slots, 2), -2, dtype=torch.int32, device=p.cu_rows.device)
+    with _on(stream):
+        out = torch.full((max(p.num_seqs, 1), slots, 2), -2, dtype=torch.int32, device=p.cu_rows.device)
+    _seen_here(stream, out)
     st = lib.va_debug_split_ranges(ctypes.byref(p.c()), ctypes.byref(kv.c()), mode, _ptr(out),
                                    _ptr(status), _stream_handle(stream))
     if st:

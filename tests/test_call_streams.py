@@ -103,3 +103,40 @@ def test_a_call_with_all_buffers_given_waits_for_nothing(world):
     side = Stream(9)
     call._order(side)
     assert side.waited == [] and world.allocated == []
+
+
+class Library:
+    """Every entry point succeeds; the split plan has one slot."""
+    def __getattr__(self, name):
+        def call(*args):
+            if name == "va_plan":
+                args[3]._obj.slots = 1
+            return 1000 if name == "va_workspace_size" else 0
+        return call
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_verify_calls_allocate_on_their_stream(world, monkeypatch, given):
+    """The unwindowed calls and the debug exports."""
+    _, (p, kv, _, _), _ = arguments()["window"]
+    side = Stream(9)
+    made = []
+    for name in ("empty", "full", "zeros"):
+        real = getattr(torch, name)
+        monkeypatch.setattr(torch, name, lambda *a, real=real, **k: made.append(world.now.cuda_stream) or real(*a, **k))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: made.append(("seen by", s.cuda_stream)))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: world.now)
+    monkeypatch.setattr(va, "lib", Library())
+    monkeypatch.setattr(va, "_stream_handle", lambda s: None)
+    kw = {"stream": side} if given else {}
+    at = 9 if given else 7
+    for call, buffers, outputs in ((lambda: va.verify_attn_chain(p, kv, **kw), 3, 2), (lambda: va.debug_row_map(p, 0, **kw), 2, 2),
+                                   (lambda: va.debug_gather_index(p, kv, 0, 10, **kw), 1, 1),
+                                   (lambda: va.debug_split_ranges(p, kv, 0, **kw), 1, 1)):
+        made.clear()
+        call()
+        assert made == [at] * buffers + ([("seen by", 7)] * outputs if given else [])
+    o, lse, ws = z(3, 4, 64), z(3, 4), z(1000)
+    made.clear()
+    va.verify_attn_chain(p, kv, o=o, lse=lse, ws=ws, **kw)
+    assert made == []

@@ -155,3 +155,21 @@ def test_a_stream_that_captures(make):
     torch.cuda.synchronize()
     right(first)
     right(second)
+
+
+def test_an_unwindowed_call_does_not_write_into_another_streams_memory():
+    import oracle
+    case = sy.mixed_tree_direct(ctx=[40, 300, 17, 130], direct=(0, 2), num_splits=2, seed=7)
+    p, kv, mode = va.upload(case, "cuda")
+    ref = oracle.verify_case(case)
+    side = torch.cuda.Stream()
+    ws = va.alloc_workspace(p, kv)
+    out = va.verify_attn(p, kv, mode, ws=ws)
+    check_window(case, out[0].cpu().numpy(), out[1].cpu().numpy(), ref, False)
+    lengths = [t.numel() * t.element_size() for t in (ws, *out)]
+    del ws, out
+    busy = busy_blocks(lengths)
+    out = va.verify_attn(p, kv, mode, stream=side)
+    assert not {t.data_ptr() for t in out} & busy
+    torch.cuda.synchronize()
+    check_window(case, out[0].cpu().numpy(), out[1].cpu().numpy(), ref, False)
