@@ -33,7 +33,8 @@
 // weights of the last row are therefore 64-bit fixed-point numbers
 // (2^39 exp(z - max) up to a vocabulary of 2^19, relative error about 2^-32)
 // summed as integers: no order of summation changes the result, and borders
-// move by about 1e-10.
+// move by about 1e-10 (over the share of the mass that is left, after
+// rejections with drafted probabilities).
 #include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
@@ -348,28 +349,18 @@ __device__ __forceinline__ unsigned long long fixed_weight(const Weights& w, con
   return y > -32.f ? (u + 1) >> 1 : 0ull;  // below 2^-46 of the maximum: 0
 }
 
-// c g for a probability g (NaN and negative count as 0, above 1 as 1), to 31
-// significant bits of c: c = c31 * 2^cs, g = m * 2^(e - 150).
-struct Cut {
-  uint32_t c31;
-  int shift;  // 150 - cs
-};
-
-__device__ __forceinline__ Cut make_cut(unsigned long long c) {
-  Cut k;
-  const int cs = max(33 - __clzll((long long)c), 0);
-  k.c31 = (uint32_t)(c >> cs);
-  k.shift = 150 - cs;
-  return k;
-}
-
-__device__ __forceinline__ unsigned long long cut_times(const Cut& k, float g) {
+// c g, rounded, for c < 2^63 and a probability g (NaN and negative count as 0,
+// above 1 as 1).  All of c enters the product: what a rejection leaves is a
+// difference of nearly equal numbers, which an error of the cut alone would
+// move by so much over the mass that is left (c cut to 31 bits: 4e-10 over it).
+__device__ __forceinline__ unsigned long long cut_times(unsigned long long c, float g) {
   const uint32_t b = __float_as_uint(fminf(fmaxf(g, 0.f), 1.f));
-  const unsigned long long m = (unsigned long long)k.c31 * ((b & 0x7FFFFFu) | 0x800000u);  // < 2^55
-  const int sh = k.shift - (int)(b >> 23);
-  // Below 0: at most 9 more bits (c up to 2^63).  A subnormal g counts double
-  // at most and is shifted out.
-  return sh >= 0 ? (sh < 64 ? m >> sh : 0ull) : m << -sh;
+  const uint32_t m = b << 8 | 0x80000000u;  // g = m 2^-32 2^(e - 126); (subnormals are shifted out)
+  const unsigned long long t = (unsigned long long)(uint32_t)(c >> 32) * m + __umulhi((uint32_t)c, m);
+  const int sh = 126 - (int)(b >> 23);
+  unsigned long long u;
+  asm("shr.u64 %0, %1, %2;" : "=l"(u) : "l"(t + t), "r"(sh));  // 0 for more than 63
+  return sh < 0 ? c : (u + 1) >> 1;  // (sh < 0: g = 1)
 }
 
 // The two halves of a cluster barrier.  Another CTA's shared memory may be
@@ -481,12 +472,12 @@ __device__ __noinline__ unsigned long long fill_unit(const WalkShared& sh, const
 // before it; a weight that reached 0 stays there, so after several of them it
 // is max(v - (c_0 + c_1 + ..) g, 0).
 __device__ __noinline__ unsigned long long sum_unit(const Unit* src, const float* guess, int vocab, int i,
-                                                    const Cut cut) {
+                                                    const unsigned long long cut) {
   const int lane = threadIdx.x & 31;
   unsigned long long sum = 0ull;
   float g[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) g[e] = cut.c31 && i + 32 * e < vocab ? guess[i + 32 * e] : 0.f;
+  for (int e = 0; e < 8; ++e) g[e] = cut && i + 32 * e < vocab ? guess[i + 32 * e] : 0.f;
   const uint32_t hi[2] = {src->hi[0][lane], src->hi[1][lane]};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -654,7 +645,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
   // The sum of this lane's weights of unit k after the rejections; the
   // weights are in the table then.  Proposals without probabilities: a
   // rejected token weighs 0 there.
-  Cut cut = {0u, 0};
+  unsigned long long cut = 0ull;
   auto unit_left = [&](int k, int nrej) {
     Unit* at = mine + (p.cached ? k : 0);
     const int i = lo + k * kUnit + lane;
@@ -669,7 +660,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
         }
         __syncwarp();
       }
-      if (cut.c31 == 0u) return sum;
+      if (cut == 0ull) return sum;
     }
     return sum_unit(at, guess, p.vocab, i, cut);
   };
@@ -714,7 +705,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
         } else {
           const float z = to_float<T>(logits[(long long)(row0 + node) * p.logits_stride + x]);
           const unsigned long long v = fixed_weight<T>(w, sh.pow2, lane, z);
-          const unsigned long long c = cut_times(make_cut(sh.cut[nrej]), qj);
+          const unsigned long long c = cut_times(sh.cut[nrej], qj);
           yes = (double)u * (double)qj * (double)sh.scale[nrej] < (double)(v > c ? v - c : 0ull);
           lost = !yes;
         }
@@ -800,7 +791,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
 #pragma unroll 1
     for (int k = p.probs ? min(have + 1, nrej) : nrej;;) {
       unsigned long long v = 0ull;
-      cut = make_cut(p.probs ? sh.cut[k] : 0ull);
+      cut = p.probs ? sh.cut[k] : 0ull;
 #pragma unroll 1
       for (int t = 0; t < units; ++t) v += unit_left(t, k);
       filled = p.cached;
@@ -876,7 +867,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
         const Unit* at = mine + (p.cached ? k : 0);
 #pragma unroll 1
         for (int i = lo + k * kUnit + lane, e = 0; e < kUnit / 32; ++e, i += 32) {
-          const unsigned long long c = cut.c31 && i < p.vocab ? cut_times(cut, guess[i]) : 0ull;
+          const unsigned long long c = cut && i < p.vocab ? cut_times(cut, guess[i]) : 0ull;
           const unsigned long long w = at->get(lane + 32 * e), x = w > c ? w - c : 0ull;
           const unsigned long long sum = warp_sum(x);
           if (t - base < sum) {
