@@ -29,20 +29,23 @@ def target(row, temperature: float):
     return w / w.sum()
 
 
-def accept_sequence(logits, probs, tokens, parent, u, v, temperature: float):
+def accept_decisions(logits, probs, tokens, parent, u, v, temperature: float):
     """One sequence: rows of logits [n][V], drafted probabilities by parent
     row (or None), tokens, parents (parent[0] = -1), numbers u [n] and v.
-    Returns (path, next token or -1, margin): margin is the smallest relative
-    distance of any decision from its border, so that a caller can tell a
-    close call from a wrong one."""
+    Returns (path, next token or -1, tests, draw): tests holds for each child
+    that was tried its relative distance |u g - r| / max(u g, r) from the
+    border, how many of its siblings were rejected before it, and the share of
+    p's mass that they left; draw is the distance of v from the nearest border
+    of the running sums (inf where nothing was drawn) and the share of p's mass
+    that they run over."""
     n = len(tokens)
-    node, path, margin = 0, [0], np.inf
+    node, path, tests = 0, [0], []
     while True:
         p = target(logits[node], temperature)
         if p is None:
-            return path, -1, margin
+            return path, -1, tests, (np.inf, 1.0)
         r = p.copy()
-        taken = None
+        taken, before, left = None, 0, 1.0
         for j in range(1, n):
             if parent[j] != node:
                 continue
@@ -56,17 +59,21 @@ def accept_sequence(logits, probs, tokens, parent, u, v, temperature: float):
                 np.asarray(probs[node], np.float64)), 0.0, 1.0)
             if probs is None:
                 g[x] = 1.0
-            left, right = float(u[j]) * g[x], r[x]
-            if max(left, right) > 0:
-                margin = min(margin, abs(left - right) / max(left, right))
-            if left < right:
+            proposed, wanted = float(u[j]) * g[x], r[x]
+            if max(proposed, wanted) > 0:
+                tests.append((abs(proposed - wanted) / max(proposed, wanted), before, left))
+            if proposed < wanted:
                 taken = j
                 break
             if probs is None:
                 r[x] = 0.0
             else:
                 r = np.maximum(r - g, 0.0)
-            r = r / r.sum() if r.sum() > 0 else p.copy()
+            before, left = before + 1, left * r.sum()
+            if r.sum() > 0:
+                r = r / r.sum()
+            else:
+                r, left = p.copy(), 1.0
         if taken is None:
             break
         node = taken
@@ -74,8 +81,15 @@ def accept_sequence(logits, probs, tokens, parent, u, v, temperature: float):
     c = np.cumsum(r)
     border = float(v) * c[-1]
     token = int(np.argmax(c > border))
-    margin = min(margin, float(np.abs(c - border).min())) if temperature else margin
-    return path, token, margin
+    return path, token, tests, (float(np.abs(c - border).min()) if temperature else np.inf, left)
+
+
+def accept_sequence(logits, probs, tokens, parent, u, v, temperature: float):
+    """(path, next token or -1, margin): margin is the smallest relative
+    distance of any decision from its border, so that a caller can tell a
+    close call from a wrong one."""
+    path, token, tests, draw = accept_decisions(logits, probs, tokens, parent, u, v, temperature)
+    return path, token, min([draw[0]] + [t[0] for t in tests])
 
 
 def accept(logits, probs, tokens, parent, kinds, cu_rows, u, v, temperature):
