@@ -118,25 +118,6 @@ __device__ __forceinline__ float accept_temperature(const AcceptParams& p, int s
   return p.temperature ? p.temperature[s] : 1.f;
 }
 
-// a b + c and a + b of two values at once.
-__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) {
-  unsigned long long x, y, z, d;
-  memcpy(&x, &a, 8);
-  memcpy(&y, &b, 8);
-  memcpy(&z, &c, 8);
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
-  memcpy(&a, &d, 8);
-  return a;
-}
-__device__ __forceinline__ float2 add_pair(float2 a, float2 b) {
-  unsigned long long x, y, d;
-  memcpy(&x, &a, 8);
-  memcpy(&y, &b, 8);
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-  memcpy(&a, &d, 8);
-  return a;
-}
-
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -173,33 +154,6 @@ struct RowStep {
         w[k] = make_uint4(c[0], c[1], c[2], c[3]);
       }
     }
-  }
-  // Values 2 e and 2 e + 1 of vector k, one register each.
-  __device__ __forceinline__ float2 pair(int k, int e) const {
-    const uint32_t c[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-    if (sizeof(T) == 4) return make_float2(__uint_as_float(c[(2 * e) & 3]), __uint_as_float(c[(2 * e + 1) & 3]));
-    return make_float2(__uint_as_float(c[e] << 16), __uint_as_float(c[e] & 0xFFFF0000u));
-  }
-  // The largest value (a NaN counts as none).
-  __device__ __forceinline__ float largest() const {
-    if (sizeof(T) == 4) {
-      float m = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) m = fmaxf(m, fmaxf(pair(k, e).x, pair(k, e).y));
-      return m;
-    }
-    __nv_bfloat162 m = bf16_pair(w[0].x);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      m = __hmax2(m, __hmax2(__hmax2(bf16_pair(w[k].x), bf16_pair(w[k].y)), __hmax2(bf16_pair(w[k].z), bf16_pair(w[k].w))));
-    return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
-  }
-  static __device__ __forceinline__ __nv_bfloat162 bf16_pair(uint32_t u) {
-    __nv_bfloat162 b;
-    memcpy(&b, &u, 4);
-    return b;
   }
   // Value e of vector k.
   __device__ __forceinline__ float at(int k, int e) const {
