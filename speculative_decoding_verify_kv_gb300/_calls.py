@@ -46,6 +46,13 @@ def _tensor(name, t, dtype, numel, device=None, optional=False):
     return t
 
 
+def _i32(name, x):
+    """A number for a 32-bit field: ctypes would cut it to that silently."""
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
+
+
 # The current stream's handle without a Stream object around it (2.9 us of
 # the 7 that a bound call took on the host).
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -164,7 +171,7 @@ class Window:
     o_dtype: int = F32
 
     def c(self) -> VaWindow:
-        return VaWindow(self.window, self.sinks, self.o_dtype)
+        return VaWindow(_i32("window", self.window), _i32("sinks", self.sinks), self.o_dtype)
 
 
 _ELEMENT = {F32: 4, BF16: 2}
@@ -245,7 +252,7 @@ class Draft:
     temperature: object = None      # float32 [num_seqs]
 
     def c(self) -> VaDraft:
-        return VaDraft(self.vocab, self.logits_dtype, _ptr(self.logits), self.logits_stride or self.vocab,
+        return VaDraft(_i32("vocab", self.vocab), self.logits_dtype, _ptr(self.logits), self.logits_stride or self.vocab,
                        _ptr(self.draft_probs), self.draft_stride or self.vocab, _ptr(self.tokens),
                        _ptr(self.accept_u), _ptr(self.sample_u), _ptr(self.temperature))
 
@@ -306,7 +313,8 @@ class PagePool:
 
     def c(self) -> VaPagePool:
         t = self.block_table
-        return VaPagePool(t.shape[0], t.shape[1], self.ref_count.numel(), _ptr(t), _ptr(self.ref_count))
+        return VaPagePool(_i32("block_table", t.shape[0]), _i32("block_table", t.shape[1]),
+                          _i32("ref_count", self.ref_count.numel()), _ptr(t), _ptr(self.ref_count))
 
 
 class _PageCall(_Call):
@@ -325,7 +333,7 @@ class _PageCall(_Call):
             _tensor(name, t, torch.int32, 0, self.device)
             if n is not None and t.numel() != n:
                 raise ValueError(f"{name}: {t.numel()} commands, the others have {n}")
-            n = t.numel()
+            n = _i32(name, t.numel())
         return n
 
 
@@ -394,8 +402,8 @@ class PageCopyCall(_Call):
         _tensor("status", status, torch.int32, 1, dev, optional=True)
         ptrs = (ctypes.c_void_p * len(pools))(*[_ptr(t) for t in pools])
         self._fn, self._out = lib.verify_attn_pages_copy, None
-        self._args = (ptrs, len(pools), bytes_of(pools[0]) // blocks, blocks, _ptr(copies), _ptr(num_copies),
-                      copies.numel() // 2, _ptr(status))
+        self._args = (ptrs, len(pools), bytes_of(pools[0]) // blocks, _i32("pools", blocks), _ptr(copies),
+                      _ptr(num_copies), _i32("copies", copies.numel() // 2), _ptr(status))
         self._keep = (tuple(pools), copies, num_copies, status)
 
 
