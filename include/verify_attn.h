@@ -304,8 +304,9 @@ va_status va_plan(const va_problem *p, const va_kv *kv, int32_t mode, va_plan_in
 
 /*
  * Optional per-kernel timing for benchmarks.  While enabled (on != 0),
- * every verify call records CUDA events on its stream before the partial
- * kernel, between the partial and merge kernels, and after the merge;
+ * every verify_attn_chain, _tree and _mixed call records CUDA events on its
+ * stream before the partial kernel, between the partial and merge kernels, and
+ * after the merge;
  * enabling restarts at slot 0 (at most 4096 calls are kept).  Inside a
  * stream capture the records become event nodes of the graph, so a replay
  * refreshes them.  va_timing_read waits for the recorded events and writes
@@ -376,13 +377,26 @@ va_status verify_attn_noalloc(const va_problem *p, const va_kv *kv, int32_t mode
  *     visible tokens are cut into (whole 64-token tiles, at least 128
  *     tokens).  About c SMs / (num_seqs * num_kv_heads) chunks fill the GPU
  *     once (va_window_splits): c CTAs run on an SM, 2 where a KV head has at
- *     most 16 query rows and else 1.  A KV head with more query rows than a
- *     block of its kernel (128, 16 for fp32 caches) gets fewer, in all about as
- *     many CTAs.  With o_dtype VA_F32 more may be made, so that none holds more
- *     than 2,048 tokens: over more, the tensor cores' running sums drift
- *     visibly.  No choice depends on the other sequences of the
- *     launch: kernel and chunks follow from the types, from num_splits and
- *     max_rows_per_seq as given, and from the sequence itself.
+ *     most 16 query rows and else 1.  Where a KV head's query rows make b > 1
+ *     blocks of its kernel (of 128 rows; of 16 on the CUDA cores: fp32 caches,
+ *     bf16 ones with a scratch KV, VA_FLAG_CUDA_CORES), each block takes
+ *     num_splits / b chunks, rounded down, and at least m: m is 1, or on the
+ *     CUDA cores a chunk per 256 tokens of window and sinks, at most
+ *     num_splits (their calls with many rows may so make up to b num_splits
+ *     CTAs per sequence and KV head, and num_splits partials of each row).
+ *     On the 128-row kernel o_dtype VA_F32 raises num_splits and m to a
+ *     chunk per 2,048 tokens, to at most 256 chunks: over more tokens the
+ *     tensor cores' running sums drift visibly.  No choice depends on the other
+ *     sequences of the launch: kernel and chunks follow from the types, from
+ *     num_splits and max_rows_per_seq as given, and from the sequence itself.
+ *   - How exactly O is summed follows from the cache and the kernel; lse is
+ *     summed in fp32 by all.  On the CUDA cores: fp32 products and sums.  bf16
+ *     caches: probabilities enter the products in 16 bits (2.5e-6 of O), or, for
+ *     o_dtype VA_F32 and up to 16 query rows per KV head (48 at head_dim 64, 32
+ *     at 128), in 24.  Q8_0 caches, as in the unwindowed calls and whatever
+ *     o_dtype is: K exactly, probabilities and V elements rounded to fp16 (2^-11
+ *     each), about 3e-4 of O.  fp32 sums of Q8_0 values are had with
+ *     VA_FLAG_CUDA_CORES.
  *   - Rows that no sequence covers stay as they were.  Where row offsets
  *     overlap (VA_DEV_BAD_ROWS), a row claimed twice holds either result.
  *   - o: [total_rows][num_heads][head_dim] of o_dtype (VA_F32, or VA_BF16:
@@ -439,6 +453,12 @@ va_status verify_attn_window(const va_problem *p, const va_kv *kv, int32_t mode,
  *   promote_len[s] (may be NULL): accepted_len[s] for a tree, 0 for a chain,
  *     as verify_attn_promote takes it;
  *   next_token[s].
+ * The first child of a node, and without draft_probs every child, is tested
+ * in fp32: p(x) to about 1e-5 of itself, and the mass that the rejected
+ * siblings took is a sum of such numbers, so that what they left is known to
+ * about 1e-7 of p's mass.  Later children with draft_probs, and the draw,
+ * use fixed-point weights: its borders are off by about 1e-10 over the share of
+ * p's mass that the rejections left.
  * Outputs of rows that no sequence covers stay as they were.  A sequence of
  * no rows gets accepted_len 0 and next_token -1.
  * Masked vocabulary entries are -inf.  A row whose logits hold NaN, +inf or
@@ -559,7 +579,8 @@ va_status verify_attn_pages_compact(const va_page_pool *pool, int32_t *copies, i
  * pair's source or target.  Nothing is copied when *status holds a finding of
  * an earlier call other than VA_DEV_BAD_COPY; a pair outside the pool is
  * passed over and sets VA_DEV_BAD_COPY, as does *num_copies > max_copies
- * (the first max_copies pairs are copied).
+ * (the first max_copies pairs are copied).  With num_pools or max_copies 0
+ * nothing is launched, and so no status set.
  */
 va_status verify_attn_pages_copy(void *const *pools, int32_t num_pools, int64_t page_bytes,
                                  int32_t num_blocks, const int32_t *copies,

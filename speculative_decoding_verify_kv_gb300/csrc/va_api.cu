@@ -496,7 +496,7 @@ static va_status check_window(const va_problem* p, const va_kv* kv, int mode, co
 }
 
 // num_splits is the chunk count of a one-row-block sequence; a sequence of
-// b row blocks takes max(1, num_splits / b) chunks.
+// b row blocks takes max(min_splits, num_splits / b) chunks.
 static Plan window_plan(const va_problem* p, const va_kv* kv, const va_window* w) {
   Plan pl = make_plan(p, kv);
   if (pl.kernel == VA_KERNEL_TENSOR_Q8) {  // the row-major kernel reads contiguous caches by pages here
@@ -515,7 +515,8 @@ static Plan window_plan(const va_problem* p, const va_kv* kv, const va_window* w
   if (pl.kernel == VA_KERNEL_TENSOR && !pl.small && w->o_dtype == VA_F32) {
     // The tensor cores round their fp32 sums towards zero at every step: O
     // drifts by some 1e-5 of itself over 4,096 tokens.  Where O is returned in
-    // fp32 a chunk holds at most 2,048.
+    // fp32 a chunk holds at most 2,048 (up to the 256 chunks there may be: a
+    // window of 524,288).
     const long long cap = kv->page_size ? (long long)kv->max_blocks_per_seq * kPage : (long long)kv->capacity;
     long long most = (long long)w->window + w->sinks + p->max_rows_per_seq + 4 * kPage;
     if (most > cap + p->max_rows_per_seq) most = cap + p->max_rows_per_seq;
@@ -526,7 +527,9 @@ static Plan window_plan(const va_problem* p, const va_kv* kv, const va_window* w
   }
   if (pl.kernel == VA_KERNEL_CUDA_CORES) {
     // Row blocks of 16: a chunk per 256 tokens of the window stays to each of
-    // them (two blocks of 600 tokens in one chunk each: 47 us, in three: 23).
+    // them (two blocks of 600 tokens in one chunk each: 47 us, in three: 23), of
+    // the num_splits asked for.  Calls whose row blocks fill the GPU by
+    // themselves gain nothing from more than one: the caller's to choose.
     const long long most = ((long long)w->window + w->sinks + 255) / 256;
     pl.min_splits = (int)(most < pl.slots ? most : pl.slots);
   }

@@ -10,9 +10,12 @@
 // cores round their running sum towards zero, which over the pages of a
 // long window is a drift of 2^-24 each (1e-5 after 4,096 tokens, measured).
 //
-// bf16: P enters as bf16 hi + lo (16 bits), and a third part where O is fp32.  Q8_0: the codes enter the MMAs as
-// exact fp16 integers, K's scales multiply the fp32 sums of each 32-element
-// block, V's elements become fp16(d q) (one rounding) and P is fp16.
+// bf16: P enters as bf16 hi + lo (16 bits), and a third part where O is fp32.
+// Q8_0: the codes enter the MMAs as exact fp16 integers, K's scales multiply the
+// fp32 sums of each 32-element block, V's elements become fp16(d q) (one
+// rounding) and P is fp16, in fp32 outputs too: some 3e-4 of O, what the
+// framework's other kernels over Q8_0 give.  (Each rounding alone moves O by
+// 2.0e-4; bf16 outputs round it by 1.7e-3 anyway, of which they make 1.70e-3.)
 #pragma once
 
 #include <string.h>
