@@ -58,8 +58,8 @@ constexpr int kMaxVocab = 1 << 20;
 // Dynamic shared memory of the walk on an SM: of one CTA of 1,024 threads or of
 // two of 512.  It holds the weights of a row's part so that a pass after a
 // rejection does not make them again; in five bytes a cluster of 8 with 512
-// threads holds 163,000 (32 chains over 131,072 values: 56 us when it was built, and 68
-// when eight-byte weights did not fit and were made again).
+// threads holds 163,000 (32 chains over 131,072 values took 68 us when
+// eight-byte weights did not fit and were made again, 56 with these).
 constexpr int kWalkBytes = 206 * 1024;
 constexpr int kWeightBytes = 5;      // of a weight kept in shared memory
 constexpr int kRowBytes = 28;        // of a row's test
@@ -446,7 +446,7 @@ __device__ __noinline__ unsigned long long sum_unit(const Unit* src, const float
 // from the same numbers, so the cluster's barriers always match.  Bound by
 // latency while there are few sequences (one: 11 us; 3 us more for each rejected
 // sibling, a pass over the kept weights and an exchange), then by its
-// instructions: 32 drawn chains over 131,072 values 33 us, issue slots 43 % used;
+// instructions: 32 drawn chains over 131,072 values 35 us, issue slots 43 % used;
 // 0.5 us for every further sequence that is drawn from its logits.  (Clusters of
 // 4, 2 and 1 for more sequences: the same time for those, half of it for greedy
 // ones, a quarter more for chains with drafted probabilities, whose weights
@@ -838,6 +838,8 @@ __global__ void __launch_bounds__(kWalkThreads, 1024 / kWalkThreads) accept_walk
   cluster.sync();  // no CTA leaves while another may still write its tables
 }
 
+// A row may start up to 7 values past a 16-byte boundary (so that a vocabulary of
+// whole pieces has one more, which holds values of such rows only).
 static int accept_pieces(int vocab) { return (vocab + 7 + kPiece - 1) / kPiece; }
 
 static va_status check_accept(const va_problem* p, const va_draft* d, int mode) {

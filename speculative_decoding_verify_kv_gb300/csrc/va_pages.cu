@@ -652,7 +652,7 @@ va_status verify_attn_pages_copy(void* const* pools, int32_t num_pools, int64_t 
     q.copies = copies;
     q.num_copies = num_copies;
     q.status = (unsigned*)status;
-    int per = (152 * 8 + m - 1) / m;
+    int per = (152 * 8 + m - 1) / m;  // eight CTAs to each of the GB300's 152 SMs
     if (per > max_copies) per = max_copies;
     cudaError_t e = launch_pages(pages_copy_kernel, dim3((unsigned)per, (unsigned)m), kCopyThreads, 1, cs, q);
     if (e != cudaSuccess) return note_cuda(e);

@@ -25,7 +25,11 @@ namespace va {
 constexpr int kSimtRows = 16;    // query rows per CTA
 constexpr int kSimtTile = 32;    // tokens per tile
 constexpr int kSimtThreads = 128;
-constexpr int kSimtWinThreads = 256;  // windowed calls: few tiles to a CTA, so more warps at each
+// Windowed calls, whatever their size: eight warps of two rows.  Against four of
+// four rows, when both were measured: 2 sequences of 200 rows, G = 4, D = 64, 19
+// us against 26 (few CTAs, each waiting for its tiles' steps); 800 rows over 8 KV
+// heads at D = 128, where the CTAs fill the GPU, 92 against 81.
+constexpr int kSimtWinThreads = 256;
 
 // Floats from one K row of the tile to the next: the scores are read one
 // value per lane and token, or (WIN) four.

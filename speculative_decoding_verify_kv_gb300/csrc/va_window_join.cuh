@@ -15,7 +15,7 @@ namespace cg = cooperative_groups;
 // Chunks that may be joined in their kernel, as one cluster; otherwise they go
 // through the workspace and the merge kernel.  Both take the same sums in the
 // same order, so that either gives the same bits.  With at most 16 rows per KV
-// head up to 16 (one token, 16 chunks at D = 64: 8.2 us against 12.5 through the
+// head up to 16 (one token, 16 chunks at D = 64: 7.4 us against 12.5 through the
 // merge kernel), with more rows 8, the portable size (96 rows of D = 256 in 16
 // chunks: 29.6 us joined, 26.5 merged).
 constexpr int kJoinFew = 16;
