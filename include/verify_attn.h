@@ -457,8 +457,10 @@ va_status verify_attn_window(const va_problem *p, const va_kv *kv, int32_t mode,
  * in fp32: p(x) to about 1e-5 of itself, and the mass that the rejected
  * siblings took is a sum of such numbers, so that what they left is known to
  * about 1e-7 of p's mass.  Later children with draft_probs, and the draw,
- * use fixed-point weights: its borders are off by about 1e-10 over the share of
- * p's mass that the rejections left.
+ * use fixed-point weights, which resolve 2^-40 of the row's largest p: the
+ * draw's borders are off by about 1e-10 over the share of p's mass that the
+ * rejections left.  A probability below that, or (in fp32) below 2^-126, may
+ * count as 0, so that no number takes its child.
  * Outputs of rows that no sequence covers stay as they were.  A sequence of
  * no rows gets accepted_len 0 and next_token -1.
  * Masked vocabulary entries are -inf.  A row whose logits hold NaN, +inf or

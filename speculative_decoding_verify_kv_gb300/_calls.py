@@ -10,10 +10,11 @@ of the C names bind and call in one go.  Two calls that may overlap in time
 need two objects (the workspace is the object's).  A stream given to a call
 is recorded with its tensors (they may be dropped before it gets there).  It
 also waits for the earlier work of the stream that the object's own buffers
-were allocated on, whose memory they may be; a function of a C name
-allocates them on the stream that it is given.  A stream that captures waits
-for captured work only: what the replay runs behind is the caller's.  One
-made current follows the rules of any PyTorch operation.
+were allocated on (which still has to exist), whose memory they may be; a
+function of a C name allocates them on the stream that it is given.  A
+stream that captures waits for captured work only: what the replay runs
+behind is the caller's.  One made current follows the rules of any PyTorch
+operation.
 """
 from __future__ import annotations
 
