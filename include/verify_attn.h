@@ -589,6 +589,184 @@ va_status verify_attn_pages_copy(void *const *pools, int32_t num_pools, int64_t 
                                  const int32_t *num_copies, int32_t max_copies, uint32_t *status,
                                  void *stream);
 
+/*
+ * Block tables and slot maps of a step, from the lengths of its requests.
+ *
+ * Sequence s (row s of the block table) holds ctx_len[s] tokens and gets
+ * rows[s] new ones (0: it sits the step out).  Its entries ceil(ctx_len / 16)
+ * to ceil((ctx_len + rows) / 16) - 1 that hold no page take fresh ones, the
+ * free pages of lowest index, in sequence order and then entry order; all
+ * others stay.  Outputs, device:
+ *   cu_rows[num_seqs + 1]: row offsets as verify calls take them; row r =
+ *     cu_rows[s] + j is the j-th new row of sequence s.
+ *   For each of its rows r < cu_rows[num_seqs]: row_seq[r] = s; position[r] =
+ *     ctx_len[s] + j, for a tree sequence ctx_len[s] + the row's depth (0 for
+ *     a root); slot[r], where the row's K/V go: block_table entry of token
+ *     ctx_len[s] + j, times 16, plus (ctx_len[s] + j) % 16.
+ *   Rows from there to max_rows (the padding of a captured graph of fixed
+ *     size): -1 in all three.
+ * mode, parent (by launch row: the caller knows the rows) and seq_kind as for
+ * verify calls; a tree sequence has at most VA_MAX_TREE_ROWS rows, a chain any
+ * number.  Everything is checked before anything changes, and a status word
+ * that is non-zero on entry counts as a finding: table and counts then stay
+ * as they were, cu_rows is 0 and the other outputs -1.  Errors: a negative
+ * number of rows, more rows than max_rows, a tree of more than
+ * VA_MAX_TREE_ROWS (VA_DEV_BAD_ROWS); a negative length, more tokens than the
+ * table's row has entries for (VA_DEV_CTX_OVERFLOW); no page, or one that
+ * other entries share, where a row goes, an entry that is neither -1 nor a
+ * page in use among those, a negative count (VA_DEV_BAD_BLOCK); a parent not
+ * in [-1, j) (VA_DEV_BAD_PARENT); too few free pages (VA_DEV_NO_PAGES).
+ */
+typedef struct va_extend {
+  const int32_t *ctx_len;   /* device [num_seqs] */
+  const int32_t *rows;      /* device [num_seqs] */
+  const int32_t *parent;    /* device [max_rows]; VA_MODE_CHAIN: not read, may be NULL */
+  const uint8_t *seq_kind;  /* device [num_seqs]; VA_MODE_MIXED only */
+  int32_t max_rows;         /* entries of row_seq, position and slot */
+} va_extend;
+
+/* Bytes of device workspace (256-byte aligned). */
+size_t verify_attn_pages_extend_workspace_size(const va_page_pool *pool);
+
+va_status verify_attn_pages_extend(const va_page_pool *pool, const va_extend *x, int32_t mode,
+                                   int32_t *cu_rows, int32_t *row_seq, int32_t *position,
+                                   int64_t *slot, void *ws, size_t ws_bytes, uint32_t *status,
+                                   void *stream);
+
+/*
+ * A latent cache: one row per token, shared by all heads, of latent_dim values
+ * (c) and rope_dim rotated ones (kr).  With up-projections Wk[h] and Wv[h],
+ * head h has the key [Wk[h] c; kr] and the value Wv[h] c, so a query
+ * [q_nope; q_rope] scores (Wk[h]^T q_nope) . c + q_rope . kr, and the output
+ * is Wv[h] applied to the weighted sum of the c.  verify_attn_latent works on
+ * that absorbed form: its queries are [Wk[h]^T q_nope; q_rope], its outputs
+ * are sums of c.  verify_attn_latent_prompt takes the expanded keys and values.
+ *   contiguous (page_size 0): cache is [num_seqs][capacity][latent_dim +
+ *     rope_dim], capacity a multiple of 16.
+ *   paged (page_size 16): [num_blocks][16][latent_dim + rope_dim], block_table
+ *     as in va_kv.
+ */
+typedef struct va_latent {
+  va_dtype dtype;              /* VA_F32 or VA_BF16 */
+  int32_t latent_dim;          /* 256 or 512 */
+  int32_t rope_dim;            /* 64 */
+  void *cache;                 /* device, 16-byte aligned */
+  int32_t page_size;           /* 0 or 16 */
+  int64_t capacity;            /* contiguous only */
+  const int32_t *block_table;  /* paged only: device [num_seqs][max_blocks_per_seq] */
+  int32_t max_blocks_per_seq;  /* paged only */
+  int32_t num_blocks;          /* paged only */
+} va_latent;
+
+/*
+ * Rows into a latent cache.  Row r of kv, [latent_dim + rope_dim] values as
+ * the down-projection gives them, becomes the cache row slot[r]: its first
+ * latent_dim values x turn into x / sqrt(mean(x^2) + norm_eps) * norm_weight
+ * (or stay, norm_weight NULL), its last rope_dim are rotated by the angles of
+ * position[r]: pair i (2i and 2i + 1 if interleaved, else i and i + rope_dim /
+ * 2) goes from (a, b) to (a cos - b sin, a sin + b cos) with cos =
+ * rope[position][i] and sin = rope[position][rope_dim / 2 + i].  With
+ * num_heads > 0 the rope parts of the row's queries, q_rope, are rotated alike
+ * into the last rope_dim values of each head of q, [num_rows][num_heads]
+ * [latent_dim + rope_dim] (whose first latent_dim values stay); q_rope may be
+ * that part of q itself.  Computed in fp32, rounded once.
+ * slot[r] = -1 leaves the cache alone, position[r] = -1 skips row and queries
+ * (padding, see verify_attn_pages_extend).  A slot outside [-1, num_slots)
+ * (VA_DEV_BAD_BLOCK) or a position outside [-1, rope_positions)
+ * (VA_DEV_CTX_OVERFLOW) sets the status bit; the row is skipped.  No two rows
+ * may have the same slot.  A status word that is non-zero on entry does not
+ * stop the call.  kv and q_rope must not overlap the cache.
+ */
+typedef struct va_latent_rows {
+  int32_t num_rows;
+  const void *kv;           /* device [num_rows][kv_stride], cache's dtype, element-aligned */
+  int64_t kv_stride;        /* elements from row to row, >= latent_dim + rope_dim */
+  const void *norm_weight;  /* device [latent_dim], cache's dtype, element-aligned, or NULL */
+  float norm_eps;           /* >= 0 */
+  const float *rope;        /* device [rope_positions][rope_dim], 16-byte aligned: cosines, then sines */
+  int32_t rope_positions;
+  int32_t interleaved;      /* 0 or 1 */
+  const int32_t *position;  /* device [num_rows] */
+  const int64_t *slot;      /* device [num_rows] */
+  int64_t num_slots;        /* rows of the cache */
+  int32_t num_heads;        /* 0 .. VA_MAX_LATENT_HEADS */
+  const void *q_rope;       /* device, element-aligned; head h of row r at r q_row_stride + h q_head_stride */
+  int64_t q_row_stride, q_head_stride;  /* elements, >= rope_dim (one head, one row: any) */
+  void *q;                  /* device, 16-byte aligned */
+} va_latent_rows;
+
+#define VA_MAX_LATENT_HEADS 256
+
+va_status verify_attn_latent_append(const va_latent *kv, const va_latent_rows *rows, uint32_t *status,
+                                    void *stream);
+
+/*
+ * Verify attention over a latent cache, absorbed form.  p as for
+ * verify_attn_chain / tree / mixed (mode), with q: [total_rows][num_heads]
+ * [latent_dim + rope_dim] of the cache's dtype, num_heads <=
+ * VA_MAX_LATENT_HEADS heads over the one row a token has, scale > 0 (the width
+ * of the expanded keys is not known here), rows' own K at positions ctx ..
+ * ctx + n - 1 of the cache.  o: [total_rows][num_heads][latent_dim] of the
+ * cache's dtype, rounded once; lse: fp32 [total_rows][num_heads].
+ * num_splits is the largest number of chunks (whole 64-token tiles, at least
+ * 128 tokens) that a sequence is cut into; where its rows times heads make b
+ * row blocks (of 128 in the tensor-core kernel; of 16 on the CUDA cores: fp32
+ * caches, VA_FLAG_CUDA_CORES) each takes num_splits / b chunks, rounded
+ * down, and at least one.  va_latent_splits gives a count that fills the
+ * GPU.  No choice depends on the other sequences of the launch.
+ * bf16: probabilities enter the second product rounded to bf16 (2^-9 of each,
+ * about what rounding o costs); their sum, and lse, are of the unrounded
+ * ones in fp32.  fp32: fp32 products and sums.
+ * Cache rows that some rows of the sequence see and others do not must be
+ * finite; others may hold anything.  Rows that no sequence covers stay as
+ * they were.  At most 65,535 sequences.  Errors as for the verify calls.  ws
+ * of at least va_latent_workspace_size() bytes (may be 0, ws may then be
+ * NULL), 256-byte aligned; contents carry nothing from call to call, and
+ * calls that may overlap in time need workspaces of their own.
+ */
+size_t va_latent_workspace_size(const va_problem *p, const va_latent *kv);
+int32_t va_latent_splits(const va_problem *p, const va_latent *kv);
+va_status verify_attn_latent(const va_problem *p, const va_latent *kv, int32_t mode, void *ws,
+                             size_t ws_bytes, void *o, float *lse, uint32_t *status, void *stream);
+
+/*
+ * Attention of prompt segments over expanded keys and values.  Rows of
+ * sequence s are cu_rows[s] .. of q, [total_rows][num_heads][nope_dim +
+ * rope_dim]; its keys are cu_kv[s] .. cu_kv[s + 1] - 1 of kv, [total_kv]
+ * [num_heads][nope_dim + value_dim] (a head's key part, then its value, as an
+ * up-projection of c gives them), with the rope part k_rope[token][rope_dim]
+ * shared by the heads (its rows may lie in a latent cache's: k_rope_stride).
+ * causal: row j of n sees the keys up to len - n + j (its own segment's keys
+ * come last); else every row sees all len keys, as for a part of the context
+ * whose result is joined by lse.  A row that sees no key (len 0, or len < n)
+ * gets o = 0 and lse = -inf.
+ * Of p, num_seqs, num_heads (<= VA_MAX_LATENT_HEADS), q_dtype, q, cu_rows,
+ * total_rows, max_rows_per_seq (any number up to 2^22), scale (0: 1 /
+ * sqrt(nope_dim + rope_dim)), num_splits and flags are read.  num_splits, the
+ * workspace, precision and the types of o ([total_rows][num_heads][value_dim])
+ * and lse as for verify_attn_latent, with row blocks per head
+ * (va_latent_prompt_splits).  Inconsistent offsets, rows beyond
+ * max_rows_per_seq: VA_DEV_BAD_ROWS, NaN.  Keys that some rows of a sequence
+ * see must be finite.
+ */
+typedef struct va_prompt {
+  va_dtype dtype;         /* VA_F32 or VA_BF16 */
+  int32_t nope_dim;       /* 64 or 128 */
+  int32_t rope_dim;       /* 64 */
+  int32_t value_dim;      /* as nope_dim */
+  const void *kv;         /* device, 16-byte aligned */
+  const void *k_rope;     /* device, 16-byte aligned */
+  int64_t k_rope_stride;  /* elements from token to token, a multiple of 16 bytes */
+  const int32_t *cu_kv;   /* device [num_seqs + 1] */
+  int32_t total_kv;       /* host copy of cu_kv[num_seqs] */
+  int32_t causal;         /* 0 or 1 */
+} va_prompt;
+
+size_t va_latent_prompt_workspace_size(const va_problem *p, const va_prompt *kv);
+int32_t va_latent_prompt_splits(const va_problem *p, const va_prompt *kv);
+va_status verify_attn_latent_prompt(const va_problem *p, const va_prompt *kv, void *ws, size_t ws_bytes,
+                                    void *o, float *lse, uint32_t *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

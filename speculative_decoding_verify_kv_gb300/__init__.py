@@ -36,6 +36,7 @@ DEV_BAD_COPY = 0x200
 # Rows per sequence (chain / tree); see VA_MAX_ROWS_PER_SEQ in the header.
 MAX_ROWS_PER_SEQ = 1024
 MAX_TREE_ROWS = 32
+MAX_LATENT_HEADS = 256
 
 STATUS_NAMES = {0: "VA_OK", 1: "VA_ERR_INVALID_ARG", 2: "VA_ERR_UNSUPPORTED",
                 3: "VA_ERR_ALIGNMENT", 4: "VA_ERR_WORKSPACE_TOO_SMALL", 5: "VA_ERR_CUDA"}
@@ -50,7 +51,10 @@ EXPORTED = ["va_version", "va_status_string", "va_last_cuda_error", "va_workspac
             "verify_attn_window", "va_window_workspace_size", "va_window_splits",
             "verify_attn_accept", "verify_attn_accept_workspace_size",
             "verify_attn_pages_workspace_size", "verify_attn_pages_fork", "verify_attn_pages_free",
-            "verify_attn_pages_compact", "verify_attn_pages_copy"]
+            "verify_attn_pages_compact", "verify_attn_pages_copy",
+            "verify_attn_pages_extend", "verify_attn_pages_extend_workspace_size", "verify_attn_latent_append",
+            "verify_attn_latent", "va_latent_workspace_size", "va_latent_splits",
+            "verify_attn_latent_prompt", "va_latent_prompt_workspace_size", "va_latent_prompt_splits"]
 
 
 class VaKV(ctypes.Structure):
@@ -88,6 +92,34 @@ class VaPagePool(ctypes.Structure):
     _fields_ = [("num_seqs", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
                 ("num_blocks", ctypes.c_int32), ("block_table", ctypes.c_void_p),
                 ("ref_count", ctypes.c_void_p)]
+
+
+class VaExtend(ctypes.Structure):
+    _fields_ = [("ctx_len", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("parent", ctypes.c_void_p),
+                ("seq_kind", ctypes.c_void_p), ("max_rows", ctypes.c_int32)]
+
+
+class VaLatent(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("latent_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("cache", ctypes.c_void_p), ("page_size", ctypes.c_int32), ("capacity", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("max_blocks_per_seq", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32)]
+
+
+class VaLatentRows(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int32), ("kv", ctypes.c_void_p), ("kv_stride", ctypes.c_int64),
+                ("norm_weight", ctypes.c_void_p), ("norm_eps", ctypes.c_float), ("rope", ctypes.c_void_p),
+                ("rope_positions", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("position", ctypes.c_void_p),
+                ("slot", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("num_heads", ctypes.c_int32),
+                ("q_rope", ctypes.c_void_p), ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("q", ctypes.c_void_p)]
+
+
+class VaPrompt(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("nope_dim", ctypes.c_int32), ("rope_dim", ctypes.c_int32),
+                ("value_dim", ctypes.c_int32), ("kv", ctypes.c_void_p), ("k_rope", ctypes.c_void_p),
+                ("k_rope_stride", ctypes.c_int64), ("cu_kv", ctypes.c_void_p), ("total_kv", ctypes.c_int32),
+                ("causal", ctypes.c_int32)]
 
 
 class VaPlanInfo(ctypes.Structure):
@@ -156,7 +188,19 @@ def _load():
             ("verify_attn_pages_compact", ctypes.c_int,
              [P(VaPagePool), ptr, ptr, ptr, ptr, size, ptr, ptr]),
             ("verify_attn_pages_copy", ctypes.c_int,
-             [P(ptr), i32, i64, i32, ptr, ptr, i32, ptr, ptr])):
+             [P(ptr), i32, i64, i32, ptr, ptr, i32, ptr, ptr]),
+            ("verify_attn_pages_extend_workspace_size", size, [P(VaPagePool)]),
+            ("verify_attn_pages_extend", ctypes.c_int,
+             [P(VaPagePool), P(VaExtend), i32, ptr, ptr, ptr, ptr, ptr, size, ptr, ptr]),
+            ("verify_attn_latent_append", ctypes.c_int, [P(VaLatent), P(VaLatentRows), ptr, ptr]),
+            ("va_latent_workspace_size", size, [P(VaProblem), P(VaLatent)]),
+            ("va_latent_splits", i32, [P(VaProblem), P(VaLatent)]),
+            ("verify_attn_latent", ctypes.c_int,
+             [P(VaProblem), P(VaLatent), i32, ptr, size, ptr, ptr, ptr, ptr]),
+            ("va_latent_prompt_workspace_size", size, [P(VaProblem), P(VaPrompt)]),
+            ("va_latent_prompt_splits", i32, [P(VaProblem), P(VaPrompt)]),
+            ("verify_attn_latent_prompt", ctypes.c_int,
+             [P(VaProblem), P(VaPrompt), ptr, size, ptr, ptr, ptr, ptr])):
         f = getattr(lib, name)
         f.restype, f.argtypes = res, args
     return lib
@@ -447,7 +491,10 @@ def timing_read(max_calls: int = 4096):
     return list(a[:n.value]), list(b[:n.value])
 
 
-from ._calls import (AcceptCall, CompactCall, Draft, ForkCall, FreeCall, PageCopyCall,  # noqa: E402,F401
-                     PagePool, Window, WindowCall, verify_attn_accept, verify_attn_pages_compact,
-                     verify_attn_pages_copy, verify_attn_pages_fork, verify_attn_pages_free,
-                     verify_attn_window, window_splits)
+from ._calls import (AcceptCall, CompactCall, Draft, ExtendCall, ForkCall, FreeCall,  # noqa: E402,F401
+                     PageCopyCall, PagePool, Window, WindowCall, verify_attn_accept,
+                     verify_attn_pages_compact, verify_attn_pages_copy, verify_attn_pages_extend,
+                     verify_attn_pages_fork, verify_attn_pages_free, verify_attn_window, window_splits)
+from ._latent import (LatentAppendCall, LatentCall, LatentKV, LatentRows, PromptCall, PromptKV,  # noqa: E402,F401
+                      latent_splits, prompt_splits, verify_attn_latent, verify_attn_latent_append,
+                      verify_attn_latent_prompt)

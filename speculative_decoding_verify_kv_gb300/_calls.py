@@ -24,7 +24,7 @@ from typing import Optional
 
 import torch
 
-from . import BF16, F32, KV, Q8_0, Problem, VaDraft, VaError, VaPagePool, VaWindow, _ptr, lib
+from . import BF16, F32, KV, Q8_0, Problem, VaDraft, VaError, VaExtend, VaPagePool, VaWindow, _ptr, lib
 
 _FLOAT = {F32: torch.float32, BF16: torch.bfloat16}
 
@@ -383,6 +383,33 @@ class CompactCall(_PageCall):
         self._keep = (_held(pool), ws, status, c)
 
 
+class ExtendCall(_PageCall):
+    """verify_attn_pages_extend: tokens held and new rows of every sequence of
+    the pool.  Returns a dict of cu_rows, row_seq, position and slot."""
+    _where = "verify_attn_pages_extend"
+
+    def __init__(self, pool: PagePool, ctx_len, rows, max_rows: int, mode: int = 0, *, parent=None, seq_kind=None,
+                 cu_rows=None, row_seq=None, position=None, slot=None, ws=None, status=None):
+        c = self._bind(pool, status)
+        dev, seqs = self.device, c.num_seqs
+        if _i32("max_rows", max_rows) < 0:
+            raise ValueError(f"max_rows: {max_rows}")
+        _tensor("ctx_len", ctx_len, torch.int32, seqs, dev)
+        _tensor("rows", rows, torch.int32, seqs, dev)
+        _tensor("parent", parent, torch.int32, max_rows if mode else 0, dev, optional=mode == 0)
+        _tensor("seq_kind", seq_kind, torch.uint8, seqs if mode == 2 else 0, dev, optional=mode != 2)
+        out = {"cu_rows": self._buffer("cu_rows", cu_rows, (seqs + 1,), torch.int32),
+               "row_seq": self._buffer("row_seq", row_seq, (max_rows,), torch.int32),
+               "position": self._buffer("position", position, (max_rows,), torch.int32),
+               "slot": self._buffer("slot", slot, (max_rows,), torch.int64)}
+        x = VaExtend(_ptr(ctx_len), _ptr(rows), _ptr(parent), _ptr(seq_kind), max_rows)
+        ws = self._workspace(ws, int(lib.verify_attn_pages_extend_workspace_size(ctypes.byref(c))))
+        self._fn, self._out = lib.verify_attn_pages_extend, out
+        self._args = (ctypes.byref(c), ctypes.byref(x), mode, _ptr(out["cu_rows"]), _ptr(out["row_seq"]),
+                      _ptr(out["position"]), _ptr(out["slot"]), _ptr(ws), ws.numel(), _ptr(status))
+        self._keep = (_held(pool), ctx_len, rows, parent, seq_kind, ws, status, c, x)
+
+
 class PageCopyCall(_Call):
     """verify_attn_pages_copy over a list of pools, tensors whose first
     dimension is the pages (the K and V arrays of every layer)."""
@@ -412,6 +439,12 @@ def verify_attn_pages_fork(pool: PagePool, src, dst, length, pages, *, stream=No
     """Fork and grow sequences of a paged cache; returns (copies, num_copies)
     for verify_attn_pages_copy."""
     return _in_one_go(ForkCall, stream, pool, src, dst, length, pages, **kw)
+
+
+def verify_attn_pages_extend(pool: PagePool, ctx_len, rows, max_rows: int, mode: int = 0, *, stream=None, **kw):
+    """Block tables, row offsets, positions and slots of a step from its
+    requests' lengths (see verify_attn_pages_extend in the header)."""
+    return _in_one_go(ExtendCall, stream, pool, ctx_len, rows, max_rows, mode, **kw)
 
 
 def verify_attn_pages_free(pool: PagePool, seq, first, last, *, status=None, stream=None):

@@ -52,7 +52,7 @@ constexpr int kMinSubTokens = 128;
 constexpr int kMaxSubSplits = 16;
 constexpr int kMaxExactTokens = 2048;  // of a chunk, see window_plan
 
-static int sm_count() {
+int sm_count() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
   int n = 0;

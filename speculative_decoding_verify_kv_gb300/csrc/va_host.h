@@ -16,6 +16,9 @@ va_status note_cuda(cudaError_t e);
 // (outside stream capture; the default streams are the current device's).
 va_status check_stream_device(cudaStream_t s);
 
+// SMs of the current device.
+int sm_count();
+
 // Set a kernel's dynamic shared memory limit, once per device (ready: a bit
 // for each, a static of the caller).
 template <typename K>

@@ -1,0 +1,365 @@
+// CUDA-core attention over latent caches and expanded prompt keys: fp32
+// products and sums, the kernel of fp32 tensors (and, asked for by flag, of
+// bf16 ones).
+//
+// One CTA owns 16 query rows and one chunk of tokens and walks it in tiles of
+// 32: scores with a token to a lane and two rows to a warp, online softmax
+// (m in log2 units, l), values accumulated in registers.  Over a latent cache
+// the values are the first DV of the key's own columns, so a tile is loaded
+// once.  The next tile's loads are under way while a tile is worked through.
+// A chunk that is a sequence's only one writes o itself; others leave (m, l,
+// acc) for the merge.
+#include <string.h>
+
+#include "va_latent.cuh"
+
+namespace va {
+
+constexpr int kLsRows = 16;
+constexpr int kLsTile = 32;
+constexpr int kLsThreads = 256;
+
+template <int DK, int DV, bool PROMPT>
+struct LsCfg {
+  static constexpr int LDK = DK + 4;  // lanes of a float4 read of a column hit banks of their own
+  static constexpr int SMEM = (kLsRows * DK + kLsTile * LDK + (PROMPT ? kLsTile * DV : 0) + kLsRows * kLsTile) * 4;
+};
+
+// Four elements at index i (a multiple of 4; rows start on 16 bytes).
+template <typename T>
+__device__ __forceinline__ float4 load4(const void* base, long long i) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + i);
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<const unsigned short*>(base) + i);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+  }
+}
+
+template <typename T, int DK, int DV, bool PROMPT>
+__global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentParams p) {
+  using C = LsCfg<DK, DV, PROMPT>;
+  constexpr int WARPS = kLsThreads / 32, RW = kLsRows / WARPS;
+  constexpr int NC = DV / 64;                      // float2 columns per lane
+  constexpr int ROW4 = (DK + (PROMPT ? DV : 0)) / 4;  // float4 pieces of a token's key and value
+  constexpr int NL = (kLsTile * ROW4 + kLsThreads - 1) / kLsThreads;
+  extern __shared__ __align__(16) float lsm[];
+  float* Qs = lsm;
+  float* Ks = Qs + kLsRows * DK;
+  float* Vs = PROMPT ? Ks + kLsTile * C::LDK : Ks;
+  constexpr int LDV = PROMPT ? DV : C::LDK;
+  float* Ps = Ks + kLsTile * C::LDK + (PROMPT ? kLsTile * DV : 0);
+  __shared__ unsigned anc_s[kLsRows];
+  __shared__ int bad_s;
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int head = blockIdx.y, s = blockIdx.z;
+  const LatentSeq q = latent_seq(p, s);
+  if (q.err & VA_DEV_BAD_ROWS) {
+    if (tid == 0) flag(p.status, q.err);
+    if (blockIdx.x == 0) latent_nan_rows(p, s, PROMPT ? head : 0, PROMPT ? 1 : p.H);
+    return;
+  }
+  const int R = latent_rows(p, q.n);
+  const int blocks = (R + kLsRows - 1) / kLsRows;
+  if (blocks == 0) return;
+  const int nchunk = latent_chunks(p, q.n);
+  const int rb = blockIdx.x % blocks, chunk = blockIdx.x / blocks;
+  const int live = latent_live(q.err ? 0 : q.len, nchunk);
+  if (chunk >= live) return;
+  const int rbase = rb * kLsRows, nrows = min(kLsRows, R - rbase);
+  int lo, hi;
+  latent_range(q.len, nchunk, chunk, &lo, &hi);
+  const int jlast = PROMPT ? rbase + nrows - 1 : (rbase + nrows - 1) / p.H;
+  hi = max(lo, min(hi, latent_end(p, q, jlast)));
+  unsigned err = q.err;
+
+  if (tid == 0) bad_s = 0;
+  __syncthreads();
+  if (tid < nrows && !err) {
+    bool bad = false;
+    anc_s[tid] = row_mask(q.kind, p.parent + q.row0, PROMPT ? rbase + tid : (rbase + tid) / p.H, &bad);
+    if (bad) atomicOr(&bad_s, (int)VA_DEV_BAD_PARENT);
+  }
+  for (int i = tid; i < nrows * (DK / 4); i += kLsThreads) {
+    const long long item = latent_item(p, q.row0, rbase + i / (DK / 4), head);
+    *reinterpret_cast<float4*>(Qs + i * 4) = load4<T>(p.q, item * DK + i % (DK / 4) * 4);
+  }
+  for (int i = nrows * DK + tid; i < kLsRows * DK; i += kLsThreads) Qs[i] = 0.f;
+
+  float4 x[NL];
+  bool lost = false;
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int k = 0; k < NL; ++k) {
+      const int i = tid + k * kLsThreads, t = t0 + i / ROW4, d = i % ROW4 * 4;
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i >= kLsTile * ROW4 || t >= hi) continue;
+      if (PROMPT) {
+        const long long row = q.key0 + t;
+        constexpr int NOPE = DK - kLatentRope;
+        if (d < NOPE) x[k] = load4<T>(p.kv, (row * p.H + head) * (NOPE + DV) + d);
+        else if (d < DK) x[k] = load4<T>(p.k_rope, row * p.kr_stride + d - NOPE);
+        else x[k] = load4<T>(p.kv, (row * p.H + head) * (NOPE + DV) + d - kLatentRope);
+      } else {
+        const long long row = latent_row(p, s, t);
+        if (row < 0) lost = true;
+        else x[k] = load4<T>(p.cache, row * DK + d);
+      }
+    }
+  };
+  float m_run[RW], l_run[RW];
+  float2 acc[RW][NC];
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    m_run[i] = -INFINITY;
+    l_run[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[i][c] = make_float2(0.f, 0.f);
+  }
+  __syncthreads();
+  err |= (unsigned)bad_s;
+  if (!err && lo < hi) load(lo);
+  for (int t0 = lo; t0 < hi && !err; t0 += kLsTile) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NL; ++k) {
+      const int i = tid + k * kLsThreads, t = i / ROW4, d = i % ROW4 * 4;
+      if (i >= kLsTile * ROW4) continue;
+      if (PROMPT && d >= DK) *reinterpret_cast<float4*>(Vs + t * LDV + d - DK) = x[k];
+      else *reinterpret_cast<float4*>(Ks + t * C::LDK + d) = x[k];
+    }
+    if (__syncthreads_or(lost)) {
+      err |= VA_DEV_BAD_BLOCK;
+      break;
+    }
+    if (t0 + kLsTile < hi) load(t0 + kLsTile);
+    if (warp * RW >= nrows) continue;
+    float sc[RW];
+#pragma unroll
+    for (int i = 0; i < RW; ++i) sc[i] = 0.f;
+#pragma unroll 8
+    for (int d = 0; d < DK; d += 4) {
+      const float4 k4 = *reinterpret_cast<const float4*>(Ks + lane * C::LDK + d);
+#pragma unroll
+      for (int i = 0; i < RW; ++i) {
+        const float4 q4 = *reinterpret_cast<const float4*>(Qs + (warp * RW + i) * DK + d);
+        sc[i] = fmaf(q4.w, k4.w, fmaf(q4.z, k4.z, fmaf(q4.y, k4.y, fmaf(q4.x, k4.x, sc[i]))));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      const int rl = warp * RW + i;
+      const int j = PROMPT ? rbase + rl : (rbase + rl) / p.H;
+      const unsigned vis = rl < nrows ? latent_bits(p, q, anc_s[rl], j, hi, t0) : 0u;
+      const float z = (vis >> lane) & 1u ? sc[i] * p.scale_log2 : -INFINITY;
+      float mx = z;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float m_new = fmaxf(m_run[i], mx);
+      const float w = m_new == -INFINITY ? 0.f : exp2f(z - m_new);
+      const float f = m_run[i] == -INFINITY ? 0.f : exp2f(m_run[i] - m_new);
+      float sum = w;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      l_run[i] = l_run[i] * f + sum;
+      m_run[i] = m_new;
+      Ps[rl * kLsTile + lane] = w;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        acc[i][c].x *= f;
+        acc[i][c].y *= f;
+      }
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int t = 0; t < kLsTile; ++t) {
+      float w[RW];
+#pragma unroll
+      for (int i = 0; i < RW; ++i) w[i] = Ps[(warp * RW + i) * kLsTile + t];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const float2 v = *reinterpret_cast<const float2*>(Vs + t * LDV + 2 * lane + 64 * c);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          acc[i][c].x = fmaf(w[i], v.x, acc[i][c].x);
+          acc[i][c].y = fmaf(w[i], v.y, acc[i][c].y);
+        }
+      }
+    }
+    __syncwarp();
+  }
+  if (err && tid == 0) flag(p.status, err);
+#pragma unroll
+  for (int i = 0; i < RW; ++i) {
+    const int rl = warp * RW + i;
+    if (rl >= nrows) continue;
+    const long long item = latent_item(p, q.row0, rbase + rl, head);
+    if (live > 1) {
+      const long long si = latent_slot(p, chunk, item);
+      if (lane == 0) {
+        p.ws_ml[2 * si] = err ? NAN : m_run[i];
+        p.ws_ml[2 * si + 1] = err ? NAN : l_run[i];
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        *reinterpret_cast<float2*>(p.ws_acc + si * DV + 2 * lane + 64 * c) = acc[i][c];
+      continue;
+    }
+    const float inv = err ? NAN : l_run[i] > 0.f ? 1.f / l_run[i] : 0.f;
+    if (lane == 0) p.lse[item] = err ? NAN : l_run[i] > 0.f ? (m_run[i] + log2f(l_run[i])) * kLn2 : -INFINITY;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const float2 v = make_float2(acc[i][c].x * inv, acc[i][c].y * inv);
+      const long long at = item * DV + 2 * lane + 64 * c;
+      if (sizeof(T) == 4) *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.o) + at) = v;
+      else *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(p.o) + at) = __floats2bfloat162_rn(v.x, v.y);
+    }
+  }
+}
+
+// Merge of a sequence's chunks, a warp per (row, head): M over the chunks,
+// then l and o with the weights 2^(m - M), in chunk order, so the sums depend
+// on the row's own partials alone.  Sequences of one chunk have their o
+// already, rows of inconsistent sequences their NaN.
+constexpr int kLmThreads = 256;
+
+template <int DV>
+__global__ void __launch_bounds__(kLmThreads) latent_merge_kernel(const LatentParams p) {
+  constexpr int NC = DV / 128 > 0 ? DV / 128 : 1;  // float4 columns per lane (DV = 64: half the lanes)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * (kLmThreads / 32) + threadIdx.x / 32;
+  if (item >= (long long)p.total_rows * p.H) return;
+  const int grow = (int)(item / p.H);
+  int s = -1;  // the last sequence that starts at or before the row
+  for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+    const unsigned m = __ballot_sync(0xffffffffu, s0 + lane < p.num_seqs && p.cu_rows[s0 + lane] <= grow);
+    if (m) s = s0 + 31 - __clz(m);
+  }
+  if (s < 0 || grow >= p.cu_rows[s + 1]) return;
+  const LatentSeq q = latent_seq(p, s);
+  if (q.err) return;  // written as NaN
+  const int live = latent_live(q.len, latent_chunks(p, q.n));
+  if (live == 1) return;
+  bool nan = false;
+  float M = -INFINITY;
+  for (int k = lane; k < live; k += 32) {
+    const long long si = latent_slot(p, k, item);
+    const float mk = p.ws_ml[2 * si], lk = p.ws_ml[2 * si + 1];
+    if (isnan(mk) || isnan(lk)) nan = true;
+    if (lk > 0.f) M = fmaxf(M, mk);
+  }
+  nan = __any_sync(0xffffffffu, nan);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float l = 0.f;
+  float4 acc[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool mine = DV >= 128 || lane < 16;
+  constexpr int B = 4;  // chunks in flight
+  for (int s0 = 0; s0 < live && !nan; s0 += B) {
+    float mm[B], ll[B];
+    float4 aa[B][NC];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const bool in = s0 + k < live;
+      const long long si = latent_slot(p, in ? s0 + k : s0, item);
+      mm[k] = in ? p.ws_ml[2 * si] : -INFINITY;
+      ll[k] = in ? p.ws_ml[2 * si + 1] : 0.f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        aa[k][c] = in && mine ? *reinterpret_cast<const float4*>(p.ws_acc + si * DV + 4 * (lane + 32 * c))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      // A chunk that a row sees nothing of: its acc is not read as data.
+      const float w = ll[k] > 0.f ? exp2f(mm[k] - M) : 0.f;
+      if (!(w > 0.f)) continue;
+      l = fmaf(w, ll[k], l);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        acc[c].x = fmaf(w, aa[k][c].x, acc[c].x);
+        acc[c].y = fmaf(w, aa[k][c].y, acc[c].y);
+        acc[c].z = fmaf(w, aa[k][c].z, acc[c].z);
+        acc[c].w = fmaf(w, aa[k][c].w, acc[c].w);
+      }
+    }
+  }
+  const float inv = nan ? NAN : l > 0.f ? 1.f / l : 0.f;
+  if (mine) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const long long at = item * DV + 4 * (lane + 32 * c);
+      const float4 v = make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv);
+      if (p.o_bf16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        uint2 w;
+        memcpy(&w.x, &a, 4);
+        memcpy(&w.y, &b, 4);
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + at) = w;
+      } else {
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + at) = v;
+      }
+    }
+  }
+  if (lane == 0) p.lse[item] = nan ? NAN : l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <typename K>
+static cudaError_t launch_one(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, const LatentParams& p) {
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T, int DK, int DV, bool PROMPT>
+static cudaError_t launch_simt_t(const LatentParams& p, dim3 grid, cudaStream_t st) {
+  static std::atomic<unsigned long long> ready{0ull};
+  constexpr int smem = LsCfg<DK, DV, PROMPT>::SMEM;
+  cudaError_t e = allow_smem(latent_simt_kernel<T, DK, DV, PROMPT>, smem, ready);
+  if (e != cudaSuccess) return e;
+  return launch_one(latent_simt_kernel<T, DK, DV, PROMPT>, grid, kLsThreads, smem, st, p);
+}
+
+template <typename T>
+static cudaError_t launch_simt_of(const LatentParams& p, dim3 grid, cudaStream_t st) {
+  if (p.prompt)
+    return p.DV == 128 ? launch_simt_t<T, 192, 128, true>(p, grid, st) : launch_simt_t<T, 128, 64, true>(p, grid, st);
+  return p.DV == 512 ? launch_simt_t<T, 576, 512, false>(p, grid, st) : launch_simt_t<T, 320, 256, false>(p, grid, st);
+}
+
+int latent_simt_rows() { return kLsRows; }
+
+cudaError_t launch_latent_simt(const LatentParams& p, dim3 grid, cudaStream_t st) {
+  return p.o_bf16 ? launch_simt_of<__nv_bfloat16>(p, grid, st) : launch_simt_of<float>(p, grid, st);
+}
+
+cudaError_t launch_latent_merge(const LatentParams& p, cudaStream_t st) {
+  const long long items = (long long)p.total_rows * p.H;
+  const dim3 grid((unsigned)((items + kLmThreads / 32 - 1) / (kLmThreads / 32)));
+  switch (p.DV) {
+    case 64: return launch_one(latent_merge_kernel<64>, grid, kLmThreads, 0, st, p);
+    case 128: return launch_one(latent_merge_kernel<128>, grid, kLmThreads, 0, st, p);
+    case 256: return launch_one(latent_merge_kernel<256>, grid, kLmThreads, 0, st, p);
+    default: return launch_one(latent_merge_kernel<512>, grid, kLmThreads, 0, st, p);
+  }
+}
+
+}  // namespace va

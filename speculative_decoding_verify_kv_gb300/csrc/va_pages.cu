@@ -45,6 +45,14 @@ struct PageParams {
   int* live;
   int* ws;
   unsigned* status;
+  // extend: a is tokens held, b new rows
+  int mode, max_rows;
+  const int* parent;
+  const unsigned char* kind;
+  int* cu;
+  int* row_seq;
+  int* position;
+  long long* slot;
 };
 
 struct PlanShared {
@@ -355,6 +363,226 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_kernel(const PagePara
   }
 }
 
+// Block tables and slot maps from request lengths.  Sequence s holds a[s]
+// tokens and gets b[s] rows: entries ceil(a / 16) to ceil((a + b) / 16) - 1
+// that hold no page take the lowest free ones, and every row learns its
+// sequence, position and slot.  Workspace: need[num_seqs] (then each
+// sequence's first fresh page), free pages found [num_blocks].
+//
+// Bound by the latency of its steps (five barriers, six with trees): 39
+// sequences of one row over 8,192 pages, one CTA; 256 sequences of up to 8
+// rows over 131,072 pages, a cluster.  Eight lanes go through a sequence's
+// entries: steps of few rows touch one or two of them, prompt segments some
+// dozens.
+constexpr int kSeqLanes = 8;
+constexpr int kCuShared = 2048;  // row offsets kept in shared memory
+
+// First index of the last sequence that starts at or before row r and has
+// rows: the largest s with cu[s] <= r (cu ascending, cu[n] > r).
+__device__ __forceinline__ int seq_of_row(const int* cu, int n, int r) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ bool extend_is_tree(const PageParams& p, int s) {
+  return p.mode == VA_MODE_TREE || (p.mode == VA_MODE_MIXED && p.kind[s] != 0);
+}
+
+template <int NC>
+__global__ void __launch_bounds__(kPlanThreads) pages_extend_kernel(const PageParams p) {
+  __shared__ PlanShared sh;
+  __shared__ unsigned long long part_rows[kCtaWarps];
+  __shared__ unsigned long long part_need[kCtaWarps];
+  __shared__ int cu_s[kCuShared + 1];
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Team<NC> team;
+  const int rank = team.rank();
+  const int tid = threadIdx.x, lane = tid & 31, gwarp = rank * kCtaWarps + tid / 32;
+  const int gtid = rank * kPlanThreads + tid;
+  int* need = p.ws;
+  int* found = need + p.num_seqs;
+  if (tid == 0) sh.err = rank == 0 ? status_before(p) : 0u;
+  team.sync();
+
+  // Check every sequence and count the pages it takes; count the free ones.
+  const int sub = lane & (kSeqLanes - 1);
+  const long long groups = (long long)NC * kPlanThreads / kSeqLanes;
+  for (long long s0 = gtid / kSeqLanes; s0 < p.num_seqs; s0 += groups) {
+    const int s = (int)s0;
+    const unsigned peers = 0xffu << (lane & ~(kSeqLanes - 1));
+    const int held = p.a[s], n = p.b[s];
+    unsigned err = 0u;
+    int fresh = 0;
+    if (n < 0 || (n > kMaxTreeRows && extend_is_tree(p, s))) {
+      err = VA_DEV_BAD_ROWS;
+    } else if (held < 0 || ((long long)held + n + kPage - 1) / kPage > p.max_blocks) {
+      err = VA_DEV_CTX_OVERFLOW;
+    } else if (n > 0) {
+      const int keep = (held + kPage - 1) / kPage, end = (held + n + kPage - 1) / kPage;
+      const int* row = p.table + (long long)s * p.max_blocks;
+      for (int c = held / kPage + sub; c < end; c += kSeqLanes) {
+        const int e = row[c];
+        // A page that rows are written to belongs to this sequence alone.
+        if (e != -1 && !(e >= 0 && e < p.num_blocks && p.ref[e] == 1)) err = VA_DEV_BAD_BLOCK;
+        if (e == -1 && c < keep) err = VA_DEV_BAD_BLOCK;  // the page that the held tokens end in
+        fresh += e == -1;
+      }
+    }
+    fresh += __shfl_xor_sync(peers, fresh, 1);
+    fresh += __shfl_xor_sync(peers, fresh, 2);
+    fresh += __shfl_xor_sync(peers, fresh, 4);
+    if (sub == 0) need[s] = fresh;
+    if (err) note_error(team, sh, err);
+  }
+  int lo, hi;
+  warp_share<NC>(p.num_blocks, gwarp, &lo, &hi);
+  unsigned freec = 0;
+#pragma unroll 8
+  for (int i = lo + lane; i < hi; i += 32) {
+    const int r = p.ref[i];
+    if (r < 0) note_error(team, sh, VA_DEV_BAD_BLOCK);
+    freec += r == 0;
+  }
+  freec = warp_add(freec);
+  share_count(team, sh, gwarp, lane, freec);
+  team.sync();
+
+  // The first CTA turns rows and needs into running totals, 1,024 sequences
+  // at a time (64-bit sums; past the limit the call fails below).
+  if (rank == 0 && read_error(team, sh) == 0u) {
+    unsigned long long base_rows = 0, base_need = 0;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
+      const int s = s0 + tid;
+      const unsigned long long a = s < p.num_seqs ? (unsigned long long)p.b[s] : 0ull;
+      const unsigned long long b = s < p.num_seqs ? (unsigned long long)need[s] : 0ull;
+      unsigned long long ia = a, ib = b;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long ua = __shfl_up_sync(0xffffffffu, ia, o), ub = __shfl_up_sync(0xffffffffu, ib, o);
+        if (lane >= o) {
+          ia += ua;
+          ib += ub;
+        }
+      }
+      if (lane == 31) {
+        part_rows[tid / 32] = ia;
+        part_need[tid / 32] = ib;
+      }
+      __syncthreads();
+      unsigned long long before_a = 0, before_b = 0, all_a = 0, all_b = 0;
+      for (int w = 0; w < kCtaWarps; ++w) {
+        if (w == tid / 32) {
+          before_a = all_a;
+          before_b = all_b;
+        }
+        all_a += part_rows[w];
+        all_b += part_need[w];
+      }
+      if (s < p.num_seqs) {
+        p.cu[s] = (int)min(base_rows + before_a + ia - a, 0x7fffffffull);
+        need[s] = (int)min(base_need + before_b + ib - b, 0x7fffffffull);
+      }
+      base_rows += all_a;
+      base_need += all_b;
+      __syncthreads();
+    }
+    if (tid == 0) {
+      p.cu[p.num_seqs] = (int)min(base_rows, 0x7fffffffull);
+      sh.total_need = (unsigned)min(base_need, 0xffffffffull);
+      sh.total_tail = (unsigned)min(base_rows, 0xffffffffull);
+      if (base_rows > (unsigned long long)p.max_rows) sh.err |= VA_DEV_BAD_ROWS;
+    }
+  }
+  team.sync();
+  unsigned err = read_error(team, sh);
+  const unsigned wanted = err ? 0u : *team.at(&sh.total_need, 0);
+  const int rows = err ? 0 : (int)*team.at(&sh.total_tail, 0);
+  const int* cu = p.cu;
+  if (!err && p.num_seqs <= kCuShared) {
+    for (int i = tid; i <= p.num_seqs; i += kPlanThreads) cu_s[i] = p.cu[i];
+    cu = cu_s;
+  }
+  __syncthreads();
+  if (!err && p.mode != VA_MODE_CHAIN) {
+    for (int r = gtid; r < rows; r += NC * kPlanThreads) {
+      const int s = seq_of_row(cu, p.num_seqs, r);
+      const int j = r - cu[s], up = p.parent[r];
+      if (extend_is_tree(p, s) && (up < -1 || up >= j)) note_error(team, sh, VA_DEV_BAD_PARENT);
+    }
+  }
+  if (p.mode != VA_MODE_CHAIN) {
+    team.sync();
+    err = read_error(team, sh);
+  }
+  if (!err && sum_before(sh, NC * kCtaWarps, lane) < wanted) err = VA_DEV_NO_PAGES;
+  if (err) {
+    team.sync();  // the first CTA's memory and the offsets are read until here
+    if (gtid == 0) flag(p.status, err);
+    for (int i = gtid; i <= p.num_seqs; i += NC * kPlanThreads) p.cu[i] = 0;
+    for (int r = gtid; r < p.max_rows; r += NC * kPlanThreads) {
+      p.row_seq[r] = p.position[r] = -1;
+      p.slot[r] = -1;
+    }
+    return;
+  }
+  // The wanted free pages, ascending, and their first reference.
+  unsigned at = sum_before(sh, gwarp, lane);
+  for (int i0 = lo; i0 < hi && at < wanted; i0 += 32) {
+    const int i = i0 + lane;
+    const bool is_free = i < hi && p.ref[i] == 0;
+    const unsigned m = __ballot_sync(0xffffffffu, is_free);
+    const unsigned r = at + __popc(m & ((1u << lane) - 1u));
+    if (is_free && r < wanted) {
+      found[r] = i;
+      p.ref[i] = 1;
+    }
+    at += __popc(m);
+  }
+  team.sync();
+  for (long long s0 = gtid / kSeqLanes; s0 < p.num_seqs; s0 += groups) {
+    const int s = (int)s0;
+    const unsigned peers = 0xffu << (lane & ~(kSeqLanes - 1));
+    const int held = p.a[s], n = p.b[s];
+    if (n == 0) continue;  // the same in all lanes of a sequence
+    const int end = (held + n + kPage - 1) / kPage;
+    int* row = p.table + (long long)s * p.max_blocks;
+    int next = need[s];
+    for (int c0 = (held + kPage - 1) / kPage; c0 < end; c0 += kSeqLanes) {
+      const int c = c0 + sub;
+      const bool fresh = c < end && row[c] == -1;
+      const unsigned m = __ballot_sync(peers, fresh) & peers;
+      if (fresh) row[c] = found[next + __popc(m & ((1u << lane) - 1u))];
+      next += __popc(m);
+    }
+  }
+  team.sync();
+  // Rows in launch order, each with its sequence by a search of the offsets.
+  for (int r = gtid; r < p.max_rows; r += NC * kPlanThreads) {
+    int seq = -1, pos = -1;
+    long long slot = -1;
+    if (r < rows) {
+      seq = seq_of_row(cu, p.num_seqs, r);
+      const int first = cu[seq], j = r - first, at_tok = p.a[seq] + j;
+      int depth = j;
+      if (p.mode != VA_MODE_CHAIN && extend_is_tree(p, seq)) {
+        depth = 0;
+        for (int u = p.parent[r]; u >= 0; u = p.parent[first + u]) ++depth;
+      }
+      pos = p.a[seq] + depth;
+      slot = (long long)p.table[(long long)seq * p.max_blocks + at_tok / kPage] * kPage + at_tok % kPage;
+    }
+    p.row_seq[r] = seq;
+    p.position[r] = pos;
+    p.slot[r] = slot;
+  }
+}
+
 // Pull the live pages together: with N pages in use, the k-th page in use
 // at or above N moves to the k-th hole below N.  Workspace: new place of
 // each page [num_blocks].
@@ -623,6 +851,43 @@ va_status verify_attn_pages_compact(const va_page_pool* pool, int32_t* copies, i
   q.ws = (int*)ws;
   cudaError_t e = launch_plan(pages_compact_kernel<1>, pages_compact_kernel<kWideCtas>,
                               pool->num_blocks + (long long)pool->num_seqs * pool->max_blocks_per_seq, cs, q);
+  return e == cudaSuccess ? VA_OK : note_cuda(e);
+}
+
+size_t verify_attn_pages_extend_workspace_size(const va_page_pool* pool) {
+  if (check_pool(pool) != VA_OK) return 0;
+  return pages_ws_bytes(pool, 0);
+}
+
+va_status verify_attn_pages_extend(const va_page_pool* pool, const va_extend* x, int32_t mode, int32_t* cu_rows,
+                                   int32_t* row_seq, int32_t* position, int64_t* slot, void* ws, size_t ws_bytes,
+                                   uint32_t* status, void* stream) {
+  va_status st = check_pool(pool);
+  if (st != VA_OK) return st;
+  if (!x || mode < VA_MODE_CHAIN || mode > VA_MODE_MIXED) return VA_ERR_INVALID_ARG;
+  if (!x->ctx_len || !x->rows || x->max_rows < 0 || !cu_rows) return VA_ERR_INVALID_ARG;
+  if (x->max_rows > (1 << 30)) return VA_ERR_UNSUPPORTED;
+  if (x->max_rows > 0 && (!row_seq || !position || !slot)) return VA_ERR_INVALID_ARG;
+  if (mode != VA_MODE_CHAIN && x->max_rows > 0 && !x->parent) return VA_ERR_INVALID_ARG;
+  if (mode == VA_MODE_MIXED && !x->seq_kind) return VA_ERR_INVALID_ARG;
+  if ((uintptr_t)slot % 8) return VA_ERR_ALIGNMENT;
+  cudaStream_t cs = (cudaStream_t)stream;
+  st = check_plan(pages_ws_bytes(pool, 0), ws, ws_bytes, cs);
+  if (st != VA_OK) return st;
+  PageParams q = page_params(pool, status);
+  q.a = x->ctx_len;
+  q.b = x->rows;
+  q.ws = (int*)ws;
+  q.mode = mode;
+  q.max_rows = x->max_rows;
+  q.parent = x->parent;
+  q.kind = x->seq_kind;
+  q.cu = cu_rows;
+  q.row_seq = row_seq;
+  q.position = position;
+  q.slot = (long long*)slot;
+  cudaError_t e = launch_plan(pages_extend_kernel<1>, pages_extend_kernel<kWideCtas>,
+                              pool->num_blocks + 8LL * pool->num_seqs + 4LL * x->max_rows, cs, q);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }
 
