@@ -154,5 +154,8 @@ __device__ __forceinline__ long long latent_slot(const LatentParams& p, int slot
 cudaError_t launch_latent_simt(const LatentParams& p, dim3 grid, cudaStream_t st);
 cudaError_t launch_latent_merge(const LatentParams& p, cudaStream_t st);
 int latent_simt_rows();
+cudaError_t launch_latent_umma(const LatentParams& p, dim3 grid, cudaStream_t st);
+int latent_umma_rows();
+int latent_umma_parts(int value_dim, bool prompt);
 
 }  // namespace va

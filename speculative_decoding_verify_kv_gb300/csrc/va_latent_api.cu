@@ -48,7 +48,7 @@ static va_status check_latent(const va_problem* p, const va_latent* kv, int mode
   if (mode == VA_MODE_MIXED && !p->seq_kind) return VA_ERR_INVALID_ARG;
   if (kv->page_size == 0) {
     if (kv->capacity < 1) return VA_ERR_INVALID_ARG;
-    if (kv->capacity % kPage || kv->capacity > (1LL << 30)) return VA_ERR_UNSUPPORTED;
+    if (kv->capacity % kPage || kv->capacity > (1LL << 28)) return VA_ERR_UNSUPPORTED;
   } else if (kv->page_size == kPage) {
     if (!kv->block_table || kv->max_blocks_per_seq < 1 || kv->num_blocks < 1) return VA_ERR_INVALID_ARG;
     if (kv->max_blocks_per_seq > (1 << 26)) return VA_ERR_UNSUPPORTED;
@@ -79,10 +79,17 @@ static va_status check_prompt(const va_problem* p, const va_prompt* kv) {
 static LatentPlan plan_rows(const va_problem* p, int dtype, int value_dim, bool prompt) {
   LatentPlan pl;
   memset((void*)&pl, 0, sizeof(pl));
-  pl.kernel = VA_KERNEL_CUDA_CORES;
-  pl.rows_per_block = latent_simt_rows();
-  pl.parts = 1;
-  pl.per_sm = 2;
+  if (dtype == VA_BF16 && !(p->flags & VA_FLAG_CUDA_CORES)) {
+    pl.kernel = VA_KERNEL_TENSOR;
+    pl.rows_per_block = latent_umma_rows();
+    pl.parts = latent_umma_parts(value_dim, prompt);
+    pl.per_sm = 1;
+  } else {
+    pl.kernel = VA_KERNEL_CUDA_CORES;
+    pl.rows_per_block = latent_simt_rows();
+    pl.parts = 1;
+    pl.per_sm = 2;
+  }
   pl.slots = p->num_splits;
   const long long rows = (long long)p->max_rows_per_seq * (prompt ? 1 : p->num_heads);
   const long long blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
@@ -152,7 +159,7 @@ static va_status check_outputs(const LatentPlan& pl, const void* ws, size_t ws_b
 }
 
 static va_status launch(const LatentParams& q, const LatentPlan& pl, cudaStream_t cs) {
-  cudaError_t e = launch_latent_simt(q, pl.grid, cs);
+  cudaError_t e = pl.kernel == VA_KERNEL_TENSOR ? launch_latent_umma(q, pl.grid, cs) : launch_latent_simt(q, pl.grid, cs);
   if (e == cudaSuccess && pl.slots > 1) e = launch_latent_merge(q, cs);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }

@@ -1,0 +1,654 @@
+// Tensor-core attention over latent caches (absorbed form) and expanded prompt
+// keys, bf16: tcgen05 + TMEM + TMA, 128 query rows to a CTA.
+//
+// Per tile of NT tokens:
+//   S = Q K^T     tcgen05.mma into one of two S buffers in TMEM
+//   softmax       eight warps, one TMEM lane (query row) per thread and half
+//                 of the tile's columns per warp; online (m, l) in log2 units,
+//                 O rescaled only when the maximum grows by more than 2^8; P
+//                 in bf16 over S's place
+//   O += P V      tcgen05.mma, A = P (TMEM), B = V tile (MN-major)
+// so that S of the next tile runs under this tile's softmax.
+//
+// Absorbed form: a token has one row of DK values and V is the first of them,
+// so the column blocks of V are loaded once and read by both products (as K
+// they are K-major, as V MN-major: the same bytes).  O of 512 columns would
+// take all of TMEM and leave none for S: with latent_dim 512 two CTAs share a
+// row block, each computes S and the softmax whole and half of O's columns
+// (832 instead of 1,088 of the 2 x 544 multiply-adds of an even split; what
+// would avoid it, exchanging S or P between the two, waits on the other CTA
+// in every tile).  The queries of the V columns go to TMEM, those of the other
+// columns stay in shared memory.
+//
+// Shared memory holds two rings of 64-column blocks of a tile: V stages of
+// VBLK blocks, freed by P.V, and single blocks of the key's other columns,
+// freed as soon as S has read them.
+//
+// Every wait is bounded (VA_DEV_TIMEOUT); on a timeout the CTA drains its own
+// copies and MMAs, frees TMEM and writes NaN.
+#include <string.h>
+
+#include "va_latent.cuh"
+#include "va_sm100.cuh"
+#include "va_tma.h"
+
+namespace va {
+using namespace sm100;
+
+constexpr int kLuM = 128;
+constexpr int kLuThreads = 384;
+constexpr uint64_t kLuWaitNs = 2000000000ull;
+constexpr int kLuPrefetch = 4;  // tiles that a cache's pages are pulled into L2 ahead
+
+template <int DK_, int DV_, bool PROMPT_>
+struct LuCfg {
+  static constexpr int DK = DK_;                     // key width
+  static constexpr int DV = DV_;                     // value width
+  static constexpr bool PROMPT = PROMPT_;
+  static constexpr int PARTS = DV > 256 ? 2 : 1;     // CTAs that share O's columns
+  static constexpr int DO = DV / PARTS;              // O columns of a CTA
+  static constexpr int NT = PROMPT ? 128 : 64;       // tokens per tile
+  static constexpr int BLK = NT * 128;               // bytes of a 64-column block
+  static constexpr int VBLK = DO / 64;               // blocks of a V stage
+  static constexpr int KBLK = PROMPT ? DK / 64 : DK / 64 - VBLK;  // other blocks of the key
+  static constexpr int QT = PROMPT ? DK : DO;        // query columns in TMEM
+  static constexpr int QS = DK - QT;                 // query columns in shared memory
+  static constexpr int NV = PROMPT ? (DV == 128 ? 2 : 4) : (DV == 512 ? 3 : 5);  // V stages
+  static constexpr int NK = PROMPT ? (DV == 128 ? 9 : 6) : (DV == 512 ? 6 : 5);  // key blocks
+  static constexpr int COL_O = 0;
+  static constexpr int COL_S = DO;
+  static constexpr int COL_Q = DO + 2 * NT;
+  static constexpr int OFF_V = 0;
+  static constexpr int OFF_K = NV * VBLK * BLK;
+  static constexpr int OFF_Q = OFF_K + NK * BLK;
+  static constexpr int OFF_END = OFF_Q + QS / 64 * kLuM * 128;
+  // The queries on their way to TMEM: in the last blocks of a ring.
+  static constexpr int QSTAGE = PROMPT ? OFF_Q - QT / 64 * kLuM * 128 : OFF_K - QT / 64 * kLuM * 128;
+  // First tile (V stage) or block (key ring) whose place they have.
+  static constexpr int QV_FIRST = PROMPT ? 1 << 30 : QSTAGE / (VBLK * BLK);
+  static constexpr int QK_FIRST = PROMPT ? (QSTAGE - OFF_K) / BLK : 1 << 30;
+  static constexpr int OROW = DO * 4 + 16;           // O staging at the end, padded rows
+  static constexpr int NB = 11 + 2 * NV + 2 * NK;    // barriers
+  static constexpr int OFF_RED = OFF_END > kLuM * OROW ? OFF_END : kLuM * OROW;
+  static constexpr int OFF_BAR = OFF_RED + 2 * 2 * kLuM * 4;
+  static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
+  static_assert(COL_Q + QT / 2 <= 512, "TMEM columns");
+  static_assert(QSTAGE >= (PROMPT ? OFF_K + KBLK * BLK : VBLK * BLK), "tile 0 beside the queries");
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+enum { LB_SFULL = 0, LB_PFULL = 2, LB_SFREE = 4, LB_QLAND = 6, LB_QREADY = 7, LB_OFINAL = 8, LB_FIX = 9, LB_SDRAIN = 10, LB_RING = 11 };
+
+struct LuMaps {
+  CUtensorMap q, k, r;  // queries; cache or expanded keys and values; rope part of prompt keys
+};
+
+__device__ __forceinline__ float lu_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+template <class C>
+__global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const LatentParams p, const __grid_constant__ LuMaps maps) {
+  constexpr int NT = C::NT, NC = NT / 2, DO = C::DO;
+  constexpr bool PROMPT = C::PROMPT;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
+  float* red = reinterpret_cast<float*>(sm + C::OFF_RED);  // [2][2][kLuM]
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sm + C::OFF_BAR + C::NB * 8);
+  volatile int* abort_p = reinterpret_cast<volatile int*>(tmem_at + 1);
+  int* err_s = reinterpret_cast<int*>(tmem_at + 2);
+
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int s = blockIdx.z;
+  const int head = PROMPT ? blockIdx.y : 0, part = PROMPT ? 0 : blockIdx.y;
+  const LatentSeq q = latent_seq(p, s);
+  if (q.err & VA_DEV_BAD_ROWS) {
+    if (tid == 0) flag(p.status, q.err);
+    if (blockIdx.x == 0 && part == 0) latent_nan_rows(p, s, head, PROMPT ? 1 : p.H);
+    return;
+  }
+  const int R = latent_rows(p, q.n);
+  const int blocks = (R + kLuM - 1) / kLuM;
+  if (blocks == 0) return;
+  const int nchunk = latent_chunks(p, q.n);
+  const int rb = blockIdx.x % blocks, chunk = blockIdx.x / blocks;
+  const int live = latent_live(q.err ? 0 : q.len, nchunk);
+  if (chunk >= live) return;
+  const int rbase = rb * kLuM, nrows = min(kLuM, R - rbase);
+  const int jfirst = PROMPT ? rbase : rbase / p.H;
+  const int jlast = PROMPT ? rbase + nrows - 1 : (rbase + nrows - 1) / p.H;
+  int lo, hi;
+  latent_range(q.len, nchunk, chunk, &lo, &hi);
+  hi = max(lo, min(hi, latent_end(p, q, jlast)));
+  const int ntiles = q.err ? 0 : (hi - lo + NT - 1) / NT;
+  // Tokens below it are seen by every row of the block.
+  const int all_see = q.kind == 1 ? min(hi, q.ctx) : (PROMPT && !p.causal) ? hi : min(hi, q.ctx + jfirst + 1);
+
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  auto vfull = [&](int i) { return bar(LB_RING + i); };
+  auto vfree = [&](int i) { return bar(LB_RING + C::NV + i); };
+  auto kfull = [&](int i) { return bar(LB_RING + 2 * C::NV + i); };
+  auto kfree = [&](int i) { return bar(LB_RING + 2 * C::NV + C::NK + i); };
+  const uint32_t base = smem_u32(sm);
+
+  if (tid == 0) {
+    *err_s = 0;
+    *abort_p = 0;
+    for (int i = 0; i < C::NB; ++i)
+      mbar_init(bar(i), i == LB_PFULL || i == LB_PFULL + 1 || i == LB_QREADY ? 8 : 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_at), 512);
+    tmem_relinquish();
+  }
+  // This thread's query row, its mask, and the chunk's pages.
+  const int quad = warp & 3;
+  const int r = quad * 32 + lane;
+  const bool is_sm = warp >= 2 && warp < 10;
+  const bool rvalid = is_sm && r < nrows;
+  const int j = rvalid ? (PROMPT ? rbase + r : (rbase + r) / p.H) : 0;
+  __syncthreads();
+  unsigned anc = 0u;
+  if (rvalid && !q.err && q.kind == 1) {
+    bool bad = false;
+    anc = row_mask(1, p.parent + q.row0, j, &bad);
+    if (bad) atomicOr(err_s, (int)VA_DEV_BAD_PARENT);
+  }
+  if (!PROMPT && p.page_size && ntiles > 0) {
+    for (int pg = lo / kPage + tid; pg < (hi + kPage - 1) / kPage; pg += kLuThreads) {
+      const int blk = p.block_table[(long long)s * p.max_blocks + pg];
+      if (blk < 0 || blk >= p.num_blocks) atomicOr(err_s, (int)VA_DEV_BAD_BLOCK);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const unsigned err = q.err | (unsigned)*err_s;
+  const uint32_t tm = *tmem_at;
+  const int work = err ? 0 : ntiles;
+  if (err && tid == 0) flag(p.status, err);
+  auto fail = [&]() {
+    *abort_p = 1;
+    flag(p.status, VA_DEV_TIMEOUT);
+  };
+  auto drain = [&](uint32_t b, uint32_t parity) {
+    int dummy = 0;
+    mbar_wait(b, parity, &dummy, kLuWaitNs);
+  };
+
+  if (work == 0) {
+    // nothing to read: straight to the outputs
+  } else if (warp == 0 || warp == 10) {
+    // ---------------------------------------------------------------- producers
+    // Warp 10: the V stages.  Warp 0: the queries, the key's other blocks, and
+    // pages into L2.  Absorbed form: lane l < 4 loads the tile's page l.
+    const bool keys = warp == 0;
+    auto page_of = [&](int t) {  // (row, plane) of a page's tokens in the cache's map
+      const int pg = t / kPage;
+      return p.page_size ? make_int2(0, p.block_table[(long long)s * p.max_blocks + pg]) : make_int2(pg * kPage, s);
+    };
+    auto load_block = [&](uint32_t dst, int t0, int col, int pages, int2 at, uint32_t b) {
+      if (PROMPT) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(b, C::BLK);
+          if (col >= C::DK - kLatentRope && keys) tma_load_2d(dst, &maps.r, 0, (int)q.key0 + t0, b);
+          else tma_load_3d(dst, &maps.k, col, head, (int)q.key0 + t0, b);
+        }
+      } else {
+        if (lane == 0) mbar_arrive_expect_tx(b, (uint32_t)pages * kPage * 128);
+        __syncwarp();
+        if (lane < pages) tma_load_3d(dst + lane * kPage * 128, &maps.k, col, at.x, at.y, b);
+      }
+    };
+    bool ok = true;
+    int issued = 0;  // tiles (V) or blocks (keys)
+    if (keys && lane == 0) {
+      mbar_arrive_expect_tx(bar(LB_QLAND), C::DK / 64 * kLuM * 128);
+      for (int c = 0; c < C::DK / 64; ++c) {
+        // Absorbed form: the columns of this part's V come first, in TMEM.
+        const int col = PROMPT ? c * 64 : c < C::VBLK ? (part * C::VBLK + c) * 64
+                                        : (c - C::VBLK < part * C::VBLK ? c - C::VBLK : c) * 64;
+        const uint32_t dst = base + (c < C::QT / 64 ? C::QSTAGE + c * kLuM * 128 : C::OFF_Q + (c - C::QT / 64) * kLuM * 128);
+        if (PROMPT) tma_load_3d(dst, &maps.q, col, head, q.row0 + rbase, bar(LB_QLAND));
+        else tma_load_2d(dst, &maps.q, col, q.row0 * p.H + rbase, bar(LB_QLAND));
+      }
+    }
+    for (int i = 0; i < work && ok; ++i) {
+      const int t0 = lo + i * NT;
+      const int pages = PROMPT ? 0 : (min(NT, hi - t0) + kPage - 1) / kPage;
+      int2 at = make_int2(0, 0);
+      if (!PROMPT && lane < pages) at = page_of(t0 + lane * kPage);
+      if (!keys) {
+        const int st = i % C::NV;
+        ok = (i != C::QV_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs)) &&
+             mbar_wait(vfree(st), ((i / C::NV) & 1) ^ 1, abort_p, kLuWaitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t dst = base + C::OFF_V + st * C::VBLK * C::BLK;
+        if (PROMPT) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(vfull(st), C::VBLK * C::BLK);
+            for (int c = 0; c < C::VBLK; ++c)
+              tma_load_3d(dst + c * C::BLK, &maps.k, C::DK - kLatentRope + c * 64, head, (int)q.key0 + t0, vfull(st));
+          }
+        } else {
+          if (lane == 0) mbar_arrive_expect_tx(vfull(st), (uint32_t)(C::VBLK * pages * kPage * 128));
+          __syncwarp();
+          if (lane < pages)
+            for (int c = 0; c < C::VBLK; ++c)
+              tma_load_3d(dst + c * C::BLK + lane * kPage * 128, &maps.k, (part * C::VBLK + c) * 64, at.x, at.y, vfull(st));
+        }
+        issued = i + 1;
+      } else {
+        for (int c = 0; c < C::KBLK && ok; ++c) {
+          const int n = i * C::KBLK + c, st = n % C::NK;
+          ok = (n != C::QK_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs)) &&
+               mbar_wait(kfree(st), ((n / C::NK) & 1) ^ 1, abort_p, kLuWaitNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const int col = PROMPT ? c * 64 : (c < part * C::VBLK ? c : c + C::VBLK) * 64;
+          load_block(base + C::OFF_K + st * C::BLK, t0, col, pages, at, kfull(st));
+          issued = n + 1;
+        }
+        // Whole pages ahead into L2; two CTAs that share them take half each.
+        if (!PROMPT && lane < 4 / C::PARTS) {
+          const int t = t0 + kLuPrefetch * NT + (lane * C::PARTS + part) * kPage;
+          if (t < hi) {
+            const int2 a = page_of(t);
+            const long long row = p.page_size ? (long long)a.y * kPage : (long long)s * p.capacity + a.x;
+            bulk_prefetch_l2(reinterpret_cast<const unsigned short*>(p.cache) + row * C::DK, kPage * C::DK * 2);
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) fail();
+    if (!keys && ok && (hi - lo) % NT != 0) {
+      // Tokens behind the range may hold anything: their V is cleared (their
+      // scores are masked).
+      const int i = work - 1, st = i % C::NV, valid = hi - lo - i * NT, rows = NT - valid;
+      if (__all_sync(0xffffffffu, mbar_wait(vfull(st), (i / C::NV) & 1, abort_p, kLuWaitNs))) {
+        unsigned char* at = sm + C::OFF_V + st * C::VBLK * C::BLK;
+        for (int u = lane; u < C::VBLK * rows * 8; u += 32)
+          *reinterpret_cast<uint4*>(at + u / (rows * 8) * C::BLK + (valid + u / 8 % rows) * 128 + (u & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(LB_FIX));
+      } else if (lane == 0) {
+        fail();
+      }
+    }
+    // No copy may still be landing when the CTA goes away.
+    if (*abort_p && lane == 0) {
+      if (keys) drain(bar(LB_QLAND), 0);
+      const int n = keys ? C::NK : C::NV;
+      for (int i = max(0, issued - n); i < issued; ++i) drain(keys ? kfull(i % n) : vfull(i % n), (i / n) & 1);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- S issuer
+    if (lane == 0) {
+      constexpr uint32_t ID = idesc_f16(kLuM, NT, true, false);
+      bool ok = mbar_wait(bar(LB_QLAND), 0, abort_p, kLuWaitNs) && mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs);
+      bool any = false;
+      for (int i = 0; i < work && ok; ++i) {
+        const int b = i & 1;
+        const uint32_t scol = tm + C::COL_S + b * NT;
+        if (i >= 2) ok = mbar_wait(bar(LB_SFREE + b), ((i - 2) >> 1) & 1, abort_p, kLuWaitNs);
+        if (!PROMPT) {
+          const int st = i % C::NV;
+          ok = ok && mbar_wait(vfull(st), (i / C::NV) & 1, abort_p, kLuWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = sdesc_sw128(base + C::OFF_V + st * C::VBLK * C::BLK, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < C::VBLK * 4; ++kk)
+            mma_ts(scol, tm + C::COL_Q + kk * 8, kd + (uint64_t)(((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4), ID,
+                   kk > 0 ? 1u : 0u);
+          any = true;
+        }
+        for (int c = 0; c < C::KBLK && ok; ++c) {
+          const int n = i * C::KBLK + c, st = n % C::NK;
+          ok = mbar_wait(kfull(st), (n / C::NK) & 1, abort_p, kLuWaitNs);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = sdesc_sw128(base + C::OFF_K + st * C::BLK, 16, 1024);
+          const uint64_t qd = sdesc_sw128(base + C::OFF_Q + c * kLuM * 128, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (PROMPT) mma_ts(scol, tm + C::COL_Q + (c * 4 + kk) * 8, kd + kk * 2, ID, c > 0 || kk > 0 ? 1u : 0u);
+            else mma_ss(scol, qd + kk * 2, kd + kk * 2, ID, 1u);
+          }
+          any = true;
+          mma_commit(kfree(st));
+        }
+        if (!ok) break;
+        mma_commit(bar(LB_SFULL + b));
+      }
+      if (!ok) {
+        fail();
+        // What was issued completes before TMEM and shared memory go.
+        if (any) {
+          mma_commit(bar(LB_SDRAIN));
+          drain(bar(LB_SDRAIN), 0);
+        }
+      }
+    }
+  } else if (warp == 11) {
+    // ---------------------------------------------------------------- P.V issuer
+    if (lane == 0) {
+      constexpr uint32_t ID = idesc_f16(kLuM, DO, true, true);
+      bool ok = true, any = false;
+      for (int i = 0; i < work; ++i) {
+        const int b = i & 1, st = i % C::NV;
+        ok = mbar_wait(bar(LB_PFULL + b), (i >> 1) & 1, abort_p, kLuWaitNs) &&
+             mbar_wait(vfull(st), (i / C::NV) & 1, abort_p, kLuWaitNs) &&
+             (i < work - 1 || (hi - lo) % NT == 0 || mbar_wait(bar(LB_FIX), 0, abort_p, kLuWaitNs));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t vd = sdesc_sw128(base + C::OFF_V + st * C::VBLK * C::BLK, C::BLK, 1024);
+#pragma unroll
+        for (int kk = 0; kk < NT / 16; ++kk)
+          mma_ts(tm + C::COL_O, tm + C::COL_S + b * NT + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), ID,
+                 i > 0 || kk > 0 ? 1u : 0u);
+        any = true;
+        mma_commit(bar(LB_SFREE + b));
+        mma_commit(vfree(st));
+      }
+      if (!ok) fail();
+      if (any) {
+        // After every P.V, in a failed run too.
+        mma_commit(bar(LB_OFINAL));
+        drain(bar(LB_OFINAL), 0);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int half = (warp - 2) >> 2;
+    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    const bool warp_live = __any_sync(0xffffffffu, rvalid);
+    bool ok = __all_sync(0xffffffffu, mbar_wait(bar(LB_QLAND), 0, abort_p, kLuWaitNs));
+    if (ok) {
+      // Query row -> TMEM: this half's 16-byte pieces of the swizzled blocks.
+      // (Rows behind the block's last hold other rows, or zeros: no one reads
+      // what comes of them.)
+      constexpr int PIECES = C::QT / 16;  // per half
+#pragma unroll 1
+      for (int c0 = half * PIECES; c0 < (half + 1) * PIECES; c0 += 4) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = c0 + k;
+          const uint4 v = *reinterpret_cast<const uint4*>(sm + C::QSTAGE + c / 8 * kLuM * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+          w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+        }
+        tmem_st16(tm + lanes + C::COL_Q + c0 * 4, w);
+      }
+      tmem_wait_st();
+      // Copies will write where these reads were.
+      fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(LB_QREADY));
+
+    float m_use = -INFINITY, l_run = 0.f;
+    const float c_r = p.scale_log2;
+    // A failed wait does not leave the loop: every iteration has one named
+    // barrier shared with the partner warp.
+    for (int i = 0; i < work; ++i) {
+      const int b = i & 1;
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(LB_SFULL + b), (i >> 1) & 1, abort_p, kLuWaitNs))) ok = false;
+      tc_fence_after();
+      const uint32_t scol = tm + lanes + C::COL_S + b * NT;
+      const int t0 = lo + i * NT + NC * half;
+      float sv[NC];
+      float mx = -INFINITY;
+      if (ok && warp_live) {
+        uint32_t sr[NC];
+        tmem_ld32_into<0>(scol + NC * half, sr);
+        if constexpr (NC > 32) tmem_ld32_into<NC - 32>(scol + NC * half + 32, sr);
+        tmem_wait_ld();
+        if (lo + (i + 1) * NT <= all_see) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            sv[c] = __uint_as_float(sr[c]);
+            mx = fmaxf(mx, sv[c]);
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < NC / 32; ++w) {
+            const unsigned vis = rvalid ? latent_bits(p, q, anc, j, hi, t0 + 32 * w) : 0u;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              sv[32 * w + c] = (vis >> c) & 1u ? __uint_as_float(sr[32 * w + c]) : -INFINITY;
+              mx = fmaxf(mx, sv[32 * w + c]);
+            }
+          }
+        }
+      }
+      // The row's maximum over both halves (raw scores; c_r > 0).
+      red[(b * 2 + half) * kLuM + r] = mx;
+      bar_sync(5 + quad, 64);
+      mx = fmaxf(mx, red[(b * 2 + (half ^ 1)) * kLuM + r]);
+      const float mt = mx * c_r;
+      const bool need = rvalid && m_use != -INFINITY && mt > m_use + 8.f;
+      const float m_new = m_use == -INFINITY || need ? mt : m_use;
+      if (ok && __any_sync(0xffffffffu, need)) {
+        // Rescale this half of the warp's O rows once the previous P.V landed.
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(LB_SFREE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_p, kLuWaitNs)))
+          ok = false;
+        if (ok) {
+          tc_fence_after();
+          const float f = need ? exp2f(m_use - m_new) : 1.f;
+#pragma unroll 1
+          for (int c0 = half * (DO / 2); c0 < (half + 1) * (DO / 2); c0 += 16) {
+            uint32_t o[16];
+            tmem_ld16(tm + lanes + C::COL_O + c0, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            tmem_st16(tm + lanes + C::COL_O + c0, o);
+          }
+          tmem_wait_st();
+          l_run *= f;
+        }
+      }
+      m_use = m_new;
+      if (ok && warp_live) {
+        uint32_t ph[NC / 2];
+        float l0 = 0.f, l1 = 0.f;
+        // A masked score (-inf) gives 0; while nothing of the row was visible
+        // every score is masked, and the 0 offset keeps them at -inf.
+        const float mneg = m_use == -INFINITY ? 0.f : -m_use;
+#pragma unroll
+        for (int c = 0; c < NC / 2; ++c) {
+          const float a = lu_ex2(fmaf(sv[2 * c], c_r, mneg));
+          const float d = lu_ex2(fmaf(sv[2 * c + 1], c_r, mneg));
+          l0 += a;
+          l1 += d;
+          // Rounded to bf16 (2^-8 at most): the matrix unit takes 16 bits, and
+          // a second part for the rest would cost P.V again, for an o that is
+          // rounded alike.
+          const __nv_bfloat162 h = __floats2bfloat162_rn(a, d);
+          ph[c] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        l_run += l0 + l1;
+        if constexpr (NC == 32) tmem_st16(scol + 16 * half, ph);
+        else tmem_st32_from<0>(scol + 32 * half, ph);
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(LB_PFULL + b));
+    }
+    if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(LB_OFINAL), 0, abort_p, kLuWaitNs))) ok = false;
+    if (!ok && lane == 0) fail();
+    tc_fence_after();
+    red[half * kLuM + r] = l_run;
+    bar_sync(5 + quad, 64);
+    const float l = red[r] + red[kLuM + r];
+    const bool bad = __any_sync(0xffffffffu, *abort_p != 0);
+    const float inv = bad ? NAN : l > 0.f ? 1.f / l : 0.f;
+    if (rvalid && half == 0 && part == 0) {
+      const long long item = latent_item(p, q.row0, rbase + r, head);
+      if (live > 1) {
+        const long long si = latent_slot(p, chunk, item);
+        p.ws_ml[2 * si] = bad ? NAN : m_use;
+        p.ws_ml[2 * si + 1] = bad ? NAN : l;
+      } else {
+        p.lse[item] = bad ? NAN : l > 0.f ? (m_use + log2f(l)) * kLn2 : -INFINITY;
+      }
+    }
+    // O rows through shared memory (its rings are idle now) to coalesced
+    // stores; fp32 sums for the merge, or the finished bf16 row.
+    if (warp_live) {
+#pragma unroll 1
+      for (int c0 = half * (DO / 2); c0 < (half + 1) * (DO / 2); c0 += 32) {
+        uint32_t o[32];
+        tmem_ld32(tm + lanes + C::COL_O + c0, o);
+        tmem_wait_ld();
+        unsigned char* row = sm + r * C::OROW;
+        if (live > 1) {
+          if (bad) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) o[c] = 0x7fffffffu;
+          }
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            *reinterpret_cast<uint4*>(row + (c0 + c) * 4) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            // A row that sees nothing has no sum (its lanes of O may hold anything).
+            const __nv_bfloat162 h = l > 0.f || bad ? __floats2bfloat162_rn(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv)
+                                                    : __floats2bfloat162_rn(0.f, 0.f);
+            w[c] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+#pragma unroll
+          for (int c = 0; c < 16; c += 4)
+            *reinterpret_cast<uint4*>(row + c0 * 2 + c * 4) = make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
+        }
+      }
+    }
+    bar_sync(1, 256);
+    const int pieces = live > 1 ? DO / 4 : DO / 8;  // of 16 bytes
+    for (int u = tid - 64; u < nrows * pieces; u += 256) {
+      const int row = u / pieces, c = u % pieces;
+      const long long item = latent_item(p, q.row0, rbase + row, head);
+      const uint4 v = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
+      if (live > 1) *reinterpret_cast<uint4*>(p.ws_acc + latent_slot(p, chunk, item) * C::DV + part * DO + c * 4) = v;
+      else *reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.o) + item * C::DV + part * DO + c * 8) = v;
+    }
+  }
+
+  if (work == 0) {
+    // An error, a chunk that the block's rows see nothing of, or no keys.
+    for (int u = tid; u < nrows * DO; u += kLuThreads) {
+      const int row = u / DO, d = u % DO;
+      const long long item = latent_item(p, q.row0, rbase + row, head);
+      if (live > 1) {
+        if (d == 0 && part == 0) {
+          const long long si = latent_slot(p, chunk, item);
+          p.ws_ml[2 * si] = err ? NAN : -INFINITY;
+          p.ws_ml[2 * si + 1] = err ? NAN : 0.f;
+        }
+      } else {
+        reinterpret_cast<unsigned short*>(p.o)[item * C::DV + part * DO + d] = err ? 0x7fffu : 0u;
+        if (d == 0 && part == 0) p.lse[item] = err ? NAN : -INFINITY;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tm, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Tiled map of bf16 rows in boxes of 64 columns, 128-byte swizzle.
+static bool lu_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box) {
+  const EncodeTiledFn fn = encode_fn();
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static bool lu_maps(LuMaps* m, const LatentParams& p, int tile) {
+  memset(m, 0, sizeof(*m));
+  const cuuint64_t dk = (cuuint64_t)p.DK, H = (cuuint64_t)p.H;
+  if (!p.prompt) {
+    const cuuint64_t qd[2] = {dk, (cuuint64_t)p.total_rows * H}, qs[1] = {dk * 2};
+    const cuuint32_t qb[2] = {64, kLuM}, kb[3] = {64, kPage, 1};
+    const cuuint64_t rows = p.page_size ? (cuuint64_t)kPage : (cuuint64_t)p.capacity;
+    const cuuint64_t kd[3] = {dk, rows, (cuuint64_t)(p.page_size ? p.num_blocks : p.num_seqs)};
+    const cuuint64_t ks[2] = {dk * 2, rows * dk * 2};
+    return lu_map(&m->q, p.q, 2, qd, qs, qb) && lu_map(&m->k, p.cache, 3, kd, ks, kb);
+  }
+  const cuuint64_t qd[3] = {dk, H, (cuuint64_t)p.total_rows}, qs[2] = {dk * 2, H * dk * 2};
+  const cuuint32_t qb[3] = {64, 1, kLuM}, kb[3] = {64, 1, (cuuint32_t)tile}, rb[2] = {64, (cuuint32_t)tile};
+  if (!lu_map(&m->q, p.q, 3, qd, qs, qb)) return false;
+  if (p.total_kv == 0) return true;  // no tile, no load
+  const cuuint64_t w = dk - kLatentRope + (cuuint64_t)p.DV, T = (cuuint64_t)p.total_kv;
+  const cuuint64_t kd[3] = {w, H, T}, ks[2] = {w * 2, H * w * 2};
+  const cuuint64_t rd[2] = {kLatentRope, T}, rs[1] = {(cuuint64_t)(T > 1 ? p.kr_stride : kLatentRope) * 2};
+  return lu_map(&m->k, p.kv, 3, kd, ks, kb) && lu_map(&m->r, p.k_rope, 2, rd, rs, rb);
+}
+
+template <class C>
+static cudaError_t launch_umma_latent(const LatentParams& p, dim3 grid, cudaStream_t st) {
+  static std::atomic<unsigned long long> ready{0ull};
+  cudaError_t e = allow_smem(latent_umma_kernel<C>, C::SMEM, ready);
+  if (e != cudaSuccess) return e;
+  LuMaps m;
+  if (!lu_maps(&m, p, C::NT)) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof(cfg));
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kLuThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, latent_umma_kernel<C>, p, m);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+int latent_umma_rows() { return kLuM; }
+int latent_umma_parts(int value_dim, bool prompt) { return !prompt && value_dim > 256 ? 2 : 1; }
+
+cudaError_t launch_latent_umma(const LatentParams& p, dim3 grid, cudaStream_t st) {
+  if (p.prompt)
+    return p.DV == 128 ? launch_umma_latent<LuCfg<192, 128, true>>(p, grid, st)
+                       : launch_umma_latent<LuCfg<128, 64, true>>(p, grid, st);
+  return p.DV == 512 ? launch_umma_latent<LuCfg<576, 512, false>>(p, grid, st)
+                     : launch_umma_latent<LuCfg<320, 256, false>>(p, grid, st);
+}
+
+}  // namespace va

@@ -68,6 +68,7 @@
 #include "va_common.cuh"
 #include "va_host.h"
 #include "va_sm100.cuh"
+#include "va_tma.h"
 #include "va_window_join.cuh"
 
 namespace va {
@@ -1321,26 +1322,6 @@ __global__ void __launch_bounds__(UCfg<D, KVT>::THREADS, 1) __maxnreg__((UCfg<D,
 
 // ---------------------------------------------------------------------------
 // Host side: tensor maps for the bf16 cache and the launch.
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = (EncodeTiledFn)ptr;
-  }
-  return fn;
-}
 
 // Tiled map over a bf16 cache: contiguous [plane][capacity][D] with boxes
 // {64, 64, 1} (by_page: {64, 16, 1}), or paged [block][KVH][16][D] with
