@@ -38,7 +38,6 @@ using namespace sm100;
 constexpr int kLuM = 128;
 constexpr int kLuThreads = 384;
 constexpr uint64_t kLuWaitNs = 2000000000ull;
-constexpr int kLuPrefetch = 4;  // tiles that a cache's pages are pulled into L2 ahead
 
 template <int DK_, int DV_, bool PROMPT_>
 struct LuCfg {
@@ -89,19 +88,67 @@ __device__ __forceinline__ float lu_ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+// MMAs and commits that a whole warp runs through and its elected lane (e != 0)
+// issues, with everything they are computed from known to be the warp's:
+// descriptors then live in uniform registers.  An issuing thread of its own
+// branch took some 100 cycles to an MMA, longer than one of 64 columns runs
+// (64 heads x 16 rows x 4 sequences of 8,000 tokens: 142 us against 112; prompts
+// of 2 x 2,048 rows, 128 heads, over 4,096 keys: 966 against 755).
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
+  return e;
+}
+
+__device__ __forceinline__ void mma_ts_by(uint32_t e, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-          dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(accumulate), "r"(e)
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+__device__ __forceinline__ void mma_ss_by(uint32_t e, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(accumulate), "r"(e)
+      : "memory");
+}
+
+__device__ __forceinline__ void commit_by(uint32_t e, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(e)
+      : "memory");
+}
+
+__device__ __forceinline__ void expect_by(uint32_t e, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(e)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_2d_by(uint32_t e, uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar), "r"(e)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_3d_by(uint32_t e, uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "r"(e)
       : "memory");
 }
 
@@ -118,7 +165,8 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
 
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // Broadcasts: what a warp has in common is known to be so.
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int s = blockIdx.z;
   const int head = PROMPT ? blockIdx.y : 0, part = PROMPT ? 0 : blockIdx.y;
   const LatentSeq q = latent_seq(p, s);
@@ -185,8 +233,9 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   __syncthreads();
   tc_fence_after();
   const unsigned err = q.err | (unsigned)*err_s;
-  const uint32_t tm = *tmem_at;
-  const int work = err ? 0 : ntiles;
+  const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_at, 0);
+  const int work = __shfl_sync(0xffffffffu, err ? 0 : ntiles, 0);
+  const bool ragged = __shfl_sync(0xffffffffu, (hi - lo) % NT, 0) != 0;  // of the last tile
   if (err && tid == 0) flag(p.status, err);
   auto fail = [&]() {
     *abort_p = 1;
@@ -201,89 +250,93 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     // nothing to read: straight to the outputs
   } else if (warp == 0 || warp == 10) {
     // ---------------------------------------------------------------- producers
-    // Warp 10: the V stages.  Warp 0: the queries, the key's other blocks, and
-    // pages into L2.  Absorbed form: lane l < 4 loads the tile's page l.
+    // Warp 10: the V stages.  Warp 0: the queries and the key's other blocks.
+    // Absorbed form: lane l < 4 looks the tile's page l up.
     const bool keys = warp == 0;
+    const uint32_t one = elected();
     auto page_of = [&](int t) {  // (row, plane) of a page's tokens in the cache's map
       const int pg = t / kPage;
       return p.page_size ? make_int2(0, p.block_table[(long long)s * p.max_blocks + pg]) : make_int2(pg * kPage, s);
     };
-    auto load_block = [&](uint32_t dst, int t0, int col, int pages, int2 at, uint32_t b) {
-      if (PROMPT) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(b, C::BLK);
-          if (col >= C::DK - kLatentRope && keys) tma_load_2d(dst, &maps.r, 0, (int)q.key0 + t0, b);
-          else tma_load_3d(dst, &maps.k, col, head, (int)q.key0 + t0, b);
-        }
-      } else {
-        if (lane == 0) mbar_arrive_expect_tx(b, (uint32_t)pages * kPage * 128);
-        __syncwarp();
-        if (lane < pages) tma_load_3d(dst + lane * kPage * 128, &maps.k, col, at.x, at.y, b);
-      }
-    };
+    const int lo_u = __shfl_sync(0xffffffffu, lo, 0), hi_u = __shfl_sync(0xffffffffu, hi, 0);
+    const int key0 = __shfl_sync(0xffffffffu, (int)q.key0, 0);
     bool ok = true;
     int issued = 0;  // tiles (V) or blocks (keys)
-    if (keys && lane == 0) {
-      mbar_arrive_expect_tx(bar(LB_QLAND), C::DK / 64 * kLuM * 128);
+    if (keys) {
+      const int qrow = __shfl_sync(0xffffffffu, PROMPT ? q.row0 + rbase : q.row0 * p.H + rbase, 0);
+      expect_by(one, bar(LB_QLAND), C::DK / 64 * kLuM * 128);
+#pragma unroll
       for (int c = 0; c < C::DK / 64; ++c) {
         // Absorbed form: the columns of this part's V come first, in TMEM.
         const int col = PROMPT ? c * 64 : c < C::VBLK ? (part * C::VBLK + c) * 64
                                         : (c - C::VBLK < part * C::VBLK ? c - C::VBLK : c) * 64;
         const uint32_t dst = base + (c < C::QT / 64 ? C::QSTAGE + c * kLuM * 128 : C::OFF_Q + (c - C::QT / 64) * kLuM * 128);
-        if (PROMPT) tma_load_3d(dst, &maps.q, col, head, q.row0 + rbase, bar(LB_QLAND));
-        else tma_load_2d(dst, &maps.q, col, q.row0 * p.H + rbase, bar(LB_QLAND));
+        if (PROMPT) tma_3d_by(one, dst, &maps.q, col, head, qrow, bar(LB_QLAND));
+        else tma_2d_by(one, dst, &maps.q, col, qrow, bar(LB_QLAND));
       }
     }
+    int st = 0;
+    uint32_t par = 1;
     for (int i = 0; i < work && ok; ++i) {
-      const int t0 = lo + i * NT;
-      const int pages = PROMPT ? 0 : (min(NT, hi - t0) + kPage - 1) / kPage;
-      int2 at = make_int2(0, 0);
-      if (!PROMPT && lane < pages) at = page_of(t0 + lane * kPage);
+      const int t0 = lo_u + i * NT;
+      const int pages = PROMPT ? 0 : (min(NT, hi_u - t0) + kPage - 1) / kPage;
+      int2 at[4];
+      if (!PROMPT) {
+        int2 a = make_int2(0, 0);
+        if (lane < pages) a = page_of(t0 + lane * kPage);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, g), __shfl_sync(0xffffffffu, a.y, g));
+      }
       if (!keys) {
-        const int st = i % C::NV;
-        ok = (i != C::QV_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs)) &&
-             mbar_wait(vfree(st), ((i / C::NV) & 1) ^ 1, abort_p, kLuWaitNs);
+        ok = (i != C::QV_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs)) && mbar_wait(vfree(st), par, abort_p, kLuWaitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t dst = base + C::OFF_V + st * C::VBLK * C::BLK;
+        const uint32_t dst = base + C::OFF_V + st * C::VBLK * C::BLK, b = vfull(st);
         if (PROMPT) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(vfull(st), C::VBLK * C::BLK);
-            for (int c = 0; c < C::VBLK; ++c)
-              tma_load_3d(dst + c * C::BLK, &maps.k, C::DK - kLatentRope + c * 64, head, (int)q.key0 + t0, vfull(st));
-          }
+          expect_by(one, b, C::VBLK * C::BLK);
+#pragma unroll
+          for (int c = 0; c < C::VBLK; ++c) tma_3d_by(one, dst + c * C::BLK, &maps.k, C::DK - kLatentRope + c * 64, head, key0 + t0, b);
         } else {
-          if (lane == 0) mbar_arrive_expect_tx(vfull(st), (uint32_t)(C::VBLK * pages * kPage * 128));
-          __syncwarp();
-          if (lane < pages)
+          expect_by(one, b, (uint32_t)(C::VBLK * pages * kPage * 128));
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            if (g >= pages) break;
+#pragma unroll
             for (int c = 0; c < C::VBLK; ++c)
-              tma_load_3d(dst + c * C::BLK + lane * kPage * 128, &maps.k, (part * C::VBLK + c) * 64, at.x, at.y, vfull(st));
+              tma_3d_by(one, dst + c * C::BLK + g * kPage * 128, &maps.k, (part * C::VBLK + c) * 64, at[g].x, at[g].y, b);
+          }
         }
         issued = i + 1;
+        if (++st == C::NV) st = 0, par ^= 1;
       } else {
-        for (int c = 0; c < C::KBLK && ok; ++c) {
-          const int n = i * C::KBLK + c, st = n % C::NK;
-          ok = (n != C::QK_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs)) &&
-               mbar_wait(kfree(st), ((n / C::NK) & 1) ^ 1, abort_p, kLuWaitNs);
+#pragma unroll
+        for (int c = 0; c < C::KBLK; ++c) {
+          const int n = i * C::KBLK + c;
+          ok = ok && (n != C::QK_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs)) &&
+               mbar_wait(kfree(st), par, abort_p, kLuWaitNs);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const int col = PROMPT ? c * 64 : (c < part * C::VBLK ? c : c + C::VBLK) * 64;
-          load_block(base + C::OFF_K + st * C::BLK, t0, col, pages, at, kfull(st));
-          issued = n + 1;
-        }
-        // Whole pages ahead into L2; two CTAs that share them take half each.
-        if (!PROMPT && lane < 4 / C::PARTS) {
-          const int t = t0 + kLuPrefetch * NT + (lane * C::PARTS + part) * kPage;
-          if (t < hi) {
-            const int2 a = page_of(t);
-            const long long row = p.page_size ? (long long)a.y * kPage : (long long)s * p.capacity + a.x;
-            bulk_prefetch_l2(reinterpret_cast<const unsigned short*>(p.cache) + row * C::DK, kPage * C::DK * 2);
+          const uint32_t dst = base + C::OFF_K + st * C::BLK, b = kfull(st);
+          if (PROMPT) {
+            expect_by(one, b, C::BLK);
+            if (c == C::KBLK - 1) tma_2d_by(one, dst, &maps.r, 0, key0 + t0, b);
+            else tma_3d_by(one, dst, &maps.k, c * 64, head, key0 + t0, b);
+          } else {
+            const int col = (c < part * C::VBLK ? c : c + C::VBLK) * 64;
+            expect_by(one, b, (uint32_t)(pages * kPage * 128));
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              if (g >= pages) break;
+              tma_3d_by(one, dst + g * kPage * 128, &maps.k, col, at[g].x, at[g].y, b);
+            }
           }
+          issued = n + 1;
+          if (++st == C::NK) st = 0, par ^= 1;
         }
       }
     }
     if (!ok && lane == 0) fail();
-    if (!keys && ok && (hi - lo) % NT != 0) {
+    if (!keys && ok && ragged) {
       // Tokens behind the range may hold anything: their V is cleared (their
       // scores are masked).
       const int i = work - 1, st = i % C::NV, valid = hi - lo - i * NT, rows = NT - valid;
@@ -307,74 +360,84 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- S issuer
-    if (lane == 0) {
-      constexpr uint32_t ID = idesc_f16(kLuM, NT, true, false);
-      bool ok = mbar_wait(bar(LB_QLAND), 0, abort_p, kLuWaitNs) && mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs);
-      bool any = false;
-      for (int i = 0; i < work && ok; ++i) {
-        const int b = i & 1;
-        const uint32_t scol = tm + C::COL_S + b * NT;
-        if (i >= 2) ok = mbar_wait(bar(LB_SFREE + b), ((i - 2) >> 1) & 1, abort_p, kLuWaitNs);
-        if (!PROMPT) {
-          const int st = i % C::NV;
-          ok = ok && mbar_wait(vfull(st), (i / C::NV) & 1, abort_p, kLuWaitNs);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t kd = sdesc_sw128(base + C::OFF_V + st * C::VBLK * C::BLK, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < C::VBLK * 4; ++kk)
-            mma_ts(scol, tm + C::COL_Q + kk * 8, kd + (uint64_t)(((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4), ID,
-                   kk > 0 ? 1u : 0u);
-          any = true;
-        }
-        for (int c = 0; c < C::KBLK && ok; ++c) {
-          const int n = i * C::KBLK + c, st = n % C::NK;
-          ok = mbar_wait(kfull(st), (n / C::NK) & 1, abort_p, kLuWaitNs);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t kd = sdesc_sw128(base + C::OFF_K + st * C::BLK, 16, 1024);
-          const uint64_t qd = sdesc_sw128(base + C::OFF_Q + c * kLuM * 128, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (PROMPT) mma_ts(scol, tm + C::COL_Q + (c * 4 + kk) * 8, kd + kk * 2, ID, c > 0 || kk > 0 ? 1u : 0u);
-            else mma_ss(scol, qd + kk * 2, kd + kk * 2, ID, 1u);
-          }
-          any = true;
-          mma_commit(kfree(st));
-        }
+    constexpr uint32_t ID = idesc_f16(kLuM, NT, true, false);
+    const uint32_t one = elected();
+    bool ok = mbar_wait(bar(LB_QLAND), 0, abort_p, kLuWaitNs) && mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs);
+    ok = __all_sync(0xffffffffu, ok);
+    bool any = false;
+    int st = 0, sk = 0;                     // V stage, key block
+    uint32_t pv = 0, pk = 0;                // their parities
+    const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, 16, 1024), kd0 = sdesc_sw128(base + C::OFF_K, 16, 1024);
+    const uint64_t qd0 = sdesc_sw128(base + C::OFF_Q, 16, 1024);
+    for (int i = 0; i < work && ok; ++i) {
+      const int b = i & 1;
+      const uint32_t scol = tm + C::COL_S + b * NT;
+      if (i >= 2) ok = mbar_wait(bar(LB_SFREE + b), ((i - 2) >> 1) & 1, abort_p, kLuWaitNs);
+      if (!PROMPT) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(vfull(st), pv, abort_p, kLuWaitNs));
         if (!ok) break;
-        mma_commit(bar(LB_SFULL + b));
+        tc_fence_after();
+        const uint64_t kd = vd0 + (uint64_t)((st * C::VBLK * C::BLK) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < C::VBLK * 4; ++kk)
+          mma_ts_by(one, scol, tm + C::COL_Q + kk * 8, kd + (uint64_t)(((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4), ID,
+                    kk > 0 ? 1u : 0u);
+        any = true;
+        if (++st == C::NV) st = 0, pv ^= 1;
       }
-      if (!ok) {
-        fail();
-        // What was issued completes before TMEM and shared memory go.
-        if (any) {
-          mma_commit(bar(LB_SDRAIN));
-          drain(bar(LB_SDRAIN), 0);
+#pragma unroll
+      for (int c = 0; c < C::KBLK; ++c) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(kfull(sk), pk, abort_p, kLuWaitNs));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kd = kd0 + (uint64_t)((sk * C::BLK) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (PROMPT) mma_ts_by(one, scol, tm + C::COL_Q + (c * 4 + kk) * 8, kd + kk * 2, ID, c > 0 || kk > 0 ? 1u : 0u);
+          else mma_ss_by(one, scol, qd0 + (uint64_t)((c * kLuM * 128) >> 4) + kk * 2, kd + kk * 2, ID, 1u);
         }
+        any = true;
+        commit_by(one, kfree(sk));
+        if (++sk == C::NK) sk = 0, pk ^= 1;
+      }
+      if (!ok) break;
+      commit_by(one, bar(LB_SFULL + b));
+    }
+    if (!ok && lane == 0) {
+      fail();
+      // What was issued completes before TMEM and shared memory go.
+      if (any) {
+        mma_commit(bar(LB_SDRAIN));
+        drain(bar(LB_SDRAIN), 0);
       }
     }
   } else if (warp == 11) {
     // ---------------------------------------------------------------- P.V issuer
-    if (lane == 0) {
-      constexpr uint32_t ID = idesc_f16(kLuM, DO, true, true);
-      bool ok = true, any = false;
-      for (int i = 0; i < work; ++i) {
-        const int b = i & 1, st = i % C::NV;
-        ok = mbar_wait(bar(LB_PFULL + b), (i >> 1) & 1, abort_p, kLuWaitNs) &&
-             mbar_wait(vfull(st), (i / C::NV) & 1, abort_p, kLuWaitNs) &&
-             (i < work - 1 || (hi - lo) % NT == 0 || mbar_wait(bar(LB_FIX), 0, abort_p, kLuWaitNs));
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t vd = sdesc_sw128(base + C::OFF_V + st * C::VBLK * C::BLK, C::BLK, 1024);
+    constexpr uint32_t ID = idesc_f16(kLuM, DO, true, true);
+    const uint32_t one = elected();
+    bool ok = true, any = false;
+    int st = 0;
+    uint32_t pv = 0;
+    const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, C::BLK, 1024);
+    for (int i = 0; i < work; ++i) {
+      const int b = i & 1;
+      ok = mbar_wait(bar(LB_PFULL + b), (i >> 1) & 1, abort_p, kLuWaitNs) &&
+           mbar_wait(vfull(st), pv, abort_p, kLuWaitNs) &&
+           (i < work - 1 || !ragged || mbar_wait(bar(LB_FIX), 0, abort_p, kLuWaitNs));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t vd = vd0 + (uint64_t)((st * C::VBLK * C::BLK) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < NT / 16; ++kk)
-          mma_ts(tm + C::COL_O, tm + C::COL_S + b * NT + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), ID,
-                 i > 0 || kk > 0 ? 1u : 0u);
-        any = true;
-        mma_commit(bar(LB_SFREE + b));
-        mma_commit(vfree(st));
-      }
+      for (int kk = 0; kk < NT / 16; ++kk)
+        mma_ts_by(one, tm + C::COL_O, tm + C::COL_S + b * NT + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), ID,
+                  i > 0 || kk > 0 ? 1u : 0u);
+      any = true;
+      commit_by(one, bar(LB_SFREE + b));
+      commit_by(one, vfree(st));
+      if (++st == C::NV) st = 0, pv ^= 1;
+    }
+    if (lane == 0) {
       if (!ok) fail();
       if (any) {
         // After every P.V, in a failed run too.
