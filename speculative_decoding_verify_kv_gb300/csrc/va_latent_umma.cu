@@ -126,6 +126,22 @@ __device__ __forceinline__ void commit_by(uint32_t e, uint32_t bar) {
       : "memory");
 }
 
+// Whether a phase has completed already.  Asked before an MMA group and used
+// after it, so that the answer is there when the issuer gets to it: a wait, even
+// one that passes, otherwise stands between two groups for some 150 cycles, and
+// the matrix unit holds only a few MMAs in advance.
+__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ void expect_by(uint32_t e, uint32_t bar, uint32_t bytes) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
@@ -369,14 +385,25 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     uint32_t pv = 0, pk = 0;                // their parities
     const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, 16, 1024), kd0 = sdesc_sw128(base + C::OFF_K, 16, 1024);
     const uint64_t qd0 = sdesc_sw128(base + C::OFF_Q, 16, 1024);
+    // What a tile starts with: its S buffer free, and its V stage (absorbed form)
+    // or first key block there.
+    auto peek_tile = [&](int i) {
+      return (i < 2 || mbar_peek(bar(LB_SFREE + (i & 1)), ((i - 2) >> 1) & 1)) &&
+             (PROMPT ? mbar_peek(kfull(sk), pk) : mbar_peek(vfull(st), pv));
+    };
+    auto wait_tile = [&](int i) {
+      return (i < 2 || mbar_wait(bar(LB_SFREE + (i & 1)), ((i - 2) >> 1) & 1, abort_p, kLuWaitNs)) &&
+             (PROMPT ? mbar_wait(kfull(sk), pk, abort_p, kLuWaitNs) : mbar_wait(vfull(st), pv, abort_p, kLuWaitNs));
+    };
+    bool there = false;
     for (int i = 0; i < work && ok; ++i) {
       const int b = i & 1;
       const uint32_t scol = tm + C::COL_S + b * NT;
-      if (i >= 2) ok = mbar_wait(bar(LB_SFREE + b), ((i - 2) >> 1) & 1, abort_p, kLuWaitNs);
+      ok = __all_sync(0xffffffffu, there || wait_tile(i));
+      if (!ok) break;
+      tc_fence_after();
       if (!PROMPT) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(vfull(st), pv, abort_p, kLuWaitNs));
-        if (!ok) break;
-        tc_fence_after();
+        there = mbar_peek(kfull(sk), pk);
         const uint64_t kd = vd0 + (uint64_t)((st * C::VBLK * C::BLK) >> 4);
 #pragma unroll
         for (int kk = 0; kk < C::VBLK * 4; ++kk)
@@ -387,18 +414,22 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       }
 #pragma unroll
       for (int c = 0; c < C::KBLK; ++c) {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(kfull(sk), pk, abort_p, kLuWaitNs));
-        if (!ok) break;
-        tc_fence_after();
+        if (!PROMPT || c > 0) {
+          ok = __all_sync(0xffffffffu, there || mbar_wait(kfull(sk), pk, abort_p, kLuWaitNs));
+          if (!ok) break;
+          tc_fence_after();
+        }
         const uint64_t kd = kd0 + (uint64_t)((sk * C::BLK) >> 4);
+        const uint32_t free = kfree(sk);
+        if (++sk == C::NK) sk = 0, pk ^= 1;
+        there = c + 1 < C::KBLK ? mbar_peek(kfull(sk), pk) : i + 1 < work && peek_tile(i + 1);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if (PROMPT) mma_ts_by(one, scol, tm + C::COL_Q + (c * 4 + kk) * 8, kd + kk * 2, ID, c > 0 || kk > 0 ? 1u : 0u);
           else mma_ss_by(one, scol, qd0 + (uint64_t)((c * kLuM * 128) >> 4) + kk * 2, kd + kk * 2, ID, 1u);
         }
         any = true;
-        commit_by(one, kfree(sk));
-        if (++sk == C::NK) sk = 0, pk ^= 1;
+        commit_by(one, free);
       }
       if (!ok) break;
       commit_by(one, bar(LB_SFULL + b));
