@@ -39,6 +39,7 @@ struct LatentParams {
   int total_kv, causal;
   int prompt;
   int slots;              // largest number of chunks of a sequence
+  int many;               // a sequence of max_rows rows may have many
   int rows_per_block;
   float* ws_acc;          // [slots][total_rows][H][DV]
   float* ws_ml;           // [slots][total_rows][H][2]  (m in log2 units, l)
@@ -156,6 +157,8 @@ cudaError_t launch_latent_merge(const LatentParams& p, cudaStream_t st);
 int latent_simt_rows();
 cudaError_t launch_latent_umma(const LatentParams& p, dim3 grid, cudaStream_t st);
 int latent_umma_rows();
+cudaError_t launch_latent_rows(const LatentParams& p, dim3 grid, cudaStream_t st);
+int latent_rows_rows(long long rows);
 int latent_umma_parts(int value_dim, bool prompt);
 
 }  // namespace va

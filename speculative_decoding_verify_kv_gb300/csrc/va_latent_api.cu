@@ -9,10 +9,12 @@ namespace va {
 
 struct LatentPlan {
   int kernel;          // VA_KERNEL_*
+  bool few;            // the tensor-core kernel for few query rows
   int rows_per_block;  // query rows of a CTA
   int parts;           // CTAs that share a row block's chunk
   int per_sm;          // CTAs of an SM
   int slots;
+  bool many;           // more than eight chunks of a sequence of the most rows
   size_t acc_bytes, ws_bytes;
   dim3 grid;
 };
@@ -81,8 +83,10 @@ static LatentPlan plan_rows(const va_problem* p, int dtype, int value_dim, bool 
   memset((void*)&pl, 0, sizeof(pl));
   if (dtype == VA_BF16 && !(p->flags & VA_FLAG_CUDA_CORES)) {
     pl.kernel = VA_KERNEL_TENSOR;
-    pl.rows_per_block = latent_umma_rows();
-    pl.parts = latent_umma_parts(value_dim, prompt);
+    const int few = prompt ? 0 : latent_rows_rows((long long)p->max_rows_per_seq * p->num_heads);
+    pl.few = few > 0;
+    pl.rows_per_block = few ? few : latent_umma_rows();
+    pl.parts = few ? 1 : latent_umma_parts(value_dim, prompt);
     pl.per_sm = 1;
   } else {
     pl.kernel = VA_KERNEL_CUDA_CORES;
@@ -93,6 +97,7 @@ static LatentPlan plan_rows(const va_problem* p, int dtype, int value_dim, bool 
   pl.slots = p->num_splits;
   const long long rows = (long long)p->max_rows_per_seq * (prompt ? 1 : p->num_heads);
   const long long blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
+  pl.many = pl.slots / (blocks > 0 ? blocks : 1) > 8;
   // A sequence of b row blocks has b max(1, slots / b) CTAs per key head.
   pl.grid = dim3((unsigned)(blocks > pl.slots ? blocks : pl.slots), (unsigned)(prompt ? p->num_heads : pl.parts),
                  (unsigned)p->num_seqs);
@@ -137,6 +142,7 @@ static LatentParams base_params(const va_problem* p, int mode, const LatentPlan&
   q.parent = p->parent;
   q.seq_kind = p->seq_kind;
   q.slots = pl.slots;
+  q.many = pl.many;
   q.rows_per_block = pl.rows_per_block;
   q.ws_acc = (float*)ws;
   q.ws_ml = ws ? (float*)((char*)ws + pl.acc_bytes) : nullptr;
@@ -159,7 +165,9 @@ static va_status check_outputs(const LatentPlan& pl, const void* ws, size_t ws_b
 }
 
 static va_status launch(const LatentParams& q, const LatentPlan& pl, cudaStream_t cs) {
-  cudaError_t e = pl.kernel == VA_KERNEL_TENSOR ? launch_latent_umma(q, pl.grid, cs) : launch_latent_simt(q, pl.grid, cs);
+  cudaError_t e = pl.few                           ? launch_latent_rows(q, pl.grid, cs)
+                  : pl.kernel == VA_KERNEL_TENSOR ? launch_latent_umma(q, pl.grid, cs)
+                                                  : launch_latent_simt(q, pl.grid, cs);
   if (e == cudaSuccess && pl.slots > 1) e = launch_latent_merge(q, cs);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }

@@ -28,16 +28,13 @@
 // copies and MMAs, frees TMEM and writes NaN.
 #include <string.h>
 
-#include "va_latent.cuh"
-#include "va_sm100.cuh"
-#include "va_tma.h"
+#include "va_latent_mma.cuh"
 
 namespace va {
 using namespace sm100;
 
 constexpr int kLuM = 128;
 constexpr int kLuThreads = 384;
-constexpr uint64_t kLuWaitNs = 2000000000ull;
 
 template <int DK_, int DV_, bool PROMPT_>
 struct LuCfg {
@@ -81,92 +78,6 @@ enum { LB_SFULL = 0, LB_PFULL = 2, LB_SFREE = 4, LB_QLAND = 6, LB_QREADY = 7, LB
 struct LuMaps {
   CUtensorMap q, k, r;  // queries; cache or expanded keys and values; rope part of prompt keys
 };
-
-__device__ __forceinline__ float lu_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// MMAs and commits that a whole warp runs through and its elected lane (e != 0)
-// issues, with everything they are computed from known to be the warp's:
-// descriptors then live in uniform registers.  An issuing thread of its own
-// branch took some 100 cycles to an MMA, longer than one of 64 columns runs
-// (64 heads x 16 rows x 4 sequences of 8,000 tokens: 142 us against 112; prompts
-// of 2 x 2,048 rows, 128 heads, over 4,096 keys: 966 against 755).
-__device__ __forceinline__ uint32_t elected() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
-  return e;
-}
-
-__device__ __forceinline__ void mma_ts_by(uint32_t e, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-      "r"(accumulate), "r"(e)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_ss_by(uint32_t e, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"(accumulate), "r"(e)
-      : "memory");
-}
-
-__device__ __forceinline__ void commit_by(uint32_t e, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(e)
-      : "memory");
-}
-
-// Whether a phase has completed already.  Asked before an MMA group and used
-// after it, so that the answer is there when the issuer gets to it: a wait, even
-// one that passes, otherwise stands between two groups for some 150 cycles, and
-// the matrix unit holds only a few MMAs in advance.
-__device__ __forceinline__ bool mbar_peek(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
-__device__ __forceinline__ void expect_by(uint32_t e, uint32_t bar, uint32_t bytes) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %2, 0;\n\t"
-      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes), "r"(e)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_2d_by(uint32_t e, uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(bar), "r"(e)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_3d_by(uint32_t e, uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %6, 0;\n\t"
-      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "r"(e)
-      : "memory");
-}
 
 template <class C>
 __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const LatentParams p, const __grid_constant__ LuMaps maps) {
@@ -259,7 +170,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   };
   auto drain = [&](uint32_t b, uint32_t parity) {
     int dummy = 0;
-    mbar_wait(b, parity, &dummy, kLuWaitNs);
+    mbar_wait(b, parity, &dummy, kLatentWaitNs);
   };
 
   if (work == 0) {
@@ -304,7 +215,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
         for (int g = 0; g < 4; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, g), __shfl_sync(0xffffffffu, a.y, g));
       }
       if (!keys) {
-        ok = (i != C::QV_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs)) && mbar_wait(vfree(st), par, abort_p, kLuWaitNs);
+        ok = (i != C::QV_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLatentWaitNs)) && mbar_wait(vfree(st), par, abort_p, kLatentWaitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t dst = base + C::OFF_V + st * C::VBLK * C::BLK, b = vfull(st);
@@ -328,8 +239,8 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
 #pragma unroll
         for (int c = 0; c < C::KBLK; ++c) {
           const int n = i * C::KBLK + c;
-          ok = ok && (n != C::QK_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs)) &&
-               mbar_wait(kfree(st), par, abort_p, kLuWaitNs);
+          ok = ok && (n != C::QK_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLatentWaitNs)) &&
+               mbar_wait(kfree(st), par, abort_p, kLatentWaitNs);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t dst = base + C::OFF_K + st * C::BLK, b = kfull(st);
@@ -356,7 +267,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       // Tokens behind the range may hold anything: their V is cleared (their
       // scores are masked).
       const int i = work - 1, st = i % C::NV, valid = hi - lo - i * NT, rows = NT - valid;
-      if (__all_sync(0xffffffffu, mbar_wait(vfull(st), (i / C::NV) & 1, abort_p, kLuWaitNs))) {
+      if (__all_sync(0xffffffffu, mbar_wait(vfull(st), (i / C::NV) & 1, abort_p, kLatentWaitNs))) {
         unsigned char* at = sm + C::OFF_V + st * C::VBLK * C::BLK;
         for (int u = lane; u < C::VBLK * rows * 8; u += 32)
           *reinterpret_cast<uint4*>(at + u / (rows * 8) * C::BLK + (valid + u / 8 % rows) * 128 + (u & 7) * 16) =
@@ -378,7 +289,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     // ---------------------------------------------------------------- S issuer
     constexpr uint32_t ID = idesc_f16(kLuM, NT, true, false);
     const uint32_t one = elected();
-    bool ok = mbar_wait(bar(LB_QLAND), 0, abort_p, kLuWaitNs) && mbar_wait(bar(LB_QREADY), 0, abort_p, kLuWaitNs);
+    bool ok = mbar_wait(bar(LB_QLAND), 0, abort_p, kLatentWaitNs) && mbar_wait(bar(LB_QREADY), 0, abort_p, kLatentWaitNs);
     ok = __all_sync(0xffffffffu, ok);
     bool any = false;
     int st = 0, sk = 0;                     // V stage, key block
@@ -392,8 +303,8 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
              (PROMPT ? mbar_peek(kfull(sk), pk) : mbar_peek(vfull(st), pv));
     };
     auto wait_tile = [&](int i) {
-      return (i < 2 || mbar_wait(bar(LB_SFREE + (i & 1)), ((i - 2) >> 1) & 1, abort_p, kLuWaitNs)) &&
-             (PROMPT ? mbar_wait(kfull(sk), pk, abort_p, kLuWaitNs) : mbar_wait(vfull(st), pv, abort_p, kLuWaitNs));
+      return (i < 2 || mbar_wait(bar(LB_SFREE + (i & 1)), ((i - 2) >> 1) & 1, abort_p, kLatentWaitNs)) &&
+             (PROMPT ? mbar_wait(kfull(sk), pk, abort_p, kLatentWaitNs) : mbar_wait(vfull(st), pv, abort_p, kLatentWaitNs));
     };
     bool there = false;
     for (int i = 0; i < work && ok; ++i) {
@@ -415,7 +326,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
 #pragma unroll
       for (int c = 0; c < C::KBLK; ++c) {
         if (!PROMPT || c > 0) {
-          ok = __all_sync(0xffffffffu, there || mbar_wait(kfull(sk), pk, abort_p, kLuWaitNs));
+          ok = __all_sync(0xffffffffu, there || mbar_wait(kfull(sk), pk, abort_p, kLatentWaitNs));
           if (!ok) break;
           tc_fence_after();
         }
@@ -452,9 +363,9 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, C::BLK, 1024);
     for (int i = 0; i < work; ++i) {
       const int b = i & 1;
-      ok = mbar_wait(bar(LB_PFULL + b), (i >> 1) & 1, abort_p, kLuWaitNs) &&
-           mbar_wait(vfull(st), pv, abort_p, kLuWaitNs) &&
-           (i < work - 1 || !ragged || mbar_wait(bar(LB_FIX), 0, abort_p, kLuWaitNs));
+      ok = mbar_wait(bar(LB_PFULL + b), (i >> 1) & 1, abort_p, kLatentWaitNs) &&
+           mbar_wait(vfull(st), pv, abort_p, kLatentWaitNs) &&
+           (i < work - 1 || !ragged || mbar_wait(bar(LB_FIX), 0, abort_p, kLatentWaitNs));
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -481,7 +392,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     const int half = (warp - 2) >> 2;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const bool warp_live = __any_sync(0xffffffffu, rvalid);
-    bool ok = __all_sync(0xffffffffu, mbar_wait(bar(LB_QLAND), 0, abort_p, kLuWaitNs));
+    bool ok = __all_sync(0xffffffffu, mbar_wait(bar(LB_QLAND), 0, abort_p, kLatentWaitNs));
     if (ok) {
       // Query row -> TMEM: this half's 16-byte pieces of the swizzled blocks.
       // (Rows behind the block's last hold other rows, or zeros: no one reads
@@ -512,7 +423,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     // barrier shared with the partner warp.
     for (int i = 0; i < work; ++i) {
       const int b = i & 1;
-      if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(LB_SFULL + b), (i >> 1) & 1, abort_p, kLuWaitNs))) ok = false;
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(LB_SFULL + b), (i >> 1) & 1, abort_p, kLatentWaitNs))) ok = false;
       tc_fence_after();
       const uint32_t scol = tm + lanes + C::COL_S + b * NT;
       const int t0 = lo + i * NT + NC * half;
@@ -550,7 +461,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       const float m_new = m_use == -INFINITY || need ? mt : m_use;
       if (ok && __any_sync(0xffffffffu, need)) {
         // Rescale this half of the warp's O rows once the previous P.V landed.
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(LB_SFREE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_p, kLuWaitNs)))
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(LB_SFREE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_p, kLatentWaitNs)))
           ok = false;
         if (ok) {
           tc_fence_after();
@@ -596,7 +507,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(LB_PFULL + b));
     }
-    if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(LB_OFINAL), 0, abort_p, kLuWaitNs))) ok = false;
+    if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(LB_OFINAL), 0, abort_p, kLatentWaitNs))) ok = false;
     if (!ok && lane == 0) fail();
     tc_fence_after();
     red[half * kLuM + r] = l_run;
@@ -681,35 +592,18 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
 }
 
 // ---------------------------------------------------------------------------
-// Tiled map of bf16 rows in boxes of 64 columns, 128-byte swizzle.
-static bool lu_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                   const cuuint32_t* box) {
-  const EncodeTiledFn fn = encode_fn();
-  const cuuint32_t es[3] = {1, 1, 1};
-  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 static bool lu_maps(LuMaps* m, const LatentParams& p, int tile) {
   memset(m, 0, sizeof(*m));
   const cuuint64_t dk = (cuuint64_t)p.DK, H = (cuuint64_t)p.H;
-  if (!p.prompt) {
-    const cuuint64_t qd[2] = {dk, (cuuint64_t)p.total_rows * H}, qs[1] = {dk * 2};
-    const cuuint32_t qb[2] = {64, kLuM}, kb[3] = {64, kPage, 1};
-    const cuuint64_t rows = p.page_size ? (cuuint64_t)kPage : (cuuint64_t)p.capacity;
-    const cuuint64_t kd[3] = {dk, rows, (cuuint64_t)(p.page_size ? p.num_blocks : p.num_seqs)};
-    const cuuint64_t ks[2] = {dk * 2, rows * dk * 2};
-    return lu_map(&m->q, p.q, 2, qd, qs, qb) && lu_map(&m->k, p.cache, 3, kd, ks, kb);
-  }
+  if (!p.prompt) return latent_query_map(&m->q, p, kLuM) && latent_cache_map(&m->k, p);
   const cuuint64_t qd[3] = {dk, H, (cuuint64_t)p.total_rows}, qs[2] = {dk * 2, H * dk * 2};
   const cuuint32_t qb[3] = {64, 1, kLuM}, kb[3] = {64, 1, (cuuint32_t)tile}, rb[2] = {64, (cuuint32_t)tile};
-  if (!lu_map(&m->q, p.q, 3, qd, qs, qb)) return false;
+  if (!latent_map(&m->q, p.q, 3, qd, qs, qb)) return false;
   if (p.total_kv == 0) return true;  // no tile, no load
   const cuuint64_t w = dk - kLatentRope + (cuuint64_t)p.DV, T = (cuuint64_t)p.total_kv;
   const cuuint64_t kd[3] = {w, H, T}, ks[2] = {w * 2, H * w * 2};
   const cuuint64_t rd[2] = {kLatentRope, T}, rs[1] = {(cuuint64_t)(T > 1 ? p.kr_stride : kLatentRope) * 2};
-  return lu_map(&m->k, p.kv, 3, kd, ks, kb) && lu_map(&m->r, p.k_rope, 2, rd, rs, rb);
+  return latent_map(&m->k, p.kv, 3, kd, ks, kb) && latent_map(&m->r, p.k_rope, 2, rd, rs, rb);
 }
 
 template <class C>

@@ -31,6 +31,11 @@ def run_check(case, **kw):
     (8, [129, 64], [32, 31], "tree", False, 1),
     (2, [33], [200], "chain", True, 4),                       # a segment of several row blocks
     (7, [10, 0, 20], [0, 2, 0], "chain", True, 2),            # sequences without rows
+    (2, [60, 200], [16, 9], "tree", True, 2),                 # few query rows: trees,
+    (3, [127, 128, 1], [5, 3, 1], "mixed", True, 3),          # trees and chains,
+    (1, [500], [32], "tree", False, 2),                       # one head,
+    (4, [300, 130], [4, 8], "chain", True, 2),                # chains
+    (1, [130, 3, 255], [16, 5, 1], "mixed", False, 1),
 ])
 def test_latent(kind, latent, heads, ctx, rows, mode, paged, splits):
     run_check(Latent(kind, heads, latent, ctx, rows, mode, paged, seed=heads + latent, splits=splits))
