@@ -29,7 +29,7 @@
 namespace va {
 
 constexpr int kLrTile = 64;
-constexpr int kLrThreads = 224;  // producer, two issuers, four softmax warps
+constexpr int kLrThreads = 256;  // two producers, two issuers, four softmax warps
 
 template <int DV_, int N_>
 struct LrCfg {
@@ -50,7 +50,7 @@ struct LrCfg {
   static constexpr int COL_S = MB * N;
   static constexpr int COLS = MB * N + 2 * N <= 128 ? 128 : 256;
   static_assert(SMEM <= 232448, "shared memory");
-  static_assert(NV >= MB + 1, "a pair to load beside the tile's");
+  static_assert(NV >= MB + 1 && MB % 2 == 0, "a pair to load beside the tile's");
 };
 
 enum { RB_QLAND = 0, RB_SFULL = 1, RB_SREAD = 3, RB_PFULL = 5, RB_PFREE = 7, RB_OFINAL = 9, RB_SDRAIN = 10, RB_RING = 11 };
@@ -166,55 +166,73 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
 
   if (work == 0) {
     // nothing to read
-  } else if (warp == 0) {
-    // ---------------------------------------------------------------- producer
+  } else if (warp == 0 || warp == 7) {
+    // ---------------------------------------------------------------- producers
+    // Warp 0: the queries, the rope blocks and even pairs.  Warp 7: odd pairs.
+    // (A copy is one block of one page, 36 to a tile: issued by one warp, they
+    // were what the call waited for.)
+    const int who = warp == 0 ? 0 : 1;
     const uint32_t one = elected();
     const int lo_u = __shfl_sync(0xffffffffu, lo, 0), hi_u = __shfl_sync(0xffffffffu, hi, 0);
-    const int qrow = __shfl_sync(0xffffffffu, q.row0 * p.H, 0);
-    expect_by(one, bar(RB_QLAND), C::DK / 64 * C::QBLK);
+    if (who == 0) {
+      const int qrow = __shfl_sync(0xffffffffu, q.row0 * p.H, 0);
+      expect_by(one, bar(RB_QLAND), C::DK / 64 * C::QBLK);
 #pragma unroll
-    for (int c = 0; c < C::DK / 64; ++c) tma_2d_by(one, base + C::OFF_Q + c * C::QBLK, &maps.q, c * 64, qrow, bar(RB_QLAND));
+      for (int c = 0; c < C::DK / 64; ++c) tma_2d_by(one, base + C::OFF_Q + c * C::QBLK, &maps.q, c * 64, qrow, bar(RB_QLAND));
+    }
     bool ok = true;
-    int nk = 0, nv = 0;  // blocks issued
-    int sk = 0, sv = 0;
+    int nk = 0, nv = who;  // rope blocks issued; the next pair
+    int sk = 0, sv = who;
     uint32_t pk = 1, pv = 1;
     for (int i = 0; i < work && ok; ++i) {
       const int t0 = lo_u + i * kLrTile;
       const int pages = (min(kLrTile, hi_u - t0) + kPage - 1) / kPage;
-      int2 at = make_int2(0, 0);  // lane l: (row, plane) of the tile's page l in the cache's map
+      int2 mine = make_int2(0, 0);  // lane l: (row, plane) of the tile's page l in the cache's map
       if (lane < pages) {
         const int pg = t0 / kPage + lane;
-        at = p.page_size ? make_int2(0, p.block_table[(long long)s * p.max_blocks + pg]) : make_int2(pg * kPage, s);
+        mine = p.page_size ? make_int2(0, p.block_table[(long long)s * p.max_blocks + pg]) : make_int2(pg * kPage, s);
       }
-#pragma unroll 1
-      for (int c = -1; c < MB; ++c) {  // the rope block, then the pairs
-        ok = __all_sync(0xffffffffu, mbar_wait(c < 0 ? kfree(sk) : vfree(sv), c < 0 ? pk : pv, abort_p, kLatentWaitNs));
+      int2 at[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, mine.x, g), __shfl_sync(0xffffffffu, mine.y, g));
+      if (who == 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(kfree(sk), pk, abort_p, kLatentWaitNs));
         if (!ok) break;
-        const uint32_t b = c < 0 ? kfull(sk) : vfull(sv);
-        const uint32_t dst = base + (c < 0 ? C::OFF_K + sk * C::BLK : C::OFF_V + sv * 2 * C::BLK);
-        const int col = c < 0 ? C::DV : c * 128;
-        expect_by(one, b, (uint32_t)((c < 0 ? 1 : 2) * pages * kPage * 128));
-#pragma unroll 1
-        for (int g = 0; g < pages; ++g) {
-          const int x = __shfl_sync(0xffffffffu, at.x, g), y = __shfl_sync(0xffffffffu, at.y, g);
-          tma_3d_by(one, dst + g * kPage * 128, &maps.k, col, x, y, b);
-          if (c >= 0) tma_3d_by(one, dst + C::BLK + g * kPage * 128, &maps.k, col + 64, x, y, b);
+        expect_by(one, kfull(sk), (uint32_t)(pages * kPage * 128));
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (g >= pages) break;
+          tma_3d_by(one, base + C::OFF_K + sk * C::BLK + g * kPage * 128, &maps.k, C::DV, at[g].x, at[g].y, kfull(sk));
         }
-        if (c < 0) {
-          ++nk;
-          if (++sk == C::NK) sk = 0, pk ^= 1;
-        } else {
-          ++nv;
-          if (++sv == C::NV) sv = 0, pv ^= 1;
+        ++nk;
+        if (++sk == C::NK) sk = 0, pk ^= 1;
+      }
+#pragma unroll
+      for (int h = 0; h < MB / 2; ++h) {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(vfree(sv), pv, abort_p, kLatentWaitNs));
+        if (!ok) break;
+        const uint32_t b = vfull(sv), dst = base + C::OFF_V + sv * 2 * C::BLK;
+        const int col = (2 * h + who) * 128;
+        expect_by(one, b, (uint32_t)(2 * pages * kPage * 128));
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (g >= pages) break;
+          tma_3d_by(one, dst + g * kPage * 128, &maps.k, col, at[g].x, at[g].y, b);
+          tma_3d_by(one, dst + C::BLK + g * kPage * 128, &maps.k, col + 64, at[g].x, at[g].y, b);
         }
+        nv += 2;
+        sv += 2;
+        if (sv >= C::NV) sv -= C::NV, pv ^= 1;
       }
     }
     if (!ok && lane == 0) fail();
     // No copy may still be landing when the CTA goes away.
     if (*abort_p && lane == 0) {
-      drain(bar(RB_QLAND), 0);
-      for (int i = max(0, nk - C::NK); i < nk; ++i) drain(kfull(i % C::NK), (i / C::NK) & 1);
-      for (int i = max(0, nv - C::NV); i < nv; ++i) drain(vfull(i % C::NV), (i / C::NV) & 1);
+      if (who == 0) {
+        drain(bar(RB_QLAND), 0);
+        for (int i = max(0, nk - C::NK); i < nk; ++i) drain(kfull(i % C::NK), (i / C::NK) & 1);
+      }
+      for (int i = nv - 2; i >= max(0, nv - 1 - C::NV); i -= 2) drain(vfull(i % C::NV), (i / C::NV) & 1);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- S issuer
