@@ -322,13 +322,21 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
     const bool token = lane < 16;
     const uint32_t lanes = (uint32_t)(quad * 32) << 16;
     const float c_r = p.scale_log2;
-    float l[N];
+    // nm: minus the reference, kUnseen while the row has seen nothing (any score
+    // then exceeds it).
+    constexpr float kUnseen = 1e30f;
+    float l[N], nm[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) l[n] = 0.f;
+    for (int n = 0; n < N; ++n) {
+      l[n] = 0.f;
+      nm[n] = kUnseen;
+    }
     bool ok = true;
     // A failed wait does not leave the loop: its barriers are shared by the four warps.
     for (int i = 0; i < work; ++i) {
       const int b = i & 1;
+      // Whether the product that read this tile's buffer of P^T is done.
+      const bool free = i < 2 || mbar_peek(bar(RB_PFREE + b), ((i - 2) >> 1) & 1);
       if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(RB_SFULL + b), (i >> 1) & 1, abort_p, kLatentWaitNs))) ok = false;
       tc_fence_after();
       uint32_t sr[N];
@@ -337,27 +345,32 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(RB_SREAD + b));
-      float z[N];
+      float z[N];  // score over the reference, in log2 units
       const int t = lo + i * kLrTile + tt;
-      bool over = false;
       if (lo + (i + 1) * kLrTile <= all_see) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) z[n] = token ? __uint_as_float(sr[n]) * c_r : -INFINITY;
+        for (int n = 0; n < N; ++n) z[n] = token ? __uint_as_float(sr[n]) : -INFINITY;
       } else {
         const int a = t - q.ctx;  // its place among the drafts
+        const bool in = token && t < hi;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           const int see = see_s[n];
-          const bool vis = token && t < hi && (a < 0 || (q.kind == 0 ? a < see : ((unsigned)see >> (a & 31)) & 1u));
-          z[n] = vis ? __uint_as_float(sr[n]) * c_r : -INFINITY;
+          const bool vis = in && (a < 0 || (q.kind == 0 ? a < see : ((unsigned)see >> (a & 31)) & 1u));
+          z[n] = vis ? __uint_as_float(sr[n]) : -INFINITY;
         }
       }
+      bool over = false;
 #pragma unroll
-      for (int n = 0; n < N; ++n) over = over || z[n] > m_s[n] + 8.f;
+      for (int n = 0; n < N; ++n) {
+        z[n] = fmaf(z[n], c_r, nm[n]);
+        over = over || z[n] > 8.f;
+      }
       if (any_of_four_warps(2, over)) {
         // New references: the rows' largest scores of this tile.
 #pragma unroll
         for (int n = 0; n < N; ++n) {
+          z[n] = z[n] > -INFINITY ? __uint_as_float(sr[n]) * c_r : -INFINITY;
           float mx = z[n];
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -385,22 +398,23 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
             tmem_st_n<N>(tm + lanes + c * N, o);
           }
           tmem_wait_st();
+        }
 #pragma unroll
-          for (int n = 0; n < N; ++n) l[n] *= f_s[n];
+        for (int n = 0; n < N; ++n) {
+          l[n] *= f_s[n];
+          nm[n] = m_s[n] == -INFINITY ? kUnseen : -m_s[n];
+          z[n] += nm[n];
         }
       }
-      // The product that read this buffer of P^T has to be done.
-      if (i > 1 && ok && !__all_sync(0xffffffffu, mbar_wait(bar(RB_PFREE + b), ((i - 2) >> 1) & 1, abort_p, kLatentWaitNs))) ok = false;
+      if (ok && !__all_sync(0xffffffffu, free || mbar_wait(bar(RB_PFREE + b), ((i - 2) >> 1) & 1, abort_p, kLatentWaitNs))) ok = false;
       unsigned char* prow = sm + C::OFF_P + b * C::QBLK;
-      const int at = tt >> 3, in = (tt & 7) * 2;
+      const int at = tt >> 3, in8 = (tt & 7) * 2;
 #pragma unroll
       for (int n = 0; n < N; ++n) {
-        const float m = m_s[n];
-        // A masked score (-inf) gives 0, also while the row has seen nothing.
-        const float w = lu_ex2(z[n] - (m == -INFINITY ? 0.f : m));
+        const float w = lu_ex2(z[n]);  // masked: 0
         l[n] += w;
         // bf16, as the matrix unit takes it (2^-8 of w at most, see the 128-row kernel).
-        if (token) *reinterpret_cast<__nv_bfloat16*>(prow + n * 128 + ((at ^ (n & 7)) << 4) + in) = __float2bfloat16_rn(w);
+        if (token) *reinterpret_cast<__nv_bfloat16*>(prow + n * 128 + ((at ^ (n & 7)) << 4) + in8) = __float2bfloat16_rn(w);
       }
       if (i == work - 1 && token && t >= hi) {
         // Tokens behind the range may hold anything: their V is cleared (S of
