@@ -98,8 +98,19 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
   int* see_s = reinterpret_cast<int*>(w_s + 4 * N);  // chain: drafts that a row sees; tree: its ancestors, as bits
 
   asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  if (tid == 0) {
+    *err_s = 0;
+    *abort_p = 0;
+    for (int i = 0; i < C::NB; ++i)
+      mbar_init(bar(i), i >= RB_SREAD && i < RB_PFREE ? 4 : 1);
+    fence_barrier_init();
+  }
+  if (tid < N) m_s[tid] = -INFINITY;
+  // Nothing but this CTA's own shared memory is touched before the work ahead
+  // on the stream has completed.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int s = blockIdx.z, chunk = blockIdx.x;
   const LatentSeq q = latent_seq(p, s);
   if (q.err & VA_DEV_BAD_ROWS) {
@@ -115,46 +126,28 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
   const int ntiles = q.err ? 0 : (hi - lo + kLrTile - 1) / kLrTile;
   const int all_see = q.kind == 1 ? min(hi, q.ctx) : min(hi, q.ctx + 1);
 
-  auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto vfull = [&](int i) { return bar(RB_RING + i); };
   auto vfree = [&](int i) { return bar(RB_RING + C::NV + i); };
   auto kfull = [&](int i) { return bar(RB_RING + 2 * C::NV + i); };
   auto kfree = [&](int i) { return bar(RB_RING + 2 * C::NV + C::NK + i); };
   const uint32_t base = smem_u32(sm);
 
-  if (tid == 0) {
-    *err_s = 0;
-    *abort_p = 0;
-    for (int i = 0; i < C::NB; ++i)
-      mbar_init(bar(i), i >= RB_SREAD && i < RB_PFREE ? 4 : 1);
-    fence_barrier_init();
-  }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_at), C::COLS);
     tmem_relinquish();
   }
-  __syncthreads();
-  if (tid < N) {
-    m_s[tid] = -INFINITY;
-    const int j = tid < R ? tid / p.H : 0;
-    bool bad = false;
-    if (q.kind == 0) see_s[tid] = j + 1;
-    else if (!q.err) see_s[tid] = (int)row_mask(1, p.parent + q.row0, j, &bad);
-    if (bad) atomicOr(err_s, (int)VA_DEV_BAD_PARENT);
-  }
-  if (p.page_size && ntiles > 0) {
-    for (int pg = lo / kPage + tid; pg < (hi + kPage - 1) / kPage; pg += kLrThreads) {
-      const int blk = p.block_table[(long long)s * p.max_blocks + pg];
-      if (blk < 0 || blk >= p.num_blocks) atomicOr(err_s, (int)VA_DEV_BAD_BLOCK);
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const unsigned err = q.err | (unsigned)*err_s;
   const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_at, 0);
-  const int work = __shfl_sync(0xffffffffu, err ? 0 : ntiles, 0);
-  if (err && tid == 0) flag(p.status, err);
+  const int work = __shfl_sync(0xffffffffu, ntiles, 0);
+  if (q.err && tid == 0) flag(p.status, q.err);
+  // A finding on the way (a bad parent or page) does not stop the pipeline: what
+  // it computes then is replaced by NaN at the end.
+  auto found = [&](unsigned bits) {
+    atomicOr(err_s, (int)bits);
+    flag(p.status, bits);
+  };
   auto fail = [&]() {
     *abort_p = 1;
     flag(p.status, VA_DEV_TIMEOUT);
@@ -190,7 +183,15 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       int2 mine = make_int2(0, 0);  // lane l: (row, plane) of the tile's page l in the cache's map
       if (lane < pages) {
         const int pg = t0 / kPage + lane;
-        mine = p.page_size ? make_int2(0, p.block_table[(long long)s * p.max_blocks + pg]) : make_int2(pg * kPage, s);
+        mine = make_int2(pg * kPage, s);
+        if (p.page_size) {
+          int blk = p.block_table[(long long)s * p.max_blocks + pg];
+          if (blk < 0 || blk >= p.num_blocks) {
+            found(VA_DEV_BAD_BLOCK);
+            blk = 0;
+          }
+          mine = make_int2(0, blk);
+        }
       }
       int2 at[4];
 #pragma unroll
@@ -331,6 +332,13 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       l[n] = 0.f;
       nm[n] = kUnseen;
     }
+    if (th < N) {
+      const int j = th < R ? th / p.H : 0;
+      bool bad_parent = false;
+      see_s[th] = q.kind == 0 ? j + 1 : (int)row_mask(1, p.parent + q.row0, j, &bad_parent);
+      if (bad_parent) found(VA_DEV_BAD_PARENT);
+    }
+    bar_sync(3, 128);
     bool ok = true;
     // A failed wait does not leave the loop: its barriers are shared by the four warps.
     for (int i = 0; i < work; ++i) {
@@ -442,7 +450,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       if (lane == 0) w_s[quad * N + n] = l[n];
     }
     bar_sync(3, 128);
-    const bool bad = *abort_p != 0;
+    const bool bad = *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0;
     auto sum_of = [&](int n) { return (w_s[n] + w_s[N + n]) + (w_s[2 * N + n] + w_s[3 * N + n]); };
     const long long item0 = (long long)q.row0 * p.H;
     if (th < R) {

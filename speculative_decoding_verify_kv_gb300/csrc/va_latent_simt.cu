@@ -222,67 +222,72 @@ __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentPar
 }
 
 // Merge of a sequence's chunks: M over the chunks, then l and o with the
-// weights 2^(m - M).  W warps share a (row, head): warp w takes chunks w, w + W,
-// .. in ascending order, then the warps' sums are added in warp order, so the
-// sums depend on the row's own partials alone.  W is 8 where a sequence of the
-// launch's most rows may have more than eight chunks, else 1 (one token of 16
-// heads in 64 chunks, the whole call: 21.6 us against 34; 1,024 rows x heads of
-// two chunks: 28 us more with eight warps to each).  Sequences of one chunk have their
-// o already, rows of inconsistent sequences their NaN.
+// weights 2^(m - M).  Which kernel merges follows from the most rows and chunks
+// that the launch allows, and the order of the sums from that and the row's own
+// partials alone.  Sequences of one chunk have their o already, rows of
+// inconsistent sequences their NaN.
 constexpr int kLmThreads = 256;
+constexpr int kLmWarps = kLmThreads / 32;
 
-template <int DV, int W>
-__global__ void __launch_bounds__(kLmThreads) latent_merge_kernel(const LatentParams p) {
-  constexpr int NC = DV / 128 > 0 ? DV / 128 : 1;  // float4 columns per lane (DV = 64: half the lanes)
-  __shared__ float4 acc_s[W > 1 ? W : 1][W > 1 ? DV / 4 : 1];
-  __shared__ float l_s[W > 1 ? W : 1];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const int lane = threadIdx.x & 31, warp = W > 1 ? threadIdx.x / 32 : 0;
-  const long long item = W > 1 ? (long long)blockIdx.x : (long long)blockIdx.x * (kLmThreads / 32) + threadIdx.x / 32;
-  if (item >= (long long)p.total_rows * p.H) return;
-  const int grow = (int)(item / p.H);
-  int s = -1;  // the last sequence that starts at or before the row
+// The sequence of item's row: the last that starts at or before it (32 at a
+// time); -1 where none covers it.
+__device__ __forceinline__ int latent_find(const LatentParams& p, int grow, int lane) {
+  int s = -1;
   for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
     const unsigned m = __ballot_sync(0xffffffffu, s0 + lane < p.num_seqs && p.cu_rows[s0 + lane] <= grow);
     if (m) s = s0 + 31 - __clz(m);
   }
-  if (s < 0 || grow >= p.cu_rows[s + 1]) return;
-  const LatentSeq q = latent_seq(p, s);
-  if (q.err) return;  // written as NaN
-  const int live = latent_live(q.len, latent_chunks(p, q.n));
-  if (live == 1) return;
-  bool nan = false;
-  float M = -INFINITY;
-  for (int k = lane; k < live; k += 32) {
-    const long long si = latent_slot(p, k, item);
-    const float mk = p.ws_ml[2 * si], lk = p.ws_ml[2 * si + 1];
-    if (isnan(mk) || isnan(lk)) nan = true;
-    if (lk > 0.f) M = fmaxf(M, mk);
+  return s >= 0 && grow < p.cu_rows[s + 1] ? s : -1;
+}
+
+__device__ __forceinline__ void latent_store4(const LatentParams& p, long long at, float4 v, float inv) {
+  v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+  if (p.o_bf16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    uint2 w;
+    memcpy(&w.x, &a, 4);
+    memcpy(&w.y, &b, 4);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + at) = w;
+  } else {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + at) = v;
   }
-  nan = __any_sync(0xffffffffu, nan);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float l = 0.f;
-  float4 acc[NC];
+}
+
+// Takes chunks first, first + step, .. (B of them in flight at once: m, l and a
+// float4 of acc together) into a running (M, l, acc) of the calling warp's lanes,
+// NC columns of 4 to a lane from column col on.
+template <int DV, int NC, int B>
+__device__ __forceinline__ void latent_gather(const LatentParams& p, long long item, int live, int first, int step, int col,
+                                              bool mine, float& M, float& l, float4 (&acc)[NC], bool& nan) {
+  M = -INFINITY;
+  l = 0.f;
 #pragma unroll
   for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const bool mine = DV >= 128 || lane < 16;
-  constexpr int B = 4;  // chunks in flight
-  for (int s0 = warp; s0 < live && !nan; s0 += B * W) {
+  for (int s0 = first; s0 < live; s0 += B * step) {
     float mm[B], ll[B];
     float4 aa[B][NC];
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      const bool in = s0 + k * W < live;
-      const long long si = latent_slot(p, in ? s0 + k * W : s0, item);
+      const bool in = s0 + k * step < live;
+      const long long si = latent_slot(p, in ? s0 + k * step : s0, item);
       mm[k] = in ? p.ws_ml[2 * si] : -INFINITY;
       ll[k] = in ? p.ws_ml[2 * si + 1] : 0.f;
 #pragma unroll
       for (int c = 0; c < NC; ++c)
-        aa[k][c] = in && mine ? *reinterpret_cast<const float4*>(p.ws_acc + si * DV + 4 * (lane + 32 * c))
+        aa[k][c] = in && mine ? *reinterpret_cast<const float4*>(p.ws_acc + si * DV + col + 128 * c)
                               : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    float bm = M;
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      if (isnan(mm[k]) || isnan(ll[k])) nan = true;
+      if (ll[k] > 0.f) bm = fmaxf(bm, mm[k]);
+    }
+    const float f = M == -INFINITY ? 0.f : exp2f(M - bm);
+    M = bm;
+    l *= f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[c] = make_float4(acc[c].x * f, acc[c].y * f, acc[c].z * f, acc[c].w * f);
 #pragma unroll
     for (int k = 0; k < B; ++k) {
       // A chunk that a row sees nothing of: its acc is not read as data.
@@ -298,45 +303,78 @@ __global__ void __launch_bounds__(kLmThreads) latent_merge_kernel(const LatentPa
       }
     }
   }
-  if constexpr (W > 1) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-      if (mine) acc_s[warp][lane + 32 * c] = acc[c];
-    if (lane == 0) l_s[warp] = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) l += l_s[w];
-  }
+}
+
+// Few chunks: a warp per (row, head).
+template <int DV>
+__global__ void __launch_bounds__(kLmThreads) latent_merge_kernel(const LatentParams p) {
+  constexpr int NC = DV / 128 > 0 ? DV / 128 : 1;  // (DV = 64: half the lanes)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * kLmWarps + threadIdx.x / 32;
+  if (item >= (long long)p.total_rows * p.H) return;
+  const int s = latent_find(p, (int)(item / p.H), lane);
+  if (s < 0) return;
+  const LatentSeq q = latent_seq(p, s);
+  const int live = latent_live(q.len, latent_chunks(p, q.n));
+  if (q.err || live == 1) return;
+  const bool mine = DV >= 128 || lane < 16;
+  float M, l;
+  float4 acc[NC];
+  bool nan = false;
+  latent_gather<DV, NC, 4>(p, item, live, 0, 1, 4 * lane, mine, M, l, acc, nan);
   const float inv = nan ? NAN : l > 0.f ? 1.f / l : 0.f;
-  auto store = [&](int col4, float4 v) {
-    const long long at = item * DV + 4 * col4;
-    v = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-    if (p.o_bf16) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-      uint2 w;
-      memcpy(&w.x, &a, 4);
-      memcpy(&w.y, &b, 4);
-      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.o) + at) = w;
-    } else {
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.o) + at) = v;
-    }
-  };
-  if constexpr (W > 1) {
-    for (int c = threadIdx.x; c < DV / 4; c += kLmThreads) {
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float4 x = acc_s[w][c];
-        v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
-      }
-      store(c, v);
-    }
-  } else if (mine) {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) store(lane + 32 * c, acc[c]);
+  for (int c = 0; c < NC; ++c)
+    if (mine) latent_store4(p, item * DV + 4 * lane + 128 * c, acc[c], inv);
+  if (lane == 0) p.lse[item] = nan ? NAN : l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// Many chunks (of few rows): a CTA per (row, head) and 128 columns, each of its
+// eight warps every eighth chunk, then the warps' sums in warp order.  With one
+// warp to a row the merge of 64 chunks was more than half of the call.
+template <int DV>
+__global__ void __launch_bounds__(kLmThreads) latent_merge_many_kernel(const LatentParams p) {
+  __shared__ float4 acc_s[kLmWarps][32];
+  __shared__ float m_s[kLmWarps], l_s[kLmWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const long long item = blockIdx.x;
+  const int s = latent_find(p, (int)(item / p.H), lane);
+  if (s < 0) return;
+  const LatentSeq q = latent_seq(p, s);
+  const int live = latent_live(q.len, latent_chunks(p, q.n));
+  if (q.err || live == 1) return;
+  const int col = blockIdx.y * 128 + 4 * lane;
+  float M, l;
+  float4 acc[1];
+  bool nan = false;
+  latent_gather<DV, 1, 8>(p, item, live, warp, kLmWarps, col, col < DV, M, l, acc, nan);
+  acc_s[warp][lane] = acc[0];
+  if (lane == 0) {
+    m_s[warp] = M;
+    l_s[warp] = l;
   }
-  if (lane == 0 && warp == 0) p.lse[item] = nan ? NAN : l > 0.f ? (M + log2f(l)) * kLn2 : -INFINITY;
+  nan = __syncthreads_or(nan) != 0;
+  if (warp != 0) return;
+  float Mall = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kLmWarps; ++w)
+    if (l_s[w] > 0.f) Mall = fmaxf(Mall, m_s[w]);
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kLmWarps; ++w) {
+    const float f = l_s[w] > 0.f ? exp2f(m_s[w] - Mall) : 0.f;
+    const float4 x = acc_s[w][lane];
+    sum = fmaf(f, l_s[w], sum);
+    t = make_float4(fmaf(f, x.x, t.x), fmaf(f, x.y, t.y), fmaf(f, x.z, t.z), fmaf(f, x.w, t.w));
+  }
+  const float inv = nan ? NAN : sum > 0.f ? 1.f / sum : 0.f;
+  if (col < DV) latent_store4(p, item * DV + col, t, inv);
+  if (lane == 0 && blockIdx.y == 0) p.lse[item] = nan ? NAN : sum > 0.f ? (Mall + log2f(sum)) * kLn2 : -INFINITY;
 }
 
 template <typename K>
@@ -381,10 +419,9 @@ cudaError_t launch_latent_simt(const LatentParams& p, dim3 grid, cudaStream_t st
 template <int DV>
 static cudaError_t launch_merge_of(const LatentParams& p, cudaStream_t st) {
   const long long items = (long long)p.total_rows * p.H;
-  constexpr int W = kLmThreads / 32;
   if (p.many)
-    return launch_one(latent_merge_kernel<DV, W>, dim3((unsigned)items), kLmThreads, 0, st, p);
-  return launch_one(latent_merge_kernel<DV, 1>, dim3((unsigned)((items + W - 1) / W)), kLmThreads, 0, st, p);
+    return launch_one(latent_merge_many_kernel<DV>, dim3((unsigned)items, (DV + 127) / 128), kLmThreads, 0, st, p);
+  return launch_one(latent_merge_kernel<DV>, dim3((unsigned)((items + kLmWarps - 1) / kLmWarps)), kLmThreads, 0, st, p);
 }
 
 cudaError_t launch_latent_merge(const LatentParams& p, cudaStream_t st) {

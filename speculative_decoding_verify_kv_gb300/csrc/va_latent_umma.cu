@@ -91,9 +91,19 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   int* err_s = reinterpret_cast<int*>(tmem_at + 2);
 
   asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   // Broadcasts: what a warp has in common is known to be so.
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+  if (tid == 0) {
+    *err_s = 0;
+    *abort_p = 0;
+    for (int i = 0; i < C::NB; ++i)
+      mbar_init(bar(i), i == LB_PFULL || i == LB_PFULL + 1 || i == LB_QREADY ? 8 : 1);
+    fence_barrier_init();
+  }
+  // Nothing but this CTA's own shared memory is touched before the work ahead
+  // on the stream has completed.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int s = blockIdx.z;
   const int head = PROMPT ? blockIdx.y : 0, part = PROMPT ? 0 : blockIdx.y;
   const LatentSeq q = latent_seq(p, s);
@@ -119,51 +129,34 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   // Tokens below it are seen by every row of the block.
   const int all_see = q.kind == 1 ? min(hi, q.ctx) : (PROMPT && !p.causal) ? hi : min(hi, q.ctx + jfirst + 1);
 
-  auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto vfull = [&](int i) { return bar(LB_RING + i); };
   auto vfree = [&](int i) { return bar(LB_RING + C::NV + i); };
   auto kfull = [&](int i) { return bar(LB_RING + 2 * C::NV + i); };
   auto kfree = [&](int i) { return bar(LB_RING + 2 * C::NV + C::NK + i); };
   const uint32_t base = smem_u32(sm);
 
-  if (tid == 0) {
-    *err_s = 0;
-    *abort_p = 0;
-    for (int i = 0; i < C::NB; ++i)
-      mbar_init(bar(i), i == LB_PFULL || i == LB_PFULL + 1 || i == LB_QREADY ? 8 : 1);
-    fence_barrier_init();
-  }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_at), 512);
     tmem_relinquish();
   }
-  // This thread's query row, its mask, and the chunk's pages.
   const int quad = warp & 3;
   const int r = quad * 32 + lane;
   const bool is_sm = warp >= 2 && warp < 10;
   const bool rvalid = is_sm && r < nrows;
   const int j = rvalid ? (PROMPT ? rbase + r : (rbase + r) / p.H) : 0;
-  __syncthreads();
-  unsigned anc = 0u;
-  if (rvalid && !q.err && q.kind == 1) {
-    bool bad = false;
-    anc = row_mask(1, p.parent + q.row0, j, &bad);
-    if (bad) atomicOr(err_s, (int)VA_DEV_BAD_PARENT);
-  }
-  if (!PROMPT && p.page_size && ntiles > 0) {
-    for (int pg = lo / kPage + tid; pg < (hi + kPage - 1) / kPage; pg += kLuThreads) {
-      const int blk = p.block_table[(long long)s * p.max_blocks + pg];
-      if (blk < 0 || blk >= p.num_blocks) atomicOr(err_s, (int)VA_DEV_BAD_BLOCK);
-    }
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const unsigned err = q.err | (unsigned)*err_s;
   const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_at, 0);
-  const int work = __shfl_sync(0xffffffffu, err ? 0 : ntiles, 0);
+  const int work = __shfl_sync(0xffffffffu, ntiles, 0);
   const bool ragged = __shfl_sync(0xffffffffu, (hi - lo) % NT, 0) != 0;  // of the last tile
-  if (err && tid == 0) flag(p.status, err);
+  if (q.err && tid == 0) flag(p.status, q.err);
+  // A finding on the way (a bad parent or page) does not stop the pipeline: what
+  // it computes then is replaced by NaN at the end.
+  auto found = [&](unsigned bits) {
+    atomicOr(err_s, (int)bits);
+    flag(p.status, bits);
+  };
   auto fail = [&]() {
     *abort_p = 1;
     flag(p.status, VA_DEV_TIMEOUT);
@@ -183,7 +176,13 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     const uint32_t one = elected();
     auto page_of = [&](int t) {  // (row, plane) of a page's tokens in the cache's map
       const int pg = t / kPage;
-      return p.page_size ? make_int2(0, p.block_table[(long long)s * p.max_blocks + pg]) : make_int2(pg * kPage, s);
+      if (p.page_size == 0) return make_int2(pg * kPage, s);
+      int blk = p.block_table[(long long)s * p.max_blocks + pg];
+      if (blk < 0 || blk >= p.num_blocks) {
+        found(VA_DEV_BAD_BLOCK);
+        blk = 0;
+      }
+      return make_int2(0, blk);
     };
     const int lo_u = __shfl_sync(0xffffffffu, lo, 0), hi_u = __shfl_sync(0xffffffffu, hi, 0);
     const int key0 = __shfl_sync(0xffffffffu, (int)q.key0, 0);
@@ -417,6 +416,12 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(LB_QREADY));
 
+    unsigned anc = 0u;
+    if (rvalid && q.kind == 1) {
+      bool bad_parent = false;
+      anc = row_mask(1, p.parent + q.row0, j, &bad_parent);
+      if (bad_parent) found(VA_DEV_BAD_PARENT);
+    }
     float m_use = -INFINITY, l_run = 0.f;
     const float c_r = p.scale_log2;
     // A failed wait does not leave the loop: every iteration has one named
@@ -511,9 +516,9 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     if (!ok && lane == 0) fail();
     tc_fence_after();
     red[half * kLuM + r] = l_run;
-    bar_sync(5 + quad, 64);
+    bar_sync(1, 256);
     const float l = red[r] + red[kLuM + r];
-    const bool bad = __any_sync(0xffffffffu, *abort_p != 0);
+    const bool bad = __any_sync(0xffffffffu, *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0);
     const float inv = bad ? NAN : l > 0.f ? 1.f / l : 0.f;
     if (rvalid && half == 0 && part == 0) {
       const long long item = latent_item(p, q.row0, rbase + r, head);
@@ -576,12 +581,12 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       if (live > 1) {
         if (d == 0 && part == 0) {
           const long long si = latent_slot(p, chunk, item);
-          p.ws_ml[2 * si] = err ? NAN : -INFINITY;
-          p.ws_ml[2 * si + 1] = err ? NAN : 0.f;
+          p.ws_ml[2 * si] = q.err ? NAN : -INFINITY;
+          p.ws_ml[2 * si + 1] = q.err ? NAN : 0.f;
         }
       } else {
-        reinterpret_cast<unsigned short*>(p.o)[item * C::DV + part * DO + d] = err ? 0x7fffu : 0u;
-        if (d == 0 && part == 0) p.lse[item] = err ? NAN : -INFINITY;
+        reinterpret_cast<unsigned short*>(p.o)[item * C::DV + part * DO + d] = q.err ? 0x7fffu : 0u;
+        if (d == 0 && part == 0) p.lse[item] = q.err ? NAN : -INFINITY;
       }
     }
   }
