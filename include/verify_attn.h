@@ -709,8 +709,9 @@ va_status verify_attn_latent_append(const va_latent *kv, const va_latent_rows *r
  * ctx + n - 1 of the cache.  o: [total_rows][num_heads][latent_dim] of the
  * cache's dtype, rounded once; lse: fp32 [total_rows][num_heads].
  * num_splits is the largest number of chunks (whole 64-token tiles, at least
- * 128 tokens) that a sequence is cut into; where its rows times heads make b
- * row blocks (of 128 in the tensor-core kernel; of 16 on the CUDA cores: fp32
+ * 128 tokens; 64 on the CUDA cores) that a sequence is cut into; where its rows times heads make b
+ * row blocks (of 128 in the tensor-core kernel, one block of up to 32 where
+ * max_rows_per_seq times num_heads is no more; of 16 on the CUDA cores: fp32
  * caches, VA_FLAG_CUDA_CORES) each takes num_splits / b chunks, rounded
  * down, and at least one.  va_latent_splits gives a count that fills the
  * GPU.  No choice depends on the other sequences of the launch.

@@ -14,7 +14,6 @@
 namespace va {
 
 constexpr int kLatentRope = 64;
-constexpr int kLatentMinChunk = 128;  // tokens
 
 struct LatentParams {
   int num_seqs, H, total_rows, max_rows, mode;
@@ -39,6 +38,7 @@ struct LatentParams {
   int total_kv, causal;
   int prompt;
   int slots;              // largest number of chunks of a sequence
+  int min_chunk;          // tokens
   int many;               // a sequence of max_rows rows may have many
   int rows_per_block;
   float* ws_acc;          // [slots][total_rows][H][DV]
@@ -99,13 +99,13 @@ __device__ __forceinline__ int latent_chunks(const LatentParams& p, int n) {
 }
 
 // Chunk c of nchunk of [0, len).
-__device__ __forceinline__ void latent_range(int len, int nchunk, int c, int* lo, int* hi) {
-  sub_range(0, len, nchunk, kLatentMinChunk, c, lo, hi);
+__device__ __forceinline__ void latent_range(const LatentParams& p, int len, int nchunk, int c, int* lo, int* hi) {
+  sub_range(0, len, nchunk, p.min_chunk, c, lo, hi);
 }
 
 // Chunks that hold tokens (they come first); 1 for a sequence of none.
-__device__ __forceinline__ int latent_live(int len, int nchunk) {
-  return max(1, live_subs(0, len, nchunk, kLatentMinChunk));
+__device__ __forceinline__ int latent_live(const LatentParams& p, int len, int nchunk) {
+  return max(1, live_subs(0, len, nchunk, p.min_chunk));
 }
 
 // Index among [total_rows][H] of query row r of a sequence (prompts: of head).

@@ -143,6 +143,7 @@ static LatentParams base_params(const va_problem* p, int mode, const LatentPlan&
   q.seq_kind = p->seq_kind;
   q.slots = pl.slots;
   q.many = pl.many;
+  q.min_chunk = pl.kernel == VA_KERNEL_TENSOR ? 128 : 64;
   q.rows_per_block = pl.rows_per_block;
   q.ws_acc = (float*)ws;
   q.ws_ml = ws ? (float*)((char*)ws + pl.acc_bytes) : nullptr;

@@ -119,10 +119,10 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
     return;
   }
   const int R = q.n * p.H;
-  const int live = latent_live(q.err ? 0 : q.len, latent_chunks(p, q.n));
+  const int live = latent_live(p, q.err ? 0 : q.len, latent_chunks(p, q.n));
   if (R == 0 || chunk >= live) return;
   int lo, hi;
-  latent_range(q.len, latent_chunks(p, q.n), chunk, &lo, &hi);
+  latent_range(p, q.len, latent_chunks(p, q.n), chunk, &lo, &hi);
   const int ntiles = q.err ? 0 : (hi - lo + kLrTile - 1) / kLrTile;
   const int all_see = q.kind == 1 ? min(hi, q.ctx) : min(hi, q.ctx + 1);
 

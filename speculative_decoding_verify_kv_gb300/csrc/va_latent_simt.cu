@@ -3,10 +3,14 @@
 // bf16 ones).
 //
 // One CTA owns 16 query rows and one chunk of tokens and walks it in tiles of
-// 32: scores with a token to a lane and two rows to a warp, online softmax
-// (m in log2 units, l), values accumulated in registers.  Over a latent cache
-// the values are the first DV of the key's own columns, so a tile is loaded
-// once.  The next tile's loads are under way while a tile is worked through.
+// 32.  Two warps share four rows: for the scores each takes half of the tile's
+// tokens (a lane: one token, half of the key's columns), for the online softmax
+// (m in log2 units, l) two of the rows, for the values half of the columns, in
+// registers; so a value read from shared memory serves four rows.  (Two rows to
+// a warp, all tokens and columns: 32 us for the 5 x 80 rows of 320 columns over
+// some 500 tokens, bound by those reads.)  Over a latent cache the values are the
+// first DV of the key's own columns, so a tile is loaded once.  The next tile's
+// loads are under way while a tile is worked through.
 // A chunk that is a sequence's only one writes o itself; others leave (m, l,
 // acc) for the merge.
 #include <string.h>
@@ -22,7 +26,8 @@ constexpr int kLsThreads = 256;
 template <int DK, int DV, bool PROMPT>
 struct LsCfg {
   static constexpr int LDK = DK + 4;  // lanes of a float4 read of a column hit banks of their own
-  static constexpr int SMEM = (kLsRows * DK + kLsTile * LDK + (PROMPT ? kLsTile * DV : 0) + kLsRows * kLsTile) * 4;
+  static constexpr int LDS = kLsTile + 1, LDP = kLsRows + 4;
+  static constexpr int SMEM = (kLsRows * DK + kLsTile * LDK + (PROMPT ? kLsTile * DV : 0) + kLsTile * LDP + kLsRows * LDS) * 4;
 };
 
 // Four elements at index i (a multiple of 4; rows start on 16 bytes).
@@ -37,11 +42,15 @@ __device__ __forceinline__ float4 load4(const void* base, long long i) {
   }
 }
 
+// The two warps of a row group.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
 template <typename T, int DK, int DV, bool PROMPT>
 __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentParams p) {
   using C = LsCfg<DK, DV, PROMPT>;
-  constexpr int WARPS = kLsThreads / 32, RW = kLsRows / WARPS;
-  constexpr int NC = DV / 64;                      // float2 columns per lane
+  constexpr int RW = 4;                            // rows that two warps share
+  constexpr int NC = DV / 2 / 32;                  // value columns per lane
+  constexpr int CV = NC > 1 ? 2 : 1;               // side by side
   constexpr int ROW4 = (DK + (PROMPT ? DV : 0)) / 4;  // float4 pieces of a token's key and value
   constexpr int NL = (kLsTile * ROW4 + kLsThreads - 1) / kLsThreads;
   extern __shared__ __align__(16) float lsm[];
@@ -49,8 +58,11 @@ __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentPar
   float* Ks = Qs + kLsRows * DK;
   float* Vs = PROMPT ? Ks + kLsTile * C::LDK : Ks;
   constexpr int LDV = PROMPT ? DV : C::LDK;
-  float* Ps = Ks + kLsTile * C::LDK + (PROMPT ? kLsTile * DV : 0);
+  float* Ps = Ks + kLsTile * C::LDK + (PROMPT ? kLsTile * DV : 0);  // weights, [token][row]
+  float* Ss = Ps + kLsTile * C::LDP;                                // scores, [row][token]
+  __shared__ float f_s[kLsRows], m_s[kLsRows], l_s[kLsRows];
   __shared__ unsigned anc_s[kLsRows];
+  __shared__ int parent_s[kMaxTreeRows];
   __shared__ int bad_s;
 
   asm volatile("griddepcontrol.launch_dependents;");
@@ -68,27 +80,14 @@ __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentPar
   if (blocks == 0) return;
   const int nchunk = latent_chunks(p, q.n);
   const int rb = blockIdx.x % blocks, chunk = blockIdx.x / blocks;
-  const int live = latent_live(q.err ? 0 : q.len, nchunk);
+  const int live = latent_live(p, q.err ? 0 : q.len, nchunk);
   if (chunk >= live) return;
   const int rbase = rb * kLsRows, nrows = min(kLsRows, R - rbase);
   int lo, hi;
-  latent_range(q.len, nchunk, chunk, &lo, &hi);
+  latent_range(p, q.len, nchunk, chunk, &lo, &hi);
   const int jlast = PROMPT ? rbase + nrows - 1 : (rbase + nrows - 1) / p.H;
   hi = max(lo, min(hi, latent_end(p, q, jlast)));
   unsigned err = q.err;
-
-  if (tid == 0) bad_s = 0;
-  __syncthreads();
-  if (tid < nrows && !err) {
-    bool bad = false;
-    anc_s[tid] = row_mask(q.kind, p.parent + q.row0, PROMPT ? rbase + tid : (rbase + tid) / p.H, &bad);
-    if (bad) atomicOr(&bad_s, (int)VA_DEV_BAD_PARENT);
-  }
-  for (int i = tid; i < nrows * (DK / 4); i += kLsThreads) {
-    const long long item = latent_item(p, q.row0, rbase + i / (DK / 4), head);
-    *reinterpret_cast<float4*>(Qs + i * 4) = load4<T>(p.q, item * DK + i % (DK / 4) * 4);
-  }
-  for (int i = nrows * DK + tid; i < kLsRows * DK; i += kLsThreads) Qs[i] = 0.f;
 
   float4 x[NL];
   bool lost = false;
@@ -111,18 +110,34 @@ __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentPar
       }
     }
   };
-  float m_run[RW], l_run[RW];
-  float2 acc[RW][NC];
+  if (!err && lo < hi) load(lo);  // under way while queries and masks are fetched
+  if (tid == 0) bad_s = 0;
+  if (q.kind == 1 && tid < q.n) parent_s[tid] = p.parent[q.row0 + tid];
+  __syncthreads();
+  if (tid < nrows && q.kind == 1) {
+    bool bad = false;
+    anc_s[tid] = row_mask(1, parent_s, (rbase + tid) / p.H, &bad);
+    if (bad) atomicOr(&bad_s, (int)VA_DEV_BAD_PARENT);
+  }
+  for (int i = tid; i < nrows * (DK / 4); i += kLsThreads) {
+    const long long item = latent_item(p, q.row0, rbase + i / (DK / 4), head);
+    *reinterpret_cast<float4*>(Qs + i * 4) = load4<T>(p.q, item * DK + i % (DK / 4) * 4);
+  }
+  for (int i = nrows * DK + tid; i < kLsRows * DK; i += kLsThreads) Qs[i] = 0.f;
+
+  const int rg = warp & 3, half = warp >> 2;  // row group; which half of tokens, rows and columns
+  float m_run[2], l_run[2], acc[RW][NC];      // m, l: rows 4 rg + 2 half and the next
 #pragma unroll
-  for (int i = 0; i < RW; ++i) {
+  for (int i = 0; i < 2; ++i) {
     m_run[i] = -INFINITY;
     l_run[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) acc[i][c] = make_float2(0.f, 0.f);
   }
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[i][c] = 0.f;
   __syncthreads();
   err |= (unsigned)bad_s;
-  if (!err && lo < hi) load(lo);
   for (int t0 = lo; t0 < hi && !err; t0 += kLsTile) {
     __syncthreads();
 #pragma unroll
@@ -137,25 +152,34 @@ __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentPar
       break;
     }
     if (t0 + kLsTile < hi) load(t0 + kLsTile);
-    if (warp * RW >= nrows) continue;
-    float sc[RW];
-#pragma unroll
-    for (int i = 0; i < RW; ++i) sc[i] = 0.f;
+    if (rg * RW >= nrows) continue;
+    {
+      const int tok = half * 16 + (lane & 15), d0 = (lane >> 4) * (DK / 2);
+      const float* kr = Ks + tok * C::LDK + d0;
+      const float* qr = Qs + rg * RW * DK + d0;
+      float sc[RW] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int d = 0; d < DK; d += 4) {
-      const float4 k4 = *reinterpret_cast<const float4*>(Ks + lane * C::LDK + d);
+      for (int d = 0; d < DK / 2; d += 4) {
+        const float4 k4 = *reinterpret_cast<const float4*>(kr + d);
+#pragma unroll
+        for (int i = 0; i < RW; ++i) {
+          const float4 q4 = *reinterpret_cast<const float4*>(qr + i * DK + d);
+          sc[i] = fmaf(q4.w, k4.w, fmaf(q4.z, k4.z, fmaf(q4.y, k4.y, fmaf(q4.x, k4.x, sc[i]))));
+        }
+      }
 #pragma unroll
       for (int i = 0; i < RW; ++i) {
-        const float4 q4 = *reinterpret_cast<const float4*>(Qs + (warp * RW + i) * DK + d);
-        sc[i] = fmaf(q4.w, k4.w, fmaf(q4.z, k4.z, fmaf(q4.y, k4.y, fmaf(q4.x, k4.x, sc[i]))));
+        sc[i] += __shfl_xor_sync(0xffffffffu, sc[i], 16);
+        if (lane < 16) Ss[(rg * RW + i) * C::LDS + tok] = sc[i];
       }
     }
+    pair_sync(1 + rg);
 #pragma unroll
-    for (int i = 0; i < RW; ++i) {
-      const int rl = warp * RW + i;
+    for (int i = 0; i < 2; ++i) {
+      const int rl = rg * RW + 2 * half + i;
       const int j = PROMPT ? rbase + rl : (rbase + rl) / p.H;
-      const unsigned vis = rl < nrows ? latent_bits(p, q, anc_s[rl], j, hi, t0) : 0u;
-      const float z = (vis >> lane) & 1u ? sc[i] * p.scale_log2 : -INFINITY;
+      const unsigned vis = rl < nrows ? latent_bits(p, q, q.kind == 1 ? anc_s[rl] : 0u, j, hi, t0) : 0u;
+      const float z = (vis >> lane) & 1u ? Ss[rl * C::LDS + lane] * p.scale_log2 : -INFINITY;
       float mx = z;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -167,56 +191,72 @@ __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentPar
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       l_run[i] = l_run[i] * f + sum;
       m_run[i] = m_new;
-      Ps[rl * kLsTile + lane] = w;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        acc[i][c].x *= f;
-        acc[i][c].y *= f;
-      }
+      Ps[lane * C::LDP + rl] = w;
+      if (lane == 0) f_s[rl] = f;
     }
-    __syncwarp();
+    pair_sync(1 + rg);
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      const float f = f_s[rg * RW + i];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) acc[i][c] *= f;
+    }
+    const float* vr = Vs + half * (DV / 2) + CV * lane;
 #pragma unroll 4
     for (int t = 0; t < kLsTile; ++t) {
-      float w[RW];
+      const float4 w4 = *reinterpret_cast<const float4*>(Ps + t * C::LDP + rg * RW);
+      const float w[RW] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
-      for (int i = 0; i < RW; ++i) w[i] = Ps[(warp * RW + i) * kLsTile + t];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const float2 v = *reinterpret_cast<const float2*>(Vs + t * LDV + 2 * lane + 64 * c);
-#pragma unroll
-        for (int i = 0; i < RW; ++i) {
-          acc[i][c].x = fmaf(w[i], v.x, acc[i][c].x);
-          acc[i][c].y = fmaf(w[i], v.y, acc[i][c].y);
+      for (int c = 0; c < NC; c += CV) {
+        float v[CV];
+        if constexpr (CV == 2) {
+          const float2 v2 = *reinterpret_cast<const float2*>(vr + t * LDV + 32 * c);
+          v[0] = v2.x;
+          v[1] = v2.y;
+        } else {
+          v[0] = vr[t * LDV + 32 * c];
         }
+#pragma unroll
+        for (int i = 0; i < RW; ++i)
+#pragma unroll
+          for (int e = 0; e < CV; ++e) acc[i][c + e] = fmaf(w[i], v[e], acc[i][c + e]);
       }
     }
-    __syncwarp();
   }
   if (err && tid == 0) flag(p.status, err);
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      m_s[rg * RW + 2 * half + i] = m_run[i];
+      l_s[rg * RW + 2 * half + i] = l_run[i];
+    }
+  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < RW; ++i) {
-    const int rl = warp * RW + i;
+    const int rl = rg * RW + i;
     if (rl >= nrows) continue;
     const long long item = latent_item(p, q.row0, rbase + rl, head);
+    const float l = l_s[rl], m = m_s[rl];
+    const int col = half * (DV / 2) + CV * lane;
     if (live > 1) {
       const long long si = latent_slot(p, chunk, item);
-      if (lane == 0) {
-        p.ws_ml[2 * si] = err ? NAN : m_run[i];
-        p.ws_ml[2 * si + 1] = err ? NAN : l_run[i];
+      if (lane == 0 && half == 0) {
+        p.ws_ml[2 * si] = err ? NAN : m;
+        p.ws_ml[2 * si + 1] = err ? NAN : l;
       }
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-        *reinterpret_cast<float2*>(p.ws_acc + si * DV + 2 * lane + 64 * c) = acc[i][c];
+      for (int c = 0; c < NC; ++c) p.ws_acc[si * DV + col + 32 * (c / CV * CV) + c % CV] = acc[i][c];
       continue;
     }
-    const float inv = err ? NAN : l_run[i] > 0.f ? 1.f / l_run[i] : 0.f;
-    if (lane == 0) p.lse[item] = err ? NAN : l_run[i] > 0.f ? (m_run[i] + log2f(l_run[i])) * kLn2 : -INFINITY;
+    const float inv = err ? NAN : l > 0.f ? 1.f / l : 0.f;
+    if (lane == 0 && half == 0) p.lse[item] = err ? NAN : l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const float2 v = make_float2(acc[i][c].x * inv, acc[i][c].y * inv);
-      const long long at = item * DV + 2 * lane + 64 * c;
-      if (sizeof(T) == 4) *reinterpret_cast<float2*>(reinterpret_cast<float*>(p.o) + at) = v;
-      else *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(p.o) + at) = __floats2bfloat162_rn(v.x, v.y);
+      const long long at = item * DV + col + 32 * (c / CV * CV) + c % CV;
+      const float v = acc[i][c] * inv;
+      if (sizeof(T) == 4) reinterpret_cast<float*>(p.o)[at] = v;
+      else reinterpret_cast<__nv_bfloat16*>(p.o)[at] = __float2bfloat16_rn(v);
     }
   }
 }
@@ -317,7 +357,7 @@ __global__ void __launch_bounds__(kLmThreads) latent_merge_kernel(const LatentPa
   const int s = latent_find(p, (int)(item / p.H), lane);
   if (s < 0) return;
   const LatentSeq q = latent_seq(p, s);
-  const int live = latent_live(q.len, latent_chunks(p, q.n));
+  const int live = latent_live(p, q.len, latent_chunks(p, q.n));
   if (q.err || live == 1) return;
   const bool mine = DV >= 128 || lane < 16;
   float M, l;
@@ -345,7 +385,7 @@ __global__ void __launch_bounds__(kLmThreads) latent_merge_many_kernel(const Lat
   const int s = latent_find(p, (int)(item / p.H), lane);
   if (s < 0) return;
   const LatentSeq q = latent_seq(p, s);
-  const int live = latent_live(q.len, latent_chunks(p, q.n));
+  const int live = latent_live(p, q.len, latent_chunks(p, q.n));
   if (q.err || live == 1) return;
   const int col = blockIdx.y * 128 + 4 * lane;
   float M, l;

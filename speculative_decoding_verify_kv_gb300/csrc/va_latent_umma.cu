@@ -117,13 +117,13 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   if (blocks == 0) return;
   const int nchunk = latent_chunks(p, q.n);
   const int rb = blockIdx.x % blocks, chunk = blockIdx.x / blocks;
-  const int live = latent_live(q.err ? 0 : q.len, nchunk);
+  const int live = latent_live(p, q.err ? 0 : q.len, nchunk);
   if (chunk >= live) return;
   const int rbase = rb * kLuM, nrows = min(kLuM, R - rbase);
   const int jfirst = PROMPT ? rbase : rbase / p.H;
   const int jlast = PROMPT ? rbase + nrows - 1 : (rbase + nrows - 1) / p.H;
   int lo, hi;
-  latent_range(q.len, nchunk, chunk, &lo, &hi);
+  latent_range(p, q.len, nchunk, chunk, &lo, &hi);
   hi = max(lo, min(hi, latent_end(p, q, jlast)));
   const int ntiles = q.err ? 0 : (hi - lo + NT - 1) / NT;
   // Tokens below it are seen by every row of the block.

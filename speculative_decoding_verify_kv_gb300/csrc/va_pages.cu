@@ -50,6 +50,7 @@ struct PageParams {
   const int* parent;
   const unsigned char* kind;
   int* cu;
+  int* row_first;  // first fresh page of each sequence (many sequences)
   int* row_seq;
   int* position;
   long long* slot;
@@ -366,19 +367,34 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_kernel(const PagePara
 // Block tables and slot maps from request lengths.  Sequence s holds a[s]
 // tokens and gets b[s] rows: entries ceil(a / 16) to ceil((a + b) / 16) - 1
 // that hold no page take the lowest free ones, and every row learns its
-// sequence, position and slot.  Workspace: need[num_seqs] (then each
-// sequence's first fresh page), free pages found [num_blocks].
+// sequence, position and slot.  Workspace: need[num_seqs], free pages found
+// [num_blocks], first fresh page [num_seqs].
 //
-// Bound by the latency of its steps (five barriers, six with trees): 39
-// sequences of one row over 8,192 pages, one CTA; 256 sequences of up to 8
-// rows over 131,072 pages, a cluster.  Eight lanes go through a sequence's
-// entries: steps of few rows touch one or two of them, prompt segments some
-// dozens.
-constexpr int kSeqLanes = 8;
-constexpr int kCuShared = 2048;  // row offsets kept in shared memory
+// Bound by the latency of its dependent steps, so there are few: check and
+// count; each CTA then has every sequence's rows and needs in its own shared
+// memory and sums them up itself; the free pages wanted; then tables and rows
+// together, since a row can tell its page from the list as well as from the
+// table.  Two barriers of the CTAs (three with trees), against six where one CTA
+// sums and the rows wait for the tables: 40 sequences of one row, 8,192 pages, 14
+// us; 256 of up to 8 over 131,072, 23 us.
+// Integers of a step that one CTA plans: 40 sequences over 8,192 pages 6.5 us,
+// 8.3 with a cluster; 256 over 131,072 18.0, and 12.6.
+constexpr long long kOneCtaExtend = 16384;
+constexpr int kSeqLanes = 8;     // go through a sequence's entries
+constexpr int kSeqShared = 2048; // sequences whose sums stand in shared memory
+constexpr unsigned kSomeHeld = 0x80000000u;  // beside the findings: an entry that would be fresh holds a page
+static_assert(kSeqLanes >= kWideCtas, "each lane of a sequence tells one CTA");
 
-// First index of the last sequence that starts at or before row r and has
-// rows: the largest s with cu[s] <= r (cu ascending, cu[n] > r).
+struct ExtendShared {
+  unsigned count[kWideCtas * kCtaWarps];  // free pages of each warp's part
+  unsigned found[kWideCtas * kCtaWarps];  // findings
+  unsigned parents;
+  unsigned long long part[2][kCtaWarps];
+  int cu[kSeqShared + 1];                 // rows, then offsets
+  int first[kSeqShared];                  // needs, then each sequence's first fresh page
+};
+
+// The largest s with cu[s] <= r: of sequences that start at r, the one with rows.
 __device__ __forceinline__ int seq_of_row(const int* cu, int n, int r) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
@@ -395,136 +411,169 @@ __device__ __forceinline__ bool extend_is_tree(const PageParams& p, int s) {
 
 template <int NC>
 __global__ void __launch_bounds__(kPlanThreads) pages_extend_kernel(const PageParams p) {
-  __shared__ PlanShared sh;
-  __shared__ unsigned long long part_rows[kCtaWarps];
-  __shared__ unsigned long long part_need[kCtaWarps];
-  __shared__ int cu_s[kCuShared + 1];
+  __shared__ ExtendShared sh;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Team<NC> team;
+  if (NC > 1) team.cluster.barrier_arrive();  // waited for before the first write into another CTA
   const int rank = team.rank();
   const int tid = threadIdx.x, lane = tid & 31, gwarp = rank * kCtaWarps + tid / 32;
   const int gtid = rank * kPlanThreads + tid;
-  int* need = p.ws;
-  int* found = need + p.num_seqs;
-  if (tid == 0) sh.err = rank == 0 ? status_before(p) : 0u;
-  team.sync();
+  const bool shared = p.num_seqs <= kSeqShared;
+  int* const need_g = p.ws;
+  int* const found = p.ws + p.num_seqs;
+  if (tid == 0) sh.parents = 0u;
 
-  // Check every sequence and count the pages it takes; count the free ones.
+  // Free pages of this warp's part, as bits while it is 1,024 pages or less.
+  int lo, hi;
+  warp_share<NC>(p.num_blocks, gwarp, &lo, &hi);
+  const bool kept = hi - lo <= 1024;
+  unsigned err = rank == 0 && tid == 0 ? status_before(p) : 0u;
+  unsigned freec = 0, bits = 0;
+  {
+    int k = 0;
+#pragma unroll 8
+    for (int i = lo + lane; i < hi; i += 32, ++k) {
+      const int r = p.ref[i];
+      if (r < 0) err |= VA_DEV_BAD_BLOCK;
+      freec += r == 0;
+      if (r == 0 && k < 32) bits |= 1u << k;
+    }
+  }
+  if (NC > 1) team.cluster.barrier_wait();
+  // Check every sequence and count the pages it takes.
   const int sub = lane & (kSeqLanes - 1);
+  const unsigned peers = 0xffu << (lane & ~(kSeqLanes - 1));
   const long long groups = (long long)NC * kPlanThreads / kSeqLanes;
   for (long long s0 = gtid / kSeqLanes; s0 < p.num_seqs; s0 += groups) {
     const int s = (int)s0;
-    const unsigned peers = 0xffu << (lane & ~(kSeqLanes - 1));
     const int held = p.a[s], n = p.b[s];
-    unsigned err = 0u;
     int fresh = 0;
     if (n < 0 || (n > kMaxTreeRows && extend_is_tree(p, s))) {
-      err = VA_DEV_BAD_ROWS;
+      err |= VA_DEV_BAD_ROWS;
     } else if (held < 0 || ((long long)held + n + kPage - 1) / kPage > p.max_blocks) {
-      err = VA_DEV_CTX_OVERFLOW;
+      err |= VA_DEV_CTX_OVERFLOW;
     } else if (n > 0) {
       const int keep = (held + kPage - 1) / kPage, end = (held + n + kPage - 1) / kPage;
       const int* row = p.table + (long long)s * p.max_blocks;
       for (int c = held / kPage + sub; c < end; c += kSeqLanes) {
         const int e = row[c];
         // A page that rows are written to belongs to this sequence alone.
-        if (e != -1 && !(e >= 0 && e < p.num_blocks && p.ref[e] == 1)) err = VA_DEV_BAD_BLOCK;
-        if (e == -1 && c < keep) err = VA_DEV_BAD_BLOCK;  // the page that the held tokens end in
+        if (e != -1 && !(e >= 0 && e < p.num_blocks && p.ref[e] == 1)) err |= VA_DEV_BAD_BLOCK;
+        if (e == -1 && c < keep) err |= VA_DEV_BAD_BLOCK;  // the page that the held tokens end in
+        if (e != -1 && c >= keep) err |= kSomeHeld;
         fresh += e == -1;
       }
     }
     fresh += __shfl_xor_sync(peers, fresh, 1);
     fresh += __shfl_xor_sync(peers, fresh, 2);
     fresh += __shfl_xor_sync(peers, fresh, 4);
-    if (sub == 0) need[s] = fresh;
-    if (err) note_error(team, sh, err);
+    if (!shared) {
+      if (sub == 0) need_g[s] = fresh;
+    } else if (sub < NC) {
+      ExtendShared* to = team.at(&sh, sub);
+      to->cu[s] = n;
+      to->first[s] = fresh;
+    }
   }
-  int lo, hi;
-  warp_share<NC>(p.num_blocks, gwarp, &lo, &hi);
-  unsigned freec = 0;
-#pragma unroll 8
-  for (int i = lo + lane; i < hi; i += 32) {
-    const int r = p.ref[i];
-    if (r < 0) note_error(team, sh, VA_DEV_BAD_BLOCK);
-    freec += r == 0;
-  }
+  __syncwarp();
   freec = warp_add(freec);
-  share_count(team, sh, gwarp, lane, freec);
+  err = __reduce_or_sync(0xffffffffu, err);
+  if (lane < NC) {
+    ExtendShared* to = team.at(&sh, lane);
+    to->count[gwarp] = freec;
+    to->found[gwarp] = err;
+  }
   team.sync();
 
-  // The first CTA turns rows and needs into running totals, 1,024 sequences
-  // at a time (64-bit sums; past the limit the call fails below).
-  if (rank == 0 && read_error(team, sh) == 0u) {
-    unsigned long long base_rows = 0, base_need = 0;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
-      const int s = s0 + tid;
-      const unsigned long long a = s < p.num_seqs ? (unsigned long long)p.b[s] : 0ull;
-      const unsigned long long b = s < p.num_seqs ? (unsigned long long)need[s] : 0ull;
-      unsigned long long ia = a, ib = b;
+  // Every CTA: findings, free pages in all and before this warp's part.
+  unsigned all_free = 0, before = 0;
+  err = 0u;
+  for (int g = lane; g < NC * kCtaWarps; g += 32) {
+    err |= sh.found[g];
+    all_free += sh.count[g];
+    before += g < gwarp ? sh.count[g] : 0u;
+  }
+  err = __reduce_or_sync(0xffffffffu, err);
+  all_free = warp_add(all_free);
+  before = warp_add(before);
+  const bool some_held = (err & kSomeHeld) != 0u;
+  err &= ~kSomeHeld;
+  // Rows and needs to running totals, 1,024 sequences at a time (64-bit sums:
+  // past the limits the call fails below).
+  unsigned long long total_rows = 0, total_need = 0;
+  for (int s0 = 0; s0 < p.num_seqs && !err; s0 += kPlanThreads) {
+    const int s = s0 + tid;
+    const unsigned long long a = s < p.num_seqs ? (unsigned long long)(shared ? sh.cu[s] : p.b[s]) : 0ull;
+    const unsigned long long b = s < p.num_seqs ? (unsigned long long)(shared ? sh.first[s] : need_g[s]) : 0ull;
+    unsigned long long ia = a, ib = b;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long ua = __shfl_up_sync(0xffffffffu, ia, o), ub = __shfl_up_sync(0xffffffffu, ib, o);
-        if (lane >= o) {
-          ia += ua;
-          ib += ub;
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long ua = __shfl_up_sync(0xffffffffu, ia, o), ub = __shfl_up_sync(0xffffffffu, ib, o);
+      if (lane >= o) {
+        ia += ua;
+        ib += ub;
       }
-      if (lane == 31) {
-        part_rows[tid / 32] = ia;
-        part_need[tid / 32] = ib;
-      }
-      __syncthreads();
-      unsigned long long before_a = 0, before_b = 0, all_a = 0, all_b = 0;
-      for (int w = 0; w < kCtaWarps; ++w) {
-        if (w == tid / 32) {
-          before_a = all_a;
-          before_b = all_b;
-        }
-        all_a += part_rows[w];
-        all_b += part_need[w];
-      }
-      if (s < p.num_seqs) {
-        p.cu[s] = (int)min(base_rows + before_a + ia - a, 0x7fffffffull);
-        need[s] = (int)min(base_need + before_b + ib - b, 0x7fffffffull);
-      }
-      base_rows += all_a;
-      base_need += all_b;
-      __syncthreads();
     }
-    if (tid == 0) {
-      p.cu[p.num_seqs] = (int)min(base_rows, 0x7fffffffull);
-      sh.total_need = (unsigned)min(base_need, 0xffffffffull);
-      sh.total_tail = (unsigned)min(base_rows, 0xffffffffull);
-      if (base_rows > (unsigned long long)p.max_rows) sh.err |= VA_DEV_BAD_ROWS;
+    if (lane == 31) {
+      sh.part[0][tid / 32] = ia;
+      sh.part[1][tid / 32] = ib;
     }
-  }
-  team.sync();
-  unsigned err = read_error(team, sh);
-  const unsigned wanted = err ? 0u : *team.at(&sh.total_need, 0);
-  const int rows = err ? 0 : (int)*team.at(&sh.total_tail, 0);
-  const int* cu = p.cu;
-  if (!err && p.num_seqs <= kCuShared) {
-    for (int i = tid; i <= p.num_seqs; i += kPlanThreads) cu_s[i] = p.cu[i];
-    cu = cu_s;
-  }
-  __syncthreads();
-  if (!err && p.mode != VA_MODE_CHAIN) {
-    for (int r = gtid; r < rows; r += NC * kPlanThreads) {
-      const int s = seq_of_row(cu, p.num_seqs, r);
-      const int j = r - cu[s], up = p.parent[r];
-      if (extend_is_tree(p, s) && (up < -1 || up >= j)) note_error(team, sh, VA_DEV_BAD_PARENT);
+    __syncthreads();
+    unsigned long long wa = sh.part[0][lane], wb = sh.part[1][lane];
+    const unsigned long long own_a = __shfl_sync(0xffffffffu, wa, tid / 32), own_b = __shfl_sync(0xffffffffu, wb, tid / 32);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long ua = __shfl_up_sync(0xffffffffu, wa, o), ub = __shfl_up_sync(0xffffffffu, wb, o);
+      if (lane >= o) {
+        wa += ua;
+        wb += ub;
+      }
     }
+    const unsigned long long pa = total_rows + __shfl_sync(0xffffffffu, wa, tid / 32) - own_a + ia - a;
+    const unsigned long long pb = total_need + __shfl_sync(0xffffffffu, wb, tid / 32) - own_b + ib - b;
+    total_rows += __shfl_sync(0xffffffffu, wa, 31);
+    total_need += __shfl_sync(0xffffffffu, wb, 31);
+    if (s < p.num_seqs) {
+      const int cu = (int)min(pa, 0x7fffffffull), first = (int)min(pb, 0x7fffffffull);
+      if (rank == 0) p.cu[s] = cu;
+      if (shared) {
+        sh.cu[s] = cu;
+        sh.first[s] = first;
+      }
+    }
+    __syncthreads();  // part
+    if (!shared && rank == 0 && s < p.num_seqs) p.row_first[s] = (int)min(pb, 0x7fffffffull);
   }
-  if (p.mode != VA_MODE_CHAIN) {
+  if (!err && total_rows > (unsigned long long)p.max_rows) err = VA_DEV_BAD_ROWS;
+  const int rows = err ? 0 : (int)total_rows;
+  if (!err) {
+    if (rank == 0 && tid == 0) p.cu[p.num_seqs] = rows;
+    if (shared && tid == 0) sh.cu[p.num_seqs] = rows;
+  }
+  if (!shared || p.mode != VA_MODE_CHAIN) {
+    if (!shared) team.sync();  // offsets in global memory
+    else __syncthreads();
+    const int* cu = shared ? sh.cu : p.cu;
+    unsigned bad = 0u;
+    if (!err && p.mode != VA_MODE_CHAIN) {
+      for (int r = gtid; r < rows; r += NC * kPlanThreads) {
+        const int s = seq_of_row(cu, p.num_seqs, r);
+        const int j = r - cu[s], up = p.parent[r];
+        if (extend_is_tree(p, s) && (up < -1 || up >= j)) bad = VA_DEV_BAD_PARENT;
+      }
+      if (bad)
+        for (int c = 0; c < NC; ++c) atomicOr(team.at(&sh.parents, c), bad);
+    }
     team.sync();
-    err = read_error(team, sh);
+    err |= sh.parents;
   }
-  if (!err && sum_before(sh, NC * kCtaWarps, lane) < wanted) err = VA_DEV_NO_PAGES;
+  if (!err && all_free < total_need) err = VA_DEV_NO_PAGES;
   if (err) {
-    team.sync();  // the first CTA's memory and the offsets are read until here
+    __syncthreads();  // the first CTA has written offsets
     if (gtid == 0) flag(p.status, err);
-    for (int i = gtid; i <= p.num_seqs; i += NC * kPlanThreads) p.cu[i] = 0;
+    if (rank == 0)
+      for (int i = tid; i <= p.num_seqs; i += kPlanThreads) p.cu[i] = 0;
     for (int r = gtid; r < p.max_rows; r += NC * kPlanThreads) {
       p.row_seq[r] = p.position[r] = -1;
       p.slot[r] = -1;
@@ -532,10 +581,11 @@ __global__ void __launch_bounds__(kPlanThreads) pages_extend_kernel(const PagePa
     return;
   }
   // The wanted free pages, ascending, and their first reference.
-  unsigned at = sum_before(sh, gwarp, lane);
-  for (int i0 = lo; i0 < hi && at < wanted; i0 += 32) {
+  const unsigned wanted = (unsigned)total_need;
+  unsigned at = before;
+  for (int i0 = lo, k = 0; i0 < hi && at < wanted; i0 += 32, ++k) {
     const int i = i0 + lane;
-    const bool is_free = i < hi && p.ref[i] == 0;
+    const bool is_free = kept ? ((bits >> k) & 1u) != 0u : i < hi && p.ref[i] == 0;
     const unsigned m = __ballot_sync(0xffffffffu, is_free);
     const unsigned r = at + __popc(m & ((1u << lane) - 1u));
     if (is_free && r < wanted) {
@@ -545,37 +595,39 @@ __global__ void __launch_bounds__(kPlanThreads) pages_extend_kernel(const PagePa
     at += __popc(m);
   }
   team.sync();
+  const int* cu = shared ? sh.cu : p.cu;
+  const int* first = shared ? sh.first : p.row_first;
   for (long long s0 = gtid / kSeqLanes; s0 < p.num_seqs; s0 += groups) {
     const int s = (int)s0;
-    const unsigned peers = 0xffu << (lane & ~(kSeqLanes - 1));
     const int held = p.a[s], n = p.b[s];
     if (n == 0) continue;  // the same in all lanes of a sequence
     const int end = (held + n + kPage - 1) / kPage;
     int* row = p.table + (long long)s * p.max_blocks;
-    int next = need[s];
+    int next = first[s];
     for (int c0 = (held + kPage - 1) / kPage; c0 < end; c0 += kSeqLanes) {
       const int c = c0 + sub;
-      const bool fresh = c < end && row[c] == -1;
+      const bool fresh = c < end && (!some_held || row[c] == -1);
       const unsigned m = __ballot_sync(peers, fresh) & peers;
       if (fresh) row[c] = found[next + __popc(m & ((1u << lane) - 1u))];
       next += __popc(m);
     }
   }
-  team.sync();
-  // Rows in launch order, each with its sequence by a search of the offsets.
+  if (some_held) team.sync();  // rows then have to see the tables
   for (int r = gtid; r < p.max_rows; r += NC * kPlanThreads) {
     int seq = -1, pos = -1;
     long long slot = -1;
     if (r < rows) {
       seq = seq_of_row(cu, p.num_seqs, r);
-      const int first = cu[seq], j = r - first, at_tok = p.a[seq] + j;
+      const int start = cu[seq], j = r - start, held = p.a[seq], tok = held + j;
       int depth = j;
       if (p.mode != VA_MODE_CHAIN && extend_is_tree(p, seq)) {
         depth = 0;
-        for (int u = p.parent[r]; u >= 0; u = p.parent[first + u]) ++depth;
+        for (int u = p.parent[r]; u >= 0; u = p.parent[start + u]) ++depth;
       }
-      pos = p.a[seq] + depth;
-      slot = (long long)p.table[(long long)seq * p.max_blocks + at_tok / kPage] * kPage + at_tok % kPage;
+      pos = held + depth;
+      const int c = tok / kPage, keep = (held + kPage - 1) / kPage;
+      const int page = c >= keep && !some_held ? found[first[seq] + c - keep] : p.table[(long long)seq * p.max_blocks + c];
+      slot = (long long)page * kPage + tok % kPage;
     }
     p.row_seq[r] = seq;
     p.position[r] = pos;
@@ -762,9 +814,15 @@ static cudaError_t launch_pages(void (*kernel)(const P), dim3 grid, int threads,
 
 // One CTA or a cluster of eight, by the integers a plan goes through.
 template <typename K>
-static cudaError_t launch_plan(K one, K wide, long long ints, cudaStream_t st, const PageParams& q) {
-  if (ints <= kOneCtaInts) return launch_pages(one, dim3(1), kPlanThreads, 1, st, q);
+static cudaError_t launch_plan(K one, K wide, long long ints, cudaStream_t st, const PageParams& q,
+                               long long most = kOneCtaInts) {
+  if (ints <= most) return launch_pages(one, dim3(1), kPlanThreads, 1, st, q);
   return launch_pages(wide, dim3(kWideCtas), kPlanThreads, kWideCtas, st, q);
+}
+
+// An extension's workspace: need and first page of each sequence, pages found.
+static size_t extend_ws_bytes(const va_page_pool* g) {
+  return (((size_t)g->num_seqs * 2 + (size_t)g->num_blocks) * 4 + 255) / 256 * 256;
 }
 
 static size_t pages_ws_bytes(const va_page_pool* g, int32_t num_forks) {
@@ -856,7 +914,7 @@ va_status verify_attn_pages_compact(const va_page_pool* pool, int32_t* copies, i
 
 size_t verify_attn_pages_extend_workspace_size(const va_page_pool* pool) {
   if (check_pool(pool) != VA_OK) return 0;
-  return pages_ws_bytes(pool, 0);
+  return extend_ws_bytes(pool);
 }
 
 va_status verify_attn_pages_extend(const va_page_pool* pool, const va_extend* x, int32_t mode, int32_t* cu_rows,
@@ -872,7 +930,7 @@ va_status verify_attn_pages_extend(const va_page_pool* pool, const va_extend* x,
   if (mode == VA_MODE_MIXED && !x->seq_kind) return VA_ERR_INVALID_ARG;
   if ((uintptr_t)slot % 8) return VA_ERR_ALIGNMENT;
   cudaStream_t cs = (cudaStream_t)stream;
-  st = check_plan(pages_ws_bytes(pool, 0), ws, ws_bytes, cs);
+  st = check_plan(extend_ws_bytes(pool), ws, ws_bytes, cs);
   if (st != VA_OK) return st;
   PageParams q = page_params(pool, status);
   q.a = x->ctx_len;
@@ -882,12 +940,13 @@ va_status verify_attn_pages_extend(const va_page_pool* pool, const va_extend* x,
   q.max_rows = x->max_rows;
   q.parent = x->parent;
   q.kind = x->seq_kind;
+  q.row_first = (int*)ws + pool->num_seqs + (size_t)pool->num_blocks;
   q.cu = cu_rows;
   q.row_seq = row_seq;
   q.position = position;
   q.slot = (long long*)slot;
   cudaError_t e = launch_plan(pages_extend_kernel<1>, pages_extend_kernel<kWideCtas>,
-                              pool->num_blocks + 8LL * pool->num_seqs + 4LL * x->max_rows, cs, q);
+                              pool->num_blocks + 8LL * pool->num_seqs + 4LL * x->max_rows, cs, q, kOneCtaExtend);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }
 
