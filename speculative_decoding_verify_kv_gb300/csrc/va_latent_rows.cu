@@ -84,6 +84,29 @@ __device__ __forceinline__ void tmem_st_n(uint32_t at, const uint32_t (&r)[N]) {
   else tmem_st32(at, r);
 }
 
+// The lanes' N values v[n] combined over the warp (op: sum or maximum), by halves:
+// each step keeps half of the values, so N shuffles at most instead of 5 N (code
+// that runs once is paid for by its size).  Lane l returns value l (N = 32) or
+// l / 2 (N = 16).
+template <int N, int BIT, class Op>
+__device__ __forceinline__ float combine_lanes(const float (&v)[N], int lane, Op op) {
+  if constexpr (N == 1) {
+    float x = v[0];
+#pragma unroll
+    for (int o = BIT; o > 0; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  } else {
+    float half[N / 2];
+    const bool up = (lane & BIT) != 0;
+#pragma unroll
+    for (int n = 0; n < N / 2; ++n) {
+      const float other = __shfl_xor_sync(0xffffffffu, up ? v[n] : v[n + N / 2], BIT);
+      half[n] = op(up ? v[n + N / 2] : v[n], other);
+    }
+    return combine_lanes<N / 2, BIT / 2>(half, lane, op);
+  }
+}
+
 template <class C>
 __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const LatentParams p, const __grid_constant__ LrMaps maps) {
   constexpr int N = C::N, MB = C::MB;
@@ -132,6 +155,23 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
   auto kfree = [&](int i) { return bar(RB_RING + 2 * C::NV + C::NK + i); };
   const uint32_t base = smem_u32(sm);
 
+  // A producer's lane l: (row, plane) of page l of the tile at t0, in the cache's map.
+  unsigned late = 0u;
+  auto look_up = [&](int t0) {
+    const int pg = t0 / kPage + lane;
+    return lane < 4 && pg * kPage < hi && p.page_size ? p.block_table[(long long)s * p.max_blocks + pg] : 0;
+  };
+  auto page_at = [&](int t0, int blk) {
+    if (p.page_size == 0) return make_int2(t0 + lane * kPage, s);
+    if (blk < 0 || blk >= p.num_blocks) {
+      late = VA_DEV_BAD_BLOCK;
+      blk = 0;
+    }
+    return make_int2(0, blk);
+  };
+  // The first tile's are looked up beside the rest of the prologue.
+  int blk0 = 0;
+  if ((warp == 0 || warp == 7) && ntiles > 0) blk0 = look_up(lo);
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_at), C::COLS);
     tmem_relinquish();
@@ -180,19 +220,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
     for (int i = 0; i < work && ok; ++i) {
       const int t0 = lo_u + i * kLrTile;
       const int pages = (min(kLrTile, hi_u - t0) + kPage - 1) / kPage;
-      int2 mine = make_int2(0, 0);  // lane l: (row, plane) of the tile's page l in the cache's map
-      if (lane < pages) {
-        const int pg = t0 / kPage + lane;
-        mine = make_int2(pg * kPage, s);
-        if (p.page_size) {
-          int blk = p.block_table[(long long)s * p.max_blocks + pg];
-          if (blk < 0 || blk >= p.num_blocks) {
-            found(VA_DEV_BAD_BLOCK);
-            blk = 0;
-          }
-          mine = make_int2(0, blk);
-        }
-      }
+      const int2 mine = page_at(t0, i == 0 ? blk0 : look_up(t0));
       int2 at[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, mine.x, g), __shfl_sync(0xffffffffu, mine.y, g));
@@ -226,6 +254,8 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
         if (sv >= C::NV) sv -= C::NV, pv ^= 1;
       }
     }
+    if (late) found(late);
+    __syncwarp();
     if (!ok && lane == 0) fail();
     // No copy may still be landing when the CTA goes away.
     if (*abort_p && lane == 0) {
@@ -377,13 +407,9 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       if (any_of_four_warps(2, over)) {
         // New references: the rows' largest scores of this tile.
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          z[n] = z[n] > -INFINITY ? __uint_as_float(sr[n]) * c_r : -INFINITY;
-          float mx = z[n];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          if (lane == 0) w_s[quad * N + n] = mx;
-        }
+        for (int n = 0; n < N; ++n) z[n] = z[n] > -INFINITY ? __uint_as_float(sr[n]) * c_r : -INFINITY;
+        const float top = combine_lanes<N, 16>(z, lane, [](float x, float y) { return fmaxf(x, y); });
+        w_s[quad * N + lane / (32 / N)] = top;
         bar_sync(3, 128);
         if (th < N) {
           const float mx = fmaxf(fmaxf(w_s[th], w_s[N + th]), fmaxf(w_s[2 * N + th], w_s[3 * N + th]));
@@ -443,12 +469,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
     if (!ok && lane == 0) fail();
     tc_fence_after();
     // Row sums over the threads.
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], o);
-      if (lane == 0) w_s[quad * N + n] = l[n];
-    }
+    w_s[quad * N + lane / (32 / N)] = combine_lanes<N, 16>(l, lane, [](float x, float y) { return x + y; });
     bar_sync(3, 128);
     const bool bad = *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0;
     auto sum_of = [&](int n) { return (w_s[n] + w_s[N + n]) + (w_s[2 * N + n] + w_s[3 * N + n]); };
@@ -464,22 +485,24 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       }
     }
     // O^T: a lane per value column, so a warp stores 32 of a row's at once.
+    if (th < R) f_s[th] = bad ? NAN : live > 1 ? 1.f : sum_of(th) > 0.f ? 1.f / sum_of(th) : 0.f;
+    bar_sync(3, 128);
+    const long long first = (live > 1 ? latent_slot(p, chunk, item0) : item0) * C::DV + th;
 #pragma unroll 1
     for (int c = 0; c < MB; ++c) {
       uint32_t o[N];
       tmem_ld_n<N>(tm + lanes + c * N, o);
       tmem_wait_ld();
-      const int d = c * 128 + th;
+      if (live > 1) {
+        float* to = p.ws_acc + first + c * 128;
 #pragma unroll
-      for (int n = 0; n < N; ++n) {
-        if (n >= R) break;
-        if (live > 1) {
-          p.ws_acc[latent_slot(p, chunk, item0 + n) * C::DV + d] = bad ? NAN : __uint_as_float(o[n]);
-        } else {
-          const float sum = sum_of(n);
-          const float v = bad ? NAN : sum > 0.f ? __uint_as_float(o[n]) / sum : 0.f;
-          reinterpret_cast<__nv_bfloat16*>(p.o)[(item0 + n) * C::DV + d] = __float2bfloat16_rn(v);
-        }
+        for (int n = 0; n < N; ++n)
+          if (n < R) to[n * C::DV] = __uint_as_float(o[n]) * f_s[n];
+      } else {
+        __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.o) + first + c * 128;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+          if (n < R) to[n * C::DV] = __float2bfloat16_rn(__uint_as_float(o[n]) * f_s[n]);
       }
     }
   }

@@ -135,6 +135,24 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   auto kfree = [&](int i) { return bar(LB_RING + 2 * C::NV + C::NK + i); };
   const uint32_t base = smem_u32(sm);
 
+  // Absorbed form, a producer's lane l < 4: (row, plane) of page l of the tile at
+  // t0, in the cache's map.
+  unsigned late = 0u;
+  auto look_up = [&](int t0) {
+    const int pg = t0 / kPage + lane;
+    return lane < 4 && pg * kPage < hi && p.page_size ? p.block_table[(long long)s * p.max_blocks + pg] : 0;
+  };
+  auto page_at = [&](int t0, int blk) {
+    if (p.page_size == 0) return make_int2(t0 + lane * kPage, s);
+    if (blk < 0 || blk >= p.num_blocks) {
+      late = VA_DEV_BAD_BLOCK;
+      blk = 0;
+    }
+    return make_int2(0, blk);
+  };
+  // The first tile's are looked up beside the rest of the prologue.
+  int blk0 = 0;
+  if (!PROMPT && (warp == 0 || warp == 10) && ntiles > 0) blk0 = look_up(lo);
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_at), 512);
     tmem_relinquish();
@@ -174,16 +192,6 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     // Absorbed form: lane l < 4 looks the tile's page l up.
     const bool keys = warp == 0;
     const uint32_t one = elected();
-    auto page_of = [&](int t) {  // (row, plane) of a page's tokens in the cache's map
-      const int pg = t / kPage;
-      if (p.page_size == 0) return make_int2(pg * kPage, s);
-      int blk = p.block_table[(long long)s * p.max_blocks + pg];
-      if (blk < 0 || blk >= p.num_blocks) {
-        found(VA_DEV_BAD_BLOCK);
-        blk = 0;
-      }
-      return make_int2(0, blk);
-    };
     const int lo_u = __shfl_sync(0xffffffffu, lo, 0), hi_u = __shfl_sync(0xffffffffu, hi, 0);
     const int key0 = __shfl_sync(0xffffffffu, (int)q.key0, 0);
     bool ok = true;
@@ -208,8 +216,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       const int pages = PROMPT ? 0 : (min(NT, hi_u - t0) + kPage - 1) / kPage;
       int2 at[4];
       if (!PROMPT) {
-        int2 a = make_int2(0, 0);
-        if (lane < pages) a = page_of(t0 + lane * kPage);
+        const int2 a = page_at(t0, i == 0 ? blk0 : look_up(t0));
 #pragma unroll
         for (int g = 0; g < 4; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, g), __shfl_sync(0xffffffffu, a.y, g));
       }
@@ -261,6 +268,8 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
         }
       }
     }
+    if (late) found(late);
+    __syncwarp();
     if (!ok && lane == 0) fail();
     if (!keys && ok && ragged) {
       // Tokens behind the range may hold anything: their V is cleared (their
