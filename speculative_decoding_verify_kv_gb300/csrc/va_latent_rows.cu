@@ -221,6 +221,8 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       const int t0 = lo_u + i * kLrTile;
       const int pages = (min(kLrTile, hi_u - t0) + kPage - 1) / kPage;
       const int2 mine = page_at(t0, i == 0 ? blk0 : look_up(t0));
+      if (late) found(late);  // before anything of the tile is loaded
+      __syncwarp();
       int2 at[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, mine.x, g), __shfl_sync(0xffffffffu, mine.y, g));
@@ -254,8 +256,6 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
         if (sv >= C::NV) sv -= C::NV, pv ^= 1;
       }
     }
-    if (late) found(late);
-    __syncwarp();
     if (!ok && lane == 0) fail();
     // No copy may still be landing when the CTA goes away.
     if (*abort_p && lane == 0) {

@@ -217,6 +217,8 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       int2 at[4];
       if (!PROMPT) {
         const int2 a = page_at(t0, i == 0 ? blk0 : look_up(t0));
+        if (late) found(late);  // before anything of the tile is loaded
+        __syncwarp();
 #pragma unroll
         for (int g = 0; g < 4; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, g), __shfl_sync(0xffffffffu, a.y, g));
       }
@@ -268,8 +270,6 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
         }
       }
     }
-    if (late) found(late);
-    __syncwarp();
     if (!ok && lane == 0) fail();
     if (!keys && ok && ragged) {
       // Tokens behind the range may hold anything: their V is cleared (their
