@@ -123,12 +123,16 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
   asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
-  if (tid == 0) {
-    *err_s = 0;
-    *abort_p = 0;
-    for (int i = 0; i < C::NB; ++i)
-      mbar_init(bar(i), i >= RB_SREAD && i < RB_PFREE ? 4 : 1);
+  if (warp == 0) {
+    if (lane == 0) {
+      *err_s = 0;
+      *abort_p = 0;
+      prefetch_map(&maps.q);
+      prefetch_map(&maps.k);
+    }
+    for (int i = lane; i < C::NB; i += 32) mbar_init(bar(i), i >= RB_SREAD && i < RB_PFREE ? 4 : 1);
     fence_barrier_init();
+    __syncwarp();
   }
   if (tid < N) m_s[tid] = -INFINITY;
   // Nothing but this CTA's own shared memory is touched before the work ahead
@@ -172,6 +176,14 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
   // The first tile's are looked up beside the rest of the prologue.
   int blk0 = 0;
   if ((warp == 0 || warp == 7) && ntiles > 0) blk0 = look_up(lo);
+  if (warp == 0 && ntiles > 0) {
+    // The queries, at once: their barrier was set up by this warp.
+    const uint32_t one = elected();
+    const int qrow = __shfl_sync(0xffffffffu, q.row0 * p.H, 0);
+    expect_by(one, bar(RB_QLAND), C::DK / 64 * C::QBLK);
+#pragma unroll
+    for (int c = 0; c < C::DK / 64; ++c) tma_2d_by(one, base + C::OFF_Q + c * C::QBLK, &maps.q, c * 64, qrow, bar(RB_QLAND));
+  }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_at), C::COLS);
     tmem_relinquish();
@@ -201,18 +213,12 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
     // nothing to read
   } else if (warp == 0 || warp == 7) {
     // ---------------------------------------------------------------- producers
-    // Warp 0: the queries, the rope blocks and even pairs.  Warp 7: odd pairs.
+    // Warp 0: the rope blocks and even pairs.  Warp 7: odd pairs.
     // (A copy is one block of one page, 36 to a tile: issued by one warp, they
     // were what the call waited for.)
     const int who = warp == 0 ? 0 : 1;
     const uint32_t one = elected();
     const int lo_u = __shfl_sync(0xffffffffu, lo, 0), hi_u = __shfl_sync(0xffffffffu, hi, 0);
-    if (who == 0) {
-      const int qrow = __shfl_sync(0xffffffffu, q.row0 * p.H, 0);
-      expect_by(one, bar(RB_QLAND), C::DK / 64 * C::QBLK);
-#pragma unroll
-      for (int c = 0; c < C::DK / 64; ++c) tma_2d_by(one, base + C::OFF_Q + c * C::QBLK, &maps.q, c * 64, qrow, bar(RB_QLAND));
-    }
     bool ok = true;
     int nk = 0, nv = who;  // rope blocks issued; the next pair
     int sk = 0, sv = who;

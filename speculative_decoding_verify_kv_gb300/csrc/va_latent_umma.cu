@@ -94,12 +94,18 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   // Broadcasts: what a warp has in common is known to be so.
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
-  if (tid == 0) {
-    *err_s = 0;
-    *abort_p = 0;
-    for (int i = 0; i < C::NB; ++i)
+  if (warp == 0) {
+    if (lane == 0) {
+      *err_s = 0;
+      *abort_p = 0;
+      prefetch_map(&maps.q);
+      prefetch_map(&maps.k);
+      if (PROMPT) prefetch_map(&maps.r);
+    }
+    for (int i = lane; i < C::NB; i += 32)
       mbar_init(bar(i), i == LB_PFULL || i == LB_PFULL + 1 || i == LB_QREADY ? 8 : 1);
     fence_barrier_init();
+    __syncwarp();
   }
   // Nothing but this CTA's own shared memory is touched before the work ahead
   // on the stream has completed.
@@ -153,6 +159,21 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   // The first tile's are looked up beside the rest of the prologue.
   int blk0 = 0;
   if (!PROMPT && (warp == 0 || warp == 10) && ntiles > 0) blk0 = look_up(lo);
+  if (warp == 0 && ntiles > 0) {
+    // The queries, at once: their barrier was set up by this warp.
+    const uint32_t one = elected();
+    const int qrow = __shfl_sync(0xffffffffu, PROMPT ? q.row0 + rbase : q.row0 * p.H + rbase, 0);
+    expect_by(one, bar(LB_QLAND), C::DK / 64 * kLuM * 128);
+#pragma unroll
+    for (int c = 0; c < C::DK / 64; ++c) {
+      // Absorbed form: the columns of this part's V come first, in TMEM.
+      const int col = PROMPT ? c * 64 : c < C::VBLK ? (part * C::VBLK + c) * 64
+                                      : (c - C::VBLK < part * C::VBLK ? c - C::VBLK : c) * 64;
+      const uint32_t dst = base + (c < C::QT / 64 ? C::QSTAGE + c * kLuM * 128 : C::OFF_Q + (c - C::QT / 64) * kLuM * 128);
+      if (PROMPT) tma_3d_by(one, dst, &maps.q, col, head, qrow, bar(LB_QLAND));
+      else tma_2d_by(one, dst, &maps.q, col, qrow, bar(LB_QLAND));
+    }
+  }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_at), 512);
     tmem_relinquish();
@@ -188,7 +209,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     // nothing to read: straight to the outputs
   } else if (warp == 0 || warp == 10) {
     // ---------------------------------------------------------------- producers
-    // Warp 10: the V stages.  Warp 0: the queries and the key's other blocks.
+    // Warp 10: the V stages.  Warp 0: the key's other blocks.
     // Absorbed form: lane l < 4 looks the tile's page l up.
     const bool keys = warp == 0;
     const uint32_t one = elected();
@@ -196,19 +217,6 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     const int key0 = __shfl_sync(0xffffffffu, (int)q.key0, 0);
     bool ok = true;
     int issued = 0;  // tiles (V) or blocks (keys)
-    if (keys) {
-      const int qrow = __shfl_sync(0xffffffffu, PROMPT ? q.row0 + rbase : q.row0 * p.H + rbase, 0);
-      expect_by(one, bar(LB_QLAND), C::DK / 64 * kLuM * 128);
-#pragma unroll
-      for (int c = 0; c < C::DK / 64; ++c) {
-        // Absorbed form: the columns of this part's V come first, in TMEM.
-        const int col = PROMPT ? c * 64 : c < C::VBLK ? (part * C::VBLK + c) * 64
-                                        : (c - C::VBLK < part * C::VBLK ? c - C::VBLK : c) * 64;
-        const uint32_t dst = base + (c < C::QT / 64 ? C::QSTAGE + c * kLuM * 128 : C::OFF_Q + (c - C::QT / 64) * kLuM * 128);
-        if (PROMPT) tma_3d_by(one, dst, &maps.q, col, head, qrow, bar(LB_QLAND));
-        else tma_2d_by(one, dst, &maps.q, col, qrow, bar(LB_QLAND));
-      }
-    }
     int st = 0;
     uint32_t par = 1;
     for (int i = 0; i < work && ok; ++i) {
@@ -572,13 +580,22 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       }
     }
     bar_sync(1, 256);
-    const int pieces = live > 1 ? DO / 4 : DO / 8;  // of 16 bytes
-    for (int u = tid - 64; u < nrows * pieces; u += 256) {
-      const int row = u / pieces, c = u % pieces;
-      const long long item = latent_item(p, q.row0, rbase + row, head);
-      const uint4 v = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
-      if (live > 1) *reinterpret_cast<uint4*>(p.ws_acc + latent_slot(p, chunk, item) * C::DV + part * DO + c * 4) = v;
-      else *reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.o) + item * C::DV + part * DO + c * 8) = v;
+    // Row r of the block is row first + r step of [total_rows][H].
+    const long long first = latent_item(p, q.row0, rbase, head), step = PROMPT ? p.H : 1;
+    if (live > 1) {
+      constexpr int PIECES = DO / 4;  // of 16 bytes
+      float* to = p.ws_acc + latent_slot(p, chunk, first) * C::DV + part * DO;
+      for (int u = tid - 64; u < nrows * PIECES; u += 256) {
+        const int row = u / PIECES, c = u % PIECES;
+        *reinterpret_cast<uint4*>(to + row * step * C::DV + c * 4) = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
+      }
+    } else {
+      constexpr int PIECES = DO / 8;
+      unsigned short* to = reinterpret_cast<unsigned short*>(p.o) + first * C::DV + part * DO;
+      for (int u = tid - 64; u < nrows * PIECES; u += 256) {
+        const int row = u / PIECES, c = u % PIECES;
+        *reinterpret_cast<uint4*>(to + row * step * C::DV + c * 8) = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
+      }
     }
   }
 
