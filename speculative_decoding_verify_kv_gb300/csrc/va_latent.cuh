@@ -19,6 +19,7 @@ struct LatentParams {
   int num_seqs, H, total_rows, max_rows, mode;
   int DK, DV;             // width of a key (rope part among it) and of a value
   float scale_log2;       // softmax scale * log2(e)
+  float scale_lo;         // what its rounding left
   const void* q;          // [total_rows][H][DK]
   const int* cu_rows;
   const int* ctx_len;

@@ -141,6 +141,7 @@ static LatentParams base_params(const va_problem* p, int mode, const LatentPlan&
   q.DV = value_dim;
   const double scale = p->scale > 0.f ? (double)p->scale : 1.0 / sqrt((double)key_dim);
   q.scale_log2 = (float)(scale * 1.4426950408889634);
+  q.scale_lo = (float)(scale * 1.4426950408889634 - (double)q.scale_log2);
   q.q = p->q;
   q.cu_rows = p->cu_rows;
   q.ctx_len = p->ctx_len;

@@ -179,12 +179,14 @@ __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentPar
       const int rl = rg * RW + 2 * half + i;
       const int j = PROMPT ? rbase + rl : (rbase + rl) / p.H;
       const unsigned vis = rl < nrows ? latent_bits(p, q, q.kind == 1 ? anc_s[rl] : 0u, j, hi, t0) : 0u;
-      const float z = (vis >> lane) & 1u ? Ss[rl * C::LDS + lane] * p.scale_log2 : -INFINITY;
-      float mx = z;
+      const float sc = Ss[rl * C::LDS + lane];
+      float mx = (vis >> lane) & 1u ? sc * p.scale_log2 : -INFINITY;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       const float m_new = fmaxf(m_run[i], mx);
-      const float w = m_new == -INFINITY ? 0.f : exp2f(z - m_new);
+      // The scale in two parts: rounded to one, it would move every score alike, by
+      // 2^-25 of it, and a weight by some 10 times that.
+      const float w = (vis >> lane) & 1u ? exp2f(fmaf(sc, p.scale_lo, fmaf(sc, p.scale_log2, -m_new))) : 0.f;
       const float f = m_run[i] == -INFINITY ? 0.f : exp2f(m_run[i] - m_new);
       float sum = w;
 #pragma unroll
