@@ -6,7 +6,7 @@
 //   softmax       eight warps, one TMEM lane (query row) per thread and half
 //                 of the tile's columns per warp; online (m, l) in log2 units,
 //                 O rescaled only when the maximum grows by more than 2^8; P
-//                 in bf16 over S's place
+//                 in bf16 (absorbed form: over S's place)
 //   O += P V      tcgen05.mma, A = P (TMEM), B = V tile (MN-major)
 // so that S of the next tile runs under this tile's softmax.
 //
@@ -47,13 +47,18 @@ struct LuCfg {
   static constexpr int BLK = NT * 128;               // bytes of a 64-column block
   static constexpr int VBLK = DO / 64;               // blocks of a V stage
   static constexpr int KBLK = PROMPT ? DK / 64 : DK / 64 - VBLK;  // other blocks of the key
-  static constexpr int QT = PROMPT ? DK : DO;        // query columns in TMEM
+  static constexpr int QT = PROMPT ? 128 : DO;       // query columns in TMEM
   static constexpr int QS = DK - QT;                 // query columns in shared memory
   static constexpr int NV = PROMPT ? (DV == 128 ? 2 : 4) : (DV == 512 ? 3 : 5);  // V stages
   static constexpr int NK = PROMPT ? (DV == 128 ? 9 : 6) : (DV == 512 ? 6 : 5);  // key blocks
   static constexpr int COL_O = 0;
   static constexpr int COL_S = DO;
-  static constexpr int COL_Q = DO + 2 * NT;
+  // Prompts: P has columns of its own, so that S(i + 2) waits for S(i) to be read
+  // only, not for P(i) V (in S's place: 755 us against 640 for 2 x 2,048 rows of
+  // 128 heads over 4,096 keys).  The absorbed form has no columns left for it.
+  static constexpr bool SEP = PROMPT;
+  static constexpr int COL_P = DO + 2 * NT;
+  static constexpr int COL_Q = COL_P + (SEP ? NT / 2 : 0);
   static constexpr int OFF_V = 0;
   static constexpr int OFF_K = NV * VBLK * BLK;
   static constexpr int OFF_Q = OFF_K + NK * BLK;
@@ -64,7 +69,7 @@ struct LuCfg {
   static constexpr int QV_FIRST = PROMPT ? 1 << 30 : QSTAGE / (VBLK * BLK);
   static constexpr int QK_FIRST = PROMPT ? (QSTAGE - OFF_K) / BLK : 1 << 30;
   static constexpr int OROW = DO * 4 + 16;           // O staging at the end, padded rows
-  static constexpr int NB = 11 + 2 * NV + 2 * NK;    // barriers
+  static constexpr int NB = 12 + 2 * NV + 2 * NK;    // barriers
   static constexpr int OFF_RED = OFF_END > kLuM * OROW ? OFF_END : kLuM * OROW;
   static constexpr int OFF_BAR = OFF_RED + 2 * 2 * kLuM * 4;
   static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
@@ -73,7 +78,7 @@ struct LuCfg {
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-enum { LB_SFULL = 0, LB_PFULL = 2, LB_SFREE = 4, LB_QLAND = 6, LB_QREADY = 7, LB_OFINAL = 8, LB_FIX = 9, LB_SDRAIN = 10, LB_RING = 11 };
+enum { LB_SFULL = 0, LB_PFULL = 2, LB_SFREE = 4, LB_QLAND = 6, LB_QREADY = 7, LB_OFINAL = 8, LB_FIX = 9, LB_SDRAIN = 10, LB_PFREE = 11, LB_RING = 12 };
 
 struct LuMaps {
   CUtensorMap q, k, r;  // queries; cache or expanded keys and values; rope part of prompt keys
@@ -103,7 +108,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       if (PROMPT) prefetch_map(&maps.r);
     }
     for (int i = lane; i < C::NB; i += 32)
-      mbar_init(bar(i), i == LB_PFULL || i == LB_PFULL + 1 || i == LB_QREADY ? 8 : 1);
+      mbar_init(bar(i), (i >= LB_PFULL && i < LB_SFREE) || (C::SEP && i >= LB_SFREE && i < LB_QLAND) || i == LB_QREADY ? 8 : 1);
     fence_barrier_init();
     __syncwarp();
   }
@@ -352,8 +357,9 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
         there = c + 1 < C::KBLK ? mbar_peek(kfull(sk), pk) : i + 1 < work && peek_tile(i + 1);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          if (PROMPT) mma_ts_by(one, scol, tm + C::COL_Q + (c * 4 + kk) * 8, kd + kk * 2, ID, c > 0 || kk > 0 ? 1u : 0u);
-          else mma_ss_by(one, scol, qd0 + (uint64_t)((c * kLuM * 128) >> 4) + kk * 2, kd + kk * 2, ID, 1u);
+          constexpr int IN_TMEM = PROMPT ? C::QT / 64 : 0;  // of the key blocks' query columns
+          if (c < IN_TMEM) mma_ts_by(one, scol, tm + C::COL_Q + (c * 4 + kk) * 8, kd + kk * 2, ID, c > 0 || kk > 0 ? 1u : 0u);
+          else mma_ss_by(one, scol, qd0 + (uint64_t)(((c - IN_TMEM) * kLuM * 128) >> 4) + kk * 2, kd + kk * 2, ID, 1u);
         }
         any = true;
         commit_by(one, free);
@@ -388,10 +394,10 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       const uint64_t vd = vd0 + (uint64_t)((st * C::VBLK * C::BLK) >> 4);
 #pragma unroll
       for (int kk = 0; kk < NT / 16; ++kk)
-        mma_ts_by(one, tm + C::COL_O, tm + C::COL_S + b * NT + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), ID,
+        mma_ts_by(one, tm + C::COL_O, tm + (C::SEP ? C::COL_P : C::COL_S + b * NT) + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), ID,
                   i > 0 || kk > 0 ? 1u : 0u);
       any = true;
-      commit_by(one, bar(LB_SFREE + b));
+      commit_by(one, bar(C::SEP ? LB_PFREE : LB_SFREE + b));
       commit_by(one, vfree(st));
       if (++st == C::NV) st = 0, pv ^= 1;
     }
@@ -474,6 +480,18 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
           }
         }
       }
+      if (C::SEP) {
+        // S(i) is in registers: its buffer may be written again.
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(LB_SFREE + b));
+      }
+      // The previous P.V: it has to be done before O is rescaled, or (prompts) P
+      // written.
+      auto pv_done = [&]() {
+        return i < 1 || (C::SEP ? mbar_wait(bar(LB_PFREE), (i - 1) & 1, abort_p, kLatentWaitNs)
+                                : mbar_wait(bar(LB_SFREE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_p, kLatentWaitNs));
+      };
       // The row's maximum over both halves (raw scores; c_r > 0).
       red[(b * 2 + half) * kLuM + r] = mx;
       bar_sync(5 + quad, 64);
@@ -483,8 +501,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       const float m_new = m_use == -INFINITY || need ? mt : m_use;
       if (ok && __any_sync(0xffffffffu, need)) {
         // Rescale this half of the warp's O rows once the previous P.V landed.
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(LB_SFREE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_p, kLatentWaitNs)))
-          ok = false;
+        if (!__all_sync(0xffffffffu, pv_done())) ok = false;
         if (ok) {
           tc_fence_after();
           const float f = need ? exp2f(m_use - m_new) : 1.f;
@@ -521,8 +538,11 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
           ph[c] = *reinterpret_cast<const uint32_t*>(&h);
         }
         l_run += l0 + l1;
-        if constexpr (NC == 32) tmem_st16(scol + 16 * half, ph);
-        else tmem_st32_from<0>(scol + 32 * half, ph);
+        const uint32_t pcol = C::SEP ? tm + lanes + C::COL_P : scol;
+        if (C::SEP && !__all_sync(0xffffffffu, pv_done())) ok = false;
+        if (C::SEP) tc_fence_after();
+        if constexpr (NC == 32) tmem_st16(pcol + 16 * half, ph);
+        else tmem_st32_from<0>(pcol + 32 * half, ph);
         tmem_wait_st();
       }
       tc_fence_before();
