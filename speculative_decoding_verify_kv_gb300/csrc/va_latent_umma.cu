@@ -446,12 +446,13 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       if (bad_parent) found(VA_DEV_BAD_PARENT);
     }
     float m_use = -INFINITY, l_run = 0.f;
+    bool there = false;  // S of the tile, seen ahead
     const float c_r = p.scale_log2;
     // A failed wait does not leave the loop: every iteration has one named
     // barrier shared with the partner warp.
     for (int i = 0; i < work; ++i) {
       const int b = i & 1;
-      if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(LB_SFULL + b), (i >> 1) & 1, abort_p, kLatentWaitNs))) ok = false;
+      if (ok && !__all_sync(0xffffffffu, there || mbar_wait(bar(LB_SFULL + b), (i >> 1) & 1, abort_p, kLatentWaitNs))) ok = false;
       tc_fence_after();
       const uint32_t scol = tm + lanes + C::COL_S + b * NT;
       const int t0 = lo + i * NT + NC * half;
@@ -463,11 +464,15 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
         if constexpr (NC > 32) tmem_ld32_into<NC - 32>(scol + NC * half + 32, sr);
         tmem_wait_ld();
         if (lo + (i + 1) * NT <= all_see) {
+          float m2 = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < NC; ++c) {
-            sv[c] = __uint_as_float(sr[c]);
-            mx = fmaxf(mx, sv[c]);
+          for (int c = 0; c < NC; c += 4) {
+            mx = max3(mx, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+            m2 = max3(m2, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
           }
+          mx = fmaxf(mx, m2);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) sv[c] = __uint_as_float(sr[c]);
         } else {
 #pragma unroll
           for (int w = 0; w < NC / 32; ++w) {
@@ -519,24 +524,29 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
         }
       }
       m_use = m_new;
+      there = i + 1 < work && mbar_peek(bar(LB_SFULL + (b ^ 1)), ((i + 1) >> 1) & 1);
       if (ok && warp_live) {
         uint32_t ph[NC / 2];
-        float l0 = 0.f, l1 = 0.f;
+        uint64_t l2 = pack2(0.f, 0.f);
         // A masked score (-inf) gives 0; while nothing of the row was visible
         // every score is masked, and the 0 offset keeps them at -inf.
         const float mneg = m_use == -INFINITY ? 0.f : -m_use;
+        const uint64_t c2 = pack2(c_r, c_r), m2 = pack2(mneg, mneg);
 #pragma unroll
         for (int c = 0; c < NC / 2; ++c) {
-          const float a = lu_ex2(fmaf(sv[2 * c], c_r, mneg));
-          const float d = lu_ex2(fmaf(sv[2 * c + 1], c_r, mneg));
-          l0 += a;
-          l1 += d;
+          float a, d;
+          unpack2(fma2(pack2(sv[2 * c], sv[2 * c + 1]), c2, m2), a, d);
+          a = lu_ex2(a);
+          d = lu_ex2(d);
+          l2 = add2(l2, pack2(a, d));
           // Rounded to bf16 (2^-8 at most): the matrix unit takes 16 bits, and
           // a second part for the rest would cost P.V again, for an o that is
           // rounded alike.
           const __nv_bfloat162 h = __floats2bfloat162_rn(a, d);
           ph[c] = *reinterpret_cast<const uint32_t*>(&h);
         }
+        float l0, l1;
+        unpack2(l2, l0, l1);
         l_run += l0 + l1;
         const uint32_t pcol = C::SEP ? tm + lanes + C::COL_P : scol;
         if (C::SEP && !__all_sync(0xffffffffu, pv_done())) ok = false;
