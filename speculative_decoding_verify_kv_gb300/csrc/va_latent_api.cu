@@ -10,6 +10,7 @@ namespace va {
 struct LatentPlan {
   int kernel;          // VA_KERNEL_*
   bool few;            // the tensor-core kernel for few query rows
+  bool pair;           // that of CTA pairs
   int rows_per_block;  // query rows of a CTA
   int parts;           // CTAs that share a row block's chunk
   int per_sm;          // CTAs of an SM
@@ -86,6 +87,9 @@ static LatentPlan plan_rows(const va_problem* p, int dtype, int value_dim, bool 
     const int few = prompt ? 0 : latent_rows_rows((long long)p->max_rows_per_seq * p->num_heads);
     pl.few = few > 0;
     pl.rows_per_block = few ? few : latent_umma_rows();
+    // 512 latent columns: pairs of CTAs, which share a row block like `parts`.
+    pl.pair = !few && !prompt && value_dim == 512;
+    if (pl.pair) pl.rows_per_block = latent_pair_rows();
     pl.parts = few ? 1 : latent_umma_parts(value_dim, prompt);
     pl.per_sm = 1;
   } else {
@@ -99,7 +103,7 @@ static LatentPlan plan_rows(const va_problem* p, int dtype, int value_dim, bool 
   const long long blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
   pl.many = pl.slots / (blocks > 0 ? blocks : 1) > 8;
   // A sequence of b row blocks has b max(1, slots / b) CTAs per key head.
-  pl.grid = dim3((unsigned)(blocks > pl.slots ? blocks : pl.slots), (unsigned)(prompt ? p->num_heads : pl.parts),
+  pl.grid = dim3((unsigned)(blocks > pl.slots ? blocks : pl.slots), (unsigned)(prompt ? p->num_heads : pl.pair ? 1 : pl.parts),
                  (unsigned)p->num_seqs);
   if (pl.slots > 1) {
     const size_t items = (size_t)pl.slots * (size_t)p->total_rows * (size_t)p->num_heads;
@@ -173,6 +177,7 @@ static va_status check_outputs(const LatentPlan& pl, const void* ws, size_t ws_b
 
 static va_status launch(const LatentParams& q, const LatentPlan& pl, cudaStream_t cs) {
   cudaError_t e = pl.few                           ? launch_latent_rows(q, pl.grid, cs)
+                  : pl.pair                       ? launch_latent_pair(q, pl.grid, cs)
                   : pl.kernel == VA_KERNEL_TENSOR ? launch_latent_umma(q, pl.grid, cs)
                                                   : launch_latent_simt(q, pl.grid, cs);
   if (e == cudaSuccess && pl.slots > 1) e = launch_latent_merge(q, cs);
