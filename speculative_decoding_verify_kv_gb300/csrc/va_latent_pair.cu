@@ -18,9 +18,9 @@
 //   O += P V     A = P, B = the value columns, each CTA holding half of them for
 //                all 128 tokens: two products of 256 columns
 //
-// Shared memory: queries, P, a ring of three groups of key blocks and one of two
-// halves of V: a tile in all.  Its key groups are loaded again while the softmax
-// and P.V of the tile before are at work, and V during S.
+// Shared memory: queries, P, and a tile: three groups of key blocks and four units
+// of V, each loaded again as soon as it has been read, key groups while the
+// softmax and P.V are at work, V during S.
 //
 // Waits are bounded (VA_DEV_TIMEOUT); on a timeout the pair ends and writes NaN.
 #include <string.h>
@@ -29,7 +29,7 @@
 
 namespace va {
 
-constexpr int kLpThreads = 384;
+constexpr int kLpThreads = 448;  // 8 softmax warps, 2 + 2 producers, 2 issuers
 constexpr int kLpRows = 64;    // of a CTA
 constexpr int kLpTile = 128;
 
@@ -38,9 +38,9 @@ struct LpCfg {
   static constexpr int KB = kLpTile / 2 * 128;      // a 64-column key block: this CTA's 64 tokens
   static constexpr int KG = 3;                      // blocks to a barrier
   static constexpr int KU = DK / 64 / KG;           // groups of a tile, and of the ring
-  static constexpr int VB = kLpTile * 128;          // a 64-column value block: all tokens
+  static constexpr int VB = kLpTile / 2 * 128;      // a 64-column value block: half of the tokens
   static constexpr int VG = 2;                      // blocks of this CTA's half of 256 columns
-  static constexpr int VU = DV / 256;               // such halves of a tile, and of the ring
+  static constexpr int VU = DV / 256 * 2;           // such units of a tile, and of the ring: (columns, tokens)
   static constexpr int QB = kLpRows * 128;
   static constexpr int PB = kLpRows * 128;          // P of 64 tokens
   static constexpr int OFF_V = 0;
@@ -50,7 +50,7 @@ struct LpCfg {
   static constexpr int OFF_END = OFF_P + 2 * PB;
   static constexpr int OROW = DV * 4 + 16;          // O staging at the end, padded rows
   static constexpr int OFF_RED = OFF_END;           // float [2][4][64]
-  static constexpr int NB = 14 + 2 * VU + 2 * KU;
+  static constexpr int NB = 16 + 2 * VU + 2 * KU;
   static constexpr int OFF_BAR = OFF_RED + 2 * 4 * kLpRows * 4;
   static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
   static constexpr int COL_O = 0, COL_S = 256;      // two S buffers of 64 columns
@@ -59,7 +59,7 @@ struct LpCfg {
 };
 
 enum { PB_SFULL = 0, PB_SREAD = 2, PB_PFULL = 4, PB_PFREE = 5, PB_QLAND = 6, PB_QALL = 7, PB_OFINAL = 8, PB_FIX = 9,
-       PB_SDRAIN = 10, PB_VLAST = 11, PB_RING = 14 };
+       PB_SDRAIN = 10, PB_VLAST = 11, PB_RING = 16 };
 
 struct LpMaps {
   CUtensorMap q, k;
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
       prefetch_map(&maps.k);
     }
     for (int i = lane; i < C::NB; i += 32)
-      mbar_init(bar(i), (i >= PB_SREAD && i <= PB_PFULL) ? 16 : i == PB_FIX || i == PB_QALL ? 2 : 1);
+      mbar_init(bar(i), (i >= PB_SREAD && i <= PB_PFULL) ? 16 : i == PB_FIX ? 4 : i == PB_QALL ? 2 : 1);
     fence_barrier_init();
     __syncwarp();
   }
@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
   };
   // The first tile's are looked up beside the rest of the prologue.
   int blk0 = 0;
-  if ((warp == 0 || warp == 10) && ntiles > 0) blk0 = look_up(lo);
+  const bool keys = warp == 0 || warp == 13, values = warp == 10 || warp == 12;
+  if ((keys || values) && ntiles > 0) blk0 = look_up(lo);
   if (warp == 0 && ntiles > 0) {
     // The queries, at once: their barrier was set up by this warp.
     const uint32_t one = elected();
@@ -178,19 +179,21 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
 
   if (work == 0) {
     // nothing to read: straight to the outputs
-  } else if (warp == 0 || warp == 10) {
+  } else if (keys || values) {
     // ---------------------------------------------------------------- producers
-    // Warp 0: the key groups, of this CTA's half of the tokens.  Warp 10: its half
-    // of V's columns, of all tokens.
-    const bool keys = warp == 0;
+    // Warps 0 and 13: the key groups, of this CTA's half of the tokens, two pages
+    // each.  Warps 10 and 12: its half of V's columns, half of the tokens each.
+    // (What is freed has to be back within a tile, and a page's block is a copy of
+    // its own: issued by one warp each they took as long again.)
+    const int who = warp >= 12 ? 1 : 0;
     const uint32_t one = elected();
     const int lo_u = __shfl_sync(0xffffffffu, lo, 0), hi_u = __shfl_sync(0xffffffffu, hi, 0);
     bool ok = true;
-    if (keys) {
+    if (warp == 0) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(PB_QLAND), 0, abort_p, kLatentWaitNs));
       if (ok && lane == 0) arrive_first(PB_QALL);
     }
-    int issued = 0;  // groups or halves
+    int issued = 0;  // groups or units
     uint32_t par = 1;
     for (int i = 0; i < work && ok; ++i) {
       const int t0 = lo_u + i * kLpTile;
@@ -199,46 +202,50 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
       if (late) found(late);  // before anything of the tile is loaded
       __syncwarp();
       if (keys) {
-        int2 at[4];  // the pages of this CTA's tokens
+        int2 at[2];
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, 4 * rank + g), __shfl_sync(0xffffffffu, a.y, 4 * rank + g));
+        for (int g = 0; g < 2; ++g)
+          at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, 4 * rank + 2 * who + g), __shfl_sync(0xffffffffu, a.y, 4 * rank + 2 * who + g));
 #pragma unroll
         for (int u = 0; u < C::KU; ++u) {
           ok = __all_sync(0xffffffffu, ok && mbar_wait(kfree(u), par, abort_p, kLatentWaitNs));
           if (!ok) break;
-          if (rank == 0) expect_by(one, kfull(u), (uint32_t)(C::KG * pages * kPage * 128));
+          if (rank == 0 && who == 0) expect_by(one, kfull(u), (uint32_t)(C::KG * pages * kPage * 128));
           const uint32_t b = at_first(kfull(u));
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            if (4 * rank + g >= pages) break;
+          for (int g = 0; g < 2; ++g) {
+            if (4 * rank + 2 * who + g >= pages) break;
 #pragma unroll
             for (int k = 0; k < C::KG; ++k)
-              tma_3d_by<true>(one, base + C::OFF_K + (u * C::KG + k) * C::KB + g * kPage * 128, &maps.k, (u * C::KG + k) * 64, at[g].x, at[g].y, b);
+              tma_3d_by<true>(one, base + C::OFF_K + (u * C::KG + k) * C::KB + (2 * who + g) * kPage * 128, &maps.k, (u * C::KG + k) * 64, at[g].x,
+                              at[g].y, b);
           }
           issued = i * C::KU + u + 1;
         }
       } else {
-        int2 at[8];
+        int2 at[4];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, g), __shfl_sync(0xffffffffu, a.y, g));
-        // The last, ragged tile lands on a barrier of each CTA's own, which then
+        for (int g = 0; g < 4; ++g)
+          at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, 4 * who + g), __shfl_sync(0xffffffffu, a.y, 4 * who + g));
+        const int mine = max(0, min(4, pages - 4 * who));
+        // The last, ragged tile lands on barriers of each CTA's own, which then
         // clears what is behind the range.
         const bool alone = ragged && i == work - 1;
 #pragma unroll
-        for (int u = 0; u < C::VU; ++u) {
+        for (int u = who; u < C::VU; u += 2) {
           ok = __all_sync(0xffffffffu, ok && mbar_wait(vfree(u), par, abort_p, kLatentWaitNs));
           if (!ok) break;
-          const uint32_t bytes = (uint32_t)(C::VG * pages * kPage * 128);
+          const uint32_t bytes = (uint32_t)(C::VG * mine * kPage * 128);
           if (alone) expect_by(one, bar(PB_VLAST + u), bytes);
           else if (rank == 0) expect_by(one, vfull(u), 2 * bytes);
           const uint32_t b = alone ? bar(PB_VLAST + u) : at_first(vfull(u));
 #pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            if (g >= pages) break;
+          for (int g = 0; g < 4; ++g) {
+            if (g >= mine) break;
 #pragma unroll
             for (int k = 0; k < C::VG; ++k)
-              tma_3d_by<true>(one, base + C::OFF_V + (u * C::VG + k) * C::VB + g * kPage * 128, &maps.k, u * 256 + rank * 128 + k * 64, at[g].x, at[g].y, b);
+              tma_3d_by<true>(one, base + C::OFF_V + (u * C::VG + k) * C::VB + g * kPage * 128, &maps.k, u / 2 * 256 + rank * 128 + k * 64, at[g].x,
+                              at[g].y, b);
           }
           issued = i * C::VU + u + 1;
         }
@@ -246,16 +253,18 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
       par ^= 1;
     }
     if (!ok && lane == 0) fail();
-    if (!keys && ok && ragged) {
+    if (values && ok && ragged) {
       // Tokens behind the range may hold anything: their V is cleared (their
       // scores are masked).
-      const int valid = hi - lo - (work - 1) * kLpTile, rows = kLpTile - valid;
+      const int valid = max(0, min(kLpTile / 2, hi - lo - (work - 1) * kLpTile - who * (kLpTile / 2))), rows = kLpTile / 2 - valid;
       bool there = true;
-      for (int u = 0; u < C::VU; ++u) there = there && mbar_wait(bar(PB_VLAST + u), 0, abort_p, kLatentWaitNs);
+      for (int u = who; u < C::VU; u += 2) there = there && mbar_wait(bar(PB_VLAST + u), 0, abort_p, kLatentWaitNs);
       if (__all_sync(0xffffffffu, there)) {
-        for (int u = lane; u < C::VU * C::VG * rows * 8; u += 32)
-          *reinterpret_cast<uint4*>(sm + C::OFF_V + u / (rows * 8) * C::VB + (valid + u / 8 % rows) * 128 + (u & 7) * 16) =
+        for (int x = lane; x < C::VU / 2 * C::VG * rows * 8; x += 32) {
+          const int blk = x / (rows * 8), u = blk / C::VG * 2 + who;
+          *reinterpret_cast<uint4*>(sm + C::OFF_V + (u * C::VG + blk % C::VG) * C::VB + (valid + x / 8 % rows) * 128 + (x & 7) * 16) =
               make_uint4(0u, 0u, 0u, 0u);
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_first(PB_FIX);
@@ -263,8 +272,8 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
         fail();
       }
     }
-    // No copy may still be landing when the pair goes away.  (The second CTA's are
-    // counted in the first, which waits for them.)
+    // No copy may still be landing when the pair goes away.  (All but the last
+    // tile's values are counted in the first CTA, which waits for them.)
     if (*abort_p && lane == 0 && rank == 0) {
       const int n = keys ? C::KU : C::VU;
       for (int i = max(0, issued - n); i < issued; ++i) drain(keys ? kfull(i % n) : vfull(i % n), (i / n) & 1);
@@ -310,20 +319,21 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
     // ---------------------------------------------------------------- P.V issuer
     constexpr uint32_t ID = idesc_f16(2 * kLpRows, 256, true, true);
     const uint32_t one = elected();
-    bool ok = true, any = false;
+    bool ok = true, any = false, there = false;
     const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, C::VB, 1024), pd0 = sdesc_sw128(base + C::OFF_P, 16, 1024);
     for (int i = 0; i < work && ok; ++i) {
       const bool fixed = ragged && i == work - 1;
       ok = mbar_wait(bar(PB_PFULL), i & 1, abort_p, kLatentWaitNs) && (!fixed || mbar_wait(bar(PB_FIX), 0, abort_p, kLatentWaitNs));
 #pragma unroll
-      for (int u = 0; u < C::VU; ++u) {
-        ok = __all_sync(0xffffffffu, ok && (fixed || mbar_wait(vfull(u), i & 1, abort_p, kLatentWaitNs)));
+      for (int u = 0; u < C::VU; ++u) {  // 256 columns, 64 tokens
+        ok = __all_sync(0xffffffffu, ok && (fixed || there || mbar_wait(vfull(u), i & 1, abort_p, kLatentWaitNs)));
         if (!ok) break;
         tc_fence_after();
+        there = u + 1 < C::VU && mbar_peek(vfull(u + 1), i & 1);
 #pragma unroll
-        for (int kk = 0; kk < kLpTile / 16; ++kk)
-          mma_ss_by<true>(one, tm + C::COL_O + u * 128, pd0 + (uint64_t)(((kk >> 2) * C::PB + (kk & 3) * 32) >> 4),
-                          vd0 + (uint64_t)((u * C::VG * C::VB + kk * 2048) >> 4), ID, i > 0 || kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < kLpTile / 2 / 16; ++kk)
+          mma_ss_by<true>(one, tm + C::COL_O + u / 2 * 128, pd0 + (uint64_t)(((u & 1) * C::PB + kk * 32) >> 4),
+                          vd0 + (uint64_t)((u * C::VG * C::VB + kk * 2048) >> 4), ID, i > 0 || (u & 1) || kk > 0 ? 1u : 0u);
         any = true;
         commit_by<true>(one, vfree(u));
       }
