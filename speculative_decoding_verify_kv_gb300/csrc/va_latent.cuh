@@ -162,6 +162,5 @@ cudaError_t launch_latent_pair(const LatentParams& p, dim3 grid, cudaStream_t st
 int latent_pair_rows();
 cudaError_t launch_latent_rows(const LatentParams& p, dim3 grid, cudaStream_t st);
 int latent_rows_rows(long long rows);
-int latent_umma_parts(int value_dim, bool prompt);
 
 }  // namespace va

@@ -87,10 +87,12 @@ static LatentPlan plan_rows(const va_problem* p, int dtype, int value_dim, bool 
     const int few = prompt ? 0 : latent_rows_rows((long long)p->max_rows_per_seq * p->num_heads);
     pl.few = few > 0;
     pl.rows_per_block = few ? few : latent_umma_rows();
-    // 512 latent columns: pairs of CTAs, which share a row block like `parts`.
+    // 512 latent columns: pairs of CTAs.  64 heads x 16 rows x 4 sequences of 8,000
+    // tokens took the 128-row kernel, with O's columns dealt to two CTAs, 86 us
+    // (64), 32 sequences of 5,100 and 64 heads 70 (55).
     pl.pair = !few && !prompt && value_dim == 512;
     if (pl.pair) pl.rows_per_block = latent_pair_rows();
-    pl.parts = few ? 1 : latent_umma_parts(value_dim, prompt);
+    pl.parts = pl.pair ? 2 : 1;
     pl.per_sm = 1;
   } else {
     pl.kernel = VA_KERNEL_CUDA_CORES;
@@ -103,7 +105,7 @@ static LatentPlan plan_rows(const va_problem* p, int dtype, int value_dim, bool 
   const long long blocks = (rows + pl.rows_per_block - 1) / pl.rows_per_block;
   pl.many = pl.slots / (blocks > 0 ? blocks : 1) > 8;
   // A sequence of b row blocks has b max(1, slots / b) CTAs per key head.
-  pl.grid = dim3((unsigned)(blocks > pl.slots ? blocks : pl.slots), (unsigned)(prompt ? p->num_heads : pl.pair ? 1 : pl.parts),
+  pl.grid = dim3((unsigned)(blocks > pl.slots ? blocks : pl.slots), (unsigned)(prompt ? p->num_heads : 1),
                  (unsigned)p->num_seqs);
   if (pl.slots > 1) {
     const size_t items = (size_t)pl.slots * (size_t)p->total_rows * (size_t)p->num_heads;

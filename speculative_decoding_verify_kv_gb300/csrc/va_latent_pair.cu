@@ -140,10 +140,13 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
     }
     return make_int2(0, blk);
   };
-  // The first tile's are looked up beside the rest of the prologue.
-  int blk0 = 0;
+  // Looked up a tile ahead; the first beside the rest of the prologue.
+  int blk0 = 0, blk1 = 0;
   const bool keys = warp == 0 || warp == 13, values = warp == 10 || warp == 12;
-  if ((keys || values) && ntiles > 0) blk0 = look_up(lo);
+  if ((keys || values) && ntiles > 0) {
+    blk0 = look_up(lo);
+    blk1 = look_up(lo + kLpTile);
+  }
   if (warp == 0 && ntiles > 0) {
     // The queries, at once: their barrier was set up by this warp.
     const uint32_t one = elected();
@@ -198,10 +201,21 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
     for (int i = 0; i < work && ok; ++i) {
       const int t0 = lo_u + i * kLpTile;
       const int pages = (min(kLpTile, hi_u - t0) + kPage - 1) / kPage;
-      const int2 a = page_at(t0, i == 0 ? blk0 : look_up(t0));
+      const int2 a = page_at(t0, blk0);
       if (late) found(late);  // before anything of the tile is loaded
       __syncwarp();
+      blk0 = blk1;
+      blk1 = look_up(t0 + 2 * kLpTile);
       if (keys) {
+        // The next tile's pages into L2: what is freed has to be back soon (32
+        // sequences of 5,100 tokens, 128 heads: 65 us without, 59 with, 61.5 two
+        // tiles ahead).
+        if (lane >= 4 * rank + 2 * who && lane < 4 * rank + 2 * who + 2) {
+          const int t = t0 + kLpTile + lane * kPage;
+          const long long row = p.page_size ? (long long)blk0 * kPage : (long long)s * p.capacity + t;
+          if (t < hi && blk0 >= 0 && (p.page_size == 0 || blk0 < p.num_blocks))
+            bulk_prefetch_l2(reinterpret_cast<const unsigned short*>(p.cache) + row * C::DK, kPage * C::DK * 2);
+        }
         int2 at[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g)

@@ -10,15 +10,11 @@
 //   O += P V      tcgen05.mma, A = P (TMEM), B = V tile (MN-major)
 // so that S of the next tile runs under this tile's softmax.
 //
-// Absorbed form: a token has one row of DK values and V is the first of them,
-// so the column blocks of V are loaded once and read by both products (as K
-// they are K-major, as V MN-major: the same bytes).  O of 512 columns would
-// take all of TMEM and leave none for S: with latent_dim 512 two CTAs share a
-// row block, each computes S and the softmax whole and half of O's columns
-// (832 instead of 1,088 of the 2 x 544 multiply-adds of an even split; what
-// would avoid it, exchanging S or P between the two, waits on the other CTA
-// in every tile).  The queries of the V columns go to TMEM, those of the other
-// columns stay in shared memory.
+// Absorbed form (256 latent columns; 512 are va_latent_pair.cu's): a token has one
+// row of DK values and V is the first of them, so the column blocks of V are
+// loaded once and read by both products (as K they are K-major, as V MN-major:
+// the same bytes).  The queries of the V columns go to TMEM, those of the rope
+// part stay in shared memory.
 //
 // Shared memory holds two rings of 64-column blocks of a tile: V stages of
 // VBLK blocks, freed by P.V, and single blocks of the key's other columns,
@@ -41,20 +37,19 @@ struct LuCfg {
   static constexpr int DK = DK_;                     // key width
   static constexpr int DV = DV_;                     // value width
   static constexpr bool PROMPT = PROMPT_;
-  static constexpr int PARTS = DV > 256 ? 2 : 1;     // CTAs that share O's columns
-  static constexpr int DO = DV / PARTS;              // O columns of a CTA
+  static constexpr int DO = DV;                      // O columns
   static constexpr int NT = PROMPT ? 128 : 64;       // tokens per tile
   static constexpr int BLK = NT * 128;               // bytes of a 64-column block
   static constexpr int VBLK = DO / 64;               // blocks of a V stage
   static constexpr int KBLK = PROMPT ? DK / 64 : DK / 64 - VBLK;  // other blocks of the key
   static constexpr int QT = PROMPT ? 128 : DO;       // query columns in TMEM
   static constexpr int QS = DK - QT;                 // query columns in shared memory
-  static constexpr int NV = PROMPT ? (DV == 128 ? 2 : 4) : (DV == 512 ? 3 : 5);  // V stages
-  static constexpr int NK = PROMPT ? (DV == 128 ? 9 : 6) : (DV == 512 ? 6 : 5);  // key blocks
+  static constexpr int NV = PROMPT ? (DV == 128 ? 2 : 4) : 5;  // V stages
+  static constexpr int NK = PROMPT ? (DV == 128 ? 9 : 6) : 5;  // key blocks
   static constexpr int COL_O = 0;
   static constexpr int COL_S = DO;
   // Prompts: P has columns of its own, so that S(i + 2) waits for S(i) to be read
-  // only, not for P(i) V (in S's place: 755 us against 640 for 2 x 2,048 rows of
+  // only, not for P(i) V (in S's place: 750 us against 714 for 2 x 2,048 rows of
   // 128 heads over 4,096 keys).  The absorbed form has no columns left for it.
   static constexpr bool SEP = PROMPT;
   static constexpr int COL_P = DO + 2 * NT;
@@ -116,11 +111,11 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   // on the stream has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int s = blockIdx.z;
-  const int head = PROMPT ? blockIdx.y : 0, part = PROMPT ? 0 : blockIdx.y;
+  const int head = PROMPT ? blockIdx.y : 0;
   const LatentSeq q = latent_seq(p, s);
   if (q.err & VA_DEV_BAD_ROWS) {
     if (tid == 0) flag(p.status, q.err);
-    if (blockIdx.x == 0 && part == 0) latent_nan_rows(p, s, head, PROMPT ? 1 : p.H);
+    if (blockIdx.x == 0) latent_nan_rows(p, s, head, PROMPT ? 1 : p.H);
     return;
   }
   const int R = latent_rows(p, q.n);
@@ -171,12 +166,9 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     expect_by(one, bar(LB_QLAND), C::DK / 64 * kLuM * 128);
 #pragma unroll
     for (int c = 0; c < C::DK / 64; ++c) {
-      // Absorbed form: the columns of this part's V come first, in TMEM.
-      const int col = PROMPT ? c * 64 : c < C::VBLK ? (part * C::VBLK + c) * 64
-                                      : (c - C::VBLK < part * C::VBLK ? c - C::VBLK : c) * 64;
       const uint32_t dst = base + (c < C::QT / 64 ? C::QSTAGE + c * kLuM * 128 : C::OFF_Q + (c - C::QT / 64) * kLuM * 128);
-      if (PROMPT) tma_3d_by(one, dst, &maps.q, col, head, qrow, bar(LB_QLAND));
-      else tma_2d_by(one, dst, &maps.q, col, qrow, bar(LB_QLAND));
+      if (PROMPT) tma_3d_by(one, dst, &maps.q, c * 64, head, qrow, bar(LB_QLAND));
+      else tma_2d_by(one, dst, &maps.q, c * 64, qrow, bar(LB_QLAND));
     }
   }
   if (warp == 1) {
@@ -251,7 +243,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
             if (g >= pages) break;
 #pragma unroll
             for (int c = 0; c < C::VBLK; ++c)
-              tma_3d_by(one, dst + c * C::BLK + g * kPage * 128, &maps.k, (part * C::VBLK + c) * 64, at[g].x, at[g].y, b);
+              tma_3d_by(one, dst + c * C::BLK + g * kPage * 128, &maps.k, c * 64, at[g].x, at[g].y, b);
           }
         }
         issued = i + 1;
@@ -270,7 +262,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
             if (c == C::KBLK - 1) tma_2d_by(one, dst, &maps.r, 0, key0 + t0, b);
             else tma_3d_by(one, dst, &maps.k, c * 64, head, key0 + t0, b);
           } else {
-            const int col = (c < part * C::VBLK ? c : c + C::VBLK) * 64;
+            const int col = (c + C::VBLK) * 64;
             expect_by(one, b, (uint32_t)(pages * kPage * 128));
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -567,7 +559,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     const float l = red[r] + red[kLuM + r];
     const bool bad = __any_sync(0xffffffffu, *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0);
     const float inv = bad ? NAN : l > 0.f ? 1.f / l : 0.f;
-    if (rvalid && half == 0 && part == 0) {
+    if (rvalid && half == 0) {
       const long long item = latent_item(p, q.row0, rbase + r, head);
       if (live > 1) {
         const long long si = latent_slot(p, chunk, item);
@@ -614,14 +606,14 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     const long long first = latent_item(p, q.row0, rbase, head), step = PROMPT ? p.H : 1;
     if (live > 1) {
       constexpr int PIECES = DO / 4;  // of 16 bytes
-      float* to = p.ws_acc + latent_slot(p, chunk, first) * C::DV + part * DO;
+      float* to = p.ws_acc + latent_slot(p, chunk, first) * C::DV;
       for (int u = tid - 64; u < nrows * PIECES; u += 256) {
         const int row = u / PIECES, c = u % PIECES;
         *reinterpret_cast<uint4*>(to + row * step * C::DV + c * 4) = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
       }
     } else {
       constexpr int PIECES = DO / 8;
-      unsigned short* to = reinterpret_cast<unsigned short*>(p.o) + first * C::DV + part * DO;
+      unsigned short* to = reinterpret_cast<unsigned short*>(p.o) + first * C::DV;
       for (int u = tid - 64; u < nrows * PIECES; u += 256) {
         const int row = u / PIECES, c = u % PIECES;
         *reinterpret_cast<uint4*>(to + row * step * C::DV + c * 8) = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
@@ -635,14 +627,14 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       const int row = u / DO, d = u % DO;
       const long long item = latent_item(p, q.row0, rbase + row, head);
       if (live > 1) {
-        if (d == 0 && part == 0) {
+        if (d == 0) {
           const long long si = latent_slot(p, chunk, item);
           p.ws_ml[2 * si] = q.err ? NAN : -INFINITY;
           p.ws_ml[2 * si + 1] = q.err ? NAN : 0.f;
         }
       } else {
-        reinterpret_cast<unsigned short*>(p.o)[item * C::DV + part * DO + d] = q.err ? 0x7fffu : 0u;
-        if (d == 0 && part == 0) p.lse[item] = q.err ? NAN : -INFINITY;
+        reinterpret_cast<unsigned short*>(p.o)[item * C::DV + d] = q.err ? 0x7fffu : 0u;
+        if (d == 0) p.lse[item] = q.err ? NAN : -INFINITY;
       }
     }
   }
@@ -690,14 +682,12 @@ static cudaError_t launch_umma_latent(const LatentParams& p, dim3 grid, cudaStre
 }
 
 int latent_umma_rows() { return kLuM; }
-int latent_umma_parts(int value_dim, bool prompt) { return !prompt && value_dim > 256 ? 2 : 1; }
 
 cudaError_t launch_latent_umma(const LatentParams& p, dim3 grid, cudaStream_t st) {
   if (p.prompt)
     return p.DV == 128 ? launch_umma_latent<LuCfg<192, 128, true>>(p, grid, st)
                        : launch_umma_latent<LuCfg<128, 64, true>>(p, grid, st);
-  return p.DV == 512 ? launch_umma_latent<LuCfg<576, 512, false>>(p, grid, st)
-                     : launch_umma_latent<LuCfg<320, 256, false>>(p, grid, st);
+  return launch_umma_latent<LuCfg<320, 256, false>>(p, grid, st);
 }
 
 }  // namespace va
