@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
     bar_sync(1, 256);
     const float l = (red[r] + red[kLpRows + r]) + (red[2 * kLpRows + r] + red[3 * kLpRows + r]);
     const bool bad = __any_sync(0xffffffffu, *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0);
-    const float inv = bad ? NAN : l > 0.f ? 1.f / l : 0.f;
+    const float inv = bad ? NAN : l != 0.f ? 1.f / l : 0.f;
     const long long first = (long long)q.row0 * p.H + rbase;
     if (rvalid && who == 0) {
       if (live > 1) {
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
         p.ws_ml[2 * si] = bad ? NAN : m_use;
         p.ws_ml[2 * si + 1] = bad ? NAN : l;
       } else {
-        p.lse[first + r] = bad ? NAN : l > 0.f ? (m_use + log2f(l)) * kLn2 : -INFINITY;
+        p.lse[first + r] = bad ? NAN : l != 0.f ? (m_use + log2f(l)) * kLn2 : -INFINITY;
       }
     }
     // O rows through shared memory (keys, values and queries are done with) to
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
           uint32_t w[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const __nv_bfloat162 h = l > 0.f || bad ? __floats2bfloat162_rn(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv)
+            const __nv_bfloat162 h = l != 0.f || bad ? __floats2bfloat162_rn(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv)
                                                     : __floats2bfloat162_rn(0.f, 0.f);
             w[c] = *reinterpret_cast<const uint32_t*>(&h);
           }

@@ -487,11 +487,11 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
         p.ws_ml[2 * si] = bad ? NAN : m;
         p.ws_ml[2 * si + 1] = bad ? NAN : sum;
       } else {
-        p.lse[item0 + th] = bad ? NAN : sum > 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+        p.lse[item0 + th] = bad ? NAN : sum != 0.f ? (m + log2f(sum)) * kLn2 : -INFINITY;
       }
     }
     // O^T: a lane per value column, so a warp stores 32 of a row's at once.
-    if (th < R) f_s[th] = bad ? NAN : live > 1 ? 1.f : sum_of(th) > 0.f ? 1.f / sum_of(th) : 0.f;
+    if (th < R) f_s[th] = bad ? NAN : live > 1 ? 1.f : sum_of(th) != 0.f ? 1.f / sum_of(th) : 0.f;
     bar_sync(3, 128);
     const long long first = (live > 1 ? latent_slot(p, chunk, item0) : item0) * C::DV + th;
 #pragma unroll 1

@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentPar
       for (int c = 0; c < NC; ++c) p.ws_acc[si * DV + col + 32 * (c / CV * CV) + c % CV] = acc[i][c];
       continue;
     }
-    const float inv = err ? NAN : l > 0.f ? 1.f / l : 0.f;
-    if (lane == 0 && half == 0) p.lse[item] = err ? NAN : l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    const float inv = err ? NAN : l != 0.f ? 1.f / l : 0.f;
+    if (lane == 0 && half == 0) p.lse[item] = err ? NAN : l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const long long at = item * DV + col + 32 * (c / CV * CV) + c % CV;

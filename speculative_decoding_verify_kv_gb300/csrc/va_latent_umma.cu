@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     bar_sync(1, 256);
     const float l = red[r] + red[kLuM + r];
     const bool bad = __any_sync(0xffffffffu, *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0);
-    const float inv = bad ? NAN : l > 0.f ? 1.f / l : 0.f;
+    const float inv = bad ? NAN : l != 0.f ? 1.f / l : 0.f;
     if (rvalid && half == 0) {
       const long long item = latent_item(p, q.row0, rbase + r, head);
       if (live > 1) {
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
         p.ws_ml[2 * si] = bad ? NAN : m_use;
         p.ws_ml[2 * si + 1] = bad ? NAN : l;
       } else {
-        p.lse[item] = bad ? NAN : l > 0.f ? (m_use + log2f(l)) * kLn2 : -INFINITY;
+        p.lse[item] = bad ? NAN : l != 0.f ? (m_use + log2f(l)) * kLn2 : -INFINITY;
       }
     }
     // O rows through shared memory (its rings are idle now) to coalesced
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             // A row that sees nothing has no sum (its lanes of O may hold anything).
-            const __nv_bfloat162 h = l > 0.f || bad ? __floats2bfloat162_rn(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv)
+            const __nv_bfloat162 h = l != 0.f || bad ? __floats2bfloat162_rn(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv)
                                                     : __floats2bfloat162_rn(0.f, 0.f);
             w[c] = *reinterpret_cast<const uint32_t*>(&h);
           }

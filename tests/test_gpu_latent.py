@@ -141,6 +141,40 @@ def test_latent_alone_and_in_company(splits):
     assert torch.equal(o[3:], o1) and torch.equal(lse[3:], lse1)
 
 
+@pytest.mark.parametrize("kind,heads,rows,latent", [("f32", 3, 5, 256), ("bf16", 3, 5, 512), ("bf16", 16, 5, 512), ("bf16", 16, 5, 256)])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_latent_not_a_number(kind, heads, rows, latent, splits):
+    """A query that is no number is its own row's matter."""
+    case = Latent(kind, heads, latent, [300, 40], [rows, 2], seed=2, splits=splits)
+    want = [t.clone() for t in case.run()]
+    case.q[2, 1, 7] = float("nan")
+    o, lse = case.run()
+    assert o[2, 1].isnan().all() and lse[2, 1].isnan()
+    keep = torch.ones_like(lse, dtype=torch.bool)
+    keep[2, 1] = False
+    assert torch.equal(o[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_prompt_not_a_number(kind, splits):
+    case = Prompt(kind, 2, 128, [140, 3], [400, 3], seed=2, splits=splits)
+    want = [t.clone() for t in case.run()]
+    case.p.q[130, 1, 7] = float("nan")
+    o, lse = case.run()
+    assert o[130, 1].isnan().all() and lse[130, 1].isnan()
+    keep = torch.ones_like(lse, dtype=torch.bool)
+    keep[130, 1] = False
+    assert torch.equal(o[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+
+
+@pytest.mark.parametrize("heads,ctx,rows,splits", [(128, 1000, 3, 1), (64, 1, 1, 1), (33, 127, 1, 2), (40, 128, 7, 6), (128, 640, 1, 5)])
+def test_latent_pairs(heads, ctx, rows, splits):
+    """Pairs of CTAs: second halves without rows, odd tiles, one tile."""
+    run_check(Latent("bf16", heads, 512, [ctx, ctx + 63, 0, 5 * ctx], [rows, 1, rows, rows], "chain", heads % 2 == 0, seed=heads,
+                     splits=splits))
+
+
 def test_latent_far_pages():
     """Offsets past 2^32 bytes: pages at the end of a pool of 6 GB."""
     width, blocks = 576, 330_000
