@@ -317,13 +317,6 @@ __device__ __forceinline__ unsigned long long cut_times(unsigned long long c, fl
   return sh < 0 ? c : (u + 1) >> 1;  // (sh < 0: g = 1)
 }
 
-// The two halves of a cluster barrier.  Another CTA's shared memory may be
-// touched only once that CTA has started, which being scheduled together does
-// not promise: every thread says so at its start, and waits for the others'
-// behind what it would wait for anyway.
-__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_met() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-
 constexpr int kMaxRej = kMaxTreeRows;  // rejected siblings of one node
 
 struct WalkShared {

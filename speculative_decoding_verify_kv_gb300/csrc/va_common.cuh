@@ -58,6 +58,13 @@ __device__ __forceinline__ void flag(unsigned* status, unsigned bits) {
   if (status) atomicOr(status, bits);
 }
 
+// The two halves of a cluster barrier.  Another CTA's shared memory may be
+// touched only once that CTA has started, which being scheduled together does
+// not promise: every thread says so at its start, and waits for the others'
+// behind what it would wait for anyway.
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_met() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // Split rule: chunk = ceil(L/S) rounded up to 16 tokens; split s covers
 // [s*chunk, min((s+1)*chunk, L)).  Sub-chunk p of P covers a 16-aligned
 // slice of that range; the number of live sub-chunks depends only on the

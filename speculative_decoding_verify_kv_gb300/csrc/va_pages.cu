@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_extend_kernel(const PagePa
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Team<NC> team;
-  if (NC > 1) team.cluster.barrier_arrive();  // waited for before the first write into another CTA
+  if (NC > 1) cluster_started();  // waited for before the first write into another CTA
   const int rank = team.rank();
   const int tid = threadIdx.x, lane = tid & 31, gwarp = rank * kCtaWarps + tid / 32;
   const int gtid = rank * kPlanThreads + tid;
@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kPlanThreads) pages_extend_kernel(const PagePa
       if (r == 0 && k < 32) bits |= 1u << k;
     }
   }
-  if (NC > 1) team.cluster.barrier_wait();
+  if (NC > 1) cluster_met();
   // Check every sequence and count the pages it takes.
   const int sub = lane & (kSeqLanes - 1);
   const unsigned peers = 0xffu << (lane & ~(kSeqLanes - 1));
