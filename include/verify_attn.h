@@ -715,7 +715,7 @@ va_status verify_attn_latent_append(const va_latent *kv, const va_latent_rows *r
  * caches, VA_FLAG_CUDA_CORES) each takes num_splits / b chunks, rounded
  * down, and at least one.  va_latent_splits gives a count that fills the
  * GPU.  No choice depends on the other sequences of the launch.
- * bf16: probabilities enter the second product rounded to bf16 (2^-9 of each,
+ * bf16: probabilities enter the second product rounded to bf16 (2^-8 of each at most,
  * about what rounding o costs); their sum, and lse, are of the unrounded
  * ones in fp32.  fp32: fp32 products and sums.
  * Cache rows that some rows of the sequence see and others do not must be

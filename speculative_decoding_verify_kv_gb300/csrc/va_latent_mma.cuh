@@ -20,12 +20,6 @@ __device__ __forceinline__ float lu_ex2(float x) {
   return y;
 }
 
-// MMAs and commits that a whole warp runs through and its elected lane (e != 0)
-// issues, with everything they are computed from known to be the warp's:
-// descriptors then live in uniform registers.  An issuing thread of its own
-// branch took some 100 cycles to an MMA, longer than one of 64 columns runs
-// (64 heads x 16 rows x 4 sequences of 8,000 tokens: 142 us against 112; prompts
-// of 2 x 2,048 rows, 128 heads, over 4,096 keys: 966 against 755).
 // Three maxima, and two products and sums, to an instruction.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -53,32 +47,29 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// MMAs and commits that a whole warp runs through and its elected lane (e != 0)
+// issues, with everything they are computed from known to be the warp's:
+// descriptors then live in uniform registers.  An issuing thread of its own
+// branch took some 100 cycles to an MMA, longer than one of 64 columns runs
+// (64 heads x 16 rows x 4 sequences of 8,000 tokens: 142 us against 112; prompts
+// of 2 x 2,048 rows, 128 heads, over 4,096 keys: 966 against 755).
 __device__ __forceinline__ uint32_t elected() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));
   return e;
 }
 
-// PAIR: one product over both CTAs of a pair (cta_group::2), issued by the first:
-// each holds its own rows of A and D and half of B, and a commit arrives in both.
-template <bool PAIR = false>
 __device__ __forceinline__ void mma_ts_by(uint32_t e, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-        "r"(accumulate), "r"(e)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-        "r"(accumulate), "r"(e)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(accumulate), "r"(e)
+      : "memory");
 }
 
+// PAIR: one product over both CTAs of a pair (cta_group::2), issued by the first:
+// each holds its own rows of A and D and half of B, and a commit arrives in both.
 template <bool PAIR = false>
 __device__ __forceinline__ void mma_ss_by(uint32_t e, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   if constexpr (PAIR)
@@ -113,20 +104,13 @@ __device__ __forceinline__ void commit_by(uint32_t e, uint32_t bar) {
         : "memory");
 }
 
-template <bool PAIR>
-__device__ __forceinline__ void tmem_alloc_of(uint32_t dst, uint32_t ncols) {
-  if constexpr (PAIR) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-  } else {
-    tmem_alloc(dst, ncols);
-    tmem_relinquish();
-  }
+// Of a pair: by one warp of each CTA.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
 }
-template <bool PAIR>
-__device__ __forceinline__ void tmem_dealloc_of(uint32_t taddr, uint32_t ncols) {
-  if constexpr (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-  else tmem_dealloc(taddr, ncols);
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
 // The same place in the shared memory of the pair's first CTA, and an arrival there.
@@ -166,25 +150,16 @@ __device__ __forceinline__ void expect_by(uint32_t e, uint32_t bar, uint32_t byt
       : "memory");
 }
 
-// PAIR: the barrier may be the other CTA's.
-template <bool PAIR = false>
 __device__ __forceinline__ void tma_2d_by(uint32_t e, uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-  if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(bar), "r"(e)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
-        "l"(map), "r"(c0), "r"(c1), "r"(bar), "r"(e)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar), "r"(e)
+      : "memory");
 }
 
+// PAIR: the barrier may be the other CTA's.
 template <bool PAIR = false>
 __device__ __forceinline__ void tma_3d_by(uint32_t e, uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar) {
   if constexpr (PAIR)
@@ -213,7 +188,6 @@ inline bool latent_map(CUtensorMap* map, const void* base, int rank, const cuuin
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
 
 // Absorbed form: all query rows of a launch, in boxes of `rows`; the cache, in
 // boxes of a page.

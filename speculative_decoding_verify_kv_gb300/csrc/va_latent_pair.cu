@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
 #pragma unroll
     for (int c = 0; c < C::DK / 64; ++c) tma_2d_by(one, base + C::OFF_Q + c * C::QB, &maps.q, c * 64, qrow, bar(PB_QLAND));
   }
-  if (warp == 1) tmem_alloc_of<true>(smem_u32(tmem_at), 512);
+  if (warp == 1) tmem_alloc_pair(smem_u32(tmem_at), 512);
   tc_fence_before();
   cluster_sync_all();  // the barriers of both CTAs are set up
   tc_fence_after();
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
   tc_fence_before();
   cluster_sync_all();  // the other CTA's products and arrivals reach into this one
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_of<true>(tm, 512);
+  if (warp == 1) tmem_dealloc_pair(tm, 512);
 }
 
 int latent_pair_rows() { return 2 * kLpRows; }

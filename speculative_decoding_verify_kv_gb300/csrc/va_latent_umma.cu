@@ -51,7 +51,9 @@ struct LuCfg {
   // Prompts: P has columns of its own, so that S(i + 2) waits for S(i) to be read
   // only, not for P(i) V (in S's place: 750 us against 714 for 2 x 2,048 rows of
   // 128 heads over 4,096 keys).  The absorbed form has no columns left for it.
-  static constexpr bool SEP = PROMPT;
+  // (Values of 64 columns take less time for P V than for the wait before P is
+  // written: 668 us with, 633 without.)
+  static constexpr bool SEP = PROMPT && DV == 128;
   static constexpr int COL_P = DO + 2 * NT;
   static constexpr int COL_Q = COL_P + (SEP ? NT / 2 : 0);
   static constexpr int OFF_V = 0;
@@ -483,7 +485,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(LB_SFREE + b));
       }
-      // The previous P.V: it has to be done before O is rescaled, or (prompts) P
+      // The previous P.V: it has to be done before O is rescaled, or (SEP) P
       // written.
       auto pv_done = [&]() {
         return i < 1 || (C::SEP ? mbar_wait(bar(LB_PFREE), (i - 1) & 1, abort_p, kLatentWaitNs)
