@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   const int blocks = (R + kLuM - 1) / kLuM;
   if (blocks == 0) return;
   const int nchunk = latent_chunks(p, q.n);
-  const int rb = blockIdx.x % blocks, chunk = blockIdx.x / blocks;
+  const int rb = PROMPT ? blocks - 1 - blockIdx.x % blocks : blockIdx.x % blocks, chunk = blockIdx.x / blocks;
   const int live = latent_live(p, q.err ? 0 : q.len, nchunk);
   if (chunk >= live) return;
   const int rbase = rb * kLuM, nrows = min(kLuM, R - rbase);
