@@ -137,10 +137,10 @@ __device__ __forceinline__ unsigned latent_bits(const LatentParams& p, const Lat
 }
 
 // NaN in o and lse of a sequence with inconsistent offsets (the rows of it
-// that exist), by one CTA.  heads: first head and how many.
-__device__ __forceinline__ void latent_nan_rows(const LatentParams& p, int s, int h0, int heads) {
+// that exist), by thread t of so many.  heads: first head and how many.
+__device__ __forceinline__ void latent_nan_rows(const LatentParams& p, int s, int h0, int heads, int t, int threads) {
   const long long a = max(0, p.cu_rows[s]), b = min(p.total_rows, p.cu_rows[s + 1]);
-  for (long long i = (long long)threadIdx.x; i < (b - a) * heads * p.DV; i += blockDim.x) {
+  for (long long i = t; i < (b - a) * heads * p.DV; i += threads) {
     const long long item = (a + i / ((long long)heads * p.DV)) * p.H + h0 + i / p.DV % heads;
     const int d = (int)(i % p.DV);
     if (p.o_bf16) reinterpret_cast<unsigned short*>(p.o)[item * p.DV + d] = 0x7fffu;
@@ -158,6 +158,8 @@ cudaError_t launch_latent_merge(const LatentParams& p, cudaStream_t st);
 int latent_simt_rows();
 cudaError_t launch_latent_umma(const LatentParams& p, dim3 grid, cudaStream_t st);
 int latent_umma_rows();
+cudaError_t launch_latent_prompt(const LatentParams& p, dim3 grid, cudaStream_t st);
+int latent_prompt_rows();
 cudaError_t launch_latent_pair(const LatentParams& p, dim3 grid, cudaStream_t st);
 int latent_pair_rows();
 cudaError_t launch_latent_rows(const LatentParams& p, dim3 grid, cudaStream_t st);

@@ -86,7 +86,7 @@ static LatentPlan plan_rows(const va_problem* p, int dtype, int value_dim, bool 
     pl.kernel = VA_KERNEL_TENSOR;
     const int few = prompt ? 0 : latent_rows_rows((long long)p->max_rows_per_seq * p->num_heads);
     pl.few = few > 0;
-    pl.rows_per_block = few ? few : latent_umma_rows();
+    pl.rows_per_block = prompt ? latent_prompt_rows() : few ? few : latent_umma_rows();
     // 512 latent columns: pairs of CTAs.  64 heads x 16 rows x 4 sequences of 8,000
     // tokens took the 128-row kernel, with O's columns dealt to two CTAs, 86 us
     // (64), 32 sequences of 5,100 and 64 heads 70 (55).
@@ -180,8 +180,9 @@ static va_status check_outputs(const LatentPlan& pl, const void* ws, size_t ws_b
 static va_status launch(const LatentParams& q, const LatentPlan& pl, cudaStream_t cs) {
   cudaError_t e = pl.few                           ? launch_latent_rows(q, pl.grid, cs)
                   : pl.pair                       ? launch_latent_pair(q, pl.grid, cs)
-                  : pl.kernel == VA_KERNEL_TENSOR ? launch_latent_umma(q, pl.grid, cs)
-                                                  : launch_latent_simt(q, pl.grid, cs);
+                  : pl.kernel != VA_KERNEL_TENSOR ? launch_latent_simt(q, pl.grid, cs)
+                  : q.prompt                      ? launch_latent_prompt(q, pl.grid, cs)
+                                                  : launch_latent_umma(q, pl.grid, cs);
   if (e == cudaSuccess && pl.slots > 1) e = launch_latent_merge(q, cs);
   return e == cudaSuccess ? VA_OK : note_cuda(e);
 }

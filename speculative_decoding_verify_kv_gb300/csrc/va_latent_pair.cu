@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
   const LatentSeq q = latent_seq(p, s);
   if (q.err & VA_DEV_BAD_ROWS) {
     if (tid == 0) flag(p.status, q.err);
-    if (blockIdx.x == 0) latent_nan_rows(p, s, 0, p.H);
+    if (blockIdx.x == 0) latent_nan_rows(p, s, 0, p.H, threadIdx.x, blockDim.x);
     return;
   }
   const int R = latent_rows(p, q.n);
@@ -321,13 +321,12 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
       if (!ok) break;
       commit_by<true>(one, bar(PB_SFULL + b));
     }
-    if (!ok && lane == 0) {
-      fail();
-      // What was issued completes before TMEM and shared memory go.
-      if (any) {
-        commit_by<true>(1u, bar(PB_SDRAIN));
-        drain(bar(PB_SDRAIN), 0);
-      }
+    if (!ok && lane == 0) fail();
+    if (!ok && any) {
+      // What was issued completes before TMEM and shared memory go.  (A commit is
+      // for what its own thread has issued.)
+      commit_by<true>(one, bar(PB_SDRAIN));
+      drain(bar(PB_SDRAIN), 0);
     }
   } else if (warp == 11 && rank == 0) {
     // ---------------------------------------------------------------- P.V issuer
@@ -353,13 +352,11 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
       }
       if (ok) commit_by<true>(one, bar(PB_PFREE));
     }
-    if (lane == 0) {
-      if (!ok) fail();
-      if (any) {
-        // After every P.V, in a failed run too.
-        commit_by<true>(1u, bar(PB_OFINAL));
-        drain(bar(PB_OFINAL), 0);
-      }
+    if (!ok && lane == 0) fail();
+    if (any) {
+      // After every P.V, in a failed run too.
+      commit_by<true>(one, bar(PB_OFINAL));
+      drain(bar(PB_OFINAL), 0);
     }
   } else if (warp >= 2 && warp < 10) {
     // ---------------------------------------------------------------- softmax

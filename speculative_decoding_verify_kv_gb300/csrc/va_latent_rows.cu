@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
   const LatentSeq q = latent_seq(p, s);
   if (q.err & VA_DEV_BAD_ROWS) {
     if (tid == 0) flag(p.status, q.err);
-    if (chunk == 0) latent_nan_rows(p, s, 0, p.H);
+    if (chunk == 0) latent_nan_rows(p, s, 0, p.H, threadIdx.x, blockDim.x);
     return;
   }
   const int R = q.n * p.H;
@@ -311,13 +311,12 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       if (!ok) break;
       commit_by(one, bar(RB_SFULL + b));
     }
-    if (!ok && lane == 0) {
-      fail();
-      // What was issued completes before TMEM and shared memory go.
-      if (any) {
-        mma_commit(bar(RB_SDRAIN));
-        drain(bar(RB_SDRAIN), 0);
-      }
+    if (!ok && lane == 0) fail();
+    if (!ok && any) {
+      // What was issued completes before TMEM and shared memory go.  (A commit is
+      // for what its own thread has issued.)
+      commit_by(one, bar(RB_SDRAIN));
+      drain(bar(RB_SDRAIN), 0);
     }
   } else if (warp == 6) {
     // ---------------------------------------------------------------- P.V issuer
@@ -344,12 +343,11 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       any = true;
       commit_by(one, bar(RB_PFREE + (i & 1)));
     }
-    if (lane == 0) {
-      if (!ok) fail();
-      if (any) {
-        mma_commit(bar(RB_OFINAL));
-        drain(bar(RB_OFINAL), 0);
-      }
+    if (!ok && lane == 0) fail();
+    if (any) {
+      // After every P.V, in a failed run too.
+      commit_by(one, bar(RB_OFINAL));
+      drain(bar(RB_OFINAL), 0);
     }
   } else {
     // ---------------------------------------------------------------- softmax

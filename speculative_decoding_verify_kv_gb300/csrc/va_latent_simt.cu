@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kLsThreads) latent_simt_kernel(const LatentPar
   const LatentSeq q = latent_seq(p, s);
   if (q.err & VA_DEV_BAD_ROWS) {
     if (tid == 0) flag(p.status, q.err);
-    if (blockIdx.x == 0) latent_nan_rows(p, s, PROMPT ? head : 0, PROMPT ? 1 : p.H);
+    if (blockIdx.x == 0) latent_nan_rows(p, s, PROMPT ? head : 0, PROMPT ? 1 : p.H, threadIdx.x, blockDim.x);
     return;
   }
   const int R = latent_rows(p, q.n);

@@ -1,20 +1,19 @@
-// Tensor-core attention over latent caches (absorbed form) and expanded prompt
-// keys, bf16: tcgen05 + TMEM + TMA, 128 query rows to a CTA.
+// Tensor-core attention over latent caches of 256 columns, bf16, more than 32 query
+// rows: tcgen05 + TMEM + TMA, 128 query rows to a CTA.
 //
-// Per tile of NT tokens:
-//   S = Q K^T     tcgen05.mma into one of two S buffers in TMEM
+// Per tile of 64 tokens:
+//   S = Q C^T     tcgen05.mma into one of two S buffers in TMEM
 //   softmax       eight warps, one TMEM lane (query row) per thread and half
 //                 of the tile's columns per warp; online (m, l) in log2 units,
 //                 O rescaled only when the maximum grows by more than 2^8; P
-//                 in bf16 (absorbed form: over S's place)
+//                 in bf16 over S's place
 //   O += P V      tcgen05.mma, A = P (TMEM), B = V tile (MN-major)
 // so that S of the next tile runs under this tile's softmax.
 //
-// Absorbed form (256 latent columns; 512 are va_latent_pair.cu's): a token has one
-// row of DK values and V is the first of them, so the column blocks of V are
-// loaded once and read by both products (as K they are K-major, as V MN-major:
-// the same bytes).  The queries of the V columns go to TMEM, those of the rope
-// part stay in shared memory.
+// A token has one row of 320 values and V is the first 256 of them, so the column
+// blocks of V are loaded once and read by both products (as K they are K-major, as
+// V MN-major: the same bytes).  The queries of the V columns go to TMEM, those of
+// the rope part stay in shared memory.
 //
 // Shared memory holds two rings of 64-column blocks of a tile: V stages of
 // VBLK blocks, freed by P.V, and single blocks of the key's other columns,
@@ -32,59 +31,45 @@ using namespace sm100;
 constexpr int kLuM = 128;
 constexpr int kLuThreads = 384;
 
-template <int DK_, int DV_, bool PROMPT_>
 struct LuCfg {
-  static constexpr int DK = DK_;                     // key width
-  static constexpr int DV = DV_;                     // value width
-  static constexpr bool PROMPT = PROMPT_;
-  static constexpr int DO = DV;                      // O columns
-  static constexpr int NT = PROMPT ? 128 : 64;       // tokens per tile
+  static constexpr int DV = 256, DK = DV + kLatentRope;
+  static constexpr int NT = 64;                      // tokens per tile
   static constexpr int BLK = NT * 128;               // bytes of a 64-column block
-  static constexpr int VBLK = DO / 64;               // blocks of a V stage
-  static constexpr int KBLK = PROMPT ? DK / 64 : DK / 64 - VBLK;  // other blocks of the key
-  static constexpr int QT = PROMPT ? 128 : DO;       // query columns in TMEM
+  static constexpr int VBLK = DV / 64;               // blocks of a V stage
+  static constexpr int KBLK = DK / 64 - VBLK;        // other blocks of the key
+  static constexpr int QT = DV;                      // query columns in TMEM
   static constexpr int QS = DK - QT;                 // query columns in shared memory
-  static constexpr int NV = PROMPT ? (DV == 128 ? 2 : 4) : 5;  // V stages
-  static constexpr int NK = PROMPT ? (DV == 128 ? 9 : 6) : 5;  // key blocks
+  static constexpr int NV = 5;                       // V stages
+  static constexpr int NK = 5;                       // key blocks
   static constexpr int COL_O = 0;
-  static constexpr int COL_S = DO;
-  // Prompts: P has columns of its own, so that S(i + 2) waits for S(i) to be read
-  // only, not for P(i) V (in S's place: 750 us against 714 for 2 x 2,048 rows of
-  // 128 heads over 4,096 keys).  The absorbed form has no columns left for it.
-  // (Values of 64 columns take less time for P V than for the wait before P is
-  // written: 668 us with, 633 without.)
-  static constexpr bool SEP = PROMPT && DV == 128;
-  static constexpr int COL_P = DO + 2 * NT;
-  static constexpr int COL_Q = COL_P + (SEP ? NT / 2 : 0);
+  static constexpr int COL_S = DV;
+  static constexpr int COL_Q = COL_S + 2 * NT;
   static constexpr int OFF_V = 0;
   static constexpr int OFF_K = NV * VBLK * BLK;
   static constexpr int OFF_Q = OFF_K + NK * BLK;
   static constexpr int OFF_END = OFF_Q + QS / 64 * kLuM * 128;
-  // The queries on their way to TMEM: in the last blocks of a ring.
-  static constexpr int QSTAGE = PROMPT ? OFF_Q - QT / 64 * kLuM * 128 : OFF_K - QT / 64 * kLuM * 128;
-  // First tile (V stage) or block (key ring) whose place they have.
-  static constexpr int QV_FIRST = PROMPT ? 1 << 30 : QSTAGE / (VBLK * BLK);
-  static constexpr int QK_FIRST = PROMPT ? (QSTAGE - OFF_K) / BLK : 1 << 30;
-  static constexpr int OROW = DO * 4 + 16;           // O staging at the end, padded rows
-  static constexpr int NB = 12 + 2 * NV + 2 * NK;    // barriers
+  // The queries on their way to TMEM: in the last V stages.
+  static constexpr int QSTAGE = OFF_K - QT / 64 * kLuM * 128;
+  static constexpr int QV_FIRST = QSTAGE / (VBLK * BLK);  // the first tile whose place they have
+  static constexpr int OROW = DV * 4 + 16;           // O staging at the end, padded rows
+  static constexpr int NB = 11 + 2 * NV + 2 * NK;    // barriers
   static constexpr int OFF_RED = OFF_END > kLuM * OROW ? OFF_END : kLuM * OROW;
   static constexpr int OFF_BAR = OFF_RED + 2 * 2 * kLuM * 4;
   static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
   static_assert(COL_Q + QT / 2 <= 512, "TMEM columns");
-  static_assert(QSTAGE >= (PROMPT ? OFF_K + KBLK * BLK : VBLK * BLK), "tile 0 beside the queries");
+  static_assert(QSTAGE >= VBLK * BLK, "tile 0 beside the queries");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-enum { LB_SFULL = 0, LB_PFULL = 2, LB_SFREE = 4, LB_QLAND = 6, LB_QREADY = 7, LB_OFINAL = 8, LB_FIX = 9, LB_SDRAIN = 10, LB_PFREE = 11, LB_RING = 12 };
+enum { LB_SFULL = 0, LB_PFULL = 2, LB_SFREE = 4, LB_QLAND = 6, LB_QREADY = 7, LB_OFINAL = 8, LB_FIX = 9, LB_SDRAIN = 10, LB_RING = 11 };
 
 struct LuMaps {
-  CUtensorMap q, k, r;  // queries; cache or expanded keys and values; rope part of prompt keys
+  CUtensorMap q, k;  // queries; cache
 };
 
-template <class C>
 __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const LatentParams p, const __grid_constant__ LuMaps maps) {
-  constexpr int NT = C::NT, NC = NT / 2, DO = C::DO;
-  constexpr bool PROMPT = C::PROMPT;
+  using C = LuCfg;
+  constexpr int NT = C::NT, NC = NT / 2, DV = C::DV;
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
   float* red = reinterpret_cast<float*>(sm + C::OFF_RED);  // [2][2][kLuM]
@@ -102,10 +87,9 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       *abort_p = 0;
       prefetch_map(&maps.q);
       prefetch_map(&maps.k);
-      if (PROMPT) prefetch_map(&maps.r);
     }
     for (int i = lane; i < C::NB; i += 32)
-      mbar_init(bar(i), (i >= LB_PFULL && i < LB_SFREE) || (C::SEP && i >= LB_SFREE && i < LB_QLAND) || i == LB_QREADY ? 8 : 1);
+      mbar_init(bar(i), (i >= LB_PFULL && i < LB_SFREE) || i == LB_QREADY ? 8 : 1);
     fence_barrier_init();
     __syncwarp();
   }
@@ -113,29 +97,27 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   // on the stream has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int s = blockIdx.z;
-  const int head = PROMPT ? blockIdx.y : 0;
   const LatentSeq q = latent_seq(p, s);
   if (q.err & VA_DEV_BAD_ROWS) {
     if (tid == 0) flag(p.status, q.err);
-    if (blockIdx.x == 0) latent_nan_rows(p, s, head, PROMPT ? 1 : p.H);
+    if (blockIdx.x == 0) latent_nan_rows(p, s, 0, p.H, tid, kLuThreads);
     return;
   }
   const int R = latent_rows(p, q.n);
   const int blocks = (R + kLuM - 1) / kLuM;
   if (blocks == 0) return;
   const int nchunk = latent_chunks(p, q.n);
-  const int rb = PROMPT ? blocks - 1 - blockIdx.x % blocks : blockIdx.x % blocks, chunk = blockIdx.x / blocks;
+  const int rb = blockIdx.x % blocks, chunk = blockIdx.x / blocks;
   const int live = latent_live(p, q.err ? 0 : q.len, nchunk);
   if (chunk >= live) return;
   const int rbase = rb * kLuM, nrows = min(kLuM, R - rbase);
-  const int jfirst = PROMPT ? rbase : rbase / p.H;
-  const int jlast = PROMPT ? rbase + nrows - 1 : (rbase + nrows - 1) / p.H;
+  const int jfirst = rbase / p.H, jlast = (rbase + nrows - 1) / p.H;
   int lo, hi;
   latent_range(p, q.len, nchunk, chunk, &lo, &hi);
   hi = max(lo, min(hi, latent_end(p, q, jlast)));
   const int ntiles = q.err ? 0 : (hi - lo + NT - 1) / NT;
   // Tokens below it are seen by every row of the block.
-  const int all_see = q.kind == 1 ? min(hi, q.ctx) : (PROMPT && !p.causal) ? hi : min(hi, q.ctx + jfirst + 1);
+  const int all_see = q.kind == 1 ? min(hi, q.ctx) : min(hi, q.ctx + jfirst + 1);
 
   auto vfull = [&](int i) { return bar(LB_RING + i); };
   auto vfree = [&](int i) { return bar(LB_RING + C::NV + i); };
@@ -143,8 +125,8 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   auto kfree = [&](int i) { return bar(LB_RING + 2 * C::NV + C::NK + i); };
   const uint32_t base = smem_u32(sm);
 
-  // Absorbed form, a producer's lane l < 4: (row, plane) of page l of the tile at
-  // t0, in the cache's map.
+  // A producer's lane l < 4: (row, plane) of page l of the tile at t0, in the
+  // cache's map.
   unsigned late = 0u;
   auto look_up = [&](int t0) {
     const int pg = t0 / kPage + lane;
@@ -160,17 +142,16 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   };
   // The first tile's are looked up beside the rest of the prologue.
   int blk0 = 0;
-  if (!PROMPT && (warp == 0 || warp == 10) && ntiles > 0) blk0 = look_up(lo);
+  if ((warp == 0 || warp == 10) && ntiles > 0) blk0 = look_up(lo);
   if (warp == 0 && ntiles > 0) {
     // The queries, at once: their barrier was set up by this warp.
     const uint32_t one = elected();
-    const int qrow = __shfl_sync(0xffffffffu, PROMPT ? q.row0 + rbase : q.row0 * p.H + rbase, 0);
+    const int qrow = __shfl_sync(0xffffffffu, q.row0 * p.H + rbase, 0);
     expect_by(one, bar(LB_QLAND), C::DK / 64 * kLuM * 128);
 #pragma unroll
     for (int c = 0; c < C::DK / 64; ++c) {
       const uint32_t dst = base + (c < C::QT / 64 ? C::QSTAGE + c * kLuM * 128 : C::OFF_Q + (c - C::QT / 64) * kLuM * 128);
-      if (PROMPT) tma_3d_by(one, dst, &maps.q, c * 64, head, qrow, bar(LB_QLAND));
-      else tma_2d_by(one, dst, &maps.q, c * 64, qrow, bar(LB_QLAND));
+      tma_2d_by(one, dst, &maps.q, c * 64, qrow, bar(LB_QLAND));
     }
   }
   if (warp == 1) {
@@ -181,7 +162,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   const int r = quad * 32 + lane;
   const bool is_sm = warp >= 2 && warp < 10;
   const bool rvalid = is_sm && r < nrows;
-  const int j = rvalid ? (PROMPT ? rbase + r : (rbase + r) / p.H) : 0;
+  const int j = rvalid ? (rbase + r) / p.H : 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -209,44 +190,35 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   } else if (warp == 0 || warp == 10) {
     // ---------------------------------------------------------------- producers
     // Warp 10: the V stages.  Warp 0: the key's other blocks.
-    // Absorbed form: lane l < 4 looks the tile's page l up.
+    // Lane l < 4 looks the tile's page l up.
     const bool keys = warp == 0;
     const uint32_t one = elected();
     const int lo_u = __shfl_sync(0xffffffffu, lo, 0), hi_u = __shfl_sync(0xffffffffu, hi, 0);
-    const int key0 = __shfl_sync(0xffffffffu, (int)q.key0, 0);
     bool ok = true;
     int issued = 0;  // tiles (V) or blocks (keys)
     int st = 0;
     uint32_t par = 1;
     for (int i = 0; i < work && ok; ++i) {
       const int t0 = lo_u + i * NT;
-      const int pages = PROMPT ? 0 : (min(NT, hi_u - t0) + kPage - 1) / kPage;
+      const int pages = (min(NT, hi_u - t0) + kPage - 1) / kPage;
       int2 at[4];
-      if (!PROMPT) {
-        const int2 a = page_at(t0, i == 0 ? blk0 : look_up(t0));
-        if (late) found(late);  // before anything of the tile is loaded
-        __syncwarp();
+      const int2 a = page_at(t0, i == 0 ? blk0 : look_up(t0));
+      if (late) found(late);  // before anything of the tile is loaded
+      __syncwarp();
 #pragma unroll
-        for (int g = 0; g < 4; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, g), __shfl_sync(0xffffffffu, a.y, g));
-      }
+      for (int g = 0; g < 4; ++g) at[g] = make_int2(__shfl_sync(0xffffffffu, a.x, g), __shfl_sync(0xffffffffu, a.y, g));
       if (!keys) {
         ok = (i != C::QV_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLatentWaitNs)) && mbar_wait(vfree(st), par, abort_p, kLatentWaitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint32_t dst = base + C::OFF_V + st * C::VBLK * C::BLK, b = vfull(st);
-        if (PROMPT) {
-          expect_by(one, b, C::VBLK * C::BLK);
+        expect_by(one, b, (uint32_t)(C::VBLK * pages * kPage * 128));
 #pragma unroll
-          for (int c = 0; c < C::VBLK; ++c) tma_3d_by(one, dst + c * C::BLK, &maps.k, C::DK - kLatentRope + c * 64, head, key0 + t0, b);
-        } else {
-          expect_by(one, b, (uint32_t)(C::VBLK * pages * kPage * 128));
+        for (int g = 0; g < 4; ++g) {
+          if (g >= pages) break;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            if (g >= pages) break;
-#pragma unroll
-            for (int c = 0; c < C::VBLK; ++c)
-              tma_3d_by(one, dst + c * C::BLK + g * kPage * 128, &maps.k, c * 64, at[g].x, at[g].y, b);
-          }
+          for (int c = 0; c < C::VBLK; ++c)
+            tma_3d_by(one, dst + c * C::BLK + g * kPage * 128, &maps.k, c * 64, at[g].x, at[g].y, b);
         }
         issued = i + 1;
         if (++st == C::NV) st = 0, par ^= 1;
@@ -254,23 +226,15 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
 #pragma unroll
         for (int c = 0; c < C::KBLK; ++c) {
           const int n = i * C::KBLK + c;
-          ok = ok && (n != C::QK_FIRST || mbar_wait(bar(LB_QREADY), 0, abort_p, kLatentWaitNs)) &&
-               mbar_wait(kfree(st), par, abort_p, kLatentWaitNs);
-          ok = __all_sync(0xffffffffu, ok);
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(kfree(st), par, abort_p, kLatentWaitNs));
           if (!ok) break;
           const uint32_t dst = base + C::OFF_K + st * C::BLK, b = kfull(st);
-          if (PROMPT) {
-            expect_by(one, b, C::BLK);
-            if (c == C::KBLK - 1) tma_2d_by(one, dst, &maps.r, 0, key0 + t0, b);
-            else tma_3d_by(one, dst, &maps.k, c * 64, head, key0 + t0, b);
-          } else {
-            const int col = (c + C::VBLK) * 64;
-            expect_by(one, b, (uint32_t)(pages * kPage * 128));
+          const int col = (c + C::VBLK) * 64;
+          expect_by(one, b, (uint32_t)(pages * kPage * 128));
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              if (g >= pages) break;
-              tma_3d_by(one, dst + g * kPage * 128, &maps.k, col, at[g].x, at[g].y, b);
-            }
+          for (int g = 0; g < 4; ++g) {
+            if (g >= pages) break;
+            tma_3d_by(one, dst + g * kPage * 128, &maps.k, col, at[g].x, at[g].y, b);
           }
           issued = n + 1;
           if (++st == C::NK) st = 0, par ^= 1;
@@ -311,15 +275,14 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     uint32_t pv = 0, pk = 0;                // their parities
     const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, 16, 1024), kd0 = sdesc_sw128(base + C::OFF_K, 16, 1024);
     const uint64_t qd0 = sdesc_sw128(base + C::OFF_Q, 16, 1024);
-    // What a tile starts with: its S buffer free, and its V stage (absorbed form)
-    // or first key block there.
+    // What a tile starts with: its S buffer free, and its V stage there.
     auto peek_tile = [&](int i) {
       return (i < 2 || mbar_peek(bar(LB_SFREE + (i & 1)), ((i - 2) >> 1) & 1)) &&
-             (PROMPT ? mbar_peek(kfull(sk), pk) : mbar_peek(vfull(st), pv));
+             mbar_peek(vfull(st), pv);
     };
     auto wait_tile = [&](int i) {
       return (i < 2 || mbar_wait(bar(LB_SFREE + (i & 1)), ((i - 2) >> 1) & 1, abort_p, kLatentWaitNs)) &&
-             (PROMPT ? mbar_wait(kfull(sk), pk, abort_p, kLatentWaitNs) : mbar_wait(vfull(st), pv, abort_p, kLatentWaitNs));
+             mbar_wait(vfull(st), pv, abort_p, kLatentWaitNs);
     };
     bool there = false;
     for (int i = 0; i < work && ok; ++i) {
@@ -328,50 +291,41 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       ok = __all_sync(0xffffffffu, there || wait_tile(i));
       if (!ok) break;
       tc_fence_after();
-      if (!PROMPT) {
-        there = mbar_peek(kfull(sk), pk);
-        const uint64_t kd = vd0 + (uint64_t)((st * C::VBLK * C::BLK) >> 4);
+      there = mbar_peek(kfull(sk), pk);
+      const uint64_t kv = vd0 + (uint64_t)((st * C::VBLK * C::BLK) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < C::VBLK * 4; ++kk)
-          mma_ts_by(one, scol, tm + C::COL_Q + kk * 8, kd + (uint64_t)(((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4), ID,
-                    kk > 0 ? 1u : 0u);
-        any = true;
-        if (++st == C::NV) st = 0, pv ^= 1;
-      }
+      for (int kk = 0; kk < C::VBLK * 4; ++kk)
+        mma_ts_by(one, scol, tm + C::COL_Q + kk * 8, kv + (uint64_t)(((kk >> 2) * C::BLK + (kk & 3) * 32) >> 4), ID,
+                  kk > 0 ? 1u : 0u);
+      any = true;
+      if (++st == C::NV) st = 0, pv ^= 1;
 #pragma unroll
       for (int c = 0; c < C::KBLK; ++c) {
-        if (!PROMPT || c > 0) {
-          ok = __all_sync(0xffffffffu, there || mbar_wait(kfull(sk), pk, abort_p, kLatentWaitNs));
-          if (!ok) break;
-          tc_fence_after();
-        }
+        ok = __all_sync(0xffffffffu, there || mbar_wait(kfull(sk), pk, abort_p, kLatentWaitNs));
+        if (!ok) break;
+        tc_fence_after();
         const uint64_t kd = kd0 + (uint64_t)((sk * C::BLK) >> 4);
         const uint32_t free = kfree(sk);
         if (++sk == C::NK) sk = 0, pk ^= 1;
         there = c + 1 < C::KBLK ? mbar_peek(kfull(sk), pk) : i + 1 < work && peek_tile(i + 1);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          constexpr int IN_TMEM = PROMPT ? C::QT / 64 : 0;  // of the key blocks' query columns
-          if (c < IN_TMEM) mma_ts_by(one, scol, tm + C::COL_Q + (c * 4 + kk) * 8, kd + kk * 2, ID, c > 0 || kk > 0 ? 1u : 0u);
-          else mma_ss_by(one, scol, qd0 + (uint64_t)(((c - IN_TMEM) * kLuM * 128) >> 4) + kk * 2, kd + kk * 2, ID, 1u);
-        }
-        any = true;
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ss_by(one, scol, qd0 + (uint64_t)((c * kLuM * 128) >> 4) + kk * 2, kd + kk * 2, ID, 1u);
         commit_by(one, free);
       }
       if (!ok) break;
       commit_by(one, bar(LB_SFULL + b));
     }
-    if (!ok && lane == 0) {
-      fail();
-      // What was issued completes before TMEM and shared memory go.
-      if (any) {
-        mma_commit(bar(LB_SDRAIN));
-        drain(bar(LB_SDRAIN), 0);
-      }
+    if (!ok && lane == 0) fail();
+    if (!ok && any) {
+      // What was issued completes before TMEM and shared memory go.  (A commit is
+      // for what its own thread has issued.)
+      commit_by(one, bar(LB_SDRAIN));
+      drain(bar(LB_SDRAIN), 0);
     }
   } else if (warp == 11) {
     // ---------------------------------------------------------------- P.V issuer
-    constexpr uint32_t ID = idesc_f16(kLuM, DO, true, true);
+    constexpr uint32_t ID = idesc_f16(kLuM, DV, true, true);
     const uint32_t one = elected();
     bool ok = true, any = false;
     int st = 0;
@@ -388,20 +342,18 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       const uint64_t vd = vd0 + (uint64_t)((st * C::VBLK * C::BLK) >> 4);
 #pragma unroll
       for (int kk = 0; kk < NT / 16; ++kk)
-        mma_ts_by(one, tm + C::COL_O, tm + (C::SEP ? C::COL_P : C::COL_S + b * NT) + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), ID,
+        mma_ts_by(one, tm + C::COL_O, tm + C::COL_S + b * NT + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), ID,
                   i > 0 || kk > 0 ? 1u : 0u);
       any = true;
-      commit_by(one, bar(C::SEP ? LB_PFREE : LB_SFREE + b));
+      commit_by(one, bar(LB_SFREE + b));
       commit_by(one, vfree(st));
       if (++st == C::NV) st = 0, pv ^= 1;
     }
-    if (lane == 0) {
-      if (!ok) fail();
-      if (any) {
-        // After every P.V, in a failed run too.
-        mma_commit(bar(LB_OFINAL));
-        drain(bar(LB_OFINAL), 0);
-      }
+    if (!ok && lane == 0) fail();
+    if (any) {
+      // After every P.V, in a failed run too.
+      commit_by(one, bar(LB_OFINAL));
+      drain(bar(LB_OFINAL), 0);
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -455,7 +407,6 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       if (ok && warp_live) {
         uint32_t sr[NC];
         tmem_ld32_into<0>(scol + NC * half, sr);
-        if constexpr (NC > 32) tmem_ld32_into<NC - 32>(scol + NC * half + 32, sr);
         tmem_wait_ld();
         if (lo + (i + 1) * NT <= all_see) {
           float m2 = -INFINITY;
@@ -468,29 +419,15 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
 #pragma unroll
           for (int c = 0; c < NC; ++c) sv[c] = __uint_as_float(sr[c]);
         } else {
+          static_assert(NC == 32, "a word of bits");
+          const unsigned vis = rvalid ? latent_bits(p, q, anc, j, hi, t0) : 0u;
 #pragma unroll
-          for (int w = 0; w < NC / 32; ++w) {
-            const unsigned vis = rvalid ? latent_bits(p, q, anc, j, hi, t0 + 32 * w) : 0u;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              sv[32 * w + c] = (vis >> c) & 1u ? __uint_as_float(sr[32 * w + c]) : -INFINITY;
-              mx = fmaxf(mx, sv[32 * w + c]);
-            }
+          for (int c = 0; c < NC; ++c) {
+            sv[c] = (vis >> c) & 1u ? __uint_as_float(sr[c]) : -INFINITY;
+            mx = fmaxf(mx, sv[c]);
           }
         }
       }
-      if (C::SEP) {
-        // S(i) is in registers: its buffer may be written again.
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(LB_SFREE + b));
-      }
-      // The previous P.V: it has to be done before O is rescaled, or (SEP) P
-      // written.
-      auto pv_done = [&]() {
-        return i < 1 || (C::SEP ? mbar_wait(bar(LB_PFREE), (i - 1) & 1, abort_p, kLatentWaitNs)
-                                : mbar_wait(bar(LB_SFREE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_p, kLatentWaitNs));
-      };
       // The row's maximum over both halves (raw scores; c_r > 0).
       red[(b * 2 + half) * kLuM + r] = mx;
       bar_sync(5 + quad, 64);
@@ -500,12 +437,12 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       const float m_new = m_use == -INFINITY || need ? mt : m_use;
       if (ok && __any_sync(0xffffffffu, need)) {
         // Rescale this half of the warp's O rows once the previous P.V landed.
-        if (!__all_sync(0xffffffffu, pv_done())) ok = false;
+        if (i > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(LB_SFREE + (b ^ 1)), ((i - 1) >> 1) & 1, abort_p, kLatentWaitNs))) ok = false;
         if (ok) {
           tc_fence_after();
           const float f = need ? exp2f(m_use - m_new) : 1.f;
 #pragma unroll 1
-          for (int c0 = half * (DO / 2); c0 < (half + 1) * (DO / 2); c0 += 16) {
+          for (int c0 = half * (DV / 2); c0 < (half + 1) * (DV / 2); c0 += 16) {
             uint32_t o[16];
             tmem_ld16(tm + lanes + C::COL_O + c0, o);
             tmem_wait_ld();
@@ -542,11 +479,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
         float l0, l1;
         unpack2(l2, l0, l1);
         l_run += l0 + l1;
-        const uint32_t pcol = C::SEP ? tm + lanes + C::COL_P : scol;
-        if (C::SEP && !__all_sync(0xffffffffu, pv_done())) ok = false;
-        if (C::SEP) tc_fence_after();
-        if constexpr (NC == 32) tmem_st16(pcol + 16 * half, ph);
-        else tmem_st32_from<0>(pcol + 32 * half, ph);
+        tmem_st16(scol + 16 * half, ph);
         tmem_wait_st();
       }
       tc_fence_before();
@@ -562,7 +495,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     const bool bad = __any_sync(0xffffffffu, *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0);
     const float inv = bad ? NAN : l != 0.f ? 1.f / l : 0.f;
     if (rvalid && half == 0) {
-      const long long item = latent_item(p, q.row0, rbase + r, head);
+      const long long item = latent_item(p, q.row0, rbase + r, 0);
       if (live > 1) {
         const long long si = latent_slot(p, chunk, item);
         p.ws_ml[2 * si] = bad ? NAN : m_use;
@@ -575,7 +508,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     // stores; fp32 sums for the merge, or the finished bf16 row.
     if (warp_live) {
 #pragma unroll 1
-      for (int c0 = half * (DO / 2); c0 < (half + 1) * (DO / 2); c0 += 32) {
+      for (int c0 = half * (DV / 2); c0 < (half + 1) * (DV / 2); c0 += 32) {
         uint32_t o[32];
         tmem_ld32(tm + lanes + C::COL_O + c0, o);
         tmem_wait_ld();
@@ -604,30 +537,29 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       }
     }
     bar_sync(1, 256);
-    // Row r of the block is row first + r step of [total_rows][H].
-    const long long first = latent_item(p, q.row0, rbase, head), step = PROMPT ? p.H : 1;
+    const long long first = latent_item(p, q.row0, rbase, 0);
     if (live > 1) {
-      constexpr int PIECES = DO / 4;  // of 16 bytes
-      float* to = p.ws_acc + latent_slot(p, chunk, first) * C::DV;
+      constexpr int PIECES = DV / 4;  // of 16 bytes
+      float* to = p.ws_acc + latent_slot(p, chunk, first) * DV;
       for (int u = tid - 64; u < nrows * PIECES; u += 256) {
         const int row = u / PIECES, c = u % PIECES;
-        *reinterpret_cast<uint4*>(to + row * step * C::DV + c * 4) = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
+        *reinterpret_cast<uint4*>(to + row * DV + c * 4) = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
       }
     } else {
-      constexpr int PIECES = DO / 8;
-      unsigned short* to = reinterpret_cast<unsigned short*>(p.o) + first * C::DV;
+      constexpr int PIECES = DV / 8;
+      unsigned short* to = reinterpret_cast<unsigned short*>(p.o) + first * DV;
       for (int u = tid - 64; u < nrows * PIECES; u += 256) {
         const int row = u / PIECES, c = u % PIECES;
-        *reinterpret_cast<uint4*>(to + row * step * C::DV + c * 8) = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
+        *reinterpret_cast<uint4*>(to + row * DV + c * 8) = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
       }
     }
   }
 
   if (work == 0) {
     // An error, a chunk that the block's rows see nothing of, or no keys.
-    for (int u = tid; u < nrows * DO; u += kLuThreads) {
-      const int row = u / DO, d = u % DO;
-      const long long item = latent_item(p, q.row0, rbase + row, head);
+    for (int u = tid; u < nrows * DV; u += kLuThreads) {
+      const int row = u / DV, d = u % DV;
+      const long long item = latent_item(p, q.row0, rbase + row, 0);
       if (live > 1) {
         if (d == 0) {
           const long long si = latent_slot(p, chunk, item);
@@ -635,7 +567,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
           p.ws_ml[2 * si + 1] = q.err ? NAN : 0.f;
         }
       } else {
-        reinterpret_cast<unsigned short*>(p.o)[item * C::DV + d] = q.err ? 0x7fffu : 0u;
+        reinterpret_cast<unsigned short*>(p.o)[item * DV + d] = q.err ? 0x7fffu : 0u;
         if (d == 0) p.lse[item] = q.err ? NAN : -INFINITY;
       }
     }
@@ -647,49 +579,28 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
 }
 
 // ---------------------------------------------------------------------------
-static bool lu_maps(LuMaps* m, const LatentParams& p, int tile) {
-  memset(m, 0, sizeof(*m));
-  const cuuint64_t dk = (cuuint64_t)p.DK, H = (cuuint64_t)p.H;
-  if (!p.prompt) return latent_query_map(&m->q, p, kLuM) && latent_cache_map(&m->k, p);
-  const cuuint64_t qd[3] = {dk, H, (cuuint64_t)p.total_rows}, qs[2] = {dk * 2, H * dk * 2};
-  const cuuint32_t qb[3] = {64, 1, kLuM}, kb[3] = {64, 1, (cuuint32_t)tile}, rb[2] = {64, (cuuint32_t)tile};
-  if (!latent_map(&m->q, p.q, 3, qd, qs, qb)) return false;
-  if (p.total_kv == 0) return true;  // no tile, no load
-  const cuuint64_t w = dk - kLatentRope + (cuuint64_t)p.DV, T = (cuuint64_t)p.total_kv;
-  const cuuint64_t kd[3] = {w, H, T}, ks[2] = {w * 2, H * w * 2};
-  const cuuint64_t rd[2] = {kLatentRope, T}, rs[1] = {(cuuint64_t)(T > 1 ? p.kr_stride : kLatentRope) * 2};
-  return latent_map(&m->k, p.kv, 3, kd, ks, kb) && latent_map(&m->r, p.k_rope, 2, rd, rs, rb);
-}
-
-template <class C>
-static cudaError_t launch_umma_latent(const LatentParams& p, dim3 grid, cudaStream_t st) {
+cudaError_t launch_latent_umma(const LatentParams& p, dim3 grid, cudaStream_t st) {
   static std::atomic<unsigned long long> ready{0ull};
-  cudaError_t e = allow_smem(latent_umma_kernel<C>, C::SMEM, ready);
+  cudaError_t e = allow_smem(latent_umma_kernel, LuCfg::SMEM, ready);
   if (e != cudaSuccess) return e;
   LuMaps m;
-  if (!lu_maps(&m, p, C::NT)) return cudaErrorInvalidValue;
+  memset(&m, 0, sizeof(m));
+  if (!latent_query_map(&m.q, p, kLuM) || !latent_cache_map(&m.k, p)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kLuThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = LuCfg::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, latent_umma_kernel<C>, p, m);
+  e = cudaLaunchKernelEx(&cfg, latent_umma_kernel, p, m);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 int latent_umma_rows() { return kLuM; }
-
-cudaError_t launch_latent_umma(const LatentParams& p, dim3 grid, cudaStream_t st) {
-  if (p.prompt)
-    return p.DV == 128 ? launch_umma_latent<LuCfg<192, 128, true>>(p, grid, st)
-                       : launch_umma_latent<LuCfg<128, 64, true>>(p, grid, st);
-  return launch_umma_latent<LuCfg<320, 256, false>>(p, grid, st);
-}
 
 }  // namespace va

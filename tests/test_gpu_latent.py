@@ -210,6 +210,30 @@ def test_prompt_long():
     run_check(Prompt("bf16", 2, 128, [700, 1025], [1700, 1025], seed=3))
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("causal,splits", [(True, 1), (True, 6), (False, 1), (False, 3)])
+def test_prompt_many_blocks(dim, causal, splits):
+    """Several row blocks to a CTA one after the other, among them some without rows
+    or keys, ragged and whole tiles; the same again, whichever CTA takes a block."""
+    case = Prompt("bf16", 70, dim, [300, 0, 1, 130, 128, 5], [420, 60, 1, 130, 384, 0], seed=dim, causal=causal, splits=splits)
+    first = [t.clone() for t in case.run()]
+    for _ in range(3):
+        again = case.run()
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    run_check(case)
+
+
+def test_prompt_many_blocks_findings():
+    """A sequence with bad offsets among many blocks."""
+    case = Prompt("bf16", 70, 128, [200, 140, 256], [300, 150, 600], seed=4)
+    want = case.oracle()
+    case.kv.cu_kv[2] = -3        # the end of the second sequence, the start of the third
+    o, lse = case.run()
+    assert case.status.item() == va.DEV_BAD_ROWS
+    assert o[200:].isnan().all() and lse[200:].isnan().all()
+    check((o[:200], lse[:200]), tuple(x[:200] for x in want), "bf16")
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_prompt_parts_join(kind):
     """A context part and the segment itself, joined by their lse, are the whole."""
