@@ -178,6 +178,11 @@ __device__ __forceinline__ void tma_3d_by(uint32_t e, uint32_t dst, const CUtens
         : "memory");
 }
 
+// Zeros in rows from .. to - 1 of a 64-column block, by a warp.
+__device__ __forceinline__ void clear_rows(unsigned char* block, int from, int to, int lane) {
+  for (int x = from * 128 + lane * 16; x < to * 128; x += 512) *reinterpret_cast<uint4*>(block + x) = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // ---------------------------------------------------------------------------
 // Tiled map of bf16 rows in boxes of 64 columns, 128-byte swizzle.
 inline bool latent_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,

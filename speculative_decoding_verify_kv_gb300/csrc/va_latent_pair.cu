@@ -270,15 +270,12 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
     if (values && ok && ragged) {
       // Tokens behind the range may hold anything: their V is cleared (their
       // scores are masked).
-      const int valid = max(0, min(kLpTile / 2, hi - lo - (work - 1) * kLpTile - who * (kLpTile / 2))), rows = kLpTile / 2 - valid;
+      const int valid = max(0, min(kLpTile / 2, hi - lo - (work - 1) * kLpTile - who * (kLpTile / 2)));
       bool there = true;
       for (int u = who; u < C::VU; u += 2) there = there && mbar_wait(bar(PB_VLAST + u), 0, abort_p, kLatentWaitNs);
       if (__all_sync(0xffffffffu, there)) {
-        for (int x = lane; x < C::VU / 2 * C::VG * rows * 8; x += 32) {
-          const int blk = x / (rows * 8), u = blk / C::VG * 2 + who;
-          *reinterpret_cast<uint4*>(sm + C::OFF_V + (u * C::VG + blk % C::VG) * C::VB + (valid + x / 8 % rows) * 128 + (x & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int u = who; u < C::VU; u += 2)
+          for (int k = 0; k < C::VG; ++k) clear_rows(sm + C::OFF_V + (u * C::VG + k) * C::VB, valid, kLpTile / 2, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) arrive_first(PB_FIX);

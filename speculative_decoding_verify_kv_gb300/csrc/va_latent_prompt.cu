@@ -11,8 +11,9 @@
 //
 // A CTA takes one block after the other: the one it was launched for, then blocks
 // whose launch it takes over (clusterlaunchcontrol), asked for one ahead.  The
-// roles go through the blocks by themselves, so that loads and S of the next run
-// under the last softmax, P V and store of this one.
+// warp that loads the keys finds out what a block is and tells the others, which
+// go through the blocks by themselves: loads and S of the next run under the last
+// softmax, P V and store of this one.
 //
 // Shared memory holds two rings of 64-column blocks of a tile: V stages of VBLK
 // blocks, freed by P V, and single key blocks, freed as soon as S has read them.
@@ -29,14 +30,25 @@ namespace va {
 using namespace sm100;
 
 constexpr int kLqM = 128;
+constexpr int kLqTile = 128;
 constexpr int kLqThreads = 384;
 constexpr int kLqWarps = kLqThreads / 32;
+
+// One block of rows over one chunk of keys.  work: its tiles; 0: none of its rows
+// sees a key; kLqSkip: no rows; kLqBad: offsets that make no sense; kLqEnd: no more.
+enum { kLqSkip = -1, kLqBad = -2, kLqEnd = -3 };
+struct LqItem {
+  int row0, rbase, nrows, head;
+  int chunk, live, ctx, lo;
+  int hi, all_see, work, key0;
+  int s, first;
+};
 
 template <int DK_, int DV_>
 struct LqCfg {
   static constexpr int DK = DK_;                     // key width
   static constexpr int DV = DV_;                     // value width
-  static constexpr int NT = 128;                     // tokens per tile
+  static constexpr int NT = kLqTile;                 // tokens per tile
   static constexpr int BLK = NT * 128;               // bytes of a 64-column block
   static constexpr int VBLK = DV / 64;               // blocks of a V stage
   static constexpr int KBLK = DK / 64;               // blocks of a key tile
@@ -59,8 +71,10 @@ struct LqCfg {
   static constexpr int OFF_Q = OFF_K + NK * BLK;
   static constexpr int OFF_RED = OFF_Q + QS / 64 * BLK;  // float [2][2][kLqM]
   static constexpr int OFF_NEXT = OFF_RED + 2 * 2 * kLqM * 4;
-  static constexpr int NB = 18 + 2 * NV + 2 * NK;    // barriers
-  static constexpr int OFF_BAR = OFF_NEXT + 2 * 16;
+  static constexpr int OFF_ITEM = OFF_NEXT + 16;     // the block at work and the next
+  static constexpr int NB = 19 + 2 * NV + 2 * NK;    // barriers
+  static constexpr int OFF_MINE = OFF_ITEM + 2 * (int)sizeof(LqItem);  // of each softmax warp
+  static constexpr int OFF_BAR = OFF_MINE + 8 * (int)sizeof(LqItem);
   static constexpr int SMEM = OFF_BAR + NB * 8 + 16;
   static_assert(BLK == kLqM * 128, "a query block in a key block's place");
   static_assert(COL_Q + QT / 2 <= 512, "TMEM columns");
@@ -68,18 +82,15 @@ struct LqCfg {
 };
 
 enum { QB_SFULL = 0, QB_PFULL = 2, QB_SFREE = 4, QB_QLAND = 6, QB_QREADY = 7, QB_QFREE = 8, QB_OFINAL = 9, QB_FIX = 10, QB_PFREE = 11,
-       QB_SDRAIN = 12, QB_ODRAIN = 13, QB_NEXT = 14, QB_TAKEN = 16, QB_RING = 18 };
+       QB_SDRAIN = 12, QB_ODRAIN = 13, QB_NEXT = 14, QB_TOLD = 15, QB_TAKEN = 17, QB_RING = 19 };
 
 struct LqMaps {
   CUtensorMap q, k, r;  // queries; expanded keys and values; rope part of the keys
 };
 
-// One block of rows over one chunk of keys.
-struct LqItem {
-  int row0, rbase, nrows, head, chunk, live;
-  int ctx, lo, hi, all_see, work;
-  int key0;
-};
+__device__ __forceinline__ void bar_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
 
 // Asks for a block that has not been launched yet: 16 bytes, which the barrier counts.
 __device__ __forceinline__ void ask_next(uint32_t dst, uint32_t bar) {
@@ -102,8 +113,135 @@ __device__ __forceinline__ bool read_next(uint32_t src, int* x, int* y, int* z) 
   return ok != 0u;
 }
 
+// Four pieces of four words in each of four lanes: lane i gets piece i of each.
+__device__ __forceinline__ void deal4(uint32_t (&w)[16], int lane) {
+#pragma unroll
+  for (int d = 1; d < 4; d *= 2) {
+    const bool high = lane & d;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a & d) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t &x = w[4 * a + k], &y = w[4 * (a | d) + k];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? x : y, d);
+        if (high) x = got;
+        else y = got;
+      }
+    }
+  }
+}
+
+// What the block (bx, head, s) of the grid is.
+__device__ __forceinline__ void find_item(const LatentParams& p, int bx, int head, int s, LqItem* it) {
+  const LatentSeq q = latent_seq(p, s);
+  it->work = q.err ? kLqBad : kLqSkip;
+  it->s = s, it->head = head, it->first = bx == 0;
+  const int blocks = (q.n + kLqM - 1) / kLqM;
+  if (q.err || blocks == 0) return;
+  const int nchunk = latent_chunks(p, q.n);
+  // A head's longest row blocks first: a few short ones end the launch (2 x 2,048
+  // rows, 128 heads: 721 us in order, 714 so).
+  const int rb = blocks - 1 - bx % blocks, chunk = bx / blocks;
+  it->live = latent_live(p, q.len, nchunk);
+  if (chunk >= it->live) return;
+  it->chunk = chunk;
+  it->row0 = q.row0, it->rbase = rb * kLqM, it->nrows = min(kLqM, q.n - it->rbase);
+  it->ctx = q.ctx, it->key0 = (int)q.key0;
+  int lo, hi;
+  latent_range(p, q.len, nchunk, chunk, &lo, &hi);
+  hi = max(lo, min(hi, latent_end(p, q, it->rbase + it->nrows - 1)));
+  it->lo = lo, it->hi = hi;
+  it->work = (hi - lo + kLqTile - 1) / kLqTile;
+  // Keys below it are seen by every row of the block.
+  it->all_see = p.causal ? min(hi, q.ctx + it->rbase + 1) : hi;
+}
+
+// What a block without work has of outputs, by thread t of 256.  (Not inlined: it
+// is rare, and its divisions cost the loop over the tiles registers.)
+template <int DV>
+__device__ __noinline__ void no_work(const LatentParams& p, const LqItem& it, int t) {
+  if (it.work == kLqBad) {
+    if (t == 0) flag(p.status, VA_DEV_BAD_ROWS);
+    if (it.first) latent_nan_rows(p, it.s, it.head, 1, t, 256);
+  } else if (it.work == 0) {
+    // A chunk that the block's rows see nothing of, or no keys.
+    for (int u = t; u < it.nrows * DV; u += 256) {
+      const long long i = latent_item(p, it.row0, it.rbase + u / DV, it.head);
+      const int d = u % DV;
+      if (it.live > 1) {
+        if (d == 0) {
+          const long long si = latent_slot(p, it.chunk, i);
+          p.ws_ml[2 * si] = -INFINITY;
+          p.ws_ml[2 * si + 1] = 0.f;
+        }
+      } else {
+        reinterpret_cast<unsigned short*>(p.o)[i * DV + d] = 0u;
+        if (d == 0) p.lse[i] = -INFINITY;
+      }
+    }
+  }
+}
+
+// A finished block's rows: row r (TMEM lane), half of O's columns.
+//
+// O: fp32 sums for the merge, or the finished bf16 row.  Four lanes exchange their
+// rows' 16-byte pieces, so that a store writes 64 bytes of a row, not 16.
+template <int DV>
+__device__ __forceinline__ void store_rows(const LatentParams& p, const LqItem& was, uint32_t col, int r, int half, float m_use, float l, bool bad) {
+  const int lane = threadIdx.x & 31;
+  const float inv = bad ? NAN : l != 0.f ? 1.f / l : 0.f;
+  const long long at = latent_item(p, was.row0, was.rbase + r, was.head);
+  const long long slot = latent_slot(p, was.chunk, at);
+  if (r < was.nrows && half == 0) {
+    if (was.live > 1) {
+      p.ws_ml[2 * slot] = bad ? NAN : m_use;
+      p.ws_ml[2 * slot + 1] = bad ? NAN : l;
+    } else {
+      p.lse[at] = bad ? NAN : l != 0.f ? (m_use + log2f(l)) * kLn2 : -INFINITY;
+    }
+  }
+  const long long at4 = __shfl_sync(0xffffffffu, was.live > 1 ? slot : at, lane & 28), step4 = p.H;
+  const int left4 = was.nrows - (r & ~3);  // rows of the four lanes
+  if (r - lane >= was.nrows) return;
+#pragma unroll 1
+  for (int c0 = half * (DV / 2); c0 < (half + 1) * (DV / 2); c0 += 32) {
+    uint32_t o[32];
+    tmem_ld32(col + c0, o);
+    tmem_wait_ld();
+    if (was.live > 1) {
+      float* to = p.ws_acc + at4 * DV + c0 + (lane & 3) * 4;
+#pragma unroll
+      for (int c = 0; c < 32; c += 16) {
+        uint32_t w[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[k] = bad ? 0x7fffffffu : o[c + k];
+        deal4(w, lane);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (t < left4) *reinterpret_cast<uint4*>(to + t * step4 * DV + c) = make_uint4(w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]);
+      }
+    } else {
+      uint32_t w[16];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        // A row that sees nothing has no sum (its lanes of O may hold anything).
+        const __nv_bfloat162 h = l != 0.f || bad ? __floats2bfloat162_rn(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv)
+                                                : __floats2bfloat162_rn(0.f, 0.f);
+        w[c] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      deal4(w, lane);
+      unsigned short* to = reinterpret_cast<unsigned short*>(p.o) + at4 * DV + c0 + (lane & 3) * 8;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (t < left4) *reinterpret_cast<uint4*>(to + t * step4 * DV) = make_uint4(w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]);
+    }
+  }
+}
+
 template <class C>
-__global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const LatentParams p, const __grid_constant__ LqMaps maps) {
+__global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const __grid_constant__ LatentParams p,
+                                                                      const __grid_constant__ LqMaps maps) {
   constexpr int NT = C::NT, NC = NT / 2, DV = C::DV;
   extern __shared__ __align__(1024) unsigned char sm[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::OFF_BAR);
@@ -123,7 +261,7 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
       prefetch_map(&maps.r);
     }
     for (int i = lane; i < C::NB; i += 32)
-      mbar_init(bar(i), (i >= QB_TAKEN && i < QB_RING) ? kLqWarps
+      mbar_init(bar(i), (i >= QB_TAKEN && i < QB_RING) ? kLqWarps - 1
                         : (i >= QB_PFULL && i < QB_SFREE) || (C::SEP && i >= QB_SFREE && i < QB_QLAND) || i == QB_QREADY ? 8 : 1);
     fence_barrier_init();
     __syncwarp();
@@ -136,9 +274,11 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  // The barriers' and TMEM's set-up.  Warp 0 needs nothing of it but its own.
+  if (warp == 0) bar_arrive(2, kLqThreads);
+  else bar_sync(2, kLqThreads);
   tc_fence_after();
-  const uint32_t tm = __shfl_sync(0xffffffffu, *tmem_at, 0);
+  const uint32_t tm = warp == 0 ? 0u : __shfl_sync(0xffffffffu, *tmem_at, 0);
 
   auto vfull = [&](int i) { return bar(QB_RING + i); };
   auto vfree = [&](int i) { return bar(QB_RING + C::NV + i); };
@@ -154,103 +294,63 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
     return mbar_wait(b, parity, &dummy, kLatentWaitNs);
   };
 
-  // A warp's way through the CTA's blocks.  asked: blocks taken over so far.
-  const uint32_t next_at = base + C::OFF_NEXT;
-  int bx = blockIdx.x, head = blockIdx.y, s = blockIdx.z, asked = 0;
-  auto ask = [&]() {  // warp 0: block asked + 1, into the place of the one before
-    const int n = asked & 1;
-    if (asked >= 2 && !drain(bar(QB_TAKEN + n), ((asked >> 1) - 1) & 1) && lane == 0) fail();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar(QB_NEXT + n), 16);
-      ask_next(next_at + n * 16, bar(QB_NEXT + n));
-    }
-    __syncwarp();
-  };
-  auto step = [&]() {
-    const int n = asked & 1;
-    if (!__all_sync(0xffffffffu, drain(bar(QB_NEXT + n), (asked >> 1) & 1))) {
-      if (lane == 0) fail();
-      return false;
-    }
-    int x, y, z;
-    const bool more = read_next(next_at + n * 16, &x, &y, &z);
-    fence_proxy_async_smem();  // the place will be written again
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(QB_TAKEN + n));
-    bx = __shfl_sync(0xffffffffu, x, 0), head = __shfl_sync(0xffffffffu, y, 0), s = __shfl_sync(0xffffffffu, z, 0);
-    ++asked;
-    return __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
-  };
-  // The block (bx, head, s): false where there are no rows, or rows without keys;
-  // of those one role (outputs) writes what they have.
-  auto item = [&](LqItem* it, bool outputs) {
-    const LatentSeq q = latent_seq(p, s);
-    if (q.err) {
-      if (outputs) {
-        if (tid == 64) flag(p.status, q.err);
-        if (bx == 0) latent_nan_rows(p, s, head, 1, tid - 64, 256);
+  // A warp's way through the CTA's blocks: the next that the first warp tells of.
+  // Those without work are the outputs' (empty) matter.
+  LqItem* items_s = reinterpret_cast<LqItem*>(sm + C::OFF_ITEM);
+  int told = 0;
+  auto next_item = [&](LqItem* it, auto empty) {
+    for (;;) {
+      const int n = told & 1;
+      if (!__all_sync(0xffffffffu, drain(bar(QB_TOLD + n), (told >> 1) & 1))) {
+        if (lane == 0) fail();
+        return false;
       }
-      return false;
+      const int work = __shfl_sync(0xffffffffu, items_s[n].work, 0);
+      if (work > 0) *it = items_s[n];
+      else empty(items_s[n]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(QB_TAKEN + n));
+      ++told;
+      if (work == kLqEnd) return false;
+      if (work > 0) break;
     }
-    const int blocks = (q.n + kLqM - 1) / kLqM;
-    if (blocks == 0) return false;
-    const int nchunk = latent_chunks(p, q.n);
-    // A head's longest row blocks first: a few short ones end the launch (2 x 2,048
-    // rows, 128 heads: 721 us in order, 714 so).
-    const int rb = blocks - 1 - bx % blocks, chunk = bx / blocks;
-    const int live = latent_live(p, q.len, nchunk);
-    if (chunk >= live) return false;
-    const int rbase = rb * kLqM, nrows = min(kLqM, q.n - rbase);
-    int lo, hi;
-    latent_range(p, q.len, nchunk, chunk, &lo, &hi);
-    hi = max(lo, min(hi, latent_end(p, q, rbase + nrows - 1)));
-    auto same = [&](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-    it->row0 = same(q.row0), it->rbase = same(rbase), it->nrows = same(nrows);
-    it->head = head, it->chunk = same(chunk), it->live = same(live);
-    it->ctx = same(q.ctx), it->lo = same(lo), it->hi = same(hi), it->key0 = same((int)q.key0);
-    it->work = same((hi - lo + NT - 1) / NT);
-    // Keys below it are seen by every row of the block.
-    it->all_see = same(p.causal ? min(hi, q.ctx + rbase + 1) : hi);
-    if (it->work > 0) return true;
-    if (outputs) {
-      // A chunk that the block's rows see nothing of, or no keys.
-      for (int u = tid - 64; u < nrows * DV; u += 256) {
-        const long long i = latent_item(p, q.row0, rbase + u / DV, head);
-        const int d = u % DV;
-        if (live > 1) {
-          if (d == 0) {
-            const long long si = latent_slot(p, chunk, i);
-            p.ws_ml[2 * si] = -INFINITY;
-            p.ws_ml[2 * si + 1] = 0.f;
-          }
-        } else {
-          reinterpret_cast<unsigned short*>(p.o)[i * DV + d] = 0u;
-          if (d == 0) p.lse[i] = -INFINITY;
-        }
-      }
-    }
-    return false;
+    // What a warp has in common is known to be so.
+    auto same = [&](int& v) { v = __shfl_sync(0xffffffffu, v, 0); };
+    same(it->row0), same(it->rbase), same(it->nrows), same(it->head), same(it->chunk), same(it->live);
+    same(it->ctx), same(it->lo), same(it->hi), same(it->all_see), same(it->work), same(it->key0);
+    return true;
   };
+  auto nothing = [](const LqItem&) {};
 
   if (warp == 0) {
     // ---------------------------------------------------------------- keys, queries
     const uint32_t one = elected();
-    bool ok = true, more = true;
-    int issued = 0, asks = 0, items = 0;  // blocks of the ring; requests; blocks with work
-    int st = 0;
+    bool ok = true;
+    int issued = 0, items = 0;  // blocks of the ring; row blocks with work
+    int st = 0, bx = blockIdx.x, head = blockIdx.y, s = blockIdx.z;
     uint32_t par = 1;
-    while (more) {
-      ask(), ++asks;
+    for (bool more = true; more; ++told) {
       LqItem it;
-      if (item(&it, false) && ok) {
+      const int n = told & 1;
+      find_item(p, bx, head, s, &it);
+      it.work = __shfl_sync(0xffffffffu, it.work, 0), it.lo = __shfl_sync(0xffffffffu, it.lo, 0), it.key0 = __shfl_sync(0xffffffffu, it.key0, 0);
+      it.row0 = __shfl_sync(0xffffffffu, it.row0, 0), it.rbase = __shfl_sync(0xffffffffu, it.rbase, 0);
+      if (told >= 2 && !__all_sync(0xffffffffu, drain(bar(QB_TAKEN + n), ((told >> 1) - 1) & 1)) && lane == 0) fail();
+      if (lane == 0) {
+        items_s[n] = it;
+        mbar_arrive(bar(QB_TOLD + n));
+        mbar_arrive_expect_tx(bar(QB_NEXT), 16);
+        ask_next(base + C::OFF_NEXT, bar(QB_NEXT));
+      }
+      __syncwarp();
+      if (it.work > 0 && ok) {
         if (C::QS > 0) {
           ok = __all_sync(0xffffffffu, items == 0 || mbar_wait(bar(QB_QFREE), (items - 1) & 1, abort_p, kLatentWaitNs));
           if (ok) {
             expect_by(one, bar(QB_QLAND), C::QS / 64 * C::BLK);
 #pragma unroll
             for (int c = C::QBLK; c < C::KBLK; ++c)
-              tma_3d_by(one, base + C::OFF_Q + (c - C::QBLK) * C::BLK, &maps.q, c * 64, it.head, it.row0 + it.rbase, bar(QB_QLAND));
+              tma_3d_by(one, base + C::OFF_Q + (c - C::QBLK) * C::BLK, &maps.q, c * 64, head, it.row0 + it.rbase, bar(QB_QLAND));
           }
         }
         if (ok) ++items;
@@ -263,32 +363,45 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
             if (!ok) break;
             const uint32_t dst = base + C::OFF_K + st * C::BLK, b = kfull(st);
             expect_by(one, b, C::BLK);
-            if (i < 0) tma_3d_by(one, dst, &maps.q, c * 64, it.head, it.row0 + it.rbase, b);
+            if (i < 0) tma_3d_by(one, dst, &maps.q, c * 64, head, it.row0 + it.rbase, b);
             else if (c == C::KBLK - 1) tma_2d_by(one, dst, &maps.r, 0, key, b);
-            else tma_3d_by(one, dst, &maps.k, c * 64, it.head, key, b);
+            else tma_3d_by(one, dst, &maps.k, c * 64, head, key, b);
             ++issued;
             if (++st == C::NK) st = 0, par ^= 1;
           }
         }
         if (!ok && lane == 0) fail();
       }
-      more = step();
+      more = __all_sync(0xffffffffu, drain(bar(QB_NEXT), told & 1));
+      if (!more && lane == 0) fail();
+      if (more) {
+        int x, y, z;
+        more = read_next(base + C::OFF_NEXT, &x, &y, &z);
+        fence_proxy_async_smem();  // the place will be written again
+        __syncwarp();
+        more = __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
+        bx = __shfl_sync(0xffffffffu, x, 0), head = __shfl_sync(0xffffffffu, y, 0), s = __shfl_sync(0xffffffffu, z, 0);
+      }
+    }
+    const int n = told & 1;
+    if (told >= 2 && !__all_sync(0xffffffffu, drain(bar(QB_TAKEN + n), ((told >> 1) - 1) & 1)) && lane == 0) fail();
+    if (lane == 0) {
+      items_s[n].work = kLqEnd;
+      mbar_arrive(bar(QB_TOLD + n));
     }
     // No copy may still be landing when the CTA goes away.
     if (*abort_p && lane == 0) {
-      if (asks > asked) drain(bar(QB_NEXT + (asked & 1)), (asked >> 1) & 1);
       if (C::QS > 0 && items > 0) drain(bar(QB_QLAND), (items - 1) & 1);
       for (int i = max(0, issued - C::NK); i < issued; ++i) drain(kfull(i % C::NK), (i / C::NK) & 1);
     }
   } else if (warp == 10) {
     // ---------------------------------------------------------------- values
     const uint32_t one = elected();
-    bool ok = true, more = true;
+    bool ok = true;
     int issued = 0, st = 0, fixed = -1;  // stages; the last one cleared
     uint32_t par = 1;
-    while (more) {
-      LqItem it;
-      if (item(&it, false) && ok) {
+    for (LqItem it; next_item(&it, nothing);) {
+      if (ok) {
         for (int i = 0; i < it.work; ++i) {
           ok = __all_sync(0xffffffffu, mbar_wait(vfree(st), par, abort_p, kLatentWaitNs));
           if (!ok) break;
@@ -300,8 +413,8 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
           ++issued;
           if (++st == C::NV) st = 0, par ^= 1;
         }
-        const int valid = it.hi - it.lo - (it.work - 1) * NT, rows = NT - valid;
-        if (ok && rows > 0) {
+        const int valid = it.hi - it.lo - (it.work - 1) * NT;
+        if (ok && valid < NT) {
           // Keys behind the range may hold anything: their V is cleared (their
           // scores are masked).
           const int last = (issued - 1) % C::NV;
@@ -313,10 +426,7 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
           fixed = issued - 1;
           ok = __all_sync(0xffffffffu, ok);
           if (ok) {
-            unsigned char* at = sm + C::OFF_V + last * C::VBLK * C::BLK;
-            for (int u = lane; u < C::VBLK * rows * 8; u += 32)
-              *reinterpret_cast<uint4*>(at + u / (rows * 8) * C::BLK + (valid + u / 8 % rows) * 128 + (u & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
+            for (int c = 0; c < C::VBLK; ++c) clear_rows(sm + C::OFF_V + (last * C::VBLK + c) * C::BLK, valid, NT, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(QB_FIX));
@@ -324,7 +434,6 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
         }
         if (!ok && lane == 0) fail();
       }
-      more = step();
     }
     if (*abort_p && lane == 0)
       for (int i = max(0, issued - C::NV); i < issued; ++i) drain(vfull(i % C::NV), (i / C::NV) & 1);
@@ -332,13 +441,12 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
     // ---------------------------------------------------------------- S issuer
     constexpr uint32_t ID = idesc_f16(kLqM, NT, true, false);
     const uint32_t one = elected();
-    bool ok = true, more = true, any = false;
+    bool ok = true, any = false;
     int sk = 0, items = 0, g = 0;  // key block, blocks with work, tiles
     uint32_t pk = 0;               // its parity
     const uint64_t kd0 = sdesc_sw128(base + C::OFF_K, 16, 1024), qd0 = sdesc_sw128(base + C::OFF_Q, 16, 1024);
-    while (more) {
-      LqItem it;
-      if (item(&it, false) && ok) {
+    for (LqItem it; next_item(&it, nothing);) {
+      if (ok) {
         ok = (C::QS == 0 || mbar_wait(bar(QB_QLAND), items & 1, abort_p, kLatentWaitNs)) &&
              mbar_wait(bar(QB_QREADY), items & 1, abort_p, kLatentWaitNs);
         ok = __all_sync(0xffffffffu, ok);
@@ -388,7 +496,6 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
         if (ok) commit_by(one, bar(QB_QFREE));
         else if (lane == 0) fail();
       }
-      more = step();
     }
     // What was issued completes before TMEM and shared memory go.
     if (any) {
@@ -399,13 +506,12 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
     // ---------------------------------------------------------------- P.V issuer
     constexpr uint32_t ID = idesc_f16(kLqM, DV, true, true);
     const uint32_t one = elected();
-    bool ok = true, more = true, any = false;
+    bool ok = true, any = false;
     int st = 0, g = 0, fixes = 0;  // V stage, tiles, ragged blocks
     uint32_t pv = 0;
     const uint64_t vd0 = sdesc_sw128(base + C::OFF_V, C::BLK, 1024);
-    while (more) {
-      LqItem it;
-      if (item(&it, false) && ok) {
+    for (LqItem it; next_item(&it, nothing);) {
+      if (ok) {
         const bool ragged = (it.hi - it.lo) % NT != 0;  // of the last tile
         for (int i = 0; i < it.work; ++i, ++g) {
           const int b = g & 1;
@@ -428,7 +534,6 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
         if (ok) commit_by(one, bar(QB_OFINAL));
         else if (lane == 0) fail();
       }
-      more = step();
     }
     if (any) {
       commit_by(one, bar(QB_ODRAIN));
@@ -444,10 +549,8 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
     int sk = 0, g = 0, items = 0;  // key block, tiles, blocks with work
     uint32_t pk = 0;
     // The next block with work, its queries on the way to TMEM.
-    auto advance = [&](LqItem* it, bool first) {
-      bool more = first || step();
-      while (more && !item(it, true)) more = step();
-      if (!more) return false;
+    auto advance = [&](LqItem* it) {
+      if (!next_item(it, [&](const LqItem& e) { no_work<DV>(p, e, tid - 64); })) return false;
       // Both halves: 16-byte pieces of a swizzled block each.  (Rows behind the
       // block's last hold other rows, or zeros: no one reads what comes of them.)
       static_assert(C::QBLK == 2, "a block to a half");
@@ -479,7 +582,15 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
     };
 
     LqItem it;
-    bool have = advance(&it, true);
+    bool have = advance(&it);
+    // What a block's rows are is kept in shared memory while the tiles are at work.
+    LqItem* mine = reinterpret_cast<LqItem*>(sm + C::OFF_MINE) + (warp - 2);
+    auto keep = [&]() {
+      __syncwarp();
+      if (lane == 0) mine->row0 = it.row0, mine->rbase = it.rbase, mine->nrows = it.nrows, mine->head = it.head, mine->chunk = it.chunk, mine->live = it.live;
+      __syncwarp();
+    };
+    keep();
     while (have) {
       const bool rvalid = r < it.nrows, warp_live = quad * 32 < it.nrows;
       // Keys below it are seen by this row.
@@ -597,8 +708,7 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
 
       // S has read this block's queries: the next one's, before this one's store.
       // (Every S of the block was waited for.)
-      const LqItem was = it;
-      have = advance(&it, false);
+      have = advance(&it);
       if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(QB_OFINAL), items & 1, abort_p, kLatentWaitNs))) ok = false;
       ++items;
       if (!ok && lane == 0) fail();
@@ -609,48 +719,8 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const Late
       const float l = lsum[r] + lsum[kLqM + r];
       bar_sync(5 + quad, 64);  // the next block's first tile writes there
       const bool bad = __any_sync(0xffffffffu, !ok || *abort_p != 0);
-      const float inv = bad ? NAN : l != 0.f ? 1.f / l : 0.f;
-      const long long at = latent_item(p, was.row0, was.rbase + r, was.head);
-      const long long slot = latent_slot(p, was.chunk, at);
-      if (rvalid && half == 0) {
-        if (was.live > 1) {
-          p.ws_ml[2 * slot] = bad ? NAN : m_use;
-          p.ws_ml[2 * slot + 1] = bad ? NAN : l;
-        } else {
-          p.lse[at] = bad ? NAN : l != 0.f ? (m_use + log2f(l)) * kLn2 : -INFINITY;
-        }
-      }
-      // O: fp32 sums for the merge, or the finished bf16 row.  A thread stores its
-      // half row itself, in whole sectors.
-      if (warp_live) {
-#pragma unroll 1
-        for (int c0 = half * (DV / 2); c0 < (half + 1) * (DV / 2); c0 += 32) {
-          uint32_t o[32];
-          tmem_ld32(tm + lanes + C::COL_O + c0, o);
-          tmem_wait_ld();
-          if (!rvalid) {
-            // not a row of the block
-          } else if (was.live > 1) {
-            uint4* to = reinterpret_cast<uint4*>(p.ws_acc + slot * DV + c0);
-#pragma unroll
-            for (int c = 0; c < 32; c += 4)
-              to[c / 4] = bad ? make_uint4(0x7fffffffu, 0x7fffffffu, 0x7fffffffu, 0x7fffffffu) : make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-          } else {
-            uint32_t w[16];
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              // A row that sees nothing has no sum (its lanes of O may hold anything).
-              const __nv_bfloat162 h = l != 0.f || bad ? __floats2bfloat162_rn(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv)
-                                                      : __floats2bfloat162_rn(0.f, 0.f);
-              w[c] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            uint4* to = reinterpret_cast<uint4*>(reinterpret_cast<unsigned short*>(p.o) + at * DV + c0);
-#pragma unroll
-            for (int c = 0; c < 16; c += 4) to[c / 4] = make_uint4(w[c], w[c + 1], w[c + 2], w[c + 3]);
-          }
-          __syncwarp();
-        }
-      }
+      store_rows<DV>(p, *mine, tm + lanes + C::COL_O, r, half, m_use, l, bad);
+      keep();
     }
   }
 

@@ -245,12 +245,9 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     if (!keys && ok && ragged) {
       // Tokens behind the range may hold anything: their V is cleared (their
       // scores are masked).
-      const int i = work - 1, st = i % C::NV, valid = hi - lo - i * NT, rows = NT - valid;
+      const int i = work - 1, st = i % C::NV, valid = hi - lo - i * NT;
       if (__all_sync(0xffffffffu, mbar_wait(vfull(st), (i / C::NV) & 1, abort_p, kLatentWaitNs))) {
-        unsigned char* at = sm + C::OFF_V + st * C::VBLK * C::BLK;
-        for (int u = lane; u < C::VBLK * rows * 8; u += 32)
-          *reinterpret_cast<uint4*>(at + u / (rows * 8) * C::BLK + (valid + u / 8 % rows) * 128 + (u & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < C::VBLK; ++c) clear_rows(sm + C::OFF_V + (st * C::VBLK + c) * C::BLK, valid, NT, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(LB_FIX));
