@@ -4,8 +4,8 @@
 // Absorbed form: a sequence's n rows x H heads are one run of query rows (row
 // j, head h at j H + h) over the one cache row that a token has.  Prompts:
 // a head's n rows, over that head's keys; blockIdx.y is the head.  Either
-// way a CTA takes one block of query rows and one chunk of the sequence's
-// tokens.
+// way a block of the grid is one block of query rows and one chunk of the
+// sequence's tokens.
 #pragma once
 
 #include "va_common.cuh"
