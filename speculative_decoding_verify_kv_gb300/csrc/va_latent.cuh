@@ -5,7 +5,7 @@
 // j, head h at j H + h) over the one cache row that a token has.  Prompts:
 // a head's n rows, over that head's keys; blockIdx.y is the head.  Either
 // way a block of the grid is one block of query rows and one chunk of the
-// sequence's tokens.
+// sequence's tokens; blockIdx.z is the sequence (tensor-core prompts: in x).
 #pragma once
 
 #include "va_common.cuh"

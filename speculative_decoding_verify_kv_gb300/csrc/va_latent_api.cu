@@ -107,6 +107,12 @@ static LatentPlan plan_rows(const va_problem* p, int dtype, int value_dim, bool 
   // A sequence of b row blocks has b max(1, slots / b) CTAs per key head.
   pl.grid = dim3((unsigned)(blocks > pl.slots ? blocks : pl.slots), (unsigned)(prompt ? p->num_heads : 1),
                  (unsigned)p->num_seqs);
+  if (prompt && pl.kernel == VA_KERNEL_TENSOR) {
+    // All sequences' blocks in a row; a sequence of b takes at most b + slots - 1.
+    const long long most = (long long)pl.grid.x * p->num_seqs;
+    const long long rows_most = p->total_rows / pl.rows_per_block + (long long)p->num_seqs * pl.slots;
+    pl.grid = dim3((unsigned)(most < rows_most ? most : rows_most), (unsigned)p->num_heads, 1u);
+  }
   if (pl.slots > 1) {
     const size_t items = (size_t)pl.slots * (size_t)p->total_rows * (size_t)p->num_heads;
     pl.acc_bytes = up256(items * (size_t)value_dim * 4);

@@ -98,18 +98,18 @@ __device__ __forceinline__ void ask_next(uint32_t dst, uint32_t bar) {
                : "memory");
 }
 // The answer: false if there is none left.
-__device__ __forceinline__ bool read_next(uint32_t src, int* x, int* y, int* z) {
-  uint32_t ok, a = 0u, b = 0u, c = 0u;
+__device__ __forceinline__ bool read_next(uint32_t src, int* x, int* y) {
+  uint32_t ok, a = 0u, b = 0u;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
-      "ld.shared.b128 h, [%4];\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t.reg .b32 z;\n\t"
+      "ld.shared.b128 h, [%3];\n\t"
       "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, h;\n\t}"
-      : "=r"(ok), "+r"(a), "+r"(b), "+r"(c)
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, z, _}, h;\n\t}"
+      : "=&r"(ok), "+r"(a), "+r"(b)
       : "r"(src)
       : "memory");
-  *x = (int)a, *y = (int)b, *z = (int)c;
+  *x = (int)a, *y = (int)b;
   return ok != 0u;
 }
 
@@ -132,29 +132,63 @@ __device__ __forceinline__ void deal4(uint32_t (&w)[16], int lane) {
   }
 }
 
-// What the block (bx, head, s) of the grid is.
-__device__ __forceinline__ void find_item(const LatentParams& p, int bx, int head, int s, LqItem* it) {
-  const LatentSeq q = latent_seq(p, s);
-  it->work = q.err ? kLqBad : kLqSkip;
-  it->s = s, it->head = head, it->first = bx == 0;
-  const int blocks = (q.n + kLqM - 1) / kLqM;
-  if (q.err || blocks == 0) return;
-  const int nchunk = latent_chunks(p, q.n);
-  // A head's longest row blocks first: a few short ones end the launch (2 x 2,048
-  // rows, 128 heads: 721 us in order, 714 so).
-  const int rb = blocks - 1 - bx % blocks, chunk = bx / blocks;
-  it->live = latent_live(p, q.len, nchunk);
-  if (chunk >= it->live) return;
-  it->chunk = chunk;
-  it->row0 = q.row0, it->rbase = rb * kLqM, it->nrows = min(kLqM, q.n - it->rbase);
-  it->ctx = q.ctx, it->key0 = (int)q.key0;
-  int lo, hi;
-  latent_range(p, q.len, nchunk, chunk, &lo, &hi);
-  hi = max(lo, min(hi, latent_end(p, q, it->rbase + it->nrows - 1)));
-  it->lo = lo, it->hi = hi;
-  it->work = (hi - lo + kLqTile - 1) / kLqTile;
-  // Keys below it are seen by every row of the block.
-  it->all_see = p.causal ? min(hi, q.ctx + it->rbase + 1) : hi;
+// What block x of a head is, found by a warp that goes through the sequences 32 at a
+// time; false behind the last.  The grid has as many blocks as the rows can have at
+// most, not as many a sequence as the longest may have, since one that is nothing
+// costs 0.8 us (15 sequences of 256 rows, 128 heads, where 4,096 rows a sequence are
+// allowed: 449 us by sequence, 142 so).  base, start: where the search stands, and
+// the blocks before it.
+__device__ __forceinline__ bool find_item(const LatentParams& p, int x, int* base, int* start, int lane, LqItem* it) {
+  it->work = kLqSkip;
+  if (x < *start) *base = *start = 0;
+  for (; *base < p.num_seqs; *base += 32) {
+    LatentSeq q;
+    int b = 0;  // blocks of the lane's sequence; a bad one has one, that says so
+    q.err = 0u, q.row0 = q.n = q.ctx = q.len = 0, q.key0 = 0;
+    if (*base + lane < p.num_seqs) {
+      q = latent_seq(p, *base + lane);
+      b = q.err ? 1 : (q.n + kLqM - 1) / kLqM * latent_chunks(p, q.n);
+    }
+    int upto = b;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    const int all = __shfl_sync(0xffffffffu, upto, 31);
+    if (x - *start >= all) {
+      *start += all;
+      continue;
+    }
+    const int at = __ffs(__ballot_sync(0xffffffffu, upto > x - *start)) - 1;
+    auto its = [&](int v) { return __shfl_sync(0xffffffffu, v, at); };
+    const int place = x - *start - its(upto - b);
+    q.err = (unsigned)its((int)q.err);
+    q.row0 = its(q.row0), q.n = its(q.n), q.ctx = its(q.ctx), q.len = its(q.len), q.kind = 0;
+    it->s = *base + at, it->first = place == 0, it->key0 = its((int)q.key0);
+    if (q.err) {
+      it->work = kLqBad;
+      return true;
+    }
+    const int blocks = (q.n + kLqM - 1) / kLqM, nchunk = latent_chunks(p, q.n);
+    // A head's longest row blocks first: a few short ones end the launch (2 x 2,048
+    // rows, 128 heads: 721 us in order, 714 so).
+    const int rb = blocks - 1 - place % blocks, chunk = place / blocks;
+    it->live = latent_live(p, q.len, nchunk);
+    if (chunk >= it->live) return true;
+    it->chunk = chunk;
+    it->row0 = q.row0, it->rbase = rb * kLqM, it->nrows = min(kLqM, q.n - it->rbase);
+    it->ctx = q.ctx;
+    int lo, hi;
+    latent_range(p, q.len, nchunk, chunk, &lo, &hi);
+    hi = max(lo, min(hi, latent_end(p, q, it->rbase + it->nrows - 1)));
+    it->lo = lo, it->hi = hi;
+    it->work = (hi - lo + kLqTile - 1) / kLqTile;
+    // Keys below it are seen by every row of the block.
+    it->all_see = p.causal ? min(hi, q.ctx + it->rbase + 1) : hi;
+    return true;
+  }
+  return false;
 }
 
 // What a block without work has of outputs, by thread t of 256.  (Not inlined: it
@@ -327,20 +361,26 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const __gr
     const uint32_t one = elected();
     bool ok = true;
     int issued = 0, items = 0;  // blocks of the ring; row blocks with work
-    int st = 0, bx = blockIdx.x, head = blockIdx.y, s = blockIdx.z;
+    int st = 0, x = blockIdx.x, head = blockIdx.y, base_s = 0, start = 0, asks = 0;
     uint32_t par = 1;
     for (bool more = true; more; ++told) {
       LqItem it;
       const int n = told & 1;
-      find_item(p, bx, head, s, &it);
+      const bool there = find_item(p, x, &base_s, &start, lane, &it);
+      // Sequences of bad offsets may leave more blocks than the grid has: the last
+      // block goes on with those.
+      const bool on = __shfl_sync(0xffffffffu, there && x >= (int)gridDim.x - 1 ? 1 : 0, 0) != 0;
+      it.head = head;
       it.work = __shfl_sync(0xffffffffu, it.work, 0), it.lo = __shfl_sync(0xffffffffu, it.lo, 0), it.key0 = __shfl_sync(0xffffffffu, it.key0, 0);
       it.row0 = __shfl_sync(0xffffffffu, it.row0, 0), it.rbase = __shfl_sync(0xffffffffu, it.rbase, 0);
       if (told >= 2 && !__all_sync(0xffffffffu, drain(bar(QB_TAKEN + n), ((told >> 1) - 1) & 1)) && lane == 0) fail();
       if (lane == 0) {
         items_s[n] = it;
         mbar_arrive(bar(QB_TOLD + n));
-        mbar_arrive_expect_tx(bar(QB_NEXT), 16);
-        ask_next(base + C::OFF_NEXT, bar(QB_NEXT));
+        if (!on) {
+          mbar_arrive_expect_tx(bar(QB_NEXT), 16);
+          ask_next(base + C::OFF_NEXT, bar(QB_NEXT));
+        }
       }
       __syncwarp();
       if (it.work > 0 && ok) {
@@ -372,15 +412,19 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const __gr
         }
         if (!ok && lane == 0) fail();
       }
-      more = __all_sync(0xffffffffu, drain(bar(QB_NEXT), told & 1));
+      if (on) {
+        ++x;
+        continue;
+      }
+      more = __all_sync(0xffffffffu, drain(bar(QB_NEXT), asks & 1));
+      ++asks;
       if (!more && lane == 0) fail();
       if (more) {
-        int x, y, z;
-        more = read_next(base + C::OFF_NEXT, &x, &y, &z);
+        more = read_next(base + C::OFF_NEXT, &x, &head);
         fence_proxy_async_smem();  // the place will be written again
         __syncwarp();
         more = __shfl_sync(0xffffffffu, more ? 1 : 0, 0) != 0;
-        bx = __shfl_sync(0xffffffffu, x, 0), head = __shfl_sync(0xffffffffu, y, 0), s = __shfl_sync(0xffffffffu, z, 0);
+        x = __shfl_sync(0xffffffffu, x, 0), head = __shfl_sync(0xffffffffu, head, 0);
       }
     }
     const int n = told & 1;

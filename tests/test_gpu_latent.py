@@ -223,6 +223,38 @@ def test_prompt_many_blocks(dim, causal, splits):
     run_check(case)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_prompt_many_sequences(kind, splits):
+    """More sequences than a warp looks at at once, most far below the bound, one bad."""
+    rows = [(7 * s) % 5 if s % 11 else 140 for s in range(77)]
+    keys = [r + s % 3 for s, r in enumerate(rows)]
+    case = Prompt(kind, 3, 64, rows, keys, seed=5, splits=splits)
+    want = case.oracle()
+    case.p.max_rows_per_seq = 1000
+    run_check(case)
+    case.p.max_rows_per_seq = 139
+    o, lse = case.run()
+    assert case.status.item() == va.DEV_BAD_ROWS
+    ok = torch.ones(len(lse), dtype=torch.bool)
+    for s in range(0, 77, 11):
+        ok[case.cu[s]:case.cu[s + 1]] = False
+    assert o[~ok].isnan().all() and lse[~ok].isnan().all()
+    check((o[ok], lse[ok]), tuple(x[ok.numpy()] for x in want), kind)
+
+
+def test_prompt_more_blocks_than_rows_have():
+    """Offsets that go back and forth: more blocks than a launch of that many rows has
+    otherwise, every second sequence bad and without rows."""
+    case = Prompt("bf16", 2, 128, [300], [300], seed=6)
+    want = case.oracle()
+    p = va.Problem(**{**vars(case.p), "num_seqs": 41, "cu_rows": torch.tensor([0, 300] * 21, dtype=torch.int32, device="cuda")})
+    kv = va.PromptKV(**{**vars(case.kv), "cu_kv": torch.tensor([0, 300] * 21, dtype=torch.int32, device="cuda")})
+    got = va.verify_attn_latent_prompt(p, kv, status=case.status)
+    assert case.status.item() == va.DEV_BAD_ROWS
+    check(got, want, "bf16")
+
+
 def test_prompt_many_blocks_findings():
     """A sequence with bad offsets among many blocks."""
     case = Prompt("bf16", 70, 128, [200, 140, 256], [300, 150, 600], seed=4)
