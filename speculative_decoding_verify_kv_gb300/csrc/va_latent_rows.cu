@@ -409,9 +409,10 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
         over = over || z[n] > 8.f;
       }
       if (any_of_four_warps(2, over)) {
-        // New references: the rows' largest scores of this tile.
+        // New references: the rows' largest scores of this tile.  (Masked is -inf alone:
+        // a score that is no number stays one, and the maximum passes it over.)
 #pragma unroll
-        for (int n = 0; n < N; ++n) z[n] = z[n] > -INFINITY ? __uint_as_float(sr[n]) * c_r : -INFINITY;
+        for (int n = 0; n < N; ++n) z[n] = z[n] == -INFINITY ? -INFINITY : __uint_as_float(sr[n]) * c_r;
         const float top = combine_lanes<N, 16>(z, lane, [](float x, float y) { return fmaxf(x, y); });
         w_s[quad * N + lane / (32 / N)] = top;
         bar_sync(3, 128);
