@@ -134,7 +134,6 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
     fence_barrier_init();
     __syncwarp();
   }
-  if (tid < N) m_s[tid] = -INFINITY;
   // Nothing but this CTA's own shared memory is touched before the work ahead
   // on the stream has completed.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -148,6 +147,9 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
   const int R = q.n * p.H;
   const int live = latent_live(p, q.err ? 0 : q.len, latent_chunks(p, q.n));
   if (R == 0 || chunk >= live) return;
+  // Columns behind the sequence's rows hold what stands there in memory (other
+  // sequences' queries): a reference that no score exceeds, so that they move none.
+  if (tid < N) m_s[tid] = tid < R ? -INFINITY : INFINITY;
   int lo, hi;
   latent_range(p, q.len, latent_chunks(p, q.n), chunk, &lo, &hi);
   const int ntiles = q.err ? 0 : (hi - lo + kLrTile - 1) / kLrTile;
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
 #pragma unroll
     for (int n = 0; n < N; ++n) {
       l[n] = 0.f;
-      nm[n] = kUnseen;
+      nm[n] = n < R ? kUnseen : -INFINITY;
     }
     if (th < N) {
       const int j = th < R ? th / p.H : 0;
@@ -411,9 +413,10 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       if (any_of_four_warps(2, over)) {
         // New references: the rows' largest scores of this tile.  (Masked is -inf alone:
         // a score that is no number stays one, and the maximum passes it over.)
+        float x[N];
 #pragma unroll
-        for (int n = 0; n < N; ++n) z[n] = z[n] == -INFINITY ? -INFINITY : __uint_as_float(sr[n]) * c_r;
-        const float top = combine_lanes<N, 16>(z, lane, [](float x, float y) { return fmaxf(x, y); });
+        for (int n = 0; n < N; ++n) x[n] = z[n] == -INFINITY ? -INFINITY : __uint_as_float(sr[n]) * c_r;
+        const float top = combine_lanes<N, 16>(x, lane, [](float x, float y) { return fmaxf(x, y); });
         w_s[quad * N + lane / (32 / N)] = top;
         bar_sync(3, 128);
         if (th < N) {
@@ -442,7 +445,9 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
         for (int n = 0; n < N; ++n) {
           l[n] *= f_s[n];
           nm[n] = m_s[n] == -INFINITY ? kUnseen : -m_s[n];
-          z[n] += nm[n];
+          // Rounded as in every other tile: a row whose reference stays has the same
+          // weights whichever row made the tile come here.
+          z[n] = z[n] == -INFINITY ? -INFINITY : fmaf(__uint_as_float(sr[n]), c_r, nm[n]);
         }
       }
       if (ok && !__all_sync(0xffffffffu, free || mbar_wait(bar(RB_PFREE + b), ((i - 2) >> 1) & 1, abort_p, kLatentWaitNs))) ok = false;

@@ -61,3 +61,31 @@ def test_nan_token(latent, heads, token):
     case.kv.cache[case.kv.block_table[0, token // 16].long(), token % 16, latent + 3] = float("nan")
     o, lse = case.run()
     assert o.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("latent", [256, 512])
+@pytest.mark.parametrize("heads,rows", [(4, 1), (8, 1), (5, 4), (40, 1)])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_alone_and_in_company(latent, heads, rows, splits):
+    """A row's bits do not depend on the next sequence's queries, which stand behind
+    its own in memory and whose scores over its tokens rise all the way."""
+    both = Latent("bf16", heads, latent, [900, 30], [rows, rows], seed=latent + heads, splits=splits)
+    rising(both, 900)
+    both.q[:rows, :, 0] = 0
+    both.q[rows:].zero_()
+    both.q[rows:, :, 0] = 50.0
+    o, lse = both.run()
+    p = va.Problem(**{**vars(both.p), "num_seqs": 1, "q": both.q[:rows].contiguous(), "total_rows": rows,
+                      "cu_rows": both.p.cu_rows[:2].contiguous(), "ctx_len": both.p.ctx_len[:1].contiguous()})
+    kv = va.LatentKV(**{**vars(both.kv), "block_table": both.kv.block_table[:1].contiguous()})
+    o1, lse1 = va.verify_attn_latent(p, kv, 0)
+    assert torch.equal(o[:rows], o1) and torch.equal(lse[:rows], lse1)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan"), 3e38])
+def test_few_rows_beside_queries_of_any_value(value):
+    both = Latent("bf16", 4, 512, [300, 30], [1, 1], seed=3)
+    want = [t[:1].clone() for t in both.run()]
+    both.q[1:] = value
+    o, lse = both.run()
+    assert torch.equal(o[:1], want[0]) and torch.equal(lse[:1], want[1])
