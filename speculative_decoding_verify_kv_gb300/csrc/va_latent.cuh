@@ -42,8 +42,10 @@ struct LatentParams {
   int min_chunk;          // tokens
   int many;               // a sequence of max_rows rows may have many
   int rows_per_block;
-  float* ws_acc;          // [slots][total_rows][H][DV]
-  float* ws_ml;           // [slots][total_rows][H][2]  (m in log2 units, l)
+  int part_seq;           // partials of a sequence and slot; 0: one for every row and head of the launch
+  int merge_seq;          // (row, head) pairs of a sequence that may have more than one chunk; 0: any of the launch
+  float* ws_acc;          // [partials][DV], see latent_part
+  float* ws_ml;           // [partials][2]  (m in log2 units, l)
   void* o;                // [total_rows][H][DV]
   float* lse;             // [total_rows][H]
   int o_bf16;
@@ -149,8 +151,18 @@ __device__ __forceinline__ void latent_nan_rows(const LatentParams& p, int s, in
   }
 }
 
-__device__ __forceinline__ long long latent_slot(const LatentParams& p, int slot, long long item) {
-  return (long long)slot * p.total_rows * p.H + item;
+// Where the partials of chunk c of a sequence stand: that of (row, head) item at
+// latent_part + item.  A sequence of more than one row block has no more than slots /
+// blocks chunks, and so no more partials than slots for each row of one block: the
+// workspace is sized by that where it is less than slots for every row of the launch
+// (one sequence of 1,024 rows, 128 heads, 512 columns, 76 slots: 20 MB, not 20 GB).
+__device__ __forceinline__ long long latent_part(const LatentParams& p, int s, int row0, int n, int c) {
+  if (p.part_seq == 0) return (long long)c * p.total_rows * p.H;
+  return (long long)s * p.part_seq * p.slots + ((long long)c * n - row0) * p.H;
+}
+// From one chunk's to the next one's.
+__device__ __forceinline__ long long latent_apart(const LatentParams& p, int n) {
+  return (long long)(p.part_seq == 0 ? p.total_rows : n) * p.H;
 }
 
 cudaError_t launch_latent_simt(const LatentParams& p, dim3 grid, cudaStream_t st);

@@ -478,10 +478,10 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
     const float l = (red[r] + red[kLpRows + r]) + (red[2 * kLpRows + r] + red[3 * kLpRows + r]);
     const bool bad = __any_sync(0xffffffffu, *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0);
     const float inv = bad ? NAN : l != 0.f ? 1.f / l : 0.f;
-    const long long first = (long long)q.row0 * p.H + rbase;
+    const long long first = (long long)q.row0 * p.H + rbase, partials = latent_part(p, s, q.row0, q.n, chunk);
     if (rvalid && who == 0) {
       if (live > 1) {
-        const long long si = latent_slot(p, chunk, first + r);
+        const long long si = partials + first + r;
         p.ws_ml[2 * si] = bad ? NAN : m_use;
         p.ws_ml[2 * si + 1] = bad ? NAN : l;
       } else {
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
     bar_sync(1, 256);
     if (live > 1) {
       constexpr int PIECES = C::DV / 4;  // of 16 bytes
-      float* to = p.ws_acc + latent_slot(p, chunk, first) * C::DV;
+      float* to = p.ws_acc + (partials + first) * C::DV;
       for (int u = tid - 64; u < nrows * PIECES; u += 256)
         *reinterpret_cast<uint4*>(to + (long long)u * 4) = *reinterpret_cast<const uint4*>(sm + u / PIECES * C::OROW + u % PIECES * 16);
     } else {
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
       const int d = u % C::DV;
       if (live > 1) {
         if (d == 0) {
-          const long long si = latent_slot(p, chunk, item);
+          const long long si = latent_part(p, s, q.row0, q.n, chunk) + item;
           p.ws_ml[2 * si] = q.err ? NAN : -INFINITY;
           p.ws_ml[2 * si + 1] = q.err ? NAN : 0.f;
         }

@@ -39,9 +39,10 @@ constexpr int kLqWarps = kLqThreads / 32;
 enum { kLqSkip = -1, kLqBad = -2, kLqEnd = -3 };
 struct LqItem {
   int row0, rbase, nrows, head;
-  int chunk, live, ctx, lo;
+  int live, ctx, lo;
   int hi, all_see, work, key0;
   int s, first;
+  long long part;  // of the chunk's partials, see latent_part
 };
 
 template <int DK_, int DV_>
@@ -176,7 +177,7 @@ __device__ __forceinline__ bool find_item(const LatentParams& p, int x, int* bas
     const int rb = blocks - 1 - place % blocks, chunk = place / blocks;
     it->live = latent_live(p, q.len, nchunk);
     if (chunk >= it->live) return true;
-    it->chunk = chunk;
+    it->part = latent_part(p, *base + at, q.row0, q.n, chunk);
     it->row0 = q.row0, it->rbase = rb * kLqM, it->nrows = min(kLqM, q.n - it->rbase);
     it->ctx = q.ctx;
     int lo, hi;
@@ -205,7 +206,7 @@ __device__ __noinline__ void no_work(const LatentParams& p, const LqItem& it, in
       const int d = u % DV;
       if (it.live > 1) {
         if (d == 0) {
-          const long long si = latent_slot(p, it.chunk, i);
+          const long long si = it.part + i;
           p.ws_ml[2 * si] = -INFINITY;
           p.ws_ml[2 * si + 1] = 0.f;
         }
@@ -226,7 +227,7 @@ __device__ __forceinline__ void store_rows(const LatentParams& p, const LqItem& 
   const int lane = threadIdx.x & 31;
   const float inv = bad ? NAN : l != 0.f ? 1.f / l : 0.f;
   const long long at = latent_item(p, was.row0, was.rbase + r, was.head);
-  const long long slot = latent_slot(p, was.chunk, at);
+  const long long slot = was.part + at;
   if (r < was.nrows && half == 0) {
     if (was.live > 1) {
       p.ws_ml[2 * slot] = bad ? NAN : m_use;
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const __gr
     }
     // What a warp has in common is known to be so.
     auto same = [&](int& v) { v = __shfl_sync(0xffffffffu, v, 0); };
-    same(it->row0), same(it->rbase), same(it->nrows), same(it->head), same(it->chunk), same(it->live);
+    same(it->row0), same(it->rbase), same(it->nrows), same(it->head), same(it->live);
     same(it->ctx), same(it->lo), same(it->hi), same(it->all_see), same(it->work), same(it->key0);
     return true;
   };
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const __gr
     LqItem* mine = reinterpret_cast<LqItem*>(sm + C::OFF_MINE) + (warp - 2);
     auto keep = [&]() {
       __syncwarp();
-      if (lane == 0) mine->row0 = it.row0, mine->rbase = it.rbase, mine->nrows = it.nrows, mine->head = it.head, mine->chunk = it.chunk, mine->live = it.live;
+      if (lane == 0) mine->row0 = it.row0, mine->rbase = it.rbase, mine->nrows = it.nrows, mine->head = it.head, mine->part = it.part, mine->live = it.live;
       __syncwarp();
     };
     keep();

@@ -483,11 +483,11 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
     bar_sync(3, 128);
     const bool bad = *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0;
     auto sum_of = [&](int n) { return (w_s[n] + w_s[N + n]) + (w_s[2 * N + n] + w_s[3 * N + n]); };
-    const long long item0 = (long long)q.row0 * p.H;
+    const long long item0 = (long long)q.row0 * p.H, part = latent_part(p, s, q.row0, q.n, chunk);
     if (th < R) {
       const float sum = sum_of(th), m = m_s[th];
       if (live > 1) {
-        const long long si = latent_slot(p, chunk, item0 + th);
+        const long long si = part + item0 + th;
         p.ws_ml[2 * si] = bad ? NAN : m;
         p.ws_ml[2 * si + 1] = bad ? NAN : sum;
       } else {
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
     // O^T: a lane per value column, so a warp stores 32 of a row's at once.
     if (th < R) f_s[th] = bad ? NAN : live > 1 ? 1.f : sum_of(th) != 0.f ? 1.f / sum_of(th) : 0.f;
     bar_sync(3, 128);
-    const long long first = (live > 1 ? latent_slot(p, chunk, item0) : item0) * C::DV + th;
+    const long long first = (live > 1 ? part + item0 : item0) * C::DV + th;
 #pragma unroll 1
     for (int c = 0; c < MB; ++c) {
       uint32_t o[N];
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
       const int d = u % C::DV;
       if (live > 1) {
         if (d == 0) {
-          const long long si = latent_slot(p, chunk, item);
+          const long long si = latent_part(p, s, q.row0, q.n, chunk) + item;
           p.ws_ml[2 * si] = p.ws_ml[2 * si + 1] = NAN;
         }
       } else {

@@ -491,10 +491,11 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     const float l = red[r] + red[kLuM + r];
     const bool bad = __any_sync(0xffffffffu, *abort_p != 0 || *reinterpret_cast<volatile int*>(err_s) != 0);
     const float inv = bad ? NAN : l != 0.f ? 1.f / l : 0.f;
+    const long long part = latent_part(p, s, q.row0, q.n, chunk);
     if (rvalid && half == 0) {
       const long long item = latent_item(p, q.row0, rbase + r, 0);
       if (live > 1) {
-        const long long si = latent_slot(p, chunk, item);
+        const long long si = part + item;
         p.ws_ml[2 * si] = bad ? NAN : m_use;
         p.ws_ml[2 * si + 1] = bad ? NAN : l;
       } else {
@@ -537,7 +538,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
     const long long first = latent_item(p, q.row0, rbase, 0);
     if (live > 1) {
       constexpr int PIECES = DV / 4;  // of 16 bytes
-      float* to = p.ws_acc + latent_slot(p, chunk, first) * DV;
+      float* to = p.ws_acc + (part + first) * DV;
       for (int u = tid - 64; u < nrows * PIECES; u += 256) {
         const int row = u / PIECES, c = u % PIECES;
         *reinterpret_cast<uint4*>(to + row * DV + c * 4) = *reinterpret_cast<const uint4*>(sm + row * C::OROW + c * 16);
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
       const long long item = latent_item(p, q.row0, rbase + row, 0);
       if (live > 1) {
         if (d == 0) {
-          const long long si = latent_slot(p, chunk, item);
+          const long long si = latent_part(p, s, q.row0, q.n, chunk) + item;
           p.ws_ml[2 * si] = q.err ? NAN : -INFINITY;
           p.ws_ml[2 * si + 1] = q.err ? NAN : 0.f;
         }

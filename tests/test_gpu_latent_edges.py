@@ -1,9 +1,11 @@
 """Edges of attention over a latent cache: queries and cached values that are no
 numbers where a sequence has one tile or every tile moves a row's maximum, and
 rows in the company of other sequences (GB300)."""
+import ctypes
+
 import pytest
 
-from latent_util import Latent
+from latent_util import Latent, Prompt, check
 
 import speculative_decoding_verify_kv_gb300 as va
 
@@ -89,3 +91,34 @@ def test_few_rows_beside_queries_of_any_value(value):
     both.q[1:] = value
     o, lse = both.run()
     assert torch.equal(o[:1], want[0]) and torch.equal(lse[:1], want[1])
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("latent,heads,ctx,rows,splits", [
+    (512, 24, [700, 900, 0, 300], [40, 2, 0, 30], 17), (256, 24, [700, 1500], [40, 2], 17), (512, 7, [1500, 300], [3, 1], 9),
+    (512, 130, [500], [25], 60), (256, 5, [200, 800, 1000], [1, 70, 9], 12)])
+def test_workspace_of_row_blocks(kind, latent, heads, ctx, rows, splits):
+    """Partials of long and short sequences stand in the workspace that the library asks
+    for, which holds no more than a row block a sequence and chunk; nothing behind it."""
+    case = Latent(kind, heads, latent, ctx, rows, seed=heads, splits=splits)
+    need = va.lib.va_latent_workspace_size(ctypes.byref(case.p.c()), ctypes.byref(case.kv.c()))
+    block = 16 if kind == "f32" else 128
+    assert need <= splits * min(len(ctx) * block, sum(rows) * heads) * (latent + 2) * 4 + 512
+    ws = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+    o, lse = case.run(ws=ws)
+    assert case.status.item() == 0 and (ws[need:] == 0x5A).all()
+    check((o, lse), case.oracle(), kind)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows,keys,splits", [([300, 7, 200], [2100, 1900, 200], 6), ([900], [1300], 16), ([5, 0, 9], [1500, 3, 800], 5)])
+def test_prompt_workspace_of_row_blocks(kind, dim, rows, keys, splits):
+    case = Prompt(kind, 3, dim, rows, keys, seed=dim, splits=splits)
+    need = va.lib.va_latent_prompt_workspace_size(ctypes.byref(case.p.c()), ctypes.byref(case.kv.c()))
+    block = 16 if kind == "f32" else 128
+    assert need <= splits * min(len(rows) * block, sum(rows)) * 3 * (dim + 2) * 4 + 512
+    ws = torch.full((need + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+    o, lse = case.run(ws=ws)
+    assert case.status.item() == 0 and (ws[need:] == 0x5A).all()
+    check((o, lse), case.oracle(), kind)
