@@ -122,6 +122,12 @@ __device__ __forceinline__ uint32_t at_first(uint32_t addr) {
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Writes to the same place in CTA `rank` of the cluster.
+__device__ __forceinline__ void store_at(uint32_t addr, int rank, int v) {
+  asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.volatile.shared::cluster.b32 [a], %2;\n\t}" ::"r"(addr), "r"(rank),
+               "r"(v)
+               : "memory");
+}
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -176,6 +182,16 @@ __device__ __forceinline__ void tma_3d_by(uint32_t e, uint32_t dst, const CUtens
         "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "r"(e)
         : "memory");
+}
+
+// A kernel that gave up on a wait ends only when its copies have landed.  Each warp
+// drains those whose barriers it armed; a copy counted on a barrier that another warp
+// or CTA did not come to arm, or issued by a warp that saw no failure, cannot be asked
+// about, so the kernel also lets the time pass (copies take some microseconds).
+constexpr uint64_t kSettleNs = 2000000ull;
+__device__ __forceinline__ void settle() {
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < kSettleNs) __nanosleep(1000);
 }
 
 // Zeros in rows from .. to - 1 of a 64-column block, by a warp.

@@ -169,8 +169,10 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
     atomicOr(err_s, (int)bits);
     flag(p.status, bits);
   };
+  // Both CTAs give up, and know it behind the closing barrier.
   auto fail = [&]() {
     *abort_p = 1;
+    store_at(smem_u32(const_cast<int*>(abort_p)), rank ^ 1, 1);
     flag(p.status, VA_DEV_TIMEOUT);
   };
   auto drain = [&](uint32_t b, uint32_t parity) {
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
       ok = __all_sync(0xffffffffu, mbar_wait(bar(PB_QLAND), 0, abort_p, kLatentWaitNs));
       if (ok && lane == 0) arrive_first(PB_QALL);
     }
-    int issued = 0;  // groups or units
+    int issued = 0;  // groups; or units of this warp, every second one
     uint32_t par = 1;
     for (int i = 0; i < work && ok; ++i) {
       const int t0 = lo_u + i * kLpTile;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
               tma_3d_by<true>(one, base + C::OFF_V + (u * C::VG + k) * C::VB + g * kPage * 128, &maps.k, u / 2 * 256 + rank * 128 + k * 64, at[g].x,
                               at[g].y, b);
           }
-          issued = i * C::VU + u + 1;
+          issued = i * (C::VU / 2) + u / 2 + 1;
         }
       }
       par ^= 1;
@@ -283,11 +285,16 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
         fail();
       }
     }
-    // No copy may still be landing when the pair goes away.  (All but the last
-    // tile's values are counted in the first CTA, which waits for them.)
-    if (*abort_p && lane == 0 && rank == 0) {
-      const int n = keys ? C::KU : C::VU;
-      for (int i = max(0, issued - n); i < issued; ++i) drain(keys ? kfull(i % n) : vfull(i % n), (i / n) & 1);
+    // No copy may still be landing when the pair goes away: the last of each group
+    // and unit, those before have been read.  Keys, and values of whole tiles, are
+    // counted in the first CTA, a ragged last tile's values in each.
+    if (*abort_p && lane == 0) {
+      const int n = keys ? C::KU : C::VU / 2;
+      for (int k = max(0, issued - n); k < issued; ++k) {
+        const int i = k / n, u = keys ? k % n : who + 2 * (k % n);
+        if (values && ragged && i == work - 1) drain(bar(PB_VLAST + u), 0);
+        else if (rank == 0) drain(keys ? kfull(u) : vfull(u), i & 1);
+      }
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------------- S issuer
@@ -552,6 +559,10 @@ __global__ void __launch_bounds__(kLpThreads, 1) latent_pair_kernel(const Latent
   tc_fence_before();
   cluster_sync_all();  // the other CTA's products and arrivals reach into this one
   tc_fence_after();
+  if (*abort_p) {  // in both or in none
+    settle();
+    cluster_sync_all();
+  }
   if (warp == 1) tmem_dealloc_pair(tm, 512);
 }
 
