@@ -772,6 +772,7 @@ __global__ void __launch_bounds__(kLqThreads, 1) latent_prompt_kernel(const __gr
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (*abort_p) settle();
   if (warp == 1) tmem_dealloc(tm, 512);
 }
 

@@ -536,6 +536,7 @@ __global__ void __launch_bounds__(kLrThreads, 1) latent_rows_kernel(const Latent
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (*abort_p) settle();
   if (warp == 1) tmem_dealloc(tm, C::COLS);
 }
 

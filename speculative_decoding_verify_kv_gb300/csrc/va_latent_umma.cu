@@ -573,6 +573,7 @@ __global__ void __launch_bounds__(kLuThreads, 1) latent_umma_kernel(const Latent
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (*abort_p) settle();
   if (warp == 1) tmem_dealloc(tm, 512);
 }
 

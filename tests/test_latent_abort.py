@@ -82,3 +82,12 @@ def test_pair_gives_up_together():
     end = text[text.rindex("tc_fence_before();"):]
     assert re.search(r"cluster_sync_all\(\);\s*tc_fence_after\(\);\s*if \(\*abort_p\) \{\s*settle\(\);\s*cluster_sync_all\(\);\s*\}"
                      r"\s*if \(warp == 1\) tmem_dealloc_pair", end)
+
+
+@pytest.mark.parametrize("name", ["rows", "umma", "prompt"])
+def test_a_late_failure_is_waited_for(name):
+    """A producer may issue its last copies and pass its own check just before another warp
+    gives up: all warps look at the word behind the last barrier."""
+    end = body(name)
+    end = end[end.rindex("tc_fence_before();"):]
+    assert re.search(r"__syncthreads\(\);\s*tc_fence_after\(\);\s*if \(\*abort_p\) settle\(\);\s*if \(warp == 1\) tmem_dealloc", end)
