@@ -3,6 +3,7 @@ numbers where a sequence has one tile or every tile moves a row's maximum, and
 rows in the company of other sequences (GB300)."""
 import ctypes
 
+import numpy as np
 import pytest
 
 from latent_util import Latent, Prompt, check
@@ -122,3 +123,115 @@ def test_prompt_workspace_of_row_blocks(kind, dim, rows, keys, splits):
     o, lse = case.run(ws=ws)
     assert case.status.item() == 0 and (ws[need:] == 0x5A).all()
     check((o, lse), case.oracle(), kind)
+
+
+@pytest.mark.parametrize("latent", [256, 512])
+@pytest.mark.parametrize("what,bits", [("block", va.DEV_BAD_BLOCK), ("far block", va.DEV_BAD_BLOCK), ("parent", va.DEV_BAD_PARENT),
+                                       ("ctx", va.DEV_CTX_OVERFLOW), ("negative", va.DEV_CTX_OVERFLOW), ("rows", va.DEV_BAD_ROWS),
+                                       ("tree", va.DEV_BAD_ROWS)])
+@pytest.mark.parametrize("splits", [1, 6])
+def test_findings_of_many_rows(latent, what, bits, splits):
+    """More than 32 query rows (pairs of CTAs, of which both have to know, and 128-row
+    blocks): a bad sequence is NaN and flagged, the others are as always."""
+    heads, rows = 24, [9, 6, 3]
+    case = Latent("bf16", heads, latent, [700, 300, 150], rows, "tree", True, seed=8, splits=splits)
+    want = case.oracle()
+    bad = slice(0, 9)
+    if what == "block":
+        case.kv.block_table[0, 20] = case.kv.num_blocks
+    elif what == "far block":
+        case.kv.block_table[0, 44] = -2       # the last page of the drafts, at the end of a ragged tile
+    elif what == "parent":
+        case.p.parent[2], bad = 2, slice(2, 3)
+    elif what == "ctx":
+        case.p.ctx_len[0] = 16 * case.kv.max_blocks_per_seq
+    elif what == "negative":
+        case.p.ctx_len[0] = -5
+    elif what == "rows":
+        case.p.max_rows_per_seq = 8
+    else:
+        case.p.ctx_len[0] = 0
+        case.p.cu_rows[:] = torch.tensor([0, 33, 34, 37], device="cuda")
+        case.p.max_rows_per_seq, case.p.total_rows = 40, 37
+        q = torch.zeros(37, heads, latent + 64, dtype=case.q.dtype, device="cuda")
+        q[34:] = case.q[15:]
+        parent = torch.full((37,), -1, dtype=torch.int32, device="cuda")
+        parent[34:] = case.p.parent[15:18]
+        case.p.q, case.p.parent = q, parent
+    mode = 2 if what == "tree" else case.mode_code  # (trees alone may not have a bound of more than 32 rows)
+    o, lse = va.verify_attn_latent(case.p, case.kv, mode, status=case.status)
+    assert case.status.item() == bits
+    if what == "tree":
+        assert o[:33].isnan().all() and lse[:33].isnan().all()
+        check((o[34:], lse[34:]), tuple(x[15:] for x in want), "bf16")
+        return
+    assert lse[bad].isnan().all() and o[bad].isnan().all()
+    check((o[9:], lse[9:]), tuple(x[9:] for x in want), "bf16")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("heads", [3, 20])
+@pytest.mark.parametrize("splits", [1, 4])
+def test_findings_of_too_many_rows(kind, heads, splits):
+    """A sequence longer than the bound is NaN in all its rows; the others are as always."""
+    case = Latent(kind, heads, 512, [200, 400, 100], [2, 9, 3], seed=3, splits=splits)
+    want = case.oracle()
+    case.p.max_rows_per_seq = 8
+    o, lse = case.run()
+    assert case.status.item() == va.DEV_BAD_ROWS
+    assert o[2:11].isnan().all() and lse[2:11].isnan().all()
+    for part in (slice(0, 2), slice(11, 14)):
+        check((o[part], lse[part]), tuple(x[part] for x in want), kind)
+
+
+@pytest.mark.parametrize("kind,heads,latent", [("bf16", 16, 512), ("bf16", 40, 512), ("bf16", 40, 256), ("f32", 4, 256)])
+@pytest.mark.parametrize("splits", [1, 6])
+def test_replayed_over_other_lengths(kind, heads, latent, splits):
+    """A captured call reads lengths, offsets and tables when it runs: fewer and more
+    chunks hold tokens than at capture, rows move between the sequences."""
+    case = Latent(kind, heads, latent, [1500, 900], [2, 2], seed=7, splits=splits)
+    ws = va.lib.va_latent_workspace_size(ctypes.byref(case.p.c()), ctypes.byref(case.kv.c()))
+    call = va.LatentCall(case.p, case.kv, 0, ws=torch.empty(max(ws, 256), dtype=torch.uint8, device="cuda"), status=case.status)
+    case.p.ctx_len[:] = torch.tensor([70, 200], device="cuda")
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for ctx, cu in (([70, 200], [0, 2, 4]), ([1500, 900], [0, 2, 4]), ([0, 830], [0, 2, 3]), ([1200, 0], [0, 1, 3]), ([3, 900], [0, 0, 2])):
+        case.p.ctx_len[:] = torch.tensor(ctx, device="cuda")
+        case.p.cu_rows[:] = torch.tensor(cu, device="cuda")
+        for t in out:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert case.status.item() == 0
+        fresh = va.LatentCall(case.p, case.kv, 0, o=torch.full_like(out[0], 7), lse=torch.full_like(out[1], 7))()
+        assert all(torch.equal(a, b) for a, b in zip(out, fresh))
+        case.ctx, case.cu = np.array(ctx, np.int32), np.array(cu, np.int32)
+        n = cu[-1]
+        case.p.total_rows = 4
+        check(tuple(t[:n] for t in out), tuple(x[:n] for x in case.oracle()), kind)
+        assert (out[0][n:] == 7).all() and (out[1][n:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("splits", [1, 5])
+def test_prompts_replayed_over_other_lengths(kind, splits):
+    case = Prompt(kind, 3, 128, [130, 70], [900, 500], seed=7, splits=splits)
+    call = va.PromptCall(case.p, case.kv, status=case.status)
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    for cu, cu_kv in (([0, 130, 200], [0, 900, 1400]), ([0, 70, 200], [0, 100, 1400]), ([0, 100, 130], [0, 1300, 1350]), ([0, 0, 130], [0, 0, 130])):
+        case.p.cu_rows[:] = torch.tensor(cu, device="cuda")
+        case.kv.cu_kv[:] = torch.tensor(cu_kv, device="cuda")
+        for t in out:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert case.status.item() == 0
+        n = cu[-1]
+        case.cu, case.cu_kv = np.array(cu, np.int32), np.array(cu_kv, np.int32)
+        check(tuple(t[:n] for t in out), tuple(x[:n] for x in case.oracle()), kind)
+        assert (out[0][n:] == 7).all() and (out[1][n:] == 7).all()
