@@ -19,7 +19,7 @@ constexpr int kQueryThreads = 128;
 constexpr int kAppendThreads = kQueryThreads + 32;
 
 struct AppendParams {
-  int rows, heads, latent, positions, interleaved;
+  int rows, heads, positions, interleaved;
   float eps;
   const void* kv;
   long long kv_stride;
@@ -230,7 +230,6 @@ va_status verify_attn_latent_append(const va_latent* kv, const va_latent_rows* n
   memset(&q, 0, sizeof(q));
   q.rows = n->num_rows;
   q.heads = n->num_heads;
-  q.latent = kv->latent_dim;
   q.positions = n->rope_positions;
   q.interleaved = n->interleaved;
   q.eps = n->norm_eps;

@@ -41,7 +41,7 @@ struct LqItem {
   int row0, rbase, nrows, head;
   int live, ctx, lo;
   int hi, all_see, work, key0;
-  int s, first;
+  int s;
   long long part;  // of the chunk's partials, see latent_part
 };
 
@@ -166,7 +166,7 @@ __device__ __forceinline__ bool find_item(const LatentParams& p, int x, int* bas
     const int place = x - *start - its(upto - b);
     q.err = (unsigned)its((int)q.err);
     q.row0 = its(q.row0), q.n = its(q.n), q.ctx = its(q.ctx), q.len = its(q.len), q.kind = 0;
-    it->s = *base + at, it->first = place == 0, it->key0 = its((int)q.key0);
+    it->s = *base + at, it->key0 = its((int)q.key0);
     if (q.err) {
       it->work = kLqBad;
       return true;
@@ -198,7 +198,7 @@ template <int DV>
 __device__ __noinline__ void no_work(const LatentParams& p, const LqItem& it, int t) {
   if (it.work == kLqBad) {
     if (t == 0) flag(p.status, VA_DEV_BAD_ROWS);
-    if (it.first) latent_nan_rows(p, it.s, it.head, 1, t, 256);
+    latent_nan_rows(p, it.s, it.head, 1, t, 256);  // its one block
   } else if (it.work == 0) {
     // A chunk that the block's rows see nothing of, or no keys.
     for (int u = t; u < it.nrows * DV; u += 256) {
