@@ -714,12 +714,16 @@ va_status verify_attn_latent_append(const va_latent *kv, const va_latent_rows *r
  * max_rows_per_seq times num_heads is no more; of 16 on the CUDA cores: fp32
  * caches, VA_FLAG_CUDA_CORES) each takes num_splits / b chunks, rounded
  * down, and at least one.  va_latent_splits gives a count that fills the
- * GPU.  No choice depends on the other sequences of the launch.
+ * GPU.  No choice depends on the other sequences of the launch.  The
+ * workspace holds the partials that can exist: num_splits for each row and
+ * head, but no more than for one row block a sequence.
  * bf16: probabilities enter the second product rounded to bf16 (2^-8 of each at most,
  * about what rounding o costs); their sum, and lse, are of the unrounded
  * ones in fp32.  fp32: fp32 products and sums.
  * Cache rows that some rows of the sequence see and others do not must be
- * finite; others may hold anything.  Rows that no sequence covers stay as
+ * finite; others may hold anything.  A query, or a cache row that all rows
+ * see, that is no number makes the rows NaN that it meets.  Scaled scores stay
+ * below 2^29 in size.  Rows that no sequence covers stay as
  * they were.  At most 65,535 sequences.  Errors as for the verify calls.  ws
  * of at least va_latent_workspace_size() bytes (may be 0, ws may then be
  * NULL), 256-byte aligned; contents carry nothing from call to call, and

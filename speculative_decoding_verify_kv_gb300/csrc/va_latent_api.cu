@@ -149,8 +149,11 @@ static int32_t fill(const va_problem* p, const LatentPlan& pl, int heads) {
 }
 
 // Keys that a chunk of a prompt should have on the tensor cores before its
-// partials and their merge pay: 256 rows x 32 heads over 1,033 keys 16.4 us
-// uncut, 19.2 in two chunks.
+// partials and their merge pay.  One segment of 256 rows, us uncut and in two chunks:
+// 32 heads over 1,024 keys 13.3 and 16.9, 2,048 19.9 and 20.0, 4,096 33.3 and 26.9; 16
+// heads 12.8 and 14.7, 19.4 and 17.6, 32.8 and 24.4; one head 12.4 and 12.1, 19.0 and
+// 15.3, 32.2 and 21.9.  Shorter chunks pay where a few blocks leave the GPU empty: one
+// head over 16,384 keys 16.5 in the 16 chunks of this rule, 12.9 in 64.
 constexpr int kPromptChunkKeys = 1024;
 
 static LatentParams base_params(const va_problem* p, int mode, const LatentPlan& pl, int key_dim, int value_dim,

@@ -51,8 +51,8 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
 // issues, with everything they are computed from known to be the warp's:
 // descriptors then live in uniform registers.  An issuing thread of its own
 // branch took some 100 cycles to an MMA, longer than one of 64 columns runs
-// (64 heads x 16 rows x 4 sequences of 8,000 tokens: 142 us against 112; prompts
-// of 2 x 2,048 rows, 128 heads, over 4,096 keys: 966 against 755).
+// (64 heads x 16 rows x 4 sequences of 8,000 tokens: 142 us against 93; prompts
+// of 2 x 2,048 rows, 128 heads, over 4,096 keys: 966 against 760).
 __device__ __forceinline__ uint32_t elected() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(e));

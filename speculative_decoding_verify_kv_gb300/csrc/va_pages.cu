@@ -377,8 +377,10 @@ __global__ void __launch_bounds__(kPlanThreads) pages_free_kernel(const PagePara
 // table.  Two barriers of the CTAs (three with trees), against six where one CTA
 // sums and the rows wait for the tables: 40 sequences of one row, 8,192 pages, 6.2
 // us against 14; 256 of up to 8 over 131,072, 12.2 against 23.
-// Integers of a step that one CTA plans: 40 sequences over 8,192 pages 6.5 us,
-// 8.3 with a cluster; 256 over 131,072 18.0, and 12.6.
+// Integers of a step that one CTA plans.  One row a sequence, us by one CTA and by a
+// cluster: 40 sequences over 8,192 pages 4.9 and 6.7, 8 over 16,000 5.1 and 6.6, over
+// 32,768 6.0 and 7.0, over 65,536 7.7 and 6.8, 1,000 over 8,192 12.9 and 8.4; 256 of 8
+// rows over 4,096 7.5 and 7.7, over 131,072 13.9 and 8.3.
 constexpr long long kOneCtaExtend = 16384;
 constexpr int kSeqLanes = 8;     // go through a sequence's entries
 constexpr int kSeqShared = 2048; // sequences whose sums stand in shared memory

@@ -235,3 +235,25 @@ def test_prompts_replayed_over_other_lengths(kind, splits):
         case.cu, case.cu_kv = np.array(cu, np.int32), np.array(cu_kv, np.int32)
         check(tuple(t[:n] for t in out), tuple(x[:n] for x in case.oracle()), kind)
         assert (out[0][n:] == 7).all() and (out[1][n:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("latent", [256, 512])
+@pytest.mark.parametrize("heads", [2, 20, 40])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_large_scores(kind, latent, heads, sign):
+    """One token whose score is +-2^28: its value and the score come back.  (Scaled to
+    log2 units the score is rounded, 2^-24 of it, by a kernel's maximum and by its
+    exponent apart: a weight of 2^+-16 that its sum has too.)"""
+    case = Latent(kind, heads, latent, [0], [1], seed=1, scale=1.0)
+    case.q.zero_()
+    case.q[..., 0] = sign * 2.0 ** 14
+    row = case.kv.cache[case.kv.block_table[0, 0].long(), 0]
+    row[0] = 2.0 ** 14
+    o, lse = case.run()
+    v = row[:latent].double()
+    # Three roundings of a score, at 2^-24 each, and the last bit of the sum.
+    assert ((lse.double() - sign * 2.0 ** 28).abs() <= 2.0 ** 28 * 2.0 ** -22).all()
+    # bf16: the weight's rounding and o's, 2^-8 each at most; fp32: weight, sum, its inverse, product.
+    step = 2.0 ** -7 if kind == "bf16" else 2.0 ** -21
+    assert ((o.double() - v).abs() <= step * v.abs()).all()
