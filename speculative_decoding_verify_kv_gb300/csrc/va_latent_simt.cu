@@ -295,9 +295,10 @@ __device__ __forceinline__ void latent_store4(const LatentParams& p, long long a
   }
 }
 
-// Takes chunks first, first + step, .. of the partials at si0, each `apart` on (B of them in flight at once: m, l and a
-// float4 of acc together) into a running (M, l, acc) of the calling warp's lanes,
-// NC columns of 4 to a lane from column col on.
+// Takes chunks first, first + step, .. of the partials at si0, each `apart` behind the
+// one before (B of them in flight at once: m, l and a float4 of acc together), into a
+// running (M, l, acc) of the calling warp's lanes, NC columns of 4 to a lane from
+// column col on.
 template <int DV, int NC, int B>
 __device__ __forceinline__ void latent_gather(const LatentParams& p, long long si0, long long apart, int live, int first, int step, int col,
                                               bool mine, float& M, float& l, float4 (&acc)[NC], bool& nan) {
@@ -354,7 +355,8 @@ __device__ __forceinline__ void latent_gather(const LatentParams& p, long long s
 // merge, and where they stand.  BY_SEQ: item counts among those of sequence s that can
 // have some, else among all of the launch, and the sequence is searched for.  One that
 // finds nothing to do costs about as much as one that does: 300 rows of 128 heads over
-// 2,300 tokens, one chunk each, 156 us by all rows of the launch, 140 by sequence, 135 without a merge.
+// 2,300 tokens, one chunk each, 156 us by all rows of the launch, 140 by sequence, 135
+// without a merge.
 struct LatentMerge {
   long long item, part, apart;
   int live;
